@@ -64,11 +64,13 @@ enum q8_status {
     Q8_OK = 0,
     Q8_EINVAL = -1,      /* bad dimension, null pointer, in_dim % 32 != 0, overflow */
     Q8_EALIGN = -2,      /* a pointer is not 16-byte aligned */
-    Q8_ERANGE = -3,      /* (device) an expert id was outside [0, n_expert) */
+    Q8_ERANGE = -3,      /* (device) an expert id was outside [0, n_expert), or a cache page, row,
+                            position or length outside its range */
     Q8_ENOMEM = -4,      /* scratch allocation failed */
     Q8_ECUDA = -5,       /* a CUDA runtime call failed (no device, launch error, ...) */
     Q8_ETIMEOUT = -6,    /* (device) a kernel's bounded wait expired; outputs undefined */
-    Q8_ESCRATCH = -7     /* the call needs more than the fixed scratch of q8_matmul_noalloc */
+    Q8_ESCRATCH = -7,    /* the call needs more than the fixed scratch of q8_matmul_noalloc */
+    Q8_ENOPAGE = -8      /* (device) a cache has too few free pages, or a row too few entries */
 };
 
 /* Library version (major*10000 + minor*100 + patch). */
@@ -288,6 +290,163 @@ int q8_moe_combine(float *out, const float *y, const float *weights, uint64_t n_
                    uint64_t dim, void *stream);
 
 /*
+ * Paged key-value cache and the attention over it: what runs between the q / kv
+ * projections and the output projection (the pages' attention reads a KV cache
+ * between attn_q_b and attn_output_a; GPU code walkthrough, trace 4).
+ *
+ * Types (Q8_TYPE_*).  "16 bit" below is F16 or BF16.
+ *
+ * Cache.  A pool of n_pages pages per layer, K and V apart; page p of layer l is
+ * at k + l*layer_stride + p*page_stride (V the same from v).  A page holds
+ * page_tokens consecutive positions of one sequence, head after head; a head's
+ * tile is
+ *   16 bit:  [page_tokens][head_dim]
+ *   Q8_0:    int8 [page_tokens][head_dim], then binary16 scales
+ *            [page_tokens][head_dim/32] (the split planes of Q8_LAYOUT_PLANES;
+ *            the q8_quantize_act quantiser per 32 values)
+ * page_tokens is 16, 32, 64, 128 or 256; head_dim 64, 128, 256 or 512.  Strides
+ * are bytes, multiples of 16; page_stride >= q8_kv_page_bytes (so the K and V of
+ * a page may alternate in one allocation).
+ * Sequences.  Row r of `table` (int32, table_stride entries apart, max_pages of
+ * them used) lists the pages of sequence r in order; position t lies in page
+ * table[r][t / page_tokens], row t % page_tokens.
+ * The struct itself is host memory, read during the call.
+ */
+#define Q8_TYPE_F32 0
+#define Q8_TYPE_F16 1
+#define Q8_TYPE_BF16 2
+#define Q8_TYPE_Q8_0 8
+typedef struct q8_kv_cache {
+    void *k, *v;             /* device: the pools of layer 0, 16-byte aligned */
+    uint64_t layer_stride;   /* bytes between layers */
+    uint64_t page_stride;    /* bytes between pages of a layer */
+    uint32_t n_layers;
+    uint32_t n_pages;
+    uint32_t page_tokens;
+    uint32_t n_kv_heads;
+    uint32_t head_dim;
+    int32_t type;            /* Q8_TYPE_F16, Q8_TYPE_BF16 or Q8_TYPE_Q8_0 */
+} q8_kv_cache;
+
+/* Bytes of one page (K or V) of one layer; 0 for a bad type or size. */
+uint64_t q8_kv_page_bytes(int type, uint32_t page_tokens, uint32_t n_kv_heads, uint32_t head_dim);
+
+/*
+ * New tokens into the cache: rotates q and k, rounds q to 16 bit, stores k and v.
+ *   q_out            out: 16 bit (out_type) [n_tok][n_heads][head_dim], or NULL (no q).
+ *   k_out, v_out     out: 16 bit [n_tok][n_kv_heads][head_dim], or NULL: the rotated
+ *                    k and v as rows for q8_attn_prompt.
+ *   c                the cache (layer `layer` is written), or NULL: no cache write,
+ *                    and seq_of, table are unused.
+ *   q, k, v          in: fp32, token t's heads back to back at q + t*q_stride (elements;
+ *                    strides are multiples of 4, so slices of one fused projection work).
+ *   positions        in: int32 [n_tok], the token's position in its sequence.
+ *   seq_of           in: int32 [n_tok], its row of `table` (n_rows rows); negative: a
+ *                    padding token, which is not stored.
+ *   cos_sin          in: fp32 [n_pos][rot_dim], cos of the rot_dim/2 angles of a position,
+ *                    then their sin; 16-byte aligned.  Unused with rope 0.
+ *   rope             0: no rotation; 1: pairs (i, i + rot_dim/2); 2: pairs (2i, 2i + 1).
+ *                    (a, b) -> (a cos - b sin, b cos + a sin), each product and sum
+ *                    rounded to fp32; dimensions from rot_dim on pass through.
+ *                    rot_dim is a multiple of 16, at most head_dim.
+ * 16-bit values are rounded to nearest even; Q8_0 is bit-exact to q8_quantize_act.
+ * A position outside [0, n_pos) (rope) or outside its row's max_pages pages, a row
+ * outside n_rows, or a page id outside the pool raises Q8_ERANGE; that token is not
+ * stored (and with a bad rope position its outputs are zeros).
+ */
+int q8_kv_append(void *q_out, void *k_out, void *v_out, int out_type, const q8_kv_cache *c, uint32_t layer,
+                 const float *q, uint64_t q_stride, const float *k, uint64_t k_stride, const float *v,
+                 uint64_t v_stride, uint32_t n_heads, uint32_t n_kv_heads, uint32_t head_dim,
+                 const int32_t *positions, const int32_t *seq_of, const int32_t *table, uint64_t table_stride,
+                 uint32_t max_pages, uint32_t n_rows, const float *cos_sin, uint32_t n_pos, uint32_t rot_dim,
+                 int rope, uint64_t n_tok, void *stream);
+
+/*
+ * Attention of one new token per sequence over its cached positions.  For
+ * sequence s and head h (key-value head h / (n_heads / n_kv_heads)):
+ *   z_j = scale * q[s][h] . k_j,  j in [max(0, len - window), len), len = seq_lens[s]
+ *         (window 0: all of [0, len)); the new token's own k and v are already stored
+ *   out[s][h] = sum_j exp(z_j) v_j / (sum_j exp(z_j) + exp(sinks[h]))
+ * without the last term when sinks is NULL.  A sequence of length 0 gives zeros.
+ *   out        out: [n_seq][n_heads][head_dim]; out_type: q's type, Q8_TYPE_F32, or
+ *              Q8_TYPE_Q8_0 (blocks for q8_matmul_q, head_dim/32 per head).
+ *   lse        out: fp32 [n_seq][n_heads], the natural logarithm of the denominator
+ *              (-inf for none), or NULL.
+ *   q          in: 16 bit, token s's heads at q + s*q_stride (elements, a multiple of 8).
+ *   c          16-bit caches must have q's type; Q8_0 goes with either.
+ *   sinks      in: fp32 [n_heads] or NULL.
+ * Statistics, products' sums and the output's sum are fp32; the weights exp(z_j - max)
+ * are rounded to 16 bit for the tensor cores (F16 for Q8_0 caches, where they carry the
+ * block scale of V).  Keys and values outside the visible range are never used, whatever
+ * they hold.  A negative length or one beyond max_pages pages is cut to the range, and a
+ * page id outside the pool leaves its positions out; both raise Q8_ERANGE.
+ * Work is split over the cached positions so that every SM gets an equal share whatever
+ * the lengths; the pieces are joined in a fixed order by the last to finish.
+ */
+int q8_attn_decode(void *out, int out_type, float *lse, const void *q, uint64_t q_stride, int q_type,
+                   const q8_kv_cache *c, uint32_t layer, const int32_t *table, uint64_t table_stride,
+                   uint32_t max_pages, const int32_t *seq_lens, uint32_t n_seq, uint32_t n_heads, float scale,
+                   uint32_t window, const float *sinks, void *stream);
+
+/*
+ * Attention over whole prompts, packed: sequence s has query rows
+ * [q_start[s], q_start[s+1]) and key-value rows [k_start[s], k_start[s+1]), the last
+ * of which belong to the same positions as its queries (more keys than queries: a
+ * prefix computed before).  Query i of Lq sees keys j <= i + Lk - Lq, with a window
+ * only the last `window` of them; formula, sinks, lse, out_type and rounding as for
+ * q8_attn_decode.  A query that sees no key gives zeros.
+ *   q          in: 16 bit (type), row r's heads at q + r*q_stride elements.
+ *   k, v       in: the same type, rows of n_kv_heads heads, k_stride / v_stride apart.
+ *              Strides are multiples of 8, all pointers 16-byte aligned.
+ *   q_start    in: int32 [n_seq + 1], k_start the same or NULL (= q_start); rising,
+ *              from 0 to at most n_q / n_k.  Values outside are cut to the range and
+ *              raise Q8_ERANGE; rows of no sequence are not written.
+ *   out        out: [n_q][n_heads][head_dim], lse [n_q][n_heads] or NULL.
+ * Rows of other sequences and keys a query may not see never change its result,
+ * whatever they hold.
+ */
+int q8_attn_prompt(void *out, int out_type, float *lse, const void *q, const void *k, const void *v, int type,
+                   uint64_t q_stride, uint64_t k_stride, uint64_t v_stride, const int32_t *q_start,
+                   const int32_t *k_start, uint32_t n_seq, uint64_t n_q, uint64_t n_k, uint32_t n_heads,
+                   uint32_t n_kv_heads, uint32_t head_dim, float scale, uint32_t window, const float *sinks,
+                   void *stream);
+
+/*
+ * The pages of a cache.  `refs` (int32 [n_pages]) counts the table rows that hold a
+ * page, 0 = free; rows of `table` and `lens` (int32, cached tokens of a row) are the
+ * sequences.  New pages are the free ones of lowest index, in the order of the
+ * requests, so results do not depend on timing.  Row ids (seqs, src, dst) are int32
+ * device arrays; a negative one is skipped, one outside n_rows raises Q8_ERANGE and is
+ * skipped.  A row may appear once in seqs / dst, and not as src and dst of one call.
+ *   q8_kv_reserve  gives row seqs[i] the pages for n_new[i] more tokens and adds
+ *                  n_new[i] to its length.
+ *   q8_kv_fork     makes row dst[i] a copy of row src[i]: whole pages are shared (refs
+ *                  + 1), a part-filled last page is copied, in all layers, to a new
+ *                  page.  dst rows are overwritten (free them first).
+ *   q8_kv_free     drops the rows' references and empties them (entries -1, length 0).
+ *   q8_kv_compact  moves the pages in use to the front of the pool: with n_used pages in
+ *                  use, those at n_used or beyond, in order, fill the free ones before
+ *                  n_used, in order.  The new table (all n_rows rows, max_pages entries,
+ *                  table_stride apart), refs and n_used[0] go to table_out, refs_out and
+ *                  n_used, the inputs stay; page data moves in place.
+ *   q8_kv_copy     copies page src[i] to dst[i] in all layers, K and V; a negative id
+ *                  skips the pair, one outside the pool also raises Q8_ERANGE.  A dst
+ *                  page may appear once, and not as a src.
+ * When reserve or fork needs more pages than are free, or a row would pass max_pages,
+ * no request of the call is carried out and Q8_ENOPAGE is raised for q8_last_error().
+ */
+int q8_kv_reserve(const q8_kv_cache *c, int32_t *table, uint64_t table_stride, uint32_t max_pages, uint32_t n_rows,
+                  int32_t *lens, int32_t *refs, const int32_t *seqs, const int32_t *n_new, uint32_t n, void *stream);
+int q8_kv_fork(const q8_kv_cache *c, int32_t *table, uint64_t table_stride, uint32_t max_pages, uint32_t n_rows,
+               int32_t *lens, int32_t *refs, const int32_t *src, const int32_t *dst, uint32_t n, void *stream);
+int q8_kv_free(const q8_kv_cache *c, int32_t *table, uint64_t table_stride, uint32_t max_pages, uint32_t n_rows,
+               int32_t *lens, int32_t *refs, const int32_t *seqs, uint32_t n, void *stream);
+int q8_kv_compact(const q8_kv_cache *c, int32_t *table_out, const int32_t *table, uint64_t table_stride,
+                  uint32_t max_pages, uint32_t n_rows, int32_t *refs_out, const int32_t *refs, int32_t *n_used,
+                  void *stream);
+int q8_kv_copy(const q8_kv_cache *c, const int32_t *src, const int32_t *dst, uint32_t n, void *stream);
+
+/*
  * Optional load-time repack of Q8_0 rows into a kernel-friendly layout (the
  * ROCm MXFP4 work on the pages found 16-byte aligned value slices with a
  * separate scale array fastest: GPU concepts page, §4c).  The repack copies or
@@ -358,9 +517,10 @@ int q8_matmul_noalloc(float *out, const void *W, uint64_t in_dim, uint64_t out_d
 
 /*
  * Synchronises `stream`, then returns and clears the device error word of
- * the current device: Q8_OK, Q8_ERANGE (an expert id was out of range) or
- * Q8_ETIMEOUT (a bounded wait inside a kernel expired), or Q8_ECUDA when the
- * synchronisation itself failed.
+ * the current device: Q8_OK, Q8_ERANGE (an expert id or a cache index was out
+ * of range), Q8_ENOPAGE (too few free cache pages) or Q8_ETIMEOUT (a bounded
+ * wait inside a kernel expired), or Q8_ECUDA when the synchronisation itself
+ * failed.
  */
 int q8_last_error(void *stream);
 
@@ -369,7 +529,7 @@ int q8_last_error(void *stream);
 const char *q8_last_cuda_error(void);
 
 /* Scratch bytes currently held on the current device, the staging buffer of
- * q8_matmul_host included (0 if none). */
+ * q8_matmul_host and the counters of q8_attn_decode included (0 if none). */
 uint64_t q8_scratch_bytes(void);
 
 /* Frees the scratch and staging buffers of every device (synchronises each first). */

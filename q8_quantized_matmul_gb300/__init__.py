@@ -20,10 +20,12 @@ LIB_PATH = os.path.join(_PKG, "libq8.so")
 QK = 32
 QB = 34
 Q8_OK, Q8_EINVAL, Q8_EALIGN, Q8_ERANGE, Q8_ENOMEM, Q8_ECUDA, Q8_ETIMEOUT, Q8_ESCRATCH = 0, -1, -2, -3, -4, -5, -6, -7
+Q8_ENOPAGE = -8
 Q8_NOALLOC_SCRATCH_BYTES = 4 << 20
 Q8_LAYOUT_PLANES, Q8_LAYOUT_TC = 0, 1
 Q8_KQ_Q2_K, Q8_KQ_Q4_K = 2, 4
 Q8_Q8K_BLOCK_BYTES = 292
+Q8_TYPE_F32, Q8_TYPE_F16, Q8_TYPE_BF16, Q8_TYPE_Q8_0 = 0, 1, 2, 8
 
 # Every symbol include/q8.h declares.
 EXPORTS = ("q8_version", "q8_strerror", "q8_quantize_act", "q8_matmul", "q8_matmul_q", "q8_moe_matmul",
@@ -31,7 +33,17 @@ EXPORTS = ("q8_version", "q8_strerror", "q8_quantize_act", "q8_matmul", "q8_matm
            "q8_release", "q8_debug_fail_next_alloc", "q8_profile_arm", "q8_profile_used", "q8_profile_read",
            "q8_matmul_noalloc", "q8_last_cuda_error", "q8_matmul_host", "q8_moe_ffn", "q8_swiglu",
            "q8_moe_combine", "q8_rmsnorm_quantize", "q8_debug_expire_waits", "q8_kq_row_bytes",
-           "q8_quantize_q8k", "q8_kq_matmul", "q8_kq_moe_matmul")
+           "q8_quantize_q8k", "q8_kq_matmul", "q8_kq_moe_matmul", "q8_kv_page_bytes", "q8_kv_append",
+           "q8_attn_decode", "q8_attn_prompt", "q8_kv_reserve", "q8_kv_fork", "q8_kv_free", "q8_kv_compact",
+           "q8_kv_copy")
+
+
+class KVCacheStruct(ctypes.Structure):
+    """q8_kv_cache of include/q8.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("layer_stride", ctypes.c_uint64),
+                ("page_stride", ctypes.c_uint64), ("n_layers", ctypes.c_uint32), ("n_pages", ctypes.c_uint32),
+                ("page_tokens", ctypes.c_uint32), ("n_kv_heads", ctypes.c_uint32), ("head_dim", ctypes.c_uint32),
+                ("type", ctypes.c_int32)]
 
 
 class Q8Error(RuntimeError):
@@ -47,6 +59,7 @@ def _load() -> ctypes.CDLL:
                           "(nvcc, sm_103a); there is no fallback path")
     L = ctypes.CDLL(LIB_PATH)
     vp, u64, u32, i32 = ctypes.c_void_p, ctypes.c_uint64, ctypes.c_uint32, ctypes.c_int
+    f32, cache = ctypes.c_float, ctypes.POINTER(KVCacheStruct)
     sig = {
         "q8_version": ([], i32),
         "q8_strerror": ([i32], ctypes.c_char_p),
@@ -77,6 +90,17 @@ def _load() -> ctypes.CDLL:
         "q8_quantize_q8k": ([vp, vp, u64, u64, vp], i32),
         "q8_kq_matmul": ([vp, vp, i32, u64, u64, vp, u64, vp], i32),
         "q8_kq_moe_matmul": ([vp, vp, i32, u32, u64, vp, u32, u64, u64, vp, i32, u64, vp], i32),
+        "q8_kv_page_bytes": ([i32, u32, u32, u32], u64),
+        "q8_kv_append": ([vp, vp, vp, i32, cache, u32, vp, u64, vp, u64, vp, u64, u32, u32, u32, vp, vp, vp, u64, u32,
+                          u32, vp, u32, u32, i32, u64, vp], i32),
+        "q8_attn_decode": ([vp, i32, vp, vp, u64, i32, cache, u32, vp, u64, u32, vp, u32, u32, f32, u32, vp, vp], i32),
+        "q8_attn_prompt": ([vp, i32, vp, vp, vp, vp, i32, u64, u64, u64, vp, vp, u32, u64, u64, u32, u32, u32, f32, u32,
+                            vp, vp], i32),
+        "q8_kv_reserve": ([cache, vp, u64, u32, u32, vp, vp, vp, vp, u32, vp], i32),
+        "q8_kv_fork": ([cache, vp, u64, u32, u32, vp, vp, vp, vp, u32, vp], i32),
+        "q8_kv_free": ([cache, vp, u64, u32, u32, vp, vp, vp, u32, vp], i32),
+        "q8_kv_compact": ([cache, vp, vp, u64, u32, u32, vp, vp, vp, vp], i32),
+        "q8_kv_copy": ([cache, vp, vp, u32, vp], i32),
     }
     for name, (args, res) in sig.items():
         f = getattr(L, name)
@@ -197,6 +221,61 @@ def q8_kq_moe_matmul(out, W_experts, fmt: int, n_expert: int, expert_stride_byte
                      in_dim: int, out_dim: int, x, x_per_pair: int, n_tok: int, stream=None) -> int:
     return _get().q8_kq_moe_matmul(_p(out), _p(W_experts), fmt, n_expert, expert_stride_bytes, _p(expert_ids), k,
                                    in_dim, out_dim, _p(x), x_per_pair, n_tok, _s(stream))
+
+
+def q8_kv_page_bytes(type: int, page_tokens: int, n_kv_heads: int, head_dim: int) -> int:
+    return _get().q8_kv_page_bytes(type, page_tokens, n_kv_heads, head_dim)
+
+
+def q8_kv_append(q_out, k_out, v_out, out_type: int, c, layer: int, q, q_stride: int, k, k_stride: int, v,
+                 v_stride: int, n_heads: int, n_kv_heads: int, head_dim: int, positions, seq_of, table,
+                 table_stride: int, max_pages: int, n_rows: int, cos_sin, n_pos: int, rot_dim: int, rope: int,
+                 n_tok: int, stream=None) -> int:
+    """c: a KVCacheStruct, or None (no cache write)."""
+    return _get().q8_kv_append(_p(q_out), _p(k_out), _p(v_out), out_type, c, layer, _p(q), q_stride, _p(k), k_stride,
+                               _p(v), v_stride, n_heads, n_kv_heads, head_dim, _p(positions), _p(seq_of), _p(table),
+                               table_stride, max_pages, n_rows, _p(cos_sin), n_pos, rot_dim, rope, n_tok, _s(stream))
+
+
+def q8_attn_decode(out, out_type: int, lse, q, q_stride: int, q_type: int, c, layer: int, table, table_stride: int,
+                   max_pages: int, seq_lens, n_seq: int, n_heads: int, scale: float, window: int, sinks,
+                   stream=None) -> int:
+    return _get().q8_attn_decode(_p(out), out_type, _p(lse), _p(q), q_stride, q_type, c, layer, _p(table), table_stride,
+                                 max_pages, _p(seq_lens), n_seq, n_heads, scale, window, _p(sinks), _s(stream))
+
+
+def q8_attn_prompt(out, out_type: int, lse, q, k, v, type: int, q_stride: int, k_stride: int, v_stride: int, q_start,
+                   k_start, n_seq: int, n_q: int, n_k: int, n_heads: int, n_kv_heads: int, head_dim: int, scale: float,
+                   window: int, sinks, stream=None) -> int:
+    return _get().q8_attn_prompt(_p(out), out_type, _p(lse), _p(q), _p(k), _p(v), type, q_stride, k_stride, v_stride,
+                                 _p(q_start), _p(k_start), n_seq, n_q, n_k, n_heads, n_kv_heads, head_dim, scale, window,
+                                 _p(sinks), _s(stream))
+
+
+def q8_kv_reserve(c, table, table_stride: int, max_pages: int, n_rows: int, lens, refs, seqs, n_new, n: int,
+                  stream=None) -> int:
+    return _get().q8_kv_reserve(c, _p(table), table_stride, max_pages, n_rows, _p(lens), _p(refs), _p(seqs), _p(n_new),
+                                n, _s(stream))
+
+
+def q8_kv_fork(c, table, table_stride: int, max_pages: int, n_rows: int, lens, refs, src, dst, n: int,
+               stream=None) -> int:
+    return _get().q8_kv_fork(c, _p(table), table_stride, max_pages, n_rows, _p(lens), _p(refs), _p(src), _p(dst), n,
+                             _s(stream))
+
+
+def q8_kv_free(c, table, table_stride: int, max_pages: int, n_rows: int, lens, refs, seqs, n: int, stream=None) -> int:
+    return _get().q8_kv_free(c, _p(table), table_stride, max_pages, n_rows, _p(lens), _p(refs), _p(seqs), n, _s(stream))
+
+
+def q8_kv_compact(c, table_out, table, table_stride: int, max_pages: int, n_rows: int, refs_out, refs, n_used,
+                  stream=None) -> int:
+    return _get().q8_kv_compact(c, _p(table_out), _p(table), table_stride, max_pages, n_rows, _p(refs_out), _p(refs),
+                                _p(n_used), _s(stream))
+
+
+def q8_kv_copy(c, src, dst, n: int, stream=None) -> int:
+    return _get().q8_kv_copy(c, _p(src), _p(dst), n, _s(stream))
 
 
 def q8_last_error(stream=None) -> int:
@@ -357,3 +436,202 @@ def kq_moe_matmul(W_experts, fmt: int, n_expert: int, expert_stride: int, ids, x
     _check(q8_kq_moe_matmul(out, W_experts, fmt, n_expert, expert_stride, ids, k, in_dim, out_dim, x,
                             int(x_per_pair), n_tok), "q8_kq_moe_matmul")
     return out
+
+
+# ------------------------------------------------------------------ paged key-value cache and attention
+class KVCache:
+    """A paged key-value cache over two tensors k and v of shape [n_layers, n_pages, ...] (layout of a page:
+    include/q8.h).  Inside a page the memory is contiguous; layers and pages may be strided, so k and v may be
+    slices of one tensor."""
+
+    def __init__(self, k, v, type: int, page_tokens: int, n_kv_heads: int, head_dim: int):
+        if k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride():
+            raise ValueError("k and v must have the same shape, type and strides")
+        size, want = k.element_size(), 1
+        for n, st in zip(reversed(k.shape[2:]), reversed(k.stride()[2:])):
+            if n != 1 and st != want:
+                raise ValueError("a page must be contiguous")
+            want *= n
+        page_bytes = q8_kv_page_bytes(type, page_tokens, n_kv_heads, head_dim)
+        if page_bytes == 0:
+            raise Q8Error(Q8_EINVAL, "q8_kv_page_bytes")
+        if want * size != page_bytes:
+            raise ValueError(f"a page has {want * size} bytes, its layout {page_bytes}")
+        self.k, self.v, self.type = k, v, type
+        self.page_tokens, self.n_kv_heads, self.head_dim = page_tokens, n_kv_heads, head_dim
+        n_layers, n_pages = k.shape[:2]
+        page_stride = k.stride(1) * size if n_pages > 1 else page_bytes
+        layer_stride = k.stride(0) * size if n_layers > 1 else n_pages * page_stride
+        self.struct = KVCacheStruct(k.data_ptr(), v.data_ptr(), layer_stride, page_stride, n_layers, n_pages,
+                                    page_tokens, n_kv_heads, head_dim, type)
+
+    @classmethod
+    def empty(cls, type: int, n_layers: int, n_pages: int, page_tokens: int, n_kv_heads: int, head_dim: int,
+              device="cuda"):
+        import torch
+        page_bytes = q8_kv_page_bytes(type, page_tokens, n_kv_heads, head_dim)
+        if page_bytes == 0:
+            raise Q8Error(Q8_EINVAL, "q8_kv_page_bytes")
+        k, v = (torch.zeros((n_layers, n_pages, page_bytes), dtype=torch.uint8, device=device) for _ in range(2))
+        return cls(k, v, type, page_tokens, n_kv_heads, head_dim)
+
+
+def _type_of(dtype) -> int:
+    import torch
+    t = {torch.float32: Q8_TYPE_F32, torch.float16: Q8_TYPE_F16, torch.bfloat16: Q8_TYPE_BF16}.get(dtype)
+    if t is None:
+        raise TypeError(f"{dtype}: float16, bfloat16 or float32 expected")
+    return t
+
+
+def _rows(t, heads_dim: int) -> int:
+    """Row stride of a [rows, heads, dim] tensor whose heads lie back to back."""
+    if t.stride(2) != 1 or (t.shape[1] != 1 and t.stride(1) != t.shape[2]):
+        raise ValueError("the heads of a row must lie back to back")
+    return t.stride(0) if t.shape[0] > 1 else heads_dim
+
+
+def _ints(**tensors) -> None:
+    import torch
+    for name, t in tensors.items():
+        if t is not None and (t.dtype != torch.int32 or not t.is_cuda or t.stride(-1) != 1 and t.shape[-1] > 1):
+            raise TypeError(f"{name}: int32 on the GPU with contiguous rows expected")
+
+
+def _out(q, heads: int, dim: int, out_type: int):
+    """Output tensor of an attention call: [rows, heads, dim], or [rows, heads, dim/32*34] Q8_0 blocks."""
+    import torch
+    if out_type == Q8_TYPE_Q8_0:
+        return torch.empty((q.shape[0], heads, dim // QK * QB), dtype=torch.uint8, device=q.device)
+    dtype = torch.float32 if out_type == Q8_TYPE_F32 else q.dtype
+    return torch.empty((q.shape[0], heads, dim), dtype=dtype, device=q.device)
+
+
+def _sinks(sinks, heads: int) -> None:
+    import torch
+    if sinks is not None and (sinks.dtype != torch.float32 or sinks.numel() != heads or not sinks.is_contiguous()):
+        raise TypeError("sinks: contiguous float32 [heads] expected")
+
+
+def kv_append(cache, layer: int, q, k, v, positions, seq_of, table, cos_sin=None, rope: int = 0, dtype=None,
+              want_kv: bool = False):
+    """Rotate and store new tokens.  q [n, heads, dim] or None, k and v [n, kv_heads, dim] float32 (heads back to
+    back, rows strided), positions and seq_of int32 [n], table int32 [rows, max_pages]; cos_sin float32
+    [n_pos, rot_dim], rope 1 (halves) or 2 (adjacent pairs); cache None: no store.
+    Returns q in `dtype` (the cache's 16-bit type, else bfloat16), or (q, k, v) with want_kv."""
+    import torch
+    n, kv_heads, dim = k.shape
+    heads = 0 if q is None else q.shape[1]
+    if any(t is not None and t.dtype != torch.float32 for t in (q, k, v, cos_sin)):
+        raise TypeError("q, k, v and cos_sin: float32 expected")
+    if v.shape != k.shape or (q is not None and (q.shape[0] != n or q.shape[2] != dim)) or positions.numel() != n:
+        raise ValueError("q, k, v and positions disagree")
+    if cache is not None and (seq_of is None or table is None or seq_of.numel() != n):
+        raise ValueError("a cache write needs seq_of and table")
+    if rope and (cos_sin is None or not cos_sin.is_contiguous()):
+        raise ValueError("rope needs a contiguous cos_sin")
+    _ints(positions=positions, seq_of=seq_of, table=table)
+    if dtype is None:
+        dtype = torch.float16 if cache is not None and cache.type == Q8_TYPE_F16 else torch.bfloat16
+    kind = _type_of(dtype)
+    q_out = None if q is None else torch.empty((n, heads, dim), dtype=dtype, device=q.device)
+    k_out, v_out = (torch.empty((n, kv_heads, dim), dtype=dtype, device=k.device) if want_kv else None
+                    for _ in range(2))
+    _check(q8_kv_append(q_out, k_out, v_out, kind, None if cache is None else cache.struct, layer, q,
+                        0 if q is None else _rows(q, heads * dim), k, _rows(k, kv_heads * dim), v,
+                        _rows(v, kv_heads * dim), heads, kv_heads, dim, positions, seq_of, table,
+                        0 if table is None else table.stride(0), 0 if table is None else table.shape[1],
+                        0 if table is None else table.shape[0], cos_sin, cos_sin.shape[0] if rope else 0,
+                        cos_sin.shape[1] if rope else 0, rope, n), "q8_kv_append")
+    return (q_out, k_out, v_out) if want_kv else q_out
+
+
+def attn_decode(q, cache, layer: int, table, seq_lens, scale=None, window: int = 0, sinks=None, out_type=None,
+                want_lse: bool = False):
+    """One new token per sequence: q [n_seq, heads, dim] 16 bit, table int32 [n_seq, max_pages], seq_lens int32
+    [n_seq] -> [n_seq, heads, dim] (and lse float32 [n_seq, heads])."""
+    import torch
+    n, heads, dim = q.shape
+    if dim != cache.head_dim or table.shape[0] != n or seq_lens.numel() != n:
+        raise ValueError("q, cache, table and seq_lens disagree")
+    _ints(table=table, seq_lens=seq_lens)
+    _sinks(sinks, heads)
+    kind = _type_of(q.dtype)
+    out_type = kind if out_type is None else out_type
+    out = _out(q, heads, dim, out_type)
+    lse = torch.empty((n, heads), dtype=torch.float32, device=q.device) if want_lse else None
+    _check(q8_attn_decode(out, out_type, lse, q, _rows(q, heads * dim), kind, cache.struct, layer, table,
+                          table.stride(0) if n > 1 else table.shape[1], table.shape[1], seq_lens, n, heads,
+                          dim ** -0.5 if scale is None else scale, window, sinks), "q8_attn_decode")
+    return (out, lse) if want_lse else out
+
+
+def attn_prompt(q, k, v, q_start, k_start=None, scale=None, window: int = 0, sinks=None, out_type=None,
+                want_lse: bool = False):
+    """Packed prompts: q [n_q, heads, dim], k and v [n_k, kv_heads, dim] 16 bit (rows strided, heads back to
+    back), q_start and k_start int32 [n_seq + 1] -> [n_q, heads, dim] (and lse float32 [n_q, heads])."""
+    import torch
+    n, heads, dim = q.shape
+    kv_heads = k.shape[1]
+    if k.shape != v.shape or k.shape[2] != dim or k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("q, k and v disagree")
+    if k_start is not None and k_start.numel() != q_start.numel():
+        raise ValueError("q_start and k_start disagree")
+    _ints(q_start=q_start, k_start=k_start)
+    _sinks(sinks, heads)
+    kind = _type_of(q.dtype)
+    out_type = kind if out_type is None else out_type
+    out = _out(q, heads, dim, out_type)
+    lse = torch.empty((n, heads), dtype=torch.float32, device=q.device) if want_lse else None
+    _check(q8_attn_prompt(out, out_type, lse, q, k, v, kind, _rows(q, heads * dim), _rows(k, kv_heads * dim),
+                          _rows(v, kv_heads * dim), q_start, k_start, q_start.numel() - 1, n, k.shape[0], heads,
+                          kv_heads, dim, dim ** -0.5 if scale is None else scale, window, sinks), "q8_attn_prompt")
+    return (out, lse) if want_lse else out
+
+
+def _table(cache, table, lens, refs):
+    """The table arguments of a page call, checked against the arrays beside it."""
+    _ints(table=table, lens=lens, refs=refs)
+    if lens.numel() != table.shape[0] or refs.numel() != cache.struct.n_pages:
+        raise ValueError("table, lens, refs and cache disagree")
+    return table, table.stride(0) if table.shape[0] > 1 else table.shape[1], table.shape[1], table.shape[0]
+
+
+def kv_reserve(cache, table, lens, refs, seqs, n_new) -> None:
+    """Pages for n_new[i] more tokens of row seqs[i]; lens grow (all int32 on the device)."""
+    _ints(seqs=seqs, n_new=n_new)
+    if n_new.numel() != seqs.numel():
+        raise ValueError("seqs and n_new disagree")
+    _check(q8_kv_reserve(cache.struct, *_table(cache, table, lens, refs), lens, refs, seqs, n_new, seqs.numel()), "q8_kv_reserve")
+
+
+def kv_fork(cache, table, lens, refs, src, dst) -> None:
+    """Row dst[i] becomes a copy of row src[i]: whole pages shared, a part-filled last page copied."""
+    _ints(src=src, dst=dst)
+    if src.numel() != dst.numel():
+        raise ValueError("src and dst disagree")
+    _check(q8_kv_fork(cache.struct, *_table(cache, table, lens, refs), lens, refs, src, dst, src.numel()), "q8_kv_fork")
+
+
+def kv_free(cache, table, lens, refs, seqs) -> None:
+    _ints(seqs=seqs)
+    _check(q8_kv_free(cache.struct, *_table(cache, table, lens, refs), lens, refs, seqs, seqs.numel()), "q8_kv_free")
+
+
+def kv_compact(cache, table, lens, refs):
+    """Moves the pages in use to the front of the pool -> (new table, new refs, number of pages in use)."""
+    import torch
+    t, stride, width, rows = _table(cache, table, lens, refs)
+    new_table = torch.empty_strided(t.shape, (stride, 1), dtype=torch.int32, device=t.device)
+    new_refs = torch.empty_like(refs)
+    used = torch.empty((), dtype=torch.int32, device=t.device)
+    _check(q8_kv_compact(cache.struct, new_table, t, stride, width, rows, new_refs, refs, used), "q8_kv_compact")
+    return new_table, new_refs, used
+
+
+def kv_copy(cache, src, dst) -> None:
+    """Page src[i] -> page dst[i] in all layers."""
+    _ints(src=src, dst=dst)
+    if src.numel() != dst.numel():
+        raise ValueError("src and dst disagree")
+    _check(q8_kv_copy(cache.struct, src, dst, src.numel()), "q8_kv_copy")

@@ -7,6 +7,7 @@
 #include "../../include/q8.h"
 #include "q8_common.cuh"
 #include "q8_kernels.h"
+#include "q8_kv.h"
 
 // Device error word (one per device context).  Kernels receive its address.
 __device__ int g_q8_device_error = 0;
@@ -24,6 +25,8 @@ struct DeviceState {
     size_t scratch_bytes = 0;
     void *stage = nullptr;       // device copies of host activations and results (q8_matmul_host)
     size_t stage_bytes = 0;
+    int *counters = nullptr;     // attention: pieces that have arrived, one per unit, zero between calls
+    size_t counter_bytes = 0;
 };
 
 std::mutex g_mutex;
@@ -153,6 +156,23 @@ int reserve_buffer(void **buf, size_t *have, size_t bytes) {
 }
 
 int reserve_scratch(DeviceState *s, size_t bytes) { return reserve_buffer(&s->scratch, &s->scratch_bytes, bytes); }
+
+// At least n counters.  New ones are cleared on `st`; a call leaves every counter it used at zero.
+int reserve_counters(DeviceState *s, size_t n, cudaStream_t st) {
+    if (n * sizeof(int) <= s->counter_bytes) return Q8_OK;
+    void *buf = s->counters;
+    const int rc = reserve_buffer(&buf, &s->counter_bytes, n * sizeof(int));
+    s->counters = static_cast<int *>(buf);
+    if (rc) return rc;
+    const cudaError_t e = cudaMemsetAsync(buf, 0, s->counter_bytes, st);
+    if (e != cudaSuccess) {   // unusable until cleared: the next call allocates again
+        cudaFree(buf);
+        s->counters = nullptr;
+        s->counter_bytes = 0;
+        cudaGetLastError();
+    }
+    return status_of(e);
+}
 
 size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 
@@ -547,7 +567,7 @@ int record_cuda_status(cudaError_t e) {
 
 extern "C" {
 
-int q8_version(void) { return 10100; }
+int q8_version(void) { return 10200; }
 
 const char *q8_strerror(int status) {
     switch (status) {
@@ -558,6 +578,7 @@ const char *q8_strerror(int status) {
         case Q8_ENOMEM: return "scratch allocation failed";
         case Q8_ECUDA: return "CUDA runtime error";
         case Q8_ETIMEOUT: return "bounded wait expired inside a kernel";
+        case Q8_ENOPAGE: return "too few free cache pages or table entries";
         case Q8_ESCRATCH: return "call exceeds the fixed scratch of q8_matmul_noalloc";
         default: return "unknown status";
     }
@@ -1097,6 +1118,338 @@ int q8_kq_moe_matmul(float *out, const void *W_experts, int fmt, uint32_t n_expe
     }));
 }
 
+// ---- paged key-value cache and the attention over it
+
+// log2 of the tokens a page, or -1.
+static int page_shift_of(uint32_t page_tokens) {
+    for (int s = 4; s <= 8; ++s)
+        if (page_tokens == 1u << s) return s;
+    return -1;
+}
+
+static bool head_dim_ok(uint32_t d) { return d == 64 || d == 128 || d == 256 || d == 512; }
+static bool type16(int t) { return t == Q8_TYPE_F16 || t == Q8_TYPE_BF16; }
+static bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+constexpr uint32_t MAX_HEADS = 4096;
+constexpr uint32_t MAX_PAGES = 1u << 24;        // of a cache, and entries of a table row
+constexpr uint32_t MAX_SEQS = 1u << 20;
+
+uint64_t q8_kv_page_bytes(int type, uint32_t page_tokens, uint32_t n_kv_heads, uint32_t head_dim) {
+    if (page_shift_of(page_tokens) < 0 || !head_dim_ok(head_dim) || n_kv_heads == 0 || n_kv_heads > MAX_HEADS) return 0;
+    const uint64_t vals = (uint64_t)page_tokens * head_dim;
+    if (type16(type)) return vals * 2 * n_kv_heads;
+    if (type == Q8_TYPE_Q8_0) return (vals + vals / q8::QK * 2) * n_kv_heads;
+    return 0;
+}
+
+// A cache's fields, as the kernels take them.
+static int check_cache(const q8_kv_cache *c, q8::KvPool &k) {
+    if (!c) return Q8_EINVAL;
+    const uint64_t bytes = q8_kv_page_bytes(c->type, c->page_tokens, c->n_kv_heads, c->head_dim);
+    if (!bytes || !c->k || !c->v || c->n_layers == 0 || c->n_layers > 65536 || c->n_pages == 0 || c->n_pages > MAX_PAGES)
+        return Q8_EINVAL;
+    if (c->page_stride < bytes || c->page_stride > ((uint64_t)1 << 40) || c->layer_stride > ((uint64_t)1 << 46))
+        return Q8_EINVAL;
+    if (c->n_layers > 1 && c->layer_stride < bytes) return Q8_EINVAL;
+    if (!aligned16(c->k) || !aligned16(c->v) || (c->page_stride & 15u) || (c->layer_stride & 15u)) return Q8_EALIGN;
+    k.k = static_cast<uint8_t *>(c->k);
+    k.v = static_cast<uint8_t *>(c->v);
+    k.layer_stride = c->layer_stride;
+    k.page_stride = c->page_stride;
+    k.n_layers = c->n_layers;
+    k.n_pages = c->n_pages;
+    k.page_shift = (uint32_t)page_shift_of(c->page_tokens);
+    k.n_kv = c->n_kv_heads;
+    k.dim = c->head_dim;
+    k.type = c->type;
+    k.tile_bytes = (uint32_t)(bytes / c->n_kv_heads);
+    return Q8_OK;
+}
+
+static int check_table(const int32_t *table, uint64_t table_stride, uint32_t max_pages) {
+    if (!table || max_pages == 0 || max_pages > MAX_PAGES || table_stride < max_pages || table_stride > ((uint64_t)1 << 32))
+        return Q8_EINVAL;
+    return aligned4(table) ? Q8_OK : Q8_EALIGN;
+}
+
+int q8_kv_append(void *q_out, void *k_out, void *v_out, int out_type, const q8_kv_cache *c, uint32_t layer,
+                 const float *q, uint64_t q_stride, const float *k, uint64_t k_stride, const float *v,
+                 uint64_t v_stride, uint32_t n_heads, uint32_t n_kv_heads, uint32_t head_dim,
+                 const int32_t *positions, const int32_t *seq_of, const int32_t *table, uint64_t table_stride,
+                 uint32_t max_pages, uint32_t n_rows, const float *cos_sin, uint32_t n_pos, uint32_t rot_dim,
+                 int rope, uint64_t n_tok, void *stream) {
+    if (!head_dim_ok(head_dim) || n_kv_heads == 0 || n_kv_heads > MAX_HEADS || n_tok > ((uint64_t)1 << 31) - 1)
+        return Q8_EINVAL;
+    if (q_out && (n_heads == 0 || n_heads > MAX_HEADS)) return Q8_EINVAL;
+    if (!type16(out_type) || rope < 0 || rope > 2) return Q8_EINVAL;
+    if (rope && (rot_dim == 0 || rot_dim % 16 || rot_dim > head_dim || n_pos == 0)) return Q8_EINVAL;
+    q8::KvAppendParams p{};
+    int rc;
+    if (c) {
+        if ((rc = check_cache(c, p.c))) return rc;
+        if (layer >= c->n_layers || c->n_kv_heads != n_kv_heads || c->head_dim != head_dim || n_rows == 0) return Q8_EINVAL;
+        if ((rc = check_table(table, table_stride, max_pages))) return rc;
+        p.c.k += layer * c->layer_stride;
+        p.c.v += layer * c->layer_stride;
+    }
+    if (n_tok == 0) return Q8_OK;
+    if ((q_out && !q) || !k || !v || !positions || (c && !seq_of) || (rope && !cos_sin)) return Q8_EINVAL;
+    const uint64_t q_row = (uint64_t)n_heads * head_dim, kv_row = (uint64_t)n_kv_heads * head_dim, most = (uint64_t)1 << 32;
+    if ((q_out && (q_stride < q_row || q_stride > most)) || k_stride < kv_row || v_stride < kv_row || k_stride > most ||
+        v_stride > most)
+        return Q8_EINVAL;
+    if (!aligned16(q_out) || !aligned16(k_out) || !aligned16(v_out) || !aligned16(q) || !aligned16(k) || !aligned16(v) ||
+        (rope && !aligned16(cos_sin)) || !aligned4(positions) || !aligned4(seq_of) || (q_out && q_stride % 4) || k_stride % 4 ||
+        v_stride % 4)
+        return Q8_EALIGN;
+    std::lock_guard<std::mutex> lk(g_mutex);
+    DeviceState *s;
+    if ((rc = get_device(&s))) return rc;
+    p.q_out = q_out;
+    p.k_out = k_out;
+    p.v_out = v_out;
+    p.out_type = out_type;
+    p.q = q_out ? q : nullptr;
+    p.k = k;
+    p.v = v;
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.n_heads = n_heads;
+    p.n_kv = n_kv_heads;
+    p.dim = head_dim;
+    p.positions = positions;
+    p.seq_of = seq_of;
+    p.table = table;
+    p.table_stride = table_stride;
+    p.max_pages = max_pages;
+    p.n_rows = n_rows;
+    p.cos_sin = cos_sin;
+    p.n_pos = n_pos;
+    p.rot_dim = rot_dim;
+    p.rope = rope;
+    p.n_tok = n_tok;
+    p.err = s->err;
+    return status_of(q8::launch_kv_append(p, s->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+int q8_attn_decode(void *out, int out_type, float *lse, const void *q, uint64_t q_stride, int q_type,
+                   const q8_kv_cache *c, uint32_t layer, const int32_t *table, uint64_t table_stride,
+                   uint32_t max_pages, const int32_t *seq_lens, uint32_t n_seq, uint32_t n_heads, float scale,
+                   uint32_t window, const float *sinks, void *stream) {
+    q8::AttnDecodeParams p{};
+    int rc = check_cache(c, p.c);
+    if (rc) return rc;
+    if (layer >= c->n_layers || n_heads == 0 || n_heads > MAX_HEADS || n_heads % c->n_kv_heads || n_seq > MAX_SEQS)
+        return Q8_EINVAL;
+    if (!type16(q_type) || (c->type != Q8_TYPE_Q8_0 && c->type != q_type)) return Q8_EINVAL;
+    if (out_type != q_type && out_type != Q8_TYPE_F32 && out_type != Q8_TYPE_Q8_0) return Q8_EINVAL;
+    if (!(scale > 0.0f) || scale > 1e30f) return Q8_EINVAL;
+    if ((rc = check_table(table, table_stride, max_pages))) return rc;
+    if ((uint64_t)max_pages * c->page_tokens > ((uint64_t)1 << 30)) return Q8_EINVAL;   // positions are 32-bit
+    if (n_seq == 0) return Q8_OK;
+    if (!out || !q || !seq_lens) return Q8_EINVAL;
+    if (q_stride < (uint64_t)n_heads * c->head_dim || q_stride > ((uint64_t)1 << 32)) return Q8_EINVAL;
+    if (!aligned16(out) || !aligned16(q) || q_stride % 8 || !aligned4(lse) || !aligned4(seq_lens) || !aligned4(sinks))
+        return Q8_EALIGN;
+    std::lock_guard<std::mutex> lk(g_mutex);
+    DeviceState *s;
+    if ((rc = get_device(&s))) return rc;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    p.c.k += layer * c->layer_stride;
+    p.c.v += layer * c->layer_stride;
+    p.table = table;
+    p.lens = seq_lens;
+    p.table_stride = table_stride;
+    p.max_pages = max_pages;
+    p.n_seq = n_seq;
+    p.n_heads = n_heads;
+    p.group = n_heads / c->n_kv_heads;
+    p.mtiles = (p.group + 15) / 16;
+    p.q = q;
+    p.q_stride = q_stride;
+    p.q_type = q_type;
+    p.out = out;
+    p.out_type = out_type;
+    p.lse = lse;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.window = window;
+    p.sinks = sinks;
+    p.err = s->err;
+    const int grid = q8::attn_decode_grid(c->head_dim, c->type, s->num_sms);
+    if ((rc = reserve_counters(s, (size_t)n_seq * c->n_kv_heads * p.mtiles, st))) return rc;
+    const size_t part = align256((size_t)grid * 2 * 16 * c->head_dim * sizeof(float));
+    if ((rc = reserve_scratch(s, part + align256((size_t)grid * 2 * 16 * 2 * sizeof(float2))))) return rc;
+    Carver cv(s->scratch);
+    p.part = cv.take<float>(part);
+    p.part_ml = cv.take<float2>((size_t)grid * 2 * 16 * 2 * sizeof(float2));
+    p.counters = s->counters;
+    return status_of(q8::launch_attn_decode(p, grid, st));
+}
+
+int q8_attn_prompt(void *out, int out_type, float *lse, const void *q, const void *k, const void *v, int type,
+                   uint64_t q_stride, uint64_t k_stride, uint64_t v_stride, const int32_t *q_start,
+                   const int32_t *k_start, uint32_t n_seq, uint64_t n_q, uint64_t n_k, uint32_t n_heads,
+                   uint32_t n_kv_heads, uint32_t head_dim, float scale, uint32_t window, const float *sinks,
+                   void *stream) {
+    if (!head_dim_ok(head_dim) || n_kv_heads == 0 || n_heads == 0 || n_heads > MAX_HEADS || n_heads % n_kv_heads)
+        return Q8_EINVAL;
+    if (!type16(type) || (out_type != type && out_type != Q8_TYPE_F32 && out_type != Q8_TYPE_Q8_0)) return Q8_EINVAL;
+    if (!(scale > 0.0f) || scale > 1e30f || n_seq > MAX_SEQS) return Q8_EINVAL;
+    if (n_q > ((uint64_t)1 << 28) || n_k > ((uint64_t)1 << 28)) return Q8_EINVAL;
+    if (n_seq == 0 || n_q == 0) return Q8_OK;
+    if (!out || !q || !k || !v || !q_start) return Q8_EINVAL;
+    const uint64_t kv_row = (uint64_t)n_kv_heads * head_dim, most = (uint64_t)1 << 32;
+    if (q_stride < (uint64_t)n_heads * head_dim || k_stride < kv_row || v_stride < kv_row || q_stride > most ||
+        k_stride > most || v_stride > most)
+        return Q8_EINVAL;
+    if (!aligned16(out) || !aligned16(q) || !aligned16(k) || !aligned16(v) || q_stride % 8 || k_stride % 8 || v_stride % 8 ||
+        !aligned4(lse) || !aligned4(q_start) || !aligned4(k_start) || !aligned4(sinks))
+        return Q8_EALIGN;
+    std::lock_guard<std::mutex> lk(g_mutex);
+    DeviceState *s;
+    int rc;
+    if ((rc = get_device(&s))) return rc;
+    q8::AttnPromptParams p{};
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.type = type;
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.q_start = q_start;
+    p.k_start = k_start;
+    p.n_seq = n_seq;
+    p.n_q = (uint32_t)n_q;
+    p.n_k = (uint32_t)n_k;
+    p.n_heads = n_heads;
+    p.n_kv = n_kv_heads;
+    p.dim = head_dim;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.window = window;
+    p.sinks = sinks;
+    p.out = out;
+    p.out_type = out_type;
+    p.lse = lse;
+    p.err = s->err;
+    return status_of(q8::launch_attn_prompt(p, s->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+// Arguments that the page calls share; fills p but for its scratch.
+static int check_pages(q8::KvPagesParams &p, const q8_kv_cache *c, int32_t *table, uint64_t table_stride,
+                       uint32_t max_pages, uint32_t n_rows) {
+    int rc = check_cache(c, p.c);
+    if (rc) return rc;
+    if ((rc = check_table(table, table_stride, max_pages))) return rc;
+    if (n_rows == 0 || n_rows > MAX_SEQS || (uint64_t)max_pages * c->page_tokens > ((uint64_t)1 << 30)) return Q8_EINVAL;
+    p.table = table;
+    p.table_stride = table_stride;
+    p.max_pages = max_pages;
+    p.n_rows = n_rows;
+    return Q8_OK;
+}
+
+// Request lists and the arrays they change.
+static int check_requests(q8::KvPagesParams &p, int32_t *lens, int32_t *refs, const int32_t *a, const int32_t *b,
+                          bool two, uint32_t n) {
+    if (n > MAX_SEQS) return Q8_EINVAL;
+    if (n && (!lens || !refs || !a || (two && !b))) return Q8_EINVAL;
+    if (!aligned4(lens) || !aligned4(refs) || !aligned4(a) || !aligned4(b)) return Q8_EALIGN;
+    p.lens = lens;
+    p.refs = refs;
+    p.src = a;
+    p.dst = b;
+    p.n = n;
+    return Q8_OK;
+}
+
+// The device, and the plan's scratch.
+static int pages_device(q8::KvPagesParams &p, DeviceState **s, bool plan) {
+    int rc = get_device(s);
+    if (rc) return rc;
+    p.err = (*s)->err;
+    if (!plan) return Q8_OK;
+    if ((rc = reserve_scratch(*s, q8::kv_pages_scratch(p.n, p.c.n_pages)))) return rc;
+    q8::kv_pages_carve(p, (*s)->scratch);
+    return Q8_OK;
+}
+
+int q8_kv_reserve(const q8_kv_cache *c, int32_t *table, uint64_t table_stride, uint32_t max_pages, uint32_t n_rows,
+                  int32_t *lens, int32_t *refs, const int32_t *seqs, const int32_t *n_new, uint32_t n, void *stream) {
+    q8::KvPagesParams p{};
+    int rc;
+    if ((rc = check_pages(p, c, table, table_stride, max_pages, n_rows))) return rc;
+    if ((rc = check_requests(p, lens, refs, seqs, n_new, true, n))) return rc;
+    if (n == 0) return Q8_OK;
+    std::lock_guard<std::mutex> lk(g_mutex);
+    DeviceState *s;
+    if ((rc = pages_device(p, &s, true))) return rc;
+    return status_of(q8::launch_kv_reserve(p, s->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+int q8_kv_fork(const q8_kv_cache *c, int32_t *table, uint64_t table_stride, uint32_t max_pages, uint32_t n_rows,
+               int32_t *lens, int32_t *refs, const int32_t *src, const int32_t *dst, uint32_t n, void *stream) {
+    q8::KvPagesParams p{};
+    int rc;
+    if ((rc = check_pages(p, c, table, table_stride, max_pages, n_rows))) return rc;
+    if ((rc = check_requests(p, lens, refs, src, dst, true, n))) return rc;
+    if (n == 0) return Q8_OK;
+    std::lock_guard<std::mutex> lk(g_mutex);
+    DeviceState *s;
+    if ((rc = pages_device(p, &s, true))) return rc;
+    return status_of(q8::launch_kv_fork(p, s->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+int q8_kv_free(const q8_kv_cache *c, int32_t *table, uint64_t table_stride, uint32_t max_pages, uint32_t n_rows,
+               int32_t *lens, int32_t *refs, const int32_t *seqs, uint32_t n, void *stream) {
+    q8::KvPagesParams p{};
+    int rc;
+    if ((rc = check_pages(p, c, table, table_stride, max_pages, n_rows))) return rc;
+    if ((rc = check_requests(p, lens, refs, seqs, nullptr, false, n))) return rc;
+    if (n == 0) return Q8_OK;
+    std::lock_guard<std::mutex> lk(g_mutex);
+    DeviceState *s;
+    if ((rc = pages_device(p, &s, false))) return rc;
+    return status_of(q8::launch_kv_free(p, static_cast<cudaStream_t>(stream)));
+}
+
+int q8_kv_compact(const q8_kv_cache *c, int32_t *table_out, const int32_t *table, uint64_t table_stride,
+                  uint32_t max_pages, uint32_t n_rows, int32_t *refs_out, const int32_t *refs, int32_t *n_used,
+                  void *stream) {
+    q8::KvPagesParams p{};
+    int rc;
+    if ((rc = check_pages(p, c, const_cast<int32_t *>(table), table_stride, max_pages, n_rows))) return rc;
+    if (!table_out || !refs_out || !refs || !n_used || table_out == table || refs_out == refs) return Q8_EINVAL;
+    if (!aligned4(table_out) || !aligned4(refs_out) || !aligned4(refs) || !aligned4(n_used)) return Q8_EALIGN;
+    p.refs = const_cast<int32_t *>(refs);
+    p.table_out = table_out;
+    p.refs_out = refs_out;
+    p.n_used = n_used;
+    std::lock_guard<std::mutex> lk(g_mutex);
+    DeviceState *s;
+    if ((rc = pages_device(p, &s, true))) return rc;
+    return status_of(q8::launch_kv_compact(p, s->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+int q8_kv_copy(const q8_kv_cache *c, const int32_t *src, const int32_t *dst, uint32_t n, void *stream) {
+    q8::KvPagesParams p{};
+    int rc = check_cache(c, p.c);
+    if (rc) return rc;
+    if (n > MAX_PAGES) return Q8_EINVAL;
+    if (n == 0) return Q8_OK;
+    if (!src || !dst) return Q8_EINVAL;
+    if (!aligned4(src) || !aligned4(dst)) return Q8_EALIGN;
+    p.src = src;
+    p.dst = dst;
+    p.n = n;
+    std::lock_guard<std::mutex> lk(g_mutex);
+    DeviceState *s;
+    if ((rc = pages_device(p, &s, false))) return rc;
+    return status_of(q8::launch_kv_copy(p, s->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
 uint64_t q8_repack_bytes(uint64_t in_dim, uint64_t rows, int layout) {
     if (in_dim == 0 || in_dim % q8::QK || check_dims(in_dim, rows, 1)) return 0;
     const uint64_t nb = in_dim / q8::QK;
@@ -1191,7 +1544,7 @@ uint64_t q8_scratch_bytes(void) {
         cudaGetLastError();
         return 0;
     }
-    return g_dev[dev].scratch_bytes + g_dev[dev].stage_bytes;
+    return g_dev[dev].scratch_bytes + g_dev[dev].stage_bytes + g_dev[dev].counter_bytes;
 }
 
 void q8_release(void) {
@@ -1202,13 +1555,15 @@ void q8_release(void) {
         return;
     }
     for (int d = 0; d < MAX_DEVICES; ++d) {
-        if (!g_dev[d].scratch && !g_dev[d].stage) continue;
+        if (!g_dev[d].scratch && !g_dev[d].stage && !g_dev[d].counters) continue;
         cudaSetDevice(d);
         cudaDeviceSynchronize();
         cudaFree(g_dev[d].scratch);
         cudaFree(g_dev[d].stage);
+        cudaFree(g_dev[d].counters);
         g_dev[d].scratch = g_dev[d].stage = nullptr;
-        g_dev[d].scratch_bytes = g_dev[d].stage_bytes = 0;
+        g_dev[d].counters = nullptr;
+        g_dev[d].scratch_bytes = g_dev[d].stage_bytes = g_dev[d].counter_bytes = 0;
     }
     cudaSetDevice(cur);
 }

@@ -1,0 +1,129 @@
+// q8_attn_prompt.cuh -- what the prompt attention kernels share: which rows a CTA works on, which
+// keys they see, and the handling of values that are not finite where some rows may not see them.
+#pragma once
+
+#include "q8_attn.cuh"
+#include "q8_kv.h"
+
+namespace q8 {
+
+// Up to BM query rows of one sequence.
+struct PromptTile {
+    int q0, k0;          // first packed row of the sequence's queries / keys
+    int row0, rows;      // first query of the tile within the sequence, and how many
+    int lk, shift;       // keys; query i (of the sequence) sees keys up to i + shift
+
+    // newest and oldest key that row r of the tile sees (none: last < first)
+    __device__ __forceinline__ int last(int r) const { return row0 + r + shift; }
+    __device__ __forceinline__ int first(int r, uint32_t window) const {
+        const int64_t f = window ? (int64_t)last(r) - window + 1 : 0;
+        return f > 0 ? (int)f : 0;
+    }
+    __device__ __forceinline__ bool sees(int r, int key, uint32_t window) const {
+        return key <= last(r) && key >= first(r, window);
+    }
+    // Keys [key, key + n) that not every row of the tile sees.
+    __device__ __forceinline__ bool masked(int key, int n, uint32_t window) const {
+        return key + n - 1 > last(0) || key < first(rows - 1, window);
+    }
+};
+
+__device__ __forceinline__ int prompt_bound(const int32_t *start, uint32_t i, uint32_t n) {
+    return (int)min((uint32_t)max(start[i], 0), n);
+}
+
+// Tile `slot` of the packed sequences in tiles of BM query rows, the newest rows of the last sequence
+// first (their rows see the most keys, so the long tiles start first).  False: no such tile.
+// Called by a whole CTA (or THREADS of it that share barrier 1); sh: three ints of shared memory.
+template <int BM, int THREADS>
+__device__ __forceinline__ bool prompt_tile(const AttnPromptParams &p, uint32_t slot, PromptTile &w, int *sh) {
+    const int tid = threadIdx.x;
+    const int32_t *ks = p.k_start ? p.k_start : p.q_start;
+    if (tid == 0) sh[0] = -1;
+    __syncthreads();
+    // sequences from the last one on, THREADS at a time
+    int64_t before = 0;
+    for (uint32_t b = 0; b < p.n_seq; b += THREADS) {
+        const uint32_t i = b + tid, s = p.n_seq - 1 - i;
+        int tiles = 0;
+        if (tid < THREADS && i < p.n_seq) {
+            const int a = prompt_bound(p.q_start, s, p.n_q), e = prompt_bound(p.q_start, s + 1, p.n_q);
+            tiles = e > a ? (e - a + BM - 1) / BM : 0;
+            if (slot == 0 && blockIdx.y == 0 && blockIdx.z == 0) {
+                const int ka = prompt_bound(ks, s, p.n_k), ke = prompt_bound(ks, s + 1, p.n_k);
+                if (e < a || ke < ka || a != p.q_start[s] || e != p.q_start[s + 1] || ka != ks[s] || ke != ks[s + 1])
+                    raise_error(p.err, DEV_ERANGE);
+            }
+        }
+        // inclusive sum over the CTA
+        int sum = tiles;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, sum, o);
+            if ((tid & 31) >= o) sum += v;
+        }
+        if (tid < THREADS && (tid & 31) == 31) sh[1 + tid / 32] = sum;
+        __syncthreads();
+        int64_t at = before + sum - tiles;
+        for (int k = 0; k < THREADS / 32; ++k) {
+            if (k < tid / 32) at += sh[1 + k];
+            before += sh[1 + k];
+        }
+        if (tiles && slot >= at && slot < at + tiles) {
+            sh[0] = (int)s;
+            sh[THREADS / 32 + 1] = (int)(at + tiles - 1 - slot);   // newest tile first
+        }
+        __syncthreads();
+        if (sh[0] >= 0) break;
+    }
+    const int s = sh[0];
+    if (s < 0) return false;
+    const int tile = sh[THREADS / 32 + 1];
+    w.q0 = prompt_bound(p.q_start, s, p.n_q);
+    const int lq = prompt_bound(p.q_start, s + 1, p.n_q) - w.q0;
+    w.k0 = prompt_bound(ks, s, p.n_k);
+    w.lk = max(prompt_bound(ks, s + 1, p.n_k) - w.k0, 0);
+    w.row0 = tile * BM;
+    w.rows = min(BM, lq - w.row0);
+    w.shift = w.lk - lq;
+    return true;
+}
+
+// Sets 16-bit values that are not finite to zero; true if there were any.
+template <bool BF16> __device__ __forceinline__ bool prompt_scrub(uint4 &x) {
+    constexpr uint32_t E = BF16 ? 0x7f80u : 0x7c00u;
+    uint32_t *w = &x.x;
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if ((w[i] & E) == E) {
+            w[i] &= 0xffff0000u;
+            any = true;
+        }
+        if ((w[i] & (E << 16)) == E << 16) {
+            w[i] &= 0x0000ffffu;
+            any = true;
+        }
+    }
+    return any;
+}
+
+// Adds the values that prompt_scrub took out of the masked tiles (of BN keys) to a row that sees them:
+// an infinity or NaN that a query does see reaches its output.  v: the sequence's first value row, at
+// the 8 dims of y.
+template <bool BF16>
+__device__ __noinline__ void prompt_restore(const AttnPromptParams &p, const PromptTile &w, const uint16_t *v, int row, int BN,
+                                            float (&y)[8]) {
+    const int k1 = min(w.last(row), w.lk - 1);
+    for (int k = w.first(row, p.window); k <= k1; ++k) {
+        if (!w.masked(k / BN * BN, BN, p.window)) continue;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint16_t b = v[(uint64_t)k * p.v_stride + e];
+            const uint16_t E = BF16 ? 0x7f80 : 0x7c00;
+            if ((b & E) == E) y[e] += BF16 ? __uint_as_float((uint32_t)b << 16) : half_bits_to_float(b);
+        }
+    }
+}
+
+}  // namespace q8

@@ -1,0 +1,123 @@
+// q8_kv.h -- internal interface of the paged key-value cache and the attention over it.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace q8 {
+
+// One layer's pools (or, for the page kernels, layer 0's) as the kernels see them.
+struct KvPool {
+    uint8_t *k, *v;
+    uint64_t layer_stride, page_stride;   // bytes
+    uint32_t n_layers, n_pages;
+    uint32_t page_shift;                  // log2 of the tokens a page
+    uint32_t n_kv, dim;
+    int type;                             // Q8_TYPE_*
+    uint32_t tile_bytes;                  // one head's tile of a page
+};
+
+struct KvAppendParams {
+    KvPool c;                             // k == nullptr: no cache write
+    void *q_out, *k_out, *v_out;
+    int out_type;
+    const float *q, *k, *v;
+    uint64_t q_stride, k_stride, v_stride;
+    uint32_t n_heads, n_kv, dim;
+    const int32_t *positions, *seq_of, *table;
+    uint64_t table_stride;
+    uint32_t max_pages, n_rows;
+    const float *cos_sin;
+    uint32_t n_pos, rot_dim;
+    int rope;
+    uint64_t n_tok;
+    int *err;
+};
+cudaError_t launch_kv_append(const KvAppendParams &p, int num_sms, cudaStream_t st);
+
+struct KvPagesParams {
+    KvPool c;
+    int32_t *table;
+    uint64_t table_stride;
+    uint32_t max_pages, n_rows;
+    int32_t *lens, *refs;
+    const int32_t *src, *dst;             // requests (reserve: rows and token counts)
+    uint32_t n;
+    int32_t *table_out, *refs_out, *n_used;
+    // scratch: status word, moves, then the lists
+    int32_t *plan;                        // [0] moves in the lists, [1] requests granted
+    int32_t *from, *to;                   // page moves
+    int32_t *off;                         // reserve / fork: first new page of a request in `fresh`
+    int32_t *fresh;                       // reserve / fork: new pages, ascending
+    int *err;
+};
+// Scratch bytes behind plan .. fresh for n requests (compact: n = 0), and the carve-up.
+size_t kv_pages_scratch(uint32_t n, uint32_t n_pages);
+void kv_pages_carve(KvPagesParams &p, void *scratch);
+cudaError_t launch_kv_reserve(const KvPagesParams &p, int num_sms, cudaStream_t st);
+cudaError_t launch_kv_fork(const KvPagesParams &p, int num_sms, cudaStream_t st);
+cudaError_t launch_kv_free(const KvPagesParams &p, cudaStream_t st);
+cudaError_t launch_kv_compact(const KvPagesParams &p, int num_sms, cudaStream_t st);
+cudaError_t launch_kv_copy(const KvPagesParams &p, int num_sms, cudaStream_t st);
+
+struct AttnDecodeParams {
+    KvPool c;
+    const int32_t *table, *lens;
+    uint64_t table_stride;
+    uint32_t max_pages, n_seq, n_heads, group, mtiles;
+    const void *q;
+    uint64_t q_stride;
+    int q_type;
+    void *out;
+    int out_type;
+    float *lse;
+    float scale_log2;                     // scale * log2(e)
+    uint32_t window;
+    const float *sinks;
+    float *part;                          // partial outputs, [2 * grid][16][dim]
+    float2 *part_ml;                      // their maxima and sums, [2 * grid][16]
+    int *counters;                        // one per unit, zero between calls
+    int *err;
+};
+// CTAs that the decode kernel of this head size and format runs with (0: unsupported).
+int attn_decode_grid(uint32_t dim, int cache_type, int num_sms);
+cudaError_t launch_attn_decode(const AttnDecodeParams &p, int grid, cudaStream_t st);
+
+struct AttnPromptParams {
+    const void *q, *k, *v;
+    int type;
+    uint64_t q_stride, k_stride, v_stride;
+    const int32_t *q_start, *k_start;
+    uint32_t n_seq;
+    uint32_t n_q, n_k;
+    uint32_t n_heads, n_kv, dim;
+    float scale_log2;
+    uint32_t window;
+    const float *sinks;
+    void *out;
+    int out_type;
+    float *lse;
+    int *err;
+};
+cudaError_t launch_attn_prompt(const AttnPromptParams &p, int num_sms, cudaStream_t st);
+
+// Launch with programmatic stream serialisation: the kernel starts while the one before
+// it drains and waits (griddepcontrol.wait) before it reads or writes anything.
+template <class P>
+cudaError_t launch_dependent(void (*kernel)(const P), const P &p, dim3 grid, int threads, size_t smem,
+                             cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
+    return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+}  // namespace q8
