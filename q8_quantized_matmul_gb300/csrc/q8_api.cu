@@ -1334,7 +1334,8 @@ int q8_attn_prompt(void *out, int out_type, float *lse, const void *q, const voi
     p.out_type = out_type;
     p.lse = lse;
     p.err = s->err;
-    return status_of(q8::launch_attn_prompt(p, s->num_sms, static_cast<cudaStream_t>(stream)));
+    if (q8::attn_prompt_on_tc(head_dim, n_k)) take_expiry(p.wait_ns, p.withhold);
+    return status_of(q8::launch_attn_prompt(p, static_cast<cudaStream_t>(stream)));
 }
 
 // Arguments that the page calls share; fills p but for its scratch.

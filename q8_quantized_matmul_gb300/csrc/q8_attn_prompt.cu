@@ -33,7 +33,7 @@ template <int D, bool BF16> __global__ void __launch_bounds__(128) k_attn_prompt
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     grid_dep_wait();
     PromptTile w;
-    if (!prompt_tile<C::BM, 128>(p, blockIdx.x, w, sh)) return;
+    if (!prompt_tile<128>(p, C::BM, blockIdx.x, blockIdx.x + blockIdx.y + blockIdx.z == 0, w, sh)) return;
     const uint32_t head = blockIdx.y, kvh = head / (p.n_heads / p.n_kv);
     const int dv0 = blockIdx.z * C::DV;
     const uint16_t *qp = static_cast<const uint16_t *>(p.q) + (uint64_t)(w.q0 + w.row0) * p.q_stride + (uint64_t)head * D;
@@ -236,8 +236,8 @@ template <bool BF16> cudaError_t launch_type(const AttnPromptParams &p, cudaStre
 
 }  // namespace
 
-cudaError_t launch_attn_prompt(const AttnPromptParams &p, int num_sms, cudaStream_t st) {
-    (void)num_sms;
+cudaError_t launch_attn_prompt(const AttnPromptParams &p, cudaStream_t st) {
+    if (attn_prompt_on_tc(p.dim, p.n_k)) return launch_attn_prompt_tc(p, st);
     return p.type == Q8_TYPE_BF16 ? launch_type<true>(p, st) : launch_type<false>(p, st);
 }
 

@@ -34,9 +34,10 @@ __device__ __forceinline__ int prompt_bound(const int32_t *start, uint32_t i, ui
 
 // Tile `slot` of the packed sequences in tiles of BM query rows, the newest rows of the last sequence
 // first (their rows see the most keys, so the long tiles start first).  False: no such tile.
-// Called by a whole CTA (or THREADS of it that share barrier 1); sh: three ints of shared memory.
-template <int BM, int THREADS>
-__device__ __forceinline__ bool prompt_tile(const AttnPromptParams &p, uint32_t slot, PromptTile &w, int *sh) {
+// Called by a whole CTA of THREADS; sh: THREADS / 32 + 2 ints of shared memory.  report: raise bad starts.
+template <int THREADS>
+__device__ __forceinline__ bool prompt_tile(const AttnPromptParams &p, int BM, uint32_t slot, bool report, PromptTile &w,
+                                            int *sh) {
     const int tid = threadIdx.x;
     const int32_t *ks = p.k_start ? p.k_start : p.q_start;
     if (tid == 0) sh[0] = -1;
@@ -46,10 +47,10 @@ __device__ __forceinline__ bool prompt_tile(const AttnPromptParams &p, uint32_t 
     for (uint32_t b = 0; b < p.n_seq; b += THREADS) {
         const uint32_t i = b + tid, s = p.n_seq - 1 - i;
         int tiles = 0;
-        if (tid < THREADS && i < p.n_seq) {
+        if (i < p.n_seq) {
             const int a = prompt_bound(p.q_start, s, p.n_q), e = prompt_bound(p.q_start, s + 1, p.n_q);
             tiles = e > a ? (e - a + BM - 1) / BM : 0;
-            if (slot == 0 && blockIdx.y == 0 && blockIdx.z == 0) {
+            if (report) {
                 const int ka = prompt_bound(ks, s, p.n_k), ke = prompt_bound(ks, s + 1, p.n_k);
                 if (e < a || ke < ka || a != p.q_start[s] || e != p.q_start[s + 1] || ka != ks[s] || ke != ks[s + 1])
                     raise_error(p.err, DEV_ERANGE);
@@ -62,7 +63,7 @@ __device__ __forceinline__ bool prompt_tile(const AttnPromptParams &p, uint32_t 
             const int v = __shfl_up_sync(0xffffffffu, sum, o);
             if ((tid & 31) >= o) sum += v;
         }
-        if (tid < THREADS && (tid & 31) == 31) sh[1 + tid / 32] = sum;
+        if ((tid & 31) == 31) sh[1 + tid / 32] = sum;
         __syncthreads();
         int64_t at = before + sum - tiles;
         for (int k = 0; k < THREADS / 32; ++k) {

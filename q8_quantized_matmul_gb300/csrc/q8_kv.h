@@ -98,8 +98,14 @@ struct AttnPromptParams {
     int out_type;
     float *lse;
     int *err;
+    // Failure-detection test hook (tcgen05 kernel; zero in normal calls): see GemvParams
+    uint64_t wait_ns;
+    int withhold;
 };
-cudaError_t launch_attn_prompt(const AttnPromptParams &p, int num_sms, cudaStream_t st);
+// Whether a call runs on the tcgen05 kernel (heads of 64 or 128 values, some keys), else mma.sync.
+inline bool attn_prompt_on_tc(uint32_t dim, uint64_t n_k) { return dim <= 128 && n_k > 0; }
+cudaError_t launch_attn_prompt_tc(const AttnPromptParams &p, cudaStream_t st);
+cudaError_t launch_attn_prompt(const AttnPromptParams &p, cudaStream_t st);
 
 // Launch with programmatic stream serialisation: the kernel starts while the one before
 // it drains and waits (griddepcontrol.wait) before it reads or writes anything.

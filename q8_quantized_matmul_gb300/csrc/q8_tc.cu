@@ -45,6 +45,7 @@
 
 #include "q8_common.cuh"
 #include "q8_kernels.h"
+#include "q8_tcgen05.cuh"
 
 namespace q8 {
 
@@ -91,44 +92,6 @@ template <bool RAW> struct Cfg {
 };
 }  // namespace tc
 
-// ---------------------------------------------------------------- PTX wrappers
-__device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-            smem_addr(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_addr(bar))
-        : "memory");
-}
-
-__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
-        "[%5];" ::"r"(smem_addr(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
-        : "memory");
-}
-
-// Generic-proxy shared-memory writes -> visible to the tensor core (async proxy).
-__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-
-__device__ __forceinline__ void tc_commit(uint64_t *bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
-                 : "memory");
-}
-
-// D[tmem] (+)= A[smem] * B[smem]^T, fp16 inputs, fp32 accumulate.
-__device__ __forceinline__ void tc_mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                           uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
 // 16 lanes x 8 columns per repetition (NR repetitions, 8 columns apart): thread
 // t gets, per repetition g, (lane t/4, columns 8g + 2(t%4) and + 1) in v[4g],
 // v[4g+1] and the same columns of lane t/4 + 8 in v[4g+2], v[4g+3].
@@ -160,34 +123,6 @@ __device__ __forceinline__ void tc_ld16x256(uint32_t taddr, uint32_t (&v)[4 * NR
                      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
                      : "r"(taddr));
     }
-}
-
-__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-
-// No instruction: ties the registers of a finished tcgen05.ld to a point after
-// tcgen05.wait::ld, so that no use of them is scheduled before the wait.
-template <int N>
-__device__ __forceinline__ void tc_regs_ready(uint32_t (&v)[N]) {
-#pragma unroll
-    for (int i = 0; i < N; i += 4) asm volatile("" : "+r"(v[i]), "+r"(v[i + 1]), "+r"(v[i + 2]), "+r"(v[i + 3]));
-}
-
-// Shared-memory matrix descriptor: K-major tile with 128-byte swizzle, rows 128
-// bytes apart, 8-row groups 1024 bytes apart (the layout a 128-byte-swizzled
-// TMA box of 64 fp16 per row produces).
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
-    uint64_t d = 0;
-    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);          // start address
-    d |= (uint64_t)1 << 16;                            // leading byte offset (unused with swizzle)
-    d |= (uint64_t)(1024u >> 4) << 32;                 // stride byte offset: 8-row group
-    d |= (uint64_t)1 << 46;                            // descriptor version
-    d |= (uint64_t)2 << 61;                            // 128-byte swizzle
-    return d;
-}
-
-// Instruction descriptor: fp32 accumulate, fp16 A and B, both K-major, N x M.
-__host__ __device__ constexpr uint32_t tc_idesc(int m, int n) {
-    return (1u << 4) | (0u << 7) | (0u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
 // (a0, a1) += (v0, v1) * (x0, x1) * (w, w), accumulator pair in one 64-bit register.

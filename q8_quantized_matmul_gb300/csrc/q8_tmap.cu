@@ -62,6 +62,23 @@ bool encode_f16_tmap(CUtensorMap *map, const void *base, uint64_t cols, uint64_t
     return r == CUDA_SUCCESS;
 }
 
+// Strided rows of fp16 or bf16 [rows][cols] (row_stride elements apart) with a 128-byte-swizzled box of 64 x
+// box_rows: rows beyond the matrix read as zero.
+bool encode_rows16_tmap(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, uint64_t row_stride,
+                        uint32_t box_rows, bool bf16) {
+    if (!load_encoder()) return false;
+    if (rows == 0 || (row_stride * 2) % 16 || (reinterpret_cast<uintptr_t>(base) & 15u)) return false;
+    cuuint64_t dims[2] = {cols, rows};
+    cuuint64_t strides[1] = {row_stride * 2};
+    cuuint32_t box[2] = {64, box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    const CUresult r = g_encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                                const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 // fp32 rows cut into Q8_0 blocks: a [n_blocks][32] view of x (one 128-byte row
 // per block) with a box of box_blocks blocks and the 128-byte swizzle, so that in
 // shared memory the 16-byte chunk j of block b lies at chunk j ^ (b & 7) of the

@@ -360,3 +360,17 @@ def test_decode_agrees_with_the_last_prompt_row(q8):
     assert q8.q8_last_error() == 0
     # both within 2^-8 of the exact value in units of the weighted mean of |v| (below 1.2 for 200 normal values)
     assert (a - b).abs().max() <= 2 * 1.2 * 2.0 ** -8
+
+
+def test_attn_prompt_wait_expires(q8):
+    """The tcgen05 prompt attention with its producer withholding every copy: it reports Q8_ETIMEOUT, returns, and
+    the next call is right again."""
+    q = torch.randn(300, 2, 128, device=DEV).bfloat16()
+    start = torch.tensor([0, 300], dtype=torch.int32, device=DEV)
+    ref = q8.attn_prompt(q, q, q, start)
+    assert q8.q8_last_error() == 0
+    q8.q8_debug_expire_waits(1, 1_000_000)
+    q8.attn_prompt(q, q, q, start)
+    assert q8.q8_last_error() == q8.Q8_ETIMEOUT
+    assert torch.equal(q8.attn_prompt(q, q, q, start), ref)
+    assert q8.q8_last_error() == 0
