@@ -12,6 +12,7 @@ C status code (0 = Q8_OK).  ``Q8Error`` is raised by the ``*_checked`` helpers.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -135,10 +136,33 @@ def _p(t) -> int:
     return t.data_ptr()
 
 
+_torch = None
+
+
+def _t():
+    """torch, imported on first use."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
+_cuda = None
+
+
+def _current_stream() -> int:
+    # the raw handle: building a torch.cuda.Stream object for it takes 3 us, a tenth of a small call
+    global _cuda
+    if _cuda is None:
+        _t().cuda.init()
+        _cuda = _t()._C
+    return _cuda._cuda_getCurrentRawStream(_cuda._cuda_getDevice())
+
+
 def _s(stream) -> int:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -439,78 +463,101 @@ def kq_moe_matmul(W_experts, fmt: int, n_expert: int, expert_stride: int, ids, x
 
 
 # ------------------------------------------------------------------ paged key-value cache and attention
+# These calls take microseconds on the GPU, so the helpers do each look-up once and call the library directly.
+@functools.lru_cache(maxsize=None)
+def _page_bytes(type: int, page_tokens: int, n_kv_heads: int, head_dim: int) -> int:
+    n = q8_kv_page_bytes(type, page_tokens, n_kv_heads, head_dim)
+    if n == 0:
+        raise Q8Error(Q8_EINVAL, "q8_kv_page_bytes")
+    return n
+
+
 class KVCache:
     """A paged key-value cache over two tensors k and v of shape [n_layers, n_pages, ...] (layout of a page:
     include/q8.h).  Inside a page the memory is contiguous; layers and pages may be strided, so k and v may be
     slices of one tensor."""
 
     def __init__(self, k, v, type: int, page_tokens: int, n_kv_heads: int, head_dim: int):
-        if k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride():
+        page_bytes = _page_bytes(type, page_tokens, n_kv_heads, head_dim)
+        shape, strides, size = k.shape, k.stride(), k.element_size()
+        if shape != v.shape or k.dtype != v.dtype or strides != v.stride():
             raise ValueError("k and v must have the same shape, type and strides")
-        size, want = k.element_size(), 1
-        for n, st in zip(reversed(k.shape[2:]), reversed(k.stride()[2:])):
-            if n != 1 and st != want:
+        want = 1
+        for i in range(len(shape) - 1, 1, -1):
+            if strides[i] != want and shape[i] != 1:
                 raise ValueError("a page must be contiguous")
-            want *= n
-        page_bytes = q8_kv_page_bytes(type, page_tokens, n_kv_heads, head_dim)
-        if page_bytes == 0:
-            raise Q8Error(Q8_EINVAL, "q8_kv_page_bytes")
+            want *= shape[i]
         if want * size != page_bytes:
             raise ValueError(f"a page has {want * size} bytes, its layout {page_bytes}")
         self.k, self.v, self.type = k, v, type
         self.page_tokens, self.n_kv_heads, self.head_dim = page_tokens, n_kv_heads, head_dim
-        n_layers, n_pages = k.shape[:2]
-        page_stride = k.stride(1) * size if n_pages > 1 else page_bytes
-        layer_stride = k.stride(0) * size if n_layers > 1 else n_pages * page_stride
-        self.struct = KVCacheStruct(k.data_ptr(), v.data_ptr(), layer_stride, page_stride, n_layers, n_pages,
+        n_layers, self.n_pages = shape[0], shape[1]
+        page_stride = strides[1] * size if shape[1] > 1 else page_bytes
+        layer_stride = strides[0] * size if n_layers > 1 else self.n_pages * page_stride
+        self.struct = KVCacheStruct(k.data_ptr(), v.data_ptr(), layer_stride, page_stride, n_layers, self.n_pages,
                                     page_tokens, n_kv_heads, head_dim, type)
 
     @classmethod
     def empty(cls, type: int, n_layers: int, n_pages: int, page_tokens: int, n_kv_heads: int, head_dim: int,
               device="cuda"):
-        import torch
-        page_bytes = q8_kv_page_bytes(type, page_tokens, n_kv_heads, head_dim)
-        if page_bytes == 0:
-            raise Q8Error(Q8_EINVAL, "q8_kv_page_bytes")
+        page_bytes = _page_bytes(type, page_tokens, n_kv_heads, head_dim)
+        torch = _t()
         k, v = (torch.zeros((n_layers, n_pages, page_bytes), dtype=torch.uint8, device=device) for _ in range(2))
         return cls(k, v, type, page_tokens, n_kv_heads, head_dim)
 
 
 def _type_of(dtype) -> int:
-    import torch
-    t = {torch.float32: Q8_TYPE_F32, torch.float16: Q8_TYPE_F16, torch.bfloat16: Q8_TYPE_BF16}.get(dtype)
+    torch = _t()
+    if dtype is torch.bfloat16:
+        return Q8_TYPE_BF16
+    if dtype is torch.float16:
+        return Q8_TYPE_F16
+    raise TypeError(f"{dtype}: float16 or bfloat16 expected")
+
+
+def _rows(t, name: str) -> int:
+    """Row stride of a [rows, heads, dim] GPU tensor whose heads lie back to back."""
+    (n, heads, dim), (r, h, d) = t.shape, t.stride()
+    if d != 1 or (h != dim and heads != 1) or not t.is_cuda:
+        raise ValueError(f"{name}: a GPU tensor whose heads lie back to back expected")
+    return r if n > 1 else heads * dim
+
+
+def _i32(t, name: str) -> int:
+    """Pointer of a contiguous int32 GPU tensor (0 for None)."""
     if t is None:
-        raise TypeError(f"{dtype}: float16, bfloat16 or float32 expected")
-    return t
+        return 0
+    if t.dtype is not _t().int32 or not t.is_cuda or not t.is_contiguous():
+        raise TypeError(f"{name}: contiguous int32 on the GPU expected")
+    return t.data_ptr()
 
 
-def _rows(t, heads_dim: int) -> int:
-    """Row stride of a [rows, heads, dim] tensor whose heads lie back to back."""
-    if t.stride(2) != 1 or (t.shape[1] != 1 and t.stride(1) != t.shape[2]):
-        raise ValueError("the heads of a row must lie back to back")
-    return t.stride(0) if t.shape[0] > 1 else heads_dim
+def _table(table):
+    """Pointer, row stride, columns and rows of a table."""
+    (rows, width), (stride, one) = table.shape, table.stride()
+    if table.dtype is not _t().int32 or not table.is_cuda or (one != 1 and width != 1):
+        raise TypeError("table: int32 [rows, max_pages] on the GPU with contiguous rows expected")
+    return table.data_ptr(), stride if rows > 1 else width, width, rows
 
 
-def _ints(**tensors) -> None:
-    import torch
-    for name, t in tensors.items():
-        if t is not None and (t.dtype != torch.int32 or not t.is_cuda or t.stride(-1) != 1 and t.shape[-1] > 1):
-            raise TypeError(f"{name}: int32 on the GPU with contiguous rows expected")
-
-
-def _out(q, heads: int, dim: int, out_type: int):
-    """Output tensor of an attention call: [rows, heads, dim], or [rows, heads, dim/32*34] Q8_0 blocks."""
-    import torch
+def _out(q, rows: int, heads: int, dim: int, kind: int, out_type):
+    """Output of an attention call and its type: [rows, heads, dim], or [rows, heads, dim/32*34] Q8_0 blocks."""
+    if out_type is None or out_type == kind:
+        return _t().empty((rows, heads, dim), dtype=q.dtype, device=q.device), kind
+    torch = _t()
     if out_type == Q8_TYPE_Q8_0:
-        return torch.empty((q.shape[0], heads, dim // QK * QB), dtype=torch.uint8, device=q.device)
-    dtype = torch.float32 if out_type == Q8_TYPE_F32 else q.dtype
-    return torch.empty((q.shape[0], heads, dim), dtype=dtype, device=q.device)
+        return torch.empty((rows, heads, dim // QK * QB), dtype=torch.uint8, device=q.device), out_type
+    if out_type == Q8_TYPE_F32:
+        return torch.empty((rows, heads, dim), dtype=torch.float32, device=q.device), out_type
+    raise Q8Error(Q8_EINVAL, "out_type")
 
 
-def _sinks(sinks, heads: int) -> None:
-    import torch
-    if sinks is not None and (sinks.dtype != torch.float32 or sinks.numel() != heads or not sinks.is_contiguous()):
-        raise TypeError("sinks: contiguous float32 [heads] expected")
+def _sinks(sinks, heads: int) -> int:
+    if sinks is None:
+        return 0
+    if sinks.dtype is not _t().float32 or sinks.numel() != heads or not sinks.is_contiguous() or not sinks.is_cuda:
+        raise TypeError("sinks: contiguous float32 [heads] on the GPU expected")
+    return sinks.data_ptr()
 
 
 def kv_append(cache, layer: int, q, k, v, positions, seq_of, table, cos_sin=None, rope: int = 0, dtype=None,
@@ -519,30 +566,45 @@ def kv_append(cache, layer: int, q, k, v, positions, seq_of, table, cos_sin=None
     back, rows strided), positions and seq_of int32 [n], table int32 [rows, max_pages]; cos_sin float32
     [n_pos, rot_dim], rope 1 (halves) or 2 (adjacent pairs); cache None: no store.
     Returns q in `dtype` (the cache's 16-bit type, else bfloat16), or (q, k, v) with want_kv."""
-    import torch
+    torch = _t()
+    f32 = torch.float32
     n, kv_heads, dim = k.shape
-    heads = 0 if q is None else q.shape[1]
-    if any(t is not None and t.dtype != torch.float32 for t in (q, k, v, cos_sin)):
-        raise TypeError("q, k, v and cos_sin: float32 expected")
-    if v.shape != k.shape or (q is not None and (q.shape[0] != n or q.shape[2] != dim)) or positions.numel() != n:
-        raise ValueError("q, k, v and positions disagree")
-    if cache is not None and (seq_of is None or table is None or seq_of.numel() != n):
-        raise ValueError("a cache write needs seq_of and table")
-    if rope and (cos_sin is None or not cos_sin.is_contiguous()):
-        raise ValueError("rope needs a contiguous cos_sin")
-    _ints(positions=positions, seq_of=seq_of, table=table)
+    if k.dtype is not f32 or v.dtype is not f32:
+        raise TypeError("k and v: float32 expected")
+    if v.shape != k.shape or positions.shape[0] != n:
+        raise ValueError("k, v and positions disagree")
     if dtype is None:
         dtype = torch.float16 if cache is not None and cache.type == Q8_TYPE_F16 else torch.bfloat16
     kind = _type_of(dtype)
-    q_out = None if q is None else torch.empty((n, heads, dim), dtype=dtype, device=q.device)
-    k_out, v_out = (torch.empty((n, kv_heads, dim), dtype=dtype, device=k.device) if want_kv else None
-                    for _ in range(2))
-    _check(q8_kv_append(q_out, k_out, v_out, kind, None if cache is None else cache.struct, layer, q,
-                        0 if q is None else _rows(q, heads * dim), k, _rows(k, kv_heads * dim), v,
-                        _rows(v, kv_heads * dim), heads, kv_heads, dim, positions, seq_of, table,
-                        0 if table is None else table.stride(0), 0 if table is None else table.shape[1],
-                        0 if table is None else table.shape[0], cos_sin, cos_sin.shape[0] if rope else 0,
-                        cos_sin.shape[1] if rope else 0, rope, n), "q8_kv_append")
+    q_out, qp, qs, qo, heads = None, 0, 0, 0, 0
+    if q is not None:
+        heads = q.shape[1]
+        if q.dtype is not f32:
+            raise TypeError("q: float32 expected")
+        if q.shape[0] != n or q.shape[2] != dim:
+            raise ValueError("q and k disagree")
+        q_out = torch.empty((n, heads, dim), dtype=dtype, device=q.device)
+        qp, qs, qo = q.data_ptr(), _rows(q, "q"), q_out.data_ptr()
+    k_out = v_out = None
+    ko = vo = 0
+    if want_kv:
+        k_out, v_out = (torch.empty((n, kv_heads, dim), dtype=dtype, device=k.device) for _ in range(2))
+        ko, vo = k_out.data_ptr(), v_out.data_ptr()
+    struct, seq, tab = None, 0, (0, 0, 0, 0)
+    if cache is not None:
+        if seq_of is None or table is None or seq_of.shape[0] != n:
+            raise ValueError("a cache write needs seq_of [n] and table")
+        struct, seq, tab = cache.struct, _i32(seq_of, "seq_of"), _table(table)
+    cs, n_pos, rot = 0, 0, 0
+    if rope:
+        if cos_sin is None or cos_sin.dtype is not f32 or not cos_sin.is_contiguous() or not cos_sin.is_cuda:
+            raise ValueError("rope needs a contiguous float32 cos_sin on the GPU")
+        cs, (n_pos, rot) = cos_sin.data_ptr(), cos_sin.shape
+    rc = _get().q8_kv_append(qo, ko, vo, kind, struct, layer, qp, qs, k.data_ptr(), _rows(k, "k"), v.data_ptr(),
+                             _rows(v, "v"), heads, kv_heads, dim, _i32(positions, "positions"), seq, *tab, cs, n_pos,
+                             rot, rope, n, _current_stream())
+    if rc:
+        raise Q8Error(rc, "q8_kv_append")
     return (q_out, k_out, v_out) if want_kv else q_out
 
 
@@ -550,19 +612,18 @@ def attn_decode(q, cache, layer: int, table, seq_lens, scale=None, window: int =
                 want_lse: bool = False):
     """One new token per sequence: q [n_seq, heads, dim] 16 bit, table int32 [n_seq, max_pages], seq_lens int32
     [n_seq] -> [n_seq, heads, dim] (and lse float32 [n_seq, heads])."""
-    import torch
     n, heads, dim = q.shape
-    if dim != cache.head_dim or table.shape[0] != n or seq_lens.numel() != n:
+    if dim != cache.head_dim or table.shape[0] != n or seq_lens.shape[0] != n:
         raise ValueError("q, cache, table and seq_lens disagree")
-    _ints(table=table, seq_lens=seq_lens)
-    _sinks(sinks, heads)
+    tab, stride, width, _ = _table(table)
     kind = _type_of(q.dtype)
-    out_type = kind if out_type is None else out_type
-    out = _out(q, heads, dim, out_type)
-    lse = torch.empty((n, heads), dtype=torch.float32, device=q.device) if want_lse else None
-    _check(q8_attn_decode(out, out_type, lse, q, _rows(q, heads * dim), kind, cache.struct, layer, table,
-                          table.stride(0) if n > 1 else table.shape[1], table.shape[1], seq_lens, n, heads,
-                          dim ** -0.5 if scale is None else scale, window, sinks), "q8_attn_decode")
+    out, out_type = _out(q, n, heads, dim, kind, out_type)
+    lse = _t().empty((n, heads), dtype=_t().float32, device=q.device) if want_lse else None
+    rc = _get().q8_attn_decode(out.data_ptr(), out_type, lse.data_ptr() if want_lse else 0, q.data_ptr(), _rows(q, "q"),
+                               kind, cache.struct, layer, tab, stride, width, _i32(seq_lens, "seq_lens"), n, heads,
+                               dim ** -0.5 if scale is None else scale, window, _sinks(sinks, heads), _current_stream())
+    if rc:
+        raise Q8Error(rc, "q8_attn_decode")
     return (out, lse) if want_lse else out
 
 
@@ -570,68 +631,84 @@ def attn_prompt(q, k, v, q_start, k_start=None, scale=None, window: int = 0, sin
                 want_lse: bool = False):
     """Packed prompts: q [n_q, heads, dim], k and v [n_k, kv_heads, dim] 16 bit (rows strided, heads back to
     back), q_start and k_start int32 [n_seq + 1] -> [n_q, heads, dim] (and lse float32 [n_q, heads])."""
-    import torch
     n, heads, dim = q.shape
-    kv_heads = k.shape[1]
-    if k.shape != v.shape or k.shape[2] != dim or k.dtype != q.dtype or v.dtype != q.dtype:
+    n_k, kv_heads, k_dim = k.shape
+    dtype = q.dtype
+    if k.shape != v.shape or k_dim != dim or k.dtype is not dtype or v.dtype is not dtype:
         raise ValueError("q, k and v disagree")
-    if k_start is not None and k_start.numel() != q_start.numel():
+    n_start = q_start.shape[0]
+    if k_start is not None and k_start.shape[0] != n_start:
         raise ValueError("q_start and k_start disagree")
-    _ints(q_start=q_start, k_start=k_start)
-    _sinks(sinks, heads)
-    kind = _type_of(q.dtype)
-    out_type = kind if out_type is None else out_type
-    out = _out(q, heads, dim, out_type)
-    lse = torch.empty((n, heads), dtype=torch.float32, device=q.device) if want_lse else None
-    _check(q8_attn_prompt(out, out_type, lse, q, k, v, kind, _rows(q, heads * dim), _rows(k, kv_heads * dim),
-                          _rows(v, kv_heads * dim), q_start, k_start, q_start.numel() - 1, n, k.shape[0], heads,
-                          kv_heads, dim, dim ** -0.5 if scale is None else scale, window, sinks), "q8_attn_prompt")
+    kind = _type_of(dtype)
+    out, out_type = _out(q, n, heads, dim, kind, out_type)
+    lse = _t().empty((n, heads), dtype=_t().float32, device=q.device) if want_lse else None
+    rc = _get().q8_attn_prompt(out.data_ptr(), out_type, lse.data_ptr() if want_lse else 0, q.data_ptr(), k.data_ptr(),
+                               v.data_ptr(), kind, _rows(q, "q"), _rows(k, "k"), _rows(v, "v"),
+                               _i32(q_start, "q_start"), _i32(k_start, "k_start"), n_start - 1, n, n_k, heads, kv_heads,
+                               dim, dim ** -0.5 if scale is None else scale, window, _sinks(sinks, heads),
+                               _current_stream())
+    if rc:
+        raise Q8Error(rc, "q8_attn_prompt")
     return (out, lse) if want_lse else out
 
 
-def _table(cache, table, lens, refs):
-    """The table arguments of a page call, checked against the arrays beside it."""
-    _ints(table=table, lens=lens, refs=refs)
-    if lens.numel() != table.shape[0] or refs.numel() != cache.struct.n_pages:
+def _pages(cache, table, lens, refs):
+    """The arguments that the page calls share: pointer, row stride, columns and rows of the table, lens, refs."""
+    tab = _table(table)
+    if lens.shape[0] != tab[3] or refs.shape[0] != cache.n_pages:
         raise ValueError("table, lens, refs and cache disagree")
-    return table, table.stride(0) if table.shape[0] > 1 else table.shape[1], table.shape[1], table.shape[0]
+    return (*tab, _i32(lens, "lens"), _i32(refs, "refs"))
 
 
 def kv_reserve(cache, table, lens, refs, seqs, n_new) -> None:
     """Pages for n_new[i] more tokens of row seqs[i]; lens grow (all int32 on the device)."""
-    _ints(seqs=seqs, n_new=n_new)
-    if n_new.numel() != seqs.numel():
+    n = seqs.shape[0]
+    if n_new.shape[0] != n:
         raise ValueError("seqs and n_new disagree")
-    _check(q8_kv_reserve(cache.struct, *_table(cache, table, lens, refs), lens, refs, seqs, n_new, seqs.numel()), "q8_kv_reserve")
+    rc = _get().q8_kv_reserve(cache.struct, *_pages(cache, table, lens, refs), _i32(seqs, "seqs"), _i32(n_new, "n_new"),
+                              n, _current_stream())
+    if rc:
+        raise Q8Error(rc, "q8_kv_reserve")
 
 
 def kv_fork(cache, table, lens, refs, src, dst) -> None:
     """Row dst[i] becomes a copy of row src[i]: whole pages shared, a part-filled last page copied."""
-    _ints(src=src, dst=dst)
-    if src.numel() != dst.numel():
+    n = src.shape[0]
+    if dst.shape[0] != n:
         raise ValueError("src and dst disagree")
-    _check(q8_kv_fork(cache.struct, *_table(cache, table, lens, refs), lens, refs, src, dst, src.numel()), "q8_kv_fork")
+    rc = _get().q8_kv_fork(cache.struct, *_pages(cache, table, lens, refs), _i32(src, "src"), _i32(dst, "dst"), n,
+                           _current_stream())
+    if rc:
+        raise Q8Error(rc, "q8_kv_fork")
 
 
 def kv_free(cache, table, lens, refs, seqs) -> None:
-    _ints(seqs=seqs)
-    _check(q8_kv_free(cache.struct, *_table(cache, table, lens, refs), lens, refs, seqs, seqs.numel()), "q8_kv_free")
+    """Rows seqs give their pages back and become empty."""
+    rc = _get().q8_kv_free(cache.struct, *_pages(cache, table, lens, refs), _i32(seqs, "seqs"), seqs.shape[0],
+                           _current_stream())
+    if rc:
+        raise Q8Error(rc, "q8_kv_free")
 
 
 def kv_compact(cache, table, lens, refs):
     """Moves the pages in use to the front of the pool -> (new table, new refs, number of pages in use)."""
-    import torch
-    t, stride, width, rows = _table(cache, table, lens, refs)
-    new_table = torch.empty_strided(t.shape, (stride, 1), dtype=torch.int32, device=t.device)
+    torch = _t()
+    tab, stride, width, rows, _, rp = _pages(cache, table, lens, refs)
+    new_table = torch.empty_strided((rows, width), (stride, 1), dtype=torch.int32, device=table.device)
     new_refs = torch.empty_like(refs)
-    used = torch.empty((), dtype=torch.int32, device=t.device)
-    _check(q8_kv_compact(cache.struct, new_table, t, stride, width, rows, new_refs, refs, used), "q8_kv_compact")
+    used = torch.empty((), dtype=torch.int32, device=table.device)
+    rc = _get().q8_kv_compact(cache.struct, new_table.data_ptr(), tab, stride, width, rows, new_refs.data_ptr(), rp,
+                              used.data_ptr(), _current_stream())
+    if rc:
+        raise Q8Error(rc, "q8_kv_compact")
     return new_table, new_refs, used
 
 
 def kv_copy(cache, src, dst) -> None:
     """Page src[i] -> page dst[i] in all layers."""
-    _ints(src=src, dst=dst)
-    if src.numel() != dst.numel():
+    n = src.shape[0]
+    if dst.shape[0] != n:
         raise ValueError("src and dst disagree")
-    _check(q8_kv_copy(cache.struct, src, dst, src.numel()), "q8_kv_copy")
+    rc = _get().q8_kv_copy(cache.struct, _i32(src, "src"), _i32(dst, "dst"), n, _current_stream())
+    if rc:
+        raise Q8Error(rc, "q8_kv_copy")
