@@ -36,10 +36,12 @@ template <int D> struct Pt {
     static constexpr int BN = 128, BM = 256;
     static constexpr int CH = D / 64;                        // 64-value chunks of a row, 16 KB a chunk of 128 rows
     static constexpr int TILE = 128 * D * 2;
-    static constexpr int NST = D == 128 ? 4 : 8;             // key / value tiles in flight, keys in the even ones
+    // stage u holds the values of key tile u - 1 and the keys of tile u, which are used in one go
+    static constexpr int STAGE = 2 * TILE;
+    static constexpr int NST = D == 128 ? 2 : 4;
     static constexpr int THREADS = 384;
     static constexpr int NBAR = 1 + 3 * NST + 2 + 2 + 2 + 1;
-    static constexpr int SMEM = 1024 + 2 * TILE + NST * TILE + NBAR * 8 + 128;
+    static constexpr int SMEM = 1024 + 2 * TILE + NST * STAGE + NBAR * 8 + 128;
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
@@ -81,7 +83,7 @@ __global__ void __launch_bounds__(Pt<D>::THREADS, 1)
     __shared__ volatile int abort_flag, dirty;
     uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint8_t *qs = smem, *ring = smem + 2 * C::TILE;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(ring + C::NST * C::TILE);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(ring + C::NST * C::STAGE);
     uint64_t *qfull = bars, *full = bars + 1, *empty = full + C::NST, *ready = empty + C::NST;
     uint64_t *sfull = ready + C::NST, *pfull = sfull + 2, *ofull = pfull + 2, *done = ofull + 2;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -151,21 +153,24 @@ __global__ void __launch_bounds__(Pt<D>::THREADS, 1)
                 }
                 __syncwarp();
             }
-            for (int n = n0, u = 0; n < n1; ++n)
-                for (int kv = 0; kv < 2; ++kv, ++u) {
-                    const int st = u % C::NST;
-                    if (__shfl_sync(0xffffffffu, (int)(!p.withhold && mbar_wait(&empty[st], ((u / C::NST) & 1) ^ 1, p.err, &abort_flag, lim) &&
-                                                       !abort_flag), 0)) {
-                        if (lane == 0) {
-                            mbar_arrive_expect_tx(&full[st], C::TILE);
-                            for (int c = 0; c < C::CH; ++c)
-                                tma_load_2d(ring + st * C::TILE + c * 16384, kv ? &tmV : &tmK, (int)kvh * D + 64 * c,
-                                            w.k0 + n * C::BN, &full[st]);
+            for (int u = 0; u <= n1 - n0 && n1 > n0; ++u) {
+                const int st = u % C::NST;
+                if (__shfl_sync(0xffffffffu, (int)(!p.withhold && mbar_wait(&empty[st], ((u / C::NST) & 1) ^ 1, p.err, &abort_flag, lim) &&
+                                                   !abort_flag), 0)) {
+                    if (lane == 0) {
+                        const bool vals = u > 0, keys = u < n1 - n0;
+                        mbar_arrive_expect_tx(&full[st], (vals && keys ? 2 : 1) * C::TILE);
+                        uint8_t *t = ring + st * C::STAGE;
+                        const int y = w.k0 + (n0 + u) * C::BN;
+                        for (int c = 0; c < C::CH; ++c) {
+                            if (vals) tma_load_2d(t + c * 16384, &tmV, (int)kvh * D + 64 * c, y - C::BN, &full[st]);
+                            if (keys) tma_load_2d(t + C::TILE + c * 16384, &tmK, (int)kvh * D + 64 * c, y, &full[st]);
                         }
-                        ++fills[st];
                     }
-                    __syncwarp();
+                    ++fills[st];
                 }
+                __syncwarp();
+            }
             if (abort_flag && lane == 0) {
                 // let every copy this warp issued land before the CTA exits
                 const uint64_t t_end = global_timer_ns() + WAIT_LIMIT_NS;
@@ -177,76 +182,54 @@ __global__ void __launch_bounds__(Pt<D>::THREADS, 1)
         } else if (warp == 9) {
             // ------------------------------------------------ UMMA issuer
             constexpr uint32_t idS = tc_idesc(128, C::BN, BF16, false), idO = tc_idesc(128, D, BF16, true);
-            const uint32_t qa = smem_addr(qs), ra = smem_addr(ring);
-            uint32_t tiles[2] = {0, 0};   // key tiles whose P V has been issued
+            // addresses in the descriptors count 16 bytes
+            const uint64_t dq = sw128_desc(smem_addr(qs)), dk = sw128_desc(smem_addr(ring) + C::TILE),
+                           dv = sw128_desc_mn(smem_addr(ring), 16384);
             bool ok = n1 == n0 || mbar_wait(qfull, 0, p.err, &abort_flag, lim);
-            auto scores = [&](int i, int st) {
-                if (lane == 0 && ok) {
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t off = (k / 4) * 16384 + (k % 4) * 32;
-                        tc_mma_f16(tmem + i * 128, sw128_desc(qa + i * C::TILE + off), sw128_desc(ra + st * C::TILE + off), idS, k > 0);
-                    }
-                }
-                if (lane == 0) tc_commit(&sfull[i]);
-                __syncwarp();
-            };
-            if (n1 > n0) {
-                ok = mbar_wait(&full[0], 0, p.err, &abort_flag, lim) && ok;
-                tc_fence_after();
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    if (n0 >= t0[i] && n0 < t1[i]) scores(i, 0);
-                if (lane == 0 && ok) tc_commit(&empty[0]);
-                __syncwarp();
-            }
-            for (int n = n0; n < n1; ++n) {
-                const int u = 2 * (n - n0) + 1, sv = u % C::NST, sk = (u + 1) % C::NST;
-                bool k_seen = false;
-                ok = mbar_wait(&ready[sv], (u / C::NST) & 1, p.err, &abort_flag, lim) && ok;
+            for (int u = 0; u <= n1 - n0 && n1 > n0; ++u) {
+                const int st = u % C::NST, n = n0 + u;       // P V of key tile n - 1, then S of key tile n
+                const uint64_t bv = dv + (uint32_t)st * (C::STAGE / 16), bk = dk + (uint32_t)st * (C::STAGE / 16);
+                ok = mbar_wait(&ready[st], (u / C::NST) & 1, p.err, &abort_flag, lim) && ok;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    if (n >= t0[i] && n < t1[i]) {
-                        ok = mbar_wait(&pfull[i], tiles[i] & 1, p.err, &abort_flag, lim) && ok;
-                        tc_fence_after();
-                        if (lane == 0 && ok) {
+                    const bool pv = n > t0[i] && n <= t1[i], sc = n >= t0[i] && n < t1[i];
+                    if (pv) ok = mbar_wait(&pfull[i], (n - 1 - t0[i]) & 1, p.err, &abort_flag, lim) && ok;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        if (pv && ok) {
 #pragma unroll
                             for (int k = 0; k < C::BN / 16; ++k)
-                                tc_mma_f16_ta(tmem + 256 + i * 128, tmem + i * 128 + 8 * k,
-                                              sw128_desc_mn(ra + sv * C::TILE + k * 2048, 16384), idO, tiles[i] > 0 || k > 0);
+                                tc_mma_f16_ta(tmem + 256 + i * 128, tmem + i * 128 + 8 * k, bv + k * (2048 / 16), idO,
+                                              n - 1 > t0[i] || k > 0);
                         }
-                        ++tiles[i];
-                        if (n == t1[i] - 1) {
-                            if (lane == 0) tc_commit(&ofull[i]);
-                            __syncwarp();
+                        if (sc) {
+                            if (ok) {
+#pragma unroll
+                                for (int k = 0; k < D / 16; ++k) {
+                                    const uint32_t off = ((k / 4) * 16384 + (k % 4) * 32) / 16;
+                                    tc_mma_f16(tmem + i * 128, dq + i * (C::TILE / 16) + off, bk + off, idS, k > 0);
+                                }
+                            }
+                            tc_commit(&sfull[i]);
+                        } else if (pv) {
+                            tc_commit(&ofull[i]);
                         }
+                        if (i == 1 && ok) tc_commit(&empty[st]);
                     }
-                    if (n + 1 >= t0[i] && n + 1 < t1[i]) {
-                        if (!k_seen) {
-                            ok = mbar_wait(&full[sk], ((u + 1) / C::NST) & 1, p.err, &abort_flag, lim) && ok;
-                            tc_fence_after();
-                            k_seen = true;
-                        }
-                        scores(i, sk);
-                    }
+                    __syncwarp();
                 }
-                if (lane == 0 && ok) {
-                    tc_commit(&empty[sv]);
-                    if (n + 1 < n1) tc_commit(&empty[sk]);
-                }
-                __syncwarp();
             }
-            if (lane == 0) tc_commit(done);
+            if (elect_one()) tc_commit(done);
             __syncwarp();
             mbar_wait(done, 0, p.err, nullptr);   // the fixed 2 s limit: TMEM is freed after this
         } else if (warp >= 10) {
             // ------------------------------------------------ V guard
             const int gt = tid - 320;
-            for (int n = n0; n < n1; ++n) {
-                const int u = 2 * (n - n0) + 1, sv = u % C::NST;
-                const bool ok = mbar_wait(&full[sv], (u / C::NST) & 1, p.err, &abort_flag, lim);
-                if (ok && w.masked(n * C::BN, C::BN, p.window)) {
-                    uint4 *t = reinterpret_cast<uint4 *>(ring + sv * C::TILE);
+            for (int u = 0; u <= n1 - n0 && n1 > n0; ++u) {
+                const int st = u % C::NST;
+                const bool ok = mbar_wait(&full[st], (u / C::NST) & 1, p.err, &abort_flag, lim);
+                if (ok && u > 0 && w.masked((n0 + u - 1) * C::BN, C::BN, p.window)) {
+                    uint4 *t = reinterpret_cast<uint4 *>(ring + st * C::STAGE);
 #pragma unroll 4
                     for (int i = gt; i < C::TILE / 16; i += 64) {
                         uint4 x = t[i];
@@ -258,7 +241,7 @@ __global__ void __launch_bounds__(Pt<D>::THREADS, 1)
                     fence_async_smem();
                 }
                 __syncwarp();
-                if (ok && lane == 0) mbar_arrive(&ready[sv]);
+                if (ok && lane == 0) mbar_arrive(&ready[st]);
             }
         } else {
             // ------------------------------------------------ softmax of tile i, one row a thread

@@ -56,6 +56,14 @@ __device__ __forceinline__ void tc_mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, 
         : "memory");
 }
 
+// True on one lane of a converged warp.  Unlike lane == 0 the compiler knows that the branch holds one
+// thread, and keeps the operands of what it issues in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // One row a thread (lane of the warp's quarter), 32 / 16 consecutive columns.
 __device__ __forceinline__ void tc_ld32(uint32_t taddr, uint32_t *v) {
     asm volatile(
