@@ -29,7 +29,7 @@ template <int D> struct Pm {
 template <int D, bool BF16> __global__ void __launch_bounds__(128) k_attn_prompt_mma(const AttnPromptParams p) {
     using C = Pm<D>;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int sh[8];
+    __shared__ int sh[10];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     grid_dep_wait();
     PromptTile w;
@@ -41,7 +41,7 @@ template <int D, bool BF16> __global__ void __launch_bounds__(128) k_attn_prompt
     const uint16_t *vp = static_cast<const uint16_t *>(p.v) + (uint64_t)w.k0 * p.v_stride + (uint64_t)kvh * D + dv0;
     uint8_t *qs = smem, *ring = smem + C::QB_;
     const uint32_t qs_s = smem_addr(qs), ring_s = smem_addr(ring);
-    if (tid == 0) sh[7] = 0;   // a masked tile held a value that is not finite
+    if (tid == 0) sh[9] = 0;   // a masked tile held a value that is not finite
 
     const int n0 = w.first(0, p.window) / C::BN, n1 = w.rows ? (w.last(w.rows - 1) + C::BN) / C::BN : 0;   // key tiles [n0, n1)
     auto stage = [&](int n) {
@@ -103,7 +103,7 @@ template <int D, bool BF16> __global__ void __launch_bounds__(128) k_attn_prompt
                 uint4 x = reinterpret_cast<uint4 *>(vt)[i];
                 if (prompt_scrub<BF16>(x)) {
                     reinterpret_cast<uint4 *>(vt)[i] = x;
-                    sh[7] = 1;
+                    sh[9] = 1;
                 }
             }
             __syncthreads();
@@ -201,7 +201,7 @@ template <int D, bool BF16> __global__ void __launch_bounds__(128) k_attn_prompt
             p.lse[(uint64_t)(w.q0 + w.row0 + row) * p.n_heads + head] = lse;
     }
     __syncwarp();
-    const bool dirty = sh[7] != 0;
+    const bool dirty = sh[9] != 0;
     for (int i = lane; i < 16 * (C::DV / 8); i += 32) {
         const int r = i / (C::DV / 8), d0 = i % (C::DV / 8) * 8, row = warp * 16 + r;
         const bool act = row < w.rows;

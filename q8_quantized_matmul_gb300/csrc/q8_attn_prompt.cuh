@@ -28,13 +28,11 @@ struct PromptTile {
     }
 };
 
-__device__ __forceinline__ int prompt_bound(const int32_t *start, uint32_t i, uint32_t n) {
-    return (int)min((uint32_t)max(start[i], 0), n);
-}
+__device__ __forceinline__ int prompt_bound(int32_t start, uint32_t n) { return (int)min((uint32_t)max(start, 0), n); }
 
 // Tile `slot` of the packed sequences in tiles of BM query rows, the newest rows of the last sequence
 // first (their rows see the most keys, so the long tiles start first).  False: no such tile.
-// Called by a whole CTA of THREADS; sh: THREADS / 32 + 2 ints of shared memory.  report: raise bad starts.
+// Called by a whole CTA of THREADS; sh: THREADS / 32 + 5 ints of shared memory.  report: raise bad starts.
 template <int THREADS>
 __device__ __forceinline__ bool prompt_tile(const AttnPromptParams &p, int BM, uint32_t slot, bool report, PromptTile &w,
                                             int *sh) {
@@ -46,15 +44,16 @@ __device__ __forceinline__ bool prompt_tile(const AttnPromptParams &p, int BM, u
     int64_t before = 0;
     for (uint32_t b = 0; b < p.n_seq; b += THREADS) {
         const uint32_t i = b + tid, s = p.n_seq - 1 - i;
-        int tiles = 0;
+        int tiles = 0, qa = 0, qe = 0, ka = 0, ke = 0;
         if (i < p.n_seq) {
-            const int a = prompt_bound(p.q_start, s, p.n_q), e = prompt_bound(p.q_start, s + 1, p.n_q);
-            tiles = e > a ? (e - a + BM - 1) / BM : 0;
-            if (report) {
-                const int ka = prompt_bound(ks, s, p.n_k), ke = prompt_bound(ks, s + 1, p.n_k);
-                if (e < a || ke < ka || a != p.q_start[s] || e != p.q_start[s + 1] || ka != ks[s] || ke != ks[s + 1])
-                    raise_error(p.err, DEV_ERANGE);
-            }
+            const int4 raw = make_int4(p.q_start[s], p.q_start[s + 1], ks[s], ks[s + 1]);
+            qa = prompt_bound(raw.x, p.n_q);
+            qe = prompt_bound(raw.y, p.n_q);
+            ka = prompt_bound(raw.z, p.n_k);
+            ke = prompt_bound(raw.w, p.n_k);
+            tiles = qe > qa ? (qe - qa + BM - 1) / BM : 0;
+            if (report && (qe < qa || ke < ka || qa != raw.x || qe != raw.y || ka != raw.z || ke != raw.w))
+                raise_error(p.err, DEV_ERANGE);
         }
         // inclusive sum over the CTA
         int sum = tiles;
@@ -71,22 +70,24 @@ __device__ __forceinline__ bool prompt_tile(const AttnPromptParams &p, int BM, u
             before += sh[1 + k];
         }
         if (tiles && slot >= at && slot < at + tiles) {
-            sh[0] = (int)s;
-            sh[THREADS / 32 + 1] = (int)(at + tiles - 1 - slot);   // newest tile first
+            sh[0] = (int)(at + tiles - 1 - slot);   // newest tile first
+            int *b4 = sh + THREADS / 32 + 1;
+            b4[0] = qa;
+            b4[1] = qe - qa;
+            b4[2] = ka;
+            b4[3] = max(ke - ka, 0);
         }
         __syncthreads();
         if (sh[0] >= 0) break;
     }
-    const int s = sh[0];
-    if (s < 0) return false;
-    const int tile = sh[THREADS / 32 + 1];
-    w.q0 = prompt_bound(p.q_start, s, p.n_q);
-    const int lq = prompt_bound(p.q_start, s + 1, p.n_q) - w.q0;
-    w.k0 = prompt_bound(ks, s, p.n_k);
-    w.lk = max(prompt_bound(ks, s + 1, p.n_k) - w.k0, 0);
-    w.row0 = tile * BM;
-    w.rows = min(BM, lq - w.row0);
-    w.shift = w.lk - lq;
+    if (sh[0] < 0) return false;
+    const int *b4 = sh + THREADS / 32 + 1;
+    w.q0 = b4[0];
+    w.k0 = b4[2];
+    w.lk = b4[3];
+    w.row0 = sh[0] * BM;
+    w.rows = min(BM, b4[1] - w.row0);
+    w.shift = w.lk - b4[1];
     return true;
 }
 

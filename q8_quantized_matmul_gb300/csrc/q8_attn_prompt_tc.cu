@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(Pt<D>::THREADS, 1)
                      const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
     using C = Pt<D>;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ int sh[16];
+    __shared__ int sh[C::THREADS / 32 + 5];
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort_flag, dirty;
     uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -264,20 +264,29 @@ __global__ void __launch_bounds__(Pt<D>::THREADS, 1)
                 tc_wait_ld();
                 tc_regs_ready(v);
                 if (n * C::BN + C::BN - 1 > w_last || n * C::BN < w_first) {
-                    const int hi = last - n * C::BN, lo = first - n * C::BN;
+                    const int hi = last - n * C::BN, lo = first - n * C::BN;   // columns lo .. hi are seen
 #pragma unroll
-                    for (int c = 0; c < 128; ++c)
-                        if (c > hi || c < lo) v[c] = 0xff800000u;
+                    for (int b = 0; b < 4; ++b) {
+                        // bits of the 32 columns from 32 b on
+                        const int h = hi + 1 - 32 * b, g = lo - 32 * b;
+                        const uint32_t below = h >= 32 ? 0xffffffffu : (h <= 0 ? 0u : (1u << h) - 1u);
+                        const uint32_t seen = g <= 0 ? below : (g >= 32 ? 0u : below & (0xffffffffu << g));
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            if (!(seen & (1u << c))) v[32 * b + c] = 0xff800000u;
+                    }
                 }
                 float x0 = __uint_as_float(v[0]), x1 = __uint_as_float(v[1]), x2 = __uint_as_float(v[2]), x3 = __uint_as_float(v[3]);
 #pragma unroll
-                for (int c = 4; c < 128; c += 4) {
-                    x0 = fmaxf(x0, __uint_as_float(v[c]));
-                    x1 = fmaxf(x1, __uint_as_float(v[c + 1]));
-                    x2 = fmaxf(x2, __uint_as_float(v[c + 2]));
-                    x3 = fmaxf(x3, __uint_as_float(v[c + 3]));
+                for (int c = 4; c < 124; c += 8) {
+                    x0 = max3(x0, __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
+                    x1 = max3(x1, __uint_as_float(v[c + 2]), __uint_as_float(v[c + 3]));
+                    x2 = max3(x2, __uint_as_float(v[c + 4]), __uint_as_float(v[c + 5]));
+                    x3 = max3(x3, __uint_as_float(v[c + 6]), __uint_as_float(v[c + 7]));
                 }
-                const float mx = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)) * p.scale_log2;
+                x0 = max3(x0, __uint_as_float(v[124]), __uint_as_float(v[125]));
+                x1 = max3(x1, __uint_as_float(v[126]), __uint_as_float(v[127]));
+                const float mx = max3(fmaxf(x0, x1), x2, x3) * p.scale_log2;
                 // a first maximum needs no rescaling: O is still zero in that row
                 const bool grow = mx > m + 8.0f;
                 float f = 1.0f;
@@ -299,26 +308,30 @@ __global__ void __launch_bounds__(Pt<D>::THREADS, 1)
                     }
                 }
                 const float neg = m == -INFINITY ? 0.0f : -m;
-                float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+                const uint64_t scale2 = pair2(p.scale_log2, p.scale_log2), neg2 = pair2(neg, neg);
+                uint64_t s0 = 0, s1 = 0;
 #pragma unroll
                 for (int b = 0; b < 128; b += 32) {
                     uint32_t pk[16];
 #pragma unroll
                     for (int c = 0; c < 32; c += 4) {
-                        const float a0 = ex2(__fmaf_rn(__uint_as_float(v[b + c]), p.scale_log2, neg));
-                        const float a1 = ex2(__fmaf_rn(__uint_as_float(v[b + c + 1]), p.scale_log2, neg));
-                        const float a2 = ex2(__fmaf_rn(__uint_as_float(v[b + c + 2]), p.scale_log2, neg));
-                        const float a3 = ex2(__fmaf_rn(__uint_as_float(v[b + c + 3]), p.scale_log2, neg));
-                        s0 += a0;
-                        s1 += a1;
-                        s2 += a2;
-                        s3 += a3;
+                        float a0, a1, a2, a3;
+                        split2(a0, a1, fma2(pair2(__uint_as_float(v[b + c]), __uint_as_float(v[b + c + 1])), scale2, neg2));
+                        split2(a2, a3, fma2(pair2(__uint_as_float(v[b + c + 2]), __uint_as_float(v[b + c + 3])), scale2, neg2));
+                        a0 = ex2(a0);
+                        a1 = ex2(a1);
+                        a2 = ex2(a2);
+                        a3 = ex2(a3);
+                        s0 = add2(s0, pair2(a0, a1));
+                        s1 = add2(s1, pair2(a2, a3));
                         pk[c / 2] = pack16<BF16>(a0, a1);
                         pk[c / 2 + 1] = pack16<BF16>(a2, a3);
                     }
                     tc_st16(tS + b / 2, pk);
                 }
-                l += (s0 + s1) + (s2 + s3);
+                float l0, l1;
+                split2(l0, l1, add2(s0, s1));
+                l += l0 + l1;
                 tc_wait_st();
                 tc_fence_before();
                 __syncwarp();
