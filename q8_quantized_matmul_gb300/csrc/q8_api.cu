@@ -1334,8 +1334,12 @@ int q8_attn_prompt(void *out, int out_type, float *lse, const void *q, const voi
     p.out_type = out_type;
     p.lse = lse;
     p.err = s->err;
-    if (q8::attn_prompt_on_tc(head_dim, n_k)) take_expiry(p.wait_ns, p.withhold);
-    return status_of(q8::launch_attn_prompt(p, static_cast<cudaStream_t>(stream)));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (!q8::attn_prompt_on_tc(head_dim, n_k)) return status_of(q8::launch_attn_prompt_mma(p, st));
+    const size_t list = q8::attn_prompt_list_bytes(p, s->num_sms);
+    if ((rc = reserve_scratch(s, list))) return rc;
+    take_expiry(p.wait_ns, p.withhold);
+    return status_of(q8::launch_attn_prompt_tc(p, list ? s->scratch : nullptr, s->num_sms, st));
 }
 
 // Arguments that the page calls share; fills p but for its scratch.

@@ -1,5 +1,5 @@
 // q8_attn_prompt.cu -- attention over whole packed prompts, causal, grouped heads: the
-// mma.sync kernel, and which kernel runs which call.
+// mma.sync kernel, for the calls that q8_attn_prompt_tc.cu does not take (attn_prompt_on_tc).
 //
 // k_attn_prompt_mma: 64 query rows of one head per CTA (16 a warp), keys in tiles of 64 (32 for heads
 // of more than 128 values) through a double buffer of asynchronous copies; running maximum, sum and
@@ -212,7 +212,7 @@ template <int D, bool BF16> __global__ void __launch_bounds__(128) k_attn_prompt
     }
 }
 
-template <int D, bool BF16> cudaError_t launch_mma(const AttnPromptParams &p, cudaStream_t st) {
+template <int D, bool BF16> cudaError_t launch_one(const AttnPromptParams &p, cudaStream_t st) {
     static bool attr_done = false;
     if (!attr_done) {
         const cudaError_t e = cudaFuncSetAttribute(k_attn_prompt_mma<D, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -226,18 +226,17 @@ template <int D, bool BF16> cudaError_t launch_mma(const AttnPromptParams &p, cu
 
 template <bool BF16> cudaError_t launch_type(const AttnPromptParams &p, cudaStream_t st) {
     switch (p.dim) {
-        case 64: return launch_mma<64, BF16>(p, st);
-        case 128: return launch_mma<128, BF16>(p, st);
-        case 256: return launch_mma<256, BF16>(p, st);
-        case 512: return launch_mma<512, BF16>(p, st);
+        case 64: return launch_one<64, BF16>(p, st);
+        case 128: return launch_one<128, BF16>(p, st);
+        case 256: return launch_one<256, BF16>(p, st);
+        case 512: return launch_one<512, BF16>(p, st);
         default: return cudaErrorInvalidValue;
     }
 }
 
 }  // namespace
 
-cudaError_t launch_attn_prompt(const AttnPromptParams &p, cudaStream_t st) {
-    if (attn_prompt_on_tc(p.dim, p.n_k)) return launch_attn_prompt_tc(p, st);
+cudaError_t launch_attn_prompt_mma(const AttnPromptParams &p, cudaStream_t st) {
     return p.type == Q8_TYPE_BF16 ? launch_type<true>(p, st) : launch_type<false>(p, st);
 }
 

@@ -8,7 +8,7 @@
 namespace q8 {
 
 // Up to BM query rows of one sequence.
-struct PromptTile {
+struct alignas(8) PromptTile {
     int q0, k0;          // first packed row of the sequence's queries / keys
     int row0, rows;      // first query of the tile within the sequence, and how many
     int lk, shift;       // keys; query i (of the sequence) sees keys up to i + shift

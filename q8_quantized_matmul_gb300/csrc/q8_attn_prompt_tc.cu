@@ -19,6 +19,11 @@
 // finite from tiles that some rows may not see (0 times infinity would reach them); they are added at the
 // end to the rows that do see them (prompt_restore).
 //
+// Calls with more tiles than SMs run one persistent CTA per SM over a list of tiles, longest first, that a
+// small kernel writes: the loads and the first S of a CTA's next tile then run under the last softmax and the
+// stores of this one (separate CTAs spent 9300 cycles each before the first and after the last product).
+// Smaller calls give each CTA its one tile directly and save that launch.
+//
 // Every wait is bounded; after one expires nothing more is issued and copies in flight are drained.
 #include "q8_attn.cuh"
 #include "q8_attn_prompt.cuh"
@@ -40,10 +45,71 @@ template <int D> struct Pt {
     static constexpr int STAGE = 2 * TILE;
     static constexpr int NST = D == 128 ? 2 : 4;
     static constexpr int THREADS = 384;
-    static constexpr int NBAR = 1 + 3 * NST + 2 + 2 + 2 + 1;
+    static constexpr int NBAR = 2 + 3 * NST + 2 + 2 + 2 + 1;
     static constexpr int SMEM = 1024 + 2 * TILE + NST * STAGE + NBAR * 8 + 128;
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
+
+// ---------------------------------------------------------------- list of tiles
+constexpr int LIST_THREADS = 1024, LIST_BINS = 1024;
+
+__device__ __forceinline__ int tile_cost(const PromptTile &w, uint32_t window) {
+    const int last = w.last(w.rows - 1);
+    return last < 0 ? 0 : last / 128 + 1 - w.first(0, window) / 128;
+}
+
+// One CTA: all tiles of 256 query rows, the ones with the most key tiles first (counting sort; the order
+// among equals does not matter to any result).
+__global__ void __launch_bounds__(LIST_THREADS) k_attn_prompt_list(const AttnPromptParams p) {
+    __shared__ int bin[LIST_BINS];
+    __shared__ int wsum[32];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    grid_dep_wait();
+    const int32_t *ks = p.k_start ? p.k_start : p.q_start;
+    bin[tid] = 0;
+    __syncthreads();
+    PromptTile *list = reinterpret_cast<PromptTile *>(p.list + 1);
+    auto each = [&](auto f) {   // a warp per sequence, a lane per tile
+        for (uint32_t s = warp; s < p.n_seq; s += LIST_THREADS / 32) {
+            const int4 raw = make_int4(p.q_start[s], p.q_start[s + 1], ks[s], ks[s + 1]);
+            const int qa = prompt_bound(raw.x, p.n_q), qe = prompt_bound(raw.y, p.n_q);
+            const int ka = prompt_bound(raw.z, p.n_k), ke = prompt_bound(raw.w, p.n_k);
+            const bool bad = qe < qa || ke < ka || qa != raw.x || qe != raw.y || ka != raw.z || ke != raw.w;
+            PromptTile w;
+            w.q0 = qa;
+            w.k0 = ka;
+            w.lk = max(ke - ka, 0);
+            w.shift = w.lk - (qe - qa);
+            for (int64_t r = lane * 256; r < qe - qa; r += 32 * 256) {
+                w.row0 = (int)r;
+                w.rows = min(256, qe - qa - w.row0);
+                const int c = tile_cost(w, p.window) >> p.list_shift;
+                f(w, LIST_BINS - 1 - min(c, LIST_BINS - 1));   // longest in the first bin
+            }
+            if (bad && lane == 0) raise_error(p.err, DEV_ERANGE);
+        }
+    };
+    each([&](const PromptTile &, int b) { atomicAdd(&bin[b], 1); });
+    __syncthreads();
+    int sum = bin[tid];
+    const int mine = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += v;
+    }
+    if (lane == 31) wsum[warp] = sum;
+    __syncthreads();
+    int before = 0;
+    for (int k = 0; k < warp; ++k) before += wsum[k];
+    bin[tid] = before + sum - mine;
+    if (tid == LIST_THREADS - 1) *reinterpret_cast<int *>(p.list) = min(before + sum, (int)p.list_cap);
+    __syncthreads();
+    each([&](const PromptTile &w, int b) {
+        const int at = atomicAdd(&bin[b], 1);
+        if (at < (int)p.list_cap) list[at] = w;   // starts that do not rise may give more tiles than rows
+    });
+}
 
 // 32 fp32 output values of one thread's row, columns d0 ..
 __device__ __forceinline__ void store_row32(const AttnPromptParams &p, uint64_t row, int d0, const float *y) {
@@ -80,16 +146,17 @@ __global__ void __launch_bounds__(Pt<D>::THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     __shared__ int sh[C::THREADS / 32 + 5];
     __shared__ uint32_t tmem_slot;
-    __shared__ volatile int abort_flag, dirty;
+    __shared__ volatile int abort_flag, dirty[8];   // dirty[k & 7] == k + 1: tile k of this CTA had values removed
     uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint8_t *qs = smem, *ring = smem + 2 * C::TILE;
     uint64_t *bars = reinterpret_cast<uint64_t *>(ring + C::NST * C::STAGE);
-    uint64_t *qfull = bars, *full = bars + 1, *empty = full + C::NST, *ready = empty + C::NST;
+    uint64_t *qfull = bars, *qempty = bars + 1, *full = bars + 2, *empty = full + C::NST, *ready = empty + C::NST;
     uint64_t *sfull = ready + C::NST, *pfull = sfull + 2, *ofull = pfull + 2, *done = ofull + 2;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
         mbar_init(qfull, 1);
+        mbar_init(qempty, 1);
         for (int i = 0; i < C::NST; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
@@ -102,7 +169,7 @@ __global__ void __launch_bounds__(Pt<D>::THREADS, 1)
         }
         mbar_init(done, 1);
         abort_flag = 0;
-        dirty = 0;
+        for (int i = 0; i < 8; ++i) dirty[i] = 0;
         fence_mbar_init();
     }
     grid_dep_wait();   // before TMEM is taken: a predecessor that still needs it is waited for
@@ -112,69 +179,95 @@ __global__ void __launch_bounds__(Pt<D>::THREADS, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    PromptTile w;
-    const bool any = prompt_tile<C::THREADS>(p, C::BM, blockIdx.y, blockIdx.x + blockIdx.y == 0, w, sh);
+    __shared__ PromptTile w_one;
+    bool one = false;
+    if (!p.list) {
+        PromptTile w;
+        one = prompt_tile<C::THREADS>(p, C::BM, blockIdx.x / p.n_heads, blockIdx.x == 0, w, sh);
+        if (one && tid == 0) w_one = w;
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
     const uint64_t lim = wait_limit(p.wait_ns);
-    const uint32_t head = blockIdx.x, kvh = head / (p.n_heads / p.n_kv);
-
-    if (any) {
-        // key tiles [t0[i], t1[i]) that query tile i sees, and [n0, n1) that either sees
-        int t0[2], t1[2], n0 = INT32_MAX, n1 = 0;
+    const uint32_t group = p.n_heads / p.n_kv;
+    // tiles of this CTA: its own, or every gridDim.x-th of the list, heads of one tile side by side
+    const uint32_t n_items = p.list ? (uint32_t)min((uint64_t)*reinterpret_cast<const uint32_t *>(p.list) * p.n_heads, (uint64_t)0xffff0000u)
+                                    : (one ? blockIdx.x + 1 : 0);
+    const uint32_t step = p.list ? gridDim.x : 0x40000000u;
+    auto load_item = [&](uint32_t id) {
+        return p.list ? p.list[1 + id / p.n_heads] : w_one;
+    };
+    // key tiles [t0[i], t1[i]) that query tile i sees, and [n0, n1) that either sees
+    struct Range {
+        int t0[2], t1[2], n0, n1;
+    };
+    auto ranges = [&](const PromptTile &w) {
+        Range r;
+        r.n0 = INT32_MAX;
+        r.n1 = 0;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int ra = 128 * i, rb = min(w.rows, ra + 128) - 1;
-            t0[i] = t1[i] = 0;
+            r.t0[i] = r.t1[i] = 0;
             if (rb >= ra && w.last(rb) >= 0) {
-                t0[i] = w.first(ra, p.window) / C::BN;
-                t1[i] = w.last(rb) / C::BN + 1;
-                n0 = min(n0, t0[i]);
-                n1 = max(n1, t1[i]);
+                r.t0[i] = w.first(ra, p.window) / C::BN;
+                r.t1[i] = w.last(rb) / C::BN + 1;
+                r.n0 = min(r.n0, r.t0[i]);
+                r.n1 = max(r.n1, r.t1[i]);
             }
         }
-        if (n1 == 0) n0 = 0;
+        if (r.n1 == 0) r.n0 = 0;
+        return r;
+    };
 
+    {
         if (warp == 8) {
             // ------------------------------------------------ TMA producer
-            uint32_t fills[C::NST] = {};
-            bool q_loaded = false;
-            if (n1 > n0 && !p.withhold) {
-                q_loaded = true;
-                if (lane == 0) {
-                    const bool two = w.rows > 128;
-                    mbar_arrive_expect_tx(qfull, (two ? 2 : 1) * C::TILE);
-                    for (int i = 0; i < (two ? 2 : 1); ++i)
-                        for (int c = 0; c < C::CH; ++c)
-                            tma_load_2d(qs + i * C::TILE + c * 16384, &tmQ, (int)head * D + 64 * c, w.q0 + w.row0 + 128 * i,
-                                        qfull);
-                }
-                __syncwarp();
-            }
-            for (int u = 0; u <= n1 - n0 && n1 > n0; ++u) {
-                const int st = u % C::NST;
-                if (__shfl_sync(0xffffffffu, (int)(!p.withhold && mbar_wait(&empty[st], ((u / C::NST) & 1) ^ 1, p.err, &abort_flag, lim) &&
-                                                   !abort_flag), 0)) {
+            uint32_t fills[C::NST] = {}, q_loads = 0, u = 0;
+            auto go = [&](uint64_t *bar, uint32_t parity) {
+                return __shfl_sync(0xffffffffu, (int)(!p.withhold && mbar_wait(bar, parity, p.err, &abort_flag, lim) && !abort_flag),
+                                   0) != 0;
+            };
+            for (uint32_t id = blockIdx.x; id < n_items; id += step) {
+                const PromptTile w = load_item(id);
+                const Range r = ranges(w);
+                const int qx = (int)(id % p.n_heads) * D, kx = (int)(id % p.n_heads / group) * D;
+                if (r.n1 == r.n0) continue;
+                if (go(qempty, (q_loads & 1) ^ 1)) {
                     if (lane == 0) {
-                        const bool vals = u > 0, keys = u < n1 - n0;
-                        mbar_arrive_expect_tx(&full[st], (vals && keys ? 2 : 1) * C::TILE);
-                        uint8_t *t = ring + st * C::STAGE;
-                        const int y = w.k0 + (n0 + u) * C::BN;
-                        for (int c = 0; c < C::CH; ++c) {
-                            if (vals) tma_load_2d(t + c * 16384, &tmV, (int)kvh * D + 64 * c, y - C::BN, &full[st]);
-                            if (keys) tma_load_2d(t + C::TILE + c * 16384, &tmK, (int)kvh * D + 64 * c, y, &full[st]);
-                        }
+                        const bool two = w.rows > 128;
+                        mbar_arrive_expect_tx(qfull, (two ? 2 : 1) * C::TILE);
+                        for (int i = 0; i < (two ? 2 : 1); ++i)
+                            for (int c = 0; c < C::CH; ++c)
+                                tma_load_2d(qs + i * C::TILE + c * 16384, &tmQ, qx + 64 * c, w.q0 + w.row0 + 128 * i, qfull);
                     }
-                    ++fills[st];
+                    ++q_loads;
                 }
                 __syncwarp();
+                for (int n = r.n0; n <= r.n1; ++n, ++u) {
+                    const int st = u % C::NST;
+                    if (go(&empty[st], ((u / C::NST) & 1) ^ 1)) {
+                        if (lane == 0) {
+                            const bool vals = n > r.n0, keys = n < r.n1;
+                            mbar_arrive_expect_tx(&full[st], (vals && keys ? 2 : 1) * C::TILE);
+                            uint8_t *t = ring + st * C::STAGE;
+                            const int y = w.k0 + n * C::BN;
+                            for (int c = 0; c < C::CH; ++c) {
+                                if (vals) tma_load_2d(t + c * 16384, &tmV, kx + 64 * c, y - C::BN, &full[st]);
+                                if (keys) tma_load_2d(t + C::TILE + c * 16384, &tmK, kx + 64 * c, y, &full[st]);
+                            }
+                        }
+                        ++fills[st];
+                    }
+                    __syncwarp();
+                }
             }
             if (abort_flag && lane == 0) {
                 // let every copy this warp issued land before the CTA exits
                 const uint64_t t_end = global_timer_ns() + WAIT_LIMIT_NS;
-                if (q_loaded) mbar_drain(qfull, 0, t_end);
+                if (q_loads) mbar_drain(qfull, (q_loads - 1u) & 1u, t_end);
                 for (int s = 0; s < C::NST; ++s)
                     if (fills[s]) mbar_drain(&full[s], (fills[s] - 1u) & 1u, t_end);
             }
@@ -185,38 +278,52 @@ __global__ void __launch_bounds__(Pt<D>::THREADS, 1)
             // addresses in the descriptors count 16 bytes
             const uint64_t dq = sw128_desc(smem_addr(qs)), dk = sw128_desc(smem_addr(ring) + C::TILE),
                            dv = sw128_desc_mn(smem_addr(ring), 16384);
-            bool ok = n1 == n0 || mbar_wait(qfull, 0, p.err, &abort_flag, lim);
-            for (int u = 0; u <= n1 - n0 && n1 > n0; ++u) {
-                const int st = u % C::NST, n = n0 + u;       // P V of key tile n - 1, then S of key tile n
-                const uint64_t bv = dv + (uint32_t)st * (C::STAGE / 16), bk = dk + (uint32_t)st * (C::STAGE / 16);
-                ok = mbar_wait(&ready[st], (u / C::NST) & 1, p.err, &abort_flag, lim) && ok;
+            bool ok = true;
+            uint32_t u = 0, q_loads = 0, p_done[2] = {0, 0};
+            for (uint32_t id = blockIdx.x; id < n_items; id += step) {
+                const PromptTile w = load_item(id);
+                const Range r = ranges(w);
+                if (r.n1 == r.n0) continue;
+                ok = mbar_wait(qfull, q_loads & 1, p.err, &abort_flag, lim) && ok;
+                ++q_loads;
+                for (int n = r.n0; n <= r.n1; ++n, ++u) {    // P V of key tile n - 1, then S of key tile n
+                    const int st = u % C::NST;
+                    const uint64_t bv = dv + (uint32_t)st * (C::STAGE / 16), bk = dk + (uint32_t)st * (C::STAGE / 16);
+                    ok = mbar_wait(&ready[st], (u / C::NST) & 1, p.err, &abort_flag, lim) && ok;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const bool pv = n > t0[i] && n <= t1[i], sc = n >= t0[i] && n < t1[i];
-                    if (pv) ok = mbar_wait(&pfull[i], (n - 1 - t0[i]) & 1, p.err, &abort_flag, lim) && ok;
-                    tc_fence_after();
-                    if (elect_one()) {
-                        if (pv && ok) {
-#pragma unroll
-                            for (int k = 0; k < C::BN / 16; ++k)
-                                tc_mma_f16_ta(tmem + 256 + i * 128, tmem + i * 128 + 8 * k, bv + k * (2048 / 16), idO,
-                                              n - 1 > t0[i] || k > 0);
+                    for (int i = 0; i < 2; ++i) {
+                        const bool pv = n > r.t0[i] && n <= r.t1[i], sc = n >= r.t0[i] && n < r.t1[i];
+                        if (pv) {
+                            ok = mbar_wait(&pfull[i], p_done[i] & 1, p.err, &abort_flag, lim) && ok;
+                            ++p_done[i];
                         }
-                        if (sc) {
-                            if (ok) {
+                        tc_fence_after();
+                        if (elect_one()) {
+                            if (pv && ok) {
 #pragma unroll
-                                for (int k = 0; k < D / 16; ++k) {
-                                    const uint32_t off = ((k / 4) * 16384 + (k % 4) * 32) / 16;
-                                    tc_mma_f16(tmem + i * 128, dq + i * (C::TILE / 16) + off, bk + off, idS, k > 0);
-                                }
+                                for (int k = 0; k < C::BN / 16; ++k)
+                                    tc_mma_f16_ta(tmem + 256 + i * 128, tmem + i * 128 + 8 * k, bv + k * (2048 / 16), idO,
+                                                  n - 1 > r.t0[i] || k > 0);
                             }
-                            tc_commit(&sfull[i]);
-                        } else if (pv) {
-                            tc_commit(&ofull[i]);
+                            if (sc) {
+                                if (ok) {
+#pragma unroll
+                                    for (int k = 0; k < D / 16; ++k) {
+                                        const uint32_t off = ((k / 4) * 16384 + (k % 4) * 32) / 16;
+                                        tc_mma_f16(tmem + i * 128, dq + i * (C::TILE / 16) + off, bk + off, idS, k > 0);
+                                    }
+                                }
+                                tc_commit(&sfull[i]);
+                            } else if (pv) {
+                                tc_commit(&ofull[i]);
+                            }
+                            if (i == 1 && ok) {
+                                tc_commit(&empty[st]);
+                                if (n == r.n1 - 1) tc_commit(qempty);
+                            }
                         }
-                        if (i == 1 && ok) tc_commit(&empty[st]);
+                        __syncwarp();
                     }
-                    __syncwarp();
                 }
             }
             if (elect_one()) tc_commit(done);
@@ -225,153 +332,179 @@ __global__ void __launch_bounds__(Pt<D>::THREADS, 1)
         } else if (warp >= 10) {
             // ------------------------------------------------ V guard
             const int gt = tid - 320;
-            for (int u = 0; u <= n1 - n0 && n1 > n0; ++u) {
-                const int st = u % C::NST;
-                const bool ok = mbar_wait(&full[st], (u / C::NST) & 1, p.err, &abort_flag, lim);
-                if (ok && u > 0 && w.masked((n0 + u - 1) * C::BN, C::BN, p.window)) {
-                    uint4 *t = reinterpret_cast<uint4 *>(ring + st * C::STAGE);
+            uint32_t u = 0;
+            int item = 0;
+            for (uint32_t id = blockIdx.x; id < n_items; id += step, ++item) {
+                const PromptTile w = load_item(id);
+                const Range r = ranges(w);
+                if (r.n1 == r.n0) continue;
+                for (int n = r.n0; n <= r.n1; ++n, ++u) {
+                    const int st = u % C::NST;
+                    const bool ok = mbar_wait(&full[st], (u / C::NST) & 1, p.err, &abort_flag, lim);
+                    if (ok && n > r.n0 && w.masked((n - 1) * C::BN, C::BN, p.window)) {
+                        uint4 *t = reinterpret_cast<uint4 *>(ring + st * C::STAGE);
 #pragma unroll 4
-                    for (int i = gt; i < C::TILE / 16; i += 64) {
-                        uint4 x = t[i];
-                        if (prompt_scrub<BF16>(x)) {
-                            t[i] = x;
-                            dirty = 1;
+                        for (int i = gt; i < C::TILE / 16; i += 64) {
+                            uint4 x = t[i];
+                            if (prompt_scrub<BF16>(x)) {
+                                t[i] = x;
+                                dirty[item & 7] = item + 1;
+                            }
                         }
+                        fence_async_smem();
                     }
-                    fence_async_smem();
+                    __syncwarp();
+                    if (ok && lane == 0) mbar_arrive(&ready[st]);
                 }
-                __syncwarp();
-                if (ok && lane == 0) mbar_arrive(&ready[st]);
             }
         } else {
             // ------------------------------------------------ softmax of tile i, one row a thread
             const int i = warp >> 2, row = i * 128 + (warp & 3) * 32 + lane;
             const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
             const uint32_t tS = tmem + lanes + i * 128, tO = tmem + lanes + 256 + i * 128;
-            const int last = w.last(row), first = w.first(row, p.window);
-            // tiles that every row of the warp sees whole need no mask
-            const int w_last = w.last(i * 128 + (warp & 3) * 32), w_first = w.first(i * 128 + (warp & 3) * 32 + 31, p.window);
-            const int ta = i ? t0[1] : t0[0], tb = i ? t1[1] : t1[0];
-            float m = -INFINITY, l = 0.0f;
-            for (int n = ta; n < tb; ++n) {
-                mbar_wait(&sfull[i], (n - ta) & 1, p.err, &abort_flag, lim);
-                tc_fence_after();
-                uint32_t v[128];
-                tc_ld32(tS, v);
-                tc_ld32(tS + 32, v + 32);
-                tc_ld32(tS + 64, v + 64);
-                tc_ld32(tS + 96, v + 96);
-                tc_wait_ld();
-                tc_regs_ready(v);
-                if (n * C::BN + C::BN - 1 > w_last || n * C::BN < w_first) {
-                    const int hi = last - n * C::BN, lo = first - n * C::BN;   // columns lo .. hi are seen
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        // bits of the 32 columns from 32 b on
-                        const int h = hi + 1 - 32 * b, g = lo - 32 * b;
-                        const uint32_t below = h >= 32 ? 0xffffffffu : (h <= 0 ? 0u : (1u << h) - 1u);
-                        const uint32_t seen = g <= 0 ? below : (g >= 32 ? 0u : below & (0xffffffffu << g));
-#pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            if (!(seen & (1u << c))) v[32 * b + c] = 0xff800000u;
-                    }
+            uint32_t s_seen = 0, o_seen = 0;
+            int item = 0;
+            for (uint32_t id = blockIdx.x; id < n_items; id += step, ++item) {
+                int last, first, w_last, w_first, ta, tb;
+                {
+                    const PromptTile w = load_item(id);
+                    const Range r = ranges(w);
+                    last = w.last(row);
+                    first = w.first(row, p.window);
+                    // tiles that every row of the warp sees whole need no mask
+                    w_last = w.last(i * 128 + (warp & 3) * 32);
+                    w_first = w.first(i * 128 + (warp & 3) * 32 + 31, p.window);
+                    ta = i ? r.t0[1] : r.t0[0];
+                    tb = i ? r.t1[1] : r.t1[0];
                 }
-                float x0 = __uint_as_float(v[0]), x1 = __uint_as_float(v[1]), x2 = __uint_as_float(v[2]), x3 = __uint_as_float(v[3]);
+                float m = -INFINITY, l = 0.0f;
+                for (int n = ta; n < tb; ++n) {
+                    mbar_wait(&sfull[i], s_seen & 1, p.err, &abort_flag, lim);
+                    ++s_seen;
+                    tc_fence_after();
+                    uint32_t v[128];
+                    tc_ld32(tS, v);
+                    tc_ld32(tS + 32, v + 32);
+                    tc_ld32(tS + 64, v + 64);
+                    tc_ld32(tS + 96, v + 96);
+                    tc_wait_ld();
+                    tc_regs_ready(v);
+                    if (n * C::BN + C::BN - 1 > w_last || n * C::BN < w_first) {
+                        const int hi = last - n * C::BN, lo = first - n * C::BN;   // columns lo .. hi are seen
 #pragma unroll
-                for (int c = 4; c < 124; c += 8) {
-                    x0 = max3(x0, __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
-                    x1 = max3(x1, __uint_as_float(v[c + 2]), __uint_as_float(v[c + 3]));
-                    x2 = max3(x2, __uint_as_float(v[c + 4]), __uint_as_float(v[c + 5]));
-                    x3 = max3(x3, __uint_as_float(v[c + 6]), __uint_as_float(v[c + 7]));
-                }
-                x0 = max3(x0, __uint_as_float(v[124]), __uint_as_float(v[125]));
-                x1 = max3(x1, __uint_as_float(v[126]), __uint_as_float(v[127]));
-                const float mx = max3(fmaxf(x0, x1), x2, x3) * p.scale_log2;
-                // a first maximum needs no rescaling: O is still zero in that row
-                const bool grow = mx > m + 8.0f;
-                float f = 1.0f;
-                if (grow) {
-                    f = m == -INFINITY ? 1.0f : ex2(m - mx);
-                    m = mx;
-                    l *= f;
-                }
-                if (__any_sync(0xffffffffu, f != 1.0f) && n > ta) {
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 16) {
-                        uint32_t o[16];
-                        tc_ld16(tO + c, o);
-                        tc_wait_ld();
-                        tc_regs_ready(o);
+                        for (int b = 0; b < 4; ++b) {
+                            // bits of the 32 columns from 32 b on
+                            const int h = hi + 1 - 32 * b, g = lo - 32 * b;
+                            const uint32_t below = h >= 32 ? 0xffffffffu : (h <= 0 ? 0u : (1u << h) - 1u);
+                            const uint32_t seen = g <= 0 ? below : (g >= 32 ? 0u : below & (0xffffffffu << g));
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        tc_st16(tO + c, o);
-                    }
-                }
-                const float neg = m == -INFINITY ? 0.0f : -m;
-                const uint64_t scale2 = pair2(p.scale_log2, p.scale_log2), neg2 = pair2(neg, neg);
-                uint64_t s0 = 0, s1 = 0;
-#pragma unroll
-                for (int b = 0; b < 128; b += 32) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int c = 0; c < 32; c += 4) {
-                        float a0, a1, a2, a3;
-                        split2(a0, a1, fma2(pair2(__uint_as_float(v[b + c]), __uint_as_float(v[b + c + 1])), scale2, neg2));
-                        split2(a2, a3, fma2(pair2(__uint_as_float(v[b + c + 2]), __uint_as_float(v[b + c + 3])), scale2, neg2));
-                        a0 = ex2(a0);
-                        a1 = ex2(a1);
-                        a2 = ex2(a2);
-                        a3 = ex2(a3);
-                        s0 = add2(s0, pair2(a0, a1));
-                        s1 = add2(s1, pair2(a2, a3));
-                        pk[c / 2] = pack16<BF16>(a0, a1);
-                        pk[c / 2 + 1] = pack16<BF16>(a2, a3);
-                    }
-                    tc_st16(tS + b / 2, pk);
-                }
-                float l0, l1;
-                split2(l0, l1, add2(s0, s1));
-                l += l0 + l1;
-                tc_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&pfull[i]);
-            }
-            // ---- results
-            const bool has = tb > ta;
-            if (has) mbar_wait(&ofull[i], 0, p.err, &abort_flag, lim);
-            tc_fence_after();
-            float lse;
-            const float f = softmax_finish(m, l, p.sinks != nullptr, p.sinks ? p.sinks[head] * 1.4426950408889634f : 0.0f, lse);
-            const bool mine = row < w.rows;
-            const uint64_t orow = (uint64_t)(w.q0 + w.row0 + row) * p.n_heads + head;
-            const bool fix = dirty != 0;
-#pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-                uint32_t o[32];
-                tc_ld32(tO + c, o);
-                tc_wait_ld();
-                tc_regs_ready(o);
-                float y[32];
-#pragma unroll
-                for (int e = 0; e < 32; ++e) y[e] = f == 0.0f ? 0.0f : __uint_as_float(o[e]) * f;
-                if (mine) {
-                    if (fix) {
-                        const uint16_t *vp = static_cast<const uint16_t *>(p.v) + (uint64_t)w.k0 * p.v_stride + (uint64_t)kvh * D + c;
-#pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            float z[8];
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) z[k] = y[e + k];
-                            prompt_restore<BF16>(p, w, vp + e, row, C::BN, z);
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) y[e + k] = z[k];
+                            for (int c = 0; c < 32; ++c)
+                                if (!(seen & (1u << c))) v[32 * b + c] = 0xff800000u;
                         }
                     }
-                    store_row32(p, orow, c, y);
+                    float x0 = __uint_as_float(v[0]), x1 = __uint_as_float(v[1]), x2 = __uint_as_float(v[2]), x3 = __uint_as_float(v[3]);
+#pragma unroll
+                    for (int c = 4; c < 124; c += 8) {
+                        x0 = max3(x0, __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
+                        x1 = max3(x1, __uint_as_float(v[c + 2]), __uint_as_float(v[c + 3]));
+                        x2 = max3(x2, __uint_as_float(v[c + 4]), __uint_as_float(v[c + 5]));
+                        x3 = max3(x3, __uint_as_float(v[c + 6]), __uint_as_float(v[c + 7]));
+                    }
+                    x0 = max3(x0, __uint_as_float(v[124]), __uint_as_float(v[125]));
+                    x1 = max3(x1, __uint_as_float(v[126]), __uint_as_float(v[127]));
+                    const float mx = max3(fmaxf(x0, x1), x2, x3) * p.scale_log2;
+                    // a first maximum needs no rescaling: O is still zero in that row
+                    const bool grow = mx > m + 8.0f;
+                    float f = 1.0f;
+                    if (grow) {
+                        f = m == -INFINITY ? 1.0f : ex2(m - mx);
+                        m = mx;
+                        l *= f;
+                    }
+                    if (__any_sync(0xffffffffu, f != 1.0f) && n > ta) {
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 16) {
+                            uint32_t o[16];
+                            tc_ld16(tO + c, o);
+                            tc_wait_ld();
+                            tc_regs_ready(o);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tc_st16(tO + c, o);
+                        }
+                    }
+                    const float neg = m == -INFINITY ? 0.0f : -m;
+                    const uint64_t scale2 = pair2(p.scale_log2, p.scale_log2), neg2 = pair2(neg, neg);
+                    uint64_t s0 = 0, s1 = 0;
+#pragma unroll
+                    for (int b = 0; b < 128; b += 32) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int c = 0; c < 32; c += 4) {
+                            float a0, a1, a2, a3;
+                            split2(a0, a1, fma2(pair2(__uint_as_float(v[b + c]), __uint_as_float(v[b + c + 1])), scale2, neg2));
+                            split2(a2, a3, fma2(pair2(__uint_as_float(v[b + c + 2]), __uint_as_float(v[b + c + 3])), scale2, neg2));
+                            a0 = ex2(a0);
+                            a1 = ex2(a1);
+                            a2 = ex2(a2);
+                            a3 = ex2(a3);
+                            s0 = add2(s0, pair2(a0, a1));
+                            s1 = add2(s1, pair2(a2, a3));
+                            pk[c / 2] = pack16<BF16>(a0, a1);
+                            pk[c / 2 + 1] = pack16<BF16>(a2, a3);
+                        }
+                        tc_st16(tS + b / 2, pk);
+                    }
+                    float l0, l1;
+                    split2(l0, l1, add2(s0, s1));
+                    l += l0 + l1;
+                    tc_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&pfull[i]);
                 }
+                // ---- results
+                const bool has = tb > ta;
+                if (has) {
+                    mbar_wait(&ofull[i], o_seen & 1, p.err, &abort_flag, lim);
+                    ++o_seen;
+                }
+                tc_fence_after();
+                const PromptTile w = load_item(id);
+                const uint32_t head = id % p.n_heads, kvh = head / group;
+                float lse;
+                const float f = softmax_finish(m, l, p.sinks != nullptr, p.sinks ? p.sinks[head] * 1.4426950408889634f : 0.0f, lse);
+                const bool mine = row < w.rows;
+                const uint64_t orow = (uint64_t)(w.q0 + w.row0 + row) * p.n_heads + head;
+                const bool fix = dirty[item & 7] == item + 1;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    tc_ld32(tO + c, o);
+                    tc_wait_ld();
+                    tc_regs_ready(o);
+                    float y[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) y[e] = f == 0.0f ? 0.0f : __uint_as_float(o[e]) * f;
+                    if (mine) {
+                        if (fix) {
+                            const uint16_t *vp = static_cast<const uint16_t *>(p.v) + (uint64_t)w.k0 * p.v_stride + (uint64_t)kvh * D + c;
+#pragma unroll
+                            for (int e = 0; e < 32; e += 8) {
+                                float z[8];
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) z[k] = y[e + k];
+                                prompt_restore<BF16>(p, w, vp + e, row, C::BN, z);
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) y[e + k] = z[k];
+                            }
+                        }
+                        store_row32(p, orow, c, y);
+                    }
+                }
+                if (p.lse && mine) p.lse[orow] = lse;
+                tc_fence_before();   // O is read: the next tile's first P V follows this warp's next arrival
             }
-            if (p.lse && mine) p.lse[orow] = lse;
         }
     }
     tc_fence_before();
@@ -382,7 +515,7 @@ __global__ void __launch_bounds__(Pt<D>::THREADS, 1)
     }
 }
 
-template <int D, bool BF16> cudaError_t launch_tc(const AttnPromptParams &p, cudaStream_t st) {
+template <int D, bool BF16> cudaError_t launch_tc(const AttnPromptParams &p, int num_sms, cudaStream_t st) {
     static bool attr_done = false;
     if (!attr_done) {
         const cudaError_t e = cudaFuncSetAttribute(k_attn_prompt_tc<D, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -396,7 +529,7 @@ template <int D, bool BF16> cudaError_t launch_tc(const AttnPromptParams &p, cud
         !encode_rows16_tmap(&tmV, p.v, (uint64_t)p.n_kv * D, p.n_k, p.v_stride, 128, BF16))
         return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.n_heads, p.n_q / Pt<D>::BM + p.n_seq);   // heads of one tile side by side, long tiles first
+    cfg.gridDim = dim3(p.list ? (unsigned)num_sms : (unsigned)(p.n_heads * (p.n_q / Pt<D>::BM + p.n_seq)));
     cfg.blockDim = dim3(Pt<D>::THREADS);
     cfg.dynamicSmemBytes = Pt<D>::SMEM;
     cfg.stream = st;
@@ -411,10 +544,22 @@ template <int D, bool BF16> cudaError_t launch_tc(const AttnPromptParams &p, cud
 
 }  // namespace
 
-cudaError_t launch_attn_prompt_tc(const AttnPromptParams &p, cudaStream_t st) {
+size_t attn_prompt_list_bytes(const AttnPromptParams &p, int num_sms) {
+    const uint64_t tiles = p.n_q / 256 + p.n_seq;
+    return tiles * p.n_heads > (uint64_t)num_sms ? (tiles + 1) * sizeof(PromptTile) : 0;
+}
+
+cudaError_t launch_attn_prompt_tc(AttnPromptParams p, void *list, int num_sms, cudaStream_t st) {
+    if (list) {
+        p.list = static_cast<PromptTile *>(list);
+        p.list_cap = p.n_q / 256 + p.n_seq;
+        for (p.list_shift = 0; (p.n_k / 128 >> p.list_shift) >= LIST_BINS - 1; ++p.list_shift) {}
+        const cudaError_t e = launch_dependent(k_attn_prompt_list, p, dim3(1), LIST_THREADS, 0, st);
+        if (e != cudaSuccess) return e;
+    }
     const bool bf = p.type == Q8_TYPE_BF16;
-    if (p.dim == 64) return bf ? launch_tc<64, true>(p, st) : launch_tc<64, false>(p, st);
-    return bf ? launch_tc<128, true>(p, st) : launch_tc<128, false>(p, st);
+    if (p.dim == 64) return bf ? launch_tc<64, true>(p, num_sms, st) : launch_tc<64, false>(p, num_sms, st);
+    return bf ? launch_tc<128, true>(p, num_sms, st) : launch_tc<128, false>(p, num_sms, st);
 }
 
 }  // namespace q8

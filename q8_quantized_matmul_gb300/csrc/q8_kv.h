@@ -83,6 +83,8 @@ struct AttnDecodeParams {
 int attn_decode_grid(uint32_t dim, int cache_type, int num_sms);
 cudaError_t launch_attn_decode(const AttnDecodeParams &p, int grid, cudaStream_t st);
 
+struct PromptTile;   // q8_attn_prompt.cuh
+
 struct AttnPromptParams {
     const void *q, *k, *v;
     int type;
@@ -101,11 +103,17 @@ struct AttnPromptParams {
     // Failure-detection test hook (tcgen05 kernel; zero in normal calls): see GemvParams
     uint64_t wait_ns;
     int withhold;
+    // tcgen05 kernel: the list of tiles (its first element holds their number), or nullptr
+    PromptTile *list;
+    uint32_t list_cap;
+    int list_shift;
 };
 // Whether a call runs on the tcgen05 kernel (heads of 64 or 128 values, some keys), else mma.sync.
 inline bool attn_prompt_on_tc(uint32_t dim, uint64_t n_k) { return dim <= 128 && n_k > 0; }
-cudaError_t launch_attn_prompt_tc(const AttnPromptParams &p, cudaStream_t st);
-cudaError_t launch_attn_prompt(const AttnPromptParams &p, cudaStream_t st);
+// Scratch for the tile list of a call (0: none needed), then the call with it.
+size_t attn_prompt_list_bytes(const AttnPromptParams &p, int num_sms);
+cudaError_t launch_attn_prompt_tc(AttnPromptParams p, void *list, int num_sms, cudaStream_t st);
+cudaError_t launch_attn_prompt_mma(const AttnPromptParams &p, cudaStream_t st);
 
 // Launch with programmatic stream serialisation: the kernel starts while the one before
 // it drains and waits (griddepcontrol.wait) before it reads or writes anything.
