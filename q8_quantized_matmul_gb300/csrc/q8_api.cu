@@ -1266,7 +1266,7 @@ int q8_attn_decode(void *out, int out_type, float *lse, const void *q, uint64_t 
     p.n_seq = n_seq;
     p.n_heads = n_heads;
     p.group = n_heads / c->n_kv_heads;
-    p.mtiles = (p.group + 15) / 16;
+    p.mtiles = (p.group + q8::attn_decode_heads(p.group) - 1) / q8::attn_decode_heads(p.group);
     p.q = q;
     p.q_stride = q_stride;
     p.q_type = q_type;
@@ -1277,7 +1277,7 @@ int q8_attn_decode(void *out, int out_type, float *lse, const void *q, uint64_t 
     p.window = window;
     p.sinks = sinks;
     p.err = s->err;
-    const int grid = q8::attn_decode_grid(c->head_dim, c->type, s->num_sms);
+    const int grid = q8::attn_decode_grid(c->head_dim, p.group, c->type, s->num_sms);
     if ((rc = reserve_counters(s, (size_t)n_seq * c->n_kv_heads * p.mtiles, st))) return rc;
     const size_t part = align256((size_t)grid * 2 * 16 * c->head_dim * sizeof(float));
     if ((rc = reserve_scratch(s, part + align256((size_t)grid * 2 * 16 * 2 * sizeof(float2))))) return rc;

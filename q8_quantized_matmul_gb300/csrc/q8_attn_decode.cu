@@ -6,12 +6,14 @@
 // (all fp32).  Every cached byte is read once, so HBM is the bound: 2 D values per position and
 // key-value head against 4 D operations per query head.
 //
-// Split.  A unit is (sequence, key-value head, tile of 16 of its query heads): those heads share every
-// K and V row and fill the 16 rows of an mma.sync tile (fewer heads leave rows idle; the tensor pipe
-// has the room).  The units' positions, in tiles of TT, form one line that is cut into equal shares,
-// one per CTA, so the lengths do not matter to the balance.  A CTA that covers a whole unit writes its
-// result; otherwise it leaves (m, l, O) in scratch, and the last CTA of a unit to arrive (one counter
-// per unit, set back to zero by it) joins the pieces in their order: the same bits on every run.
+// Split.  A unit is (sequence, key-value head, tile of 8 or 16 of its query heads).  The products run
+// transposed, positions (scores) and V dimensions (output) along the 16 rows of an mma.sync tile and the
+// heads that share K and V along its 8 columns: groups of up to 8 heads waste no rows, and the accumulators
+// of 8 heads by 128 dimensions take 32 registers.  P goes from one product's layout to the other's by
+// movmatrix.  The units' positions, in tiles of TT, form one line that is cut into equal shares, one per
+// CTA, so the lengths do not matter to the balance.  A CTA that covers a whole unit writes its result;
+// otherwise it leaves (m, l, O) in scratch, and the last CTA of a unit to arrive (one counter per unit, set
+// back to zero by it) joins the pieces in their order: the same bits on every run.
 //
 // Inside a CTA each of the four warps takes its own 16 (Q8_0: 32) positions of a tile through its own
 // ring of stages, filled by 16-byte asynchronous copies, and keeps its own (m, l, O): no CTA barrier
@@ -32,8 +34,10 @@
 namespace q8 {
 namespace {
 
-template <int D, int FMT> struct Dec {   // FMT 0: f16, 1: bf16, 2: Q8_0 with f16 q, 3: Q8_0 with bf16 q
+// FMT 0: f16, 1: bf16, 2: Q8_0 with f16 q, 3: Q8_0 with bf16 q; NT tiles of 8 heads a unit
+template <int D, int FMT, int NT> struct Dec {
     static constexpr bool Q8 = FMT >= 2, BF16 = FMT & 1;
+    static constexpr int HR = 8 * NT;                    // heads of a unit
     static constexpr int W = 4;                          // warps
     static constexpr int ST = Q8 ? 32 : 16;              // positions of a warp's slice
     static constexpr int DV = D > 256 ? 256 : D;         // V dimensions of a warp
@@ -45,11 +49,12 @@ template <int D, int FMT> struct Dec {   // FMT 0: f16, 1: bf16, 2: Q8_0 with f1
     static constexpr int STAGE = KB + VB + KSB + VSB;
     static constexpr int NST = D <= 128 ? 3 : 2;         // stages of a warp
     static constexpr bool QREG = D <= 128;               // q fragments in registers (else shared memory)
-    static constexpr int QS = QREG ? 0 : D / 16 * 512;   // q fragments, [k step][lane] of 16 bytes
-    static constexpr int MERGE = 16 * DV * 4;            // a warp's O at the end of a share
+    static constexpr int QS = QREG ? 0 : D / 16 * NT * 256;   // q fragments, [k step][head tile][lane] of 8 bytes
+    static constexpr int MERGE = HR * DV * 4;            // a warp's O at the end of a share
     static constexpr int RING = NST * STAGE > MERGE ? NST * STAGE : MERGE;
-    static constexpr int SMEM = W * RING + QS + W * 16 * 8 + 64;
-    static constexpr int CTAS = SMEM * 4 <= 220 * 1024 && D < 128 ? 4 : (SMEM * 2 <= 220 * 1024 && D <= 128 ? 2 : 1);
+    static constexpr int SMEM = W * RING + QS + W * HR * 8 + 64;
+    static constexpr int FIT = 224 * 1024 / SMEM;
+    static constexpr int CTAS = FIT < 1 ? 1 : (D == 64 ? (FIT < 4 ? FIT : 4) : (D == 128 ? (FIT < 3 ? FIT : 3) : 1));
     static constexpr float BIAS = Q8 ? 15.0f : 0.0f;     // weights are 2^(z - M + BIAS)
     static_assert(STAGE % 128 == 0, "stage alignment");
 };
@@ -75,6 +80,33 @@ template <bool BF16> __device__ __forceinline__ void bytes_to_pairs(uint32_t u, 
         lo = pack16<true>(f0, f1);
         hi = pack16<true>(f2, f3);
     }
+}
+
+// N 32-bit words of shared memory, N * 4 bytes aligned (at most 16).
+template <int N> __device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint8_t *p) {
+    if constexpr (N == 1) {
+        w[0] = *reinterpret_cast<const uint32_t *>(p);
+    } else if constexpr (N == 2) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        w[0] = v.x;
+        w[1] = v.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(p + 4 * i);
+            w[i] = v.x;
+            w[i + 1] = v.y;
+            w[i + 2] = v.z;
+            w[i + 3] = v.w;
+        }
+    }
+}
+
+// 8 x 8 16-bit matrix, two elements of row lane / 4 a thread, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 
 struct Seq {
@@ -111,13 +143,14 @@ __device__ __forceinline__ void finish8(const AttnDecodeParams &p, uint32_t s, u
     if (active && p.lse && d0 == 0) p.lse[row] = lse;
 }
 
-template <int D, int FMT> __global__ void __launch_bounds__(128, Dec<D, FMT>::CTAS) k_attn_decode(const AttnDecodeParams p) {
-    using C = Dec<D, FMT>;
+template <int D, int FMT, int NT>
+__global__ void __launch_bounds__(128, Dec<D, FMT, NT>::CTAS) k_attn_decode(const AttnDecodeParams p) {
+    using C = Dec<D, FMT, NT>;
     constexpr bool BF16 = C::BF16, Q8 = C::Q8;
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t *qs = smem + C::W * C::RING;
-    float2 *ml = reinterpret_cast<float2 *>(qs + C::QS);        // [warp][16]
-    int *sh = reinterpret_cast<int *>(ml + C::W * 16);          // small shared words
+    float2 *ml = reinterpret_cast<float2 *>(qs + C::QS);        // [warp][HR]
+    int *sh = reinterpret_cast<int *>(ml + C::W * C::HR);          // small shared words
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, c = lane & 3;
     const int half = warp % C::NDH, slice = warp / C::NDH;
@@ -185,45 +218,53 @@ template <int D, int FMT> __global__ void __launch_bounds__(128, Dec<D, FMT>::CT
     }
 
     bool first = true;
-    for (int64_t t = t0; t < t1; first = false) {
+    for (int64_t tile = t0; tile < t1; first = false) {
         Seq q = seq_of<C>(p, s, false);
-        while (t >= s_base + (int64_t)q.tiles * units_per_seq) {
+        while (tile >= s_base + (int64_t)q.tiles * units_per_seq) {
             s_base += (int64_t)q.tiles * units_per_seq;
             q = seq_of<C>(p, ++s, false);
         }
-        const uint32_t unit = (uint32_t)((t - s_base) / q.tiles);
+        const uint32_t unit = (uint32_t)((tile - s_base) / q.tiles);
         const int64_t u0 = s_base + (int64_t)unit * q.tiles;     // the unit's tiles on the line
-        const int ta = (int)(t - u0), tb = (int)min((int64_t)q.tiles, t1 - u0);
+        const int ta = (int)(tile - u0), tb = (int)min((int64_t)q.tiles, t1 - u0);
         const uint32_t kvh = unit / p.mtiles, mt = unit % p.mtiles;
-        const uint32_t head0 = kvh * p.group + mt * 16;
-        const int rows = (int)min(16u, p.group - mt * 16);
-        const bool two = rows > 8;
+        const uint32_t head0 = kvh * p.group + mt * C::HR;
+        const int rows = (int)min((uint32_t)C::HR, p.group - mt * C::HR);
 
         // ---- q fragments
         const uint16_t *qrow = static_cast<const uint16_t *>(p.q) + (uint64_t)s * p.q_stride + (uint64_t)head0 * D;
-        // K step ks covers 16 values; in a thread's fragment a0, a1 (rows g, g + 8) hold values k0, k0 + 1
-        // and a2, a3 values k1, k1 + 1: of 16 in the usual order, or, for Q8_0, four in a row out of the
-        // eight that one thread reads from each block.
-        auto qfrag = [&](int ks, uint32_t (&f)[4]) {
+        // K step ks covers 16 values of head 8 t + g: a thread holds values k0, k0 + 1 and k1, k1 + 1, in the usual
+        // order, or, for Q8_0, four in a row out of the eight that one thread reads from each block.
+        auto qfrag = [&](int ks, int t, uint32_t (&f)[2]) {
             const int k0 = Q8 ? ks / 2 * 32 + 8 * c + ks % 2 * 4 : ks * 16 + 2 * c, k1 = Q8 ? k0 + 2 : k0 + 8;
-            const uint16_t *ra = qrow + g * D, *rb = ra + 8 * D;
-            f[0] = g < rows ? *reinterpret_cast<const uint32_t *>(ra + k0) : 0u;
-            f[1] = g + 8 < rows ? *reinterpret_cast<const uint32_t *>(rb + k0) : 0u;
-            f[2] = g < rows ? *reinterpret_cast<const uint32_t *>(ra + k1) : 0u;
-            f[3] = g + 8 < rows ? *reinterpret_cast<const uint32_t *>(rb + k1) : 0u;
+            const uint16_t *r = qrow + (8 * t + g) * D;
+            f[0] = 8 * t + g < rows ? *reinterpret_cast<const uint32_t *>(r + k0) : 0u;
+            f[1] = 8 * t + g < rows ? *reinterpret_cast<const uint32_t *>(r + k1) : 0u;
         };
-        uint32_t qr[C::QREG ? D / 16 : 1][4];
+        uint32_t qr[C::QREG ? D / 16 : 1][NT][2];
         if constexpr (C::QREG) {
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) qfrag(ks, qr[ks]);
+            for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+                for (int t = 0; t < NT; ++t) qfrag(ks, t, qr[ks][t]);
         } else {
-            for (int ks = warp; ks < D / 16; ks += C::W) {
-                uint32_t f[4];
-                qfrag(ks, f);
-                reinterpret_cast<uint4 *>(qs)[ks * 32 + lane] = make_uint4(f[0], f[1], f[2], f[3]);
+            for (int i = warp; i < D / 16 * NT; i += C::W) {
+                uint32_t f[2];
+                qfrag(i / NT, i % NT, f);
+                reinterpret_cast<uint2 *>(qs)[i * 32 + lane] = make_uint2(f[0], f[1]);
             }
             __syncthreads();
         }
+        auto q_of = [&](int ks, int t, uint32_t &b0, uint32_t &b1) {
+            if constexpr (C::QREG) {
+                b0 = qr[ks][t][0];
+                b1 = qr[ks][t][1];
+            } else {
+                const uint2 f = reinterpret_cast<const uint2 *>(qs)[(ks * NT + t) * 32 + lane];
+                b0 = f.x;
+                b1 = f.y;
+            }
+        };
 
         // ---- staging: slice i of this warp covers positions pos0 + i * TT ..
         const int pos0 = q.start + ta * C::TT + slice * C::ST, n_it = tb - ta;
@@ -255,11 +296,11 @@ template <int D, int FMT> __global__ void __launch_bounds__(128, Dec<D, FMT>::CT
                     const int bit = it % C::NST * 2 + j;
                     dead_of = (dead_of & ~(1u << bit)) | (id < 0 ? 1u << bit : 0u);
                     const int a = p0 + 16 * j;                   // 16 positions of one page
-                    const uint64_t tile = (uint64_t)max(id, 0) * p.c.page_stride + (uint64_t)kvh * p.c.tile_bytes;
+                    const uint64_t page = (uint64_t)max(id, 0) * p.c.page_stride + (uint64_t)kvh * p.c.tile_bytes;
                     const uint32_t in = (uint32_t)a & ((1u << p.c.page_shift) - 1u);
                     constexpr int ROW = D * (Q8 ? 1 : 2), CH = ROW / 16, VCH = C::DV * (Q8 ? 1 : 2) / 16;
-                    const uint8_t *k = p.c.k + tile + (uint64_t)in * ROW;
-                    const uint8_t *v = p.c.v + tile + (uint64_t)in * ROW + half * VCH * 16;
+                    const uint8_t *k = p.c.k + page + (uint64_t)in * ROW;
+                    const uint8_t *v = p.c.v + page + (uint64_t)in * ROW + half * VCH * 16;
 #pragma unroll
                     for (int e = 0; e < 16 * CH / 32; ++e) {
                         const int i = e * 32 + lane, r = i / CH, ch = i % CH;
@@ -276,7 +317,7 @@ template <int D, int FMT> __global__ void __launch_bounds__(128, Dec<D, FMT>::CT
                     }
                     if constexpr (Q8) {                           // scales: not masked here, see below
                         constexpr int SR = D / 32 * 2, SV = C::DV / 32 * 2;   // bytes a position
-                        const uint64_t so = tile + ((uint64_t)D << p.c.page_shift) + (uint64_t)in * SR;
+                        const uint64_t so = page + ((uint64_t)D << p.c.page_shift) + (uint64_t)in * SR;
                         const bool ok = id >= 0 && a < q.hi;
 #pragma unroll
                         for (int e = 0; e < (16 * SR + 511) / 512; ++e) {
@@ -299,10 +340,18 @@ template <int D, int FMT> __global__ void __launch_bounds__(128, Dec<D, FMT>::CT
             cp_async_commit();
         };
 
-        float o[C::DV / 8][4];
+        // O, transposed: tile dt, head tile t: rows (dims) g and g + 8, columns (heads) 2c and 2c + 1
+        float o[C::DV / 16][NT][4];
 #pragma unroll
-        for (int i = 0; i < C::DV / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+        for (int i = 0; i < C::DV / 16; ++i)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) o[i][t][0] = o[i][t][1] = o[i][t][2] = o[i][t][3] = 0.0f;
+        float m[NT][2], l[NT][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            m[t][0] = m[t][1] = -INFINITY;
+            l[t][0] = l[t][1] = 0.0f;
+        }
 #pragma unroll
         for (int i = 0; i < C::NST - 1; ++i) stage(i);
 
@@ -314,171 +363,186 @@ template <int D, int FMT> __global__ void __launch_bounds__(128, Dec<D, FMT>::CT
             const uint32_t st_s = ring_s + (it % C::NST) * C::STAGE;
             const int p0 = pos0 + it * C::TT;
             if (p0 < q.hi) {                                     // the last tile may end before this slice
-                constexpr int NT = C::ST / 8;
-                float z[NT][4];
+                constexpr int MT = C::ST / 16;                   // tiles of 16 positions: rows g and g + 8
+                float z[MT][NT][4];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) z[n][0] = z[n][1] = z[n][2] = z[n][3] = 0.0f;
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) z[i][t][0] = z[i][t][1] = z[i][t][2] = z[i][t][3] = 0.0f;
                 // ---- scores
                 if constexpr (!Q8) {
-                    const int r = (lane >> 4) * 8 + (lane & 7), hc = (lane >> 3) & 1;
+                    const int r = ((lane >> 3) & 1) * 8 + (lane & 7), hc = lane >> 4;
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks) {
-                        uint32_t b[4];
-                        ldsm4(b, st_s + r * (D * 2) + swz<D, Q8, false>(r, ks * 2 + hc) * 16);
-                        if constexpr (C::QREG) {
-                            mma16<BF16>(z[0], qr[ks], b[0], b[1]);
-                            mma16<BF16>(z[1], qr[ks], b[2], b[3]);
-                        } else {
-                            const uint4 f = reinterpret_cast<const uint4 *>(qs)[ks * 32 + lane];
-                            const uint32_t a[4] = {f.x, f.y, f.z, f.w};
-                            mma16<BF16>(z[0], a, b[0], b[1]);
-                            mma16<BF16>(z[1], a, b[2], b[3]);
+                        uint32_t a[4];
+                        ldsm4(a, st_s + r * (D * 2) + swz<D, Q8, false>(r, ks * 2 + hc) * 16);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            uint32_t b0, b1;
+                            q_of(ks, t, b0, b1);
+                            mma16<BF16>(z[0][t], a, b0, b1);
                         }
                     }
                 } else {
-                    const uint16_t *ks_s = reinterpret_cast<const uint16_t *>(st + C::KB + C::VB);
 #pragma unroll
-                    for (int b = 0; b < D / 32; ++b) {
-                        uint32_t a0[4], a1[4];
-                        if constexpr (C::QREG) {
+                    for (int i = 0; i < MT; ++i) {
+                        const int ra = 16 * i + g, rb = ra + 8;
+                        uint32_t da[D / 64], db[D / 64];         // K scales of the thread's two positions
+                        load_words<D / 64>(da, st + C::KB + C::VB + ra * (D / 16));
+                        load_words<D / 64>(db, st + C::KB + C::VB + rb * (D / 16));
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                a0[i] = qr[2 * b][i];
-                                a1[i] = qr[2 * b + 1][i];
+                        for (int b = 0; b < D / 32; ++b) {
+                            const uint2 wa = *reinterpret_cast<const uint2 *>(st + ra * D + swz<D, true, false>(ra, 2 * b) * 16 + 8 * c);
+                            const uint2 wb = *reinterpret_cast<const uint2 *>(st + rb * D + swz<D, true, false>(rb, 2 * b) * 16 + 8 * c);
+                            uint32_t a0[4], a1[4];
+                            bytes_to_pairs<BF16>(wa.x ^ 0x80808080u, a0[0], a0[2]);
+                            bytes_to_pairs<BF16>(wb.x ^ 0x80808080u, a0[1], a0[3]);
+                            bytes_to_pairs<BF16>(wa.y ^ 0x80808080u, a1[0], a1[2]);
+                            bytes_to_pairs<BF16>(wb.y ^ 0x80808080u, a1[1], a1[3]);
+                            const float sa = half_bits_to_float((uint16_t)(da[b / 2] >> (b % 2 * 16)));
+                            const float sb = half_bits_to_float((uint16_t)(db[b / 2] >> (b % 2 * 16)));
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) {
+                                uint32_t b0, b1;
+                                float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                                q_of(2 * b, t, b0, b1);
+                                mma16<BF16>(acc, a0, b0, b1);
+                                q_of(2 * b + 1, t, b0, b1);
+                                mma16<BF16>(acc, a1, b0, b1);
+                                z[i][t][0] += acc[0] * sa;
+                                z[i][t][1] += acc[1] * sa;
+                                z[i][t][2] += acc[2] * sb;
+                                z[i][t][3] += acc[3] * sb;
                             }
-                        } else {
-                            const uint4 f0 = reinterpret_cast<const uint4 *>(qs)[2 * b * 32 + lane];
-                            const uint4 f1 = reinterpret_cast<const uint4 *>(qs)[(2 * b + 1) * 32 + lane];
-                            a0[0] = f0.x; a0[1] = f0.y; a0[2] = f0.z; a0[3] = f0.w;
-                            a1[0] = f1.x; a1[1] = f1.y; a1[2] = f1.z; a1[3] = f1.w;
-                        }
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            const int r = 8 * n + g, ch = swz<D, true, false>(r, 2 * b);
-                            const uint2 w = *reinterpret_cast<const uint2 *>(st + r * D + ch * 16 + 8 * c);
-                            uint32_t b0, b1, b2, b3;
-                            bytes_to_pairs<BF16>(w.x ^ 0x80808080u, b0, b1);
-                            bytes_to_pairs<BF16>(w.y ^ 0x80808080u, b2, b3);
-                            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                            mma16<BF16>(acc, a0, b0, b1);
-                            mma16<BF16>(acc, a1, b2, b3);
-                            const float d0 = half_bits_to_float(ks_s[(8 * n + 2 * c) * (D / 32) + b]);
-                            const float d1 = half_bits_to_float(ks_s[(8 * n + 2 * c + 1) * (D / 32) + b]);
-                            z[n][0] += acc[0] * d0;
-                            z[n][1] += acc[1] * d1;
-                            z[n][2] += acc[2] * d0;
-                            z[n][3] += acc[3] * d1;
                         }
                     }
                 }
                 // ---- mask, running maximum
                 const bool edge = p0 < q.lo || p0 + C::ST > q.hi;
-                const uint32_t dead = (dead_of >> (it % C::NST * 2)) & (C::ST / 16 == 2 ? 3u : 1u);   // bit j: piece j
+                const uint32_t dead = (dead_of >> (it % C::NST * 2)) & (MT == 2 ? 3u : 1u);   // bit j: piece j
                 float e_max = 0.0f;                              // Q8_0: |V scales| < 2^e_max
-                const uint16_t *vs_s = reinterpret_cast<const uint16_t *>(st + C::KB + C::VB + C::KSB);
+                const uint8_t *vs_s = st + C::KB + C::VB + C::KSB;
                 if constexpr (Q8) {
                     const int at = p0 + lane;                    // one position a lane
                     uint32_t big = 0;
-                    if (at >= q.lo && at < q.hi && !((dead >> (lane / 16)) & 1))
+                    if (at >= q.lo && at < q.hi && !((dead >> (lane / 16)) & 1)) {
+                        uint32_t w[C::DV / 64];
+                        load_words<C::DV / 64>(w, vs_s + lane * (C::DV / 16));
 #pragma unroll
-                        for (int i = 0; i < C::DV / 32; ++i) big = max(big, (uint32_t)vs_s[lane * (C::DV / 32) + i] & 0x7fffu);
+                        for (int i = 0; i < C::DV / 64; ++i) big = max(big, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+                    }
                     big = __reduce_max_sync(0xffffffffu, big);
                     e_max = (float)((int)(big >> 10) - 14);
                 }
-                float mx[2] = {-INFINITY, -INFINITY};
+                uint32_t seen = ~0u;                             // bit 2 i + h: position 16 i + g + 8 h
+                if (edge || dead) {
+                    seen = 0;
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float v = z[n][i] * p.scale_log2;
-                        if (edge || dead) {
-                            const int at = p0 + 8 * n + 2 * c + (i & 1);
-                            if (at < q.lo || at >= q.hi || ((dead >> (n / 2)) & 1)) v = -INFINITY;
-                        }
-                        z[n][i] = v;
-                        mx[i >> 1] = fmaxf(mx[i >> 1], v);
+                    for (int i = 0; i < 2 * MT; ++i) {
+                        const int at = p0 + 8 * i + g;
+                        seen |= (uint32_t)(at >= q.lo && at < q.hi && !((dead >> (i / 2)) & 1)) << i;
                     }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
-                    mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
-                    mx[h] += e_max;
                 }
-                const bool grow = mx[0] > m[0] || mx[1] > m[1];
-                if (__any_sync(0xffffffffu, grow)) {
+                float mx[NT][2];
+                bool grow = false;
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    mx[t][0] = mx[t][1] = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float v = z[i][t][e] * p.scale_log2;
+                            if (!(seen & (1u << (2 * i + (e >> 1))))) v = -INFINITY;
+                            z[i][t][e] = v;
+                            mx[t][e & 1] = fmaxf(mx[t][e & 1], v);
+                        }
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const float mn = fmaxf(m[h], mx[h]);
-                        const float f = m[h] == -INFINITY ? 0.0f : ex2(m[h] - mn);
-                        m[h] = mn;
-                        l[h] *= f;
 #pragma unroll
-                        for (int i = 0; i < C::DV / 8; ++i) {
-                            o[i][2 * h] *= f;
-                            o[i][2 * h + 1] *= f;
-                        }
+                        for (int x = 4; x < 32; x <<= 1) mx[t][h] = fmaxf(mx[t][h], __shfl_xor_sync(0xffffffffu, mx[t][h], x));
+                        mx[t][h] += e_max;
+                        grow |= mx[t][h] > m[t][h];
                     }
+                }
+                if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float mn = fmaxf(m[t][h], mx[t][h]);
+                            const float f = m[t][h] == -INFINITY ? 0.0f : ex2(m[t][h] - mn);
+                            m[t][h] = mn;
+                            l[t][h] *= f;
+#pragma unroll
+                            for (int i = 0; i < C::DV / 16; ++i) {
+                                o[i][t][h] *= f;
+                                o[i][t][2 + h] *= f;
+                            }
+                        }
                 }
                 // ---- weights
-                const float s0 = m[0] == -INFINITY ? 0.0f : m[0] - C::BIAS, s1 = m[1] == -INFINITY ? 0.0f : m[1] - C::BIAS;
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    z[n][0] = ex2(z[n][0] - s0);
-                    z[n][1] = ex2(z[n][1] - s0);
-                    l[0] += z[n][0] + z[n][1];
-                    if (two) {
-                        z[n][2] = ex2(z[n][2] - s1);
-                        z[n][3] = ex2(z[n][3] - s1);
-                        l[1] += z[n][2] + z[n][3];
-                    } else {
-                        z[n][2] = z[n][3] = 0.0f;
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float s = m[t][h] == -INFINITY ? 0.0f : m[t][h] - C::BIAS;
+#pragma unroll
+                        for (int i = 0; i < MT; ++i) {
+                            z[i][t][h] = ex2(z[i][t][h] - s);
+                            z[i][t][2 + h] = ex2(z[i][t][2 + h] - s);
+                            l[t][h] += z[i][t][h] + z[i][t][2 + h];
+                        }
                     }
-                }
-                // ---- O += P V
+                // ---- O^T += V^T P^T
                 if constexpr (!Q8) {
-                    const uint32_t a[4] = {pack16<BF16>(z[0][0], z[0][1]), pack16<BF16>(z[0][2], z[0][3]),
-                                           pack16<BF16>(z[1][0], z[1][1]), pack16<BF16>(z[1][2], z[1][3])};
-                    const int r = ((lane >> 3) & 1) * 8 + (lane & 7), hc = lane >> 4;
+                    uint32_t b[NT][2];
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        b[t][0] = transpose8(pack16<BF16>(z[0][t][0], z[0][t][1]));
+                        b[t][1] = transpose8(pack16<BF16>(z[0][t][2], z[0][t][3]));
+                    }
+                    const int r = (lane >> 4) * 8 + (lane & 7), hc = (lane >> 3) & 1;
 #pragma unroll
                     for (int n = 0; n < C::DV / 16; ++n) {
-                        uint32_t b[4];
-                        ldsm4t(b, st_s + C::KB + r * (C::DV * 2) + swz<C::DV, Q8, true>(r, n * 2 + hc) * 16);
-                        mma16<BF16>(o[2 * n], a, b[0], b[1]);
-                        mma16<BF16>(o[2 * n + 1], a, b[2], b[3]);
+                        uint32_t a[4];
+                        ldsm4t(a, st_s + C::KB + r * (C::DV * 2) + swz<C::DV, Q8, true>(r, n * 2 + hc) * 16);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) mma16<BF16>(o[n][t], a, b[t][0], b[t][1]);
                     }
                 } else {
-                    // weights carry the V scale of their position and block; a masked weight is 0 whatever
-                    // the scale beside it holds
-                    auto w = [](float pz, uint16_t d) { return pz == 0.0f ? 0.0f : pz * half_bits_to_float(d); };
 #pragma unroll
-                    for (int kk = 0; kk < C::ST / 16; ++kk) {
+                    for (int i = 0; i < MT; ++i) {
+                        // the weights carry the V scale of their position and block; nothing beside a masked
+                        // position is used, whatever it holds
+                        const int ra = 16 * i + g;
+                        uint32_t da[C::DV / 64], db[C::DV / 64];
+                        load_words<C::DV / 64>(da, vs_s + ra * (C::DV / 16));
+                        load_words<C::DV / 64>(db, vs_s + (ra + 8) * (C::DV / 16));
+                        const uint32_t ka = seen & (1u << (2 * i)) ? 0xffffffffu : 0u, kb = seen & (2u << (2 * i)) ? 0xffffffffu : 0u;
+                        const int r0 = 16 * i + 2 * c;
 #pragma unroll
                         for (int b = 0; b < C::DV / 32; ++b) {
-                            const int r0 = 16 * kk + 2 * c;
-                            const uint16_t d0 = vs_s[r0 * (C::DV / 32) + b], d1 = vs_s[(r0 + 1) * (C::DV / 32) + b];
-                            const uint16_t d8 = vs_s[(r0 + 8) * (C::DV / 32) + b], d9 = vs_s[(r0 + 9) * (C::DV / 32) + b];
-                            const float(&za)[4] = z[2 * kk];
-                            const float(&zb)[4] = z[2 * kk + 1];
-                            const uint32_t a[4] = {pack16<false>(w(za[0], d0), w(za[1], d1)),
-                                                   pack16<false>(w(za[2], d0), w(za[3], d1)),
-                                                   pack16<false>(w(zb[0], d8), w(zb[1], d9)),
-                                                   pack16<false>(w(zb[2], d8), w(zb[3], d9))};
+                            const float sa = half_bits_to_float((uint16_t)((da[b / 2] & ka) >> (b % 2 * 16)));
+                            const float sb = half_bits_to_float((uint16_t)((db[b / 2] & kb) >> (b % 2 * 16)));
                             // four dims (4g ..) of four positions: pairs along the positions
                             auto word = [&](int r) {
-                                const int ch = swz<C::DV, true, true>(r, 2 * b);
-                                return *reinterpret_cast<const uint32_t *>(st + C::KB + r * C::DV + ch * 16 + 4 * g) ^ 0x80808080u;
+                                return *reinterpret_cast<const uint32_t *>(st + C::KB + r * C::DV +
+                                                                           swz<C::DV, true, true>(r, 2 * b) * 16 + 4 * g) ^ 0x80808080u;
                             };
                             const uint32_t w0 = word(r0), w1 = word(r0 + 1), w8 = word(r0 + 8), w9 = word(r0 + 9);
-                            uint32_t x0, x1, x2, x3, y0, y1, y2, y3;
-                            bytes_to_pairs<false>(__byte_perm(w0, w1, 0x5140), x0, x1);
-                            bytes_to_pairs<false>(__byte_perm(w0, w1, 0x7362), x2, x3);
-                            bytes_to_pairs<false>(__byte_perm(w8, w9, 0x5140), y0, y1);
-                            bytes_to_pairs<false>(__byte_perm(w8, w9, 0x7362), y2, y3);
-                            // column g of tile 4b + j is dim 32b + 4g + j
-                            mma16<false>(o[4 * b], a, x0, y0);
-                            mma16<false>(o[4 * b + 1], a, x1, y1);
-                            mma16<false>(o[4 * b + 2], a, x2, y2);
-                            mma16<false>(o[4 * b + 3], a, x3, y3);
+                            uint32_t a0[4], a1[4];               // dims 4g, 4g + 1 and 4g + 2, 4g + 3 of the block
+                            bytes_to_pairs<false>(__byte_perm(w0, w1, 0x5140), a0[0], a0[1]);
+                            bytes_to_pairs<false>(__byte_perm(w0, w1, 0x7362), a1[0], a1[1]);
+                            bytes_to_pairs<false>(__byte_perm(w8, w9, 0x5140), a0[2], a0[3]);
+                            bytes_to_pairs<false>(__byte_perm(w8, w9, 0x7362), a1[2], a1[3]);
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) {
+                                const uint32_t b0 = transpose8(pack16<false>(z[i][t][0] * sa, z[i][t][1] * sa));
+                                const uint32_t b1 = transpose8(pack16<false>(z[i][t][2] * sb, z[i][t][3] * sb));
+                                mma16<false>(o[2 * b][t], a0, b0, b1);
+                                mma16<false>(o[2 * b + 1][t], a1, b0, b1);
+                            }
                         }
                     }
                 }
@@ -488,25 +552,23 @@ template <int D, int FMT> __global__ void __launch_bounds__(128, Dec<D, FMT>::CT
         cp_async_wait<0>();
 
         // ---- the CTA's share of the unit: four warps' pieces joined
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-        }
-        float *mo = reinterpret_cast<float *>(ring);             // [16][DV]
+        float *mo = reinterpret_cast<float *>(ring);             // [HR][DV]
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < C::DV / 8; ++i)
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                // accumulator columns 2c, 2c + 1 of tile i; Q8_0 tiles interleave their block's dims by four
-                const int col = Q8 ? i / 4 * 32 + 4 * (2 * c + (e & 1)) + i % 4 : 8 * i + 2 * c + (e & 1);
-                mo[(g + (e >> 1) * 8) * C::DV + col] = o[i][e];
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) l[t][h] += __shfl_xor_sync(0xffffffffu, l[t][h], x);
+                if (g == 0) ml[warp * C::HR + 8 * t + 2 * c + h] = make_float2(m[t][h], l[t][h]);
+#pragma unroll
+                for (int i = 0; i < C::DV / 16; ++i) {
+                    // Q8_0 tiles hold dims 4 g + 0, 1 and 4 g + 2, 3 of a block
+                    float *dst = mo + (8 * t + 2 * c + h) * C::DV;
+                    dst[Q8 ? i / 2 * 32 + 4 * g + i % 2 * 2 : 16 * i + g] = o[i][t][h];
+                    dst[Q8 ? i / 2 * 32 + 4 * g + i % 2 * 2 + 1 : 16 * i + g + 8] = o[i][t][2 + h];
+                }
             }
-        if (c == 0) {
-            ml[warp * 16 + g] = make_float2(m[0], l[0]);
-            ml[warp * 16 + g + 8] = make_float2(m[1], l[1]);
-        }
         __syncthreads();
         const bool whole = ta == 0 && tb == q.tiles;
         const uint64_t slot = 2 * (uint64_t)blockIdx.x + (first ? 0 : 1);
@@ -516,10 +578,10 @@ template <int D, int FMT> __global__ void __launch_bounds__(128, Dec<D, FMT>::CT
             const int row = act ? i / (D / 8) : 0, d0 = i % (D / 8) * 8, h = d0 / C::DV;
             float mt = -INFINITY, lt = 0.0f, y[8] = {};
 #pragma unroll
-            for (int w = 0; w < C::SL; ++w) mt = fmaxf(mt, ml[(w * C::NDH + h) * 16 + row].x);
+            for (int w = 0; w < C::SL; ++w) mt = fmaxf(mt, ml[(w * C::NDH + h) * C::HR + row].x);
 #pragma unroll
             for (int w = 0; w < C::SL; ++w) {
-                const float2 x = ml[(w * C::NDH + h) * 16 + row];
+                const float2 x = ml[(w * C::NDH + h) * C::HR + row];
                 const float f = x.x == -INFINITY ? 0.0f : ex2(x.x - mt);
                 lt += x.y * f;
                 const float *src = reinterpret_cast<const float *>(smem + (w * C::NDH + h) * C::RING) + row * C::DV + d0 % C::DV;
@@ -579,51 +641,55 @@ template <int D, int FMT> __global__ void __launch_bounds__(128, Dec<D, FMT>::CT
             }
         }
         __syncthreads();   // the rings, ml and sh are free again
-        t = u0 + tb;
+        tile = u0 + tb;
     }
 }
 
-template <int D, int FMT> int grid_of(int num_sms) { return num_sms * Dec<D, FMT>::CTAS; }
-
-template <int D, int FMT> cudaError_t launch_one(const AttnDecodeParams &p, int grid, cudaStream_t st) {
+template <int D, int FMT, int NT> cudaError_t launch_one(const AttnDecodeParams &p, int grid, cudaStream_t st) {
     static bool attr_done = false;
     if (!attr_done) {
-        const cudaError_t e = cudaFuncSetAttribute(k_attn_decode<D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   Dec<D, FMT>::SMEM);
+        const cudaError_t e = cudaFuncSetAttribute(k_attn_decode<D, FMT, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   Dec<D, FMT, NT>::SMEM);
         if (e != cudaSuccess) return e;
         attr_done = true;
     }
-    return launch_dependent(k_attn_decode<D, FMT>, p, dim3((unsigned)grid), 128, Dec<D, FMT>::SMEM, st);
+    return launch_dependent(k_attn_decode<D, FMT, NT>, p, dim3((unsigned)grid), 128, Dec<D, FMT, NT>::SMEM, st);
 }
 
-template <int D> cudaError_t launch_dim(const AttnDecodeParams &p, int grid, cudaStream_t st) {
+template <int D, int NT> cudaError_t launch_dim(const AttnDecodeParams &p, int grid, cudaStream_t st) {
     const bool bf = p.q_type == Q8_TYPE_BF16;
-    if (p.c.type == Q8_TYPE_Q8_0) return bf ? launch_one<D, 3>(p, grid, st) : launch_one<D, 2>(p, grid, st);
-    return bf ? launch_one<D, 1>(p, grid, st) : launch_one<D, 0>(p, grid, st);
+    if (p.c.type == Q8_TYPE_Q8_0) return bf ? launch_one<D, 3, NT>(p, grid, st) : launch_one<D, 2, NT>(p, grid, st);
+    return bf ? launch_one<D, 1, NT>(p, grid, st) : launch_one<D, 0, NT>(p, grid, st);
 }
 
-template <int D> int grid_dim_of(int cache_type, int num_sms) {
-    return cache_type == Q8_TYPE_Q8_0 ? grid_of<D, 2>(num_sms) : grid_of<D, 0>(num_sms);
+template <int D> cudaError_t launch_heads(const AttnDecodeParams &p, int grid, cudaStream_t st) {
+    return attn_decode_heads(p.group) == 8 ? launch_dim<D, 1>(p, grid, st) : launch_dim<D, 2>(p, grid, st);
+}
+
+template <int D> int grid_of(uint32_t group, int cache_type, int num_sms) {
+    const bool q8 = cache_type == Q8_TYPE_Q8_0;
+    if (attn_decode_heads(group) == 8) return num_sms * (q8 ? Dec<D, 2, 1>::CTAS : Dec<D, 0, 1>::CTAS);
+    return num_sms * (q8 ? Dec<D, 2, 2>::CTAS : Dec<D, 0, 2>::CTAS);
 }
 
 }  // namespace
 
-int attn_decode_grid(uint32_t dim, int cache_type, int num_sms) {
+int attn_decode_grid(uint32_t dim, uint32_t group, int cache_type, int num_sms) {
     switch (dim) {
-        case 64: return grid_dim_of<64>(cache_type, num_sms);
-        case 128: return grid_dim_of<128>(cache_type, num_sms);
-        case 256: return grid_dim_of<256>(cache_type, num_sms);
-        case 512: return grid_dim_of<512>(cache_type, num_sms);
+        case 64: return grid_of<64>(group, cache_type, num_sms);
+        case 128: return grid_of<128>(group, cache_type, num_sms);
+        case 256: return grid_of<256>(group, cache_type, num_sms);
+        case 512: return grid_of<512>(group, cache_type, num_sms);
         default: return 0;
     }
 }
 
 cudaError_t launch_attn_decode(const AttnDecodeParams &p, int grid, cudaStream_t st) {
     switch (p.c.dim) {
-        case 64: return launch_dim<64>(p, grid, st);
-        case 128: return launch_dim<128>(p, grid, st);
-        case 256: return launch_dim<256>(p, grid, st);
-        case 512: return launch_dim<512>(p, grid, st);
+        case 64: return launch_heads<64>(p, grid, st);
+        case 128: return launch_heads<128>(p, grid, st);
+        case 256: return launch_heads<256>(p, grid, st);
+        case 512: return launch_heads<512>(p, grid, st);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -79,8 +79,10 @@ struct AttnDecodeParams {
     int *counters;                        // one per unit, zero between calls
     int *err;
 };
+// Query heads of a unit: 8 when the group that shares a key-value head has no more, else 16.
+inline uint32_t attn_decode_heads(uint32_t group) { return group <= 8 ? 8 : 16; }
 // CTAs that the decode kernel of this head size and format runs with (0: unsupported).
-int attn_decode_grid(uint32_t dim, int cache_type, int num_sms);
+int attn_decode_grid(uint32_t dim, uint32_t group, int cache_type, int num_sms);
 cudaError_t launch_attn_decode(const AttnDecodeParams &p, int grid, cudaStream_t st);
 
 struct PromptTile;   // q8_attn_prompt.cuh
