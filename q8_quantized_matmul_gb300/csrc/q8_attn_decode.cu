@@ -47,7 +47,7 @@ template <int D, int FMT, int NT> struct Dec {
     static constexpr int KB = ST * D * (Q8 ? 1 : 2), VB = ST * DV * (Q8 ? 1 : 2);
     static constexpr int KSB = Q8 ? ST * (D / 32) * 2 : 0, VSB = Q8 ? ST * (DV / 32) * 2 : 0;
     static constexpr int STAGE = KB + VB + KSB + VSB;
-    static constexpr int NST = D <= 128 ? 3 : 2;         // stages of a warp
+    static constexpr int NST = Q8 && D <= 128 ? 3 : 2;         // stages of a warp
     static constexpr bool QREG = D <= 128;               // q fragments in registers (else shared memory)
     static constexpr int QS = QREG ? 0 : D / 16 * NT * 256;   // q fragments, [k step][head tile][lane] of 8 bytes
     static constexpr int MERGE = HR * DV * 4;            // a warp's O at the end of a share
@@ -442,6 +442,13 @@ __global__ void __launch_bounds__(128, Dec<D, FMT, NT>::CTAS) k_attn_decode(cons
                         const int at = p0 + 8 * i + g;
                         seen |= (uint32_t)(at >= q.lo && at < q.hi && !((dead >> (i / 2)) & 1)) << i;
                     }
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (!(seen & (1u << (2 * i + (e >> 1))))) z[i][t][e] = -INFINITY;
                 }
                 float mx[NT][2];
                 bool grow = false;
@@ -452,16 +459,13 @@ __global__ void __launch_bounds__(128, Dec<D, FMT, NT>::CTAS) k_attn_decode(cons
                     for (int i = 0; i < MT; ++i)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            float v = z[i][t][e] * p.scale_log2;
-                            if (!(seen & (1u << (2 * i + (e >> 1))))) v = -INFINITY;
-                            z[i][t][e] = v;
-                            mx[t][e & 1] = fmaxf(mx[t][e & 1], v);
+                            mx[t][e & 1] = fmaxf(mx[t][e & 1], z[i][t][e]);
                         }
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
 #pragma unroll
                         for (int x = 4; x < 32; x <<= 1) mx[t][h] = fmaxf(mx[t][h], __shfl_xor_sync(0xffffffffu, mx[t][h], x));
-                        mx[t][h] += e_max;
+                        mx[t][h] = mx[t][h] * p.scale_log2 + e_max;
                         grow |= mx[t][h] > m[t][h];
                     }
                 }
@@ -486,11 +490,11 @@ __global__ void __launch_bounds__(128, Dec<D, FMT, NT>::CTAS) k_attn_decode(cons
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const float s = m[t][h] == -INFINITY ? 0.0f : m[t][h] - C::BIAS;
+                        const float s = m[t][h] == -INFINITY ? 0.0f : C::BIAS - m[t][h];
 #pragma unroll
                         for (int i = 0; i < MT; ++i) {
-                            z[i][t][h] = ex2(z[i][t][h] - s);
-                            z[i][t][2 + h] = ex2(z[i][t][2 + h] - s);
+                            z[i][t][h] = ex2(__fmaf_rn(z[i][t][h], p.scale_log2, s));
+                            z[i][t][2 + h] = ex2(__fmaf_rn(z[i][t][2 + h], p.scale_log2, s));
                             l[t][h] += z[i][t][h] + z[i][t][2 + h];
                         }
                     }
