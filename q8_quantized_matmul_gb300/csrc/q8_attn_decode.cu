@@ -614,32 +614,67 @@ __global__ void __launch_bounds__(128, Dec<D, FMT, NT>::CTAS) k_attn_decode(cons
                 return k;
             };
             const int64_t c0 = cta_of(u0), c1 = cta_of(u1 - 1);
-            __threadfence();
-            __syncthreads();
             const uint64_t id = (uint64_t)s * units_per_seq + unit;
-            if (tid == 0) sh[0] = atomicAdd(p.counters + id, 1) == (int)(c1 - c0);
+            __syncthreads();
+            if (tid == 0) {
+                __threadfence();                                 // the whole CTA's piece before its arrival
+                sh[0] = atomicAdd(p.counters + id, 1) == (int)(c1 - c0);
+                __threadfence();
+            }
             __syncthreads();
             if (sh[0]) {                                         // the last piece: join them in order
-                __threadfence();
-                const bool c0_first = total * c0 / shares == u0;   // the unit opens that share
+                const int n_part = (int)(c1 - c0) + 1;
+                // the first piece is its CTA's second share when that CTA began with another unit
+                const uint64_t first_slot = 2 * (uint64_t)c0 + (total * c0 / shares == u0 ? 0 : 1);
+                auto slot_of = [&](int k) { return k == 0 ? first_slot : 2 * (uint64_t)(c0 + k); };
+                // maximum and sum of each row (and half of its dims), a warp a row
+                for (int pr = warp; pr < rows * C::NDH; pr += C::W) {
+                    const int row = pr / C::NDH, h = pr % C::NDH;
+                    float mt = -INFINITY, lt = 0.0f;
+                    for (int k = lane; k < n_part; k += 32) mt = fmaxf(mt, __ldcg(&p.part_ml[(slot_of(k) * 16 + row) * 2 + h].x));
+#pragma unroll
+                    for (int x = 1; x < 32; x <<= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, x));
+                    for (int k = lane; k < n_part; k += 32) {
+                        const float2 v = __ldcg(&p.part_ml[(slot_of(k) * 16 + row) * 2 + h]);
+                        lt += v.x == -INFINITY ? 0.0f : v.y * ex2(v.x - mt);
+                    }
+#pragma unroll
+                    for (int x = 1; x < 32; x <<= 1) lt += __shfl_xor_sync(0xffffffffu, lt, x);
+                    if (lane == 0) ml[pr] = make_float2(mt, lt);
+                }
+                __syncthreads();
                 for (int i = tid; i < (items + 31) / 32 * 32; i += 128) {
                     const bool act = i < items;
                     const int row = act ? i / (D / 8) : 0, d0 = i % (D / 8) * 8, h = d0 / C::DV;
-                    float mt = -INFINITY, lt = 0.0f, y[8] = {};
-                    for (int64_t k = c0; k <= c1; ++k) {
-                        const uint64_t sl = 2 * (uint64_t)k + (k == c0 && !c0_first ? 1 : 0);
-                        const float2 x = __ldcg(&p.part_ml[(sl * 16 + row) * 2 + h]);
-                        const float4 *src = reinterpret_cast<const float4 *>(p.part + (sl * 16 + row) * D + d0);
-                        const float4 va = __ldcg(src), vb = __ldcg(src + 1);
-                        const float mn = fmaxf(mt, x.x);
-                        const float fo = mt == -INFINITY ? 0.0f : ex2(mt - mn), fn = x.x == -INFINITY ? 0.0f : ex2(x.x - mn);
-                        mt = mn;
-                        lt = lt * fo + x.y * fn;
-                        const float v[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};
+                    const float2 t = ml[row * C::NDH + h];
+                    float y[8] = {};
+                    for (int k0 = 0; k0 < n_part; k0 += 8) {     // eight pieces' loads in flight
+                        float f[8];
+                        float4 va[8], vb[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) y[e] = y[e] * fo + v[e] * fn;
+                        for (int u = 0; u < 8; ++u) {
+                            const bool ok = k0 + u < n_part;
+                            const uint64_t sl = slot_of(ok ? k0 + u : k0);
+                            const float mk = __ldcg(&p.part_ml[(sl * 16 + row) * 2 + h].x);
+                            const float4 *src = reinterpret_cast<const float4 *>(p.part + (sl * 16 + row) * D + d0);
+                            va[u] = __ldcg(src);
+                            vb[u] = __ldcg(src + 1);
+                            f[u] = ok && mk != -INFINITY ? ex2(mk - t.x) : 0.0f;
+                        }
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) {
+                            if (f[u] == 0.0f) continue;          // nothing seen there (or beyond the last piece)
+                            y[0] += va[u].x * f[u];
+                            y[1] += va[u].y * f[u];
+                            y[2] += va[u].z * f[u];
+                            y[3] += va[u].w * f[u];
+                            y[4] += vb[u].x * f[u];
+                            y[5] += vb[u].y * f[u];
+                            y[6] += vb[u].z * f[u];
+                            y[7] += vb[u].w * f[u];
+                        }
                     }
-                    finish8(p, s, head0 + row, d0, mt - C::BIAS, lt, y, act);
+                    finish8(p, s, head0 + row, d0, t.x - C::BIAS, t.y, y, act);
                 }
                 if (tid == 0) p.counters[id] = 0;
             }
