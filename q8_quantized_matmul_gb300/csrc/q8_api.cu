@@ -1277,6 +1277,18 @@ int q8_attn_decode(void *out, int out_type, float *lse, const void *q, uint64_t 
     p.window = window;
     p.sinks = sinks;
     p.err = s->err;
+    if (q8::attn_decode_on_tc(c->head_dim, p.group, c->type != Q8_TYPE_Q8_0)) {
+        p.mtiles = (p.group + 63) / 64;
+        const size_t slots = 2 * (size_t)s->num_sms, units = (size_t)n_seq * c->n_kv_heads * p.mtiles;
+        const size_t part = align256(slots * 64 * c->head_dim * sizeof(float)), ml = align256(slots * 64 * sizeof(float2));
+        if ((rc = reserve_scratch(s, part + ml + align256(units * sizeof(int4))))) return rc;
+        Carver cv(s->scratch);
+        p.part = cv.take<float>(part);
+        p.part_ml = cv.take<float2>(ml);
+        p.units = cv.take<int4>(units * sizeof(int4));
+        take_expiry(p.wait_ns, p.withhold);
+        return status_of(q8::launch_attn_decode_tc(p, s->num_sms, st));
+    }
     const int grid = q8::attn_decode_grid(c->head_dim, p.group, c->type, s->num_sms);
     if ((rc = reserve_counters(s, (size_t)n_seq * c->n_kv_heads * p.mtiles, st))) return rc;
     const size_t part = align256((size_t)grid * 2 * 16 * c->head_dim * sizeof(float));

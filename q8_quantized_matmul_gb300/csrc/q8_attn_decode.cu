@@ -29,6 +29,7 @@
 #include <algorithm>
 
 #include "q8_attn.cuh"
+#include "q8_attn_decode.cuh"
 #include "q8_kv.h"
 
 namespace q8 {
@@ -109,40 +110,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     return y;
 }
 
-struct Seq {
-    int lo, hi;          // visible positions [lo, hi)
-    int start;           // lo rounded down to 16: the first staged position
-    int tiles;
-};
-
-template <class C> __device__ __forceinline__ Seq seq_of(const AttnDecodeParams &p, uint32_t s, bool raise) {
-    const int64_t most = (int64_t)p.max_pages << p.c.page_shift;
-    int64_t n = p.lens[s];
-    if (n < 0 || n > most) {
-        if (raise) raise_error(p.err, DEV_ERANGE);
-        n = n < 0 ? 0 : most;
-    }
-    Seq q;
-    q.hi = (int)n;
-    q.lo = p.window && n > p.window ? (int)(n - p.window) : 0;
-    q.start = q.lo & ~15;
-    q.tiles = (q.hi - q.start + C::TT - 1) / C::TT;
-    return q;
-}
-
-// Final values of one output chunk (8 dims of a head).
-__device__ __forceinline__ void finish8(const AttnDecodeParams &p, uint32_t s, uint32_t head, int d0, float m, float l,
-                                        float (&o)[8], bool active) {
-    float lse;
-    const float f = softmax_finish(m, l, p.sinks != nullptr, p.sinks && active ? p.sinks[head] * 1.4426950408889634f : 0.0f,
-                                   lse);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = f == 0.0f ? 0.0f : o[e] * f;
-    const uint64_t row = (uint64_t)s * p.n_heads + head;
-    store_out8(p.out, p.out_type, row * p.c.dim + d0, o, active);
-    if (active && p.lse && d0 == 0) p.lse[row] = lse;
-}
-
 template <int D, int FMT, int NT>
 __global__ void __launch_bounds__(128, Dec<D, FMT, NT>::CTAS) k_attn_decode(const AttnDecodeParams p) {
     using C = Dec<D, FMT, NT>;
@@ -167,7 +134,7 @@ __global__ void __launch_bounds__(128, Dec<D, FMT, NT>::CTAS) k_attn_decode(cons
         int64_t *scan = reinterpret_cast<int64_t *>(smem);       // before the ring is used
         const uint32_t per = (p.n_seq + 127) / 128, a = min(p.n_seq, tid * per), b = min(p.n_seq, a + per);
         int64_t mine = 0;
-        for (uint32_t i = a; i < b; ++i) mine += seq_of<C>(p, i, blockIdx.x == 0).tiles;
+        for (uint32_t i = a; i < b; ++i) mine += seq_of(C::TT, 16, p, i, blockIdx.x == 0).tiles;
         mine *= units_per_seq;
         int64_t sum = mine;
 #pragma unroll
@@ -194,7 +161,7 @@ __global__ void __launch_bounds__(128, Dec<D, FMT, NT>::CTAS) k_attn_decode(cons
         if (t0 < t1 && before <= t0 && t0 < before + mine) {
             uint32_t i = a;
             for (;; ++i) {
-                const int64_t n = (int64_t)seq_of<C>(p, i, false).tiles * units_per_seq;
+                const int64_t n = (int64_t)seq_of(C::TT, 16, p, i, false).tiles * units_per_seq;
                 if (t0 < before + n) break;
                 before += n;
             }
@@ -209,7 +176,7 @@ __global__ void __launch_bounds__(128, Dec<D, FMT, NT>::CTAS) k_attn_decode(cons
 
     // ---- sequences with nothing visible: zeros
     for (uint32_t e = blockIdx.x; e < p.n_seq; e += gridDim.x) {
-        if (seq_of<C>(p, e, false).tiles) continue;
+        if (seq_of(C::TT, 16, p, e, false).tiles) continue;
         for (uint32_t i = tid; i < (p.n_heads * (D / 8) + 31) / 32 * 32; i += 128) {
             float o[8] = {};
             const bool act = i < p.n_heads * (D / 8);
@@ -219,10 +186,10 @@ __global__ void __launch_bounds__(128, Dec<D, FMT, NT>::CTAS) k_attn_decode(cons
 
     bool first = true;
     for (int64_t tile = t0; tile < t1; first = false) {
-        Seq q = seq_of<C>(p, s, false);
+        Seq q = seq_of(C::TT, 16, p, s, false);
         while (tile >= s_base + (int64_t)q.tiles * units_per_seq) {
             s_base += (int64_t)q.tiles * units_per_seq;
-            q = seq_of<C>(p, ++s, false);
+            q = seq_of(C::TT, 16, p, ++s, false);
         }
         const uint32_t unit = (uint32_t)((tile - s_base) / q.tiles);
         const int64_t u0 = s_base + (int64_t)unit * q.tiles;     // the unit's tiles on the line

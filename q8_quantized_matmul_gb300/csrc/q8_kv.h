@@ -78,7 +78,17 @@ struct AttnDecodeParams {
     float2 *part_ml;                      // their maxima and sums, [2 * grid][16]
     int *counters;                        // one per unit, zero between calls
     int *err;
+    // tcgen05 kernel: per unit the slot of its first piece, that piece's CTA and the number of pieces;
+    // part and part_ml then hold 64 rows a slot
+    int4 *units;
+    uint64_t wait_ns;                     // failure-detection test hook, see GemvParams
+    int withhold;
 };
+// Whether a call runs on the tcgen05 kernel: 16-bit caches, large heads, more query heads on a key-value head
+// than one unit of the mma.sync kernel takes (64 heads of 512 on one, 16 sequences of up to 4100 positions:
+// AAA us against BBB us).
+inline bool attn_decode_on_tc(uint32_t dim, uint32_t group, bool cache16) { return cache16 && dim >= 256 && group > 16; }
+cudaError_t launch_attn_decode_tc(const AttnDecodeParams &p, int grid, cudaStream_t st);
 // Query heads of a unit: 8 when the group that shares a key-value head has no more, else 16.
 inline uint32_t attn_decode_heads(uint32_t group) { return group <= 8 ? 8 : 16; }
 // CTAs that the decode kernel of this head size and format runs with (0: unsupported).

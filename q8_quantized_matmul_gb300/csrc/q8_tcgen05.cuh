@@ -124,10 +124,11 @@ __device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t saddr, uint32_t lead)
     return (sw128_desc(saddr) & ~((uint64_t)0x3fff << 16)) | (uint64_t)(lead >> 4) << 16;
 }
 
-// Instruction descriptor: fp32 accumulate, fp16 (or bf16) A and B, A K-major, B K-major (or N contiguous), N x M.
-__host__ __device__ constexpr uint32_t tc_idesc(int m, int n, bool bf16 = false, bool b_mn = false) {
-    return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((b_mn ? 1u : 0u) << 16) |
-           ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+// Instruction descriptor: fp32 accumulate, fp16 (or bf16) A and B, K-major or with N (b_mn), M (a_mn)
+// contiguous, N x M.
+__host__ __device__ constexpr uint32_t tc_idesc(int m, int n, bool bf16 = false, bool b_mn = false, bool a_mn = false) {
+    return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((a_mn ? 1u : 0u) << 15) |
+           ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
 }  // namespace q8

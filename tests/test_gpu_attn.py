@@ -230,6 +230,77 @@ def test_decode_in_a_graph_and_on_a_stream(q8):
         assert torch.equal(b, ref)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("dim", [256, 512])
+@pytest.mark.parametrize("heads,kv", [(64, 1), (17, 1), (40, 2), (130, 2)])
+def test_decode_many_heads_on_one(q8, kind, dim, heads, kv):
+    """More than 16 query heads on a key-value head: the tcgen05 kernel, with full, part and several head tiles."""
+    check_decode(q8, kind, [0, 1, 127, 128, 129, 300], heads=heads, kv=kv, dim=dim, page=32, seed=heads, sinks=heads != 64)
+
+
+@pytest.mark.parametrize("page", [16, 64, 128, 256])
+@pytest.mark.parametrize("window", [0, 1, 50, 130])
+def test_decode_many_heads_pages_and_windows(q8, page, window):
+    check_decode(q8, "f16", [700, 131, 0, 16], heads=20, kv=1, dim=512, page=page, window=window, seed=page + window, strided=True,
+                 layers=2, layer=1)
+
+
+@pytest.mark.parametrize("out", ["f32", "q8"])
+def test_decode_many_heads_output_types(q8, out):
+    check_decode(q8, "bf16", [70, 0, 300], heads=33, kv=1, dim=512, page=32, out=out)
+
+
+def test_decode_many_heads_long(q8):
+    """Units over many CTAs, and more sequences than CTAs."""
+    check_decode(q8, "bf16", [6000, 5, 900], heads=18, kv=1, dim=256, page=64)
+    check_decode(q8, "f16", [int(x) for x in np.random.default_rng(6).integers(0, 30, 170)], heads=17, kv=1, dim=256, page=16)
+
+
+def test_decode_many_heads_growing_scores(q8):
+    """Scores that rise along the sequence: the running maxima move in many steps."""
+    pool = Pool(q8, "f16", [900], 1, 512, 32, 8)
+    q = torch.randn(1, 24, 512, device=DEV).half()
+    k = pool.cache.k.view(torch.float16).view(1, -1, 1, 32, 512)
+    ramp = torch.linspace(-1.0, 1.0, 900)
+    row = (q[0, 0].float().cpu() * 0.06)
+    for j in range(900):
+        k[0, int(pool.table[0, j // 32]), 0, j % 32] = (row * ramp[j] * 8).half().to(DEV)
+    keys = f64(k[0, pool.table[0, :29].long()])[:, 0].reshape(-1, 512)[:900]
+    got = f64(q8.attn_decode(q, pool.cache, 0, pool.table, pool.lens_t))
+    assert q8.q8_last_error() == 0
+    for h in range(24):
+        r, _, b, _ = attend(f64(q[0, h])[None], keys, pool.rows[0][1][:, 0], np.ones((1, 900), bool), 512 ** -0.5, None, "f16", "f16")
+        check(got[0, h][None], r, b, f"head {h}")
+
+
+def test_decode_many_heads_bad_pages(q8):
+    pool = Pool(q8, "bf16", [200, 64], 1, 512, 32, 3)
+    q = torch.randn(2, 24, 512, device=DEV).bfloat16()
+    good = q8.attn_decode(q, pool.cache, 0, pool.table, pool.lens_t)
+    for bad in (-1, pool.cache.struct.n_pages, 1 << 30):
+        t = pool.table.clone()
+        t[0, 6] = bad                                                # positions 192 .. 199
+        o = q8.attn_decode(q, pool.cache, 0, t, pool.lens_t)
+        assert q8.q8_last_error() == q8.Q8_ERANGE
+        ref = q8.attn_decode(q, pool.cache, 0, pool.table, torch.tensor([192, 64], dtype=torch.int32, device=DEV))
+        assert torch.equal(o[0], ref[0]) and torch.equal(o[1], good[1])
+    o = q8.attn_decode(q, pool.cache, 0, torch.full_like(pool.table, -1), pool.lens_t)
+    assert torch.all(o == 0) and q8.q8_last_error() == q8.Q8_ERANGE
+
+
+def test_decode_many_heads_wait_expires(q8):
+    """The tcgen05 decode kernel with its producer withholding every copy reports Q8_ETIMEOUT and returns."""
+    pool = Pool(q8, "bf16", [200, 64], 1, 512, 32, 3)
+    q = torch.randn(2, 24, 512, device=DEV).bfloat16()
+    ref = q8.attn_decode(q, pool.cache, 0, pool.table, pool.lens_t)
+    assert q8.q8_last_error() == 0
+    q8.q8_debug_expire_waits(1, 1_000_000)
+    q8.attn_decode(q, pool.cache, 0, pool.table, pool.lens_t)
+    assert q8.q8_last_error() == q8.Q8_ETIMEOUT
+    assert torch.equal(q8.attn_decode(q, pool.cache, 0, pool.table, pool.lens_t), ref)
+    assert q8.q8_last_error() == 0
+
+
 # ------------------------------------------------------------------ whole prompts
 def check_prompt(q8, kind, qlens, klens, heads, kv, dim, window=0, sinks=False, seed=0, out=None, poison=True):
     rng = np.random.default_rng(seed)
