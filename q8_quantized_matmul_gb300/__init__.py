@@ -12,7 +12,6 @@ C status code (0 = Q8_OK).  ``Q8Error`` is raised by the ``*_checked`` helpers.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -463,13 +462,28 @@ def kq_moe_matmul(W_experts, fmt: int, n_expert: int, expert_stride: int, ids, x
 
 
 # ------------------------------------------------------------------ paged key-value cache and attention
-# These calls take microseconds on the GPU, so the helpers do each look-up once and call the library directly.
-@functools.lru_cache(maxsize=None)
-def _page_bytes(type: int, page_tokens: int, n_kv_heads: int, head_dim: int) -> int:
-    n = q8_kv_page_bytes(type, page_tokens, n_kv_heads, head_dim)
-    if n == 0:
-        raise Q8Error(Q8_EINVAL, "q8_kv_page_bytes")
-    return n
+# These calls take microseconds on the GPU, so their marshalling is compiled: csrc/q8_torch.cpp.
+EXT_PATH = os.path.join(_PKG, "_q8torch.so")
+_ext_mod = None
+
+
+def _load_ext():
+    global _ext_mod
+    if not os.path.exists(EXT_PATH):
+        raise ImportError(f"{EXT_PATH} is missing: build it with `python -m q8_quantized_matmul_gb300.build`")
+    import importlib.machinery
+    import importlib.util
+
+    import torch  # noqa: F401  (the module uses torch's libraries)
+    loader = importlib.machinery.ExtensionFileLoader("_q8torch", EXT_PATH)
+    mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_q8torch", loader))
+    loader.exec_module(mod)
+    L = _get()
+    mod.init(Q8Error, *(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in (
+        "q8_kv_page_bytes", "q8_kv_append", "q8_attn_decode", "q8_attn_prompt", "q8_kv_reserve", "q8_kv_fork",
+        "q8_kv_free", "q8_kv_compact", "q8_kv_copy")))
+    _ext_mod = mod
+    return mod
 
 
 class KVCache:
@@ -477,87 +491,28 @@ class KVCache:
     include/q8.h).  Inside a page the memory is contiguous; layers and pages may be strided, so k and v may be
     slices of one tensor."""
 
+    __slots__ = ("k", "v", "type", "page_tokens", "n_kv_heads", "head_dim", "struct", "address")
+
     def __init__(self, k, v, type: int, page_tokens: int, n_kv_heads: int, head_dim: int):
-        page_bytes = _page_bytes(type, page_tokens, n_kv_heads, head_dim)
-        shape, strides, size = k.shape, k.stride(), k.element_size()
-        if shape != v.shape or k.dtype != v.dtype or strides != v.stride():
-            raise ValueError("k and v must have the same shape, type and strides")
-        want = 1
-        for i in range(len(shape) - 1, 1, -1):
-            if strides[i] != want and shape[i] != 1:
-                raise ValueError("a page must be contiguous")
-            want *= shape[i]
-        if want * size != page_bytes:
-            raise ValueError(f"a page has {want * size} bytes, its layout {page_bytes}")
+        self.struct = struct = KVCacheStruct()
+        self.address = address = ctypes.addressof(struct)
+        (_ext_mod or _load_ext()).fill_cache(address, k, v, type, page_tokens, n_kv_heads, head_dim)
         self.k, self.v, self.type = k, v, type
         self.page_tokens, self.n_kv_heads, self.head_dim = page_tokens, n_kv_heads, head_dim
-        n_layers, self.n_pages = shape[0], shape[1]
-        page_stride = strides[1] * size if shape[1] > 1 else page_bytes
-        layer_stride = strides[0] * size if n_layers > 1 else self.n_pages * page_stride
-        self.struct = KVCacheStruct(k.data_ptr(), v.data_ptr(), layer_stride, page_stride, n_layers, self.n_pages,
-                                    page_tokens, n_kv_heads, head_dim, type)
+
+    @property
+    def n_pages(self) -> int:
+        return self.struct.n_pages
 
     @classmethod
     def empty(cls, type: int, n_layers: int, n_pages: int, page_tokens: int, n_kv_heads: int, head_dim: int,
               device="cuda"):
-        page_bytes = _page_bytes(type, page_tokens, n_kv_heads, head_dim)
-        torch = _t()
+        import torch
+        page_bytes = q8_kv_page_bytes(type, page_tokens, n_kv_heads, head_dim)
+        if page_bytes == 0:
+            raise Q8Error(Q8_EINVAL, "q8_kv_page_bytes")
         k, v = (torch.zeros((n_layers, n_pages, page_bytes), dtype=torch.uint8, device=device) for _ in range(2))
         return cls(k, v, type, page_tokens, n_kv_heads, head_dim)
-
-
-def _type_of(dtype) -> int:
-    torch = _t()
-    if dtype is torch.bfloat16:
-        return Q8_TYPE_BF16
-    if dtype is torch.float16:
-        return Q8_TYPE_F16
-    raise TypeError(f"{dtype}: float16 or bfloat16 expected")
-
-
-def _rows(t, name: str) -> int:
-    """Row stride of a [rows, heads, dim] GPU tensor whose heads lie back to back."""
-    (n, heads, dim), (r, h, d) = t.shape, t.stride()
-    if d != 1 or (h != dim and heads != 1) or not t.is_cuda:
-        raise ValueError(f"{name}: a GPU tensor whose heads lie back to back expected")
-    return r if n > 1 else heads * dim
-
-
-def _i32(t, name: str) -> int:
-    """Pointer of a contiguous int32 GPU tensor (0 for None)."""
-    if t is None:
-        return 0
-    if t.dtype is not _t().int32 or not t.is_cuda or not t.is_contiguous():
-        raise TypeError(f"{name}: contiguous int32 on the GPU expected")
-    return t.data_ptr()
-
-
-def _table(table):
-    """Pointer, row stride, columns and rows of a table."""
-    (rows, width), (stride, one) = table.shape, table.stride()
-    if table.dtype is not _t().int32 or not table.is_cuda or (one != 1 and width != 1):
-        raise TypeError("table: int32 [rows, max_pages] on the GPU with contiguous rows expected")
-    return table.data_ptr(), stride if rows > 1 else width, width, rows
-
-
-def _out(q, rows: int, heads: int, dim: int, kind: int, out_type):
-    """Output of an attention call and its type: [rows, heads, dim], or [rows, heads, dim/32*34] Q8_0 blocks."""
-    if out_type is None or out_type == kind:
-        return _t().empty((rows, heads, dim), dtype=q.dtype, device=q.device), kind
-    torch = _t()
-    if out_type == Q8_TYPE_Q8_0:
-        return torch.empty((rows, heads, dim // QK * QB), dtype=torch.uint8, device=q.device), out_type
-    if out_type == Q8_TYPE_F32:
-        return torch.empty((rows, heads, dim), dtype=torch.float32, device=q.device), out_type
-    raise Q8Error(Q8_EINVAL, "out_type")
-
-
-def _sinks(sinks, heads: int) -> int:
-    if sinks is None:
-        return 0
-    if sinks.dtype is not _t().float32 or sinks.numel() != heads or not sinks.is_contiguous() or not sinks.is_cuda:
-        raise TypeError("sinks: contiguous float32 [heads] on the GPU expected")
-    return sinks.data_ptr()
 
 
 def kv_append(cache, layer: int, q, k, v, positions, seq_of, table, cos_sin=None, rope: int = 0, dtype=None,
@@ -566,149 +521,52 @@ def kv_append(cache, layer: int, q, k, v, positions, seq_of, table, cos_sin=None
     back, rows strided), positions and seq_of int32 [n], table int32 [rows, max_pages]; cos_sin float32
     [n_pos, rot_dim], rope 1 (halves) or 2 (adjacent pairs); cache None: no store.
     Returns q in `dtype` (the cache's 16-bit type, else bfloat16), or (q, k, v) with want_kv."""
-    torch = _t()
-    f32 = torch.float32
-    n, kv_heads, dim = k.shape
-    if k.dtype is not f32 or v.dtype is not f32:
-        raise TypeError("k and v: float32 expected")
-    if v.shape != k.shape or positions.shape[0] != n:
-        raise ValueError("k, v and positions disagree")
     if dtype is None:
-        dtype = torch.float16 if cache is not None and cache.type == Q8_TYPE_F16 else torch.bfloat16
-    kind = _type_of(dtype)
-    q_out, qp, qs, qo, heads = None, 0, 0, 0, 0
-    if q is not None:
-        heads = q.shape[1]
-        if q.dtype is not f32:
-            raise TypeError("q: float32 expected")
-        if q.shape[0] != n or q.shape[2] != dim:
-            raise ValueError("q and k disagree")
-        q_out = torch.empty((n, heads, dim), dtype=dtype, device=q.device)
-        qp, qs, qo = q.data_ptr(), _rows(q, "q"), q_out.data_ptr()
-    k_out = v_out = None
-    ko = vo = 0
-    if want_kv:
-        k_out, v_out = (torch.empty((n, kv_heads, dim), dtype=dtype, device=k.device) for _ in range(2))
-        ko, vo = k_out.data_ptr(), v_out.data_ptr()
-    struct, seq, tab = None, 0, (0, 0, 0, 0)
-    if cache is not None:
-        if seq_of is None or table is None or seq_of.shape[0] != n:
-            raise ValueError("a cache write needs seq_of [n] and table")
-        struct, seq, tab = cache.struct, _i32(seq_of, "seq_of"), _table(table)
-    cs, n_pos, rot = 0, 0, 0
-    if rope:
-        if cos_sin is None or cos_sin.dtype is not f32 or not cos_sin.is_contiguous() or not cos_sin.is_cuda:
-            raise ValueError("rope needs a contiguous float32 cos_sin on the GPU")
-        cs, (n_pos, rot) = cos_sin.data_ptr(), cos_sin.shape
-    rc = _get().q8_kv_append(qo, ko, vo, kind, struct, layer, qp, qs, k.data_ptr(), _rows(k, "k"), v.data_ptr(),
-                             _rows(v, "v"), heads, kv_heads, dim, _i32(positions, "positions"), seq, *tab, cs, n_pos,
-                             rot, rope, n, _current_stream())
-    if rc:
-        raise Q8Error(rc, "q8_kv_append")
-    return (q_out, k_out, v_out) if want_kv else q_out
+        kind = Q8_TYPE_F16 if cache is not None and cache.type == Q8_TYPE_F16 else Q8_TYPE_BF16
+    else:
+        torch = _t()
+        kind = Q8_TYPE_BF16 if dtype is torch.bfloat16 else Q8_TYPE_F16
+        if kind == Q8_TYPE_F16 and dtype is not torch.float16:
+            raise TypeError(f"{dtype}: float16 or bfloat16 expected")
+    return (_ext_mod or _load_ext()).kv_append(None if cache is None else cache.address, layer, q, k, v, positions,
+                                               seq_of, table, cos_sin, rope, kind, want_kv)
 
 
 def attn_decode(q, cache, layer: int, table, seq_lens, scale=None, window: int = 0, sinks=None, out_type=None,
                 want_lse: bool = False):
     """One new token per sequence: q [n_seq, heads, dim] 16 bit, table int32 [n_seq, max_pages], seq_lens int32
     [n_seq] -> [n_seq, heads, dim] (and lse float32 [n_seq, heads])."""
-    n, heads, dim = q.shape
-    if dim != cache.head_dim or table.shape[0] != n or seq_lens.shape[0] != n:
-        raise ValueError("q, cache, table and seq_lens disagree")
-    tab, stride, width, _ = _table(table)
-    kind = _type_of(q.dtype)
-    out, out_type = _out(q, n, heads, dim, kind, out_type)
-    lse = _t().empty((n, heads), dtype=_t().float32, device=q.device) if want_lse else None
-    rc = _get().q8_attn_decode(out.data_ptr(), out_type, lse.data_ptr() if want_lse else 0, q.data_ptr(), _rows(q, "q"),
-                               kind, cache.struct, layer, tab, stride, width, _i32(seq_lens, "seq_lens"), n, heads,
-                               dim ** -0.5 if scale is None else scale, window, _sinks(sinks, heads), _current_stream())
-    if rc:
-        raise Q8Error(rc, "q8_attn_decode")
-    return (out, lse) if want_lse else out
+    return (_ext_mod or _load_ext()).attn_decode(q, cache.address, layer, table, seq_lens, scale, window, sinks,
+                                                 out_type, want_lse)
 
 
 def attn_prompt(q, k, v, q_start, k_start=None, scale=None, window: int = 0, sinks=None, out_type=None,
                 want_lse: bool = False):
     """Packed prompts: q [n_q, heads, dim], k and v [n_k, kv_heads, dim] 16 bit (rows strided, heads back to
     back), q_start and k_start int32 [n_seq + 1] -> [n_q, heads, dim] (and lse float32 [n_q, heads])."""
-    n, heads, dim = q.shape
-    n_k, kv_heads, k_dim = k.shape
-    dtype = q.dtype
-    if k.shape != v.shape or k_dim != dim or k.dtype is not dtype or v.dtype is not dtype:
-        raise ValueError("q, k and v disagree")
-    n_start = q_start.shape[0]
-    if k_start is not None and k_start.shape[0] != n_start:
-        raise ValueError("q_start and k_start disagree")
-    kind = _type_of(dtype)
-    out, out_type = _out(q, n, heads, dim, kind, out_type)
-    lse = _t().empty((n, heads), dtype=_t().float32, device=q.device) if want_lse else None
-    rc = _get().q8_attn_prompt(out.data_ptr(), out_type, lse.data_ptr() if want_lse else 0, q.data_ptr(), k.data_ptr(),
-                               v.data_ptr(), kind, _rows(q, "q"), _rows(k, "k"), _rows(v, "v"),
-                               _i32(q_start, "q_start"), _i32(k_start, "k_start"), n_start - 1, n, n_k, heads, kv_heads,
-                               dim, dim ** -0.5 if scale is None else scale, window, _sinks(sinks, heads),
-                               _current_stream())
-    if rc:
-        raise Q8Error(rc, "q8_attn_prompt")
-    return (out, lse) if want_lse else out
-
-
-def _pages(cache, table, lens, refs):
-    """The arguments that the page calls share: pointer, row stride, columns and rows of the table, lens, refs."""
-    tab = _table(table)
-    if lens.shape[0] != tab[3] or refs.shape[0] != cache.n_pages:
-        raise ValueError("table, lens, refs and cache disagree")
-    return (*tab, _i32(lens, "lens"), _i32(refs, "refs"))
+    return (_ext_mod or _load_ext()).attn_prompt(q, k, v, q_start, k_start, scale, window, sinks, out_type, want_lse)
 
 
 def kv_reserve(cache, table, lens, refs, seqs, n_new) -> None:
     """Pages for n_new[i] more tokens of row seqs[i]; lens grow (all int32 on the device)."""
-    n = seqs.shape[0]
-    if n_new.shape[0] != n:
-        raise ValueError("seqs and n_new disagree")
-    rc = _get().q8_kv_reserve(cache.struct, *_pages(cache, table, lens, refs), _i32(seqs, "seqs"), _i32(n_new, "n_new"),
-                              n, _current_stream())
-    if rc:
-        raise Q8Error(rc, "q8_kv_reserve")
+    (_ext_mod or _load_ext()).kv_reserve(cache.address, table, lens, refs, seqs, n_new)
 
 
 def kv_fork(cache, table, lens, refs, src, dst) -> None:
     """Row dst[i] becomes a copy of row src[i]: whole pages shared, a part-filled last page copied."""
-    n = src.shape[0]
-    if dst.shape[0] != n:
-        raise ValueError("src and dst disagree")
-    rc = _get().q8_kv_fork(cache.struct, *_pages(cache, table, lens, refs), _i32(src, "src"), _i32(dst, "dst"), n,
-                           _current_stream())
-    if rc:
-        raise Q8Error(rc, "q8_kv_fork")
+    (_ext_mod or _load_ext()).kv_fork(cache.address, table, lens, refs, src, dst)
 
 
 def kv_free(cache, table, lens, refs, seqs) -> None:
     """Rows seqs give their pages back and become empty."""
-    rc = _get().q8_kv_free(cache.struct, *_pages(cache, table, lens, refs), _i32(seqs, "seqs"), seqs.shape[0],
-                           _current_stream())
-    if rc:
-        raise Q8Error(rc, "q8_kv_free")
+    (_ext_mod or _load_ext()).kv_free(cache.address, table, lens, refs, seqs)
 
 
 def kv_compact(cache, table, lens, refs):
     """Moves the pages in use to the front of the pool -> (new table, new refs, number of pages in use)."""
-    torch = _t()
-    tab, stride, width, rows, _, rp = _pages(cache, table, lens, refs)
-    new_table = torch.empty_strided((rows, width), (stride, 1), dtype=torch.int32, device=table.device)
-    new_refs = torch.empty_like(refs)
-    used = torch.empty((), dtype=torch.int32, device=table.device)
-    rc = _get().q8_kv_compact(cache.struct, new_table.data_ptr(), tab, stride, width, rows, new_refs.data_ptr(), rp,
-                              used.data_ptr(), _current_stream())
-    if rc:
-        raise Q8Error(rc, "q8_kv_compact")
-    return new_table, new_refs, used
+    return (_ext_mod or _load_ext()).kv_compact(cache.address, table, lens, refs)
 
 
 def kv_copy(cache, src, dst) -> None:
     """Page src[i] -> page dst[i] in all layers."""
-    n = src.shape[0]
-    if dst.shape[0] != n:
-        raise ValueError("src and dst disagree")
-    rc = _get().q8_kv_copy(cache.struct, _i32(src, "src"), _i32(dst, "dst"), n, _current_stream())
-    if rc:
-        raise Q8Error(rc, "q8_kv_copy")
+    (_ext_mod or _load_ext()).kv_copy(cache.address, src, dst)

@@ -4,6 +4,7 @@ Each .cu file under csrc/ is compiled in parallel with nvcc
 (``-gencode arch=compute_103a,code=sm_103a``, no fast-math, IEEE division and
 square root) and linked into ``q8_quantized_matmul_gb300/libq8.so`` with the
 CUDA runtime linked statically, so loading the library needs no GPU.
+``csrc/q8_torch.cpp`` becomes ``_q8torch.so`` beside it (g++, torch's headers).
 
     python -m q8_quantized_matmul_gb300.build
 """
@@ -21,6 +22,7 @@ CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libq8.so")
 HEADER = os.path.join(ROOT, "include", "q8.h")
+TORCH_EXT = os.path.join(PKG, "_q8torch.so")   # csrc/q8_torch.cpp: the tensor helpers' marshalling
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # No fast-math: '/' must be the IEEE division and subnormals must be kept
@@ -46,9 +48,9 @@ def _deps() -> list[str]:
 
 
 def stale() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(TORCH_EXT)):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(TORCH_EXT))
     return any(os.path.getmtime(f) > t for f in _deps())
 
 
@@ -61,6 +63,26 @@ def _compile(src: str, extra: list[str]) -> str:
     return obj
 
 
+def _compile_torch() -> None:
+    """The CPython module of the tensor helpers, against the installed torch's headers and libraries."""
+    import sysconfig
+
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    tmp = TORCH_EXT + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "g++", "-O1", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-isystem", inc, "-isystem",
+           os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", sysconfig.get_paths()["include"],
+           "-isystem", cuda, os.path.join(CSRC, "q8_torch.cpp"), "-o", tmp, f"-L{lib}", "-lc10", "-ltorch_cpu",
+           "-lc10_cuda", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for q8_torch.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, TORCH_EXT)
+
+
 def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = None) -> str:
     """Compile and link libq8.so if any source is newer than it (or force)."""
     if not force and not stale():
@@ -68,14 +90,17 @@ def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = N
     os.makedirs(OBJ, exist_ok=True)
     extra = ["-Xptxas", "-v"] if verbose_ptxas else []
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=jobs or min(len(srcs), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=jobs or min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        ext = ex.submit(_compile_torch)
         objs = list(ex.map(lambda s: _compile(s, extra), srcs))
+        ext.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    os.utime(TORCH_EXT)
     return LIB
 
 
