@@ -31,9 +31,10 @@ struct KvAppendParams {
     uint32_t n_pos, rot_dim;
     int rope;
     uint64_t n_tok;
+    uint32_t tokens_cta;                  // set by the launcher
     int *err;
 };
-cudaError_t launch_kv_append(const KvAppendParams &p, int num_sms, cudaStream_t st);
+cudaError_t launch_kv_append(KvAppendParams p, int num_sms, cudaStream_t st);
 
 struct KvPagesParams {
     KvPool c;
