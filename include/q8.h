@@ -396,7 +396,8 @@ int q8_attn_decode(void *out, int out_type, float *lse, const void *q, uint64_t 
  * only the last `window` of them; formula, sinks, lse, out_type and rounding as for
  * q8_attn_decode.  A query that sees no key gives zeros.
  *   q          in: 16 bit (type), row r's heads at q + r*q_stride elements.
- *   k, v       in: the same type, rows of n_kv_heads heads, k_stride / v_stride apart.
+ *   k, v       in: the same type, rows of n_kv_heads heads, k_stride / v_stride apart
+ *              (NULL when n_k is 0).
  *              Strides are multiples of 8, all pointers 16-byte aligned.
  *   q_start    in: int32 [n_seq + 1], k_start the same or NULL (= q_start); rising,
  *              from 0 to at most n_q / n_k.  Values outside are cut to the range and
@@ -565,8 +566,9 @@ void q8_debug_fail_next_alloc(int count);
  * kernels (the weight-streaming GEMV and the tcgen05 GEMM that q8_matmul,
  * q8_matmul_q and q8_matmul_host launch, and the TMA-fed kernel that
  * q8_rmsnorm_quantize runs for rows of at most 4096 values and at least 12
- * rows per SM, and the tcgen05 kernel that q8_attn_prompt runs for heads of 64
- * or 128 values) run with every wait limited to
+ * rows per SM, and the tcgen05 kernels of q8_attn_prompt and, for 16-bit
+ * caches with more than 16 query heads of 256 or 512 values on a key-value
+ * head, of q8_attn_decode) run with every wait limited to
  * limit_ns nanoseconds (0: the normal 2 s) and with their producer issuing no
  * copy at all, so the consumers wait on buffers that never fill.  Each such
  * kernel then raises Q8_ETIMEOUT for q8_last_error(), stops waiting, lets any

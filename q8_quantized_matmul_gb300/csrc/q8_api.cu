@@ -1311,7 +1311,7 @@ int q8_attn_prompt(void *out, int out_type, float *lse, const void *q, const voi
     if (!(scale > 0.0f) || scale > 1e30f || n_seq > MAX_SEQS) return Q8_EINVAL;
     if (n_q > ((uint64_t)1 << 28) || n_k > ((uint64_t)1 << 28)) return Q8_EINVAL;
     if (n_seq == 0 || n_q == 0) return Q8_OK;
-    if (!out || !q || !k || !v || !q_start) return Q8_EINVAL;
+    if (!out || !q || (n_k && (!k || !v)) || !q_start) return Q8_EINVAL;
     const uint64_t kv_row = (uint64_t)n_kv_heads * head_dim, most = (uint64_t)1 << 32;
     if (q_stride < (uint64_t)n_heads * head_dim || k_stride < kv_row || v_stride < kv_row || q_stride > most ||
         k_stride > most || v_stride > most)
@@ -1347,11 +1347,10 @@ int q8_attn_prompt(void *out, int out_type, float *lse, const void *q, const voi
     p.lse = lse;
     p.err = s->err;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (!q8::attn_prompt_on_tc(head_dim, n_k)) return status_of(q8::launch_attn_prompt_mma(p, st));
     const size_t list = q8::attn_prompt_list_bytes(p, s->num_sms);
     if ((rc = reserve_scratch(s, list))) return rc;
     take_expiry(p.wait_ns, p.withhold);
-    return status_of(q8::launch_attn_prompt_tc(p, list ? s->scratch : nullptr, s->num_sms, st));
+    return status_of(q8::launch_attn_prompt(p, list ? s->scratch : nullptr, s->num_sms, st));
 }
 
 // Arguments that the page calls share; fills p but for its scratch.

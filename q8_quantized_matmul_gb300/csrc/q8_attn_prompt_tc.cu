@@ -26,9 +26,8 @@
 //
 // Every wait is bounded; after one expires nothing more is issued and copies in flight are drained.
 #include "q8_attn.cuh"
-#include "q8_attn_prompt.cuh"
+#include "q8_attn_prompt_tc.cuh"
 #include "q8_kv.h"
-#include "q8_tcgen05.cuh"
 
 namespace q8 {
 
@@ -58,7 +57,7 @@ __device__ __forceinline__ int tile_cost(const PromptTile &w, uint32_t window) {
     return last < 0 ? 0 : last / 128 + 1 - w.first(0, window) / 128;
 }
 
-// One CTA: all tiles of 256 query rows, the ones with the most key tiles first (counting sort; the order
+// One CTA: all tiles of list_rows query rows, the ones with the most key tiles first (counting sort; the order
 // among equals does not matter to any result).
 __global__ void __launch_bounds__(LIST_THREADS) k_attn_prompt_list(const AttnPromptParams p) {
     __shared__ int bin[LIST_BINS];
@@ -80,9 +79,9 @@ __global__ void __launch_bounds__(LIST_THREADS) k_attn_prompt_list(const AttnPro
             w.k0 = ka;
             w.lk = max(ke - ka, 0);
             w.shift = w.lk - (qe - qa);
-            for (int64_t r = lane * 256; r < qe - qa; r += 32 * 256) {
+            for (int64_t r = (int64_t)lane * p.list_rows; r < qe - qa; r += 32 * (int64_t)p.list_rows) {
                 w.row0 = (int)r;
-                w.rows = min(256, qe - qa - w.row0);
+                w.rows = min(p.list_rows, qe - qa - w.row0);
                 const int c = tile_cost(w, p.window) >> p.list_shift;
                 f(w, LIST_BINS - 1 - min(c, LIST_BINS - 1));   // longest in the first bin
             }
@@ -109,33 +108,6 @@ __global__ void __launch_bounds__(LIST_THREADS) k_attn_prompt_list(const AttnPro
         const int at = atomicAdd(&bin[b], 1);
         if (at < (int)p.list_cap) list[at] = w;   // starts that do not rise may give more tiles than rows
     });
-}
-
-// 32 fp32 output values of one thread's row, columns d0 ..
-__device__ __forceinline__ void store_row32(const AttnPromptParams &p, uint64_t row, int d0, const float *y) {
-    const uint64_t i0 = row * p.dim + d0;
-    if (p.out_type == Q8_TYPE_Q8_0) {
-        float amax = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) amax = fmaxf(amax, fabsf(y[i]));
-        const float d = __fdiv_rn(amax, 127.0f);
-        uint16_t *dst = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(p.out) + i0 / QK * QB);
-        dst[0] = d != 0.0f ? __half_as_ushort(__float2half_rn(d)) : 0;
-#pragma unroll 4
-        for (int i = 0; i < 16; ++i) {
-            const int a = d != 0.0f ? (int)roundf(__fdiv_rn(y[2 * i], d)) : 0;
-            const int b = d != 0.0f ? (int)roundf(__fdiv_rn(y[2 * i + 1], d)) : 0;
-            dst[1 + i] = (uint16_t)((a & 0xff) | (b & 0xff) << 8);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float x[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = y[8 * i + e];
-            store_out8(p.out, p.out_type, i0 + 8 * i, x, true);
-        }
-    }
 }
 
 template <int D, bool BF16>
@@ -389,30 +361,8 @@ __global__ void __launch_bounds__(Pt<D>::THREADS, 1)
                     tc_ld32(tS + 96, v + 96);
                     tc_wait_ld();
                     tc_regs_ready(v);
-                    if (n * C::BN + C::BN - 1 > w_last || n * C::BN < w_first) {
-                        const int hi = last - n * C::BN, lo = first - n * C::BN;   // columns lo .. hi are seen
-#pragma unroll
-                        for (int b = 0; b < 4; ++b) {
-                            // bits of the 32 columns from 32 b on
-                            const int h = hi + 1 - 32 * b, g = lo - 32 * b;
-                            const uint32_t below = h >= 32 ? 0xffffffffu : (h <= 0 ? 0u : (1u << h) - 1u);
-                            const uint32_t seen = g <= 0 ? below : (g >= 32 ? 0u : below & (0xffffffffu << g));
-#pragma unroll
-                            for (int c = 0; c < 32; ++c)
-                                if (!(seen & (1u << c))) v[32 * b + c] = 0xff800000u;
-                        }
-                    }
-                    float x0 = __uint_as_float(v[0]), x1 = __uint_as_float(v[1]), x2 = __uint_as_float(v[2]), x3 = __uint_as_float(v[3]);
-#pragma unroll
-                    for (int c = 4; c < 124; c += 8) {
-                        x0 = max3(x0, __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
-                        x1 = max3(x1, __uint_as_float(v[c + 2]), __uint_as_float(v[c + 3]));
-                        x2 = max3(x2, __uint_as_float(v[c + 4]), __uint_as_float(v[c + 5]));
-                        x3 = max3(x3, __uint_as_float(v[c + 6]), __uint_as_float(v[c + 7]));
-                    }
-                    x0 = max3(x0, __uint_as_float(v[124]), __uint_as_float(v[125]));
-                    x1 = max3(x1, __uint_as_float(v[126]), __uint_as_float(v[127]));
-                    const float mx = max3(fmaxf(x0, x1), x2, x3) * p.scale_log2;
+                    if (n * C::BN + C::BN - 1 > w_last || n * C::BN < w_first) row_mask(v, first - n * C::BN, last - n * C::BN);
+                    const float mx = row_max(v) * p.scale_log2;
                     // a first maximum needs no rescaling: O is still zero in that row
                     const bool grow = mx > m + 8.0f;
                     float f = 1.0f;
@@ -421,43 +371,8 @@ __global__ void __launch_bounds__(Pt<D>::THREADS, 1)
                         m = mx;
                         l *= f;
                     }
-                    if (__any_sync(0xffffffffu, f != 1.0f) && n > ta) {
-#pragma unroll 1
-                        for (int c = 0; c < D; c += 16) {
-                            uint32_t o[16];
-                            tc_ld16(tO + c, o);
-                            tc_wait_ld();
-                            tc_regs_ready(o);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            tc_st16(tO + c, o);
-                        }
-                    }
-                    const float neg = m == -INFINITY ? 0.0f : -m;
-                    const uint64_t scale2 = pair2(p.scale_log2, p.scale_log2), neg2 = pair2(neg, neg);
-                    uint64_t s0 = 0, s1 = 0;
-#pragma unroll
-                    for (int b = 0; b < 128; b += 32) {
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int c = 0; c < 32; c += 4) {
-                            float a0, a1, a2, a3;
-                            split2(a0, a1, fma2(pair2(__uint_as_float(v[b + c]), __uint_as_float(v[b + c + 1])), scale2, neg2));
-                            split2(a2, a3, fma2(pair2(__uint_as_float(v[b + c + 2]), __uint_as_float(v[b + c + 3])), scale2, neg2));
-                            a0 = ex2(a0);
-                            a1 = ex2(a1);
-                            a2 = ex2(a2);
-                            a3 = ex2(a3);
-                            s0 = add2(s0, pair2(a0, a1));
-                            s1 = add2(s1, pair2(a2, a3));
-                            pk[c / 2] = pack16<BF16>(a0, a1);
-                            pk[c / 2 + 1] = pack16<BF16>(a2, a3);
-                        }
-                        tc_st16(tS + b / 2, pk);
-                    }
-                    float l0, l1;
-                    split2(l0, l1, add2(s0, s1));
-                    l += l0 + l1;
+                    if (__any_sync(0xffffffffu, f != 1.0f) && n > ta) row_rescale<D>(tO, f);
+                    l += row_weights<BF16>(v, p.scale_log2, m, tS);
                     tc_wait_st();
                     tc_fence_before();
                     __syncwarp();
@@ -477,31 +392,8 @@ __global__ void __launch_bounds__(Pt<D>::THREADS, 1)
                 const bool mine = row < w.rows;
                 const uint64_t orow = (uint64_t)(w.q0 + w.row0 + row) * p.n_heads + head;
                 const bool fix = dirty[item & 7] == item + 1;
-#pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                    uint32_t o[32];
-                    tc_ld32(tO + c, o);
-                    tc_wait_ld();
-                    tc_regs_ready(o);
-                    float y[32];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) y[e] = f == 0.0f ? 0.0f : __uint_as_float(o[e]) * f;
-                    if (mine) {
-                        if (fix) {
-                            const uint16_t *vp = static_cast<const uint16_t *>(p.v) + (uint64_t)w.k0 * p.v_stride + (uint64_t)kvh * D + c;
-#pragma unroll
-                            for (int e = 0; e < 32; e += 8) {
-                                float z[8];
-#pragma unroll
-                                for (int k = 0; k < 8; ++k) z[k] = y[e + k];
-                                prompt_restore<BF16>(p, w, vp + e, row, C::BN, z);
-#pragma unroll
-                                for (int k = 0; k < 8; ++k) y[e + k] = z[k];
-                            }
-                        }
-                        store_row32(p, orow, c, y);
-                    }
-                }
+                const uint16_t *vp = static_cast<const uint16_t *>(p.v) + (uint64_t)w.k0 * p.v_stride + (uint64_t)kvh * D;
+                row_output<D, BF16>(p, w, tO, f, mine, orow, 0, fix ? vp : nullptr, row);
                 if (p.lse && mine) p.lse[orow] = lse;
                 tc_fence_before();   // O is read: the next tile's first P V follows this warp's next arrival
             }
@@ -525,9 +417,10 @@ template <int D, bool BF16> cudaError_t launch_tc(const AttnPromptParams &p, int
     }
     alignas(64) CUtensorMap tmQ, tmK, tmV;
     if (!encode_rows16_tmap(&tmQ, p.q, (uint64_t)p.n_heads * D, p.n_q, p.q_stride, 128, BF16) ||
-        !encode_rows16_tmap(&tmK, p.k, (uint64_t)p.n_kv * D, p.n_k, p.k_stride, 128, BF16) ||
-        !encode_rows16_tmap(&tmV, p.v, (uint64_t)p.n_kv * D, p.n_k, p.v_stride, 128, BF16))
+        (p.n_k && (!encode_rows16_tmap(&tmK, p.k, (uint64_t)p.n_kv * D, p.n_k, p.k_stride, 128, BF16) ||
+                   !encode_rows16_tmap(&tmV, p.v, (uint64_t)p.n_kv * D, p.n_k, p.v_stride, 128, BF16))))
         return cudaErrorInvalidValue;
+    if (!p.n_k) tmK = tmV = tmQ;   // no key tile is loaded
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p.list ? (unsigned)num_sms : (unsigned)(p.n_heads * (p.n_q / Pt<D>::BM + p.n_seq)));
     cfg.blockDim = dim3(Pt<D>::THREADS);
@@ -545,18 +438,20 @@ template <int D, bool BF16> cudaError_t launch_tc(const AttnPromptParams &p, int
 }  // namespace
 
 size_t attn_prompt_list_bytes(const AttnPromptParams &p, int num_sms) {
-    const uint64_t tiles = p.n_q / 256 + p.n_seq;
-    return tiles * p.n_heads > (uint64_t)num_sms ? (tiles + 1) * sizeof(PromptTile) : 0;
+    const uint64_t rows = attn_prompt_tile_rows(p.dim), tiles = p.n_q / rows + p.n_seq;
+    return tiles * p.n_heads * attn_prompt_parts(p.dim) > (uint64_t)num_sms ? (tiles + 1) * sizeof(PromptTile) : 0;
 }
 
-cudaError_t launch_attn_prompt_tc(AttnPromptParams p, void *list, int num_sms, cudaStream_t st) {
+cudaError_t launch_attn_prompt(AttnPromptParams p, void *list, int num_sms, cudaStream_t st) {
+    p.list_rows = (int)attn_prompt_tile_rows(p.dim);
     if (list) {
         p.list = static_cast<PromptTile *>(list);
-        p.list_cap = p.n_q / 256 + p.n_seq;
+        p.list_cap = p.n_q / (uint32_t)p.list_rows + p.n_seq;
         for (p.list_shift = 0; (p.n_k / 128 >> p.list_shift) >= LIST_BINS - 1; ++p.list_shift) {}
         const cudaError_t e = launch_dependent(k_attn_prompt_list, p, dim3(1), LIST_THREADS, 0, st);
         if (e != cudaSuccess) return e;
     }
+    if (p.dim > 128) return launch_attn_prompt_wide(p, num_sms, st);
     const bool bf = p.type == Q8_TYPE_BF16;
     if (p.dim == 64) return bf ? launch_tc<64, true>(p, num_sms, st) : launch_tc<64, false>(p, num_sms, st);
     return bf ? launch_tc<128, true>(p, num_sms, st) : launch_tc<128, false>(p, num_sms, st);

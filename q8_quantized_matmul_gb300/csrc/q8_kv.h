@@ -113,20 +113,22 @@ struct AttnPromptParams {
     int out_type;
     float *lse;
     int *err;
-    // Failure-detection test hook (tcgen05 kernel; zero in normal calls): see GemvParams
+    // Failure-detection test hook (zero in normal calls): see GemvParams
     uint64_t wait_ns;
     int withhold;
-    // tcgen05 kernel: the list of tiles (its first element holds their number), or nullptr
+    // the list of tiles (its first element holds their number), or nullptr
     PromptTile *list;
     uint32_t list_cap;
-    int list_shift;
+    int list_shift, list_rows;
 };
-// Whether a call runs on the tcgen05 kernel (heads of 64 or 128 values, some keys), else mma.sync.
-inline bool attn_prompt_on_tc(uint32_t dim, uint64_t n_k) { return dim <= 128 && n_k > 0; }
+// Query rows of a tile, and the parts of a head's dims that are worked on apart: two tiles of 128 rows share a
+// CTA up to 128 dims; above, O of one tile and 256 dims takes half of TMEM.
+inline uint32_t attn_prompt_tile_rows(uint32_t dim) { return dim <= 128 ? 256 : 128; }
+inline uint32_t attn_prompt_parts(uint32_t dim) { return dim <= 256 ? 1 : dim / 256; }
 // Scratch for the tile list of a call (0: none needed), then the call with it.
 size_t attn_prompt_list_bytes(const AttnPromptParams &p, int num_sms);
-cudaError_t launch_attn_prompt_tc(AttnPromptParams p, void *list, int num_sms, cudaStream_t st);
-cudaError_t launch_attn_prompt_mma(const AttnPromptParams &p, cudaStream_t st);
+cudaError_t launch_attn_prompt(AttnPromptParams p, void *list, int num_sms, cudaStream_t st);
+cudaError_t launch_attn_prompt_wide(const AttnPromptParams &p, int num_sms, cudaStream_t st);
 
 // Launch with programmatic stream serialisation: the kernel starts while the one before
 // it drains and waits (griddepcontrol.wait) before it reads or writes anything.

@@ -367,6 +367,38 @@ def test_prompt_window_and_sinks(q8, dim, window):
     check_prompt(q8, "bf16", [300, 66, 1], [300, 150, 1], heads=2, kv=1, dim=dim, window=window, sinks=True, seed=window)
 
 
+def test_prompt_without_any_key(q8):
+    for dim in (64, 512):
+        q = torch.randn(5, 2, dim, device=DEV).half()
+        none = torch.empty(0, 1, dim, device=DEV, dtype=torch.float16)
+        start, empty = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in ([0, 2, 5], [0, 0, 0]))
+        o, lse = q8.attn_prompt(q, none, none, start, empty, want_lse=True)
+        assert torch.all(o == 0) and torch.all(lse == -float("inf")) and q8.q8_last_error() == 0
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256, 512])
+def test_prompt_more_tiles_than_sms(q8, dim):
+    """Persistent CTAs over the list of tiles: many sequences, empty ones among them, several tiles a CTA."""
+    rng = np.random.default_rng(dim)
+    lens = [int(x) for x in rng.integers(0, 300, 90)]
+    keys = [n + int(e) for n, e in zip(lens, rng.integers(-40, 60, 90).clip(min=[-n for n in lens]))]
+    check_prompt(q8, "bf16", lens, keys, heads=2, kv=1, dim=dim, seed=dim, window=200, sinks=True)
+
+
+def test_prompt_growing_scores(q8):
+    """Scores that rise along the sequence: outputs are rescaled in many key tiles."""
+    for dim in (64, 128, 512):
+        n = 1000
+        g = torch.Generator().manual_seed(dim)
+        q, v = (torch.randn((n, 1, dim), generator=g).half().to(DEV) for _ in range(2))
+        ramp = torch.linspace(-1.0, 1.0, n).to(DEV)[:, None, None]
+        k = (q[n // 2:n // 2 + 1].float() * ramp * 0.06 * 8).half()
+        got = f64(q8.attn_prompt(q, k, v, torch.tensor([0, n], dtype=torch.int32, device=DEV)))
+        see = np.tril(np.ones((n, n), bool))
+        r, _, b, _ = attend(f64(q)[:, 0], f64(k)[:, 0], f64(v)[:, 0], see, dim ** -0.5, None, "f16", "f16")
+        check(got[:, 0], r, b, f"dim {dim}")
+
+
 def test_prompt_long(q8):
     check_prompt(q8, "bf16", [1500], [1500], heads=2, kv=1, dim=128, seed=1)
     check_prompt(q8, "f16", [1100, 40], [1300, 40], heads=2, kv=1, dim=64, seed=2, window=600)
