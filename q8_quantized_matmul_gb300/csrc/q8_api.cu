@@ -1347,6 +1347,7 @@ int q8_attn_prompt(void *out, int out_type, float *lse, const void *q, const voi
     p.lse = lse;
     p.err = s->err;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    q8::attn_prompt_tiling(p, s->num_sms);
     const size_t list = q8::attn_prompt_list_bytes(p, s->num_sms);
     if ((rc = reserve_scratch(s, list))) return rc;
     take_expiry(p.wait_ns, p.withhold);

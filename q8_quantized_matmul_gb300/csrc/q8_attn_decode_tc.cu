@@ -26,7 +26,7 @@
 namespace q8 {
 
 bool encode_3d16_tmap(CUtensorMap *map, const void *base, uint64_t cols, uint64_t n1, uint64_t n2, uint64_t stride1,
-                      uint64_t stride2, uint32_t box1, bool bf16);
+                      uint64_t stride2, uint32_t box1, uint32_t box2, bool bf16);
 
 namespace {
 
@@ -527,9 +527,9 @@ template <int D, bool BF16> cudaError_t launch_tc(const AttnDecodeParams &p, int
     }
     alignas(64) CUtensorMap tmQ, tmK, tmV;
     const uint32_t tokens = 1u << p.c.page_shift, box = tokens < 128 ? tokens : 128;
-    if (!encode_3d16_tmap(&tmQ, p.q, D, p.n_heads, p.n_seq, D, p.q_stride, Dt<D>::HT, BF16) ||
-        !encode_3d16_tmap(&tmK, p.c.k, D, (uint64_t)p.c.n_kv * tokens, p.c.n_pages, D, p.c.page_stride / 2, box, BF16) ||
-        !encode_3d16_tmap(&tmV, p.c.v, D, (uint64_t)p.c.n_kv * tokens, p.c.n_pages, D, p.c.page_stride / 2, box, BF16))
+    if (!encode_3d16_tmap(&tmQ, p.q, D, p.n_heads, p.n_seq, D, p.q_stride, Dt<D>::HT, 1, BF16) ||
+        !encode_3d16_tmap(&tmK, p.c.k, D, (uint64_t)p.c.n_kv * tokens, p.c.n_pages, D, p.c.page_stride / 2, box, 1, BF16) ||
+        !encode_3d16_tmap(&tmV, p.c.v, D, (uint64_t)p.c.n_kv * tokens, p.c.n_pages, D, p.c.page_stride / 2, box, 1, BF16))
         return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);

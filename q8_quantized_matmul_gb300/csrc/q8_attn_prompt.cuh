@@ -7,7 +7,7 @@
 
 namespace q8 {
 
-// Up to BM query rows of one sequence.
+// Up to tile_tokens queries of one sequence (a row is a query token here, whatever heads are packed with it).
 struct alignas(8) PromptTile {
     int q0, k0;          // first packed row of the sequence's queries / keys
     int row0, rows;      // first query of the tile within the sequence, and how many
@@ -30,7 +30,7 @@ struct alignas(8) PromptTile {
 
 __device__ __forceinline__ int prompt_bound(int32_t start, uint32_t n) { return (int)min((uint32_t)max(start, 0), n); }
 
-// Tile `slot` of the packed sequences in tiles of BM query rows, the newest rows of the last sequence
+// Tile `slot` of the packed sequences in tiles of BM queries, the newest rows of the last sequence
 // first (their rows see the most keys, so the long tiles start first).  False: no such tile.
 // Called by a whole CTA of THREADS; sh: THREADS / 32 + 5 ints of shared memory.  report: raise bad starts.
 template <int THREADS>

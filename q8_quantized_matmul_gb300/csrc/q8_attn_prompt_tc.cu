@@ -1,7 +1,8 @@
 // q8_attn_prompt_tc.cu -- attention over whole packed prompts on the 5th-generation tensor cores,
 // heads of 64 or 128 values.
 //
-// A CTA works on 256 query rows of one head as two tiles of 128 rows, over key tiles of 128.  Per key
+// A CTA works on 256 rows as two tiles of 128, over key tiles of 128.  A row is a query of one head; the heads
+// of a group may be packed beside each other (attn_prompt_pack), so short prompts fill their tiles too.  Per key
 // tile and query tile: S = Q K^T (D/16 UMMAs) into 128 TMEM columns; one thread per row reads its S,
 // keeps the running maximum m and sum l, writes P = 2^(S - m) as 16-bit pairs over S; O += P V
 // (8 UMMAs, P from TMEM) into D further columns.  S of both tiles (256 columns) and O of both (2 D) fill
@@ -33,11 +34,13 @@ namespace q8 {
 
 bool encode_rows16_tmap(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, uint64_t row_stride,
                         uint32_t box_rows, bool bf16);
+bool encode_3d16_tmap(CUtensorMap *map, const void *base, uint64_t cols, uint64_t n1, uint64_t n2, uint64_t stride1,
+                      uint64_t stride2, uint32_t box1, uint32_t box2, bool bf16);
 
 namespace {
 
 template <int D> struct Pt {
-    static constexpr int BN = 128, BM = 256;
+    static constexpr int BN = 128;
     static constexpr int CH = D / 64;                        // 64-value chunks of a row, 16 KB a chunk of 128 rows
     static constexpr int TILE = 128 * D * 2;
     // stage u holds the values of key tile u - 1 and the keys of tile u, which are used in one go
@@ -57,7 +60,7 @@ __device__ __forceinline__ int tile_cost(const PromptTile &w, uint32_t window) {
     return last < 0 ? 0 : last / 128 + 1 - w.first(0, window) / 128;
 }
 
-// One CTA: all tiles of list_rows query rows, the ones with the most key tiles first (counting sort; the order
+// One CTA: all tiles of tile_tokens queries, the ones with the most key tiles first (counting sort; the order
 // among equals does not matter to any result).
 __global__ void __launch_bounds__(LIST_THREADS) k_attn_prompt_list(const AttnPromptParams p) {
     __shared__ int bin[LIST_BINS];
@@ -79,9 +82,9 @@ __global__ void __launch_bounds__(LIST_THREADS) k_attn_prompt_list(const AttnPro
             w.k0 = ka;
             w.lk = max(ke - ka, 0);
             w.shift = w.lk - (qe - qa);
-            for (int64_t r = (int64_t)lane * p.list_rows; r < qe - qa; r += 32 * (int64_t)p.list_rows) {
+            for (int64_t r = (int64_t)lane * p.tile_tokens; r < qe - qa; r += 32 * (int64_t)p.tile_tokens) {
                 w.row0 = (int)r;
-                w.rows = min(p.list_rows, qe - qa - w.row0);
+                w.rows = min(p.tile_tokens, qe - qa - w.row0);
                 const int c = tile_cost(w, p.window) >> p.list_shift;
                 f(w, LIST_BINS - 1 - min(c, LIST_BINS - 1));   // longest in the first bin
             }
@@ -151,11 +154,12 @@ __global__ void __launch_bounds__(Pt<D>::THREADS, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    const uint32_t per_tile = p.n_heads / p.pack;   // items of a tile: groups of packed heads
     __shared__ PromptTile w_one;
     bool one = false;
     if (!p.list) {
         PromptTile w;
-        one = prompt_tile<C::THREADS>(p, C::BM, blockIdx.x / p.n_heads, blockIdx.x == 0, w, sh);
+        one = prompt_tile<C::THREADS>(p, p.tile_tokens, blockIdx.x / per_tile, blockIdx.x == 0, w, sh);
         if (one && tid == 0) w_one = w;
     }
     tc_fence_before();
@@ -165,11 +169,11 @@ __global__ void __launch_bounds__(Pt<D>::THREADS, 1)
     const uint64_t lim = wait_limit(p.wait_ns);
     const uint32_t group = p.n_heads / p.n_kv;
     // tiles of this CTA: its own, or every gridDim.x-th of the list, heads of one tile side by side
-    const uint32_t n_items = p.list ? (uint32_t)min((uint64_t)*reinterpret_cast<const uint32_t *>(p.list) * p.n_heads, (uint64_t)0xffff0000u)
+    const uint32_t n_items = p.list ? (uint32_t)min((uint64_t)*reinterpret_cast<const uint32_t *>(p.list) * per_tile, (uint64_t)0xffff0000u)
                                     : (one ? blockIdx.x + 1 : 0);
     const uint32_t step = p.list ? gridDim.x : 0x40000000u;
     auto load_item = [&](uint32_t id) {
-        return p.list ? p.list[1 + id / p.n_heads] : w_one;
+        return p.list ? p.list[1 + id / per_tile] : w_one;
     };
     // key tiles [t0[i], t1[i]) that query tile i sees, and [n0, n1) that either sees
     struct Range {
@@ -181,7 +185,7 @@ __global__ void __launch_bounds__(Pt<D>::THREADS, 1)
         r.n1 = 0;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int ra = 128 * i, rb = min(w.rows, ra + 128) - 1;
+            const int ra = p.half * i, rb = min(w.rows, ra + p.half) - 1;
             r.t0[i] = r.t1[i] = 0;
             if (rb >= ra && w.last(rb) >= 0) {
                 r.t0[i] = w.first(ra, p.window) / C::BN;
@@ -205,15 +209,15 @@ __global__ void __launch_bounds__(Pt<D>::THREADS, 1)
             for (uint32_t id = blockIdx.x; id < n_items; id += step) {
                 const PromptTile w = load_item(id);
                 const Range r = ranges(w);
-                const int qx = (int)(id % p.n_heads) * D, kx = (int)(id % p.n_heads / group) * D;
+                const int head0 = (int)(id % per_tile) * p.pack, kx = head0 / (int)group * D;
                 if (r.n1 == r.n0) continue;
                 if (go(qempty, (q_loads & 1) ^ 1)) {
                     if (lane == 0) {
-                        const bool two = w.rows > 128;
-                        mbar_arrive_expect_tx(qfull, (two ? 2 : 1) * C::TILE);
-                        for (int i = 0; i < (two ? 2 : 1); ++i)
+                        const int n = w.rows > p.half ? 2 : 1;
+                        mbar_arrive_expect_tx(qfull, (uint32_t)(n * C::CH * p.half * p.pack * 128));
+                        for (int i = 0; i < n; ++i)
                             for (int c = 0; c < C::CH; ++c)
-                                tma_load_2d(qs + i * C::TILE + c * 16384, &tmQ, qx + 64 * c, w.q0 + w.row0 + 128 * i, qfull);
+                                tma_load_3d(qs + i * C::TILE + c * 16384, &tmQ, 64 * c, head0, w.q0 + w.row0 + p.half * i, qfull);
                     }
                     ++q_loads;
                 }
@@ -331,7 +335,8 @@ __global__ void __launch_bounds__(Pt<D>::THREADS, 1)
             }
         } else {
             // ------------------------------------------------ softmax of tile i, one row a thread
-            const int i = warp >> 2, row = i * 128 + (warp & 3) * 32 + lane;
+            const int i = warp >> 2, r0 = (warp & 3) * 32;
+            const RowOf me(p, i, r0 + lane);
             const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
             const uint32_t tS = tmem + lanes + i * 128, tO = tmem + lanes + 256 + i * 128;
             uint32_t s_seen = 0, o_seen = 0;
@@ -341,11 +346,11 @@ __global__ void __launch_bounds__(Pt<D>::THREADS, 1)
                 {
                     const PromptTile w = load_item(id);
                     const Range r = ranges(w);
-                    last = w.last(row);
-                    first = w.first(row, p.window);
+                    last = w.last(me.token);
+                    first = w.first(me.token, p.window);
                     // tiles that every row of the warp sees whole need no mask
-                    w_last = w.last(i * 128 + (warp & 3) * 32);
-                    w_first = w.first(i * 128 + (warp & 3) * 32 + 31, p.window);
+                    w_last = w.last(RowOf(p, i, r0).token);
+                    w_first = w.first(RowOf(p, i, r0 + 31).token, p.window);
                     ta = i ? r.t0[1] : r.t0[0];
                     tb = i ? r.t1[1] : r.t1[0];
                 }
@@ -386,14 +391,14 @@ __global__ void __launch_bounds__(Pt<D>::THREADS, 1)
                 }
                 tc_fence_after();
                 const PromptTile w = load_item(id);
-                const uint32_t head = id % p.n_heads, kvh = head / group;
+                const uint32_t head = id % per_tile * p.pack + me.head, kvh = head / group;
                 float lse;
                 const float f = softmax_finish(m, l, p.sinks != nullptr, p.sinks ? p.sinks[head] * 1.4426950408889634f : 0.0f, lse);
-                const bool mine = row < w.rows;
-                const uint64_t orow = (uint64_t)(w.q0 + w.row0 + row) * p.n_heads + head;
+                const bool mine = me.used && me.token < w.rows;
+                const uint64_t orow = (uint64_t)(w.q0 + w.row0 + me.token) * p.n_heads + head;
                 const bool fix = dirty[item & 7] == item + 1;
                 const uint16_t *vp = static_cast<const uint16_t *>(p.v) + (uint64_t)w.k0 * p.v_stride + (uint64_t)kvh * D;
-                row_output<D, BF16>(p, w, tO, f, mine, orow, 0, fix ? vp : nullptr, row);
+                row_output<D, BF16>(p, w, tO, f, mine, orow, 0, fix ? vp : nullptr, me.token);
                 if (p.lse && mine) p.lse[orow] = lse;
                 tc_fence_before();   // O is read: the next tile's first P V follows this warp's next arrival
             }
@@ -416,13 +421,13 @@ template <int D, bool BF16> cudaError_t launch_tc(const AttnPromptParams &p, int
         attr_done = true;
     }
     alignas(64) CUtensorMap tmQ, tmK, tmV;
-    if (!encode_rows16_tmap(&tmQ, p.q, (uint64_t)p.n_heads * D, p.n_q, p.q_stride, 128, BF16) ||
+    if (!encode_3d16_tmap(&tmQ, p.q, D, p.n_heads, p.n_q, D, p.q_stride, (uint32_t)p.pack, (uint32_t)p.half, BF16) ||
         (p.n_k && (!encode_rows16_tmap(&tmK, p.k, (uint64_t)p.n_kv * D, p.n_k, p.k_stride, 128, BF16) ||
                    !encode_rows16_tmap(&tmV, p.v, (uint64_t)p.n_kv * D, p.n_k, p.v_stride, 128, BF16))))
         return cudaErrorInvalidValue;
     if (!p.n_k) tmK = tmV = tmQ;   // no key tile is loaded
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.list ? (unsigned)num_sms : (unsigned)(p.n_heads * (p.n_q / Pt<D>::BM + p.n_seq)));
+    cfg.gridDim = dim3(p.list ? (unsigned)num_sms : (unsigned)(p.n_heads / p.pack * (p.n_q / p.tile_tokens + p.n_seq)));
     cfg.blockDim = dim3(Pt<D>::THREADS);
     cfg.dynamicSmemBytes = Pt<D>::SMEM;
     cfg.stream = st;
@@ -437,16 +442,21 @@ template <int D, bool BF16> cudaError_t launch_tc(const AttnPromptParams &p, int
 
 }  // namespace
 
+void attn_prompt_tiling(AttnPromptParams &p, int num_sms) {
+    p.pack = attn_prompt_pack(p.n_heads / p.n_kv, p.n_kv, p.dim, p.n_q, p.n_seq, num_sms);
+    p.half = 128 / p.pack;
+    p.tile_tokens = p.half * attn_prompt_halves(p.dim);
+}
+
 size_t attn_prompt_list_bytes(const AttnPromptParams &p, int num_sms) {
-    const uint64_t rows = attn_prompt_tile_rows(p.dim), tiles = p.n_q / rows + p.n_seq;
-    return tiles * p.n_heads * attn_prompt_parts(p.dim) > (uint64_t)num_sms ? (tiles + 1) * sizeof(PromptTile) : 0;
+    const uint64_t tiles = p.n_q / p.tile_tokens + p.n_seq;
+    return tiles * (p.n_heads / p.pack) * attn_prompt_parts(p.dim) > (uint64_t)num_sms ? (tiles + 1) * sizeof(PromptTile) : 0;
 }
 
 cudaError_t launch_attn_prompt(AttnPromptParams p, void *list, int num_sms, cudaStream_t st) {
-    p.list_rows = (int)attn_prompt_tile_rows(p.dim);
     if (list) {
         p.list = static_cast<PromptTile *>(list);
-        p.list_cap = p.n_q / (uint32_t)p.list_rows + p.n_seq;
+        p.list_cap = p.n_q / p.tile_tokens + p.n_seq;
         for (p.list_shift = 0; (p.n_k / 128 >> p.list_shift) >= LIST_BINS - 1; ++p.list_shift) {}
         const cudaError_t e = launch_dependent(k_attn_prompt_list, p, dim3(1), LIST_THREADS, 0, st);
         if (e != cudaSuccess) return e;

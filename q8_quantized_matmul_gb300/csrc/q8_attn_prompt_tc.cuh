@@ -7,6 +7,19 @@
 
 namespace q8 {
 
+// Row r (0 .. 127) of half i of a tile: its token within the tile (the last one for rows that hold none) and its
+// head among the packed ones.
+struct RowOf {
+    int token, head;
+    bool used;
+    __device__ __forceinline__ RowOf(const AttnPromptParams &p, int i, int r) {
+        const int t = r / p.pack;
+        used = t < p.half;
+        token = i * p.half + min(t, p.half - 1);
+        head = r - t * p.pack;
+    }
+};
+
 // Columns outside lo .. hi become -inf.
 __device__ __forceinline__ void row_mask(uint32_t (&v)[128], int lo, int hi) {
 #pragma unroll
@@ -105,7 +118,7 @@ __device__ __forceinline__ void store_row32(const AttnPromptParams &p, uint64_t 
     }
 }
 
-// N columns of O times f as the output's dims d0 .. of packed row `orow`; vp (or nullptr): the first value row
+// N columns of O times f as the output's dims d0 .. of `orow` (a token's head); row: the token within the tile; vp (or nullptr): the first value row
 // of the sequence, at this head's first dim, when values that are not finite were taken out (prompt_restore).
 template <int N, bool BF16>
 __device__ __forceinline__ void row_output(const AttnPromptParams &p, const PromptTile &w, uint32_t tO, float f, bool mine,

@@ -1,7 +1,7 @@
 // q8_attn_prompt_wide.cu -- attention over whole packed prompts on the 5th-generation tensor cores, heads of
 // 256 or 512 values.
 //
-// A work item is 128 query rows of one head and 256 of its output dims (heads of 512: two items, which both
+// A work item is 128 rows (queries of one head, or of several packed heads) and 256 of their output dims (heads of 512: two items, which both
 // compute the scores).  TMEM: two buffers of S (128 columns each) and O (256).  S of key tile n + 1 is issued
 // before P V of tile n, so the softmax of a tile (about 1000 cycles) runs under the next one's S (2048 cycles at
 // 512 values, 1024 at 256) and the tensor pipe does not wait for it.  Operands stream through a ring of slots of
@@ -18,6 +18,8 @@ namespace q8 {
 
 bool encode_rows16_tmap(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, uint64_t row_stride,
                         uint32_t box_rows, bool bf16);
+bool encode_3d16_tmap(CUtensorMap *map, const void *base, uint64_t cols, uint64_t n1, uint64_t n2, uint64_t stride1,
+                      uint64_t stride2, uint32_t box1, uint32_t box2, bool bf16);
 
 namespace {
 
@@ -75,11 +77,11 @@ __global__ void __launch_bounds__(Pw<D>::THREADS, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    const uint32_t per_tile = p.n_heads * C::PARTS;   // items of a tile: heads, and the parts of each side by side
+    const uint32_t per_tile = p.n_heads / p.pack * C::PARTS;   // items of a tile: groups of packed heads, their parts side by side
     bool one = false;
     if (!p.list) {
         PromptTile w;
-        one = prompt_tile<C::THREADS>(p, C::BM, blockIdx.x / per_tile, blockIdx.x == 0, w, sh);
+        one = prompt_tile<C::THREADS>(p, p.tile_tokens, blockIdx.x / per_tile, blockIdx.x == 0, w, sh);
         if (one && tid == 0) w_one = w;
     }
     tc_fence_before();
@@ -127,13 +129,13 @@ __global__ void __launch_bounds__(Pw<D>::THREADS, 1)
             int n0, n1;
             range(w, n0, n1);
             if (n1 == n0) continue;
-            const uint32_t r = id % per_tile, head = r / C::PARTS;
-            const int kx = (int)(head / group) * D, vx = kx + (int)(r % C::PARTS) * C::DV;
+            const uint32_t r = id % per_tile, head0 = r / C::PARTS * p.pack;
+            const int kx = (int)(head0 / group) * D, vx = kx + (int)(r % C::PARTS) * C::DV;
             if (go(qempty, (q_loads & 1) ^ 1)) {
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(qfull, C::QBYTES);
+                    mbar_arrive_expect_tx(qfull, (uint32_t)(D / 64 * p.half * p.pack * 128));
                     for (int c = 0; c < D / 64; ++c)
-                        tma_load_2d(qs + c * C::CHUNK, &tmQ, (int)head * D + 64 * c, w.q0 + w.row0, qfull);
+                        tma_load_3d(qs + c * C::CHUNK, &tmQ, 64 * c, (int)head0, w.q0 + w.row0, qfull);
                 }
                 ++q_loads;
             }
@@ -255,7 +257,7 @@ __global__ void __launch_bounds__(Pw<D>::THREADS, 1)
         }
     } else {
         // ------------------------------------------------ softmax, one row a thread
-        const int row = tid;
+        const RowOf me(p, 0, tid);
         const uint32_t lanes = (uint32_t)(warp * 32) << 16;
         const uint32_t tO = tmem + lanes + 256;
         uint32_t nt = 0;
@@ -268,11 +270,11 @@ __global__ void __launch_bounds__(Pw<D>::THREADS, 1)
             {
                 const PromptTile w = load_item(id);
                 range(w, n0, n1);
-                last = w.last(row);
-                first = w.first(row, p.window);
+                last = w.last(me.token);
+                first = w.first(me.token, p.window);
                 // tiles that every row of the warp sees whole need no mask
-                w_last = w.last(warp * 32);
-                w_first = w.first(warp * 32 + 31, p.window);
+                w_last = w.last(RowOf(p, 0, warp * 32).token);
+                w_first = w.first(RowOf(p, 0, warp * 32 + 31).token, p.window);
             }
             float m = -INFINITY, l = 0.0f;
             for (int n = n0; n < n1; ++n, ++nt) {
@@ -310,14 +312,14 @@ __global__ void __launch_bounds__(Pw<D>::THREADS, 1)
             if (n1 > n0) p_v_done(nt - 1);
             tc_fence_after();
             const PromptTile w = load_item(id);
-            const uint32_t r = id % per_tile, head = r / C::PARTS, kvh = head / group;
+            const uint32_t r = id % per_tile, head = r / C::PARTS * p.pack + me.head, kvh = head / group;
             const int d0 = (int)(r % C::PARTS) * C::DV;
             float lse;
             const float f = softmax_finish(m, l, p.sinks != nullptr, p.sinks ? p.sinks[head] * 1.4426950408889634f : 0.0f, lse);
-            const bool mine = row < w.rows;
-            const uint64_t orow = (uint64_t)(w.q0 + w.row0 + row) * p.n_heads + head;
+            const bool mine = me.used && me.token < w.rows;
+            const uint64_t orow = (uint64_t)(w.q0 + w.row0 + me.token) * p.n_heads + head;
             const uint16_t *vp = static_cast<const uint16_t *>(p.v) + (uint64_t)w.k0 * p.v_stride + (uint64_t)kvh * D;
-            row_output<C::DV, BF16>(p, w, tO, f, mine, orow, d0, dirty[item & 7] == item + 1 ? vp : nullptr, row);
+            row_output<C::DV, BF16>(p, w, tO, f, mine, orow, d0, dirty[item & 7] == item + 1 ? vp : nullptr, me.token);
             if (p.lse && mine && d0 == 0) p.lse[orow] = lse;
             tc_fence_before();   // O is read: the next item's first P V follows this warp's next arrival
         }
@@ -339,13 +341,13 @@ template <int D, bool BF16> cudaError_t launch_wide(const AttnPromptParams &p, i
         attr_done = true;
     }
     alignas(64) CUtensorMap tmQ, tmK, tmV;
-    if (!encode_rows16_tmap(&tmQ, p.q, (uint64_t)p.n_heads * D, p.n_q, p.q_stride, 128, BF16) ||
+    if (!encode_3d16_tmap(&tmQ, p.q, D, p.n_heads, p.n_q, D, p.q_stride, (uint32_t)p.pack, (uint32_t)p.half, BF16) ||
         (p.n_k && (!encode_rows16_tmap(&tmK, p.k, (uint64_t)p.n_kv * D, p.n_k, p.k_stride, 128, BF16) ||
                    !encode_rows16_tmap(&tmV, p.v, (uint64_t)p.n_kv * D, p.n_k, p.v_stride, 128, BF16))))
         return cudaErrorInvalidValue;
     if (!p.n_k) tmK = tmV = tmQ;   // no key tile is loaded
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.list ? (unsigned)num_sms : (unsigned)(p.n_heads * Pw<D>::PARTS * (p.n_q / Pw<D>::BM + p.n_seq)));
+    cfg.gridDim = dim3(p.list ? (unsigned)num_sms : (unsigned)(p.n_heads / p.pack * Pw<D>::PARTS * (p.n_q / p.tile_tokens + p.n_seq)));
     cfg.blockDim = dim3(Pw<D>::THREADS);
     cfg.dynamicSmemBytes = Pw<D>::SMEM;
     cfg.stream = st;

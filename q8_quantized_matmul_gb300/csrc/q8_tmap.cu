@@ -79,15 +79,15 @@ bool encode_rows16_tmap(CUtensorMap *map, const void *base, uint64_t cols, uint6
     return r == CUDA_SUCCESS;
 }
 
-// fp16 or bf16 [n2][n1][cols], strides in elements, with a 128-byte-swizzled box of 64 x box1 x 1; out of bounds
-// reads as zero.
+// fp16 or bf16 [n2][n1][cols], strides in elements, with a 128-byte-swizzled box of 64 x box1 x box2; out of
+// bounds reads as zero.
 bool encode_3d16_tmap(CUtensorMap *map, const void *base, uint64_t cols, uint64_t n1, uint64_t n2, uint64_t stride1,
-                      uint64_t stride2, uint32_t box1, bool bf16) {
+                      uint64_t stride2, uint32_t box1, uint32_t box2, bool bf16) {
     if (!load_encoder()) return false;
     if (n1 == 0 || n2 == 0 || stride1 % 8 || stride2 % 8 || (reinterpret_cast<uintptr_t>(base) & 15u)) return false;
     cuuint64_t dims[3] = {cols, n1, n2};
     cuuint64_t strides[2] = {stride1 * 2, stride2 * 2};
-    cuuint32_t box[3] = {64, box1, 1};
+    cuuint32_t box[3] = {64, box1, box2};
     cuuint32_t estr[3] = {1, 1, 1};
     const CUresult r = g_encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
                                 const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
