@@ -134,6 +134,7 @@ __global__ void __launch_bounds__(128, Dec<D, FMT, NT>::CTAS) k_attn_decode(cons
         int64_t *scan = reinterpret_cast<int64_t *>(smem);       // before the ring is used
         const uint32_t per = (p.n_seq + 127) / 128, a = min(p.n_seq, tid * per), b = min(p.n_seq, a + per);
         int64_t mine = 0;
+#pragma unroll 8
         for (uint32_t i = a; i < b; ++i) mine += seq_of(C::TT, 16, p, i, blockIdx.x == 0).tiles;
         mine *= units_per_seq;
         int64_t sum = mine;

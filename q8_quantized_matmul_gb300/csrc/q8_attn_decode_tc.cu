@@ -129,6 +129,7 @@ __global__ void __launch_bounds__(Dt<D>::THREADS, 1)
     {
         const uint32_t per = (p.n_seq + C::THREADS - 1) / C::THREADS, a = min(p.n_seq, tid * per), b = min(p.n_seq, a + per);
         int64_t mine = 0;
+#pragma unroll 8
         for (uint32_t i = a; i < b; ++i) mine += seq_of(C::TT, box, p, i, blockIdx.x == 0).tiles;
         mine *= units_per_seq;
         int64_t sum = mine;

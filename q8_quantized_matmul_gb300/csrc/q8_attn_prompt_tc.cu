@@ -71,24 +71,39 @@ __global__ void __launch_bounds__(LIST_THREADS) k_attn_prompt_list(const AttnPro
     bin[tid] = 0;
     __syncthreads();
     PromptTile *list = reinterpret_cast<PromptTile *>(p.list + 1);
-    auto each = [&](auto f) {   // a warp per sequence, a lane per tile
-        for (uint32_t s = warp; s < p.n_seq; s += LIST_THREADS / 32) {
-            const int4 raw = make_int4(p.q_start[s], p.q_start[s + 1], ks[s], ks[s + 1]);
-            const int qa = prompt_bound(raw.x, p.n_q), qe = prompt_bound(raw.y, p.n_q);
-            const int ka = prompt_bound(raw.z, p.n_k), ke = prompt_bound(raw.w, p.n_k);
-            const bool bad = qe < qa || ke < ka || qa != raw.x || qe != raw.y || ka != raw.z || ke != raw.w;
-            PromptTile w;
-            w.q0 = qa;
-            w.k0 = ka;
-            w.lk = max(ke - ka, 0);
-            w.shift = w.lk - (qe - qa);
-            for (int64_t r = (int64_t)lane * p.tile_tokens; r < qe - qa; r += 32 * (int64_t)p.tile_tokens) {
-                w.row0 = (int)r;
-                w.rows = min(p.tile_tokens, qe - qa - w.row0);
-                const int c = tile_cost(w, p.window) >> p.list_shift;
-                f(w, LIST_BINS - 1 - min(c, LIST_BINS - 1));   // longest in the first bin
+    auto each = [&](auto f) {   // a lane per sequence; the warp together for long ones, a lane per tile
+        const uint32_t per = min(32u, (p.n_seq + 31) / 32);   // sequences of a warp: few ones are spread over the warps
+        for (uint32_t s0 = warp * per; s0 < p.n_seq; s0 += 32 * per) {
+            const uint32_t s = s0 + lane;
+            int qa = 0, qe = 0, ka = 0, ke = 0;
+            if (lane < per && s < p.n_seq) {
+                const int4 raw = make_int4(p.q_start[s], p.q_start[s + 1], ks[s], ks[s + 1]);
+                qa = prompt_bound(raw.x, p.n_q);
+                qe = prompt_bound(raw.y, p.n_q);
+                ka = prompt_bound(raw.z, p.n_k);
+                ke = prompt_bound(raw.w, p.n_k);
+                if (qe < qa || ke < ka || qa != raw.x || qe != raw.y || ka != raw.z || ke != raw.w) raise_error(p.err, DEV_ERANGE);
             }
-            if (bad && lane == 0) raise_error(p.err, DEV_ERANGE);
+            auto tiles = [&](int a, int e, int k0, int k1, int64_t from, int64_t by) {
+                PromptTile w;
+                w.q0 = a;
+                w.k0 = k0;
+                w.lk = max(k1 - k0, 0);
+                w.shift = w.lk - (e - a);
+                for (int64_t r = from * p.tile_tokens; r < e - a; r += by * p.tile_tokens) {
+                    w.row0 = (int)r;
+                    w.rows = min(p.tile_tokens, e - a - w.row0);
+                    const int c = tile_cost(w, p.window) >> p.list_shift;
+                    f(w, LIST_BINS - 1 - min(c, LIST_BINS - 1));   // longest in the first bin
+                }
+            };
+            const bool alone = qe - qa <= 4 * p.tile_tokens;
+            if (alone) tiles(qa, qe, ka, ke, 0, 1);
+            for (uint32_t rest = __ballot_sync(0xffffffffu, !alone); rest; rest &= rest - 1) {
+                const int src = __ffs(rest) - 1;
+                tiles(__shfl_sync(0xffffffffu, qa, src), __shfl_sync(0xffffffffu, qe, src), __shfl_sync(0xffffffffu, ka, src),
+                      __shfl_sync(0xffffffffu, ke, src), lane, 32);
+            }
         }
     };
     each([&](const PromptTile &, int b) { atomicAdd(&bin[b], 1); });

@@ -210,6 +210,42 @@ def test_decode_bad_pages_and_lengths(q8):
     assert torch.all(o[0] == 0) and torch.equal(o[1], good[1]) and q8.q8_last_error() == q8.Q8_ERANGE
 
 
+@pytest.mark.parametrize("heads,kv,dim", [(8, 2, 128), (24, 1, 512)])
+def test_decode_beyond_four_gigabytes(q8, heads, kv, dim):
+    """Pages whose offsets pass 32 bits, by decode, append and the page copies."""
+    page, n = 64, 150
+    page_bytes = q8.q8_kv_page_bytes(q8.Q8_TYPE_F16, page, kv, dim)
+    n_pages = (5 << 30) // page_bytes
+    cache = q8.KVCache(*(torch.empty((1, n_pages, page_bytes), dtype=torch.uint8, device=DEV) for _ in range(2)),
+                       q8.Q8_TYPE_F16, page, kv, dim)
+    table = torch.tensor([[n_pages - 1, n_pages - 7, n_pages - 2]], dtype=torch.int32, device=DEV)
+    small = q8.KVCache.empty(q8.Q8_TYPE_F16, 1, 3, page, kv, dim)
+    near = torch.tensor([[2, 0, 1]], dtype=torch.int32, device=DEV)
+    q, k, v = (torch.randn(n, h, dim, device=DEV) for h in (heads, kv, kv))
+    pos = torch.arange(n, dtype=torch.int32, device=DEV)
+    for c, t in ((cache, table), (small, near)):
+        q16 = q8.kv_append(c, 0, q, k, v, pos, torch.zeros_like(pos), t)
+    lens = torch.tensor([n], dtype=torch.int32, device=DEV)
+    ref = q8.attn_decode(q16[-1:], small, 0, near, lens)
+    assert torch.equal(q8.attn_decode(q16[-1:], cache, 0, table, lens), ref)
+    moved = torch.tensor([[n_pages - 20, n_pages - 30, n_pages - 9]], dtype=torch.int32, device=DEV)
+    q8.kv_copy(cache, table[0], moved[0])
+    assert torch.equal(q8.attn_decode(q16[-1:], cache, 0, moved, lens), ref) and q8.q8_last_error() == 0
+
+
+def test_decode_thousands_of_sequences(q8):
+    """Rows of many short sequences against the same rows one call each."""
+    rng = np.random.default_rng(9)
+    lens = [int(x) for x in rng.integers(0, 20, 3000)]
+    pool = Pool(q8, "bf16", lens, 1, 64, 16, 9)
+    q = torch.randn(3000, 2, 64, device=DEV).bfloat16()
+    o = q8.attn_decode(q, pool.cache, 0, pool.table, pool.lens_t)
+    for i in (0, 1, 17, 1500, 2998, 2999):
+        one = q8.attn_decode(q[i:i + 1], pool.cache, 0, pool.table[i:i + 1], pool.lens_t[i:i + 1])
+        assert torch.equal(one[0], o[i])
+    assert q8.q8_last_error() == 0
+
+
 def test_decode_in_a_graph_and_on_a_stream(q8):
     pool = Pool(q8, "bf16", [300, 64, 0, 17], 2, 128, 32, 4)
     q = torch.randn(4, 8, 128, device=DEV).bfloat16()
@@ -383,6 +419,24 @@ def test_prompt_more_tiles_than_sms(q8, dim):
     lens = [int(x) for x in rng.integers(0, 300, 90)]
     keys = [n + int(e) for n, e in zip(lens, rng.integers(-40, 60, 90).clip(min=[-n for n in lens]))]
     check_prompt(q8, "bf16", lens, keys, heads=2, kv=1, dim=dim, seed=dim, window=200, sinks=True)
+
+
+def test_prompt_thousands_of_sequences(q8):
+    """Many sequences, one of them long, against the same sequences in calls of their own."""
+    rng = np.random.default_rng(3)
+    lens = rng.integers(0, 6, 2500)
+    lens[1234] = 2000
+    start = np.concatenate([[0], np.cumsum(lens)])
+    n = int(start[-1])
+    q, k, v = (torch.randn(n, h, 64, device=DEV).half() for h in (4, 2, 2))
+    st = torch.tensor(start, dtype=torch.int32, device=DEV)
+    o = q8.attn_prompt(q, k, v, st)
+    for s in (0, 5, 1234, 2400, 2499):
+        a, b = int(start[s]), int(start[s + 1])
+        if a < b:
+            one = q8.attn_prompt(q[a:b], k[a:b], v[a:b], torch.tensor([0, b - a], dtype=torch.int32, device=DEV))
+            assert (one.float() - o[a:b].float()).abs().max() <= 2.0 ** -9 * 5     # |v| < 5, weights rounded to 2^-11
+    assert q8.q8_last_error() == 0
 
 
 def test_prompt_growing_scores(q8):
