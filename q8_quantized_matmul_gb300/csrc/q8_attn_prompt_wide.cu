@@ -95,7 +95,12 @@ __global__ void __launch_bounds__(Pw<D>::THREADS, 1)
     const uint32_t group = p.n_heads / p.n_kv;
     const uint32_t n_items = p.list ? (uint32_t)min((uint64_t)*reinterpret_cast<const uint32_t *>(p.list) * per_tile, (uint64_t)0xffff0000u)
                                     : (one ? blockIdx.x + 1 : 0);
-    const uint32_t step = p.list ? gridDim.x : 0x40000000u;
+    // Every second round of the list is dealt out backwards: the longest of one round goes with the shortest of
+    // the next (4096 tokens, 32 heads of 128: 132 -> 111 us).
+    auto item_of = [&](uint32_t round) {
+        if (!p.list) return round ? 0xffffffffu : (uint32_t)blockIdx.x;
+        return round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : (uint32_t)blockIdx.x);
+    };
     auto load_item = [&](uint32_t id) { return p.list ? p.list[1 + id / per_tile] : w_one; };
     // key tiles [n0, n1) that the rows see
     auto range = [&](const PromptTile &w, int &n0, int &n1) {
@@ -127,7 +132,7 @@ __global__ void __launch_bounds__(Pw<D>::THREADS, 1)
                 __syncwarp();
             }
         };
-        for (uint32_t id = blockIdx.x; id < n_items; id += step) {
+        for (uint32_t round = 0, id; (id = item_of(round)) < n_items; ++round) {
             const PromptTile w = load_item(id);
             int n0, n1;
             range(w, n0, n1);
@@ -189,7 +194,7 @@ __global__ void __launch_bounds__(Pw<D>::THREADS, 1)
                 __syncwarp();
             }
         };
-        for (uint32_t id = blockIdx.x; id < n_items; id += step) {
+        for (uint32_t round = 0, id; (id = item_of(round)) < n_items; ++round) {
             const PromptTile w = load_item(id);
             int n0, n1;
             range(w, n0, n1);
@@ -247,7 +252,7 @@ __global__ void __launch_bounds__(Pw<D>::THREADS, 1)
                 if (ok && lane == 0) mbar_arrive(&ready[st]);
             }
         };
-        for (uint32_t id = blockIdx.x; id < n_items; id += step, ++item) {
+        for (uint32_t round = 0, id; (id = item_of(round)) < n_items; ++round, ++item) {
             const PromptTile w = load_item(id);
             int n0, n1;
             range(w, n0, n1);
@@ -268,7 +273,7 @@ __global__ void __launch_bounds__(Pw<D>::THREADS, 1)
         // P V of key tile t has ended.  The one two before it had when S of tile t was complete, so the parity
         // tells the two apart.
         auto p_v_done = [&](uint32_t t) { mbar_wait(&odone[t & 1], (t >> 1) & 1, p.err, &abort_flag, lim); };
-        for (uint32_t id = blockIdx.x; id < n_items; id += step, ++item) {
+        for (uint32_t round = 0, id; (id = item_of(round)) < n_items; ++round, ++item) {
             int last, first, w_last, w_first, n0, n1;
             {
                 const PromptTile w = load_item(id);
