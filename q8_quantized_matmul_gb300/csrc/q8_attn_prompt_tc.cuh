@@ -28,6 +28,7 @@ __device__ __forceinline__ void row_mask(uint32_t (&v)[128], int lo, int hi) {
         const int h = hi + 1 - 32 * b, g = lo - 32 * b;
         const uint32_t below = h >= 32 ? 0xffffffffu : (h <= 0 ? 0u : (1u << h) - 1u);
         const uint32_t seen = g <= 0 ? below : (g >= 32 ? 0u : below & (0xffffffffu << g));
+        if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;   // most words of an edge tile are whole
 #pragma unroll
         for (int c = 0; c < 32; ++c)
             if (!(seen & (1u << c))) v[32 * b + c] = 0xff800000u;
@@ -107,6 +108,19 @@ __device__ __forceinline__ void store_row32(const AttnPromptParams &p, uint64_t 
             const int b = d != 0.0f ? (int)roundf(__fdiv_rn(y[2 * i + 1], d)) : 0;
             dst[1 + i] = (uint16_t)((a & 0xff) | (b & 0xff) << 8);
         }
+    } else if (p.out_type != Q8_TYPE_F32 && (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0) {
+        // a thread's row leaves in whole 32-byte sectors
+        const bool bf = p.out_type == Q8_TYPE_BF16;
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] = bf ? pack16<true>(y[2 * i], y[2 * i + 1]) : pack16<false>(y[2 * i], y[2 * i + 1]);
+        uint16_t *dst = static_cast<uint16_t *>(p.out) + i0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst + 16 * i), "r"(w[8 * i]), "r"(w[8 * i + 1]),
+                         "r"(w[8 * i + 2]), "r"(w[8 * i + 3]), "r"(w[8 * i + 4]), "r"(w[8 * i + 5]), "r"(w[8 * i + 6]),
+                         "r"(w[8 * i + 7])
+                         : "memory");
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
