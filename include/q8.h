@@ -35,7 +35,9 @@
  *   - Results are deterministic: the same inputs give the same bits on every
  *     run (fixed reduction order, no floating-point atomics).
  *   - The library keeps a per-device grow-only scratch buffer for quantised
- *     activations and routing tables (the pages' reused aligned Q8 scratch).
+ *     activations, routing tables and the pieces of split attention (the
+ *     pages' reused aligned Q8 scratch).  Growing it allocates: make a first
+ *     call of each size before a stream capture.
  *     Calls that use scratch must not run concurrently on different streams
  *     of the same device.  q8_release() frees it.
  *   - Kernels are launched with programmatic stream serialisation: a kernel
