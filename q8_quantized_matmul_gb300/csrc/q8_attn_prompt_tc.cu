@@ -485,8 +485,8 @@ cudaError_t launch_attn_prompt(AttnPromptParams p, void *list, int num_sms, cuda
         if (e != cudaSuccess) return e;
     }
     if (p.dim > 128) return launch_attn_prompt_wide(p, num_sms, st);
+    if (p.dim == 64) return launch_attn_prompt_64(p, num_sms, st);
     const bool bf = p.type == Q8_TYPE_BF16;
-    if (p.dim == 64) return bf ? launch_tc<64, true>(p, num_sms, st) : launch_tc<64, false>(p, num_sms, st);
     return bf ? launch_tc<128, true>(p, num_sms, st) : launch_tc<128, false>(p, num_sms, st);
 }
 

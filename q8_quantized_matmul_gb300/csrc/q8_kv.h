@@ -153,6 +153,7 @@ inline int attn_prompt_pack(uint32_t group, uint32_t n_kv, uint32_t dim, uint64_
 void attn_prompt_tiling(AttnPromptParams &p, int num_sms);
 size_t attn_prompt_list_bytes(const AttnPromptParams &p, int num_sms);
 cudaError_t launch_attn_prompt(AttnPromptParams p, void *list, int num_sms, cudaStream_t st);
+cudaError_t launch_attn_prompt_64(const AttnPromptParams &p, int num_sms, cudaStream_t st);
 cudaError_t launch_attn_prompt_wide(const AttnPromptParams &p, int num_sms, cudaStream_t st);
 
 // Launch with programmatic stream serialisation: the kernel starts while the one before
