@@ -19,9 +19,6 @@ struct alignas(8) PromptTile {
         const int64_t f = window ? (int64_t)last(r) - window + 1 : 0;
         return f > 0 ? (int)f : 0;
     }
-    __device__ __forceinline__ bool sees(int r, int key, uint32_t window) const {
-        return key <= last(r) && key >= first(r, window);
-    }
     // Keys [key, key + n) that not every row of the tile sees.
     __device__ __forceinline__ bool masked(int key, int n, uint32_t window) const {
         return key + n - 1 > last(0) || key < first(rows - 1, window);
