@@ -1290,12 +1290,14 @@ int q8_attn_decode(void *out, int out_type, float *lse, const void *q, uint64_t 
         return status_of(q8::launch_attn_decode_tc(p, s->num_sms, st));
     }
     const int grid = q8::attn_decode_grid(c->head_dim, p.group, c->type, s->num_sms);
-    if ((rc = reserve_counters(s, (size_t)n_seq * c->n_kv_heads * p.mtiles, st))) return rc;
-    const size_t part = align256((size_t)grid * 2 * 16 * c->head_dim * sizeof(float));
-    if ((rc = reserve_scratch(s, part + align256((size_t)grid * 2 * 16 * 2 * sizeof(float2))))) return rc;
+    const size_t slots = (size_t)grid * 2;
+    if ((rc = reserve_counters(s, (size_t)n_seq * c->n_kv_heads * p.mtiles + slots, st))) return rc;
+    const size_t part = align256(slots * 16 * c->head_dim * sizeof(float)), ml = align256(slots * 16 * 2 * sizeof(float2));
+    if ((rc = reserve_scratch(s, part + 2 * ml))) return rc;
     Carver cv(s->scratch);
     p.part = cv.take<float>(part);
-    p.part_ml = cv.take<float2>((size_t)grid * 2 * 16 * 2 * sizeof(float2));
+    p.part_ml = cv.take<float2>(ml);
+    p.group_ml = cv.take<float2>(ml);
     p.counters = s->counters;
     return status_of(q8::launch_attn_decode(p, grid, st));
 }

@@ -13,7 +13,8 @@
 // movmatrix.  The units' positions, in tiles of TT, form one line that is cut into equal shares, one per
 // CTA, so the lengths do not matter to the balance.  A CTA that covers a whole unit writes its result;
 // otherwise it leaves (m, l, O) in scratch, and the last CTA of a unit to arrive (one counter per unit, set
-// back to zero by it) joins the pieces in their order: the same bits on every run.
+// back to zero by it) joins the pieces in their order: the same bits on every run.  A unit of many pieces is
+// joined in two steps of up to GROUP pieces, so that no CTA reads hundreds of them one round after another.
 //
 // Inside a CTA each of the four warps takes its own 16 (Q8_0: 32) positions of a tile through its own
 // ring of stages, filled by 16-byte asynchronous copies, and keeps its own (m, l, O): no CTA barrier
@@ -36,6 +37,11 @@ namespace q8 {
 namespace {
 
 // FMT 0: f16, 1: bf16, 2: Q8_0 with f16 q, 3: Q8_0 with bf16 q; NT tiles of 8 heads a unit
+constexpr int GROUP = 16;                                // pieces that one CTA joins
+// When no sequence has more tiles than this, CTAs take whole units: the join costs about 2 us, as much as these tiles one
+// after another.
+constexpr int SHORT = 5;
+
 template <int D, int FMT, int NT> struct Dec {
     static constexpr bool Q8 = FMT >= 2, BF16 = FMT & 1;
     static constexpr int HR = 8 * NT;                    // heads of a unit
@@ -53,7 +59,7 @@ template <int D, int FMT, int NT> struct Dec {
     static constexpr int QS = QREG ? 0 : D / 16 * NT * 256;   // q fragments, [k step][head tile][lane] of 8 bytes
     static constexpr int MERGE = HR * DV * 4;            // a warp's O at the end of a share
     static constexpr int RING = NST * STAGE > MERGE ? NST * STAGE : MERGE;
-    static constexpr int SMEM = W * RING + QS + W * HR * 8 + 64;
+    static constexpr int SMEM = W * RING + QS + W * HR * 8 + 64 + 64;
     static constexpr int FIT = 224 * 1024 / SMEM;
     static constexpr int CTAS = FIT < 1 ? 1 : (D == 64 ? (FIT < 4 ? FIT : 4) : (D == 128 ? (FIT < 3 ? FIT : 3) : 1));
     static constexpr float BIAS = Q8 ? 15.0f : 0.0f;     // weights are 2^(z - M + BIAS)
@@ -118,6 +124,7 @@ __global__ void __launch_bounds__(128, Dec<D, FMT, NT>::CTAS) k_attn_decode(cons
     uint8_t *qs = smem + C::W * C::RING;
     float2 *ml = reinterpret_cast<float2 *>(qs + C::QS);        // [warp][HR]
     int *sh = reinterpret_cast<int *>(ml + C::W * C::HR);          // small shared words
+    float *sink = reinterpret_cast<float *>(sh + 16);               // the unit's heads' sinks, in log2 units
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, c = lane & 3;
     const int half = warp % C::NDH, slice = warp / C::NDH;
@@ -130,12 +137,23 @@ __global__ void __launch_bounds__(128, Dec<D, FMT, NT>::CTAS) k_attn_decode(cons
     int64_t total, t0, t1;
     uint32_t s, shares;
     int64_t s_base;                                              // first tile of sequence s on the line
+    bool by_unit;
+    // a unit's length on the line
+    auto on_line = [&](const Seq &q) { return by_unit ? min(q.tiles, 1) : q.tiles; };
     {
         int64_t *scan = reinterpret_cast<int64_t *>(smem);       // before the ring is used
         const uint32_t per = (p.n_seq + 127) / 128, a = min(p.n_seq, tid * per), b = min(p.n_seq, a + per);
         int64_t mine = 0;
+        int seen = 0, most = 0;                                  // sequences with tiles, the most tiles
 #pragma unroll 8
-        for (uint32_t i = a; i < b; ++i) mine += seq_of(C::TT, 16, p, i, blockIdx.x == 0).tiles;
+        for (uint32_t i = a; i < b; ++i) {
+            const int n = seq_of(C::TT, 16, p, i, blockIdx.x == 0).tiles;
+            mine += n;
+            seen += n > 0;
+            most = max(most, n);
+        }
+        by_unit = !__syncthreads_or(most > SHORT);
+        if (by_unit) mine = seen;
         mine *= units_per_seq;
         int64_t sum = mine;
 #pragma unroll
@@ -162,7 +180,7 @@ __global__ void __launch_bounds__(128, Dec<D, FMT, NT>::CTAS) k_attn_decode(cons
         if (t0 < t1 && before <= t0 && t0 < before + mine) {
             uint32_t i = a;
             for (;; ++i) {
-                const int64_t n = (int64_t)seq_of(C::TT, 16, p, i, false).tiles * units_per_seq;
+                const int64_t n = (int64_t)on_line(seq_of(C::TT, 16, p, i, false)) * units_per_seq;
                 if (t0 < before + n) break;
                 before += n;
             }
@@ -181,23 +199,27 @@ __global__ void __launch_bounds__(128, Dec<D, FMT, NT>::CTAS) k_attn_decode(cons
         for (uint32_t i = tid; i < (p.n_heads * (D / 8) + 31) / 32 * 32; i += 128) {
             float o[8] = {};
             const bool act = i < p.n_heads * (D / 8);
-            finish8(p, e, act ? i / (D / 8) : 0, i % (D / 8) * 8, -INFINITY, 0.0f, o, act);
+            const uint32_t head = act ? i / (D / 8) : 0;
+            finish8(p, e, head, i % (D / 8) * 8, sink_of(p, head, act), -INFINITY, 0.0f, o, act);
         }
     }
 
     bool first = true;
     for (int64_t tile = t0; tile < t1; first = false) {
         Seq q = seq_of(C::TT, 16, p, s, false);
-        while (tile >= s_base + (int64_t)q.tiles * units_per_seq) {
-            s_base += (int64_t)q.tiles * units_per_seq;
+        while (tile >= s_base + (int64_t)on_line(q) * units_per_seq) {
+            s_base += (int64_t)on_line(q) * units_per_seq;
             q = seq_of(C::TT, 16, p, ++s, false);
         }
-        const uint32_t unit = (uint32_t)((tile - s_base) / q.tiles);
-        const int64_t u0 = s_base + (int64_t)unit * q.tiles;     // the unit's tiles on the line
-        const int ta = (int)(tile - u0), tb = (int)min((int64_t)q.tiles, t1 - u0);
+        const int len = on_line(q);
+        const uint32_t unit = (uint32_t)((tile - s_base) / len);
+        const int64_t u0 = s_base + (int64_t)unit * len, u1 = u0 + len;   // the unit on the line
+        const int ta = by_unit ? 0 : (int)(tile - u0), tb = by_unit ? q.tiles : (int)min((int64_t)len, t1 - u0);
         const uint32_t kvh = unit / p.mtiles, mt = unit % p.mtiles;
         const uint32_t head0 = kvh * p.group + mt * C::HR;
         const int rows = (int)min((uint32_t)C::HR, p.group - mt * C::HR);
+
+        if (p.sinks && tid < rows) sink[tid] = p.sinks[head0 + tid] * 1.4426950408889634f;   // read after the next barrier
 
         // ---- q fragments
         const uint16_t *qrow = static_cast<const uint16_t *>(p.q) + (uint64_t)s * p.q_stride + (uint64_t)head0 * D;
@@ -216,7 +238,8 @@ __global__ void __launch_bounds__(128, Dec<D, FMT, NT>::CTAS) k_attn_decode(cons
 #pragma unroll
                 for (int t = 0; t < NT; ++t) qfrag(ks, t, qr[ks][t]);
         } else {
-            for (int i = warp; i < D / 16 * NT; i += C::W) {
+#pragma unroll 8
+            for (int i = warp; i < D / 16 * NT; i += C::W) {     // eight fragments' loads in flight
                 uint32_t f[2];
                 qfrag(i / NT, i % NT, f);
                 reinterpret_cast<uint2 *>(qs)[i * 32 + lane] = make_uint2(f[0], f[1]);
@@ -563,7 +586,7 @@ __global__ void __launch_bounds__(128, Dec<D, FMT, NT>::CTAS) k_attn_decode(cons
                 for (int e = 0; e < 8; ++e) y[e] += v[e] * f;
             }
             if (whole) {
-                finish8(p, s, head0 + row, d0, mt - C::BIAS, lt, y, act);
+                finish8(p, s, head0 + row, d0, sink[row], mt - C::BIAS, lt, y, act);
             } else if (act) {
                 float4 *dst = reinterpret_cast<float4 *>(p.part + (slot * 16 + row) * D + d0);
                 dst[0] = make_float4(y[0], y[1], y[2], y[3]);
@@ -574,7 +597,6 @@ __global__ void __launch_bounds__(128, Dec<D, FMT, NT>::CTAS) k_attn_decode(cons
         }
         if (!whole) {
             // pieces of the unit: CTAs c0 .. c1 of the line
-            const int64_t u1 = u0 + q.tiles;
             auto cta_of = [&](int64_t x) {                       // the CTA whose share holds tile x
                 int64_t k = x * shares / total;
                 while (total * (k + 1) / shares <= x) ++k;
@@ -582,73 +604,58 @@ __global__ void __launch_bounds__(128, Dec<D, FMT, NT>::CTAS) k_attn_decode(cons
                 return k;
             };
             const int64_t c0 = cta_of(u0), c1 = cta_of(u1 - 1);
-            const uint64_t id = (uint64_t)s * units_per_seq + unit;
-            __syncthreads();
-            if (tid == 0) {
-                __threadfence();                                 // the whole CTA's piece before its arrival
-                sh[0] = atomicAdd(p.counters + id, 1) == (int)(c1 - c0);
-                __threadfence();
-            }
-            __syncthreads();
-            if (sh[0]) {                                         // the last piece: join them in order
-                const int n_part = (int)(c1 - c0) + 1;
-                // the first piece is its CTA's second share when that CTA began with another unit
-                const uint64_t first_slot = 2 * (uint64_t)c0 + (total * c0 / shares == u0 ? 0 : 1);
-                auto slot_of = [&](int k) { return k == 0 ? first_slot : 2 * (uint64_t)(c0 + k); };
-                // maximum and sum of each row (and half of its dims), a warp a row
-                for (int pr = warp; pr < rows * C::NDH; pr += C::W) {
-                    const int row = pr / C::NDH, h = pr % C::NDH;
-                    float mt = -INFINITY, lt = 0.0f;
-                    for (int k = lane; k < n_part; k += 32) mt = fmaxf(mt, __ldcg(&p.part_ml[(slot_of(k) * 16 + row) * 2 + h].x));
-#pragma unroll
-                    for (int x = 1; x < 32; x <<= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, x));
-                    for (int k = lane; k < n_part; k += 32) {
-                        const float2 v = __ldcg(&p.part_ml[(slot_of(k) * 16 + row) * 2 + h]);
-                        lt += v.x == -INFINITY ? 0.0f : v.y * ex2(v.x - mt);
-                    }
-#pragma unroll
-                    for (int x = 1; x < 32; x <<= 1) lt += __shfl_xor_sync(0xffffffffu, lt, x);
-                    if (lane == 0) ml[pr] = make_float2(mt, lt);
+            const int n_part = (int)(c1 - c0) + 1;
+            // the first piece is its CTA's second share when that CTA began with another unit
+            const uint64_t first_slot = 2 * (uint64_t)c0 + (total * c0 / shares == u0 ? 0 : 1);
+            auto slot_of = [&](int k) { return k == 0 ? first_slot : 2 * (uint64_t)(c0 + k); };
+            // Up to GROUP pieces are joined by the last CTA to arrive.  Of more, each GROUP in a row are joined by the
+            // last of them, in the place of the first, and the groups by the last of those.
+            const int k_own = (int)(blockIdx.x - c0), k_first = n_part > GROUP ? k_own / GROUP * GROUP : 0;
+            const int n_own = min(GROUP, n_part - k_first);
+            // whether this CTA is the last of n to arrive; the counter is then zero again
+            auto last_of = [&](int *counter, int n) {
+                __syncthreads();                                 // the whole CTA's piece before its arrival
+                if (tid == 0) {
+                    __threadfence();
+                    sh[0] = atomicAdd(counter, 1) == n - 1;
+                    if (sh[0]) *counter = 0;
+                    __threadfence();
                 }
                 __syncthreads();
+                return sh[0] != 0;
+            };
+            int *const unit_counter = p.counters + (uint64_t)s * units_per_seq + unit;
+            int *const group_counter = p.counters + (uint64_t)p.n_seq * units_per_seq + slot_of(k_first);
+            // pieces k0, k0 + step, .. (n of them): the result, or one piece in the place of the first
+            auto join = [&](int k0, int step, int n, const float2 *from, bool result) {
                 for (int i = tid; i < (items + 31) / 32 * 32; i += 128) {
                     const bool act = i < items;
                     const int row = act ? i / (D / 8) : 0, d0 = i % (D / 8) * 8, h = d0 / C::DV;
-                    const float2 t = ml[row * C::NDH + h];
-                    float y[8] = {};
-                    for (int k0 = 0; k0 < n_part; k0 += 8) {     // eight pieces' loads in flight
-                        float f[8];
-                        float4 va[8], vb[8];
-#pragma unroll
-                        for (int u = 0; u < 8; ++u) {
-                            const bool ok = k0 + u < n_part;
-                            const uint64_t sl = slot_of(ok ? k0 + u : k0);
-                            const float mk = __ldcg(&p.part_ml[(sl * 16 + row) * 2 + h].x);
-                            const float4 *src = reinterpret_cast<const float4 *>(p.part + (sl * 16 + row) * D + d0);
-                            va[u] = __ldcg(src);
-                            vb[u] = __ldcg(src + 1);
-                            f[u] = ok && mk != -INFINITY ? ex2(mk - t.x) : 0.0f;
-                        }
-#pragma unroll
-                        for (int u = 0; u < 8; ++u) {
-                            if (f[u] == 0.0f) continue;          // nothing seen there (or beyond the last piece)
-                            y[0] += va[u].x * f[u];
-                            y[1] += va[u].y * f[u];
-                            y[2] += va[u].z * f[u];
-                            y[3] += va[u].w * f[u];
-                            y[4] += vb[u].x * f[u];
-                            y[5] += vb[u].y * f[u];
-                            y[6] += vb[u].z * f[u];
-                            y[7] += vb[u].w * f[u];
-                        }
+                    float mj, lj, y[8];
+                    join8(n, [&](int k) { return p.part + (slot_of(k0 + k * step) * 16 + row) * D + d0; },
+                          [&](int k) { return from + (slot_of(k0 + k * step) * 16 + row) * 2 + h; }, mj, lj, y);
+                    if (result) {
+                        finish8(p, s, head0 + row, d0, sink[row], mj - C::BIAS, lj, y, act);
+                    } else if (act) {
+                        const uint64_t to = slot_of(k0) * 16 + row;
+                        float4 *dst = reinterpret_cast<float4 *>(p.part + to * D + d0);
+                        dst[0] = make_float4(y[0], y[1], y[2], y[3]);
+                        dst[1] = make_float4(y[4], y[5], y[6], y[7]);
+                        // beside the pieces' own, which other threads still read
+                        if (d0 % C::DV == 0) p.group_ml[to * 2 + h] = make_float2(mj, lj);
                     }
-                    finish8(p, s, head0 + row, d0, t.x - C::BIAS, t.y, y, act);
                 }
-                if (tid == 0) p.counters[id] = 0;
+            };
+            if (n_part <= GROUP) {
+                if (last_of(unit_counter, n_part)) join(0, 1, n_part, p.part_ml, true);
+            } else if (last_of(group_counter, n_own)) {
+                join(k_first, 1, n_own, p.part_ml, false);
+                const int groups = (n_part + GROUP - 1) / GROUP;
+                if (last_of(unit_counter, groups)) join(0, GROUP, groups, p.group_ml, true);
             }
         }
         __syncthreads();   // the rings, ml and sh are free again
-        tile = u0 + tb;
+        tile = min(u1, t1);
     }
 }
 

@@ -518,39 +518,11 @@ template <int D> __global__ void __launch_bounds__(128) k_attn_decode_join(const
     const int d0 = threadIdx.x % TH * 8;
     const int4 un = p.units[((uint64_t)s * p.c.n_kv + kvh) * p.mtiles + mt];
     auto slot_of = [&](int k) { return k == 0 ? (uint64_t)un.x : 2 * (uint64_t)(un.y + k); };
-    // a warp works on one head: a lane a piece for the maximum, then eight pieces' loads in flight
-    const int lane = threadIdx.x & 31;
-    float m = -INFINITY, l = 0.0f, y[8] = {};
-    for (int k = lane; k < un.z; k += 32) m = fmaxf(m, __ldcg(&p.part_ml[slot_of(k) * 64 + row].x));
-#pragma unroll
-    for (int x = 1; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-    for (int k0 = 0; k0 < un.z; k0 += 8) {
-        float4 va[8], vb[8];
-        float2 ml[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint64_t sl = slot_of(min(k0 + i, un.z - 1));
-            ml[i] = __ldcg(&p.part_ml[sl * 64 + row]);
-            const float4 *src = reinterpret_cast<const float4 *>(p.part + (sl * 64 + row) * D + d0);
-            va[i] = __ldcg(src);
-            vb[i] = __ldcg(src + 1);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (k0 + i >= un.z || ml[i].x == -INFINITY) continue;
-            const float f = ex2(ml[i].x - m);
-            l += ml[i].y * f;
-            y[0] += va[i].x * f;
-            y[1] += va[i].y * f;
-            y[2] += va[i].z * f;
-            y[3] += va[i].w * f;
-            y[4] += vb[i].x * f;
-            y[5] += vb[i].y * f;
-            y[6] += vb[i].z * f;
-            y[7] += vb[i].w * f;
-        }
-    }
-    finish8(p, s, head, d0, m, l, y, act);
+    const float sink = sink_of(p, head, act);
+    float m, l, y[8];
+    join8(un.z, [&](int k) { return p.part + (slot_of(k) * 64 + row) * D + d0; },
+          [&](int k) { return p.part_ml + slot_of(k) * 64 + row; }, m, l, y);
+    finish8(p, s, head, d0, sink, m, l, y, act);
 }
 
 template <int D, bool BF16> cudaError_t launch_tc(const AttnDecodeParams &p, int grid, cudaStream_t st) {

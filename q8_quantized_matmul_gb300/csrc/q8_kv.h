@@ -76,8 +76,8 @@ struct AttnDecodeParams {
     uint32_t window;
     const float *sinks;
     float *part;                          // partial outputs, [2 * grid][16][dim]
-    float2 *part_ml;                      // their maxima and sums, [2 * grid][16]
-    int *counters;                        // one per unit, zero between calls
+    float2 *part_ml, *group_ml;           // maxima and sums of pieces and of joined groups, [2 * grid][16][2]
+    int *counters;                        // one per unit and one per slot of a piece, zero between calls
     int *err;
     // tcgen05 kernel: per unit the slot of its first piece, that piece's CTA and the number of pieces;
     // part and part_ml then hold 64 rows a slot
