@@ -193,13 +193,16 @@ __global__ void __launch_bounds__(128, Dec<D, FMT, NT>::CTAS) k_attn_decode(cons
         __syncthreads();
     }
 
-    // ---- sequences with nothing visible: zeros
-    for (uint32_t e = blockIdx.x; e < p.n_seq; e += gridDim.x) {
-        if (seq_of(C::TT, 16, p, e, false).tiles) continue;
-        for (uint32_t i = tid; i < (p.n_heads * (D / 8) + 31) / 32 * 32; i += 128) {
-            float o[8] = {};
-            const bool act = i < p.n_heads * (D / 8);
+    // ---- sequences with nothing visible: zeros, 128 chunks of 8 values a CTA, those without a share first
+    {
+        const uint32_t items = p.n_heads * (D / 8), parts = (items + 127) / 128;
+        const uint32_t from = (blockIdx.x + gridDim.x - shares) % gridDim.x;
+        for (uint64_t w = from; w < (uint64_t)p.n_seq * parts; w += gridDim.x) {
+            const uint32_t e = (uint32_t)(w / parts), i = (uint32_t)(w % parts) * 128 + tid;
+            if (seq_of(C::TT, 16, p, e, false).tiles) continue;
+            const bool act = i < items;
             const uint32_t head = act ? i / (D / 8) : 0;
+            float o[8] = {};
             finish8(p, e, head, i % (D / 8) * 8, sink_of(p, head, act), -INFINITY, 0.0f, o, act);
         }
     }

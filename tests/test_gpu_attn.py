@@ -337,6 +337,31 @@ def test_decode_many_heads_wait_expires(q8):
     assert q8.q8_last_error() == 0
 
 
+@pytest.mark.parametrize("kind,dim,heads,kv", [("f16", 64, 16, 1), ("bf16", 128, 3, 1), ("q8", 128, 4, 2), ("q8", 512, 2, 1)])
+def test_decode_pieces_joined_in_groups(q8, kind, dim, heads, kv):
+    """Few units over all CTAs: their pieces are joined in groups, with sequences of a few tiles and of none beside."""
+    check_decode(q8, kind, [21000, 0, 70, 9001], heads=heads, kv=kv, dim=dim, page=64, seed=dim, sinks=True)
+    check_decode(q8, kind, [30011], heads=heads, kv=kv, dim=dim, page=128, seed=dim + 1, window=25000)
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16", "q8"])
+@pytest.mark.parametrize("dim", [64, 128, 256, 512])
+def test_decode_whole_units(q8, kind, dim):
+    """Short sequences only: CTAs take whole units, more of them than CTAs, empty ones among them."""
+    rng = np.random.default_rng(dim)
+    check_decode(q8, kind, [0, 1, 0, 63, 64, 65, 128, 0], heads=6, kv=2, dim=dim, page=16, seed=1, sinks=True)
+    check_decode(q8, kind, [int(x) * int(x > 3) for x in rng.integers(0, 40, 330)], heads=2, kv=2, dim=dim, page=16, seed=2)
+    check_decode(q8, kind, [0, 0, 0], heads=5, kv=1, dim=dim, page=16, seed=3)
+
+
+@pytest.mark.parametrize("heads", [17, 64])
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+def test_decode_many_heads_little_room(q8, kind, heads):
+    """More than 16 query heads on a key-value head with room for a few positions, or a window of a few."""
+    check_decode(q8, kind, [0, 1, 40, 64], heads=heads, kv=1, dim=512, page=64, seed=heads, sinks=True)
+    check_decode(q8, kind, [300, 0, 64, 1000], heads=heads, kv=1, dim=256, page=32, seed=heads, window=30)
+
+
 # ------------------------------------------------------------------ whole prompts
 def check_prompt(q8, kind, qlens, klens, heads, kv, dim, window=0, sinks=False, seed=0, out=None, poison=True):
     rng = np.random.default_rng(seed)
