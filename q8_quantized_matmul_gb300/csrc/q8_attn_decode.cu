@@ -14,7 +14,7 @@
 // CTA, so the lengths do not matter to the balance.  A CTA that covers a whole unit writes its result;
 // otherwise it leaves (m, l, O) in scratch, and the last CTA of a unit to arrive (one counter per unit, set
 // back to zero by it) joins the pieces in their order: the same bits on every run.  A unit of many pieces is
-// joined in two steps of up to GROUP pieces, so that no CTA reads hundreds of them one round after another.
+// joined in two steps, so that no CTA reads hundreds of them one round after another.
 //
 // Inside a CTA each of the four warps takes its own 16 (Q8_0: 32) positions of a tile through its own
 // ring of stages, filled by 16-byte asynchronous copies, and keeps its own (m, l, O): no CTA barrier
@@ -37,7 +37,9 @@ namespace q8 {
 namespace {
 
 // FMT 0: f16, 1: bf16, 2: Q8_0 with f16 q, 3: Q8_0 with bf16 q; NT tiles of 8 heads a unit
-constexpr int GROUP = 16;                                // pieces that one CTA joins
+// Pieces that one CTA joins at once, and in groups when there are more (24 pieces a unit: in groups 12.1 us, at once 10.7;
+// 30: 12.4 and 13.6; 228: 21 and 68).
+constexpr int AT_ONCE = 24, GROUP = 16;
 // When no sequence has more tiles than this, CTAs take whole units: the join costs about 2 us, as much as these tiles one
 // after another.
 constexpr int SHORT = 5;
@@ -611,9 +613,9 @@ __global__ void __launch_bounds__(128, Dec<D, FMT, NT>::CTAS) k_attn_decode(cons
             // the first piece is its CTA's second share when that CTA began with another unit
             const uint64_t first_slot = 2 * (uint64_t)c0 + (total * c0 / shares == u0 ? 0 : 1);
             auto slot_of = [&](int k) { return k == 0 ? first_slot : 2 * (uint64_t)(c0 + k); };
-            // Up to GROUP pieces are joined by the last CTA to arrive.  Of more, each GROUP in a row are joined by the
+            // Up to AT_ONCE pieces are joined by the last CTA to arrive.  Of more, each GROUP in a row are joined by the
             // last of them, in the place of the first, and the groups by the last of those.
-            const int k_own = (int)(blockIdx.x - c0), k_first = n_part > GROUP ? k_own / GROUP * GROUP : 0;
+            const int k_own = (int)(blockIdx.x - c0), k_first = n_part > AT_ONCE ? k_own / GROUP * GROUP : 0;
             const int n_own = min(GROUP, n_part - k_first);
             // whether this CTA is the last of n to arrive; the counter is then zero again
             auto last_of = [&](int *counter, int n) {
@@ -649,7 +651,7 @@ __global__ void __launch_bounds__(128, Dec<D, FMT, NT>::CTAS) k_attn_decode(cons
                     }
                 }
             };
-            if (n_part <= GROUP) {
+            if (n_part <= AT_ONCE) {
                 if (last_of(unit_counter, n_part)) join(0, 1, n_part, p.part_ml, true);
             } else if (last_of(group_counter, n_own)) {
                 join(k_first, 1, n_own, p.part_ml, false);
