@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(Dt<D>::THREADS, 1)
         // ------------------------------------------------ TMA producer: lane j the j-th piece of a page
         uint32_t fills[C::NST] = {}, q_loads = 0, u = 0, n = 0;
         auto go = [&](uint64_t *bar, uint32_t parity) {
-            return __shfl_sync(0xffffffffu, (int)(!p.withhold && mbar_wait(bar, parity, p.err, &abort_flag, lim) && !abort_flag), 0) != 0;
+            return __shfl_sync(0xffffffffu, (int)(!p.withhold && tile_wait(bar, parity, p.err, &abort_flag, lim) && !abort_flag), 0) != 0;
         };
         for (int64_t at = L.t0; at < L.t1;) {
             const Segment64 g = segment(at, w);
@@ -298,12 +298,12 @@ __global__ void __launch_bounds__(Dt<D>::THREADS, 1)
         uint32_t u = 0, n = 0, q_loads = 0;
         for (int64_t at = L.t0; at < L.t1;) {
             const Segment64 g = segment(at, w);
-            ok = mbar_wait(qfull, q_loads & 1, p.err, &abort_flag, lim) && ok;
+            ok = tile_wait(qfull, q_loads & 1, p.err, &abort_flag, lim) && ok;
             ++q_loads;
             for (int it = g.ta; it < g.tb; ++it, ++n) {
                 for (int j = 0; j < C::KS; ++j, ++u) {
                     const int st = u % C::NST;
-                    ok = mbar_wait(&ready[st], (u / C::NST) & 1, p.err, &abort_flag, lim) && ok;
+                    ok = tile_wait(&ready[st], (u / C::NST) & 1, p.err, &abort_flag, lim) && ok;
                     tc_fence_after();
                     if (elect_one()) {
                         if (ok) {
@@ -321,10 +321,10 @@ __global__ void __launch_bounds__(Dt<D>::THREADS, 1)
                     }
                     __syncwarp();
                 }
-                ok = mbar_wait(pfull, n & 1, p.err, &abort_flag, lim) && ok;
+                ok = tile_wait(pfull, n & 1, p.err, &abort_flag, lim) && ok;
                 for (int j = 0; j < C::KS; ++j, ++u) {
                     const int st = u % C::NST;
-                    ok = mbar_wait(&ready[st], (u / C::NST) & 1, p.err, &abort_flag, lim) && ok;
+                    ok = tile_wait(&ready[st], (u / C::NST) & 1, p.err, &abort_flag, lim) && ok;
                     tc_fence_after();
                     if (elect_one()) {
                         if (ok) {
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(Dt<D>::THREADS, 1)
         }
         if (elect_one()) tc_commit(done);
         __syncwarp();
-        mbar_wait(done, 0, p.err, nullptr);   // the fixed 2 s limit: TMEM is freed after this
+        tile_wait(done, 0, p.err, nullptr);   // the fixed 2 s limit: TMEM is freed after this
     } else if (warp >= 6) {
         // ------------------------------------------------ V guard: two threads a position's row
         const int gt = tid - 192;
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(Dt<D>::THREADS, 1)
             for (int it = g.ta; it < g.tb; ++it, ++n)
                 for (int j = 0; j < 2 * C::KS; ++j, ++u) {
                     const int st = u % C::NST;
-                    const bool ok = mbar_wait(&full[st], (u / C::NST) & 1, p.err, &abort_flag, lim);
+                    const bool ok = tile_wait(&full[st], (u / C::NST) & 1, p.err, &abort_flag, lim);
                     if (ok && j >= C::KS) {
                         const int p0 = g.q.start + it * C::TT;
                         const uint32_t okm = pieces_ok[n & 1], all = (2u << ((128 >> box_shift) - 1)) - 1u;
@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(Dt<D>::THREADS, 1)
             if (tid < 64) sm_m[tid] = -INFINITY;
             named_bar_sync(2, 128);
             for (int it = g.ta; it < g.tb; ++it, ++n) {
-                mbar_wait(sfull, n & 1, p.err, &abort_flag, lim);
+                tile_wait(sfull, n & 1, p.err, &abort_flag, lim);
                 tc_fence_after();
                 const int pos = g.q.start + it * C::TT + r;
                 const bool seen = pos >= g.q.lo && pos < g.q.hi && ((pieces_ok[n & 1] >> (r >> box_shift)) & 1);
@@ -465,7 +465,7 @@ __global__ void __launch_bounds__(Dt<D>::THREADS, 1)
                 if (lane == 0) mbar_arrive(pfull);
             }
             // ---- this share's piece: sums over the positions, O^T as it stands
-            mbar_wait(ofull, o_seen & 1, p.err, &abort_flag, lim);
+            tile_wait(ofull, o_seen & 1, p.err, &abort_flag, lim);
             ++o_seen;
             tc_fence_after();
             reduce64(l, [](float a, float b) { return a + b; });

@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(P64::THREADS, 1)
             // ------------------------------------------------ TMA producer
             uint32_t fills[C::NST] = {}, q_loads = 0, u = 0;
             auto go = [&](uint64_t *bar, uint32_t parity) {
-                return __shfl_sync(0xffffffffu, (int)(!p.withhold && mbar_wait(bar, parity, p.err, &abort_flag, lim) && !abort_flag),
+                return __shfl_sync(0xffffffffu, (int)(!p.withhold && tile_wait(bar, parity, p.err, &abort_flag, lim) && !abort_flag),
                                    0) != 0;
             };
             for (uint32_t round = 0, id; (id = item_of(round)) < n_items; ++round) {
@@ -197,10 +197,10 @@ __global__ void __launch_bounds__(P64::THREADS, 1)
                 const Range r = ranges(w);
                 const int N = r.n1 - r.n0;
                 if (N == 0) continue;
-                ok = mbar_wait(qfull, q_loads & 1, p.err, &abort_flag, lim) && ok;
+                ok = tile_wait(qfull, q_loads & 1, p.err, &abort_flag, lim) && ok;
                 ++q_loads;
                 auto ready_unit = [&](uint32_t u) {
-                    ok = mbar_wait(&ready[u % C::NST], (u / C::NST) & 1, p.err, &abort_flag, lim) && ok;
+                    ok = tile_wait(&ready[u % C::NST], (u / C::NST) & 1, p.err, &abort_flag, lim) && ok;
                 };
                 auto active = [&](int i, int m) { return m + r.n0 >= r.t0[i] && m + r.n0 < r.t1[i]; };
                 // one thread: S of key tile m and query tile i
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(P64::THREADS, 1)
                         // P V of pair 2 m + i; S of the pair three on: the other query tile, key tile m + 1 + i
                         const int ms = m + 1 + i;
                         const bool pv = active(i, m), sc = ms < N && active(1 - i, ms), more = m + r.n0 > r.t0[i];
-                        if (pv) ok = mbar_wait(&pfull[2 * i + (cp[i] & 1)], (cp[i] >> 1) & 1, p.err, &abort_flag, lim) && ok;
+                        if (pv) ok = tile_wait(&pfull[2 * i + (cp[i] & 1)], (cp[i] >> 1) & 1, p.err, &abort_flag, lim) && ok;
                         tc_fence_after();
                         if (elect_one()) {
                             if (pv) {
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(P64::THREADS, 1)
             }
             if (elect_one()) tc_commit(done);
             __syncwarp();
-            mbar_wait(done, 0, p.err, nullptr);   // the fixed 2 s limit: TMEM is freed after this
+            tile_wait(done, 0, p.err, nullptr);   // the fixed 2 s limit: TMEM is freed after this
         } else if (warp >= 10) {
             // ------------------------------------------------ V guard
             const int gt = tid - 320;
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(P64::THREADS, 1)
                 if (r.n1 == r.n0) continue;
                 for (int n = r.n0; n < r.n1 + 2; ++n, ++u) {
                     const int st = u % C::NST;
-                    const bool ok = mbar_wait(&full[st], (u / C::NST) & 1, p.err, &abort_flag, lim);
+                    const bool ok = tile_wait(&full[st], (u / C::NST) & 1, p.err, &abort_flag, lim);
                     if (ok && n >= r.n0 + 2 && w.masked((n - 2) * C::BN, C::BN, p.window)) {
                         uint4 *t = reinterpret_cast<uint4 *>(ring + st * C::STAGE);
 #pragma unroll 4
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(P64::THREADS, 1)
                 float m = -INFINITY, l = 0.0f;
 #pragma unroll 1
                 for (int n = ta; n < tb; ++n) {
-                    mbar_wait(&sfull[i * 2 + (c & 1)], (c >> 1) & 1, p.err, &abort_flag, lim);
+                    tile_wait(&sfull[i * 2 + (c & 1)], (c >> 1) & 1, p.err, &abort_flag, lim);
                     tc_fence_after();
                     uint32_t v[128];
                     tc_ld32(tS, v);
@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(P64::THREADS, 1)
                         l *= f;
                     }
                     if (__any_sync(0xffffffffu, f != 1.0f) && n > ta) {
-                        mbar_wait(&odone[i * 2 + ((c - 1) & 1)], ((c - 1) >> 1) & 1, p.err, &abort_flag, lim);   // P V of the step before
+                        tile_wait(&odone[i * 2 + ((c - 1) & 1)], ((c - 1) >> 1) & 1, p.err, &abort_flag, lim);   // P V of the step before
                         tc_fence_after();
                         row_rescale<C::D>(tO, f);
                     }
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(P64::THREADS, 1)
                     tS = tS >= tmem + lanes + 128 ? tS - 128 : tS + 256;   // two pairs on
                 }
                 // ---- results
-                if (tb > ta) mbar_wait(&odone[i * 2 + ((c - 1) & 1)], ((c - 1) >> 1) & 1, p.err, &abort_flag, lim);
+                if (tb > ta) tile_wait(&odone[i * 2 + ((c - 1) & 1)], ((c - 1) >> 1) & 1, p.err, &abort_flag, lim);
                 tc_fence_after();
                 const PromptTile w = load_item(id);
                 const uint32_t head = id % per_tile * p.pack + me.head, kvh = head / group;

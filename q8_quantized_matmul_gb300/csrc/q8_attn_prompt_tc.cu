@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(Pt::THREADS, 1)
             // ------------------------------------------------ TMA producer
             uint32_t fills[C::NST] = {}, q_loads = 0, u = 0;
             auto go = [&](uint64_t *bar, uint32_t parity) {
-                return __shfl_sync(0xffffffffu, (int)(!p.withhold && mbar_wait(bar, parity, p.err, &abort_flag, lim) && !abort_flag),
+                return __shfl_sync(0xffffffffu, (int)(!p.withhold && tile_wait(bar, parity, p.err, &abort_flag, lim) && !abort_flag),
                                    0) != 0;
             };
             for (uint32_t round = 0, id; (id = item_of(round)) < n_items; ++round) {
@@ -285,17 +285,17 @@ __global__ void __launch_bounds__(Pt::THREADS, 1)
                 const PromptTile w = load_item(id);
                 const Range r = ranges(w);
                 if (r.n1 == r.n0) continue;
-                ok = mbar_wait(qfull, q_loads & 1, p.err, &abort_flag, lim) && ok;
+                ok = tile_wait(qfull, q_loads & 1, p.err, &abort_flag, lim) && ok;
                 ++q_loads;
                 for (int n = r.n0; n <= r.n1; ++n, ++u) {    // P V of key tile n - 1, then S of key tile n
                     const int st = u % C::NST;
                     const uint64_t bv = dv + (uint32_t)st * (C::STAGE / 16), bk = dk + (uint32_t)st * (C::STAGE / 16);
-                    ok = mbar_wait(&ready[st], (u / C::NST) & 1, p.err, &abort_flag, lim) && ok;
+                    ok = tile_wait(&ready[st], (u / C::NST) & 1, p.err, &abort_flag, lim) && ok;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const bool pv = n > r.t0[i] && n <= r.t1[i], sc = n >= r.t0[i] && n < r.t1[i];
                         if (pv) {
-                            ok = mbar_wait(&pfull[i], p_done[i] & 1, p.err, &abort_flag, lim) && ok;
+                            ok = tile_wait(&pfull[i], p_done[i] & 1, p.err, &abort_flag, lim) && ok;
                             ++p_done[i];
                         }
                         tc_fence_after();
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(Pt::THREADS, 1)
             }
             if (elect_one()) tc_commit(done);
             __syncwarp();
-            mbar_wait(done, 0, p.err, nullptr);   // the fixed 2 s limit: TMEM is freed after this
+            tile_wait(done, 0, p.err, nullptr);   // the fixed 2 s limit: TMEM is freed after this
         } else if (warp >= 10) {
             // ------------------------------------------------ V guard
             const int gt = tid - 320;
@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(Pt::THREADS, 1)
                 if (r.n1 == r.n0) continue;
                 for (int n = r.n0; n <= r.n1; ++n, ++u) {
                     const int st = u % C::NST;
-                    const bool ok = mbar_wait(&full[st], (u / C::NST) & 1, p.err, &abort_flag, lim);
+                    const bool ok = tile_wait(&full[st], (u / C::NST) & 1, p.err, &abort_flag, lim);
                     if (ok && n > r.n0 && w.masked((n - 1) * C::BN, C::BN, p.window)) {
                         uint4 *t = reinterpret_cast<uint4 *>(ring + st * C::STAGE);
 #pragma unroll 4
@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(Pt::THREADS, 1)
                 }
                 float m = -INFINITY, l = 0.0f;
                 for (int n = ta; n < tb; ++n) {
-                    mbar_wait(&sfull[i], s_seen & 1, p.err, &abort_flag, lim);
+                    tile_wait(&sfull[i], s_seen & 1, p.err, &abort_flag, lim);
                     ++s_seen;
                     tc_fence_after();
                     uint32_t v[128];
@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(Pt::THREADS, 1)
                 // ---- results
                 const bool has = tb > ta;
                 if (has) {
-                    mbar_wait(&ofull[i], o_seen & 1, p.err, &abort_flag, lim);
+                    tile_wait(&ofull[i], o_seen & 1, p.err, &abort_flag, lim);
                     ++o_seen;
                 }
                 tc_fence_after();

@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(Pw<D>::THREADS, 1)
         // ------------------------------------------------ TMA producer
         uint32_t fills[C::NST] = {}, q_loads = 0, u = 0;
         auto go = [&](uint64_t *bar, uint32_t parity) {
-            return __shfl_sync(0xffffffffu, (int)(!p.withhold && mbar_wait(bar, parity, p.err, &abort_flag, lim) && !abort_flag), 0) != 0;
+            return __shfl_sync(0xffffffffu, (int)(!p.withhold && tile_wait(bar, parity, p.err, &abort_flag, lim) && !abort_flag), 0) != 0;
         };
         auto slots = [&](const CUtensorMap *map, int n_slots, int x, int y) {
             for (int j = 0; j < n_slots; ++j, ++u) {
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(Pw<D>::THREADS, 1)
             const uint32_t tS = tmem + (t & 1) * 128;
             for (int j = 0; j < C::KS; ++j, ++u) {
                 const int st = u % C::NST;
-                ok = mbar_wait(&ready[st], (u / C::NST) & 1, p.err, &abort_flag, lim) && ok;
+                ok = tile_wait(&ready[st], (u / C::NST) & 1, p.err, &abort_flag, lim) && ok;
                 tc_fence_after();
                 if (elect_one()) {
                     if (ok) {
@@ -199,15 +199,15 @@ __global__ void __launch_bounds__(Pw<D>::THREADS, 1)
             int n0, n1;
             range(w, n0, n1);
             if (n1 == n0) continue;
-            ok = mbar_wait(qfull, q_loads & 1, p.err, &abort_flag, lim) && ok;
+            ok = tile_wait(qfull, q_loads & 1, p.err, &abort_flag, lim) && ok;
             ++q_loads;
             scores(nt, n0 + 1 == n1);
             for (int n = n0; n < n1; ++n, ++nt) {
                 if (n + 1 < n1) scores(nt + 1, n + 2 == n1);
-                ok = mbar_wait(&pfull[nt & 1], (nt >> 1) & 1, p.err, &abort_flag, lim) && ok;
+                ok = tile_wait(&pfull[nt & 1], (nt >> 1) & 1, p.err, &abort_flag, lim) && ok;
                 for (int j = 0; j < C::VS; ++j, ++u) {
                     const int st = u % C::NST;
-                    ok = mbar_wait(&ready[st], (u / C::NST) & 1, p.err, &abort_flag, lim) && ok;
+                    ok = tile_wait(&ready[st], (u / C::NST) & 1, p.err, &abort_flag, lim) && ok;
                     tc_fence_after();
                     if (elect_one()) {
                         if (ok) {
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(Pw<D>::THREADS, 1)
         }
         if (elect_one()) tc_commit(done);
         __syncwarp();
-        mbar_wait(done, 0, p.err, nullptr);   // the fixed 2 s limit: TMEM is freed after this
+        tile_wait(done, 0, p.err, nullptr);   // the fixed 2 s limit: TMEM is freed after this
     } else if (warp >= 6) {
         // ------------------------------------------------ V guard
         const int gt = tid - 192;
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(Pw<D>::THREADS, 1)
         auto pass = [&](int n_slots, bool scrub) {
             for (int j = 0; j < n_slots; ++j, ++u) {
                 const int st = u % C::NST;
-                const bool ok = mbar_wait(&full[st], (u / C::NST) & 1, p.err, &abort_flag, lim);
+                const bool ok = tile_wait(&full[st], (u / C::NST) & 1, p.err, &abort_flag, lim);
                 if (ok && scrub) {
                     uint4 *t = reinterpret_cast<uint4 *>(ring + st * C::SLOT);
 #pragma unroll 4
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(Pw<D>::THREADS, 1)
         int item = 0;
         // P V of key tile t has ended.  The one two before it had when S of tile t was complete, so the parity
         // tells the two apart.
-        auto p_v_done = [&](uint32_t t) { mbar_wait(&odone[t & 1], (t >> 1) & 1, p.err, &abort_flag, lim); };
+        auto p_v_done = [&](uint32_t t) { tile_wait(&odone[t & 1], (t >> 1) & 1, p.err, &abort_flag, lim); };
         for (uint32_t round = 0, id; (id = item_of(round)) < n_items; ++round, ++item) {
             int last, first, w_last, w_first, n0, n1;
             {
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(Pw<D>::THREADS, 1)
             float m = -INFINITY, l = 0.0f;
             for (int n = n0; n < n1; ++n, ++nt) {
                 const uint32_t tS = tmem + lanes + (nt & 1) * 128;
-                mbar_wait(&sfull[nt & 1], (nt >> 1) & 1, p.err, &abort_flag, lim);
+                tile_wait(&sfull[nt & 1], (nt >> 1) & 1, p.err, &abort_flag, lim);
                 tc_fence_after();
                 uint32_t v[128];
                 tc_ld32(tS, v);

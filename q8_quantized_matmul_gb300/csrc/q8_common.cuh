@@ -81,15 +81,13 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
 // may still be in flight, and only the producer's drain may wait for it.
 __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, int *err, volatile int *abort,
                                           uint64_t limit_ns = WAIT_LIMIT_NS) {
-    // the clock is read only once a wait has lasted: a read takes longer than most waits
-    uint64_t t0 = 0;
-    for (uint32_t it = 0;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    uint64_t t0 = global_timer_ns();
+    for (uint32_t it = 1;; ++it) {
         if (mbar_try_wait(bar, parity)) return true;
-        if ((it & 255u) == 31u) {
+        if ((it & 255u) == 0u) {
             if (abort && *abort) return false;
-            const uint64_t t = global_timer_ns();
-            if (t0 == 0) t0 = t;
-            if (t - t0 > limit_ns) {
+            if (global_timer_ns() - t0 > limit_ns) {
                 raise_error(err, DEV_ETIMEOUT);
                 if (abort) *abort = 1;
                 return false;
