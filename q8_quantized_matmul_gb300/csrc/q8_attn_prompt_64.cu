@@ -280,15 +280,7 @@ __global__ void __launch_bounds__(P64::THREADS, 1)
                     const int st = u % C::NST;
                     const bool ok = tile_wait(&full[st], (u / C::NST) & 1, p.err, &abort_flag, lim);
                     if (ok && n >= r.n0 + 2 && w.masked((n - 2) * C::BN, C::BN, p.window)) {
-                        uint4 *t = reinterpret_cast<uint4 *>(ring + st * C::STAGE);
-#pragma unroll 4
-                        for (int i = gt; i < C::TILE / 16; i += 64) {
-                            uint4 x = t[i];
-                            if (prompt_scrub<BF16>(x)) {
-                                t[i] = x;
-                                dirty[item & 7] = item + 1;
-                            }
-                        }
+                        prompt_scrub_tile<BF16, C::TILE>(ring + st * C::STAGE, gt, &dirty[item & 7], item + 1);
                         fence_async_smem();
                     }
                     __syncwarp();

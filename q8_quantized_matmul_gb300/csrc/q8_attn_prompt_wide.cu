@@ -237,15 +237,7 @@ __global__ void __launch_bounds__(Pw<D>::THREADS, 1)
                 const int st = u % C::NST;
                 const bool ok = tile_wait(&full[st], (u / C::NST) & 1, p.err, &abort_flag, lim);
                 if (ok && scrub) {
-                    uint4 *t = reinterpret_cast<uint4 *>(ring + st * C::SLOT);
-#pragma unroll 4
-                    for (int i = gt; i < C::SLOT / 16; i += 64) {
-                        uint4 x = t[i];
-                        if (prompt_scrub<BF16>(x)) {
-                            t[i] = x;
-                            dirty[item & 7] = item + 1;
-                        }
-                    }
+                    prompt_scrub_tile<BF16, C::SLOT>(ring + st * C::SLOT, gt, &dirty[item & 7], item + 1);
                     fence_async_smem();
                 }
                 __syncwarp();
