@@ -345,9 +345,7 @@ __global__ void __launch_bounds__(P64::THREADS, 1)
                     ++c;
                     tS = tS >= tmem + lanes + 128 ? tS - 128 : tS + 256;   // two pairs on
                 }
-                // ---- results
-                if (tb > ta) tile_wait(&odone[i * 2 + ((c - 1) & 1)], ((c - 1) >> 1) & 1, p.err, &abort_flag, lim);
-                tc_fence_after();
+                // ---- results; what does not need O comes before the wait for it
                 const PromptTile w = load_item(id);
                 const uint32_t head = id % per_tile * p.pack + me.head, kvh = head / group;
                 float lse;
@@ -355,8 +353,10 @@ __global__ void __launch_bounds__(P64::THREADS, 1)
                 const bool mine = me.used && me.token < w.rows;
                 const uint64_t orow = (uint64_t)(w.q0 + w.row0 + me.token) * p.n_heads + head;
                 const uint16_t *vp = static_cast<const uint16_t *>(p.v) + (uint64_t)w.k0 * p.v_stride + (uint64_t)kvh * C::D;
-                row_output<C::D, BF16>(p, w, tO, f, mine, orow, 0, dirty[item & 7] == item + 1 ? vp : nullptr, me.token);
                 if (p.lse && mine) p.lse[orow] = lse;
+                if (tb > ta) tile_wait(&odone[i * 2 + ((c - 1) & 1)], ((c - 1) >> 1) & 1, p.err, &abort_flag, lim);
+                tc_fence_after();
+                row_output<C::D, BF16>(p, w, tO, f, mine, orow, 0, dirty[item & 7] == item + 1 ? vp : nullptr, me.token);
                 tc_fence_before();   // O is read: the next tile's first P V follows this warp's next arrival
             }
         }

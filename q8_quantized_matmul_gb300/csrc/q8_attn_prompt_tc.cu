@@ -400,23 +400,21 @@ __global__ void __launch_bounds__(Pt::THREADS, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&pfull[i]);
                 }
-                // ---- results
-                const bool has = tb > ta;
-                if (has) {
-                    tile_wait(&ofull[i], o_seen & 1, p.err, &abort_flag, lim);
-                    ++o_seen;
-                }
-                tc_fence_after();
+                // ---- results; what does not need O comes before the wait for it
                 const PromptTile w = load_item(id);
                 const uint32_t head = id % per_tile * p.pack + me.head, kvh = head / group;
                 float lse;
                 const float f = softmax_finish(m, l, p.sinks != nullptr, p.sinks ? p.sinks[head] * 1.4426950408889634f : 0.0f, lse);
                 const bool mine = me.used && me.token < w.rows;
                 const uint64_t orow = (uint64_t)(w.q0 + w.row0 + me.token) * p.n_heads + head;
-                const bool fix = dirty[item & 7] == item + 1;
                 const uint16_t *vp = static_cast<const uint16_t *>(p.v) + (uint64_t)w.k0 * p.v_stride + (uint64_t)kvh * D;
-                row_output<D, BF16>(p, w, tO, f, mine, orow, 0, fix ? vp : nullptr, me.token);
                 if (p.lse && mine) p.lse[orow] = lse;
+                if (tb > ta) {
+                    tile_wait(&ofull[i], o_seen & 1, p.err, &abort_flag, lim);
+                    ++o_seen;
+                }
+                tc_fence_after();
+                row_output<D, BF16>(p, w, tO, f, mine, orow, 0, dirty[item & 7] == item + 1 ? vp : nullptr, me.token);
                 tc_fence_before();   // O is read: the next tile's first P V follows this warp's next arrival
             }
         }

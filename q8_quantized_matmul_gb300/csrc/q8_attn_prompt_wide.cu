@@ -308,9 +308,7 @@ __global__ void __launch_bounds__(Pw<D>::THREADS, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&pfull[nt & 1]);
             }
-            // ---- results
-            if (n1 > n0) p_v_done(nt - 1);
-            tc_fence_after();
+            // ---- results; what does not need O comes before the wait for it
             const PromptTile w = load_item(id);
             const uint32_t r = id % per_tile, head = r / C::PARTS * p.pack + me.head, kvh = head / group;
             const int d0 = (int)(r % C::PARTS) * C::DV;
@@ -319,8 +317,10 @@ __global__ void __launch_bounds__(Pw<D>::THREADS, 1)
             const bool mine = me.used && me.token < w.rows;
             const uint64_t orow = (uint64_t)(w.q0 + w.row0 + me.token) * p.n_heads + head;
             const uint16_t *vp = static_cast<const uint16_t *>(p.v) + (uint64_t)w.k0 * p.v_stride + (uint64_t)kvh * D;
-            row_output<C::DV, BF16>(p, w, tO, f, mine, orow, d0, dirty[item & 7] == item + 1 ? vp : nullptr, me.token);
             if (p.lse && mine && d0 == 0) p.lse[orow] = lse;
+            if (n1 > n0) p_v_done(nt - 1);
+            tc_fence_after();
+            row_output<C::DV, BF16>(p, w, tO, f, mine, orow, d0, dirty[item & 7] == item + 1 ? vp : nullptr, me.token);
             tc_fence_before();   // O is read: the next item's first P V follows this warp's next arrival
         }
     }
