@@ -33,49 +33,67 @@ __device__ __forceinline__ int prompt_bound(int32_t start, uint32_t n) { return 
 template <int THREADS>
 __device__ __forceinline__ bool prompt_tile(const AttnPromptParams &p, int BM, uint32_t slot, bool report, PromptTile &w,
                                             int *sh) {
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31;
     const int32_t *ks = p.k_start ? p.k_start : p.q_start;
-    if (tid == 0) sh[0] = -1;
-    __syncthreads();
-    // sequences from the last one on, THREADS at a time
-    int64_t before = 0;
-    for (uint32_t b = 0; b < p.n_seq; b += THREADS) {
-        const uint32_t i = b + tid, s = p.n_seq - 1 - i;
-        int tiles = 0, qa = 0, qe = 0, ka = 0, ke = 0;
-        if (i < p.n_seq) {
-            const int4 raw = make_int4(p.q_start[s], p.q_start[s + 1], ks[s], ks[s + 1]);
-            qa = prompt_bound(raw.x, p.n_q);
-            qe = prompt_bound(raw.y, p.n_q);
-            ka = prompt_bound(raw.z, p.n_k);
-            ke = prompt_bound(raw.w, p.n_k);
-            tiles = qe > qa ? (qe - qa + BM - 1) / BM : 0;
-            if (report && (qe < qa || ke < ka || qa != raw.x || qe != raw.y || ka != raw.z || ke != raw.w))
-                raise_error(p.err, DEV_ERANGE);
-        }
-        // inclusive sum over the CTA
-        int sum = tiles;
+    int tiles, qa, qe, ka, ke;
+    auto sequence = [&](uint32_t i) {                // the i-th from the last
+        tiles = qa = qe = ka = ke = 0;
+        if (i >= p.n_seq) return;
+        const uint32_t s = p.n_seq - 1 - i;
+        const int4 raw = make_int4(p.q_start[s], p.q_start[s + 1], ks[s], ks[s + 1]);
+        qa = prompt_bound(raw.x, p.n_q);
+        qe = prompt_bound(raw.y, p.n_q);
+        ka = prompt_bound(raw.z, p.n_k);
+        ke = prompt_bound(raw.w, p.n_k);
+        tiles = qe > qa ? (qe - qa + BM - 1) / BM : 0;
+        if (report && (qe < qa || ke < ka || qa != raw.x || qe != raw.y || ka != raw.z || ke != raw.w))
+            raise_error(p.err, DEV_ERANGE);
+    };
+    auto sum_to = [&](int sum) {                     // inclusive, over the warp
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int v = __shfl_up_sync(0xffffffffu, sum, o);
-            if ((tid & 31) >= o) sum += v;
+            if (lane >= o) sum += v;
         }
-        if ((tid & 31) == 31) sh[1 + tid / 32] = sum;
-        __syncthreads();
-        int64_t at = before + sum - tiles;
-        for (int k = 0; k < THREADS / 32; ++k) {
-            if (k < tid / 32) at += sh[1 + k];
-            before += sh[1 + k];
-        }
+        return sum;
+    };
+    auto claim = [&](int64_t at) {                   // this thread's sequence holds the tiles from `at` on
         if (tiles && slot >= at && slot < at + tiles) {
-            sh[0] = (int)(at + tiles - 1 - slot);   // newest tile first
+            sh[0] = (int)(at + tiles - 1 - slot);    // newest tile first
             int *b4 = sh + THREADS / 32 + 1;
             b4[0] = qa;
             b4[1] = qe - qa;
             b4[2] = ka;
             b4[3] = max(ke - ka, 0);
         }
+    };
+    if (p.n_seq <= 32) {                             // one warp, one barrier
+        if (tid < 32) {
+            if (lane == 0) sh[0] = -1;
+            __syncwarp();
+            sequence(lane);
+            claim(sum_to(tiles) - tiles);
+        }
         __syncthreads();
-        if (sh[0] >= 0) break;
+    } else {
+        if (tid == 0) sh[0] = -1;
+        __syncthreads();
+        // sequences from the last one on, THREADS at a time
+        int64_t before = 0;
+        for (uint32_t b = 0; b < p.n_seq; b += THREADS) {
+            sequence(b + tid);
+            const int sum = sum_to(tiles);
+            if (lane == 31) sh[1 + tid / 32] = sum;
+            __syncthreads();
+            int64_t at = before + sum - tiles;
+            for (int k = 0; k < THREADS / 32; ++k) {
+                if (k < tid / 32) at += sh[1 + k];
+                before += sh[1 + k];
+            }
+            claim(at);
+            __syncthreads();
+            if (sh[0] >= 0) break;
+        }
     }
     if (sh[0] < 0) return false;
     const int *b4 = sh + THREADS / 32 + 1;
