@@ -146,7 +146,29 @@ __global__ void __launch_bounds__(128, Dec<D, FMT, NT>::CTAS) k_attn_decode(cons
     bool by_unit;
     // a unit's length on the line
     auto on_line = [&](const Seq &q) { return by_unit ? min(q.tiles, 1) : (q.tiles ? q.tiles + HEAD : 0); };
-    {
+    auto share_of = [&](int64_t n) {
+        total = n;
+        shares = n < (int64_t)gridDim.x ? (uint32_t)n : gridDim.x;   // every share has a tile
+        t0 = t1 = 0;
+        if (blockIdx.x >= shares) return;
+        t0 = n * blockIdx.x / shares;
+        t1 = n * (blockIdx.x + 1) / shares;
+    };
+    if (p.n_seq <= 32) {                                         // every warp for itself: no barriers
+        const int n = lane < (int)p.n_seq ? seq_of(C::TT, 16, p, lane, blockIdx.x == 0 && warp == 0).tiles : 0;
+        by_unit = __all_sync(0xffffffffu, n <= SHORT);
+        const int64_t mine = (int64_t)(by_unit ? min(n, 1) : (n ? n + HEAD : 0)) * units_per_seq;
+        int64_t sum = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += v;
+        }
+        share_of(__shfl_sync(0xffffffffu, sum, 31));
+        const uint32_t hit = __ballot_sync(0xffffffffu, t0 < t1 && sum - mine <= t0 && t0 < sum);
+        s = hit ? (uint32_t)__ffs((int)hit) - 1 : 0;
+        s_base = __shfl_sync(0xffffffffu, sum - mine, (int)s);
+    } else {
         int64_t *scan = reinterpret_cast<int64_t *>(smem);       // before the ring is used
         const uint32_t per = (p.n_seq + 127) / 128, a = min(p.n_seq, tid * per), b = min(p.n_seq, a + per);
         int64_t mine = 0;
@@ -175,13 +197,7 @@ __global__ void __launch_bounds__(128, Dec<D, FMT, NT>::CTAS) k_attn_decode(cons
             if (w < warp) before += scan[w];
             total += scan[w];
         }
-        shares = total < (int64_t)gridDim.x ? (uint32_t)total : gridDim.x;   // every share has a tile
-        if (blockIdx.x < shares) {
-            t0 = total * blockIdx.x / shares;
-            t1 = total * (blockIdx.x + 1) / shares;
-        } else {
-            t0 = t1 = 0;
-        }
+        share_of(total);
         // one thread's range holds t0 (when the share is not empty)
         if (t0 < t1 && before <= t0 && t0 < before + mine) {
             uint32_t i = a;
