@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(Dt<D>::THREADS, 1)
                                 if (pos >= g.q.lo && pos < g.q.hi && ((okm >> (r >> box_shift)) & 1)) continue;
                                 uint4 *row = reinterpret_cast<uint4 *>(t + (gt & 1) * C::CHUNK + r * 128);
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) row[e] = make_uint4(0, 0, 0, 0);
+                                for (int e = 0; e < 8; ++e) row[(e + r) & 7] = make_uint4(0, 0, 0, 0);   // rows 128 bytes apart: other banks
                             }
                             fence_async_smem();
                         }

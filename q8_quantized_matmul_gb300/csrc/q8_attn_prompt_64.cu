@@ -7,8 +7,8 @@
 // a tile.  O of both tiles takes only 128 TMEM columns here, so there are three S buffers.  The pairs x = 2 (key tile)
 // + (query tile) of an item form one sequence; pair x works in buffer x % 3, and S of pair x + 3 is issued right behind
 // P V of pair x, in one group: the next scores of a tile are ready when its softmax of the last ones ends.
-// Measured: one prompt of 8192 tokens, 32 heads on 8, 252 us (1.09 PFLOP/s; 2060 cycles a key tile; 274 us with one
-// buffer a tile); 12 packed prompts with a window of 1024 89 us (95).  Of the 2060 the softmax takes 1350 (probe: a
+// Measured: one prompt of 8192 tokens, 32 heads on 8, 250 us (1.10 PFLOP/s; 2050 cycles a key tile; 274 us with one
+// buffer a tile); 12 packed prompts with a window of 1024 85 us (with one buffer 6 more).  Of the 2050 the softmax takes 1350 (probe: a
 // warp's step 881 cycles alone, two on a scheduler 1346); the rest is waits for S behind the other tile's group.
 // Registers are split 104 / 200 between the roles: with 168 a thread the softmax spills (a step 1150 instead of 885).
 // Two issuing warps, one a query tile, gained 1 % on the long prompt and lost 10 % on the short ones.

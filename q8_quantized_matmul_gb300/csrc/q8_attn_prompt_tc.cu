@@ -9,7 +9,7 @@
 // the SM's 512 columns.  While the threads of one tile work on its softmax the tensor cores run the
 // other tile's products, so the two overlap: a key tile costs the tensor pipe about 2048
 // cycles for both query tiles and the softmax warps about 1350.  One prompt of 8192 tokens with 32 heads on 8 takes
-// 351 us (1.57 PFLOP/s, at the card's power limit), one of 4096 tokens 107 us (1.29).
+// 339 us (1.62 PFLOP/s, at the card's power limit), one of 4096 tokens 100 us (1.37).
 //
 // O is rescaled only when a row's maximum has grown by more than 2^8 since the last time (the weights
 // then stay below 2^8, harmless in either 16-bit type); the result is the same sum in other units.  The

@@ -87,9 +87,9 @@ struct AttnDecodeParams {
 };
 // Whether a call runs on the tcgen05 kernel: 16-bit caches, large heads, more query heads on a key-value head
 // than one unit of the mma.sync kernel takes (64 heads of 512 on one, 16 sequences of up to 4100 positions:
-// 29 us against 76 us), and room for more than a few positions a sequence (most: what the window or the row of pages
-// allows; 64 heads of 512, 1 / 16 / 48 sequences of up to 64: 16.2 / 20.3 / 25.1 us there, 11.6 / 12.2 / 23.7 us
-// on mma.sync; of up to 128: 14.6 / 20.0 / 25.2 against 14.8 / 15.6 / 30.5).
+// 26 us against 76 us), and room for more than a few positions a sequence (most: what the window or the row of pages
+// allows; 64 heads of 512, 1 / 16 / 48 sequences of up to 64: 14.8 / 16.8 / 21.5 us there, 11.6 / 12.2 / 23.7 us
+// on mma.sync; of up to 128: 15.1 / 16.8 / 21.5 against 14.8 / 15.6 / 30.5).
 inline bool attn_decode_on_tc(uint32_t dim, uint32_t group, bool cache16, uint64_t most) {
     return cache16 && dim >= 256 && group > 16 && most > 64;
 }
