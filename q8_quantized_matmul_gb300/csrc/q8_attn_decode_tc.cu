@@ -10,7 +10,8 @@
 // 16-bit weights to shared memory and keeps its own sums l[64].  The running maximum of a head is moved
 // only when a score exceeds it by more than 2^8 (one vote a step); then the maxima are reduced and O^T, l
 // rescaled.  Cached bytes enter once through a ring of 32 KB slots (128 positions x 128 dims, by TMA page by
-// page, K and V in turn): 128 KB in flight, HBM bound.
+// page, K and V in turn), 128 KB in flight.  16 sequences of up to 4100 positions take 26 us, three times the bytes'
+// time: with 1.4 steps a CTA the start (256 KB a CTA) and the pieces set it, not the stream.
 //
 // The line of steps is cut into equal shares as in the mma.sync kernel; every share of a unit leaves its
 // (m, l, O) in scratch (a unit's 128 KB would take one CTA 10 us to join) and k_attn_decode_join adds them,

@@ -7,7 +7,8 @@
 // 512 values, 1024 at 256) and the tensor pipe does not wait for it.  Operands stream through a ring of slots of
 // 128 keys x 128 dims (32 KB); at 512 values q takes 128 KB of shared memory and three slots are left.  Reading
 // both operands of S there (128 bytes a cycle) and filling the ring bound the kernel: at 512 values a key tile
-// moves 512 KB through shared memory, 4096 cycles, for three quarters as many of products.
+// moves 512 KB through shared memory, 4096 cycles, for three quarters as many of products.  One prompt of 4096
+// tokens with 16 heads of 256 on one takes 105 us (1.31 PFLOP/s), of 2048 with 64 heads of 512 339 us (0.81).
 //
 // Roles, list of tiles, lazy rescaling and the V guard are those of q8_attn_prompt_tc.cu.  O is rescaled only
 // after the P V before has ended (its own barrier, since S of the next tile no longer implies it).
