@@ -556,3 +556,17 @@ def test_attn_prompt_wait_expires(q8):
     assert q8.q8_last_error() == q8.Q8_ETIMEOUT
     assert torch.equal(q8.attn_prompt(q, q, q, start), ref)
     assert q8.q8_last_error() == 0
+
+
+@pytest.mark.parametrize("dim,tokens,heads", [(64, 300, 2), (64, 3000, 16), (256, 300, 2), (512, 150, 2)])
+def test_attn_prompt_wait_expires_other_dims(q8, dim, tokens, heads):
+    """The same for the kernels of the other head sizes, with one tile a CTA and with the list of tiles."""
+    q = torch.randn(tokens, heads, dim, device=DEV).bfloat16()
+    start = torch.tensor([0, tokens], dtype=torch.int32, device=DEV)
+    ref = q8.attn_prompt(q, q, q, start)
+    assert q8.q8_last_error() == 0
+    q8.q8_debug_expire_waits(1, 1_000_000)
+    q8.attn_prompt(q, q, q, start)
+    assert q8.q8_last_error() == q8.Q8_ETIMEOUT
+    assert torch.equal(q8.attn_prompt(q, q, q, start), ref)
+    assert q8.q8_last_error() == 0
