@@ -379,7 +379,8 @@ int q8_kv_append(void *q_out, void *k_out, void *v_out, int out_type, const q8_k
  *   sinks      in: fp32 [n_heads] or NULL.
  * Statistics, products' sums and the output's sum are fp32; the weights exp(z_j - max)
  * are rounded to 16 bit for the tensor cores (F16 for Q8_0 caches, where they carry the
- * block scale of V).  Keys and values outside the visible range are never used, whatever
+ * block scale of V; fp16 weights are counted in units that keep 10 bits down to 2^-21 of the
+ * largest, and some down to 2^-32).  Keys and values outside the visible range are never used, whatever
  * they hold.  A negative length or one beyond max_pages pages is cut to the range, and a
  * page id outside the pool leaves its positions out; both raise Q8_ERANGE.
  * Work is split over the cached positions so that every SM gets an equal share whatever

@@ -43,6 +43,17 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// The power of two that a row's weights are counted in: with the largest score (log2 units) at x they are 2^(z - r),
+// r = x - UP.  In fp16 a weight below 2^-14 loses bits and one below 2^-25 is nothing, so the largest is put at 2^UP:
+// one key far ahead of 60 000 others would else take the little that each of these has.  Of scores beyond 2^20 (steps of
+// 1/8) x itself: the rounding of z - r could take 2^UP past the largest fp16 number.
+template <int UP> __device__ __forceinline__ float weight_ref(float x) {
+    if constexpr (UP == 0) return x;
+    return fabsf(x) < 1048576.0f ? x - (float)UP : x;
+}
+// UP of the kernels whose weights pass the largest one by up to 2^8 before they rescale.
+template <bool BF16> constexpr int LAZY_UP = BF16 ? 0 : 7;
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float y;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));

@@ -28,7 +28,8 @@
 // Q8_0 pages: int8 quants are exact in either 16-bit type.  The score sums each 32-value block on its
 // own and folds the block's K scale in fp32, exact but for fp32 rounding.  V's scale goes into the
 // weights, one fp16 rounding each: 2^(z - M + 15) d with M >= m + e, every |d| < 2^e of the slice, so
-// products stay below 2^15 and the weights keep 29 binades above the smallest normal.
+// products stay below 2^15 and the weights keep 29 binades above the smallest normal.  The weights of fp16 caches are
+// 2^(z - m + 15) for the same reason.
 #include <algorithm>
 
 #include "q8_attn.cuh"
@@ -70,7 +71,7 @@ template <int D, int FMT, int NT> struct Dec {
     static constexpr int SMEM = W * RING + QS + W * HR * 8 + 64 + 64;
     static constexpr int FIT = 224 * 1024 / SMEM;
     static constexpr int CTAS = FIT < 1 ? 1 : (D == 64 ? (FIT < 4 ? FIT : 4) : (D == 128 ? (FIT < 3 ? FIT : 3) : 1));
-    static constexpr float BIAS = Q8 ? 15.0f : 0.0f;     // weights are 2^(z - M + BIAS)
+    static constexpr int UP = FMT == 1 ? 0 : 15;         // fp16 weights: the largest is 2^15 (weight_ref)
     static_assert(STAGE % 128 == 0, "stage alignment");
 };
 
@@ -495,7 +496,7 @@ __global__ void __launch_bounds__(128, Dec<D, FMT, NT>::CTAS) k_attn_decode(cons
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const float mn = fmaxf(m[t][h], mx[t][h]);
-                            const float f = m[t][h] == -INFINITY ? 0.0f : ex2(m[t][h] - mn);
+                            const float f = m[t][h] == -INFINITY ? 0.0f : ex2(weight_ref<C::UP>(m[t][h]) - weight_ref<C::UP>(mn));
                             m[t][h] = mn;
                             l[t][h] *= f;
 #pragma unroll
@@ -510,7 +511,7 @@ __global__ void __launch_bounds__(128, Dec<D, FMT, NT>::CTAS) k_attn_decode(cons
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const float s = m[t][h] == -INFINITY ? 0.0f : C::BIAS - m[t][h];
+                        const float s = m[t][h] == -INFINITY ? 0.0f : -weight_ref<C::UP>(m[t][h]);
 #pragma unroll
                         for (int i = 0; i < MT; ++i) {
                             z[i][t][h] = ex2(__fmaf_rn(z[i][t][h], p.scale_log2, s));
@@ -584,7 +585,7 @@ __global__ void __launch_bounds__(128, Dec<D, FMT, NT>::CTAS) k_attn_decode(cons
             for (int h = 0; h < 2; ++h) {
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) l[t][h] += __shfl_xor_sync(0xffffffffu, l[t][h], x);
-                if (g == 0) ml[warp * C::HR + 8 * t + 2 * c + h] = make_float2(m[t][h], l[t][h]);
+                if (g == 0) ml[warp * C::HR + 8 * t + 2 * c + h] = make_float2(weight_ref<C::UP>(m[t][h]), l[t][h]);
 #pragma unroll
                 for (int i = 0; i < C::DV / 16; ++i) {
                     // Q8_0 tiles hold dims 4 g + 0, 1 and 4 g + 2, 3 of a block
@@ -615,7 +616,7 @@ __global__ void __launch_bounds__(128, Dec<D, FMT, NT>::CTAS) k_attn_decode(cons
                 for (int e = 0; e < 8; ++e) y[e] += v[e] * f;
             }
             if (whole) {
-                finish8(p, s, head0 + row, d0, sink[row], mt - C::BIAS, lt, y, act);
+                finish8(p, s, head0 + row, d0, sink[row], mt, lt, y, act);
             } else if (act) {
                 float4 *dst = reinterpret_cast<float4 *>(p.part + (slot * 16 + row) * D + d0);
                 dst[0] = make_float4(y[0], y[1], y[2], y[3]);
@@ -664,7 +665,7 @@ __global__ void __launch_bounds__(128, Dec<D, FMT, NT>::CTAS) k_attn_decode(cons
                     join8(n, [&](int k) { return p.part + (slot_of(k0 + k * step) * 16 + row) * D + d0; },
                           [&](int k) { return from + (slot_of(k0 + k * step) * 16 + row) * 2 + h; }, mj, lj, y);
                     if (result) {
-                        finish8(p, s, head0 + row, d0, sink[row], mj - C::BIAS, lj, y, act);
+                        finish8(p, s, head0 + row, d0, sink[row], mj, lj, y, act);
                     } else if (act) {
                         const uint64_t to = slot_of(k0) * 16 + row;
                         float4 *dst = reinterpret_cast<float4 *>(p.part + to * D + d0);

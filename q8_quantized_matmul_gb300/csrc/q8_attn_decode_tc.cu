@@ -39,7 +39,7 @@ template <int D> struct Dt {
     static constexpr int QBYTES = HT * D * 2, PBYTES = TT * HT * 2;
     static constexpr int THREADS = 256;
     static constexpr int NBAR = 2 + 3 * NST + 3 + 1;
-    static constexpr int FLOATS = HT * (1 + 1 + 4);          // m, factors, per-warp maxima
+    static constexpr int FLOATS = HT * (1 + 1 + 1 + 4);      // m, references, factors, per-warp maxima
     static constexpr int SMEM = 1024 + QBYTES + PBYTES + NST * SLOT + NBAR * 8 + FLOATS * 4 + 64;
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
@@ -98,7 +98,8 @@ __global__ void __launch_bounds__(Dt<D>::THREADS, 1)
     uint64_t *bars = reinterpret_cast<uint64_t *>(ring + C::NST * C::SLOT);
     uint64_t *qfull = bars, *qempty = bars + 1, *full = bars + 2, *empty = full + C::NST, *ready = empty + C::NST;
     uint64_t *sfull = ready + C::NST, *pfull = sfull + 1, *ofull = pfull + 1, *done = ofull + 1;
-    float *sm_m = reinterpret_cast<float *>(bars + C::NBAR), *sm_f = sm_m + C::HT, *sm_w = sm_f + C::HT;
+    float *sm_m = reinterpret_cast<float *>(bars + C::NBAR), *sm_r = sm_m + C::HT, *sm_f = sm_r + C::HT,
+          *sm_w = sm_f + C::HT;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint64_t lim = wait_limit(p.wait_ns);
 
@@ -387,7 +388,10 @@ __global__ void __launch_bounds__(Dt<D>::THREADS, 1)
             float l[64];
 #pragma unroll
             for (int h = 0; h < 64; ++h) l[h] = 0.0f;
-            if (tid < 64) sm_m[tid] = -INFINITY;
+            if (tid < 64) {
+                sm_m[tid] = -INFINITY;
+                sm_r[tid] = 0.0f;                            // 2^(-inf - 0): a head that has seen nothing has no weights
+            }
             named_bar_sync(2, 128);
             for (int it = g.ta; it < g.tb; ++it, ++n) {
                 tile_wait(sfull, n & 1, p.err, &abort_flag, lim);
@@ -424,7 +428,9 @@ __global__ void __launch_bounds__(Dt<D>::THREADS, 1)
                         const float mx = fmaxf(fmaxf(sm_w[tid], sm_w[64 + tid]), fmaxf(sm_w[128 + tid], sm_w[192 + tid]));
                         const float now = mx > old + 8.0f ? mx : old;
                         sm_m[tid] = now;
-                        sm_f[tid] = old == now || old == -INFINITY ? 1.0f : ex2(old - now);   // a first maximum: nothing to rescale
+                        sm_r[tid] = now == -INFINITY ? 0.0f : weight_ref<LAZY_UP<BF16>>(now);
+                        // a first maximum: nothing to rescale
+                        sm_f[tid] = old == now || old == -INFINITY ? 1.0f : ex2(weight_ref<LAZY_UP<BF16>>(old) - weight_ref<LAZY_UP<BF16>>(now));
                     }
                     named_bar_sync(2, 128);
                     if (it > g.ta) {
@@ -446,12 +452,12 @@ __global__ void __launch_bounds__(Dt<D>::THREADS, 1)
                 uint32_t pk[32];
 #pragma unroll
                 for (int h = 0; h < 64; h += 4) {
-                    const float4 m4 = *reinterpret_cast<const float4 *>(sm_m + h);
-                    const float mm[4] = {m4.x, m4.y, m4.z, m4.w};
+                    const float4 r4 = *reinterpret_cast<const float4 *>(sm_r + h);
+                    const float rr[4] = {r4.x, r4.y, r4.z, r4.w};
                     float a[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        a[e] = ex2(z[h + e] - (mm[e] == -INFINITY ? 0.0f : mm[e]));
+                        a[e] = ex2(z[h + e] - rr[e]);
                         l[h + e] += a[e];
                     }
                     pk[h / 2] = pack16<BF16>(a[0], a[1]);
@@ -476,7 +482,7 @@ __global__ void __launch_bounds__(Dt<D>::THREADS, 1)
             named_bar_sync(2, 128);
             const uint64_t slot = 2 * (uint64_t)blockIdx.x + (first ? 0 : 1);
             if (tid < 64)
-                p.part_ml[slot * 64 + tid] = make_float2(sm_m[tid], (sm_w[tid] + sm_w[64 + tid]) + (sm_w[128 + tid] + sm_w[192 + tid]));
+                p.part_ml[slot * 64 + tid] = make_float2(weight_ref<LAZY_UP<BF16>>(sm_m[tid]), (sm_w[tid] + sm_w[64 + tid]) + (sm_w[128 + tid] + sm_w[192 + tid]));
 #pragma unroll 1
             for (int c = 0; c < D / 128 * 64; c += 32) {
                 uint32_t o[32];

@@ -12,7 +12,8 @@
 // 339 us (1.62 PFLOP/s, at the card's power limit), one of 4096 tokens 100 us (1.37).
 //
 // O is rescaled only when a row's maximum has grown by more than 2^8 since the last time (the weights
-// then stay below 2^8, harmless in either 16-bit type); the result is the same sum in other units.  The
+// then stay below 2^8 in bf16; in fp16 they are counted in units 2^7 smaller, see weight_ref, and stay below 2^15);
+// the result is the same sum in other units.  The
 // threads of a tile do that themselves: S of the next key tile is complete only after this tile's P V is,
 // so O is at rest between the two.
 //
@@ -389,12 +390,12 @@ __global__ void __launch_bounds__(Pt::THREADS, 1)
                     const bool grow = mx > m + 8.0f;
                     float f = 1.0f;
                     if (grow) {
-                        f = m == -INFINITY ? 1.0f : ex2(m - mx);
+                        f = m == -INFINITY ? 1.0f : ex2(weight_ref<LAZY_UP<BF16>>(m) - weight_ref<LAZY_UP<BF16>>(mx));
                         m = mx;
                         l *= f;
                     }
                     if (__any_sync(0xffffffffu, f != 1.0f) && n > ta) row_rescale<D>(tO, f);
-                    l += row_weights<BF16>(v, p.scale_log2, m, tS);
+                    l += row_weights<BF16>(v, p.scale_log2, weight_ref<LAZY_UP<BF16>>(m), tS);
                     tc_wait_st();
                     tc_fence_before();
                     __syncwarp();
@@ -404,7 +405,7 @@ __global__ void __launch_bounds__(Pt::THREADS, 1)
                 const PromptTile w = load_item(id);
                 const uint32_t head = id % per_tile * p.pack + me.head, kvh = head / group;
                 float lse;
-                const float f = softmax_finish(m, l, p.sinks != nullptr, p.sinks ? p.sinks[head] * 1.4426950408889634f : 0.0f, lse);
+                const float f = softmax_finish(weight_ref<LAZY_UP<BF16>>(m), l, p.sinks != nullptr, p.sinks ? p.sinks[head] * 1.4426950408889634f : 0.0f, lse);
                 const bool mine = me.used && me.token < w.rows;
                 const uint64_t orow = (uint64_t)(w.q0 + w.row0 + me.token) * p.n_heads + head;
                 const uint16_t *vp = static_cast<const uint16_t *>(p.v) + (uint64_t)w.k0 * p.v_stride + (uint64_t)kvh * D;

@@ -63,9 +63,9 @@ template <int N> __device__ __forceinline__ void row_rescale(uint32_t tO, float 
     }
 }
 
-// Weights 2^(scale v - m), written as 16-bit pairs over the scores; their sum (before rounding).
-template <bool BF16> __device__ __forceinline__ float row_weights(const uint32_t (&v)[128], float scale, float m, uint32_t tS) {
-    const float neg = m == -INFINITY ? 0.0f : -m;
+// Weights 2^(scale v - r), written as 16-bit pairs over the scores; their sum (before rounding).
+template <bool BF16> __device__ __forceinline__ float row_weights(const uint32_t (&v)[128], float scale, float r, uint32_t tS) {
+    const float neg = r == -INFINITY ? 0.0f : -r;
     const uint64_t scale2 = pair2(scale, scale), neg2 = pair2(neg, neg);
     uint64_t s0 = 0, s1 = 0;
 #pragma unroll

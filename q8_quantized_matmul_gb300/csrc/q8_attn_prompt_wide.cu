@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(Pw<D>::THREADS, 1)
                 // a first maximum needs no rescaling: O is still zero in that row
                 float f = 1.0f;
                 if (mx > m + 8.0f) {
-                    f = m == -INFINITY ? 1.0f : ex2(m - mx);
+                    f = m == -INFINITY ? 1.0f : ex2(weight_ref<LAZY_UP<BF16>>(m) - weight_ref<LAZY_UP<BF16>>(mx));
                     m = mx;
                     l *= f;
                 }
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(Pw<D>::THREADS, 1)
                     tc_fence_after();
                     row_rescale<C::DV>(tO, f);
                 }
-                l += row_weights<BF16>(v, p.scale_log2, m, tS);
+                l += row_weights<BF16>(v, p.scale_log2, weight_ref<LAZY_UP<BF16>>(m), tS);
                 tc_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(Pw<D>::THREADS, 1)
             const uint32_t r = id % per_tile, head = r / C::PARTS * p.pack + me.head, kvh = head / group;
             const int d0 = (int)(r % C::PARTS) * C::DV;
             float lse;
-            const float f = softmax_finish(m, l, p.sinks != nullptr, p.sinks ? p.sinks[head] * 1.4426950408889634f : 0.0f, lse);
+            const float f = softmax_finish(weight_ref<LAZY_UP<BF16>>(m), l, p.sinks != nullptr, p.sinks ? p.sinks[head] * 1.4426950408889634f : 0.0f, lse);
             const bool mine = me.used && me.token < w.rows;
             const uint64_t orow = (uint64_t)(w.q0 + w.row0 + me.token) * p.n_heads + head;
             const uint16_t *vp = static_cast<const uint16_t *>(p.v) + (uint64_t)w.k0 * p.v_stride + (uint64_t)kvh * D;

@@ -1,0 +1,97 @@
+"""GPU tests of the attention kernels at the ends of their numbers."""
+import numpy as np
+import pytest
+
+from tests.attn_plain import attend
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module")
+def q8():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from q8_quantized_matmul_gb300 import build
+    build.build()
+    import q8_quantized_matmul_gb300 as m
+    torch.cuda.set_device(0)
+    return m
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+def far_below(n, dim, seed):
+    """Keys and values [n, 1, dim] fp16: every 128th key is 17.5 ahead of the others in natural logarithms and has
+    values of zero, the others have values of 500 to 1000: the output is what the small weights add up to."""
+    g = torch.Generator().manual_seed(seed)
+    k = torch.full((n, 1, dim), -17.5 * dim ** -0.5)
+    v = torch.rand((n, 1, dim), generator=g) * 500 + 500
+    k[5::128], v[5::128] = 0.0, 0.0
+    return k.half().to(DEV), v.half().to(DEV)
+
+
+def check_far_below(got, k, v, rows, last, dim, what):
+    """The bound of tests/attn_plain.py with weights of 8 bits (2^-8 of the weighted mean; fp16 keeps at least 6 of a
+    weight at 2^-25 of the largest: the rest) plus half a step of fp16 below its normal numbers, 2^-25, counted in units
+    2^7 below the largest weight: 2^-32 |v| a key."""
+    kf, vf = k.cpu().double().numpy()[:, 0], v.cpu().double().numpy()[:, 0]
+    q = np.ones((1, dim))
+    for r in rows:
+        n = last(r) + 1
+        ref, lse, bound, _ = attend(q, kf[:n], vf[:n], np.ones((1, n), bool), dim ** -0.5, None, "bf16", "f32")
+        bound = bound + 2.0 ** -32 * np.abs(vf[:n]).sum(0) / np.exp(lse[0] - (kf[:n] @ q[0] * dim ** -0.5).max())
+        assert np.all(ref[0] > 2.0 * bound[0])                       # a kernel that loses these weights cannot pass
+        err = np.abs(got[r] - ref)
+        assert np.all(err <= bound), f"{what}, row {r}: {(err / bound).max():.2f} of the bound"
+
+
+@pytest.mark.parametrize("dim,heads", [(64, 2), (128, 12), (256, 2), (512, 2), (256, 24), (512, 24)])
+def test_decode_sums_weights_far_below_the_largest(q8, dim, heads):
+    lens, page = [3000, 700], 64
+    cache = q8.KVCache.empty(q8.Q8_TYPE_F16, 1, 60, page, 1, dim)
+    table = i32([list(range(47)), [*range(47, 58), *[-1] * 36]])
+    rows = [far_below(n, dim, i) for i, n in enumerate(lens)]
+    for i, (k, v) in enumerate(rows):
+        pos = torch.arange(lens[i], dtype=torch.int32, device=DEV)
+        q8.kv_append(cache, 0, None, k.float(), v.float(), pos, torch.full_like(pos, i), table)
+    q = torch.ones(2, heads, dim, device=DEV, dtype=torch.float16)
+    got = q8.attn_decode(q, cache, 0, table, i32(lens), out_type=q8.Q8_TYPE_F32).cpu().double().numpy()
+    assert q8.q8_last_error() == 0
+    for i, (k, v) in enumerate(rows):
+        for h in (0, heads - 1):
+            check_far_below(got[i, h][None], k, v, [0], lambda r: lens[i] - 1, dim, f"sequence {i} head {h}")
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256, 512])
+def test_prompt_sums_weights_far_below_the_largest(q8, dim):
+    n = 700
+    k, v = far_below(n, dim, dim)
+    q = torch.ones(n, 2, dim, device=DEV, dtype=torch.float16)
+    got = q8.attn_prompt(q, k, v, i32([0, n]), out_type=q8.Q8_TYPE_F32).cpu().double().numpy()
+    assert q8.q8_last_error() == 0
+    for h in range(2):
+        check_far_below(got[:, h], k, v, [0, 4, 5, 6, 127, 128, 300, 699], lambda r: r, dim, f"head {h}")
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("dim,heads", [(64, 2), (128, 2), (512, 24)])
+def test_very_large_scores(q8, kind, dim, heads):
+    """Scores of 2^23 to 2^25 (log2 units, steps of 1 to 4): equal keys share the weight, whatever the distance of their scores' roundings."""
+    dt = torch.float16 if kind == "f16" else torch.bfloat16
+    n = 150
+    q = torch.full((n, heads, dim), 1000.0, device=DEV).to(dt)
+    k = torch.full((n, 1, dim), 1000.0, device=DEV).to(dt)
+    v = torch.full((n, 1, dim), 3.0, device=DEV).to(dt)
+    o = q8.attn_prompt(q, k, v, i32([0, n]), out_type=q8.Q8_TYPE_F32)
+    cache = q8.KVCache.empty(q8.Q8_TYPE_F16 if kind == "f16" else q8.Q8_TYPE_BF16, 1, 5, 32, 1, dim)
+    pos, table = torch.arange(n, dtype=torch.int32, device=DEV), i32([[0, 1, 2, 3, 4]])
+    q8.kv_append(cache, 0, None, k.float(), v.float(), pos, torch.zeros_like(pos), table)
+    d = q8.attn_decode(q[:1].contiguous(), cache, 0, table, i32([n]), out_type=q8.Q8_TYPE_F32)
+    assert q8.q8_last_error() == 0
+    u = 2.0 ** (-11 if kind == "f16" else -8)                       # a weight's rounding, and the sums'
+    for x in (o, d):
+        assert (x - 3.0).abs().max() <= 3.0 * (u + 2.0 ** -18)
