@@ -369,7 +369,8 @@ int q8_kv_append(void *q_out, void *k_out, void *v_out, int out_type, const q8_k
  *   z_j = scale * q[s][h] . k_j,  j in [max(0, len - window), len), len = seq_lens[s]
  *         (window 0: all of [0, len)); the new token's own k and v are already stored
  *   out[s][h] = sum_j exp(z_j) v_j / (sum_j exp(z_j) + exp(sinks[h]))
- * without the last term when sinks is NULL.  A sequence of length 0 gives zeros.
+ * without the last term when sinks is NULL (a sink of -inf adds nothing, one of +inf leaves
+ * zeros and an lse of +inf).  A sequence of length 0 gives zeros.
  *   out        out: [n_seq][n_heads][head_dim]; out_type: q's type, Q8_TYPE_F32, or
  *              Q8_TYPE_Q8_0 (blocks for q8_matmul_q, head_dim/32 per head).
  *   lse        out: fp32 [n_seq][n_heads], the natural logarithm of the denominator

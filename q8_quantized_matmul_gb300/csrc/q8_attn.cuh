@@ -136,6 +136,10 @@ __device__ __forceinline__ void load8s(float (&y)[8], const float *p) {
 // The row's terms are sums of 2^(z - m): l of them plus, with a sink logit (log2 units), its own.
 __device__ __forceinline__ float softmax_finish(float m, float l, bool has_sink, float sink, float &lse) {
     float f = 1.0f, total = l, mt = m;
+    if (has_sink && sink == INFINITY) {                // takes all the weight (m - sink is no number)
+        lse = l + INFINITY;
+        return l * 0.0f;
+    }
     if (has_sink) {
         mt = fmaxf(m, sink);
         if (mt == -INFINITY) mt = 0.0f;                // both empty: total stays 0

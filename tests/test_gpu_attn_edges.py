@@ -95,3 +95,27 @@ def test_very_large_scores(q8, kind, dim, heads):
     u = 2.0 ** (-11 if kind == "f16" else -8)                       # a weight's rounding, and the sums'
     for x in (o, d):
         assert (x - 3.0).abs().max() <= 3.0 * (u + 2.0 ** -18)
+
+
+@pytest.mark.parametrize("dim,heads", [(64, 4), (128, 4), (256, 4), (512, 20)])
+def test_infinite_sinks(q8, dim, heads):
+    """exp(sink) = 0 adds nothing; exp(sink) = inf leaves nothing for the keys: zeros, and a denominator of inf."""
+    n = 200
+    g = torch.Generator().manual_seed(dim)
+    q, k, v = (torch.randn((n, h, dim), generator=g).half().to(DEV) for h in (heads, 1, 1))
+    sinks = torch.zeros(heads, device=DEV)
+    sinks[1], sinks[2] = -float("inf"), float("inf")
+    cache = q8.KVCache.empty(q8.Q8_TYPE_F16, 1, 8, 32, 1, dim)
+    pos, table = torch.arange(n, dtype=torch.int32, device=DEV), i32([list(range(8))])
+    q8.kv_append(cache, 0, None, k.float(), v.float(), pos, torch.zeros_like(pos), table)
+    prompt = lambda s: q8.attn_prompt(q, k, v, i32([0, n]), sinks=s, want_lse=True)
+    decode = lambda s: q8.attn_decode(q[-2:].contiguous(), cache, 0, table.repeat(2, 1), i32([n, 0]), sinks=s, want_lse=True)
+    for call in (prompt, decode):
+        o, lse = call(sinks)
+        plain, plain_lse = call(None)
+        zero, zero_lse = call(torch.zeros_like(sinks))
+        assert torch.equal(o[:, 1], plain[:, 1]) and torch.equal(lse[:, 1], plain_lse[:, 1])
+        assert torch.all(o[:, 2] == 0) and torch.all(lse[:, 2] == float("inf"))
+        rest = [h for h in range(heads) if h not in (1, 2)]
+        assert torch.equal(o[:, rest], zero[:, rest]) and torch.equal(lse[:, rest], zero_lse[:, rest])
+    assert q8.q8_last_error() == 0
