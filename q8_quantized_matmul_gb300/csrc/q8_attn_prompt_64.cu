@@ -47,7 +47,9 @@ __global__ void __launch_bounds__(P64::THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     __shared__ int sh[C::THREADS / 32 + 5];
     __shared__ uint32_t tmem_slot;
-    __shared__ volatile int abort_flag, dirty[8];   // dirty[k & 7] == k + 1: tile k of this CTA had values removed
+    // dirty[k & 7] == k + 1: item k of this CTA had values removed; more: a later item's mark lies over item k's, whose
+    // rows are then looked through in any case (the guard passes items without a key, and the other query tile's, unhindered)
+    __shared__ volatile int abort_flag, dirty[8];
     uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint8_t *qs = smem, *ring = smem + 2 * C::TILE;
     uint64_t *bars = reinterpret_cast<uint64_t *>(ring + C::NST * C::STAGE);
@@ -356,7 +358,7 @@ __global__ void __launch_bounds__(P64::THREADS, 1)
                 if (p.lse && mine) p.lse[orow] = lse;
                 if (tb > ta) tile_wait(&odone[i * 2 + ((c - 1) & 1)], ((c - 1) >> 1) & 1, p.err, &abort_flag, lim);
                 tc_fence_after();
-                row_output<C::D, BF16>(p, w, tO, f, mine, orow, 0, dirty[item & 7] == item + 1 ? vp : nullptr, me.token);
+                row_output<C::D, BF16>(p, w, tO, f, mine, orow, 0, dirty[item & 7] > item ? vp : nullptr, me.token);
                 tc_fence_before();   // O is read: the next tile's first P V follows this warp's next arrival
             }
         }

@@ -44,7 +44,9 @@ __global__ void __launch_bounds__(Pw<D>::THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     __shared__ int sh[C::THREADS / 32 + 5];
     __shared__ uint32_t tmem_slot;
-    __shared__ volatile int abort_flag, dirty[8];   // dirty[k & 7] == k + 1: item k of this CTA had values removed
+    // dirty[k & 7] == k + 1: item k of this CTA had values removed; more: a later item's mark lies over item k's, whose
+    // rows are then looked through in any case (the guard passes items without a key, and the other query tile's, unhindered)
+    __shared__ volatile int abort_flag, dirty[8];
     __shared__ PromptTile w_one;
     uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint8_t *qs = smem, *ring = smem + C::QBYTES;
@@ -321,7 +323,7 @@ __global__ void __launch_bounds__(Pw<D>::THREADS, 1)
             if (p.lse && mine && d0 == 0) p.lse[orow] = lse;
             if (n1 > n0) p_v_done(nt - 1);
             tc_fence_after();
-            row_output<C::DV, BF16>(p, w, tO, f, mine, orow, d0, dirty[item & 7] == item + 1 ? vp : nullptr, me.token);
+            row_output<C::DV, BF16>(p, w, tO, f, mine, orow, d0, dirty[item & 7] > item ? vp : nullptr, me.token);
             tc_fence_before();   // O is read: the next item's first P V follows this warp's next arrival
         }
     }

@@ -119,3 +119,28 @@ def test_infinite_sinks(q8, dim, heads):
         rest = [h for h in range(heads) if h not in (1, 2)]
         assert torch.equal(o[:, rest], zero[:, rest]) and torch.equal(lse[:, rest], zero_lse[:, rest])
     assert q8.q8_last_error() == 0
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_prompt_infinite_values_beside_sequences_without_keys(q8, dim):
+    """Sequences of one key, each with an infinity among its values, among many that have queries and no key, beside one
+    of 131 000 keys, with which sequences of no key and of one lie together in the list of tiles: each row of one key is
+    that key's values."""
+    rng = np.random.default_rng(dim)
+    one = rng.random(200_000) < 0.1
+    qlen, klen = np.where(one, 1, 2), np.where(one, 1, 0)
+    qlen[77], klen[77] = 1, 131_000
+    q0, k0 = (np.concatenate([[0], np.cumsum(x)]) for x in (qlen, klen))
+    one[77] = False
+    q = torch.randn(int(q0[-1]), 1, dim, device=DEV).half()
+    k, v = (torch.randn(int(k0[-1]), 1, dim, device=DEV).half() for _ in range(2))
+    keys = torch.from_numpy(k0[:-1][one]).to(DEV)
+    rows = torch.from_numpy(q0[:-1][one]).to(DEV)
+    v[keys, 0, keys % dim] = float("inf")
+    for _ in range(3):
+        o = q8.attn_prompt(q, k, v, i32(q0), i32(k0))
+        assert torch.equal(o[rows], v[keys])
+        none = torch.ones(q.shape[0], dtype=torch.bool, device=DEV)
+        none[rows] = none[int(q0[77])] = False
+        assert torch.all(o[none] == 0) and torch.isfinite(o[int(q0[77])]).all()
+    assert q8.q8_last_error() == 0
