@@ -11,6 +11,7 @@
 //                 in flight a thread (32 forks of 3, 16 layers: 18 us with the plan, 5.4 TB/s).
 #include "q8_attn.cuh"
 #include "q8_kv.h"
+#include "q8_kv_plan.h"
 
 namespace q8 {
 namespace {
@@ -120,14 +121,14 @@ __global__ void __launch_bounds__(APPEND_THREADS) k_kv_append(const KvAppendPara
 // ---------------------------------------------------------------- plans (one CTA)
 constexpr int PLAN_THREADS = 1024;
 
-// Inclusive sum over the CTA; `total` on every thread.
-__device__ __forceinline__ int block_scan(int v, int &total, int *warp_sums) {
+// Inclusive sum over the CTA, held at cap (add_pages); `total` on every thread.
+__device__ __forceinline__ int block_scan(int v, int &total, int *warp_sums, int cap = 1 << 30) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int s = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int n = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += n;
+        if (lane >= o) s = add_pages(s, n, cap);
     }
     if (lane == 31) warp_sums[warp] = s;
     __syncthreads();
@@ -136,19 +137,15 @@ __device__ __forceinline__ int block_scan(int v, int &total, int *warp_sums) {
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int n = __shfl_up_sync(0xffffffffu, w, o);
-            if (lane >= o) w += n;
+            if (lane >= o) w = add_pages(w, n, cap);
         }
         warp_sums[lane] = w;
     }
     __syncthreads();
-    const int r = s + (warp ? warp_sums[warp - 1] : 0);
+    const int r = warp ? add_pages(s, warp_sums[warp - 1], cap) : s;
     total = warp_sums[31];
     __syncthreads();   // warp_sums is free again
     return r;
-}
-
-__device__ __forceinline__ int pages_of(int64_t tokens, uint32_t shift) {
-    return (int)((tokens + (1 << shift) - 1) >> shift);
 }
 
 // A row id of a request, or -1 (out of range: raises).
@@ -181,13 +178,11 @@ template <bool FORK> __device__ __forceinline__ int need_of(const KvPagesParams 
         if (row_id(p, p.dst[i]) < 0) return 0;
         return (n & ((1 << p.c.page_shift) - 1)) ? 1 : 0;
     } else {
-        const int64_t grown = (int64_t)n + p.dst[i];
         if (p.dst[i] < 0) {
             raise_error(p.err, DEV_ERANGE);
             return 0;
         }
-        if (grown > ((int64_t)p.max_pages << p.c.page_shift)) return -1;
-        return pages_of(grown, p.c.page_shift) - pages_of(n, p.c.page_shift);
+        return new_pages(n, p.dst[i], p.max_pages, p.c.page_shift, p.c.n_pages);
     }
 }
 
@@ -199,7 +194,8 @@ template <bool FORK> __global__ void __launch_bounds__(PLAN_THREADS) k_kv_grant_
     grid_dep_wait();
     if (threadIdx.x == 0) refused = 0;
     __syncthreads();
-    int64_t need = 0;
+    const int cap = (int)p.c.n_pages + 1;
+    int need = 0;
     for (uint32_t b = 0; b < p.n; b += PLAN_THREADS) {
         const uint32_t i = b + threadIdx.x;
         int v = i < p.n ? need_of<FORK>(p, i) : 0;
@@ -208,11 +204,11 @@ template <bool FORK> __global__ void __launch_bounds__(PLAN_THREADS) k_kv_grant_
             v = 0;
         }
         int total;
-        const int s = block_scan(v, total, ws);
-        if (i < p.n) p.off[i] = need + s - v > INT32_MAX ? INT32_MAX : (int)(need + s - v);
-        need += total;
+        const int s = block_scan(v, total, ws, cap);
+        if (i < p.n) p.off[i] = add_pages(need, s - v, cap);
+        need = add_pages(need, total, cap);
     }
-    int64_t found = 0;
+    int found = 0;
     for (uint32_t b = 0; b < p.c.n_pages && found < need; b += PLAN_THREADS * 4) {
         const uint32_t i = b + threadIdx.x * 4;
         int z[4], v = 0;
@@ -222,7 +218,7 @@ template <bool FORK> __global__ void __launch_bounds__(PLAN_THREADS) k_kv_grant_
             v += z[e];
         }
         int total;
-        int64_t at = found + block_scan(v, total, ws) - v;
+        int at = found + block_scan(v, total, ws) - v;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             if (z[e]) {
