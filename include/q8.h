@@ -422,7 +422,8 @@ int q8_attn_prompt(void *out, int out_type, float *lse, const void *q, const voi
  * sequences.  New pages are the free ones of lowest index, in the order of the
  * requests, so results do not depend on timing.  Row ids (seqs, src, dst) are int32
  * device arrays; a negative one is skipped, one outside n_rows raises Q8_ERANGE and is
- * skipped.  A row may appear once in seqs / dst, and not as src and dst of one call.
+ * skipped.  A row may appear once in seqs / dst, and not as src and dst of one call (else the
+ * entries and counts that its requests concern are undefined; nothing else is touched).
  *   q8_kv_reserve  gives row seqs[i] the pages for n_new[i] more tokens and adds
  *                  n_new[i] to its length.
  *   q8_kv_fork     makes row dst[i] a copy of row src[i]: whole pages are shared (refs

@@ -169,19 +169,22 @@ __device__ __forceinline__ int row_len(const KvPagesParams &p, int row) {
     return (int)n;
 }
 
-// New pages that request i needs; -1: it cannot be granted at all.
-template <bool FORK> __device__ __forceinline__ int need_of(const KvPagesParams &p, uint32_t i) {
+// New pages that request i needs; -1: it cannot be granted at all.  had: its row's length, -1: nothing to do.
+template <bool FORK> __device__ __forceinline__ int need_of(const KvPagesParams &p, uint32_t i, int &had) {
+    had = -1;
     const int row = row_id(p, p.src[i]);
     if (row < 0) return 0;
     const int n = row_len(p, row);
     if constexpr (FORK) {
         if (row_id(p, p.dst[i]) < 0) return 0;
+        had = n;
         return (n & ((1 << p.c.page_shift) - 1)) ? 1 : 0;
     } else {
         if (p.dst[i] < 0) {
             raise_error(p.err, DEV_ERANGE);
             return 0;
         }
+        had = n;
         return new_pages(n, p.dst[i], p.max_pages, p.c.page_shift, p.c.n_pages);
     }
 }
@@ -198,7 +201,9 @@ template <bool FORK> __global__ void __launch_bounds__(PLAN_THREADS) k_kv_grant_
     int need = 0;
     for (uint32_t b = 0; b < p.n; b += PLAN_THREADS) {
         const uint32_t i = b + threadIdx.x;
-        int v = i < p.n ? need_of<FORK>(p, i) : 0;
+        int had;
+        int v = i < p.n ? need_of<FORK>(p, i, had) : 0;
+        if (i < p.n) p.had[i] = had;
         if (v < 0) {
             refused = 1;
             v = 0;
@@ -322,16 +327,16 @@ __global__ void __launch_bounds__(COPY_THREADS) k_kv_copy(const KvPagesParams p)
     copy_pages(p.c, p.src, p.dst, p.n, p.err);
 }
 
-// Rows of granted reservations: entries of the new pages, their counts, the lengths.
+// Rows of granted reservations: entries of the new pages, their counts, the lengths.  Both apply kernels go by the
+// lengths of the plan: a row that a call names twice, against the rules, ends up with one of its results and stray counts,
+// but nothing past the planned entries and pages is touched.
 __global__ void __launch_bounds__(COPY_THREADS) k_kv_reserve_apply(const KvPagesParams p) {
     grid_dep_wait();
     if (!p.plan[1]) return;
     for (uint32_t i = blockIdx.x; i < p.n; i += gridDim.x) {
-        const int32_t row = p.src[i], more = p.dst[i];
-        if (row < 0 || (uint32_t)row >= p.n_rows || more <= 0) continue;
-        const int n = row_len(p, row);
+        const int32_t row = p.src[i], more = p.dst[i], n = p.had[i];
+        if (n < 0 || more == 0) continue;
         const int had = pages_of(n, p.c.page_shift), now = pages_of((int64_t)n + more, p.c.page_shift);
-        __syncthreads();   // every thread has read the length
         for (int s = had + threadIdx.x; s < now; s += COPY_THREADS) {
             const int page = p.fresh[p.off[i] + s - had];
             p.table[(uint64_t)row * p.table_stride + s] = page;
@@ -346,9 +351,9 @@ __global__ void __launch_bounds__(COPY_THREADS) k_kv_fork_apply(const KvPagesPar
     grid_dep_wait();
     if (!p.plan[1]) return;
     for (uint32_t i = blockIdx.x; i < p.n; i += gridDim.x) {
-        const int32_t a = p.src[i], b = p.dst[i];
-        if (a < 0 || b < 0 || (uint32_t)a >= p.n_rows || (uint32_t)b >= p.n_rows) continue;
-        const int n = row_len(p, a), whole = n >> p.c.page_shift;
+        const int32_t a = p.src[i], b = p.dst[i], n = p.had[i];
+        if (n < 0) continue;
+        const int whole = n >> p.c.page_shift;
         const bool part = (n & ((1 << p.c.page_shift) - 1)) != 0;
         const int32_t *src = p.table + (uint64_t)a * p.table_stride;
         int32_t *dst = p.table + (uint64_t)b * p.table_stride;
@@ -371,10 +376,8 @@ __global__ void __launch_bounds__(COPY_THREADS) k_kv_fork_apply(const KvPagesPar
     const uint32_t per = p.c.n_layers * 2 * chunks;
     for (uint64_t w = blockIdx.x; w < (uint64_t)p.n * per; w += gridDim.x) {
         const uint32_t i = (uint32_t)(w / per), r = (uint32_t)(w % per), lv = r / chunks, o0 = r % chunks * COPY_CHUNK;
-        const int32_t a = p.src[i], b = p.dst[i];
-        if (a < 0 || b < 0 || (uint32_t)a >= p.n_rows || (uint32_t)b >= p.n_rows) continue;
-        const int n = row_len(p, a);
-        if (!(n & ((1 << p.c.page_shift) - 1))) continue;
+        const int32_t a = p.src[i], n = p.had[i];
+        if (n < 0 || !(n & ((1 << p.c.page_shift) - 1))) continue;
         const int32_t from = p.table[(uint64_t)a * p.table_stride + (n >> p.c.page_shift)], to = p.fresh[p.off[i]];
         if (from < 0 || (uint32_t)from >= p.c.n_pages) {
             if (threadIdx.x == 0) raise_error(p.err, DEV_ERANGE);
@@ -461,7 +464,7 @@ cudaError_t launch_kv_append(KvAppendParams p, int num_sms, cudaStream_t st) {
 }
 
 size_t kv_pages_scratch(uint32_t n, uint32_t n_pages) {
-    return 256 + up256((size_t)n_pages * 4) * 3 + up256((size_t)(n > n_pages ? n : n_pages) * 4);
+    return 256 + up256((size_t)n_pages * 4) * 3 + up256((size_t)(n > n_pages ? n : n_pages) * 4) + up256((size_t)n * 4);
 }
 
 void kv_pages_carve(KvPagesParams &p, void *scratch) {
@@ -472,6 +475,7 @@ void kv_pages_carve(KvPagesParams &p, void *scratch) {
     p.to = reinterpret_cast<int32_t *>(b + 256 + list);
     p.fresh = reinterpret_cast<int32_t *>(b + 256 + 2 * list);
     p.off = reinterpret_cast<int32_t *>(b + 256 + 3 * list);
+    p.had = reinterpret_cast<int32_t *>(b + 256 + 3 * list + up256((size_t)(p.n > p.c.n_pages ? p.n : p.c.n_pages) * 4));
 }
 
 cudaError_t launch_kv_reserve(const KvPagesParams &p, int num_sms, cudaStream_t st) {

@@ -49,6 +49,7 @@ struct KvPagesParams {
     int32_t *plan;                        // [0] moves in the lists, [1] requests granted
     int32_t *from, *to;                   // page moves
     int32_t *off;                         // reserve / fork: first new page of a request in `fresh`
+    int32_t *had;                         // reserve / fork: the row's (fork: source's) length when planned, -1: skipped
     int32_t *fresh;                       // reserve / fork: new pages, ascending
     int *err;
 };

@@ -35,3 +35,28 @@ def test_reserve_sums_beyond_32_bits(q8, n_pages):
     assert q8.q8_last_error() == 0 and table[5, :4].tolist() == [0, 1, 2, -1] and table[9, :2].tolist() == [3, -1]
     del table
     torch.cuda.empty_cache()
+
+
+def test_requests_that_name_a_row_twice_touch_nothing_else(q8):
+    """Against the rules of q8.h: the rows and pages concerned may come out either way, all others stay."""
+    page, n_pages, width, rows = 16, 40, 2, 6
+    for _ in range(20):
+        cache = q8.KVCache.empty(q8.Q8_TYPE_F16, 1, n_pages, page, 1, 64)
+        wide = torch.full((rows + 4, width), 12345, dtype=torch.int32, device=DEV)      # rows beyond the table's
+        wide[:rows] = -1
+        counts = torch.full((n_pages + 64,), 777, dtype=torch.int32, device=DEV)
+        counts[:n_pages] = 0
+        table, refs, lens = wide[:rows], counts[:n_pages], torch.zeros(rows, dtype=torch.int32, device=DEV)
+        q8.kv_reserve(cache, table, lens, refs, i32([0, 5]), i32([7, 5]))
+        before = wide.clone()
+        # each fits its row of 32 tokens alone, not after the other, and needs no page or one
+        q8.kv_reserve(cache, table, lens, refs, i32([5, 5, 5, 5] * 8), i32([11, 8, 20, 27] * 8))
+        assert q8.q8_last_error() in (0, q8.Q8_ERANGE)
+        assert torch.equal(wide[:5], before[:5]) and torch.equal(wide[rows:], before[rows:])
+        assert torch.all(counts[n_pages:] == 777) and int(table.max()) < n_pages and int(table.min()) >= -1
+        assert 5 <= int(lens[5]) <= 32
+        # a source that is overwritten by the same call
+        q8.kv_fork(cache, table, lens, refs, i32([0, 5, 0]), i32([5, 1, 1]))
+        assert q8.q8_last_error() in (0, q8.Q8_ERANGE)
+        assert torch.equal(wide[0], before[0]) and torch.equal(wide[2:5], before[2:5]) and torch.equal(wide[rows:], before[rows:])
+        assert torch.all(counts[n_pages:] == 777) and int(table.max()) < n_pages and int(table.min()) >= -1
