@@ -405,7 +405,8 @@ int q8_attn_decode(void *out, int out_type, float *lse, const void *q, uint64_t 
  *              Strides are multiples of 8, all pointers 16-byte aligned.
  *   q_start    in: int32 [n_seq + 1], k_start the same or NULL (= q_start); rising,
  *              from 0 to at most n_q / n_k.  Values outside are cut to the range and
- *              raise Q8_ERANGE; rows of no sequence are not written.
+ *              raise Q8_ERANGE, as do starts that fall, after which any row may be left
+ *              unwritten; rows of no sequence are not written.
  *   out        out: [n_q][n_heads][head_dim], lse [n_q][n_heads] or NULL.
  * Rows of other sequences and keys a query may not see never change its result,
  * whatever they hold.

@@ -67,11 +67,33 @@ __device__ __forceinline__ int tile_cost(const PromptTile &w, uint32_t window) {
 __global__ void __launch_bounds__(LIST_THREADS) k_attn_prompt_list(const AttnPromptParams p) {
     __shared__ int bin[LIST_BINS];
     __shared__ int wsum[32];
+    __shared__ unsigned long long all;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     grid_dep_wait();
     const int32_t *ks = p.k_start ? p.k_start : p.q_start;
     bin[tid] = 0;
+    if (tid == 0) all = 0;
     __syncthreads();
+    // Rising starts give at most list_cap tiles.  Starts that fall in between may give 2^20 sequences all rows each: more
+    // than the list, 32 bits or one CTA's time hold, and no tile of them is worked on.
+    {
+        uint64_t mine = 0;
+        for (uint32_t s = tid; s < p.n_seq; s += LIST_THREADS) {
+            const int n = prompt_bound(p.q_start[s + 1], p.n_q) - prompt_bound(p.q_start[s], p.n_q);
+            if (n > 0) mine += (uint32_t)(n + p.tile_tokens - 1) / (uint32_t)p.tile_tokens;
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+        if (lane == 0 && mine) atomicAdd(&all, mine);
+        __syncthreads();
+        if (all > p.list_cap) {
+            if (tid == 0) {
+                *reinterpret_cast<int *>(p.list) = 0;
+                raise_error(p.err, DEV_ERANGE);
+            }
+            return;
+        }
+    }
     PromptTile *list = reinterpret_cast<PromptTile *>(p.list + 1);
     auto each = [&](auto f) {   // a lane per sequence; the warp together for long ones, a lane per tile
         const uint32_t per = min(32u, (p.n_seq + 31) / 32);   // sequences of a warp: few ones are spread over the warps
@@ -122,11 +144,10 @@ __global__ void __launch_bounds__(LIST_THREADS) k_attn_prompt_list(const AttnPro
     int before = 0;
     for (int k = 0; k < warp; ++k) before += wsum[k];
     bin[tid] = before + sum - mine;
-    if (tid == LIST_THREADS - 1) *reinterpret_cast<int *>(p.list) = min(before + sum, (int)p.list_cap);
+    if (tid == LIST_THREADS - 1) *reinterpret_cast<int *>(p.list) = before + sum;
     __syncthreads();
     each([&](const PromptTile &w, int b) {
-        const int at = atomicAdd(&bin[b], 1);
-        if (at < (int)p.list_cap) list[at] = w;   // starts that do not rise may give more tiles than rows
+        list[atomicAdd(&bin[b], 1)] = w;
     });
 }
 

@@ -144,3 +144,21 @@ def test_prompt_infinite_values_beside_sequences_without_keys(q8, dim):
         none[rows] = none[int(q0[77])] = False
         assert torch.all(o[none] == 0) and torch.isfinite(o[int(q0[77])]).all()
     assert q8.q8_last_error() == 0
+
+
+@pytest.mark.parametrize("tokens,seqs", [(3000, 400), (1 << 21, 1 << 20)])
+def test_prompt_starts_that_fall(q8, tokens, seqs):
+    """Starts that go back and forth make each second sequence all the rows, 2^32 tiles in the larger case: an error,
+    soon, nothing outside the outputs, and the next call is right."""
+    q = torch.randn(tokens, 2, 64, device=DEV).half()
+    k = torch.randn(tokens, 1, 64, device=DEV).half()
+    n = tokens // 100
+    small = i32([0, n // 3, n])
+    ref = q8.attn_prompt(q[:n], k, k, small)
+    start = torch.zeros(seqs + 1, dtype=torch.int32, device=DEV)
+    start[1::2] = tokens
+    for _ in range(2):
+        q8.attn_prompt(q, k, k, start)
+        assert q8.q8_last_error() == q8.Q8_ERANGE
+    assert torch.equal(q8.attn_prompt(q[:n], k, k, small), ref)
+    assert q8.q8_last_error() == 0
