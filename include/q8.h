@@ -37,7 +37,9 @@
  *   - The library keeps a per-device grow-only scratch buffer for quantised
  *     activations, routing tables and the pieces of split attention (the
  *     pages' reused aligned Q8 scratch).  Growing it allocates: make a first
- *     call of each size before a stream capture.
+ *     call of each size before a stream capture.  A graph keeps the memory that
+ *     its calls were captured with, whatever later calls need: such memory is
+ *     held until q8_release(), after which the graph must not run.
  *     Calls that use scratch must not run concurrently on different streams
  *     of the same device.  q8_release() frees it.
  *   - Kernels are launched with programmatic stream serialisation: a kernel
@@ -536,7 +538,8 @@ int q8_last_error(void *stream);
 const char *q8_last_cuda_error(void);
 
 /* Scratch bytes currently held on the current device, the staging buffer of
- * q8_matmul_host and the counters of q8_attn_decode included (0 if none). */
+ * q8_matmul_host, the counters of q8_attn_decode and what is kept for graphs
+ * included (0 if none). */
 uint64_t q8_scratch_bytes(void);
 
 /* Frees the scratch and staging buffers of every device (synchronises each first). */

@@ -1,6 +1,7 @@
 // q8_api.cu -- the C ABI (include/q8.h): host-side validation, per-device
 // scratch and error word, and dispatch to the kernels.
 #include <cstdint>
+#include <cstdlib>
 #include <cstring>
 #include <mutex>
 
@@ -17,16 +18,27 @@ namespace {
 constexpr int MAX_DEVICES = 64;
 constexpr uint32_t MAX_EXPERTS = 16384;
 
+// Grow-only device memory.  A graph holds the address that a captured call was given, so from the first captured
+// call on the buffer is not freed when a larger one takes its place, but kept for the graph.
+struct Buffer {
+    void *p = nullptr;
+    size_t bytes = 0;
+    bool captured = false;
+};
+struct Kept {
+    void *p;
+    size_t bytes;
+    Kept *next;
+};
+
 struct DeviceState {
     bool ready = false;
     int num_sms = 0;
     int *err = nullptr;          // device address of g_q8_device_error
-    void *scratch = nullptr;
-    size_t scratch_bytes = 0;
-    void *stage = nullptr;       // device copies of host activations and results (q8_matmul_host)
-    size_t stage_bytes = 0;
-    int *counters = nullptr;     // attention: pieces that have arrived, one per unit, zero between calls
-    size_t counter_bytes = 0;
+    Buffer scratch;
+    Buffer stage;                // device copies of host activations and results (q8_matmul_host)
+    Buffer counters;             // attention: pieces that have arrived, one int per unit, zero between calls
+    Kept *kept = nullptr;        // replaced buffers that graphs may use
 };
 
 std::mutex g_mutex;
@@ -129,46 +141,58 @@ int get_device(DeviceState **out) {
     return Q8_OK;
 }
 
-// Grow-only device buffer of at least `bytes`.  Growing synchronises the device
-// (cudaFree does), so a call that grows it must not overlap work of another
-// stream that still uses the old buffer -- scratch users are single-stream.
-int reserve_buffer(void **buf, size_t *have, size_t bytes) {
-    if (bytes <= *have) return Q8_OK;
-    if (g_fail_next_alloc > 0) {
-        --g_fail_next_alloc;
-        return Q8_ENOMEM;
-    }
-    size_t want = bytes + bytes / 4;
-    want = (want + ((size_t)1 << 20) - 1) & ~(((size_t)1 << 20) - 1);
-    if (*buf) {
-        cudaFree(*buf);
-        *buf = nullptr;
-        *have = 0;
-    }
-    void *p = nullptr;
-    if (cudaMalloc(&p, want) != cudaSuccess) {
+bool capturing(cudaStream_t st) {
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(st, &cs) != cudaSuccess) {
         cudaGetLastError();
-        return Q8_ENOMEM;
+        return false;
     }
-    *buf = p;
-    *have = want;
+    return cs != cudaStreamCaptureStatusNone;
+}
+
+// At least `bytes` in a buffer, for a call on `st`.  Growing one that no graph uses synchronises the device (cudaFree
+// does), so a call that grows it must not overlap work of another stream that still uses the old memory -- scratch
+// users are single-stream.
+int reserve_buffer(DeviceState *s, Buffer &b, size_t bytes, cudaStream_t st) {
+    if (bytes > b.bytes) {
+        if (g_fail_next_alloc > 0) {
+            --g_fail_next_alloc;
+            return Q8_ENOMEM;
+        }
+        size_t want = bytes + bytes / 4;
+        want = (want + ((size_t)1 << 20) - 1) & ~(((size_t)1 << 20) - 1);
+        if (b.p && b.captured) {
+            Kept *k = static_cast<Kept *>(malloc(sizeof(Kept)));
+            if (!k) return Q8_ENOMEM;
+            *k = Kept{b.p, b.bytes, s->kept};
+            s->kept = k;
+        } else if (b.p) {
+            cudaFree(b.p);
+        }
+        b = Buffer{};
+        void *p = nullptr;
+        if (cudaMalloc(&p, want) != cudaSuccess) {
+            cudaGetLastError();
+            return Q8_ENOMEM;
+        }
+        b.p = p;
+        b.bytes = want;
+    }
+    if (!b.captured && b.p) b.captured = capturing(st);
     return Q8_OK;
 }
 
-int reserve_scratch(DeviceState *s, size_t bytes) { return reserve_buffer(&s->scratch, &s->scratch_bytes, bytes); }
+int reserve_scratch(DeviceState *s, size_t bytes, cudaStream_t st) { return reserve_buffer(s, s->scratch, bytes, st); }
 
 // At least n counters.  New ones are cleared on `st`; a call leaves every counter it used at zero.
 int reserve_counters(DeviceState *s, size_t n, cudaStream_t st) {
-    if (n * sizeof(int) <= s->counter_bytes) return Q8_OK;
-    void *buf = s->counters;
-    const int rc = reserve_buffer(&buf, &s->counter_bytes, n * sizeof(int));
-    s->counters = static_cast<int *>(buf);
-    if (rc) return rc;
-    const cudaError_t e = cudaMemsetAsync(buf, 0, s->counter_bytes, st);
+    const bool grows = n * sizeof(int) > s->counters.bytes;
+    const int rc = reserve_buffer(s, s->counters, n * sizeof(int), st);
+    if (rc || !grows) return rc;
+    const cudaError_t e = cudaMemsetAsync(s->counters.p, 0, s->counters.bytes, st);
     if (e != cudaSuccess) {   // unusable until cleared: the next call allocates again
-        cudaFree(buf);
-        s->counters = nullptr;
-        s->counter_bytes = 0;
+        cudaFree(s->counters.p);
+        s->counters = Buffer{};
         cudaGetLastError();
     }
     return status_of(e);
@@ -329,9 +353,9 @@ int run_tc(DeviceState *s, float *out, const void *W, uint64_t in_dim, uint64_t 
     const size_t need = (expand ? align256(out_dim * in_dim * 2) + align256(nb * m_ld * 4) : 0) +
                         align256(n_ld * in_dim * 2) + align256(nb * n_ld * 4) +
                         (ksplit > 1 ? align256(ksplit * n_tok * out_dim * 4) : 0);
-    int rc = reserve_scratch(s, need);
+    int rc = reserve_scratch(s, need, st);
     if (rc) return rc;
-    Carver cv(s->scratch);
+    Carver cv(s->scratch.p);
     const __half *a16 = packed ? a16_pre : nullptr;
     const float *dwT = packed ? dwT_pre : nullptr;
     __half *a16_x = expand ? cv.take<__half>(out_dim * in_dim * 2) : nullptr;
@@ -625,8 +649,8 @@ static int dispatch_matmul(DeviceState *s, float *out, const void *W, uint64_t i
     if (x && (!host_io || n_tok <= 2) && nb % 8 == 0 && q8::gemv_fuses_quantiser(n_tok, nb))
         return run_dense(s, out, W, in_dim, out_dim, nullptr, nullptr, x, n_tok, st);
     const uint64_t n_pad = (n_tok + 15) & ~(uint64_t)15;
-    if ((rc = reserve_scratch(s, planes_bytes(n_pad, in_dim)))) return rc;
-    Carver cv(s->scratch);
+    if ((rc = reserve_scratch(s, planes_bytes(n_pad, in_dim), st))) return rc;
+    Carver cv(s->scratch.p);
     int8_t *qx = cv.take<int8_t>(n_pad * in_dim);
     float *dx = cv.take<float>(n_pad * nb * sizeof(float));
     cudaError_t e = x ? q8::launch_quantize_planes(qx, dx, x, in_dim, n_pad, nullptr, n_tok, s->num_sms, st, host_io)
@@ -692,8 +716,8 @@ int q8_matmul_host(float *out_host, const void *W, uint64_t in_dim, uint64_t out
     float *od_host = static_cast<float *>(mapped_host_pointer(out_host));
     if (xd_host && od_host) return dispatch_matmul(s, od_host, W, in_dim, out_dim, xd_host, nullptr, n_tok, st, true);
     const size_t x_bytes = n_tok * in_dim * sizeof(float), out_bytes = n_tok * out_dim * sizeof(float);
-    if ((rc = reserve_buffer(&s->stage, &s->stage_bytes, align256(x_bytes) + align256(out_bytes)))) return rc;
-    Carver cv(s->stage);
+    if ((rc = reserve_buffer(s, s->stage, align256(x_bytes) + align256(out_bytes), st))) return rc;
+    Carver cv(s->stage.p);
     float *xd = cv.take<float>(x_bytes);
     float *od = cv.take<float>(out_bytes);
     if ((rc = status_of(cudaMemcpyAsync(xd, x_host, x_bytes, cudaMemcpyHostToDevice, st)))) return rc;
@@ -733,8 +757,9 @@ int q8_moe_matmul(float *out, const void *W_experts, uint32_t n_expert, uint64_t
     c.x_per_pair = x_per_pair;
     c.n_tok = n_tok;
     const MoeLayout L = moe_layout(c);
-    if ((rc = reserve_scratch(s, L.need))) return rc;
-    return moe_run(s, c, L, s->scratch, static_cast<cudaStream_t>(stream));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if ((rc = reserve_scratch(s, L.need, st))) return rc;
+    return moe_run(s, c, L, s->scratch.p, st);
 }
 
 int q8_swiglu(float *mid, const float *gate, const float *up, uint64_t n, float limit, void *stream) {
@@ -786,9 +811,9 @@ static int ffn_gemv_run(DeviceState *s, const MoeCall &gu, const MoeLayout &L, c
     if ((L.nb % 8) || (nbm % 8) || L.tc_cap) return Q8_EINVAL;
     int rc;
     const size_t region = align256(L.need);
-    if ((rc = reserve_scratch(s, region + planes_bytes(L.max_rows, mid_dim) + align256(L.n_pairs * out_dim * 4))))
+    if ((rc = reserve_scratch(s, region + planes_bytes(L.max_rows, mid_dim) + align256(L.n_pairs * out_dim * 4), st)))
         return rc;
-    Carver cv(s->scratch);
+    Carver cv(s->scratch.p);
     int32_t *counts = cv.take<int32_t>(gu.n_expert * 4);
     int32_t *row0_of = cv.take<int32_t>(gu.n_expert * 4);
     uint8_t *plans = cv.take<uint8_t>(q8::ROUTE_CLASSES * L.plan_bytes);
@@ -797,7 +822,7 @@ static int ffn_gemv_run(DeviceState *s, const MoeCall &gu, const MoeLayout &L, c
     int32_t *dst_row = cv.take<int32_t>(L.n_pairs * 4);
     int8_t *qx = cv.take<int8_t>(L.max_rows * gu.in_dim);
     float *dx = cv.take<float>(L.max_rows * L.nb * sizeof(float));
-    Carver cv2(static_cast<uint8_t *>(s->scratch) + region);
+    Carver cv2(static_cast<uint8_t *>(s->scratch.p) + region);
     int8_t *qmid = cv2.take<int8_t>(L.max_rows * mid_dim);
     float *dmid = cv2.take<float>(L.max_rows * nbm * sizeof(float));
     float *y = cv2.take<float>(L.n_pairs * out_dim * 4);
@@ -910,8 +935,8 @@ int q8_moe_ffn(float *out, const void *W_gate, const void *W_up, const void *W_d
     // scratch: the routed calls' region (reused by both), then gate, up, mid and y
     const size_t region = align256(Lgu.need > Ldn.need ? Lgu.need : Ldn.need);
     const size_t mid_bytes = align256(n_pairs * mid_dim * 4);
-    if ((rc = reserve_scratch(s, region + 3 * mid_bytes + align256(n_pairs * out_dim * 4)))) return rc;
-    Carver cv(static_cast<uint8_t *>(s->scratch) + region);
+    if ((rc = reserve_scratch(s, region + 3 * mid_bytes + align256(n_pairs * out_dim * 4), st))) return rc;
+    Carver cv(static_cast<uint8_t *>(s->scratch.p) + region);
     float *gate = cv.take<float>(n_pairs * mid_dim * 4);
     float *up = cv.take<float>(n_pairs * mid_dim * 4);
     float *mid = cv.take<float>(n_pairs * mid_dim * 4);
@@ -925,11 +950,11 @@ int q8_moe_ffn(float *out, const void *W_gate, const void *W_up, const void *W_d
         gu.pair = true;
         gu.limit = limit;
         gu.out[0] = mid;
-        if ((rc = moe_run(s, gu, Lgu, s->scratch, st))) return rc;
+        if ((rc = moe_run(s, gu, Lgu, s->scratch.p, st))) return rc;
     } else {
         gu.out[0] = gate;
         gu.out[1] = up;
-        if ((rc = moe_run(s, gu, Lgu, s->scratch, st))) return rc;
+        if ((rc = moe_run(s, gu, Lgu, s->scratch.p, st))) return rc;
         // a pair with a bad id: its gate row is zero, its up row unwritten; mid is zeroed
         if ((rc = status_of(q8::launch_swiglu(mid, gate, up, n_pairs * mid_dim, limit, expert_ids, n_expert, mid_dim,
                                               s->num_sms, st))))
@@ -937,7 +962,7 @@ int q8_moe_ffn(float *out, const void *W_gate, const void *W_up, const void *W_d
     }
     dn.x = mid;
     dn.out[0] = y;
-    if ((rc = moe_run(s, dn, Ldn, s->scratch, st))) return rc;
+    if ((rc = moe_run(s, dn, Ldn, s->scratch.p, st))) return rc;
     return status_of(q8::launch_combine(out, y, expert_weights, n_tok, k, out_dim, s->num_sms, st));
 }
 
@@ -1017,8 +1042,8 @@ int q8_kq_matmul(float *out, const void *W, int fmt, uint64_t in_dim, uint64_t o
     DeviceState *s;
     if ((rc = get_device(&s))) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if ((rc = reserve_scratch(s, q8k_planes_bytes(n_tok, in_dim)))) return rc;
-    Carver cv(s->scratch);
+    if ((rc = reserve_scratch(s, q8k_planes_bytes(n_tok, in_dim), st))) return rc;
+    Carver cv(s->scratch.p);
     const Q8kPlanes q = take_q8k_planes(cv, n_tok, in_dim);
     cudaError_t e = q8::launch_quantize_q8k(q.qx, q.dx, q.xs, nullptr, x, in_dim, n_tok, s->num_sms, st);
     if (e != cudaSuccess) return status_of(e);
@@ -1072,8 +1097,8 @@ int q8_kq_moe_matmul(float *out, const void *W_experts, int fmt, uint32_t n_expe
     const size_t plan_bytes = q8::route_plan_bytes(n_expert);
     const size_t need = align256(n_expert * 4) * 2 + q8::ROUTE_CLASSES * align256(plan_bytes) +
                         align256(max_rows * 4) * 2 + q8k_planes_bytes(x_rows, in_dim);
-    if ((rc = reserve_scratch(s, need))) return rc;
-    Carver cv(s->scratch);
+    if ((rc = reserve_scratch(s, need, st))) return rc;
+    Carver cv(s->scratch.p);
     int32_t *counts = cv.take<int32_t>(n_expert * 4);
     int32_t *row0_of = cv.take<int32_t>(n_expert * 4);
     uint8_t *plans = cv.take<uint8_t>(q8::ROUTE_CLASSES * plan_bytes);
@@ -1282,8 +1307,8 @@ int q8_attn_decode(void *out, int out_type, float *lse, const void *q, uint64_t 
         p.mtiles = (p.group + 63) / 64;
         const size_t slots = 2 * (size_t)s->num_sms, units = (size_t)n_seq * c->n_kv_heads * p.mtiles;
         const size_t part = align256(slots * 64 * c->head_dim * sizeof(float)), ml = align256(slots * 64 * sizeof(float2));
-        if ((rc = reserve_scratch(s, part + ml + align256(units * sizeof(int4))))) return rc;
-        Carver cv(s->scratch);
+        if ((rc = reserve_scratch(s, part + ml + align256(units * sizeof(int4)), st))) return rc;
+        Carver cv(s->scratch.p);
         p.part = cv.take<float>(part);
         p.part_ml = cv.take<float2>(ml);
         p.units = cv.take<int4>(units * sizeof(int4));
@@ -1294,12 +1319,12 @@ int q8_attn_decode(void *out, int out_type, float *lse, const void *q, uint64_t 
     const size_t slots = (size_t)grid * 2;
     if ((rc = reserve_counters(s, (size_t)n_seq * c->n_kv_heads * p.mtiles + slots, st))) return rc;
     const size_t part = align256(slots * 16 * c->head_dim * sizeof(float)), ml = align256(slots * 16 * 2 * sizeof(float2));
-    if ((rc = reserve_scratch(s, part + 2 * ml))) return rc;
-    Carver cv(s->scratch);
+    if ((rc = reserve_scratch(s, part + 2 * ml, st))) return rc;
+    Carver cv(s->scratch.p);
     p.part = cv.take<float>(part);
     p.part_ml = cv.take<float2>(ml);
     p.group_ml = cv.take<float2>(ml);
-    p.counters = s->counters;
+    p.counters = static_cast<int *>(s->counters.p);
     return status_of(q8::launch_attn_decode(p, grid, st));
 }
 
@@ -1352,9 +1377,9 @@ int q8_attn_prompt(void *out, int out_type, float *lse, const void *q, const voi
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     q8::attn_prompt_tiling(p, s->num_sms);
     const size_t list = q8::attn_prompt_list_bytes(p, s->num_sms);
-    if ((rc = reserve_scratch(s, list))) return rc;
+    if ((rc = reserve_scratch(s, list, st))) return rc;
     take_expiry(p.wait_ns, p.withhold);
-    return status_of(q8::launch_attn_prompt(p, list ? s->scratch : nullptr, s->num_sms, st));
+    return status_of(q8::launch_attn_prompt(p, list ? s->scratch.p : nullptr, s->num_sms, st));
 }
 
 // Arguments that the page calls share; fills p but for its scratch.
@@ -1386,13 +1411,13 @@ static int check_requests(q8::KvPagesParams &p, int32_t *lens, int32_t *refs, co
 }
 
 // The device, and the plan's scratch.
-static int pages_device(q8::KvPagesParams &p, DeviceState **s, bool plan) {
+static int pages_device(q8::KvPagesParams &p, DeviceState **s, bool plan, cudaStream_t st) {
     int rc = get_device(s);
     if (rc) return rc;
     p.err = (*s)->err;
     if (!plan) return Q8_OK;
-    if ((rc = reserve_scratch(*s, q8::kv_pages_scratch(p.n, p.c.n_pages)))) return rc;
-    q8::kv_pages_carve(p, (*s)->scratch);
+    if ((rc = reserve_scratch(*s, q8::kv_pages_scratch(p.n, p.c.n_pages), st))) return rc;
+    q8::kv_pages_carve(p, (*s)->scratch.p);
     return Q8_OK;
 }
 
@@ -1405,7 +1430,7 @@ int q8_kv_reserve(const q8_kv_cache *c, int32_t *table, uint64_t table_stride, u
     if (n == 0) return Q8_OK;
     std::lock_guard<std::mutex> lk(g_mutex);
     DeviceState *s;
-    if ((rc = pages_device(p, &s, true))) return rc;
+    if ((rc = pages_device(p, &s, true, static_cast<cudaStream_t>(stream)))) return rc;
     return status_of(q8::launch_kv_reserve(p, s->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
@@ -1418,7 +1443,7 @@ int q8_kv_fork(const q8_kv_cache *c, int32_t *table, uint64_t table_stride, uint
     if (n == 0) return Q8_OK;
     std::lock_guard<std::mutex> lk(g_mutex);
     DeviceState *s;
-    if ((rc = pages_device(p, &s, true))) return rc;
+    if ((rc = pages_device(p, &s, true, static_cast<cudaStream_t>(stream)))) return rc;
     return status_of(q8::launch_kv_fork(p, s->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
@@ -1431,7 +1456,7 @@ int q8_kv_free(const q8_kv_cache *c, int32_t *table, uint64_t table_stride, uint
     if (n == 0) return Q8_OK;
     std::lock_guard<std::mutex> lk(g_mutex);
     DeviceState *s;
-    if ((rc = pages_device(p, &s, false))) return rc;
+    if ((rc = pages_device(p, &s, false, static_cast<cudaStream_t>(stream)))) return rc;
     return status_of(q8::launch_kv_free(p, static_cast<cudaStream_t>(stream)));
 }
 
@@ -1449,7 +1474,7 @@ int q8_kv_compact(const q8_kv_cache *c, int32_t *table_out, const int32_t *table
     p.n_used = n_used;
     std::lock_guard<std::mutex> lk(g_mutex);
     DeviceState *s;
-    if ((rc = pages_device(p, &s, true))) return rc;
+    if ((rc = pages_device(p, &s, true, static_cast<cudaStream_t>(stream)))) return rc;
     return status_of(q8::launch_kv_compact(p, s->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
@@ -1466,7 +1491,7 @@ int q8_kv_copy(const q8_kv_cache *c, const int32_t *src, const int32_t *dst, uin
     p.n = n;
     std::lock_guard<std::mutex> lk(g_mutex);
     DeviceState *s;
-    if ((rc = pages_device(p, &s, false))) return rc;
+    if ((rc = pages_device(p, &s, false, static_cast<cudaStream_t>(stream)))) return rc;
     return status_of(q8::launch_kv_copy(p, s->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
@@ -1525,11 +1550,11 @@ int q8_matmul_packed(float *out, const void *Wp, int layout, uint64_t in_dim, ui
                       reinterpret_cast<const __half *>(base), reinterpret_cast<const float *>(base + m_ld * in_dim * 2));
     }
     const uint64_t n_pad = (n_tok + 15) & ~(uint64_t)15;
-    if ((rc = reserve_scratch(s, planes_bytes(n_pad, in_dim)))) return rc;
-    Carver cv(s->scratch);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if ((rc = reserve_scratch(s, planes_bytes(n_pad, in_dim), st))) return rc;
+    Carver cv(s->scratch.p);
     int8_t *qx = cv.take<int8_t>(n_pad * in_dim);
     float *dx = cv.take<float>(n_pad * (in_dim / q8::QK) * sizeof(float));
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
     if ((rc = status_of(q8::launch_quantize_planes(qx, dx, x, in_dim, n_pad, nullptr, n_tok, s->num_sms, st))))
         return rc;
     return status_of(timed_launch(st, [&] {
@@ -1564,7 +1589,10 @@ uint64_t q8_scratch_bytes(void) {
         cudaGetLastError();
         return 0;
     }
-    return g_dev[dev].scratch_bytes + g_dev[dev].stage_bytes + g_dev[dev].counter_bytes;
+    const DeviceState &s = g_dev[dev];
+    uint64_t n = s.scratch.bytes + s.stage.bytes + s.counters.bytes;
+    for (const Kept *k = s.kept; k; k = k->next) n += k->bytes;
+    return n;
 }
 
 void q8_release(void) {
@@ -1575,15 +1603,19 @@ void q8_release(void) {
         return;
     }
     for (int d = 0; d < MAX_DEVICES; ++d) {
-        if (!g_dev[d].scratch && !g_dev[d].stage && !g_dev[d].counters) continue;
+        DeviceState &s = g_dev[d];
+        if (!s.scratch.p && !s.stage.p && !s.counters.p && !s.kept) continue;
         cudaSetDevice(d);
         cudaDeviceSynchronize();
-        cudaFree(g_dev[d].scratch);
-        cudaFree(g_dev[d].stage);
-        cudaFree(g_dev[d].counters);
-        g_dev[d].scratch = g_dev[d].stage = nullptr;
-        g_dev[d].counters = nullptr;
-        g_dev[d].scratch_bytes = g_dev[d].stage_bytes = g_dev[d].counter_bytes = 0;
+        for (Buffer *b : {&s.scratch, &s.stage, &s.counters}) {
+            cudaFree(b->p);
+            *b = Buffer{};
+        }
+        while (Kept *k = s.kept) {
+            s.kept = k->next;
+            cudaFree(k->p);
+            free(k);
+        }
     }
     cudaSetDevice(cur);
 }
