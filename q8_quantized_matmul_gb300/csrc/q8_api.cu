@@ -184,12 +184,18 @@ int reserve_buffer(DeviceState *s, Buffer &b, size_t bytes, cudaStream_t st) {
 
 int reserve_scratch(DeviceState *s, size_t bytes, cudaStream_t st) { return reserve_buffer(s, s->scratch, bytes, st); }
 
-// At least n counters.  New ones are cleared on `st`; a call leaves every counter it used at zero.
+// At least n counters.  New ones are cleared here and now, on a stream of their own: on the caller's, a capture would
+// keep the clearing for the graph and leave the calls before its first replay without.  A call leaves every counter it
+// used at zero.
 int reserve_counters(DeviceState *s, size_t n, cudaStream_t st) {
     const bool grows = n * sizeof(int) > s->counters.bytes;
     const int rc = reserve_buffer(s, s->counters, n * sizeof(int), st);
     if (rc || !grows) return rc;
-    const cudaError_t e = cudaMemsetAsync(s->counters.p, 0, s->counters.bytes, st);
+    cudaStream_t own = nullptr;
+    cudaError_t e = cudaStreamCreateWithFlags(&own, cudaStreamNonBlocking);
+    if (e == cudaSuccess) e = cudaMemsetAsync(s->counters.p, 0, s->counters.bytes, own);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(own);
+    if (own) cudaStreamDestroy(own);
     if (e != cudaSuccess) {   // unusable until cleared: the next call allocates again
         cudaFree(s->counters.p);
         s->counters = Buffer{};

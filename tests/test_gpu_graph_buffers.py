@@ -1,4 +1,6 @@
 """Graphs of captured calls keep working when later calls need more scratch than there was at the capture."""
+import ctypes
+
 import numpy as np
 import pytest
 
@@ -86,3 +88,35 @@ def test_graphs_outlive_growing_buffers(q8, mode):
     torch.cuda.synchronize()
     q8.q8_release()
     assert q8.q8_scratch_bytes() == 0
+
+
+def test_counters_made_within_a_capture(q8):
+    """A relaxed capture may allocate; what it makes serves the calls before the graph's first replay too."""
+    decode = long_decode(q8, [20000, 700], 8, 2, 128)
+    ref = decode().clone()
+    torch.cuda.synchronize()
+    q8.q8_release()
+    torch.cuda.empty_cache()
+    g = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(g, capture_error_mode="relaxed"):
+        out = decode()
+    # no clearing in the graph: the calls before its replay would do without
+    cu, n, kind = ctypes.CDLL("libcuda.so.1"), ctypes.c_size_t(), ctypes.c_int()
+    graph = ctypes.c_void_p(g.raw_cuda_graph())
+    assert cu.cuGraphGetNodes(graph, None, ctypes.byref(n)) == 0
+    nodes = (ctypes.c_void_p * n.value)()
+    assert cu.cuGraphGetNodes(graph, nodes, ctypes.byref(n)) == 0
+    for node in nodes:
+        assert cu.cuGraphNodeGetType(ctypes.c_void_p(node), ctypes.byref(kind)) == 0
+        assert kind.value == 0, "a node that is not a kernel"
+    g.instantiate()
+    for _ in range(3):
+        assert torch.equal(decode(), ref)
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref)
+    assert q8.q8_last_error() == 0
+    del g
+    torch.cuda.synchronize()
+    q8.q8_release()
