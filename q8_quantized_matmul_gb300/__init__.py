@@ -486,16 +486,22 @@ def _load_ext():
     return mod
 
 
+class _CacheBlock(ctypes.Structure):
+    """What csrc/q8_torch.cpp is given: the cache and the device of its pages (-1: the host)."""
+    _fields_ = [("cache", KVCacheStruct), ("device", ctypes.c_int32)]
+
+
 class KVCache:
     """A paged key-value cache over two tensors k and v of shape [n_layers, n_pages, ...] (layout of a page:
     include/q8.h).  Inside a page the memory is contiguous; layers and pages may be strided, so k and v may be
-    slices of one tensor."""
+    slices of one tensor.  The calls below take a cache on the current device only, as all their tensors."""
 
     __slots__ = ("k", "v", "type", "page_tokens", "n_kv_heads", "head_dim", "struct", "address")
 
     def __init__(self, k, v, type: int, page_tokens: int, n_kv_heads: int, head_dim: int):
-        self.struct = struct = KVCacheStruct()
-        self.address = address = ctypes.addressof(struct)
+        block = _CacheBlock()
+        self.struct = block.cache
+        self.address = address = ctypes.addressof(block)
         (_ext_mod or _load_ext()).fill_cache(address, k, v, type, page_tokens, n_kv_heads, head_dim)
         self.k, self.v, self.type = k, v, type
         self.page_tokens, self.n_kv_heads, self.head_dim = page_tokens, n_kv_heads, head_dim

@@ -132,9 +132,28 @@ at::Tensor output(const at::Tensor &q, int64_t rows, int64_t heads, int64_t dim,
     raise_status(Q8_EINVAL, "out_type");
 }
 
-void *stream() { return c10::cuda::getCurrentCUDAStream().stream(); }
+// What a KVCache's address points to: the cache, and the device of its pages (-1: the host).
+struct Cache {
+    q8_kv_cache c;
+    int32_t device;
+};
 
-const q8_kv_cache *cache_of(PyObject *o) { return o == Py_None ? nullptr : static_cast<const q8_kv_cache *>(PyLong_AsVoidPtr(o)); }
+const q8_kv_cache *cache_of(PyObject *o) { return o == Py_None ? nullptr : &static_cast<const Cache *>(PyLong_AsVoidPtr(o))->c; }
+
+int device_of(const q8_kv_cache *c) { return reinterpret_cast<const Cache *>(c)->device; }
+
+void on_gpu(const q8_kv_cache *c) {
+    if (c && device_of(c) < 0) raise(PyExc_TypeError, "cache: pages on the GPU expected");
+}
+
+// The current stream, for a call on these tensors (None among them) and the cache: all on its device.
+void *stream_for(const q8_kv_cache *c, PyObject *const *a, std::initializer_list<int> tensors) {
+    const c10::cuda::CUDAStream st = c10::cuda::getCurrentCUDAStream();
+    bool here = !c || device_of(c) == st.device_index();
+    for (const int i : tensors) here = here && (a[i] == Py_None || THPVariable_Unpack(a[i]).get_device() == st.device_index());
+    if (!here) raise(PyExc_ValueError, "tensors and a cache on the current device expected");
+    return st.stream();
+}
 
 PyObject *wrap(const at::Tensor &t) { return THPVariable_Wrap(t); }
 
@@ -158,14 +177,16 @@ void arity(Py_ssize_t got, Py_ssize_t want) {
 // fill_cache(address, k, v, type, page_tokens, n_kv_heads, head_dim)
 PyObject *fill_cache(PyObject *const *a, Py_ssize_t n) {
     arity(n, 7);
-    q8_kv_cache *c = static_cast<q8_kv_cache *>(PyLong_AsVoidPtr(a[0]));
+    Cache *const cache = static_cast<Cache *>(PyLong_AsVoidPtr(a[0]));
+    q8_kv_cache *const c = &cache->c;
     const at::Tensor &k = tensor(a[1], "k"), &v = tensor(a[2], "v");
     const int type = (int)integer(a[3]);
     const uint32_t tokens = word(a[4], "page_tokens"), kv = word(a[5], "n_kv_heads"), dim = word(a[6], "head_dim");
     const uint64_t page = f_page_bytes(type, tokens, kv, dim);
     if (!page) raise_status(Q8_EINVAL, "q8_kv_page_bytes");
-    if (k.dim() < 3 || k.sizes() != v.sizes() || k.scalar_type() != v.scalar_type() || k.strides() != v.strides())
-        raise(PyExc_ValueError, "k and v must have the same shape, type and strides: [n_layers, n_pages, ...]");
+    if (k.dim() < 3 || k.sizes() != v.sizes() || k.scalar_type() != v.scalar_type() || k.strides() != v.strides() ||
+        k.device() != v.device())
+        raise(PyExc_ValueError, "k and v must have the same shape, type, strides and device: [n_layers, n_pages, ...]");
     int64_t want = 1;
     for (int64_t i = k.dim() - 1; i >= 2; --i) {
         if (k.stride(i) != want && k.size(i) != 1) raise(PyExc_ValueError, "a page must be contiguous");
@@ -186,6 +207,7 @@ PyObject *fill_cache(PyObject *const *a, Py_ssize_t n) {
     c->n_kv_heads = kv;
     c->head_dim = dim;
     c->type = type;
+    cache->device = k.is_cuda() ? k.get_device() : -1;
     Py_RETURN_NONE;
 }
 
@@ -193,6 +215,7 @@ PyObject *fill_cache(PyObject *const *a, Py_ssize_t n) {
 PyObject *kv_append(PyObject *const *a, Py_ssize_t n) {
     arity(n, 12);
     const q8_kv_cache *c = cache_of(a[0]);
+    on_gpu(c);
     const uint32_t layer = word(a[1], "layer");
     const at::Tensor &k = tensor(a[3], "k"), &v = tensor(a[4], "v");
     const int rope = (int)integer(a[9]), kind = (int)integer(a[10]);
@@ -240,7 +263,9 @@ PyObject *kv_append(PyObject *const *a, Py_ssize_t n) {
     const int32_t *pos = ints(a[5], "positions");
     const float *kp = static_cast<const float *>(k.data_ptr()), *vp = static_cast<const float *>(v.data_ptr());
     void *qop = qo.defined() ? qo.data_ptr() : nullptr, *kop = ko.defined() ? ko.data_ptr() : nullptr,
-         *vop = vo.defined() ? vo.data_ptr() : nullptr, *st = stream();
+         *vop = vo.defined() ? vo.data_ptr() : nullptr;
+    void *st = c ? stream_for(c, a, {2, 3, 4, 5, 6, 7}) : stream_for(c, a, {2, 3, 4, 5});
+    if (rope) stream_for(c, a, {8});
     call("q8_kv_append", [&] {
         return f_append(qop, kop, vop, kind, c, layer, qp, qs, kp, kst, vp, vst, (uint32_t)heads, (uint32_t)kv, (uint32_t)dim, pos,
                         seq, t.p, t.stride, (uint32_t)t.width, (uint32_t)t.rows, cs, (uint32_t)n_pos, (uint32_t)rot, rope, tok, st);
@@ -258,6 +283,7 @@ PyObject *attn_decode(PyObject *const *a, Py_ssize_t n) {
     if (q.dim() != 3 || q.size(2) != c->head_dim || tensor(a[3], "table").dim() != 2 || tensor(a[3], "table").size(0) != q.size(0) ||
         length(a[4], "seq_lens") != q.size(0))
         raise(PyExc_ValueError, "q, cache, table and seq_lens disagree");
+    on_gpu(c);
     const int64_t seqs = q.size(0), heads = q.size(1), dim = q.size(2);
     const Table t = table_of(a[3]);
     const int32_t *lens = ints(a[4], "seq_lens");
@@ -270,7 +296,7 @@ PyObject *attn_decode(PyObject *const *a, Py_ssize_t n) {
     const at::Tensor out = output(q, seqs, heads, dim, kind, a[8], out_type);
     at::Tensor lse;
     if (a[9] == Py_True) lse = at::empty({seqs, heads}, q.options().dtype(at::kFloat));
-    void *op = out.data_ptr(), *qp = q.data_ptr(), *st = stream();
+    void *op = out.data_ptr(), *qp = q.data_ptr(), *st = stream_for(c, a, {0, 3, 4, 7});
     float *lp = lse.defined() ? static_cast<float *>(lse.data_ptr()) : nullptr;
     call("q8_attn_decode", [&] {
         return f_decode(op, out_type, lp, qp, qs, kind, c, layer, t.p, t.stride, (uint32_t)t.width, lens, (uint32_t)seqs, (uint32_t)heads,
@@ -299,7 +325,7 @@ PyObject *attn_prompt(PyObject *const *a, Py_ssize_t n) {
     const at::Tensor out = output(q, rows, heads, dim, kind, a[8], out_type);
     at::Tensor lse;
     if (a[9] == Py_True) lse = at::empty({rows, heads}, q.options().dtype(at::kFloat));
-    void *op = out.data_ptr(), *qp = q.data_ptr(), *kp = k.data_ptr(), *vp = v.data_ptr(), *st = stream();
+    void *op = out.data_ptr(), *qp = q.data_ptr(), *kp = k.data_ptr(), *vp = v.data_ptr(), *st = stream_for(nullptr, a, {0, 1, 2, 3, 4, 7});
     float *lp = lse.defined() ? static_cast<float *>(lse.data_ptr()) : nullptr;
     const uint64_t n_k = k.size(0);
     const uint32_t kv = (uint32_t)k.size(1);
@@ -320,6 +346,7 @@ struct Pages {
 Pages pages_of(PyObject *const *a) {
     Pages p;
     p.c = cache_of(a[0]);
+    on_gpu(p.c);
     p.t = table_of(a[1]);
     int64_t n_lens = 0, n_refs = 0;
     p.lens = const_cast<int32_t *>(ints(a[2], "lens", &n_lens));
@@ -336,7 +363,7 @@ template <class F> PyObject *pages_two(PyObject *const *a, Py_ssize_t n, F f, co
     int64_t na = 0, nb = 0;
     const int32_t *x = ints(a[4], "rows", &na), *y = ints(a[5], "second list", &nb);
     if (na != nb) raise(PyExc_ValueError, "the two lists disagree");
-    void *st = stream();
+    void *st = stream_for(p.c, a, {1, 2, 3, 4, 5});
     call(what, [&] { return f(p.c, p.t.p, p.t.stride, (uint32_t)p.t.width, (uint32_t)p.t.rows, p.lens, p.refs, x, y, (uint32_t)na, st); });
     Py_RETURN_NONE;
 }
@@ -350,7 +377,7 @@ PyObject *kv_free(PyObject *const *a, Py_ssize_t n) {
     const Pages p = pages_of(a);
     int64_t na = 0;
     const int32_t *x = ints(a[4], "seqs", &na);
-    void *st = stream();
+    void *st = stream_for(p.c, a, {1, 2, 3, 4});
     call("q8_kv_free", [&] {
         return f_free(p.c, p.t.p, p.t.stride, (uint32_t)p.t.width, (uint32_t)p.t.rows, p.lens, p.refs, x, (uint32_t)na, st);
     });
@@ -366,7 +393,7 @@ PyObject *kv_compact(PyObject *const *a, Py_ssize_t n) {
     const at::Tensor nr = at::empty({(int64_t)p.c->n_pages}, t.options()), used = at::empty({}, t.options());
     int32_t *ntp = static_cast<int32_t *>(nt.data_ptr()), *nrp = static_cast<int32_t *>(nr.data_ptr()),
             *up = static_cast<int32_t *>(used.data_ptr());
-    void *st = stream();
+    void *st = stream_for(p.c, a, {1, 2, 3});
     call("q8_kv_compact", [&] {
         return f_compact(p.c, ntp, p.t.p, p.t.stride, (uint32_t)p.t.width, (uint32_t)p.t.rows, nrp, p.refs, up, st);
     });
@@ -377,10 +404,11 @@ PyObject *kv_compact(PyObject *const *a, Py_ssize_t n) {
 PyObject *kv_copy(PyObject *const *a, Py_ssize_t n) {
     arity(n, 3);
     const q8_kv_cache *c = cache_of(a[0]);
+    on_gpu(c);
     int64_t na = 0, nb = 0;
     const int32_t *x = ints(a[1], "src", &na), *y = ints(a[2], "dst", &nb);
     if (na != nb) raise(PyExc_ValueError, "src and dst disagree");
-    void *st = stream();
+    void *st = stream_for(c, a, {1, 2});
     call("q8_kv_copy", [&] { return f_copy(c, x, y, (uint32_t)na, st); });
     Py_RETURN_NONE;
 }

@@ -179,3 +179,20 @@ def test_wrong_tensors_are_refused(q8):
         q8.attn_decode(q, c, 0, torch.zeros(2, 2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
     with pytest.raises(ValueError):
         q8.attn_prompt(q, q, q[:, :1], torch.zeros(2, dtype=torch.int32))
+
+
+def test_caches_on_the_host_are_refused(q8):
+    """Every call refuses a cache whose pages lie in host memory, before anything else that is wrong with its tensors."""
+    import torch
+    c = q8.KVCache.empty(q8.Q8_TYPE_F16, 1, 4, 64, 2, 64, device="cpu")
+    i32 = lambda *shape: torch.zeros(shape, dtype=torch.int32)
+    x = torch.zeros(1, 2, 64)
+    for call in (lambda: q8.attn_decode(x.half(), c, 0, i32(1, 2), i32(1)),
+                 lambda: q8.kv_append(c, 0, x, x, x, i32(1), i32(1), i32(1, 2)),
+                 lambda: q8.kv_reserve(c, i32(1, 2), i32(1), i32(4), i32(1), i32(1)),
+                 lambda: q8.kv_fork(c, i32(1, 2), i32(1), i32(4), i32(1), i32(1)),
+                 lambda: q8.kv_free(c, i32(1, 2), i32(1), i32(4), i32(1)),
+                 lambda: q8.kv_compact(c, i32(1, 2), i32(1), i32(4)),
+                 lambda: q8.kv_copy(c, i32(1), i32(1))):
+        with pytest.raises(TypeError, match="cache: pages on the GPU"):
+            call()

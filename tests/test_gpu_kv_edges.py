@@ -60,3 +60,18 @@ def test_requests_that_name_a_row_twice_touch_nothing_else(q8):
         assert q8.q8_last_error() in (0, q8.Q8_ERANGE)
         assert torch.equal(wide[0], before[0]) and torch.equal(wide[2:5], before[2:5]) and torch.equal(wide[rows:], before[rows:])
         assert torch.all(counts[n_pages:] == 777) and int(table.max()) < n_pages and int(table.min()) >= -1
+
+
+def test_caches_on_the_host_are_refused(q8):
+    """With everything else on the GPU; a pair of pools on different devices makes no cache."""
+    c = q8.KVCache.empty(q8.Q8_TYPE_F16, 1, 4, 64, 2, 64, device="cpu")
+    x, table, one, refs = torch.zeros(1, 2, 64, device=DEV), i32([[0, 1]]), i32([0]), i32([0] * 4)
+    for call in (lambda: q8.attn_decode(x.half(), c, 0, table, one), lambda: q8.kv_append(c, 0, x, x, x, one, one, table),
+                 lambda: q8.kv_reserve(c, table, one, refs, one, one), lambda: q8.kv_fork(c, table, one, refs, one, one),
+                 lambda: q8.kv_free(c, table, one, refs, one), lambda: q8.kv_compact(c, table, one, refs),
+                 lambda: q8.kv_copy(c, one, one)):
+        with pytest.raises(TypeError, match="cache: pages on the GPU"):
+            call()
+    with pytest.raises(ValueError, match="device"):
+        q8.KVCache(c.k.to(DEV), c.v, q8.Q8_TYPE_F16, 64, 2, 64)
+    assert q8.q8_last_error() == 0
