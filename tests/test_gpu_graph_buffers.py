@@ -49,7 +49,7 @@ def grow(q8):
     q = torch.zeros(n, kv, 64, device=DEV, dtype=torch.bfloat16)
     q8.attn_decode(q, cache, 0, torch.zeros(n, 1, dtype=torch.int32, device=DEV), torch.zeros(n, dtype=torch.int32, device=DEV))
     W = torch.from_numpy(inputs.weights(512, 8192, seed=1)).to(DEV)
-    q8.matmul(W, torch.randn(8192, 8192, device=DEV), 8192)
+    q8.matmul(W, torch.randn(8192, 8192, device=DEV), 512)
     torch.cuda.synchronize()
     assert q8.q8_scratch_bytes() > before + (64 << 20)
     return [torch.full((1 << 20,), 0x55555555, dtype=torch.int32, device=DEV) for _ in range(256)]
@@ -64,7 +64,7 @@ def test_graphs_outlive_growing_buffers(q8, mode):
     start = i32([0, *np.cumsum([70] * 40)])
     pq, pk = (torch.randn(2800, h, 64, device=DEV).bfloat16() for h in (8, 2))
     calls = {"mma.sync decode": long_decode(q8, [20000, 700], 8, 2, 128), "tcgen05 decode": long_decode(q8, [6000, 90], 24, 1, 512),
-             "prompt": lambda: q8.attn_prompt(pq, pk, pk, start), "matmul": lambda: q8.matmul(W, x, 2048)}
+             "prompt": lambda: q8.attn_prompt(pq, pk, pk, start), "matmul": lambda: q8.matmul(W, x, 1024)}
     refs = {name: f().clone() for name, f in calls.items()}          # sizes the buffers
     held = q8.q8_scratch_bytes()
     graphs = {}
