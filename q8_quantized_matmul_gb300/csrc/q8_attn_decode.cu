@@ -35,6 +35,7 @@
 #include "q8_attn.cuh"
 #include "q8_attn_decode.cuh"
 #include "q8_kv.h"
+#include "q8_launch.h"
 
 namespace q8 {
 namespace {
@@ -690,13 +691,9 @@ __global__ void __launch_bounds__(128, Dec<D, FMT, NT>::CTAS) k_attn_decode(cons
 }
 
 template <int D, int FMT, int NT> cudaError_t launch_one(const AttnDecodeParams &p, int grid, cudaStream_t st) {
-    static bool attr_done = false;
-    if (!attr_done) {
-        const cudaError_t e = cudaFuncSetAttribute(k_attn_decode<D, FMT, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   Dec<D, FMT, NT>::SMEM);
-        if (e != cudaSuccess) return e;
-        attr_done = true;
-    }
+    static SmemAllowed allowed;
+    const cudaError_t es = allow_smem(allowed, reinterpret_cast<const void *>(k_attn_decode<D, FMT, NT>), Dec<D, FMT, NT>::SMEM);
+    if (es != cudaSuccess) return es;
     return launch_dependent(k_attn_decode<D, FMT, NT>, p, dim3((unsigned)grid), 128, Dec<D, FMT, NT>::SMEM, st);
 }
 

@@ -22,6 +22,7 @@
 #include "q8_attn.cuh"
 #include "q8_attn_decode.cuh"
 #include "q8_kv.h"
+#include "q8_launch.h"
 #include "q8_tcgen05.cuh"
 
 namespace q8 {
@@ -533,12 +534,9 @@ template <int D> __global__ void __launch_bounds__(128) k_attn_decode_join(const
 }
 
 template <int D, bool BF16> cudaError_t launch_tc(const AttnDecodeParams &p, int grid, cudaStream_t st) {
-    static bool attr_done = false;
-    if (!attr_done) {
-        const cudaError_t e = cudaFuncSetAttribute(k_attn_decode_tc<D, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, Dt<D>::SMEM);
-        if (e != cudaSuccess) return e;
-        attr_done = true;
-    }
+    static SmemAllowed allowed;
+    const cudaError_t es = allow_smem(allowed, reinterpret_cast<const void *>(k_attn_decode_tc<D, BF16>), Dt<D>::SMEM);
+    if (es != cudaSuccess) return es;
     alignas(64) CUtensorMap tmQ, tmK, tmV;
     const uint32_t tokens = 1u << p.c.page_shift, box = tokens < 128 ? tokens : 128;
     if (!encode_3d16_tmap(&tmQ, p.q, D, p.n_heads, p.n_seq, D, p.q_stride, Dt<D>::HT, 1, BF16) ||

@@ -19,6 +19,7 @@
 // c - 2 was committed ahead of S of c, and the issuer waits for every P in order.
 #include "q8_attn_prompt_tc.cuh"
 #include "q8_kv.h"
+#include "q8_launch.h"
 
 namespace q8 {
 
@@ -372,13 +373,9 @@ __global__ void __launch_bounds__(P64::THREADS, 1)
 }
 
 template <bool BF16> cudaError_t launch_64(const AttnPromptParams &p, int num_sms, cudaStream_t st) {
-    static bool attr_done = false;
-    if (!attr_done) {
-        const cudaError_t e = cudaFuncSetAttribute(k_attn_prompt_64<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   P64::SMEM);
-        if (e != cudaSuccess) return e;
-        attr_done = true;
-    }
+    static SmemAllowed allowed;
+    const cudaError_t es = allow_smem(allowed, reinterpret_cast<const void *>(k_attn_prompt_64<BF16>), P64::SMEM);
+    if (es != cudaSuccess) return es;
     alignas(64) CUtensorMap tmQ, tmK, tmV;
     if (!encode_3d16_tmap(&tmQ, p.q, P64::D, p.n_heads, p.n_q, P64::D, p.q_stride, (uint32_t)p.pack, (uint32_t)p.half, BF16) ||
         (p.n_k && (!encode_rows16_tmap(&tmK, p.k, (uint64_t)p.n_kv * P64::D, p.n_k, p.k_stride, 128, BF16) ||

@@ -14,6 +14,7 @@
 // after the P V before has ended (its own barrier, since S of the next tile no longer implies it).
 #include "q8_attn_prompt_tc.cuh"
 #include "q8_kv.h"
+#include "q8_launch.h"
 
 namespace q8 {
 
@@ -336,13 +337,9 @@ __global__ void __launch_bounds__(Pw<D>::THREADS, 1)
 }
 
 template <int D, bool BF16> cudaError_t launch_wide(const AttnPromptParams &p, int num_sms, cudaStream_t st) {
-    static bool attr_done = false;
-    if (!attr_done) {
-        const cudaError_t e = cudaFuncSetAttribute(k_attn_prompt_wide<D, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   Pw<D>::SMEM);
-        if (e != cudaSuccess) return e;
-        attr_done = true;
-    }
+    static SmemAllowed allowed;
+    const cudaError_t es = allow_smem(allowed, reinterpret_cast<const void *>(k_attn_prompt_wide<D, BF16>), Pw<D>::SMEM);
+    if (es != cudaSuccess) return es;
     alignas(64) CUtensorMap tmQ, tmK, tmV;
     if (!encode_3d16_tmap(&tmQ, p.q, D, p.n_heads, p.n_q, D, p.q_stride, (uint32_t)p.pack, (uint32_t)p.half, BF16) ||
         (p.n_k && (!encode_rows16_tmap(&tmK, p.k, (uint64_t)p.n_kv * D, p.n_k, p.k_stride, 128, BF16) ||

@@ -67,6 +67,7 @@
 
 #include "q8_common.cuh"
 #include "q8_kernels.h"
+#include "q8_launch.h"
 #include "q8_quant.cuh"
 
 namespace q8 {
@@ -1063,14 +1064,11 @@ cudaError_t launch_gemv(const GemvParams &p, int mode, int grid, cudaStream_t st
         {{nullptr, gemv_fn<KIND_PAIR, 1>(1), gemv_fn<KIND_PAIR, 1>(2)},
          {nullptr, gemv_fn<KIND_PAIR, 2>(1), gemv_fn<KIND_PAIR, 2>(2)},
          {nullptr, nullptr, nullptr}}};
-    static bool attr_done[3][3][3] = {};
+    static SmemAllowed allowed[3][3][3];
     const void *fn = fns[kind][subm - 1][mode];
     if (!fn) return cudaErrorInvalidValue;
-    if (!attr_done[kind][subm - 1][mode]) {
-        cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)gv::SMEM);
-        if (e != cudaSuccess) return e;
-        attr_done[kind][subm - 1][mode] = true;
-    }
+    const cudaError_t es = allow_smem(allowed[kind][subm - 1][mode], fn, gv::SMEM);
+    if (es != cudaSuccess) return es;
     alignas(64) CUtensorMap tmap, tmap2;
     const uint64_t row_bytes = (uint64_t)p.nb * QB;
     const uint64_t mats = p.plan ? p.n_expert : 1;

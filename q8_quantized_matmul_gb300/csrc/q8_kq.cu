@@ -29,6 +29,7 @@
 // memory (the limit there) serves two rows; in the direct kernel, one row.
 #include "q8_common.cuh"
 #include "q8_kernels.h"
+#include "q8_launch.h"
 
 namespace q8 {
 
@@ -664,13 +665,9 @@ uint32_t kq_stream_rows(uint64_t row_bytes, uint64_t in_dim, int tokg) {
 }
 
 template <int FMT, int TOKG> static cudaError_t launch_stream(const KqParams &p, int num_sms, cudaStream_t st) {
-    static bool attr_done = false;
-    if (!attr_done) {
-        cudaError_t e = cudaFuncSetAttribute(k_kq_stream<FMT, TOKG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)kqs::Layout<TOKG>::SMEM);
-        if (e != cudaSuccess) return e;
-        attr_done = true;
-    }
+    static SmemAllowed allowed;
+    const cudaError_t es = allow_smem(allowed, reinterpret_cast<const void *>(k_kq_stream<FMT, TOKG>), kqs::Layout<TOKG>::SMEM);
+    if (es != cudaSuccess) return es;
     k_kq_stream<FMT, TOKG><<<num_sms, kqs::THREADS, kqs::Layout<TOKG>::SMEM, st>>>(p);
     return cudaGetLastError();
 }

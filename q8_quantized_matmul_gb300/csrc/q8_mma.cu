@@ -25,6 +25,7 @@
 // table written on the device by the routing kernels.
 #include "q8_common.cuh"
 #include "q8_kernels.h"
+#include "q8_launch.h"
 
 namespace q8 {
 
@@ -308,13 +309,10 @@ cudaError_t launch_mma(const MmaParams &p, int grid, cudaStream_t st) {
     if (((srow / 16) & 1u) == 0) srow += 16;   // odd multiple of 16 bytes: conflict-free rows
     const uint32_t stage_bytes = (RBR * srow + 127u) & ~127u;
     const size_t smem = mma_smem_bytes(stage_bytes);
-    static bool attr_done = false;   // per process; the limit is the same on every device
-    if (!attr_done) {
-        cudaError_t e = cudaFuncSetAttribute(k_mma, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)mma_smem_bytes(((RBR * (KCMAX * QB + 16)) + 127u) & ~127u));
-        if (e != cudaSuccess) return e;
-        attr_done = true;
-    }
+    static SmemAllowed allowed;
+    const cudaError_t es = allow_smem(allowed, reinterpret_cast<const void *>(k_mma),
+                                      mma_smem_bytes(((RBR * (KCMAX * QB + 16)) + 127u) & ~127u));
+    if (es != cudaSuccess) return es;
     k_mma<<<grid, NTHREADS, smem, st>>>(p, kc, srow, stage_bytes);
     return cudaGetLastError();
 }

@@ -45,6 +45,7 @@
 
 #include "q8_common.cuh"
 #include "q8_kernels.h"
+#include "q8_launch.h"
 #include "q8_tcgen05.cuh"
 
 namespace q8 {
@@ -676,13 +677,9 @@ cudaError_t launch_tc_expand(__half *a16, float *dwT, const uint8_t *W, uint32_t
 template <bool G, bool RAW>
 static cudaError_t launch_tc_variant(const TcParams &p, const CUtensorMap &tmA, const CUtensorMap &tmB, int grid,
                                      cudaStream_t st) {
-    static bool attr_done = false;
-    if (!attr_done) {
-        cudaError_t e = cudaFuncSetAttribute(k_tc_gemm<G, RAW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)tc::Cfg<RAW>::SMEM);
-        if (e != cudaSuccess) return e;
-        attr_done = true;
-    }
+    static SmemAllowed allowed;
+    const cudaError_t es = allow_smem(allowed, reinterpret_cast<const void *>(k_tc_gemm<G, RAW>), tc::Cfg<RAW>::SMEM);
+    if (es != cudaSuccess) return es;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(tc::Cfg<RAW>::NTHREADS);
