@@ -470,7 +470,8 @@ _ext_mod = None
 def _load_ext():
     global _ext_mod
     if not os.path.exists(EXT_PATH):
-        raise ImportError(f"{EXT_PATH} is missing: build it with `python -m q8_quantized_matmul_gb300.build`")
+        raise ImportError(f"{EXT_PATH} is missing: build it with `python -m q8_quantized_matmul_gb300.build` where "
+                          "torch is installed")
     import importlib.machinery
     import importlib.util
 

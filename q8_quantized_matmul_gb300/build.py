@@ -4,13 +4,16 @@ Each .cu file under csrc/ is compiled in parallel with nvcc
 (``-gencode arch=compute_103a,code=sm_103a``, no fast-math, IEEE division and
 square root) and linked into ``q8_quantized_matmul_gb300/libq8.so`` with the
 CUDA runtime linked statically, so loading the library needs no GPU.
-``csrc/q8_torch.cpp`` becomes ``_q8torch.so`` beside it (g++, torch's headers).
+``csrc/q8_torch.cpp`` becomes ``_q8torch.so`` beside it (g++, torch's headers) where torch is installed: the C
+library needs nvcc alone.
 
     python -m q8_quantized_matmul_gb300.build
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -42,16 +45,42 @@ def sources() -> list[str]:
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
 
 
-def _deps() -> list[str]:
-    files = [HEADER] + [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    return files
+def _newer(out: str, files: list[str]) -> bool:
+    """Whether one of the files is newer than `out`, or there is no such file."""
+    if not os.path.exists(out):
+        return True
+    t = os.path.getmtime(out)
+    return any(os.path.getmtime(f) > t for f in files)
+
+
+def torch_version() -> str | None:
+    """The installed torch's version (not imported for it), or None."""
+    try:
+        return importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:   # a source tree on the path has no metadata
+        return "of a source tree" if importlib.util.find_spec("torch") else None
+
+
+def lib_stale() -> bool:
+    return _newer(LIB, [HEADER] + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f != "q8_torch.cpp"])
+
+
+def ext_stale() -> bool:
+    """Whether the tensor helpers' module is to be built: never without torch, again for another one."""
+    version = torch_version()
+    if version is None:
+        return False
+    if _newer(TORCH_EXT, [HEADER, os.path.join(CSRC, "q8_torch.cpp")]):
+        return True
+    try:
+        with open(os.path.join(OBJ, "torch_version")) as f:
+            return f.read() != f"{version} python {sys.version}"
+    except OSError:
+        return True
 
 
 def stale() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(TORCH_EXT)):
-        return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(TORCH_EXT))
-    return any(os.path.getmtime(f) > t for f in _deps())
+    return lib_stale() or ext_stale()
 
 
 def _compile(src: str, extra: list[str]) -> str:
@@ -83,24 +112,36 @@ def _compile_torch() -> None:
     os.replace(tmp, TORCH_EXT)
 
 
-def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = None) -> str:
-    """Compile and link libq8.so if any source is newer than it (or force)."""
-    if not force and not stale():
-        return LIB
-    os.makedirs(OBJ, exist_ok=True)
-    extra = ["-Xptxas", "-v"] if verbose_ptxas else []
-    srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=jobs or min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
-        ext = ex.submit(_compile_torch)
-        objs = list(ex.map(lambda s: _compile(s, extra), srcs))
-        ext.result()
+def _link(objs: list[str]) -> None:
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    os.utime(TORCH_EXT)
+
+
+def _build_ext() -> None:
+    _compile_torch()
+    with open(os.path.join(OBJ, "torch_version"), "w") as f:
+        f.write(f"{torch_version()} python {sys.version}")
+
+
+def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = None) -> str:
+    """Compile what is older than its sources (or all, with force): libq8.so, and with torch installed _q8torch.so.
+    An error of the latter is raised once libq8.so is in place."""
+    lib, ext = force or lib_stale(), torch_version() is not None and (force or ext_stale())
+    if not (lib or ext):
+        return LIB
+    os.makedirs(OBJ, exist_ok=True)
+    extra = ["-Xptxas", "-v"] if verbose_ptxas else []
+    srcs = sources()
+    with cf.ThreadPoolExecutor(max_workers=jobs or min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        helpers = ex.submit(_build_ext) if ext else None
+        if lib:
+            _link(list(ex.map(lambda s: _compile(s, extra), srcs)))
+        if helpers:
+            helpers.result()
     return LIB
 
 
