@@ -136,15 +136,11 @@ __device__ __forceinline__ void load8s(float (&y)[8], const float *p) {
 // The row's terms are sums of 2^(z - m): l of them plus, with a sink logit (log2 units), its own.
 __device__ __forceinline__ float softmax_finish(float m, float l, bool has_sink, float sink, float &lse) {
     float f = 1.0f, total = l, mt = m;
-    if (has_sink && sink == INFINITY) {                // takes all the weight (m - sink is no number)
-        lse = l + INFINITY;
-        return l * 0.0f;
-    }
     if (has_sink) {
         mt = fmaxf(m, sink);
         if (mt == -INFINITY) mt = 0.0f;                // both empty: total stays 0
         f = m == -INFINITY ? 0.0f : ex2(m - mt);
-        total = l * f + ex2(sink - mt);
+        total = l * f + ex2(sink == mt ? 0.0f : sink - mt);   // a sink of +inf takes all the weight: inf - inf is no number
     }
     lse = total == 0.0f ? -INFINITY : (mt + log2f(total)) * 0.6931471805599453f;
     return total == 0.0f ? 0.0f : f / total;
