@@ -68,35 +68,15 @@ __device__ __forceinline__ int tile_cost(const PromptTile &w, uint32_t window) {
 __global__ void __launch_bounds__(LIST_THREADS) k_attn_prompt_list(const AttnPromptParams p) {
     __shared__ int bin[LIST_BINS];
     __shared__ int wsum[32];
-    __shared__ unsigned long long all;
+    __shared__ uint32_t wrows[32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     grid_dep_wait();
     const int32_t *ks = p.k_start ? p.k_start : p.q_start;
     bin[tid] = 0;
-    if (tid == 0) all = 0;
     __syncthreads();
-    // Rising starts give at most list_cap tiles.  Starts that fall in between may give 2^20 sequences all rows each: more
-    // than the list, 32 bits or one CTA's time hold, and no tile of them is worked on.
-    {
-        uint64_t mine = 0;
-        for (uint32_t s = tid; s < p.n_seq; s += LIST_THREADS) {
-            const int n = prompt_bound(p.q_start[s + 1], p.n_q) - prompt_bound(p.q_start[s], p.n_q);
-            if (n > 0) mine += (uint32_t)(n + p.tile_tokens - 1) / (uint32_t)p.tile_tokens;
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-        if (lane == 0 && mine) atomicAdd(&all, mine);
-        __syncthreads();
-        if (all > p.list_cap) {
-            if (tid == 0) {
-                *reinterpret_cast<int *>(p.list) = 0;
-                raise_error(p.err, DEV_ERANGE);
-            }
-            return;
-        }
-    }
     PromptTile *list = reinterpret_cast<PromptTile *>(p.list + 1);
-    auto each = [&](auto f) {   // a lane per sequence; the warp together for long ones, a lane per tile
+    // a lane per sequence; the warp together for long ones, a lane per tile; go: whether to, given a lane's rows
+    auto each = [&](auto go, auto f) {
         const uint32_t per = min(32u, (p.n_seq + 31) / 32);   // sequences of a warp: few ones are spread over the warps
         for (uint32_t s0 = warp * per; s0 < p.n_seq; s0 += 32 * per) {
             const uint32_t s = s0 + lane;
@@ -109,6 +89,7 @@ __global__ void __launch_bounds__(LIST_THREADS) k_attn_prompt_list(const AttnPro
                 ke = prompt_bound(raw.w, p.n_k);
                 if (qe < qa || ke < ka || qa != raw.x || qe != raw.y || ka != raw.z || ke != raw.w) raise_error(p.err, DEV_ERANGE);
             }
+            if (!go((uint32_t)max(qe - qa, 0))) break;
             auto tiles = [&](int a, int e, int k0, int k1, int64_t from, int64_t by) {
                 PromptTile w;
                 w.q0 = a;
@@ -131,8 +112,28 @@ __global__ void __launch_bounds__(LIST_THREADS) k_attn_prompt_list(const AttnPro
             }
         }
     };
-    each([&](const PromptTile &, int b) { atomicAdd(&bin[b], 1); });
+    // Sequences of rising starts have n_q rows together, and their tiles fit the list.  With starts that fall in between,
+    // 2^20 sequences may have all rows each: more tiles than the list, 32 bits or one CTA's time hold.  A warp stops when it
+    // alone passes n_q, and no tile is worked on.
+    auto warp_sum = [](uint32_t n) {
+        return ((uint64_t)__reduce_add_sync(0xffffffffu, n >> 16) << 16) + __reduce_add_sync(0xffffffffu, n & 0xffffu);
+    };
+    uint64_t rows = 0;
+    each(
+        [&](uint32_t n) {
+            rows += warp_sum(n);
+            return rows <= p.n_q;
+        },
+        [&](const PromptTile &, int b) { atomicAdd(&bin[b], 1); });
+    if (lane == 0) wrows[warp] = (uint32_t)min(rows, (uint64_t)0xffffffffu);
     __syncthreads();
+    if (warp_sum(wrows[lane]) > p.n_q) {
+        if (tid == 0) {
+            *reinterpret_cast<int *>(p.list) = 0;
+            raise_error(p.err, DEV_ERANGE);
+        }
+        return;
+    }
     int sum = bin[tid];
     const int mine = sum;
 #pragma unroll
@@ -147,7 +148,7 @@ __global__ void __launch_bounds__(LIST_THREADS) k_attn_prompt_list(const AttnPro
     bin[tid] = before + sum - mine;
     if (tid == LIST_THREADS - 1) *reinterpret_cast<int *>(p.list) = before + sum;
     __syncthreads();
-    each([&](const PromptTile &w, int b) {
+    each([](uint32_t) { return true; }, [&](const PromptTile &w, int b) {
         list[atomicAdd(&bin[b], 1)] = w;
     });
 }
