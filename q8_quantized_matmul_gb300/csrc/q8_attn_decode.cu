@@ -40,18 +40,15 @@
 namespace q8 {
 namespace {
 
-// FMT 0: f16, 1: bf16, 2: Q8_0 with f16 q, 3: Q8_0 with bf16 q; NT tiles of 8 heads a unit
 // Pieces that one CTA joins at once, and in groups when there are more (24 pieces a unit: in groups 12.1 us, at once 10.7;
 // 30: 12.4 and 13.6; 228: 21 and 68).
 constexpr int AT_ONCE = 24, GROUP = 16;
-// When no sequence has more tiles than this, CTAs take whole units: the join costs about 2 us, as much as these tiles one
-// after another.
-constexpr int SHORT = 5;
 // Tiles of the line before each unit's first that hold nothing: a CTA that works on two units pays for the second start
 // with fewer tiles (24 units over 608 CTAs: 16.8 -> 14.0 us; 60 Q8_0 units over 304: 27.8 -> 24.4; 32 long ones: 63.4 ->
 // 61.8; 8 and 16 tiles gain on few units and lose on many).
 constexpr int HEAD = 2;
 
+// FMT 0: f16, 1: bf16, 2: Q8_0 with f16 q, 3: Q8_0 with bf16 q; NT tiles of 8 heads a unit
 template <int D, int FMT, int NT> struct Dec {
     static constexpr bool Q8 = FMT >= 2, BF16 = FMT & 1;
     static constexpr int HR = 8 * NT;                    // heads of a unit
@@ -64,6 +61,14 @@ template <int D, int FMT, int NT> struct Dec {
     static constexpr int KB = ST * D * (Q8 ? 1 : 2), VB = ST * DV * (Q8 ? 1 : 2);
     static constexpr int KSB = Q8 ? ST * (D / 32) * 2 : 0, VSB = Q8 ? ST * (DV / 32) * 2 : 0;
     static constexpr int STAGE = KB + VB + KSB + VSB;
+    // When no sequence has more tiles than this, CTAs take whole units: joining pieces costs 2 to 3 us (heads of 512: 6
+    // to 9), as much as these tiles one after another.  One sequence of t tiles, 8 or 16 heads a unit, pieces / whole units, us:
+    //   16 bit:  64 values t = 8 6.6 / 6.5, 10 7.3 / 7.4;  128 t = 5 7.0 / 6.6, 6 7.0 / 7.3;  256 t = 4 9.5 / 8.6, 5 9.7 / 9.8;
+    //            512 t = 5 12.4 / 12.7, 16 heads 18.8 / 16.0
+    //   Q8_0:    64 values t = 4 7.4 / 6.6, 5 7.6 / 7.6;  128 t = 3 8.5 / 7.9, 4 8.5 / 9.2;  256 t = 2 10.9 / 11.1, 5 12.4 / 21.9;
+    //            512 t = 2 17.0 / 16.0, 3 16.9 / 21.4
+    // (16 and 48 sequences cross later, by up to four tiles, at 512 values in Q8_0 as early.)
+    static constexpr int SHORT = Q8 ? (D == 64 ? 5 : D == 128 ? 3 : 2) : (D == 64 ? 8 : 5);
     static constexpr int NST = Q8 && D <= 128 ? 3 : 2;         // stages of a warp
     static constexpr bool QREG = D <= 128;               // q fragments in registers (else shared memory)
     static constexpr int QS = QREG ? 0 : D / 16 * NT * 256;   // q fragments, [k step][head tile][lane] of 8 bytes
@@ -160,7 +165,7 @@ __global__ void __launch_bounds__(128, Dec<D, FMT, NT>::CTAS) k_attn_decode(cons
     };
     if (p.n_seq <= 32) {                                         // every warp for itself: no barriers
         const int n = lane < (int)p.n_seq ? seq_of(C::TT, 16, p, lane, blockIdx.x == 0 && warp == 0).tiles : 0;
-        by_unit = __all_sync(0xffffffffu, n <= SHORT);
+        by_unit = __all_sync(0xffffffffu, n <= C::SHORT);
         const int64_t mine = (int64_t)(by_unit ? min(n, 1) : (n ? n + HEAD : 0)) * units_per_seq;
         int64_t sum = mine;
 #pragma unroll
@@ -184,7 +189,7 @@ __global__ void __launch_bounds__(128, Dec<D, FMT, NT>::CTAS) k_attn_decode(cons
             seen += n > 0;
             most = max(most, n);
         }
-        by_unit = !__syncthreads_or(most > SHORT);
+        by_unit = !__syncthreads_or(most > C::SHORT);
         mine = by_unit ? seen : mine + (int64_t)HEAD * seen;
         mine *= units_per_seq;
         int64_t sum = mine;
