@@ -577,7 +577,7 @@ void q8_debug_fail_next_alloc(int count);
  * q8_rmsnorm_quantize runs for rows of at most 4096 values and at least 12
  * rows per SM, and the tcgen05 kernels of q8_attn_prompt and, for 16-bit
  * caches with more than 16 query heads of 256 or 512 values on a key-value
- * head, of q8_attn_decode) run with every wait limited to
+ * head and room for more than 256 positions, of q8_attn_decode) run with every wait limited to
  * limit_ns nanoseconds (0: the normal 2 s) and with their producer issuing no
  * copy at all, so the consumers wait on buffers that never fill.  Each such
  * kernel then raises Q8_ETIMEOUT for q8_last_error(), stops waiting, lets any

@@ -1309,7 +1309,7 @@ int q8_attn_decode(void *out, int out_type, float *lse, const void *q, uint64_t 
     p.sinks = sinks;
     p.err = s->err;
     const uint64_t room = (uint64_t)max_pages << p.c.page_shift, most = window && window < room ? window : room;
-    if (q8::attn_decode_on_tc(c->head_dim, p.group, c->type != Q8_TYPE_Q8_0, most)) {
+    if (q8::attn_decode_on_tc(c->head_dim, p.group, c->type != Q8_TYPE_Q8_0, most, (uint64_t)n_seq * c->n_kv_heads, s->num_sms)) {
         p.mtiles = (p.group + 63) / 64;
         const size_t slots = 2 * (size_t)s->num_sms, units = (size_t)n_seq * c->n_kv_heads * p.mtiles;
         const size_t part = align256(slots * 64 * c->head_dim * sizeof(float)), ml = align256(slots * 64 * sizeof(float2));

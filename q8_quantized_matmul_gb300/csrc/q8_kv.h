@@ -86,17 +86,24 @@ struct AttnDecodeParams {
     uint64_t wait_ns;                     // failure-detection test hook, see GemvParams
     int withhold;
 };
-// Whether a call runs on the tcgen05 kernel: 16-bit caches, large heads, more query heads on a key-value head
-// than one unit of the mma.sync kernel takes (64 heads of 512 on one, 16 sequences of up to 4100 positions:
-// 26 us against 76 us), and room for more than a few positions a sequence (most: what the window or the row of pages
-// allows; 64 heads of 512, 1 / 16 / 48 sequences of up to 64: 14.8 / 16.8 / 21.5 us there, 11.6 / 12.2 / 23.7 us
-// on mma.sync; of up to 128: 15.1 / 16.8 / 21.5 against 14.8 / 15.6 / 30.5).
-inline bool attn_decode_on_tc(uint32_t dim, uint32_t group, bool cache16, uint64_t most) {
-    return cache16 && dim >= 256 && group > 16 && most > 64;
+// Query heads of an mma.sync unit: 8 when the group that shares a key-value head has no more, else 16.
+inline uint32_t attn_decode_heads(uint32_t group) { return group <= 8 ? 8 : 16; }
+// Whether a call runs on the tcgen05 kernel: 16-bit caches, heads of 256 or 512, more query heads on a key-value head
+// than one unit of the mma.sync kernel takes (64 heads of 512 on one, 16 sequences of up to 4100 positions: 26 us against
+// 76), and room for more than some positions a sequence (most: what the window or the row of pages allows; the lengths are
+// on the device).  mma.sync starts sooner and does as many units (16 heads of a sequence) at a time as there are SMs, but
+// reads the cache once a unit.  tcgen05 / mma.sync, us:
+//   up to one unit an SM    512 values, 64 heads, 16 sequences: 128 positions 18.0 / 15.4, 192 17.5 / 24.5
+//                           256 values, the same: 256 positions 13.7 / 11.1, 512 13.8 / 21.6
+//   up to three             512 values, 24 heads, 200 sequences: 32 positions 31.5 / 26.6, 64 31.6 / 32.5
+//                           256 values, 64 heads, 48 sequences: 64 positions 15.8 / 13.5, 128 16.3 / 16.2, 192 16.2 / 18.5
+//   more                    64 heads, 200 sequences of 16 positions: 512 values 48.8 / 52.8, 256 values 30.8 / 34.2
+inline bool attn_decode_on_tc(uint32_t dim, uint32_t group, bool cache16, uint64_t most, uint64_t seq_heads, int num_sms) {
+    if (!cache16 || dim < 256 || group <= 16) return false;
+    const uint64_t units = seq_heads * ((group + 15) / 16);
+    return most > (units <= (uint64_t)num_sms ? 65536 / dim : units <= 3 * (uint64_t)num_sms ? 16384 / dim : 0);
 }
 cudaError_t launch_attn_decode_tc(const AttnDecodeParams &p, int grid, cudaStream_t st);
-// Query heads of a unit: 8 when the group that shares a key-value head has no more, else 16.
-inline uint32_t attn_decode_heads(uint32_t group) { return group <= 8 ? 8 : 16; }
 // CTAs that the decode kernel of this head size and format runs with (0: unsupported).
 int attn_decode_grid(uint32_t dim, uint32_t group, int cache_type, int num_sms);
 cudaError_t launch_attn_decode(const AttnDecodeParams &p, int grid, cudaStream_t st);

@@ -162,3 +162,27 @@ def test_prompt_starts_that_fall(q8, tokens, seqs):
         assert q8.q8_last_error() == q8.Q8_ERANGE
     assert torch.equal(q8.attn_prompt(q[:n], k, k, small), ref)
     assert q8.q8_last_error() == 0
+
+
+@pytest.mark.parametrize("dim,heads,seqs", [(512, 64, 3), (256, 24, 3), (512, 24, 120), (256, 64, 40), (512, 64, 160)])
+def test_decode_kernels_agree_on_either_side_of_their_rule(q8, dim, heads, seqs):
+    """The same sequences with rows of pages that leave room for few positions and for many, which run on different
+    kernels: each within half a step of bf16 of the weighted mean of |v| (below 4) for its weights, and the logarithm of
+    the denominator within 2 (D + 8) 2^-23 of sum |q k| scale (below 16 for 512 normal values) for the scores' sums."""
+    page, n_pages = 16, 8 * seqs
+    g = torch.Generator().manual_seed(seqs)
+    cache = q8.KVCache.empty(q8.Q8_TYPE_BF16, 1, n_pages, page, 1, dim)
+    for pool in (cache.k, cache.v):
+        pool.view(torch.bfloat16).copy_(torch.randn(pool.view(torch.bfloat16).shape, generator=g).clamp(-4, 4))
+    lens = torch.randint(0, 65, (seqs,), generator=g).int()
+    lens[0], lens[-1] = 0, 64
+    table = torch.randperm(n_pages, generator=g)[:4 * seqs].view(seqs, 4).int().to(DEV)
+    wide = torch.full((seqs, 40), -1, dtype=torch.int32, device=DEV)
+    wide[:, :4] = table
+    q = torch.randn(seqs, heads, dim, generator=g).bfloat16().to(DEV)
+    for window in (0, 10):
+        (a, la), (b, lb) = (q8.attn_decode(q, cache, 0, t, lens.to(DEV), window=window, out_type=q8.Q8_TYPE_F32, want_lse=True)
+                            for t in (table, wide))
+        assert (a - b).abs().max() <= 2 * 4 * (2.0 ** -8 + 2.0 ** -18)
+        assert torch.equal(la.isinf(), lb.isinf()) and (la - lb)[~la.isinf()].abs().max() <= 2 * 2 * 520 * 16 * 2.0 ** -23
+    assert q8.q8_last_error() == 0
