@@ -41,7 +41,10 @@
  *     its calls were captured with, whatever later calls need: such memory is
  *     held until q8_release(), after which the graph must not run.
  *     Calls that use scratch must not run concurrently on different streams
- *     of the same device.  q8_release() frees it.
+ *     of the same device.  Two that overlap spoil their own results; split
+ *     attention (q8_attn_decode) also counts its pieces there, and after an
+ *     overlap may join them wrongly in later calls too, until q8_release(),
+ *     which frees all scratch.
  *   - Kernels are launched with programmatic stream serialisation: a kernel
  *     may start while the one before it on the stream finishes, once that one
  *     has signalled its dependents.  Everything a kernel reads is read after

@@ -33,7 +33,7 @@ __device__ __forceinline__ bool tile_wait(uint64_t *bar, uint32_t parity, int *e
 
 // Programmatic launches: the wait for the kernel before this one.  (Leave for the next kernel to start early,
 // griddepcontrol.launch_dependents, measured slower or no faster in every kernel here: its waiting CTAs take
-// slots and cache from this one.  64x512 decode 32 -> 36 us, 8192-token prompt 390 -> 408, small calls the same.)
+// slots and cache from this one.  64x512 decode 32 -> 36 us, 8192-token prompt 390 -> 408, small calls the same, when those took 32 and 390.)
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // 2^x on the special-function unit (relative error about 2^-22; 2^-inf = 0).

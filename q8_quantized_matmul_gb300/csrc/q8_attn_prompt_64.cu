@@ -7,7 +7,7 @@
 // a tile.  O of both tiles takes only 128 TMEM columns here, so there are three S buffers.  The pairs x = 2 (key tile)
 // + (query tile) of an item form one sequence; pair x works in buffer x % 3, and S of pair x + 3 is issued right behind
 // P V of pair x, in one group: the next scores of a tile are ready when its softmax of the last ones ends.
-// Measured: one prompt of 8192 tokens, 32 heads on 8, 250 us (1.10 PFLOP/s; 2050 cycles a key tile; 274 us with one
+// Measured: one prompt of 8192 tokens, 32 heads on 8, 250 to 257 us (1.10 PFLOP/s; 2050 cycles a key tile; 274 us with one
 // buffer a tile); 12 packed prompts with a window of 1024 85 us (with one buffer 6 more).  Of the 2050 the softmax takes 1350 (probe: a
 // warp's step 881 cycles alone, two on a scheduler 1346); the rest is waits for S behind the other tile's group.
 // Registers are split 104 / 200 between the roles: with 168 a thread the softmax spills (a step 1150 instead of 885).
@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(P64::THREADS, 1)
     const uint32_t n_items = p.list ? (uint32_t)min((uint64_t)*reinterpret_cast<const uint32_t *>(p.list) * per_tile, (uint64_t)0xffff0000u)
                                     : (one ? blockIdx.x + 1 : 0);
     // Every second round of the list is dealt out backwards: the longest of one round goes with the shortest of
-    // the next (4096 tokens, 32 heads of 128: 132 -> 111 us).
+    // the next (4096 tokens, 32 heads of 64 on 8: 93 -> 76 us).
     auto item_of = [&](uint32_t round) {
         if (!p.list) return round ? 0xffffffffu : (uint32_t)blockIdx.x;
         return round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : (uint32_t)blockIdx.x);

@@ -9,7 +9,7 @@
 // the SM's 512 columns.  While the threads of one tile work on its softmax the tensor cores run the
 // other tile's products, so the two overlap: a key tile costs the tensor pipe about 2048
 // cycles for both query tiles and the softmax warps about 1350.  One prompt of 8192 tokens with 32 heads on 8 takes
-// 339 us (1.62 PFLOP/s, at the card's power limit), one of 4096 tokens 100 us (1.37).
+// 339 us (1.62 PFLOP/s, at the card's power limit), one of 4096 tokens 101 us (1.36).
 //
 // O is rescaled only when a row's maximum has grown by more than 2^8 since the last time (the weights
 // then stay below 2^8 in bf16; in fp16 they are counted in units 2^7 smaller, see weight_ref, and stay below 2^15);
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(Pt::THREADS, 1)
     const uint32_t n_items = p.list ? (uint32_t)min((uint64_t)*reinterpret_cast<const uint32_t *>(p.list) * per_tile, (uint64_t)0xffff0000u)
                                     : (one ? blockIdx.x + 1 : 0);
     // Every second round of the list is dealt out backwards: the longest of one round goes with the shortest of
-    // the next (4096 tokens, 32 heads of 128: 132 -> 111 us).
+    // the next (4096 tokens, 32 heads of 128 on 8: 122 -> 101 us).
     auto item_of = [&](uint32_t round) {
         if (!p.list) return round ? 0xffffffffu : (uint32_t)blockIdx.x;
         return round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : (uint32_t)blockIdx.x);

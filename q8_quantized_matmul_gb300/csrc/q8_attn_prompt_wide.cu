@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(Pw<D>::THREADS, 1)
     const uint32_t n_items = p.list ? (uint32_t)min((uint64_t)*reinterpret_cast<const uint32_t *>(p.list) * per_tile, (uint64_t)0xffff0000u)
                                     : (one ? blockIdx.x + 1 : 0);
     // Every second round of the list is dealt out backwards: the longest of one round goes with the shortest of
-    // the next (4096 tokens, 32 heads of 128: 132 -> 111 us).
+    // the next (4096 tokens, 16 heads of 256 on one: 126 -> 106 us).
     auto item_of = [&](uint32_t round) {
         if (!p.list) return round ? 0xffffffffu : (uint32_t)blockIdx.x;
         return round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : (uint32_t)blockIdx.x);

@@ -141,10 +141,10 @@ struct AttnPromptParams {
 inline int attn_prompt_halves(uint32_t dim) { return dim <= 128 ? 2 : 1; }
 inline uint32_t attn_prompt_parts(uint32_t dim) { return dim <= 256 ? 1 : dim / 256; }
 // Heads packed into the rows, a divisor of the group: the smallest whose tiles, for sequences of the average
-// length, all run at once (one 77-token prompt, 32 heads on 8: 9.7 us with 32 CTAs, 12.3 with 16); failing that
+// length, all run at once (one 77-token prompt, 32 heads on 8: 7.5 us with 32 CTAs, 9.0 with 16); failing that
 // the one with the fewest tiles, the largest of equals (its heads share their keys' copies).  Short prompts
-// fill their tiles that way (10 sequences of up to 39 tokens, 64 heads of 512: 81 -> 28 us), and the tiles of a
-// window span fewer keys (12 packed prompts, window 1024: 112 -> 100 us).
+// fill their tiles that way (10 sequences of up to 39 tokens, 64 heads of 512: 63 -> 12.8 us), and the tiles of a
+// window span fewer keys (12 packed prompts, heads of 64, window 1024: 101 -> 85 us).
 inline int attn_prompt_pack(uint32_t group, uint32_t n_kv, uint32_t dim, uint64_t n_q, uint32_t n_seq, int num_sms) {
     const uint64_t avg = (n_q + n_seq - 1) / n_seq;
     uint64_t best = ~(uint64_t)0;
