@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 
 from tests.attn_plain import attend
+from tests.test_gpu_attn import check_prompt
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
@@ -186,3 +187,55 @@ def test_decode_kernels_agree_on_either_side_of_their_rule(q8, dim, heads, seqs)
         assert (a - b).abs().max() <= 2 * 4 * (2.0 ** -8 + 2.0 ** -18)
         assert torch.equal(la.isinf(), lb.isinf()) and (la - lb)[~la.isinf()].abs().max() <= 2 * 2 * 520 * 16 * 2.0 ** -23
     assert q8.q8_last_error() == 0
+
+
+@pytest.mark.parametrize("window", [1, 64, 129, 300])
+@pytest.mark.parametrize("heads,kv", [(2, 1), (20, 1), (6, 3)])
+def test_prompt_windows_of_heads_of_512(q8, window, heads, kv):
+    check_prompt(q8, "bf16", [300, 5, 0, 140], [300, 205, 30, 90], heads=heads, kv=kv, dim=512, window=window, sinks=True, seed=window)
+
+
+def test_raw_calls_agree_with_the_tensor_helpers(q8):
+    """The package's bindings of the C entry points, one per call, against the helpers on the same tensors."""
+    n, heads, kv, dim, page, pages = 100, 4, 2, 64, 16, 20
+    g = torch.Generator().manual_seed(1)
+    q, k, v = (torch.randn((n, h, dim), generator=g).to(DEV) for h in (heads, kv, kv))
+    cs = torch.randn((n, dim), generator=g).to(DEV)
+    pos, seq = torch.arange(n, dtype=torch.int32, device=DEV), torch.zeros(n, dtype=torch.int32, device=DEV)
+    row, other, many = i32([0]), i32([1]), i32([n])
+    state = []
+    for raw in (False, True):
+        c = q8.KVCache.empty(q8.Q8_TYPE_Q8_0, 1, pages, page, kv, dim)
+        table, lens, refs = torch.full((2, 9), -1, dtype=torch.int32, device=DEV), i32([0, 0]), i32([1] + [0] * (pages - 1))
+        if not raw:
+            q8.kv_reserve(c, table, lens, refs, row, many)
+            q16, k16, v16 = q8.kv_append(c, 0, q, k, v, pos, seq, table, cs, 1, torch.float16, want_kv=True)
+            q8.kv_fork(c, table, lens, refs, row, other)
+            o, lse = q8.attn_decode(q16[-2:].contiguous(), c, 0, table, lens, window=50, want_lse=True)
+            p, plse = q8.attn_prompt(q16, k16, v16, i32([0, 40, n]), want_lse=True)
+            q8.kv_free(c, table, lens, refs, row)
+            t2, r2, used = q8.kv_compact(c, table, lens, refs)
+            q8.kv_copy(c, row, i32([pages - 1]))
+        else:
+            s, f16, sc = c.struct, q8.Q8_TYPE_F16, dim ** -0.5
+            new = lambda t: torch.empty_like(t)
+            assert q8.q8_kv_reserve(s, table, 9, 9, 2, lens, refs, row, many, 1) == 0
+            q16, k16, v16 = q.half(), k.half(), v.half()
+            assert q8.q8_kv_append(q16, k16, v16, f16, s, 0, q, heads * dim, k, kv * dim, v, kv * dim, heads, kv, dim, pos, seq, table,
+                                   9, 9, 2, cs, n, dim, 1, n) == 0
+            assert q8.q8_kv_fork(s, table, 9, 9, 2, lens, refs, row, other, 1) == 0
+            o, lse = new(q16[-2:]), torch.empty(2, heads, device=DEV)
+            assert q8.q8_attn_decode(o, f16, lse, q16[-2:].contiguous(), heads * dim, f16, s, 0, table, 9, 9, lens, 2, heads, sc, 50, None) == 0
+            p, plse = new(q16), torch.empty(n, heads, device=DEV)
+            start = i32([0, 40, n])
+            assert q8.q8_attn_prompt(p, f16, plse, q16, k16, v16, f16, heads * dim, kv * dim, kv * dim, start, None, 2, n, n, heads, kv,
+                                     dim, sc, 0, None) == 0
+            assert q8.q8_kv_free(s, table, 9, 9, 2, lens, refs, row, 1) == 0
+            t2, r2, used = new(table), new(refs), torch.empty((), dtype=torch.int32, device=DEV)
+            assert q8.q8_kv_compact(s, t2, table, 9, 9, 2, r2, refs, used) == 0
+            last = i32([pages - 1])
+            assert q8.q8_kv_copy(s, row, last, 1) == 0
+        assert q8.q8_last_error() == 0
+        state.append([q16, k16, v16, o, lse, p, plse, t2, r2, used, table, lens, refs, c.k, c.v])
+    for a, b in zip(*state):
+        assert torch.equal(a, b)
