@@ -187,6 +187,10 @@ PyObject *fill_cache(PyObject *const *a, Py_ssize_t n) {
     if (k.dim() < 3 || k.sizes() != v.sizes() || k.scalar_type() != v.scalar_type() || k.strides() != v.strides() ||
         k.device() != v.device())
         raise(PyExc_ValueError, "k and v must have the same shape, type, strides and device: [n_layers, n_pages, ...]");
+    // bytes (any integer type) hold every format; values only their own
+    if (at::isFloatingType(k.scalar_type()) &&
+        !(type == Q8_TYPE_F16 && k.scalar_type() == at::kHalf) && !(type == Q8_TYPE_BF16 && k.scalar_type() == at::kBFloat16))
+        raise(PyExc_TypeError, "k and v: values of the cache's type, or bytes, expected");
     int64_t want = 1;
     for (int64_t i = k.dim() - 1; i >= 2; --i) {
         if (k.stride(i) != want && k.size(i) != 1) raise(PyExc_ValueError, "a page must be contiguous");

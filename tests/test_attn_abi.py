@@ -196,3 +196,17 @@ def test_caches_on_the_host_are_refused(q8):
                  lambda: q8.kv_copy(c, i32(1), i32(1))):
         with pytest.raises(TypeError, match="cache: pages on the GPU"):
             call()
+
+
+def test_pools_of_another_type_are_refused(q8):
+    import torch
+    for dt in (torch.float16, torch.bfloat16, torch.float32, torch.uint8, torch.int16):
+        size = {torch.float32: 4, torch.uint8: 1}.get(dt, 2)
+        for code, mine in ((q8.Q8_TYPE_F16, torch.float16), (q8.Q8_TYPE_BF16, torch.bfloat16), (q8.Q8_TYPE_Q8_0, None)):
+            n = q8.q8_kv_page_bytes(code, 64, 2, 64) // size
+            k = torch.zeros(1, 4, n, dtype=dt)
+            if dt in (mine, torch.uint8, torch.int16):
+                assert q8.KVCache(k, k.clone(), code, 64, 2, 64).n_pages == 4
+            else:
+                with pytest.raises(TypeError, match="cache's type"):
+                    q8.KVCache(k, k.clone(), code, 64, 2, 64)
