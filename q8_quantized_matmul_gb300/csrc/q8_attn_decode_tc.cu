@@ -13,9 +13,10 @@
 // page, K and V in turn), 128 KB in flight.  16 sequences of up to 4100 positions take 26 us, three times the bytes'
 // time: with 1.4 steps a CTA the start (256 KB a CTA) and the pieces set it, not the stream.
 //
-// The line of steps is cut into equal shares as in the mma.sync kernel; every share of a unit leaves its
-// (m, l, O) in scratch (a unit's 128 KB would take one CTA 10 us to join) and k_attn_decode_join adds them,
-// two heads a CTA, in order.
+// The line of steps is cut into equal shares as in the mma.sync kernel.  A CTA that has all of a unit writes its
+// result; of a unit that is cut every share leaves its (m, l, O) in scratch (a unit's 128 KB would take one CTA 10 us to
+// join) and k_attn_decode_join adds them, two heads a CTA, in order.  Only the first and the last unit of a share can be
+// cut, so each CTA has two places there.
 //
 // Positions that are not visible are masked in S; their V rows are set to zero in shared memory before the
 // product (guard warps), whatever the page holds there.  Waits are bounded as everywhere.
@@ -74,6 +75,32 @@ struct Line {                                                // a CTA's share of
     uint32_t s, shares;
     int run;                                                 // steps of an element of the line
 };
+
+// One dim (this thread's) of N heads from `h0` on, times each head's factor (0: nothing seen), as the result of sequence s.  The
+// 32 lanes of a warp hold 32 dims in a row, which are a Q8_0 block.
+template <int N>
+__device__ __forceinline__ void store_dim(const AttnDecodeParams &p, uint32_t s, uint32_t head0, int h0, int rows, int d, const uint32_t (&o)[N],
+                                          const float *factor) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        if (h0 + e >= rows) break;
+        const float f = factor[h0 + e], y = f == 0.0f ? 0.0f : __uint_as_float(o[e]) * f;
+        const uint64_t i = ((uint64_t)s * p.n_heads + head0 + h0 + e) * p.c.dim + d;
+        if (p.out_type == Q8_TYPE_F32) {
+            static_cast<float *>(p.out)[i] = y;
+        } else if (p.out_type == Q8_TYPE_BF16) {
+            static_cast<__nv_bfloat16 *>(p.out)[i] = __float2bfloat16_rn(y);
+        } else if (p.out_type == Q8_TYPE_F16) {
+            static_cast<__half *>(p.out)[i] = __float2half_rn(y);
+        } else {
+            const float amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fabsf(y), 0.0f))));
+            const float q = __fdiv_rn(amax, 127.0f);
+            uint8_t *blk = static_cast<uint8_t *>(p.out) + i / QK * QB;
+            blk[2 + i % QK] = (uint8_t)(q != 0.0f ? (int)roundf(__fdiv_rn(y, q)) : 0);
+            if (i % QK == 0) *reinterpret_cast<uint16_t *>(blk) = q != 0.0f ? __half_as_ushort(__float2half_rn(q)) : 0;
+        }
+    }
+}
 
 // The segment (part of one unit) that starts at element `at` of the line.
 struct Segment64 {
@@ -472,7 +499,7 @@ __global__ void __launch_bounds__(Dt<D>::THREADS, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(pfull);
             }
-            // ---- this share's piece: sums over the positions, O^T as it stands
+            // ---- sums over the positions, then O^T: the unit's result, or this share's piece as it stands
             tile_wait(ofull, o_seen & 1, p.err, &abort_flag, lim);
             ++o_seen;
             tc_fence_after();
@@ -482,21 +509,39 @@ __global__ void __launch_bounds__(Dt<D>::THREADS, 1)
             sm_w[warp * 64 + 2 * lane + 1] = l[1];
             named_bar_sync(2, 128);
             const uint64_t slot = 2 * (uint64_t)blockIdx.x + (first ? 0 : 1);
-            if (tid < 64)
-                p.part_ml[slot * 64 + tid] = make_float2(weight_ref<LAZY_UP<BF16>>(sm_m[tid]), (sm_w[tid] + sm_w[64 + tid]) + (sm_w[128 + tid] + sm_w[192 + tid]));
+            const bool whole = g.ta == 0 && g.tb == g.q.tiles;
+            if (tid < 64) {
+                const float m = weight_ref<LAZY_UP<BF16>>(sm_m[tid]), sum = (sm_w[tid] + sm_w[64 + tid]) + (sm_w[128 + tid] + sm_w[192 + tid]);
+                if (whole) {
+                    const bool act = tid < g.rows;
+                    float lse;
+                    sm_f[tid] = softmax_finish(m, sum, p.sinks != nullptr, sink_of(p, g.head0 + tid, act), lse);
+                    if (act && p.lse) p.lse[(uint64_t)g.s * p.n_heads + g.head0 + tid] = lse;
+                } else {
+                    p.part_ml[slot * 64 + tid] = make_float2(m, sum);
+                }
+            }
+            if (whole) named_bar_sync(2, 128);               // the factors
 #pragma unroll 1
             for (int c = 0; c < D / 128 * 64; c += 32) {
                 uint32_t o[32];
                 tc_ld32(tmem + lanes + 64 + c, o);
                 tc_wait_ld();
                 tc_regs_ready(o);
-                float *dst = p.part + (slot * 64 + (c & 63)) * D + (c >> 6) * 128 + r;
+                const int d = (c >> 6) * 128 + r;
+                if (whole) {
+                    store_dim(p, g.s, g.head0, c & 63, g.rows, d, o, sm_f);
+                } else {
+                    float *dst = p.part + (slot * 64 + (c & 63)) * D + d;
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    if ((c & 63) + e < g.rows) dst[(uint64_t)e * D] = __uint_as_float(o[e]);
+                    for (int e = 0; e < 32; ++e)
+                        if ((c & 63) + e < g.rows) dst[(uint64_t)e * D] = __uint_as_float(o[e]);
+                }
             }
             tc_fence_before();
-            if (g.ta == 0 && tid == 0) {
+            if (whole && tid == 0) {
+                p.units[g.unit_id] = make_int4(0, 0, -1, 0); // nothing to join
+            } else if (g.ta == 0 && tid == 0) {
                 // the unit starts here: where its pieces are (the first in this CTA, the others each CTA's first)
                 int64_t last = (g.u0 + g.elements - 1) * L.shares / L.total;
                 while (L.total * (last + 1) / L.shares <= g.u0 + g.elements - 1) ++last;
@@ -525,6 +570,7 @@ template <int D> __global__ void __launch_bounds__(128) k_attn_decode_join(const
     const uint32_t kvh = head / p.group, mt = head % p.group / 64, row = head % p.group % 64;
     const int d0 = threadIdx.x % TH * 8;
     const int4 un = p.units[((uint64_t)s * p.c.n_kv + kvh) * p.mtiles + mt];
+    if (un.z < 0) return;                                    // written by the CTA that had all of it (the whole warp)
     auto slot_of = [&](int k) { return k == 0 ? (uint64_t)un.x : 2 * (uint64_t)(un.y + k); };
     const float sink = sink_of(p, head, act);
     float m, l, y[8];

@@ -80,7 +80,8 @@ struct AttnDecodeParams {
     float2 *part_ml, *group_ml;           // maxima and sums of pieces and of joined groups, [2 * grid][16][2]
     int *counters;                        // one per unit and one per slot of a piece, zero between calls
     int *err;
-    // tcgen05 kernel: per unit the slot of its first piece, that piece's CTA and the number of pieces;
+    // tcgen05 kernel: per unit the slot of its first piece, that piece's CTA and the number of pieces (-1: none, the
+    // result is written);
     // part and part_ml then hold 64 rows a slot
     int4 *units;
     uint64_t wait_ns;                     // failure-detection test hook, see GemvParams

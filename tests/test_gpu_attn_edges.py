@@ -239,3 +239,55 @@ def test_raw_calls_agree_with_the_tensor_helpers(q8):
         state.append([q16, k16, v16, o, lse, p, plse, t2, r2, used, table, lens, refs, c.k, c.v])
     for a, b in zip(*state):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("out", [None, "f32", "q8"])
+@pytest.mark.parametrize("kind,dim,heads,kv,lens", [
+    ("bf16", 512, 64, 2, [1, 125, 40, 0, 300, 7, 90, 128, 129] * 16),     # 256 units with a step or more over 152 CTAs
+    ("f16", 256, 33, 5, [1, 70, 20, 0] * 40),                             # 600 of one step: several a CTA
+    ("bf16", 256, 17, 1, [4000] * 3 + [9] * 300)])                        # long ones that are cut beside short ones
+def test_decode_several_units_of_wide_heads_in_a_cta(q8, kind, dim, heads, kv, lens, out):
+    """More (sequence, key-value head, 64 query heads) than CTAs, and shares that hold many short ones: every row against
+    the definition in 64 bits on the GPU, with the error terms of tests/attn_plain.py."""
+    page, dt = 64, torch.bfloat16 if kind == "bf16" else torch.float16
+    n, group, need = len(lens), heads, [-(-m // 64) for m in lens]
+    heads *= kv
+    g = torch.Generator(device=DEV).manual_seed(dim)
+    normal = lambda *s: torch.randn(s, generator=g, device=DEV).to(dt)
+    k, v = normal(1, sum(need), kv, page, dim), normal(1, sum(need), kv, page, dim)
+    table, at = np.full((n, 64), -1, np.int32), 0
+    order = np.random.default_rng(dim).permutation(sum(need))
+    for i, m in enumerate(need):
+        table[i, :m] = order[at:at + m]
+        at += m
+    cache = q8.KVCache(k, v, q8.Q8_TYPE_BF16 if kind == "bf16" else q8.Q8_TYPE_F16, page, kv, dim)
+    q, sinks = normal(n, heads, dim), torch.randn(heads, generator=g, device=DEV)
+    code = {None: None, "f32": q8.Q8_TYPE_F32, "q8": q8.Q8_TYPE_Q8_0}[out]
+    call = lambda c: q8.attn_decode(q, cache, 0, torch.from_numpy(table).to(DEV), i32(lens), sinks=sinks, out_type=c, want_lse=True)
+    o, lse = call(code)
+    assert q8.q8_last_error() == 0
+    if out == "q8":
+        o32, _ = call(q8.Q8_TYPE_F32)
+        assert torch.equal(o.view(n, -1), q8.quantize_act(o32.view(n, -1)))
+        return
+    half = {"bf16": 2.0 ** -8, "f16": 2.0 ** -11}[kind]
+    scale = dim ** -0.5
+    for i, m in enumerate(lens):
+        pages = torch.from_numpy(table[i, :need[i]]).long().to(DEV)
+        kk, vv = (x[0, pages].transpose(0, 1).reshape(kv, -1, dim)[:, :m].double().repeat_interleave(group, 0) for x in (k, v))
+        qq = q[i].double()[:, None]
+        z = (qq @ kk.transpose(1, 2))[:, 0] * scale
+        full = torch.logsumexp(torch.cat([z, sinks.double()[:, None]], 1), 1)
+        w = torch.exp(z - full[:, None])
+        ref, mean = (w[:, None] @ vv)[:, 0], (w[:, None] @ vv.abs())[:, 0]
+        dz = ((dim + 8) * 2.0 ** -23 * scale * (qq.abs() @ kk.abs().transpose(1, 2))[:, 0] + 4 * z.abs() * 2.0 ** -23).amax(1) if m else torch.zeros_like(full)
+        sums = 2.0 ** -21 + (m / 8 + 16) * 2.0 ** -23
+        bound = mean * (half + 2 * dz[:, None] + sums) + (2.0 ** -24 if out else half) * ref.abs() + 1e-30
+        if kind == "f16" and m:
+            bound = bound + 2.0 ** -32 * m * vv.abs().amax(1)
+        if kind == "f16" and not out:
+            bound = bound + 2.0 ** -25                                # half a step of fp16 below its normal numbers
+        err = (o[i].double() - ref).abs()
+        assert torch.all(err <= bound), f"sequence {i} of {m}: {float((err / bound).max()):.2f} of the bound"
+        assert torch.all((lse[i].double() - full).abs() <= 2 * dz + sums + 8 * full.abs() * 2.0 ** -24), f"lse of sequence {i}"
+    assert torch.equal(o, call(code)[0])
