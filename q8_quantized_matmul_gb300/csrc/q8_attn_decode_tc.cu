@@ -14,9 +14,9 @@
 // time: with 1.4 steps a CTA the start (256 KB a CTA) and the pieces set it, not the stream.
 //
 // The line of steps is cut into equal shares as in the mma.sync kernel.  A CTA that has all of a unit writes its
-// result; of a unit that is cut every share leaves its (m, l, O) in scratch (a unit's 128 KB would take one CTA 10 us to
-// join) and k_attn_decode_join adds them, two heads a CTA, in order.  Only the first and the last unit of a share can be
-// cut, so each CTA has two places there.
+// result (200 sequences of 16 positions: 48.8 -> 30.5 us); of a unit that is cut every share leaves its (m, l, O) in scratch (a
+// unit's 128 KB would take one CTA 10 us to join) and k_attn_decode_join adds them, two heads a CTA, in order.  Only the
+// first and the last unit of a share can be cut, so each CTA has two places there.
 //
 // Positions that are not visible are masked in S; their V rows are set to zero in shared memory before the
 // product (guard warps), whatever the page holds there.  Waits are bounded as everywhere.
@@ -76,29 +76,45 @@ struct Line {                                                // a CTA's share of
     int run;                                                 // steps of an element of the line
 };
 
-// One dim (this thread's) of N heads from `h0` on, times each head's factor (0: nothing seen), as the result of sequence s.  The
-// 32 lanes of a warp hold 32 dims in a row, which are a Q8_0 block.
-template <int N>
-__device__ __forceinline__ void store_dim(const AttnDecodeParams &p, uint32_t s, uint32_t head0, int h0, int rows, int d, const uint32_t (&o)[N],
-                                          const float *factor) {
+// A lane's value of the Q8_0 block that the warp's 32 lanes hold.
+__device__ __noinline__ void store_q8_lane(uint8_t *blk, float y) {
+    const int lane = threadIdx.x & 31;
+    const float d = __fdiv_rn(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fabsf(y), 0.0f)))), 127.0f);
+    blk[2 + lane] = (uint8_t)(d != 0.0f ? (int)roundf(__fdiv_rn(y, d)) : 0);
+    if (lane == 0) *reinterpret_cast<uint16_t *>(blk) = d != 0.0f ? __half_as_ushort(__float2half_rn(d)) : 0;
+}
+
+// One dim (this thread's) of `n` of 32 heads, times each head's factor (0: nothing seen), as results; i0: place of the first,
+// the next heads' lie D on.  The type is asked for once: asked for each value, a unit took 40 us to write, not 3.
+template <int D>
+__device__ __forceinline__ void store_dim(const AttnDecodeParams &p, uint64_t i0, int n, const uint32_t (&o)[32], const float *factor) {
+    float y[32];
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-        if (h0 + e >= rows) break;
-        const float f = factor[h0 + e], y = f == 0.0f ? 0.0f : __uint_as_float(o[e]) * f;
-        const uint64_t i = ((uint64_t)s * p.n_heads + head0 + h0 + e) * p.c.dim + d;
-        if (p.out_type == Q8_TYPE_F32) {
-            static_cast<float *>(p.out)[i] = y;
-        } else if (p.out_type == Q8_TYPE_BF16) {
-            static_cast<__nv_bfloat16 *>(p.out)[i] = __float2bfloat16_rn(y);
-        } else if (p.out_type == Q8_TYPE_F16) {
-            static_cast<__half *>(p.out)[i] = __float2half_rn(y);
-        } else {
-            const float amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fabsf(y), 0.0f))));
-            const float q = __fdiv_rn(amax, 127.0f);
-            uint8_t *blk = static_cast<uint8_t *>(p.out) + i / QK * QB;
-            blk[2 + i % QK] = (uint8_t)(q != 0.0f ? (int)roundf(__fdiv_rn(y, q)) : 0);
-            if (i % QK == 0) *reinterpret_cast<uint16_t *>(blk) = q != 0.0f ? __half_as_ushort(__float2half_rn(q)) : 0;
-        }
+    for (int e = 0; e < 32; e += 4) {
+        const float4 f4 = *reinterpret_cast<const float4 *>(factor + e);
+        const float f[4] = {f4.x, f4.y, f4.z, f4.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) y[e + k] = f[k] == 0.0f ? 0.0f : __uint_as_float(o[e + k]) * f[k];
+    }
+    if (p.out_type == Q8_TYPE_Q8_0) {
+        uint8_t *blk = static_cast<uint8_t *>(p.out) + i0 / QK * QB;
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            if (e < n) store_q8_lane(blk + (size_t)e * (D / QK * QB), y[e]);
+    } else if (p.out_type == Q8_TYPE_F32) {
+        float *dst = static_cast<float *>(p.out) + i0;
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            if (e < n) dst[(size_t)e * D] = y[e];
+    } else {
+        uint16_t *dst = static_cast<uint16_t *>(p.out) + i0;
+        const bool bf = p.out_type == Q8_TYPE_BF16;
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) w[e / 2] = bf ? pack16<true>(y[e], y[e + 1]) : pack16<false>(y[e], y[e + 1]);
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            if (e < n) dst[(size_t)e * D] = (uint16_t)(w[e / 2] >> (e % 2 * 16));
     }
 }
 
@@ -509,7 +525,9 @@ __global__ void __launch_bounds__(Dt<D>::THREADS, 1)
             sm_w[warp * 64 + 2 * lane + 1] = l[1];
             named_bar_sync(2, 128);
             const uint64_t slot = 2 * (uint64_t)blockIdx.x + (first ? 0 : 1);
-            const bool whole = g.ta == 0 && g.tb == g.q.tiles;
+            // (A line of runs gives a CTA one piece at most, and a piece leaves sooner than a result: 16 sequences of up to 4100
+            // positions 27.1 -> 26.3 us.)
+            const bool whole = g.ta == 0 && g.tb == g.q.tiles && L.run == 1;
             if (tid < 64) {
                 const float m = weight_ref<LAZY_UP<BF16>>(sm_m[tid]), sum = (sm_w[tid] + sm_w[64 + tid]) + (sm_w[128 + tid] + sm_w[192 + tid]);
                 if (whole) {
@@ -521,21 +539,28 @@ __global__ void __launch_bounds__(Dt<D>::THREADS, 1)
                     p.part_ml[slot * 64 + tid] = make_float2(m, sum);
                 }
             }
-            if (whole) named_bar_sync(2, 128);               // the factors
+            if (!whole) {
 #pragma unroll 1
-            for (int c = 0; c < D / 128 * 64; c += 32) {
-                uint32_t o[32];
-                tc_ld32(tmem + lanes + 64 + c, o);
-                tc_wait_ld();
-                tc_regs_ready(o);
-                const int d = (c >> 6) * 128 + r;
-                if (whole) {
-                    store_dim(p, g.s, g.head0, c & 63, g.rows, d, o, sm_f);
-                } else {
-                    float *dst = p.part + (slot * 64 + (c & 63)) * D + d;
+                for (int c = 0; c < D / 128 * 64; c += 32) {
+                    uint32_t o[32];
+                    tc_ld32(tmem + lanes + 64 + c, o);
+                    tc_wait_ld();
+                    tc_regs_ready(o);
+                    float *dst = p.part + (slot * 64 + (c & 63)) * D + (c >> 6) * 128 + r;
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
                         if ((c & 63) + e < g.rows) dst[(uint64_t)e * D] = __uint_as_float(o[e]);
+                }
+            } else {
+                named_bar_sync(2, 128);                      // the factors
+#pragma unroll 1
+                for (int c = 0; c < D / 128 * 64; c += 32) {
+                    uint32_t o[32];
+                    tc_ld32(tmem + lanes + 64 + c, o);
+                    tc_wait_ld();
+                    tc_regs_ready(o);
+                    const int h0 = c & 63, d = (c >> 6) * 128 + r;
+                    store_dim<D>(p, ((uint64_t)g.s * p.n_heads + g.head0 + h0) * D + d, g.rows - h0, o, sm_f + h0);
                 }
             }
             tc_fence_before();
@@ -570,9 +595,9 @@ template <int D> __global__ void __launch_bounds__(128) k_attn_decode_join(const
     const uint32_t kvh = head / p.group, mt = head % p.group / 64, row = head % p.group % 64;
     const int d0 = threadIdx.x % TH * 8;
     const int4 un = p.units[((uint64_t)s * p.c.n_kv + kvh) * p.mtiles + mt];
-    if (un.z < 0) return;                                    // written by the CTA that had all of it (the whole warp)
     auto slot_of = [&](int k) { return k == 0 ? (uint64_t)un.x : 2 * (uint64_t)(un.y + k); };
     const float sink = sink_of(p, head, act);
+    if (un.z < 0) return;                                    // written by the CTA that had all of it (the whole warp)
     float m, l, y[8];
     join8(un.z, [&](int k) { return p.part + (slot_of(k) * 64 + row) * D + d0; },
           [&](int k) { return p.part_ml + slot_of(k) * 64 + row; }, m, l, y);

@@ -94,15 +94,13 @@ inline uint32_t attn_decode_heads(uint32_t group) { return group <= 8 ? 8 : 16; 
 // 76), and room for more than some positions a sequence (most: what the window or the row of pages allows; the lengths are
 // on the device).  mma.sync starts sooner and does as many units (16 heads of a sequence) at a time as there are SMs, but
 // reads the cache once a unit.  tcgen05 / mma.sync, us:
-//   up to one unit an SM    512 values, 64 heads, 16 sequences: 128 positions 18.0 / 15.4, 192 17.5 / 24.5
-//                           256 values, the same: 256 positions 13.7 / 11.1, 512 13.8 / 21.6
-//   up to three             512 values, 24 heads, 200 sequences: 32 positions 31.5 / 26.6, 64 31.6 / 32.5
-//                           256 values, 64 heads, 48 sequences: 64 positions 15.8 / 13.5, 128 16.3 / 16.2, 192 16.2 / 18.5
-//   more                    64 heads, 200 sequences of 16 positions: 512 values 48.8 / 52.8, 256 values 30.8 / 34.2
+//   up to one unit an SM    512 values, 64 heads, 16 sequences: 128 positions 16.4 / 15.4, 192 17.9 / 24.8
+//                           256 values, the same: 256 positions 13.9 / 11.0, 512 14.1 / 20.6
+//   more                    512 values, 24 heads, 200 sequences: 16 positions 26.0 / 25.2, 64 26.4 / 32.8
+//                           256 values, the same: 16 positions 18.9 / 17.3, 96 19.6 / 21.8; 64 heads 21.3 / 34.1
 inline bool attn_decode_on_tc(uint32_t dim, uint32_t group, bool cache16, uint64_t most, uint64_t seq_heads, int num_sms) {
     if (!cache16 || dim < 256 || group <= 16) return false;
-    const uint64_t units = seq_heads * ((group + 15) / 16);
-    return most > (units <= (uint64_t)num_sms ? 65536 / dim : units <= 3 * (uint64_t)num_sms ? 16384 / dim : 0);
+    return seq_heads * ((group + 15) / 16) > (uint64_t)num_sms || most > 65536 / dim;
 }
 cudaError_t launch_attn_decode_tc(const AttnDecodeParams &p, int grid, cudaStream_t st);
 // CTAs that the decode kernel of this head size and format runs with (0: unsupported).
