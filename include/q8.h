@@ -121,6 +121,37 @@ int q8_rmsnorm_quantize(void *xq, float *y, const float *x, const float *gamma, 
                         uint64_t n_tok, float eps, void *stream);
 
 /*
+ * The residual path between two blocks: the norm after a block, its gate, the scaled
+ * residual sum and the norm before the next block, in one pass.  Per token row t:
+ *   u  = y[t],  or with post != 0  (y[t] * r(y[t])) * gamma_post
+ *   h' = residual_scale * h[t] + gate * u       rounded to h_type, stored in h_out[t]
+ *   n  = (h' * r(h')) * gamma_next              stored in n_out[t]
+ *   r(x) = 1 / sqrt(S / dim + eps),  S = sum_i x_i^2
+ * fp32 arithmetic, every product, sum, quotient and root rounded to nearest on its own, in
+ * the order written; S is the sum rounded to fp32 once (it is carried in two fp32 words,
+ * relative error below 2^-44), so results do not depend on an order of summation.  The
+ * norm before the next block is that of the stored h'.
+ *   n_out      out: [n_tok][dim] of n_type: Q8_TYPE_Q8_0 (blocks for q8_matmul_q, exactly
+ *              the q8_quantize_act bytes of n), F32, F16 or BF16; NULL: only h'.
+ *   h_out      out: rows h_out_stride apart, of h_type; may be h (with h's stride); NULL:
+ *              h' is not stored (then n_out must be given).
+ *   h          in: the residual stream, F32, F16 or BF16, rows h_stride apart.
+ *   y          in: the block's result, F32, F16 or BF16, rows y_stride apart.
+ *   gamma_post, gamma_next  in: fp32 [dim], or NULL for all ones (gamma_post is used with
+ *              post != 0 only).
+ *   gate       in: fp32, row t at gate + t*gate_stride (0: one row for all tokens); NULL:
+ *              no gate.
+ *   residual_scale  finite;  eps > 0 and finite.
+ * dim % 32 == 0, at most 32768.  Strides are elements, multiples of 8, at least dim (gate:
+ * a multiple of 4, or 0); pointers 16-byte aligned.  h_out and n_out must not overlap y,
+ * gate or the gammas, nor each other.  NaN and infinities stay in their row.
+ */
+int q8_residual_norm(void *n_out, int n_type, void *h_out, uint64_t h_out_stride, const void *h, int h_type,
+                     uint64_t h_stride, const void *y, int y_type, uint64_t y_stride, int post, const float *gamma_post,
+                     const float *gate, uint64_t gate_stride, float residual_scale, const float *gamma_next, float eps,
+                     uint64_t dim, uint64_t n_tok, void *stream);
+
+/*
  * Q8_0 matmul from fp32 activations (GPU code walkthrough, trace 3:
  * ds4_gpu_matmul_q8_0_tensor(out, model_map, ..., weight_offset, in_dim,
  * out_dim, x, n_tok); here W is already a device pointer to the weight rows).
@@ -421,6 +452,66 @@ int q8_attn_prompt(void *out, int out_type, float *lse, const void *q, const voi
                    const int32_t *k_start, uint32_t n_seq, uint64_t n_q, uint64_t n_k, uint32_t n_heads,
                    uint32_t n_kv_heads, uint32_t head_dim, float scale, uint32_t window, const float *sinks,
                    void *stream);
+
+/*
+ * Cached keys and values back as rows, for the attention of a prompt's next part over what
+ * is cached (q8_attn_prompt takes rows).  For s < n_seq and i < k_start[s+1] - k_start[s],
+ * with position t = first[s] + i of table row r = seqs[s]:
+ *   k_out[k_start[s] + i][h] = K[r][t][h],  v_out the same from V
+ * the values that the cache holds (Q8_0: d * q), rounded to out_type (to nearest even; cached
+ * values of out_type are copied).
+ *   k_out, v_out  out: F32, F16 or BF16 (out_type), rows of n_kv_heads heads, k_stride and
+ *              v_stride elements apart (multiples of 8); either may be NULL.
+ *   seqs       in: int32 [n_seq], rows of `table` (n_rows of them), or NULL: row s.
+ *   first      in: int32 [n_seq], or NULL: zeros.
+ *   k_start    in: int32 [n_seq + 1], rising, from 0 to at most n_k; as in q8_attn_prompt, values
+ *              outside are cut to the range and raise Q8_ERANGE, as do starts that fall, after
+ *              which any row may be left unwritten; rows of no sequence are not written.
+ * A row of `table` outside n_rows, a negative position or one beyond max_pages pages, and a page id
+ * outside the pool raise Q8_ERANGE; such rows are zeros.
+ */
+int q8_kv_read(void *k_out, uint64_t k_stride, void *v_out, uint64_t v_stride, int out_type, const q8_kv_cache *c,
+               uint32_t layer, const int32_t *table, uint64_t table_stride, uint32_t max_pages, uint32_t n_rows,
+               const int32_t *seqs, const int32_t *first, const int32_t *k_start, uint32_t n_seq, uint64_t n_k,
+               void *stream);
+
+/*
+ * Low-rank adapters of many requests beside a shared projection: each token has its own
+ * adapter, added to what q8_matmul or q8_matmul_q gave for all of them.  With a =
+ * adapter_of[t]:
+ *   out[t][o] = base[t][o] + scales[a] * sum_{i < ranks[a]} B_a[o][i] * (sum_j A_a[i][j] x[t][j])
+ * and out[t] = base[t] (zeros without a base) for a negative a.
+ *   out        out: fp32, rows out_stride apart; may be base (with base's stride).
+ *   base       in: fp32, rows base_stride apart, or NULL: zeros.
+ *   x          in: the projection's input, x_type F32, F16, BF16 (rows x_stride apart, in
+ *              elements, a multiple of 8) or Q8_0 (the blocks that q8_matmul_q takes, rows
+ *              back to back: x_stride is in_dim; the values are d * q).
+ *   adapters   A: 16 bit [n_adapters][max_rank][in_dim], adapters a_stride elements apart;
+ *              B: 16 bit [n_adapters][out_dim][max_rank], b_stride elements apart (multiples
+ *              of 8; so the pools of several projections or layers may lie in one
+ *              allocation).  ranks int32 [n_adapters], 0 to max_rank, or NULL (max_rank);
+ *              scales fp32 [n_adapters] or NULL (1).  What A and B hold from an adapter's
+ *              rank on is never used.  max_rank is a multiple of 8, at most 128;
+ *              n_adapters at most 16384; in_dim % 32 == 0.  The struct is host memory, read
+ *              during the call.
+ *   adapter_of in: int32 [n_tok], in any order (tokens of one adapter need not be neighbours).
+ * x, the rank-sized sums and all other sums keep fp32 accuracy (24 bits of every x and of every
+ * rank-sized sum take part in the products, which are exact, sums in fp32); a value beyond 2^127
+ * or not finite makes its token's row not finite.  An id of n_adapters or beyond counts as negative, a
+ * rank outside its range is cut to it; both raise Q8_ERANGE.  Pointers are 16-byte aligned (the id, rank
+ * and scale arrays 4-byte).
+ */
+typedef struct q8_adapters {
+    const void *a, *b;       /* device */
+    uint64_t a_stride, b_stride;
+    const int32_t *ranks;
+    const float *scales;
+    uint64_t in_dim, out_dim;
+    uint32_t n_adapters, max_rank;
+    int32_t type;            /* Q8_TYPE_F16 or Q8_TYPE_BF16 */
+} q8_adapters;
+int q8_lora(float *out, uint64_t out_stride, const float *base, uint64_t base_stride, const void *x, int x_type,
+            uint64_t x_stride, const q8_adapters *adapters, const int32_t *adapter_of, uint64_t n_tok, void *stream);
 
 /*
  * The pages of a cache.  `refs` (int32 [n_pages]) counts the table rows that hold a

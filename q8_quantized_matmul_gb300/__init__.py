@@ -35,7 +35,7 @@ EXPORTS = ("q8_version", "q8_strerror", "q8_quantize_act", "q8_matmul", "q8_matm
            "q8_moe_combine", "q8_rmsnorm_quantize", "q8_debug_expire_waits", "q8_kq_row_bytes",
            "q8_quantize_q8k", "q8_kq_matmul", "q8_kq_moe_matmul", "q8_kv_page_bytes", "q8_kv_append",
            "q8_attn_decode", "q8_attn_prompt", "q8_kv_reserve", "q8_kv_fork", "q8_kv_free", "q8_kv_compact",
-           "q8_kv_copy")
+           "q8_kv_copy", "q8_kv_read", "q8_residual_norm", "q8_lora")
 
 
 class KVCacheStruct(ctypes.Structure):
@@ -44,6 +44,14 @@ class KVCacheStruct(ctypes.Structure):
                 ("page_stride", ctypes.c_uint64), ("n_layers", ctypes.c_uint32), ("n_pages", ctypes.c_uint32),
                 ("page_tokens", ctypes.c_uint32), ("n_kv_heads", ctypes.c_uint32), ("head_dim", ctypes.c_uint32),
                 ("type", ctypes.c_int32)]
+
+
+class AdaptersStruct(ctypes.Structure):
+    """q8_adapters of include/q8.h."""
+    _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("a_stride", ctypes.c_uint64),
+                ("b_stride", ctypes.c_uint64), ("ranks", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("in_dim", ctypes.c_uint64), ("out_dim", ctypes.c_uint64), ("n_adapters", ctypes.c_uint32),
+                ("max_rank", ctypes.c_uint32), ("type", ctypes.c_int32)]
 
 
 class Q8Error(RuntimeError):
@@ -101,6 +109,10 @@ def _load() -> ctypes.CDLL:
         "q8_kv_free": ([cache, vp, u64, u32, u32, vp, vp, vp, u32, vp], i32),
         "q8_kv_compact": ([cache, vp, vp, u64, u32, u32, vp, vp, vp, vp], i32),
         "q8_kv_copy": ([cache, vp, vp, u32, vp], i32),
+        "q8_kv_read": ([vp, u64, vp, u64, i32, cache, u32, vp, u64, u32, u32, vp, vp, vp, u32, u64, vp], i32),
+        "q8_residual_norm": ([vp, i32, vp, u64, vp, i32, u64, vp, i32, u64, i32, vp, vp, u64, f32, vp, f32, u64, u64,
+                              vp], i32),
+        "q8_lora": ([vp, u64, vp, u64, vp, i32, u64, ctypes.POINTER(AdaptersStruct), vp, u64, vp], i32),
     }
     for name, (args, res) in sig.items():
         f = getattr(L, name)
@@ -301,6 +313,27 @@ def q8_kv_copy(c, src, dst, n: int, stream=None) -> int:
     return _get().q8_kv_copy(c, _p(src), _p(dst), n, _s(stream))
 
 
+def q8_kv_read(k_out, k_stride: int, v_out, v_stride: int, out_type: int, c, layer: int, table, table_stride: int,
+               max_pages: int, n_rows: int, seqs, first, k_start, n_seq: int, n_k: int, stream=None) -> int:
+    return _get().q8_kv_read(_p(k_out), k_stride, _p(v_out), v_stride, out_type, c, layer, _p(table), table_stride,
+                             max_pages, n_rows, _p(seqs), _p(first), _p(k_start), n_seq, n_k, _s(stream))
+
+
+def q8_residual_norm(n_out, n_type: int, h_out, h_out_stride: int, h, h_type: int, h_stride: int, y, y_type: int,
+                     y_stride: int, post: int, gamma_post, gate, gate_stride: int, residual_scale: float, gamma_next,
+                     eps: float, dim: int, n_tok: int, stream=None) -> int:
+    return _get().q8_residual_norm(_p(n_out), n_type, _p(h_out), h_out_stride, _p(h), h_type, h_stride, _p(y), y_type,
+                                   y_stride, post, _p(gamma_post), _p(gate), gate_stride, residual_scale,
+                                   _p(gamma_next), eps, dim, n_tok, _s(stream))
+
+
+def q8_lora(out, out_stride: int, base, base_stride: int, x, x_type: int, x_stride: int, adapters, adapter_of,
+            n_tok: int, stream=None) -> int:
+    """adapters: an AdaptersStruct."""
+    return _get().q8_lora(_p(out), out_stride, _p(base), base_stride, _p(x), x_type, x_stride, adapters, _p(adapter_of),
+                          n_tok, _s(stream))
+
+
 def q8_last_error(stream=None) -> int:
     return _get().q8_last_error(_s(stream))
 
@@ -461,7 +494,7 @@ def kq_moe_matmul(W_experts, fmt: int, n_expert: int, expert_stride: int, ids, x
     return out
 
 
-# ------------------------------------------------------------------ paged key-value cache and attention
+# ------------------------------------------------------------------ paged key-value cache, attention, a layer's paths
 # These calls take microseconds on the GPU, so their marshalling is compiled: csrc/q8_torch.cpp.
 EXT_PATH = os.path.join(_PKG, "_q8torch.so")
 _ext_mod = None
@@ -482,7 +515,7 @@ def _load_ext():
     L = _get()
     mod.init(Q8Error, *(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in (
         "q8_kv_page_bytes", "q8_kv_append", "q8_attn_decode", "q8_attn_prompt", "q8_kv_reserve", "q8_kv_fork",
-        "q8_kv_free", "q8_kv_compact", "q8_kv_copy")))
+        "q8_kv_free", "q8_kv_compact", "q8_kv_copy", "q8_kv_read", "q8_residual_norm", "q8_lora")))
     _ext_mod = mod
     return mod
 
@@ -577,3 +610,30 @@ def kv_compact(cache, table, lens, refs):
 def kv_copy(cache, src, dst) -> None:
     """Page src[i] -> page dst[i] in all layers."""
     (_ext_mod or _load_ext()).kv_copy(cache.address, src, dst)
+
+
+def kv_read(cache, layer: int, table, k_start, n_k: int, first=None, seqs=None, out_type=None, out=None):
+    """Cached tokens as rows: sequence s takes rows k_start[s] to k_start[s + 1] (int32 [n_seq + 1], ending at most at
+    n_k), its tokens from position first[s] (int32, None: 0) of table row seqs[s] (int32, None: s) on.
+    -> k and v [n_k, kv_heads, dim] in out_type (the cache's 16-bit type; bfloat16 for Q8_0), or in out = (k, v), whose
+    rows of no sequence stay as they are."""
+    k, v = (None, None) if out is None else out
+    return (_ext_mod or _load_ext()).kv_read(cache.address, layer, table, k_start, n_k, seqs, first, out_type, k, v)
+
+
+def residual_norm(h, y, gamma_next, eps: float, gamma_post=None, post: bool = False, gate=None,
+                  residual_scale: float = 1.0, out_type=Q8_TYPE_Q8_0, h_out=None):
+    """h' = residual_scale h + gate u, u = y or (post) its RMS norm times gamma_post; n = RMS norm of h' times
+    gamma_next.  h and y [n_tok, dim] float32 or 16 bit (rows strided), gammas float32 [dim] or None, gate float32
+    [dim] or [n_tok, dim] or None.  -> (n, h'): n as Q8_0 blocks [n_tok, dim/32*34] or values of out_type (None: no n);
+    h' in a new tensor, in h_out (which may be h), or not stored (h_out False)."""
+    return (_ext_mod or _load_ext()).residual_norm(h, y, gamma_next, eps, gamma_post, post, gate, residual_scale,
+                                                   out_type, h_out)
+
+
+def lora(x, a, b, adapter_of, ranks=None, scales=None, base=None, out=None):
+    """base + scales[i] b[i] (a[i] x[t]) with i = adapter_of[t] (int32 [n_tok]; negative: base alone).  x [n_tok, in_dim]
+    float32, 16 bit or Q8_0 blocks (uint8 [n_tok, in_dim/32*34]); a [n, rank, in_dim] and b [n, out_dim, rank] 16 bit;
+    ranks int32 [n] (None: all of them), scales float32 [n] (None: 1); base and out float32 [n_tok, out_dim] (rows
+    strided), out may be base.  -> out."""
+    return (_ext_mod or _load_ext()).lora(x, a, b, adapter_of, ranks, scales, base, out)

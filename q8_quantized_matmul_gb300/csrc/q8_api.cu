@@ -9,6 +9,7 @@
 #include "q8_common.cuh"
 #include "q8_kernels.h"
 #include "q8_kv.h"
+#include "q8_layer.h"
 
 // Device error word (one per device context).  Kernels receive its address.
 __device__ int g_q8_device_error = 0;
@@ -597,7 +598,7 @@ int record_cuda_status(cudaError_t e) {
 
 extern "C" {
 
-int q8_version(void) { return 10200; }
+int q8_version(void) { return 10300; }
 
 const char *q8_strerror(int status) {
     switch (status) {
@@ -1160,6 +1161,7 @@ static int page_shift_of(uint32_t page_tokens) {
 
 static bool head_dim_ok(uint32_t d) { return d == 64 || d == 128 || d == 256 || d == 512; }
 static bool type16(int t) { return t == Q8_TYPE_F16 || t == Q8_TYPE_BF16; }
+static bool value_type(int t) { return t == Q8_TYPE_F32 || type16(t); }
 static bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 constexpr uint32_t MAX_HEADS = 4096;
@@ -1388,6 +1390,46 @@ int q8_attn_prompt(void *out, int out_type, float *lse, const void *q, const voi
     return status_of(q8::launch_attn_prompt(p, list ? s->scratch.p : nullptr, s->num_sms, st));
 }
 
+int q8_kv_read(void *k_out, uint64_t k_stride, void *v_out, uint64_t v_stride, int out_type, const q8_kv_cache *c,
+               uint32_t layer, const int32_t *table, uint64_t table_stride, uint32_t max_pages, uint32_t n_rows,
+               const int32_t *seqs, const int32_t *first, const int32_t *k_start, uint32_t n_seq, uint64_t n_k,
+               void *stream) {
+    q8::KvReadParams p{};
+    int rc = check_cache(c, p.c);
+    if (rc) return rc;
+    if ((rc = check_table(table, table_stride, max_pages))) return rc;
+    if (layer >= c->n_layers || n_rows == 0 || n_seq > MAX_SEQS || n_k > ((uint64_t)1 << 28)) return Q8_EINVAL;
+    if (!value_type(out_type) || (!seqs && n_seq > n_rows)) return Q8_EINVAL;
+    if (n_seq == 0 || n_k == 0) return Q8_OK;
+    if ((!k_out && !v_out) || !k_start) return Q8_EINVAL;
+    const uint64_t row = (uint64_t)c->n_kv_heads * c->head_dim, most = (uint64_t)1 << 32;
+    if ((k_out && (k_stride < row || k_stride > most)) || (v_out && (v_stride < row || v_stride > most))) return Q8_EINVAL;
+    if (!aligned16(k_out) || !aligned16(v_out) || (k_out && k_stride % 8) || (v_out && v_stride % 8) || !aligned4(seqs) ||
+        !aligned4(first) || !aligned4(k_start))
+        return Q8_EALIGN;
+    std::lock_guard<std::mutex> lk(g_mutex);
+    DeviceState *s;
+    if ((rc = get_device(&s))) return rc;
+    p.c.k += layer * c->layer_stride;
+    p.c.v += layer * c->layer_stride;
+    p.k_out = k_out;
+    p.v_out = v_out;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.out_type = out_type;
+    p.table = table;
+    p.seqs = seqs;
+    p.first = first;
+    p.k_start = k_start;
+    p.table_stride = table_stride;
+    p.max_pages = max_pages;
+    p.n_rows = n_rows;
+    p.n_seq = n_seq;
+    p.n_k = (uint32_t)n_k;
+    p.err = s->err;
+    return status_of(q8::launch_kv_read(p, s->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
 // Arguments that the page calls share; fills p but for its scratch.
 static int check_pages(q8::KvPagesParams &p, const q8_kv_cache *c, int32_t *table, uint64_t table_stride,
                        uint32_t max_pages, uint32_t n_rows) {
@@ -1499,6 +1541,101 @@ int q8_kv_copy(const q8_kv_cache *c, const int32_t *src, const int32_t *dst, uin
     DeviceState *s;
     if ((rc = pages_device(p, &s, false, static_cast<cudaStream_t>(stream)))) return rc;
     return status_of(q8::launch_kv_copy(p, s->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+// ---- around a layer's projections
+
+int q8_residual_norm(void *n_out, int n_type, void *h_out, uint64_t h_out_stride, const void *h, int h_type,
+                     uint64_t h_stride, const void *y, int y_type, uint64_t y_stride, int post, const float *gamma_post,
+                     const float *gate, uint64_t gate_stride, float residual_scale, const float *gamma_next, float eps,
+                     uint64_t dim, uint64_t n_tok, void *stream) {
+    if (dim == 0 || dim % q8::QK || dim > q8::RESIDUAL_MAX_DIM || n_tok > ((uint64_t)1 << 31) - 1) return Q8_EINVAL;
+    if (!value_type(h_type) || !value_type(y_type) || (n_out && n_type != Q8_TYPE_Q8_0 && !value_type(n_type))) return Q8_EINVAL;
+    if (!(eps > 0.0f) || eps == __builtin_inff()) return Q8_EINVAL;
+    if (!(residual_scale - residual_scale == 0.0f)) return Q8_EINVAL;   // NaN or infinite
+    if (n_tok == 0) return Q8_OK;
+    if ((!n_out && !h_out) || !h || !y) return Q8_EINVAL;
+    const uint64_t most = (uint64_t)1 << 32;
+    if (h_stride < dim || h_stride > most || y_stride < dim || y_stride > most) return Q8_EINVAL;
+    if (h_out && (h_out_stride < dim || h_out_stride > most)) return Q8_EINVAL;
+    if (h_out == h && h_out_stride != h_stride) return Q8_EINVAL;
+    if (gate && gate_stride && (gate_stride < dim || gate_stride > most)) return Q8_EINVAL;
+    if (!aligned16(n_out) || !aligned16(h_out) || !aligned16(h) || !aligned16(y) || !aligned16(gamma_post) || !aligned16(gate) ||
+        !aligned16(gamma_next) || h_stride % 8 || y_stride % 8 || (h_out && h_out_stride % 8) || (gate && gate_stride % 4))
+        return Q8_EALIGN;
+    std::lock_guard<std::mutex> lk(g_mutex);
+    DeviceState *s;
+    int rc;
+    if ((rc = get_device(&s))) return rc;
+    q8::ResidualNormParams p{};
+    p.n_out = n_out;
+    p.n_type = n_type;
+    p.h_out = h_out;
+    p.h = h;
+    p.y = y;
+    p.h_out_stride = h_out_stride;
+    p.h_stride = h_stride;
+    p.y_stride = y_stride;
+    p.gamma_post = gamma_post;
+    p.gate = gate;
+    p.gamma_next = gamma_next;
+    p.gate_stride = gate_stride;
+    p.post = post != 0;
+    p.residual_scale = residual_scale;
+    p.eps = eps;
+    p.dim = (uint32_t)dim;
+    p.n_tok = n_tok;
+    return status_of(q8::launch_residual_norm(p, h_type, y_type, s->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+int q8_lora(float *out, uint64_t out_stride, const float *base, uint64_t base_stride, const void *x, int x_type,
+            uint64_t x_stride, const q8_adapters *adapters, const int32_t *adapter_of, uint64_t n_tok, void *stream) {
+    if (!adapters) return Q8_EINVAL;
+    const q8_adapters &ad = *adapters;
+    int rc = check_dims(ad.in_dim, ad.out_dim, n_tok);
+    if (rc) return rc;
+    if (!type16(ad.type) || (x_type != Q8_TYPE_Q8_0 && !value_type(x_type))) return Q8_EINVAL;
+    if (ad.max_rank == 0 || ad.max_rank % 8 || ad.max_rank > q8::LORA_MAX_RANK) return Q8_EINVAL;
+    if (ad.n_adapters == 0 || ad.n_adapters > q8::LORA_MAX_ADAPTERS) return Q8_EINVAL;
+    const uint64_t most = (uint64_t)1 << 32, a_one = ad.max_rank * ad.in_dim, b_one = ad.max_rank * ad.out_dim;
+    if (a_one > most || b_one > 32 * most) return Q8_EINVAL;
+    if (ad.n_adapters > 1 && (ad.a_stride < a_one || ad.a_stride > 256 * most || ad.b_stride < b_one || ad.b_stride > 256 * most))
+        return Q8_EINVAL;
+    if (n_tok == 0 || ad.out_dim == 0) return Q8_OK;
+    if (!out || !x || !ad.a || !ad.b || !adapter_of) return Q8_EINVAL;
+    if (out_stride < ad.out_dim || out_stride > most || (base && (base_stride < ad.out_dim || base_stride > most))) return Q8_EINVAL;
+    if (out == base && out_stride != base_stride) return Q8_EINVAL;
+    if (x_type == Q8_TYPE_Q8_0 ? x_stride != ad.in_dim : (x_stride < ad.in_dim || x_stride > most)) return Q8_EINVAL;
+    if (!aligned16(out) || !aligned16(base) || !aligned16(x) || !aligned16(ad.a) || !aligned16(ad.b) || x_stride % 8 ||
+        (ad.n_adapters > 1 && (ad.a_stride % 8 || ad.b_stride % 8)) || !aligned4(ad.ranks) || !aligned4(ad.scales) ||
+        !aligned4(adapter_of))
+        return Q8_EALIGN;
+    std::lock_guard<std::mutex> lk(g_mutex);
+    DeviceState *s;
+    if ((rc = get_device(&s))) return rc;
+    q8::LoraParams p{};
+    p.out = out;
+    p.base = base;
+    p.x = x;
+    p.out_stride = out_stride;
+    p.base_stride = base_stride;
+    p.x_stride = x_stride;
+    p.x_type = x_type;
+    p.a = static_cast<const uint16_t *>(ad.a);
+    p.b = static_cast<const uint16_t *>(ad.b);
+    p.a_stride = ad.a_stride;
+    p.b_stride = ad.b_stride;
+    p.ranks = ad.ranks;
+    p.scales = ad.scales;
+    p.in_dim = (uint32_t)ad.in_dim;
+    p.out_dim = (uint32_t)ad.out_dim;
+    p.n_adapters = ad.n_adapters;
+    p.max_rank = ad.max_rank;
+    p.bf16 = ad.type == Q8_TYPE_BF16;
+    p.adapter_of = adapter_of;
+    p.n_tok = (uint32_t)n_tok;
+    p.err = s->err;
+    return status_of(q8::launch_lora(p, s->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
 uint64_t q8_repack_bytes(uint64_t in_dim, uint64_t rows, int layout) {

@@ -118,6 +118,90 @@ __global__ void __launch_bounds__(APPEND_THREADS) k_kv_append(const KvAppendPara
     }
 }
 
+// ---------------------------------------------------------------- reading back
+constexpr int READ_THREADS = 256;
+constexpr int READ_ROWS = 32;             // rows of a CTA
+
+// Value chunk d0 .. d0 + 7 of a cached row, as fp32.
+__device__ __forceinline__ void cached8(float (&y)[8], const uint8_t *tile, uint32_t t, uint32_t d0, const KvPool &c) {
+    if (c.type == Q8_TYPE_Q8_0) {
+        const uint2 q = *reinterpret_cast<const uint2 *>(tile + (uint64_t)t * c.dim + d0);
+        const float d = half_bits_to_float(*reinterpret_cast<const uint16_t *>(
+            tile + ((uint64_t)c.dim << c.page_shift) + ((uint64_t)t * (c.dim / QK) + d0 / QK) * 2));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = (float)(int8_t)((e < 4 ? q.x : q.y) >> (8 * (e & 3))) * d;
+        return;
+    }
+    const uint4 v = *reinterpret_cast<const uint4 *>(tile + ((uint64_t)t * c.dim + d0) * 2);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        y[2 * e] = c.type == Q8_TYPE_BF16 ? __uint_as_float(w[e] << 16) : half_bits_to_float((uint16_t)w[e]);
+        y[2 * e + 1] = c.type == Q8_TYPE_BF16 ? __uint_as_float(w[e] & 0xffff0000u) : half_bits_to_float((uint16_t)(w[e] >> 16));
+    }
+}
+
+// Rows [32 blockIdx.x, ...) of K (blockIdx.y 0) or V: where each lies is looked up once, then one thread per 8 values.
+__global__ void __launch_bounds__(READ_THREADS) k_kv_read(const KvReadParams p) {
+    __shared__ int2 at[READ_ROWS];        // page (-1: none, the row is zeros; -2: no row), row in the page
+    grid_dep_wait();
+    const bool v = blockIdx.y == (p.k_out ? 1u : 0u);
+    if (blockIdx.x == 0 && blockIdx.y == 0) {
+        bool bad = false;
+        for (uint32_t s = threadIdx.x; s <= p.n_seq; s += READ_THREADS) {
+            const int32_t k = p.k_start[s];
+            bad |= k < 0 || (uint32_t)k > p.n_k || (s && k < p.k_start[s - 1]) || (!s && k);
+        }
+        if (bad) raise_error(p.err, DEV_ERANGE);
+    }
+    const uint32_t row0 = blockIdx.x * READ_ROWS, rows = min((uint32_t)READ_ROWS, p.n_k - row0);
+    if (threadIdx.x < rows) {
+        const int32_t row = (int32_t)(row0 + threadIdx.x);
+        // the last sequence that starts at or before the row
+        uint32_t lo = 0, hi = p.n_seq + 1;
+        while (lo < hi) {
+            const uint32_t mid = (lo + hi) / 2;
+            if (p.k_start[mid] <= row) lo = mid + 1;
+            else hi = mid;
+        }
+        int2 a = make_int2(-2, 0);
+        if (lo > 0 && lo <= p.n_seq) {
+            const uint32_t s = lo - 1;
+            const int32_t r = p.seqs ? p.seqs[s] : (int32_t)s;
+            const int64_t pos = (int64_t)(p.first ? p.first[s] : 0) + row - p.k_start[s];
+            const int64_t slot = pos >> p.c.page_shift;
+            a.x = -1;
+            if (r >= 0 && (uint32_t)r < p.n_rows && pos >= 0 && slot < p.max_pages) {
+                const int32_t page = p.table[(uint64_t)r * p.table_stride + slot];
+                if (page >= 0 && (uint32_t)page < p.c.n_pages) a = make_int2(page, (int)(pos & ((1 << p.c.page_shift) - 1)));
+            }
+            if (a.x < 0) raise_error(p.err, DEV_ERANGE);
+        }
+        at[threadIdx.x] = a;
+    }
+    __syncthreads();
+    const uint32_t shift = 28 - __clz(p.c.dim), per_row = p.c.n_kv << shift, items = rows * per_row;
+    const uint8_t *pool = v ? p.c.v : p.c.k;
+    void *out = v ? p.v_out : p.k_out;
+    const uint64_t stride = v ? p.v_stride : p.k_stride;
+#pragma unroll 4
+    for (uint32_t i = threadIdx.x; i < items; i += READ_THREADS) {
+        const uint32_t r = i / per_row, c = i - r * per_row, h = c >> shift, d0 = (c & ((1u << shift) - 1u)) * 8;
+        const int2 a = at[r];
+        if (a.x == -2) continue;
+        const uint8_t *tile = pool + (uint64_t)max(a.x, 0) * p.c.page_stride + (uint64_t)h * p.c.tile_bytes;
+        if (p.c.type == p.out_type) {
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (a.x >= 0) w = *reinterpret_cast<const uint4 *>(tile + ((uint64_t)a.y * p.c.dim + d0) * 2);
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + (row0 + r) * stride + c * 8) = w;
+            continue;
+        }
+        float y[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+        if (a.x >= 0) cached8(y, tile, a.y, d0, p.c);
+        store_out8(out, p.out_type, (row0 + r) * stride + c * 8, y, true);
+    }
+}
+
 // ---------------------------------------------------------------- plans (one CTA)
 constexpr int PLAN_THREADS = 1024;
 
@@ -461,6 +545,11 @@ cudaError_t launch_kv_append(KvAppendParams p, int num_sms, cudaStream_t st) {
     const uint64_t ctas = (p.n_tok + p.tokens_cta - 1) / p.tokens_cta;
     const uint64_t parts = ctas >= 2 * (uint64_t)num_sms ? 1 : (per_tok + APPEND_THREADS - 1) / APPEND_THREADS;
     return launch_dependent(k_kv_append, p, dim3((unsigned)ctas, (unsigned)parts), APPEND_THREADS, 0, st);
+}
+
+cudaError_t launch_kv_read(const KvReadParams &p, int, cudaStream_t st) {
+    const unsigned ctas = (p.n_k + READ_ROWS - 1) / READ_ROWS;
+    return launch_dependent(k_kv_read, p, dim3(ctas, (p.k_out ? 1u : 0u) + (p.v_out ? 1u : 0u)), READ_THREADS, 0, st);
 }
 
 size_t kv_pages_scratch(uint32_t n, uint32_t n_pages) {

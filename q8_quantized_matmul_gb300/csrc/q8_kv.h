@@ -36,6 +36,18 @@ struct KvAppendParams {
 };
 cudaError_t launch_kv_append(KvAppendParams p, int num_sms, cudaStream_t st);
 
+struct KvReadParams {
+    KvPool c;
+    void *k_out, *v_out;                  // or nullptr
+    uint64_t k_stride, v_stride;          // elements
+    int out_type;
+    const int32_t *table, *seqs, *first, *k_start;
+    uint64_t table_stride;
+    uint32_t max_pages, n_rows, n_seq, n_k;
+    int *err;
+};
+cudaError_t launch_kv_read(const KvReadParams &p, int num_sms, cudaStream_t st);
+
 struct KvPagesParams {
     KvPool c;
     int32_t *table;

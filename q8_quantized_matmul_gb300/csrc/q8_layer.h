@@ -1,0 +1,48 @@
+// q8_layer.h -- internal interface of the calls around a layer's projections: the residual path's norms and the
+// low-rank adapters.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace q8 {
+
+struct ResidualNormParams {
+    void *n_out;                          // or nullptr
+    int n_type;
+    void *h_out;                          // or nullptr
+    const void *h, *y;
+    uint64_t h_out_stride, h_stride, y_stride;   // elements
+    const float *gamma_post, *gate, *gamma_next;
+    uint64_t gate_stride;
+    int post;
+    float residual_scale, eps;
+    uint32_t dim;
+    uint64_t n_tok;
+};
+constexpr uint32_t RESIDUAL_MAX_DIM = 32768;
+// h_type, y_type: Q8_TYPE_F32, F16 or BF16.
+cudaError_t launch_residual_norm(const ResidualNormParams &p, int h_type, int y_type, int num_sms, cudaStream_t st);
+
+struct LoraParams {
+    float *out;
+    const float *base;                    // or nullptr
+    const void *x;
+    uint64_t out_stride, base_stride, x_stride;   // elements; Q8_0 rows: x_stride is in_dim
+    int x_type;
+    const uint16_t *a, *b;
+    uint64_t a_stride, b_stride;          // elements
+    const int32_t *ranks;                 // or nullptr
+    const float *scales;                  // or nullptr
+    uint32_t in_dim, out_dim;
+    uint32_t n_adapters, max_rank;
+    int bf16;                             // type of A and B
+    const int32_t *adapter_of;
+    uint32_t n_tok;
+    int *err;
+    uint32_t splits;                      // clusters that share a group's outputs (set by the launcher)
+};
+constexpr uint32_t LORA_MAX_RANK = 128, LORA_MAX_ADAPTERS = 16384;
+cudaError_t launch_lora(const LoraParams &p, int num_sms, cudaStream_t st);
+
+}  // namespace q8

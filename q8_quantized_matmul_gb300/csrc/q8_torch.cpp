@@ -1,5 +1,5 @@
-// q8_torch.cpp -- the tensor helpers of the paged cache and the attention (attn_decode, kv_append, ...) as a
-// CPython module: argument checks, output tensors and the call, nothing else.  These calls take 3 to 10 us on
+// q8_torch.cpp -- the tensor helpers of the paged cache, the attention and the calls around a layer's projections
+// (attn_decode, kv_append, residual_norm, lora, ...) as a CPython module: argument checks, output tensors and the call, nothing else.  These calls take 3 to 10 us on
 // the GPU, and the same marshalling through ctypes and tensor methods took 10 to 14 us of host time a call
 // (measured on Grace; here 5 to 7 us, of which the launch itself is 3).
 //
@@ -26,6 +26,9 @@ decltype(&q8_kv_fork) f_fork;
 decltype(&q8_kv_free) f_free;
 decltype(&q8_kv_compact) f_compact;
 decltype(&q8_kv_copy) f_copy;
+decltype(&q8_kv_read) f_read;
+decltype(&q8_residual_norm) f_residual;
+decltype(&q8_lora) f_lora;
 
 struct Raised {};   // a Python exception is set
 
@@ -417,9 +420,189 @@ PyObject *kv_copy(PyObject *const *a, Py_ssize_t n) {
     Py_RETURN_NONE;
 }
 
-// init(Q8Error, addresses of the nine entry points)
-PyObject *init(PyObject *const *a, Py_ssize_t n) {
+// kv_read(cache, layer, table, k_start, n_k, seqs, first, out_type, k_out, v_out)
+PyObject *kv_read(PyObject *const *a, Py_ssize_t n) {
     arity(n, 10);
+    const q8_kv_cache *c = cache_of(a[0]);
+    if (!c) raise(PyExc_TypeError, "cache: a KVCache expected");
+    on_gpu(c);
+    const uint32_t layer = word(a[1], "layer");
+    const Table t = table_of(a[2]);
+    const int64_t n_start = length(a[3], "k_start"), rows = word(a[4], "n_k");
+    if (n_start < 1) raise(PyExc_ValueError, "k_start: [n_seq + 1] expected");
+    if ((a[5] != Py_None && length(a[5], "seqs") != n_start - 1) || (a[6] != Py_None && length(a[6], "first") != n_start - 1) ||
+        (a[5] == Py_None && n_start - 1 > t.rows))
+        raise(PyExc_ValueError, "table, k_start, seqs and first disagree");
+    const int32_t *start = ints(a[3], "k_start"), *seqs = ints(a[5], "seqs"), *first = ints(a[6], "first");
+    int out_type = a[7] != Py_None ? (int)integer(a[7]) : c->type == Q8_TYPE_Q8_0 ? Q8_TYPE_BF16 : c->type;
+    const int64_t heads = c->n_kv_heads, dim = c->head_dim;
+    at::Tensor k, v;
+    if (a[8] != Py_None || a[9] != Py_None) {
+        if (a[8] == Py_None || a[9] == Py_None) raise(PyExc_ValueError, "out: both k and v expected");
+        k = tensor(a[8], "k");
+        v = tensor(a[9], "v");
+        const int kind = k.scalar_type() == at::kFloat ? Q8_TYPE_F32 : type16(k.scalar_type());
+        if (v.scalar_type() != k.scalar_type() || (a[7] != Py_None && kind != out_type)) raise(PyExc_TypeError, "out: k, v and out_type disagree");
+        for (const at::Tensor *x : {&k, &v})
+            if (x->dim() != 3 || x->size(0) < rows || x->size(1) != heads || x->size(2) != dim)
+                raise(PyExc_ValueError, "out: k and v of at least n_k rows [n_kv_heads, head_dim] expected");
+        out_type = kind;
+    } else {
+        const auto type = out_type == Q8_TYPE_F32 ? at::kFloat : out_type == Q8_TYPE_BF16 ? at::kBFloat16 : at::kHalf;
+        if (out_type != Q8_TYPE_F32 && out_type != Q8_TYPE_BF16 && out_type != Q8_TYPE_F16) raise_status(Q8_EINVAL, "out_type");
+        const auto opt = tensor(a[2], "table").options().dtype(type);
+        k = at::empty({rows, heads, dim}, opt);
+        v = at::empty({rows, heads, dim}, opt);
+    }
+    const int64_t ks = row_stride(k, "k"), vs = row_stride(v, "v");
+    void *kp = k.data_ptr(), *vp = v.data_ptr(), *st = stream_for(c, a, {2, 3, 5, 6, 8, 9});
+    call("q8_kv_read", [&] {
+        return f_read(kp, ks, vp, vs, out_type, c, layer, t.p, t.stride, (uint32_t)t.width, (uint32_t)t.rows, seqs, first, start,
+                      (uint32_t)(n_start - 1), rows, st);
+    });
+    return Py_BuildValue("(NN)", wrap(k), wrap(v));
+}
+
+// [rows, n] GPU tensor with contiguous rows: its row stride.
+int64_t matrix_stride(const at::Tensor &t, int64_t rows, int64_t n, const char *name) {
+    if (t.dim() != 2 || !t.is_cuda() || t.size(0) != rows || t.size(1) != n || (t.stride(1) != 1 && n != 1)) {
+        PyErr_Format(PyExc_ValueError, "%s: a GPU tensor [%lld, %lld] with contiguous rows expected", name, (long long)rows, (long long)n);
+        throw Raised{};
+    }
+    return rows > 1 ? t.stride(0) : n;
+}
+
+int value_type(const at::Tensor &t) { return t.scalar_type() == at::kFloat ? Q8_TYPE_F32 : type16(t.scalar_type()); }
+
+const float *floats(PyObject *o, int64_t n, const char *name) {
+    if (o == Py_None) return nullptr;
+    const at::Tensor &t = tensor(o, name);
+    if (t.scalar_type() != at::kFloat || t.numel() != n || !t.is_contiguous() || !t.is_cuda()) {
+        PyErr_Format(PyExc_TypeError, "%s: contiguous float32 of %lld values on the GPU expected", name, (long long)n);
+        throw Raised{};
+    }
+    return static_cast<const float *>(t.data_ptr());
+}
+
+float real(PyObject *o) {
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) throw Raised{};
+    return (float)v;
+}
+
+// residual_norm(h, y, gamma_next, eps, gamma_post, post, gate, residual_scale, out_type, h_out) -> n, h_out
+// out_type None: no n; h_out None: a new tensor, False: not stored
+PyObject *residual_norm(PyObject *const *a, Py_ssize_t n) {
+    arity(n, 10);
+    const at::Tensor &h = tensor(a[0], "h"), &y = tensor(a[1], "y");
+    if (h.dim() != 2) raise(PyExc_ValueError, "h: [n_tok, dim] expected");
+    const int64_t tok = h.size(0), dim = h.size(1);
+    const int64_t hs = matrix_stride(h, tok, dim, "h"), ys = matrix_stride(y, tok, dim, "y");
+    const int ht = value_type(h), yt = value_type(y), post = PyObject_IsTrue(a[5]);
+    if (post < 0) throw Raised{};
+    const float *next = floats(a[2], dim, "gamma_next"), *before = floats(a[4], dim, "gamma_post"), *gate = nullptr;
+    const float eps = real(a[3]), scale = real(a[7]);
+    int64_t gs = 0;
+    if (a[6] != Py_None) {
+        const at::Tensor &g = tensor(a[6], "gate");
+        if (g.dim() == 1) gate = floats(a[6], dim, "gate");
+        else {
+            if (g.scalar_type() != at::kFloat) raise(PyExc_TypeError, "gate: float32 expected");
+            gs = matrix_stride(g, tok, dim, "gate");
+            gate = static_cast<const float *>(g.data_ptr());
+        }
+    }
+    at::Tensor out, ho;
+    int out_type = Q8_TYPE_F32;
+    if (a[8] != Py_None) {
+        out_type = (int)integer(a[8]);
+        if (out_type == Q8_TYPE_Q8_0) out = at::empty({tok, dim / Q8_BLOCK * Q8_BLOCK_BYTES}, h.options().dtype(at::kByte));
+        else if (out_type == Q8_TYPE_F32) out = at::empty({tok, dim}, h.options().dtype(at::kFloat));
+        else if (out_type == Q8_TYPE_BF16) out = at::empty({tok, dim}, h.options().dtype(at::kBFloat16));
+        else if (out_type == Q8_TYPE_F16) out = at::empty({tok, dim}, h.options().dtype(at::kHalf));
+        else raise_status(Q8_EINVAL, "out_type");
+    }
+    int64_t hos = 0;
+    if (a[9] == Py_None) {
+        ho = at::empty({tok, dim}, h.options());
+        hos = dim;
+    } else if (a[9] != Py_False) {
+        ho = tensor(a[9], "h_out");
+        if (ho.scalar_type() != h.scalar_type()) raise(PyExc_TypeError, "h_out: h's type expected");
+        hos = matrix_stride(ho, tok, dim, "h_out");
+    }
+    void *op = out.defined() ? out.data_ptr() : nullptr, *hop = ho.defined() ? ho.data_ptr() : nullptr;
+    const void *hp = h.data_ptr(), *yp = y.data_ptr();
+    void *st = a[9] == Py_False ? stream_for(nullptr, a, {0, 1, 2, 4, 6}) : stream_for(nullptr, a, {0, 1, 2, 4, 6, 9});
+    call("q8_residual_norm", [&] {
+        return f_residual(op, out_type, hop, hos, hp, ht, hs, yp, yt, ys, post, before, gate, gs, scale, next, eps, dim, tok, st);
+    });
+    return Py_BuildValue("(NN)", none_or(out), none_or(ho));
+}
+
+// lora(x, a, b, adapter_of, ranks, scales, base, out) -> out
+PyObject *lora(PyObject *const *a, Py_ssize_t n) {
+    arity(n, 8);
+    const at::Tensor &x = tensor(a[0], "x"), &wa = tensor(a[1], "a"), &wb = tensor(a[2], "b");
+    if (x.dim() != 2 || wa.dim() != 3 || wb.dim() != 3 || wa.size(0) != wb.size(0) || wa.size(1) != wb.size(2))
+        raise(PyExc_ValueError, "x [n_tok, in_dim], a [n, rank, in_dim] and b [n, out_dim, rank] expected");
+    if (wa.scalar_type() != wb.scalar_type()) raise(PyExc_TypeError, "a and b: one type expected");
+    const int64_t tok = x.size(0), in = wa.size(2), od = wb.size(1), rank = wa.size(1), count = wa.size(0);
+    for (const at::Tensor *w : {&wa, &wb})
+        if (!w->is_cuda() || (w->stride(2) != 1 && w->size(2) != 1) || (w->stride(1) != w->size(2) && w->size(1) != 1))
+            raise(PyExc_ValueError, "a and b: adapters of contiguous rows on the GPU expected");
+    q8_adapters ad{};
+    ad.a = wa.data_ptr();
+    ad.b = wb.data_ptr();
+    ad.a_stride = count > 1 ? wa.stride(0) : rank * in;
+    ad.b_stride = count > 1 ? wb.stride(0) : rank * od;
+    ad.ranks = a[4] == Py_None ? nullptr : ints(a[4], "ranks");
+    if (ad.ranks && length(a[4], "ranks") != count) raise(PyExc_ValueError, "ranks: [n] expected");
+    ad.scales = floats(a[5], count, "scales");
+    ad.in_dim = in;
+    ad.out_dim = od;
+    if (count > 0xffffffffll || rank > 0xffffffffll) raise(PyExc_ValueError, "a: out of range");
+    ad.n_adapters = (uint32_t)count;
+    ad.max_rank = (uint32_t)rank;
+    ad.type = type16(wa.scalar_type());
+    int xt;
+    int64_t xs;
+    if (x.scalar_type() == at::kByte) {
+        xt = Q8_TYPE_Q8_0;
+        if (!x.is_cuda() || !x.is_contiguous() || in % Q8_BLOCK || x.size(1) != in / Q8_BLOCK * Q8_BLOCK_BYTES)
+            raise(PyExc_ValueError, "x: contiguous Q8_0 rows of in_dim values on the GPU expected");
+        xs = in;
+    } else {
+        xt = value_type(x);
+        xs = matrix_stride(x, tok, in, "x");
+    }
+    if (length(a[3], "adapter_of") != tok) raise(PyExc_ValueError, "adapter_of: [n_tok] expected");
+    const int32_t *ids = ints(a[3], "adapter_of");
+    const float *base = nullptr;
+    int64_t bs = 0, os = od;
+    if (a[6] != Py_None) {
+        const at::Tensor &t = tensor(a[6], "base");
+        if (t.scalar_type() != at::kFloat) raise(PyExc_TypeError, "base: float32 expected");
+        bs = matrix_stride(t, tok, od, "base");
+        base = static_cast<const float *>(t.data_ptr());
+    }
+    at::Tensor out;
+    if (a[7] == Py_None) out = at::empty({tok, od}, x.options().dtype(at::kFloat));
+    else {
+        out = tensor(a[7], "out");
+        if (out.scalar_type() != at::kFloat) raise(PyExc_TypeError, "out: float32 expected");
+        os = matrix_stride(out, tok, od, "out");
+    }
+    float *op = static_cast<float *>(out.data_ptr());
+    const void *xp = x.data_ptr();
+    void *st = stream_for(nullptr, a, {0, 1, 2, 3, 4, 5, 6, 7});
+    call("q8_lora", [&] { return f_lora(op, os, base, bs, xp, xt, xs, &ad, ids, tok, st); });
+    return wrap(out);
+}
+
+// init(Q8Error, addresses of the twelve entry points)
+PyObject *init(PyObject *const *a, Py_ssize_t n) {
+    arity(n, 13);
     Py_INCREF(a[0]);
     g_error = a[0];
     f_page_bytes = reinterpret_cast<decltype(f_page_bytes)>(PyLong_AsVoidPtr(a[1]));
@@ -431,6 +614,9 @@ PyObject *init(PyObject *const *a, Py_ssize_t n) {
     f_free = reinterpret_cast<decltype(f_free)>(PyLong_AsVoidPtr(a[7]));
     f_compact = reinterpret_cast<decltype(f_compact)>(PyLong_AsVoidPtr(a[8]));
     f_copy = reinterpret_cast<decltype(f_copy)>(PyLong_AsVoidPtr(a[9]));
+    f_read = reinterpret_cast<decltype(f_read)>(PyLong_AsVoidPtr(a[10]));
+    f_residual = reinterpret_cast<decltype(f_residual)>(PyLong_AsVoidPtr(a[11]));
+    f_lora = reinterpret_cast<decltype(f_lora)>(PyLong_AsVoidPtr(a[12]));
     Py_RETURN_NONE;
 }
 
@@ -448,7 +634,8 @@ template <PyObject *(*F)(PyObject *const *, Py_ssize_t)> PyObject *guarded(PyObj
 #define Q8_METHOD(f) {#f, (PyCFunction)(void (*)(void))guarded<f>, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {Q8_METHOD(init),       Q8_METHOD(fill_cache), Q8_METHOD(kv_append), Q8_METHOD(attn_decode),
                          Q8_METHOD(attn_prompt), Q8_METHOD(kv_reserve), Q8_METHOD(kv_fork),   Q8_METHOD(kv_free),
-                         Q8_METHOD(kv_compact),  Q8_METHOD(kv_copy),    {nullptr, nullptr, 0, nullptr}};
+                         Q8_METHOD(kv_compact),  Q8_METHOD(kv_copy),    Q8_METHOD(kv_read),   Q8_METHOD(residual_norm),
+                         Q8_METHOD(lora),        {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_q8torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
