@@ -1635,7 +1635,10 @@ int q8_lora(float *out, uint64_t out_stride, const float *base, uint64_t base_st
     p.adapter_of = adapter_of;
     p.n_tok = (uint32_t)n_tok;
     p.err = s->err;
-    return status_of(q8::launch_lora(p, s->num_sms, static_cast<cudaStream_t>(stream)));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (p.n_tok <= q8::LORA_FEW) return status_of(q8::launch_lora(p, s->num_sms, st));
+    if ((rc = reserve_scratch(s, q8::lora_tc_scratch(p.n_tok, p.n_adapters, p.max_rank), st))) return rc;
+    return status_of(q8::launch_lora_tc(p, s->scratch.p, s->num_sms, st));
 }
 
 uint64_t q8_repack_bytes(uint64_t in_dim, uint64_t rows, int layout) {

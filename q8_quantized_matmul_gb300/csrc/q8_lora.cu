@@ -3,9 +3,7 @@
 // k_lora: a cluster of 8 CTAs takes up to T tokens of one adapter.  Each CTA multiplies A by its eighth of x, the
 // eighths are added through distributed shared memory in a fixed order, and each CTA then has its share of the outputs.
 // One launch and no memory between the two products; fp32 throughout (16-bit weights times fp32, fused multiply-adds).
-#include "q8_attn.cuh"
-#include "q8_kv.h"
-#include "q8_layer.h"
+#include "q8_lora.cuh"
 
 namespace q8 {
 namespace {
@@ -13,33 +11,6 @@ namespace {
 constexpr int LC = 8;            // CTAs of a cluster
 constexpr int LT = 256;          // threads of a CTA
 constexpr uint32_t XS = 1024;    // values of x that a CTA holds at a time
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ float ld_cluster(const float *p, uint32_t cta) {
-    uint32_t a;
-    float v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(cta));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-    return v;
-}
-
-__device__ __forceinline__ float value16(uint32_t bits, bool bf16) {
-    return bf16 ? __uint_as_float(bits << 16) : half_bits_to_float((uint16_t)bits);
-}
-__device__ __forceinline__ void values16(float (&v)[8], const uint4 &r, bool bf16) {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        v[2 * e] = value16(w[e] & 0xffffu, bf16);
-        v[2 * e + 1] = value16(w[e] >> 16, bf16);
-    }
-}
 
 // Values i .. i + 7 (i a multiple of 8) of a token's x.
 __device__ __forceinline__ void x8(float (&v)[8], const LoraParams &p, uint64_t tok, uint32_t i) {
@@ -94,11 +65,7 @@ template <int T> __global__ void __cluster_dims__(LC, 1, 1) __launch_bounds__(LT
         }
         if (lane == 0) n_mine = min(m, (uint32_t)T);
     }
-    int32_t rank = p.ranks ? p.ranks[id] : (int32_t)p.max_rank;
-    if (rank < 0 || rank > (int32_t)p.max_rank) {
-        if (t == 0) raise_error(p.err, DEV_ERANGE);
-        rank = rank < 0 ? 0 : (int32_t)p.max_rank;
-    }
+    const uint32_t rank = rank_of(p, id, t == 0);
     for (uint32_t i = t; i < T * LORA_MAX_RANK; i += LT) part[i / LORA_MAX_RANK][i % LORA_MAX_RANK] = 0.0f;
     __syncthreads();
     const uint32_t n = n_mine;
@@ -114,7 +81,7 @@ template <int T> __global__ void __cluster_dims__(LC, 1, 1) __launch_bounds__(LT
             *reinterpret_cast<float4 *>(&xs[1][m][c * 4]) = make_float4(v[4], v[5], v[6], v[7]);
         }
         __syncthreads();
-        for (uint32_t r = warp; r < (uint32_t)rank; r += LT / 32) {
+        for (uint32_t r = warp; r < rank; r += LT / 32) {
             const uint16_t *row = a + (uint64_t)r * p.in_dim + s0;
             float acc[T];
 #pragma unroll
@@ -150,13 +117,13 @@ template <int T> __global__ void __cluster_dims__(LC, 1, 1) __launch_bounds__(LT
     cluster_arrive();
     cluster_wait();
     const float scale = p.scales ? p.scales[id] : 1.0f;
-    const uint32_t ranks8 = ((uint32_t)rank + 7) & ~7u;
+    const uint32_t ranks8 = (rank + 7) & ~7u;
     for (uint32_t i = t; i < n * ranks8; i += LT) {
         const uint32_t m = i / ranks8, r = i - m * ranks8;
         float v = 0.0f;
-        if (r < (uint32_t)rank) {
+        if (r < rank) {
 #pragma unroll
-            for (uint32_t q = 0; q < LC; ++q) v += ld_cluster(&part[m][r], q);
+            for (uint32_t q = 0; q < LC; ++q) v += ld_cluster(cluster_addr(&part[m][r], q));
             v *= scale;
         }
         low[m][r] = v;
@@ -173,7 +140,7 @@ template <int T> __global__ void __cluster_dims__(LC, 1, 1) __launch_bounds__(LT
             float w[8];
             values16(w, __ldg(row + c), p.bf16);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = c * 8 + e < (uint32_t)rank ? w[e] : 0.0f;
+            for (int e = 0; e < 8; ++e) w[e] = c * 8 + e < rank ? w[e] : 0.0f;
 #pragma unroll
             for (int m = 0; m < T; ++m)
                 if (m < n) {
