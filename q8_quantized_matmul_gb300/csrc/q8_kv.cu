@@ -121,23 +121,21 @@ __global__ void __launch_bounds__(APPEND_THREADS) k_kv_append(const KvAppendPara
 // ---------------------------------------------------------------- reading back
 constexpr int READ_THREADS = 256;
 constexpr int READ_ROWS = 32;             // rows of a CTA
+constexpr int READ_AHEAD = 4;
 
-// Value chunk d0 .. d0 + 7 of a cached row, as fp32.
-__device__ __forceinline__ void cached8(float (&y)[8], const uint8_t *tile, uint32_t t, uint32_t d0, const KvPool &c) {
-    if (c.type == Q8_TYPE_Q8_0) {
-        const uint2 q = *reinterpret_cast<const uint2 *>(tile + (uint64_t)t * c.dim + d0);
-        const float d = half_bits_to_float(*reinterpret_cast<const uint16_t *>(
-            tile + ((uint64_t)c.dim << c.page_shift) + ((uint64_t)t * (c.dim / QK) + d0 / QK) * 2));
+// Eight cached values as they lie in a page (Q8_0: quants in x and y, and their scale), as fp32.
+__device__ __forceinline__ void cached8(float (&y)[8], const uint4 &v, uint16_t d, int type) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if (type == Q8_TYPE_Q8_0) {
+        const float s = half_bits_to_float(d);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = (float)(int8_t)((e < 4 ? q.x : q.y) >> (8 * (e & 3))) * d;
+        for (int e = 0; e < 8; ++e) y[e] = (float)(int8_t)(w[e / 4] >> (8 * (e & 3))) * s;
         return;
     }
-    const uint4 v = *reinterpret_cast<const uint4 *>(tile + ((uint64_t)t * c.dim + d0) * 2);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        y[2 * e] = c.type == Q8_TYPE_BF16 ? __uint_as_float(w[e] << 16) : half_bits_to_float((uint16_t)w[e]);
-        y[2 * e + 1] = c.type == Q8_TYPE_BF16 ? __uint_as_float(w[e] & 0xffff0000u) : half_bits_to_float((uint16_t)(w[e] >> 16));
+        y[2 * e] = type == Q8_TYPE_BF16 ? __uint_as_float(w[e] << 16) : half_bits_to_float((uint16_t)w[e]);
+        y[2 * e + 1] = type == Q8_TYPE_BF16 ? __uint_as_float(w[e] & 0xffff0000u) : half_bits_to_float((uint16_t)(w[e] >> 16));
     }
 }
 
@@ -184,21 +182,54 @@ __global__ void __launch_bounds__(READ_THREADS) k_kv_read(const KvReadParams p) 
     const uint8_t *pool = v ? p.c.v : p.c.k;
     void *out = v ? p.v_out : p.k_out;
     const uint64_t stride = v ? p.v_stride : p.k_stride;
-#pragma unroll 4
-    for (uint32_t i = threadIdx.x; i < items; i += READ_THREADS) {
-        const uint32_t r = i / per_row, c = i - r * per_row, h = c >> shift, d0 = (c & ((1u << shift) - 1u)) * 8;
-        const int2 a = at[r];
-        if (a.x == -2) continue;
-        const uint8_t *tile = pool + (uint64_t)max(a.x, 0) * p.c.page_stride + (uint64_t)h * p.c.tile_bytes;
-        if (p.c.type == p.out_type) {
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (a.x >= 0) w = *reinterpret_cast<const uint4 *>(tile + ((uint64_t)a.y * p.c.dim + d0) * 2);
-            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + (row0 + r) * stride + c * 8) = w;
-            continue;
+    const uint32_t dr = READ_THREADS / per_row, dc = READ_THREADS % per_row;
+    uint32_t r = threadIdx.x / per_row, c = threadIdx.x % per_row;
+    // READ_AHEAD loads in flight a thread
+    for (uint32_t i0 = threadIdx.x; i0 < items; i0 += READ_AHEAD * READ_THREADS) {
+        uint4 w[READ_AHEAD];
+        uint16_t d[READ_AHEAD];
+        uint32_t rs[READ_AHEAD], cs[READ_AHEAD];
+#pragma unroll
+        for (int j = 0; j < READ_AHEAD; ++j) {
+            rs[j] = r;
+            cs[j] = c;
+            w[j] = make_uint4(0, 0, 0, 0);
+            d[j] = 0;
+            if (i0 + j * READ_THREADS < items) {
+                const int2 a = at[r];
+                if (a.x >= 0) {
+                    const uint32_t h = c >> shift, d0 = (c & ((1u << shift) - 1u)) * 8;
+                    const uint8_t *tile = pool + (uint64_t)a.x * p.c.page_stride + (uint64_t)h * p.c.tile_bytes;
+                    if (p.c.type == Q8_TYPE_Q8_0) {
+                        const uint2 q = __ldcs(reinterpret_cast<const uint2 *>(tile + (uint64_t)a.y * p.c.dim + d0));
+                        w[j].x = q.x;
+                        w[j].y = q.y;
+                        d[j] = __ldg(reinterpret_cast<const uint16_t *>(tile + ((uint64_t)p.c.dim << p.c.page_shift) +
+                                                                        ((uint64_t)a.y * (p.c.dim / QK) + d0 / QK) * 2));
+                    } else {
+                        w[j] = __ldcs(reinterpret_cast<const uint4 *>(tile + ((uint64_t)a.y * p.c.dim + d0) * 2));
+                    }
+                }
+            }
+            r += dr;
+            c += dc;
+            if (c >= per_row) {
+                c -= per_row;
+                ++r;
+            }
         }
-        float y[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-        if (a.x >= 0) cached8(y, tile, a.y, d0, p.c);
-        store_out8(out, p.out_type, (row0 + r) * stride + c * 8, y, true);
+#pragma unroll
+        for (int j = 0; j < READ_AHEAD; ++j) {
+            if (i0 + j * READ_THREADS >= items || at[rs[j]].x == -2) continue;
+            const uint64_t to = (row0 + rs[j]) * stride + cs[j] * 8;
+            if (p.c.type == p.out_type) {
+                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + to) = w[j];
+                continue;
+            }
+            float y[8];
+            cached8(y, w[j], d[j], p.c.type);
+            store_out8(out, p.out_type, to, y, true);
+        }
     }
 }
 

@@ -19,6 +19,7 @@ struct ResidualNormParams {
     float residual_scale, eps;
     uint32_t dim;
     uint64_t n_tok;
+    bool whole;                           // fp32 rows start on 32-byte boundaries (set by the launcher)
 };
 constexpr uint32_t RESIDUAL_MAX_DIM = 32768;
 // h_type, y_type: Q8_TYPE_F32, F16 or BF16.

@@ -487,11 +487,19 @@ template <int NW> __global__ void __launch_bounds__(TT) k_lora_expand(const Lora
         if (t < count) toks[t] = p.perm[T.y + t];
         if (T.x == NO_ADAPTER) {
             __syncthreads();
-            const uint32_t o1 = min(p.out_dim, ch1 * OM);
-            for (uint32_t r = 0; r < count; ++r) {
-                const uint64_t tok = toks[r];
-                for (uint32_t o = ch0 * OM + t; o < o1; o += TT)
-                    p.out[tok * p.out_stride + o] = p.base ? p.base[tok * p.base_stride + o] : 0.0f;
+            const uint32_t o0 = ch0 * OM, wide = min(p.out_dim, ch1 * OM) - o0;
+            for (uint32_t i = t; i < count * wide; i += 8 * TT) {
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t j = i + e * TT;
+                    v[e] = p.base && j < count * wide ? p.base[(uint64_t)toks[j / wide] * p.base_stride + o0 + j % wide] : 0.0f;
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t j = i + e * TT;
+                    if (j < count * wide) p.out[(uint64_t)toks[j / wide] * p.out_stride + o0 + j % wide] = v[e];
+                }
             }
             continue;
         }
