@@ -1603,7 +1603,8 @@ int q8_lora(float *out, uint64_t out_stride, const float *base, uint64_t base_st
         return Q8_EINVAL;
     if (n_tok == 0 || ad.out_dim == 0) return Q8_OK;
     if (!out || !x || !ad.a || !ad.b || !adapter_of) return Q8_EINVAL;
-    if (out_stride < ad.out_dim || out_stride > most || (base && (base_stride < ad.out_dim || base_stride > most))) return Q8_EINVAL;
+    const uint64_t wide = ((uint64_t)1 << 30) - 1;   // rows of out and base are less than 4 GiB apart
+    if (out_stride < ad.out_dim || out_stride > wide || (base && (base_stride < ad.out_dim || base_stride > wide))) return Q8_EINVAL;
     if (out == base && out_stride != base_stride) return Q8_EINVAL;
     if (x_type == Q8_TYPE_Q8_0 ? x_stride != ad.in_dim : (x_stride < ad.in_dim || x_stride > most)) return Q8_EINVAL;
     if (!aligned16(out) || !aligned16(base) || !aligned16(x) || !aligned16(ad.a) || !aligned16(ad.b) || x_stride % 8 ||

@@ -126,6 +126,13 @@ template <int N> __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// Four int8 as fp32: 2^23 + (q + 128) is put together from its bytes (conversions run at a quarter of the rate).
+__device__ __forceinline__ void quants4(float (&v)[4], uint32_t q) {
+    q ^= 0x80808080u;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(__byte_perm(q, 0x4b000000u, 0x7440 + e)) - 8388736.0f;
+}
+
 __device__ __forceinline__ void load8s(float (&y)[8], const float *p) {
     const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
     y[0] = a.x; y[1] = a.y; y[2] = a.z; y[3] = a.w;

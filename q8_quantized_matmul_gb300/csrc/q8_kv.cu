@@ -129,7 +129,12 @@ __device__ __forceinline__ void cached8(float (&y)[8], const uint4 &v, uint16_t 
     if (type == Q8_TYPE_Q8_0) {
         const float s = half_bits_to_float(d);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = (float)(int8_t)(w[e / 4] >> (8 * (e & 3))) * s;
+        for (int h = 0; h < 2; ++h) {
+            float q[4];
+            quants4(q, w[h]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[4 * h + e] = q[e] * s;
+        }
         return;
     }
 #pragma unroll

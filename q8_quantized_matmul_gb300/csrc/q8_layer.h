@@ -47,6 +47,7 @@ struct LoraParams {
     int4 *tiles;
     uint32_t *perm;
     uint16_t *low;
+    uint32_t shrink_cluster;              // CTAs that share a tile of tokens (set by the launcher)
 };
 constexpr uint32_t LORA_MAX_RANK = 128, LORA_MAX_ADAPTERS = 16384;
 constexpr uint32_t LORA_FEW = 64;         // up to so many tokens take launch_lora

@@ -7,8 +7,8 @@
 //   k_lora_expand  tiles of 128 outputs (rows) by the tile's tokens (columns): a warp's lanes hold neighbouring outputs of one
 //                  token, so base and out are read and written in whole lines.
 //
-// fp32 accuracy from 16-bit products: an fp32 value is the exact sum of three bf16 terms (24 bits; each rounds what the ones
-// before left), an fp16 weight of two, and a product of two bf16 is exact in the fp32 accumulators.  Terms below 2^-24 of the
+// fp32 accuracy from 16-bit products: an fp32 value is the exact sum of three bf16 terms (8 of its 24 bits each), an fp16
+// weight of two, and a product of two bf16 is exact in the fp32 accumulators.  Terms below 2^-24 of the
 // product are left out.  The first terms' products and the rest are summed apart, for the tensor cores drop what is shifted
 // out of a sum.  bf16 x takes one term, fp16 x two (one and kind f16 with fp16 adapters).
 #include "q8_launch.h"
@@ -21,8 +21,8 @@ namespace {
 constexpr uint32_t TM = 128;              // tokens of a tile
 constexpr uint32_t KB = 64;               // values of a K step: a 128-byte row of 16-bit terms
 constexpr uint32_t PLANE = TM * 128;      // bytes of one term's 128 x 64 tile
-constexpr int SC = 8;                     // CTAs of a cluster of k_lora_shrink
-constexpr int TT = 256;
+constexpr uint32_t SC_MOST = 8;           // CTAs of a cluster of k_lora_shrink
+constexpr uint32_t SMEM_MOST = 225 * 1024;   // dynamic shared memory; the barriers and token lists come on top
 constexpr int NO_ADAPTER = -1;
 
 // ---------------------------------------------------------------- route
@@ -109,14 +109,14 @@ __global__ void __launch_bounds__(RT) k_lora_route(const LoraParams p) {
 }
 
 // ---------------------------------------------------------------- terms
-// Two fp32 values as N packed bf16 pairs that sum to them (each rounds what is left).
+// Two fp32 values as N packed bf16 pairs that sum to them: each takes the next 8 bits of what is left (three take all 24).
 template <int N> __device__ __forceinline__ void terms2(uint32_t (&t)[N], float a, float b) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        t[i] = pack16<true>(a, b);
+        t[i] = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
         if (i + 1 < N) {
-            a = __fsub_rn(a, __uint_as_float(t[i] << 16));
-            b = __fsub_rn(b, __uint_as_float(t[i] & 0xffff0000u));
+            a = __fsub_rn(a, __uint_as_float(__float_as_uint(a) & 0xffff0000u));
+            b = __fsub_rn(b, __uint_as_float(__float_as_uint(b) & 0xffff0000u));
         }
     }
 }
@@ -168,420 +168,624 @@ __device__ __forceinline__ void tmem_free(uint32_t tmem, uint32_t cols) {
 // ---------------------------------------------------------------- shrink
 enum XKind { X_F32, X_Q8, X_RAW, X_F16 };   // RAW: 16-bit values as they are; F16: split into two bf16 terms
 
-// What a thread holds of a K step of x: four values of each of 8 rows, or eight values of each of 4.
-template <int XK> struct XRegs {
-    static constexpr int ROWS = XK == X_F32 || XK == X_Q8 ? 8 : 4;
-    uint4 v[ROWS];
-};
-template <> struct XRegs<X_Q8> {
-    static constexpr int ROWS = 8;
-    uint32_t q[8];
-    uint16_t d[8];
-};
-
-template <int XK>
-__device__ __forceinline__ void load_x(XRegs<XK> &r, const LoraParams &p, const uint32_t (&tok)[XRegs<XK>::ROWS], uint32_t k0) {
-    constexpr bool FOUR = XRegs<XK>::ROWS == 8;
-    const uint32_t k = k0 + (FOUR ? threadIdx.x % 16 * 4 : threadIdx.x % 8 * 8);
-    const bool in = k < p.in_dim;
-#pragma unroll
-    for (int i = 0; i < XRegs<XK>::ROWS; ++i) {
-        const bool live = in && tok[i] != 0xffffffffu;
-        if constexpr (XK == X_Q8) {
-            r.q[i] = 0;
-            r.d[i] = 0;
-            if (live) {
-                const uint16_t *b = reinterpret_cast<const uint16_t *>(static_cast<const uint8_t *>(p.x) +
-                                                                       ((uint64_t)tok[i] * (p.in_dim / QK) + k / QK) * QB);
-                r.d[i] = __ldg(b);
-                r.q[i] = __ldg(b + 1 + k % QK / 2) | (uint32_t)__ldg(b + 2 + k % QK / 2) << 16;
-            }
-        } else {
-            r.v[i] = make_uint4(0, 0, 0, 0);
-            if (live)
-                r.v[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p.x) +
-                                                               ((uint64_t)tok[i] * p.x_stride + k) * (XK == X_F32 ? 4 : 2)));
-        }
-    }
-}
-
-template <int XK, int NX> __device__ __forceinline__ void store_x(uint8_t *tile, const XRegs<XK> &r) {
-    constexpr bool FOUR = XRegs<XK>::ROWS == 8;
-    const uint32_t t = threadIdx.x;
-#pragma unroll
-    for (int i = 0; i < XRegs<XK>::ROWS; ++i) {
-        if constexpr (FOUR) {
-            const uint32_t row = t / 16 + 16 * i, at = swizzled(row, t % 16 / 2) + t % 2 * 8;
-            float v[4];
-            if constexpr (XK == X_F32) {
-                v[0] = __uint_as_float(r.v[i].x);
-                v[1] = __uint_as_float(r.v[i].y);
-                v[2] = __uint_as_float(r.v[i].z);
-                v[3] = __uint_as_float(r.v[i].w);
-            } else {
-                const float d = half_bits_to_float(r.d[i]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = (float)(int8_t)(r.q[i] >> (8 * e)) * d;
-            }
-            uint32_t a[NX], b[NX];
-            terms2<NX>(a, v[0], v[1]);
-            terms2<NX>(b, v[2], v[3]);
-#pragma unroll
-            for (int j = 0; j < NX; ++j) *reinterpret_cast<uint2 *>(tile + j * PLANE + at) = make_uint2(a[j], b[j]);
-        } else {
-            const uint32_t row = t / 8 + 32 * i, at = swizzled(row, t % 8);
-            uint4 c[NX];
-            if constexpr (XK == X_F16) terms_f16<NX>(c, r.v[i]);
-            else c[0] = r.v[i];
-#pragma unroll
-            for (int j = 0; j < NX; ++j) *reinterpret_cast<uint4 *>(tile + j * PLANE + at) = c[j];
-        }
-    }
-}
-
-// The weights' rows of a K step, 8 values of rows t / 8, t / 8 + 32, ...
-struct WRegs {
-    uint4 v[LORA_MAX_RANK / 32];
-};
-__device__ __forceinline__ void load_w(WRegs &r, const LoraParams &p, const uint16_t *a, uint32_t rank, uint32_t k0) {
-    const uint32_t k = k0 + threadIdx.x % 8 * 8;
-#pragma unroll
-    for (uint32_t i = 0; i < LORA_MAX_RANK / 32; ++i) {
-        const uint32_t row = threadIdx.x / 8 + 32 * i;
-        r.v[i] = make_uint4(0, 0, 0, 0);
-        if (row < rank && k < p.in_dim) r.v[i] = __ldg(reinterpret_cast<const uint4 *>(a + (uint64_t)row * p.in_dim + k));
-    }
-}
-template <int NW> __device__ __forceinline__ void store_w(uint8_t *tile, uint32_t step, const WRegs &r, uint32_t rows) {
-#pragma unroll
-    for (uint32_t i = 0; i < LORA_MAX_RANK / 32; ++i) {
-        const uint32_t row = threadIdx.x / 8 + 32 * i;
-        if (row >= rows) continue;
-        uint4 c[NW];
-        if constexpr (NW == 2) terms_f16<NW>(c, r.v[i]);
-        else c[0] = r.v[i];
-#pragma unroll
-        for (int j = 0; j < NW; ++j) *reinterpret_cast<uint4 *>(tile + j * step + swizzled(row, threadIdx.x % 8)) = c[j];
-    }
-}
+// Warps 0-15 turn raw rows into terms, two groups of eight a K step in turn, and finish the tile; warps 16-19 copy raw rows into a ring, warp 20 issues the products.
+// The warps that fence their shared-memory writes for the tensor cores load nothing from global memory themselves: the fence
+// waits for a warp's outstanding loads (with the loads in registers, two steps ahead, a step took 2.4 us).
+constexpr int CONVERT = 512, GROUP = 256, COPY = 128, ST = CONVERT + COPY + 32;
+constexpr uint32_t MAX_RAW = 4;
 
 __host__ __device__ constexpr uint32_t round16(uint32_t r) { return (r + 15u) & ~15u; }
 
-template <int NX, int NW> __host__ __device__ constexpr uint32_t shrink_stage(uint32_t max_rank) {
-    return NX * PLANE + NW * round16(max_rank) * 128;
+template <int XK> constexpr uint32_t RAW_PITCH = XK == X_F32 ? 256 : XK == X_Q8 ? 80 : 128;   // bytes of a raw row of x
+struct ShrinkShape {
+    uint32_t stage, stages, raw, raws, body, smem;           // as many converting groups as stages
+};
+template <int XK, int NX, int NW> __host__ __device__ constexpr ShrinkShape shrink_shape(uint32_t max_rank) {
+    ShrinkShape s{};
+    const uint32_t cols = round16(max_rank), room = SMEM_MOST - 1024;
+    s.stage = NX * PLANE + NW * cols * 128;
+    s.raw = TM * RAW_PITCH<XK> + cols * 128;
+    s.stages = 2 * s.stage + 2 * s.raw <= room ? 2 : 1;
+    s.body = s.stages * s.stage;
+    const uint32_t part = TM * (cols + 4) * 4;               // the CTA's sums take the stages' place
+    if (s.body < part) s.body = part;
+    s.body = (s.body + 1023) & ~1023u;
+    s.raws = (room - s.body) / s.raw;
+    if (s.raws > MAX_RAW) s.raws = MAX_RAW;
+    if (s.stages == 2) s.raws &= ~1u;                        // a raw slot stays with one group, so none runs a phase of it ahead
+    s.smem = 1024 + s.body + s.raws * s.raw;
+    return s;
 }
-template <int NX, int NW> __host__ __device__ constexpr uint32_t shrink_smem(uint32_t max_rank) {
-    const uint32_t two = 2 * shrink_stage<NX, NW>(max_rank), part = TM * (round16(max_rank) + 4) * 4;
-    return 1024 + (two > part ? two : part);
+
+// `bytes` of 16 or 4 global -> shared, the rest zeros.
+__device__ __forceinline__ void cp_async16_part(uint32_t dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async4_part(uint32_t dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+// This thread's copies so far count as one arrival once they have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// An arrival at the same barrier of another CTA of the cluster, after all that this CTA's threads wrote before.
+__device__ __forceinline__ void arrive_at(uint64_t *bar, uint32_t cta) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr(bar, cta)) : "memory");
+}
+__device__ __forceinline__ bool cluster_bar_wait(uint64_t *bar, uint32_t parity, int *err, volatile int *abort) {
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t it = 0;; ++it) {
+        uint32_t ok;
+        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(ok)
+                     : "r"(smem_addr(bar)), "r"(parity)
+                     : "memory");
+        if (ok) return true;
+        if ((it & 255u) == 255u) {
+            if (*abort) return false;
+            if (global_timer_ns() - t0 > WAIT_LIMIT_NS) {
+                raise_error(err, DEV_ETIMEOUT);
+                *abort = 1;
+                return false;
+            }
+        }
+    }
+}
+
+// One K step of x and of the weights, as they lie in memory, by the copying warps (thread b of 128).
+template <int XK>
+__device__ __forceinline__ void copy_raw(const LoraParams &p, uint8_t *raw, const uint16_t *a, uint32_t rank, const uint32_t *toks, uint32_t count,
+                                         uint32_t k0, uint32_t b) {
+    const uint32_t x_dst = smem_addr(raw), w_dst = x_dst + TM * RAW_PITCH<XK>;
+    const uint32_t left = min(KB, p.in_dim - k0);            // 32 or 64 values
+    if constexpr (XK == X_Q8) {
+        constexpr uint32_t WORDS = 18;                       // 68 bytes from an even address: the words that hold them
+        const uint8_t *x = static_cast<const uint8_t *>(p.x);
+#pragma unroll 6
+        for (uint32_t i = b; i < count * WORDS; i += COPY) {
+            const uint32_t row = i / WORDS, w = i - row * WORDS;
+            const uint64_t s = ((uint64_t)toks[row] * (p.in_dim / QK) + k0 / QK) * QB, at = (s & ~(uint64_t)3) + 4 * w, end = s + left / QK * QB;
+            cp_async4_part(x_dst + row * RAW_PITCH<XK> + 4 * w, x + (at < end ? at : 0), at < end ? (uint32_t)min((uint64_t)4, end - at) : 0u);
+        }
+    } else {
+        constexpr uint32_t SIZE = XK == X_F32 ? 4 : 2, LANES = KB * SIZE / 16;   // threads of a row
+        const uint32_t c = b % LANES;
+        const bool in = c * 16 < left * SIZE;
+        const uint8_t *x = static_cast<const uint8_t *>(p.x) + ((uint64_t)k0 * SIZE + (in ? c * 16 : 0));
+#pragma unroll 8
+        for (uint32_t row = b / LANES; row < count; row += COPY / LANES)
+            cp_async16_part(x_dst + row * RAW_PITCH<XK> + c * 16, x + (uint64_t)toks[row] * p.x_stride * SIZE, in ? 16 : 0);
+    }
+    const uint32_t c = b % 8;
+    const bool in = c * 8 < left;
+#pragma unroll 4
+    for (uint32_t row = b / 8; row < rank; row += COPY / 8)
+        cp_async16_part(w_dst + row * 128 + c * 16, a + (uint64_t)row * p.in_dim + k0 + (in ? c * 8 : 0), in ? 16 : 0);
+}
+
+// A raw step as terms in a stage (thread t of a group's 256).
+template <int XK, int NX, int NW>
+__device__ __forceinline__ void convert(const LoraParams &p, uint8_t *stage, const uint8_t *raw, const uint32_t *toks, uint32_t k0, uint32_t cols,
+                                        uint32_t w_step, uint64_t *raw_empty, uint32_t t) {
+    constexpr uint32_t LANES = XK == X_F32 || XK == X_Q8 ? 16 : 8, ROWS = TM * LANES / GROUP, WROWS = LORA_MAX_RANK * 8 / GROUP;
+    const uint32_t c = t % LANES;
+    uint4 x[ROWS], w[WROWS];
+#pragma unroll
+    for (uint32_t i = 0; i < ROWS; ++i) {
+        const uint32_t row = t / LANES + i * (GROUP / LANES);
+        if constexpr (XK == X_Q8) {
+            // the row's copy starts on a word; its first block 0 or 2 bytes behind that
+            const uint32_t odd = ((uint32_t)(p.in_dim / QK) & toks[row] & 1u) * 2;
+            const uint16_t *blk = reinterpret_cast<const uint16_t *>(raw + row * RAW_PITCH<XK> + odd + (c >= 8 ? QB : 0));
+            const bool in = k0 + c * 4 < p.in_dim;
+            x[i].x = in ? blk[1 + c % 8 * 2] | (uint32_t)blk[2 + c % 8 * 2] << 16 : 0u;
+            x[i].y = in ? blk[0] : 0u;
+        } else {
+            x[i] = *reinterpret_cast<const uint4 *>(raw + row * RAW_PITCH<XK> + c * 16);
+        }
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < WROWS; ++i) {
+        const uint32_t row = t / 8 + i * (GROUP / 8);
+        if (row < cols) w[i] = *reinterpret_cast<const uint4 *>(raw + TM * RAW_PITCH<XK> + row * 128 + t % 8 * 16);
+    }
+    __syncwarp();
+    if (t % 32 == 0) mbar_arrive(raw_empty);
+#pragma unroll
+    for (uint32_t i = 0; i < ROWS; ++i) {
+        const uint32_t row = t / LANES + i * (GROUP / LANES);
+        if constexpr (LANES == 16) {
+            const uint32_t at = swizzled(row, c / 2) + c % 2 * 8;
+            float v[4] = {__uint_as_float(x[i].x), __uint_as_float(x[i].y), __uint_as_float(x[i].z), __uint_as_float(x[i].w)};
+            if constexpr (XK == X_Q8) {
+                quants4(v, x[i].x);
+                const float d = half_bits_to_float((uint16_t)x[i].y);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] *= d;
+            }
+            uint32_t lo[NX], hi[NX];
+            terms2<NX>(lo, v[0], v[1]);
+            terms2<NX>(hi, v[2], v[3]);
+#pragma unroll
+            for (int j = 0; j < NX; ++j) *reinterpret_cast<uint2 *>(stage + j * PLANE + at) = make_uint2(lo[j], hi[j]);
+        } else {
+            uint4 y[NX];
+            if constexpr (XK == X_F16) terms_f16<NX>(y, x[i]);
+            else y[0] = x[i];
+#pragma unroll
+            for (int j = 0; j < NX; ++j) *reinterpret_cast<uint4 *>(stage + j * PLANE + swizzled(row, c)) = y[j];
+        }
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < WROWS; ++i) {
+        const uint32_t row = t / 8 + i * (GROUP / 8);
+        if (row >= cols) continue;
+        uint4 y[NW];
+        if constexpr (NW == 2) terms_f16<NW>(y, w[i]);
+        else y[0] = w[i];
+#pragma unroll
+        for (int j = 0; j < NW; ++j) *reinterpret_cast<uint4 *>(stage + NX * PLANE + j * w_step + swizzled(row, t % 8)) = y[j];
+    }
 }
 
 template <int XK, int NX, int NW>
-__global__ void __cluster_dims__(SC, 1, 1) __launch_bounds__(TT) k_lora_shrink(const LoraParams p) {
+__global__ void __launch_bounds__(ST, 1) k_lora_shrink(const LoraParams p) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort_flag;
-    __shared__ uint64_t done[2];
+    __shared__ uint32_t toks[2][TM];
+    __shared__ uint64_t raw_full[MAX_RAW], raw_empty[MAX_RAW], st_full[2], st_empty[2], tok_full[2], tok_empty[2], d_full, parts_ready,
+        parts_read;
     uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-    const uint32_t t = threadIdx.x, warp = t >> 5, k = cluster_rank();
-    const uint32_t cols_max = round16(p.max_rank), w_step = cols_max * 128, stage = shrink_stage<NX, NW>(p.max_rank);
+    const ShrinkShape sh = shrink_shape<XK, NX, NW>(p.max_rank);
+    uint8_t *ring = smem + sh.body;
+    const uint32_t t = threadIdx.x, warp = t >> 5, lane = t & 31u, k = cluster_rank(), SC = p.shrink_cluster;
+    const uint32_t cols_max = round16(p.max_rank), w_step = cols_max * 128;
     const uint32_t tmem_cols = cols_max <= 16 ? 32 : cols_max <= 32 ? 64 : cols_max <= 64 ? 128 : 256, rest = tmem_cols / 2;
     if (t == 0) {
-        mbar_init(&done[0], 1);
-        mbar_init(&done[1], 1);
+        for (uint32_t i = 0; i < MAX_RAW; ++i) {
+            mbar_init(&raw_full[i], COPY);
+            mbar_init(&raw_empty[i], GROUP / 32);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&st_full[i], GROUP / 32);
+            mbar_init(&st_empty[i], 1);
+            mbar_init(&tok_full[i], 1);
+            mbar_init(&tok_empty[i], CONVERT / 32);
+        }
+        mbar_init(&d_full, 1);
+        mbar_init(&parts_ready, SC);
+        mbar_init(&parts_read, SC);
         abort_flag = 0;
         fence_mbar_init();
     }
+    cluster_arrive();   // every CTA's barriers are there
+    cluster_wait();
     grid_dep_wait();
-    if (warp == 0) tmem_alloc(&tmem_slot, tmem_cols);
+    if (warp == ST / 32 - 1) tmem_alloc(&tmem_slot, tmem_cols);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
-    const int n_tiles = p.tiles[0].x;
+    const int n_tiles = p.tiles[0].x, clusters = (int)(gridDim.x / SC);
     const uint32_t nb = (p.in_dim + KB - 1) / KB, kb0 = nb * k / SC, kb1 = nb * (k + 1) / SC;
-    uint32_t u = 0;                                          // K steps so far
-    for (int tile = blockIdx.x / SC; tile < n_tiles; tile += gridDim.x / SC) {
+    const auto wait = [&](uint64_t *bar, uint32_t parity) { return tile_wait(bar, parity, p.err, &abort_flag); };
+    uint32_t n = 0;                                          // K steps so far
+    int tiles = 0;                                           // tiles so far
+    for (int tile = (int)(blockIdx.x / SC); tile < n_tiles; tile += clusters) {
         const int4 T = p.tiles[1 + tile];
         if (T.x == NO_ADAPTER) continue;
-        const uint32_t count = T.z, rank = T.w, cols = round16(rank);
-        const uint16_t *a = p.a + (uint64_t)T.x * p.a_stride;
-        const uint32_t idesc = tc_idesc(TM, cols, !(XK == X_RAW && !p.bf16 && NW == 1));
-        uint32_t tok[XRegs<XK>::ROWS];
-#pragma unroll
-        for (int i = 0; i < XRegs<XK>::ROWS; ++i) {
-            const uint32_t row = XRegs<XK>::ROWS == 8 ? t / 16 + 16 * i : t / 8 + 32 * i;
-            tok[i] = row < count ? p.perm[T.y + row] : 0xffffffffu;
-        }
-        XRegs<XK> x;
-        WRegs w;
-        if (kb0 < kb1) {
-            load_x<XK>(x, p, tok, kb0 * KB);
-            load_w(w, p, a, rank, kb0 * KB);
-        }
-        for (uint32_t b = kb0; b < kb1; ++b, ++u) {
-            XRegs<XK> xn;
-            WRegs wn;
-            if (b + 1 < kb1) {
-                load_x<XK>(xn, p, tok, (b + 1) * KB);
-                load_w(wn, p, a, rank, (b + 1) * KB);
+        const uint32_t count = T.z, rank = T.w, cols = round16(rank), pitch = cols + 4;
+        uint32_t *tok = toks[tiles & 1];
+        if (warp >= CONVERT / 32 && warp < (CONVERT + COPY) / 32) {
+            // ------------------------------------------------ raw rows -> ring
+            const uint32_t b = t - CONVERT;
+            const uint16_t *a = p.a + (uint64_t)T.x * p.a_stride;
+            if (tiles >= 2) wait(&tok_empty[tiles & 1], (tiles / 2 - 1) & 1);
+            if (b < count) tok[b] = p.perm[T.y + b];
+            named_bar_sync(1, COPY);
+            if (b == 0) mbar_arrive(&tok_full[tiles & 1]);
+            for (uint32_t kb = kb0; kb < kb1; ++kb, ++n) {
+                const uint32_t r = n % sh.raws, use = n / sh.raws;
+                if (use) wait(&raw_empty[r], (use - 1) & 1);
+                copy_raw<XK>(p, ring + r * sh.raw, a, rank, tok, count, kb * KB, b);
+                cp_async_arrive(&raw_full[r]);
             }
-            uint8_t *s = smem + (u & 1) * stage;
-            if (u >= 2) tile_wait(&done[u & 1], (u / 2 - 1) & 1, p.err, &abort_flag);
-            store_x<XK, NX>(s, x);
-            store_w<NW>(s + NX * PLANE, w_step, w, cols);
-            fence_async_smem();
-            __syncthreads();
-            if (warp == 0 && elect_one()) {
+        } else if (warp == ST / 32 - 1) {
+            // ------------------------------------------------ products
+            const uint32_t idesc = tc_idesc(TM, cols, !(XK == X_RAW && !p.bf16 && NW == 1));
+            for (uint32_t kb = kb0; kb < kb1; ++kb, ++n) {
+                const uint32_t s = n % sh.stages;
+                wait(&st_full[s], (n / sh.stages) & 1);
                 tc_fence_after();
-                issue_terms<NX, NW, true>(tmem, rest, smem_addr(s), PLANE, smem_addr(s) + NX * PLANE, w_step, KB / 16, idesc, b != kb0, b != kb0);
-                tc_commit(&done[u & 1]);
+                if (elect_one()) {
+                    const uint32_t at = smem_addr(smem + s * sh.stage);
+                    issue_terms<NX, NW, true>(tmem, rest, at, PLANE, at + NX * PLANE, w_step, KB / 16, idesc, kb != kb0, kb != kb0);
+                    tc_commit(&st_empty[s]);
+                    if (kb + 1 == kb1) tc_commit(&d_full);
+                }
+                __syncwarp();
             }
-            if (b + 1 < kb1) {
-                x = xn;
-                w = wn;
+        } else {
+            // ------------------------------------------------ terms
+            wait(&tok_full[tiles & 1], (tiles / 2) & 1);
+            for (uint32_t kb = kb0; kb < kb1; ++kb, ++n) {
+                if (n % sh.stages != t / GROUP) continue;
+                const uint32_t r = n % sh.raws, s = n % sh.stages, use = n / sh.stages;
+                wait(&raw_full[r], (n / sh.raws) & 1);
+                if (use) wait(&st_empty[s], (use - 1) & 1);
+                convert<XK, NX, NW>(p, smem + s * sh.stage, ring + r * sh.raw, tok, kb * KB, cols, w_step, &raw_empty[r], t % GROUP);
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&st_full[s]);
             }
-        }
-        // this CTA's sums, one row a thread
-        float *part = reinterpret_cast<float *>(smem);
-        const uint32_t pitch = cols + 4;
-        if (kb0 < kb1) {
-            tile_wait(&done[(u - 1) & 1], ((u - 1) / 2) & 1, p.err, &abort_flag);
+            if (lane == 0) mbar_arrive(&tok_empty[tiles & 1]);
+            // this CTA's sums, one row a thread
+            float *part = reinterpret_cast<float *>(smem);
+            if (kb0 < kb1) wait(&d_full, tiles & 1);
+            tc_fence_after();
+            named_bar_sync(2, CONVERT);
+            const uint32_t row = (warp & 3) * 32 + lane;
+            for (uint32_t c = (warp >> 2) * 16; c < cols; c += 16 * (CONVERT / 128)) {
+                uint32_t d0[16], d1[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) d0[e] = d1[e] = 0;
+                if (kb0 < kb1) {
+                    const uint32_t at = tmem + ((warp & 3) << 21) + c;
+                    tc_ld16(at, d0);
+                    if constexpr (NX + NW > 2) tc_ld16(at + rest, d1);
+                    tc_wait_ld();
+                    tc_regs_ready(d0);
+                    tc_regs_ready(d1);
+                }
+#pragma unroll
+                for (int e = 0; e < 16; e += 4) {
+                    float4 v = make_float4(__uint_as_float(d0[e]), __uint_as_float(d0[e + 1]), __uint_as_float(d0[e + 2]), __uint_as_float(d0[e + 3]));
+                    if constexpr (NX + NW > 2) {
+                        v.x += __uint_as_float(d1[e]);
+                        v.y += __uint_as_float(d1[e + 1]);
+                        v.z += __uint_as_float(d1[e + 2]);
+                        v.w += __uint_as_float(d1[e + 3]);
+                    }
+                    *reinterpret_cast<float4 *>(part + row * pitch + c + e) = v;
+                }
+            }
+            tc_fence_before();
+            named_bar_sync(2, CONVERT);
+            if (t < SC) arrive_at(&parts_ready, t);
+            cluster_bar_wait(&parts_ready, tiles & 1, p.err, &abort_flag);
+            // an eighth of the rows: the parts in order, the scale, three terms
+            const float scale = p.scales ? p.scales[T.x] : 1.0f;
+            const uint32_t r0 = count * k / SC, r1 = count * (k + 1) / SC, quads = cols / 4;
+            for (uint32_t i = t; i < (r1 - r0) * quads; i += CONVERT) {
+                const uint32_t r = r0 + i / quads, c = i % quads * 4;
+                float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (uint32_t q = 0; q < SC_MOST; ++q) {
+                    if (q >= SC) break;
+                    const float4 f = ld_cluster4(cluster_addr(part + r * pitch + c, q));
+                    v[0] += f.x;
+                    v[1] += f.y;
+                    v[2] += f.z;
+                    v[3] += f.w;
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = c + e < rank ? v[e] * scale : 0.0f;
+                uint32_t lo[3], hi[3];
+                terms2<3>(lo, v[0], v[1]);
+                terms2<3>(hi, v[2], v[3]);
+                uint16_t *dst = p.low + (uint64_t)(T.y + r) * 3 * cols_max + c;
+#pragma unroll
+                for (int j = 0; j < 3; ++j) *reinterpret_cast<uint2 *>(dst + j * cols_max) = make_uint2(lo[j], hi[j]);
+            }
+            // the stages may be written over once every CTA has read
+            named_bar_sync(2, CONVERT);
+            if (t < SC) arrive_at(&parts_read, t);
+            cluster_bar_wait(&parts_read, tiles & 1, p.err, &abort_flag);
             tc_fence_after();
         }
-        __syncthreads();
-        const uint32_t row = (warp & 3) * 32 + (t & 31);
-        for (uint32_t c = (warp >> 2) * 16; c < cols; c += 32) {
-            uint32_t d0[16], d1[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) d0[e] = d1[e] = 0;
-            if (kb0 < kb1) {
-                const uint32_t at = tmem + ((warp & 3) << 21) + c;
-                tc_ld16(at, d0);
-                if constexpr (NX + NW > 2) tc_ld16(at + rest, d1);
-                tc_wait_ld();
-                tc_regs_ready(d0);
-                tc_regs_ready(d1);
-            }
-#pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-                float4 v = make_float4(__uint_as_float(d0[e]), __uint_as_float(d0[e + 1]), __uint_as_float(d0[e + 2]), __uint_as_float(d0[e + 3]));
-                if constexpr (NX + NW > 2) {
-                    v.x += __uint_as_float(d1[e]);
-                    v.y += __uint_as_float(d1[e + 1]);
-                    v.z += __uint_as_float(d1[e + 2]);
-                    v.w += __uint_as_float(d1[e + 3]);
-                }
-                *reinterpret_cast<float4 *>(part + row * pitch + c + e) = v;
-            }
-        }
-        tc_fence_before();
-        cluster_arrive();
-        cluster_wait();
-        tc_fence_after();
-        // an eighth of the rows: the parts in order, the scale, three terms
-        const float scale = p.scales ? p.scales[T.x] : 1.0f;
-        const uint32_t r0 = count * k / SC, r1 = count * (k + 1) / SC, quads = cols / 4;
-        for (uint32_t i = t; i < (r1 - r0) * quads; i += TT) {
-            const uint32_t r = r0 + i / quads, c = i % quads * 4;
-            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (uint32_t q = 0; q < SC; ++q) {
-                const float4 f = ld_cluster4(cluster_addr(part + r * pitch + c, q));
-                v[0] += f.x;
-                v[1] += f.y;
-                v[2] += f.z;
-                v[3] += f.w;
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = c + e < rank ? v[e] * scale : 0.0f;
-            uint32_t lo[3], hi[3];
-            terms2<3>(lo, v[0], v[1]);
-            terms2<3>(hi, v[2], v[3]);
-            uint16_t *dst = p.low + (uint64_t)(T.y + r) * 3 * cols_max + c;
-#pragma unroll
-            for (int j = 0; j < 3; ++j) *reinterpret_cast<uint2 *>(dst + j * cols_max) = make_uint2(lo[j], hi[j]);
-        }
-        cluster_arrive();   // parts may be written over once every CTA has read them
-        cluster_wait();
+        ++tiles;
     }
+    if (warp >= CONVERT / 32 && warp < (CONVERT + COPY) / 32) cp_async_wait<0>();   // nothing lands after the CTA has gone
+    tc_fence_before();
     __syncthreads();
-    if (warp == 0) tmem_free(tmem, tmem_cols);
+    if (warp == ST / 32 - 1) tmem_free(tmem, tmem_cols);
+    cluster_arrive();   // no CTA leaves while another may still read its sums, expired waits included
+    cluster_wait();
 }
 
 // ---------------------------------------------------------------- expand
+// base comes into a ring of slots of 32 tokens by 128 outputs (512-byte pieces of rows, asynchronous copies), the products are
+// added on the way out.  What is in flight does not depend on the registers of the warps that add.
+//   warps 0-15   four groups of four, slots in turn: slot + product -> out
+//   warps 16-17  base -> slots, in turn
+//   warp 18      products
+//   warps 19-22  B (and at a new tile the rank-sized sums) -> shared memory
 constexpr uint32_t OM = 128;              // outputs of a tile
+constexpr int E_GROUPS = 4, E_COPY0 = 4 * E_GROUPS, E_COPIES = 2, E_MMA = E_COPY0 + E_COPIES, E_B0 = E_MMA + 1, B_THREADS = 128, ET = E_B0 * 32 + B_THREADS;
+constexpr uint32_t SLOT_TOK = 32, SLOT = SLOT_TOK * OM * 4, MAX_SLOTS = 8;
 
 __host__ __device__ constexpr uint32_t kblocks(uint32_t max_rank) { return (round16(max_rank) + KB - 1) / KB; }
-template <int NW> __host__ __device__ constexpr uint32_t expand_smem(uint32_t max_rank) {
-    return 1024 + kblocks(max_rank) * PLANE * (3 + 2 * NW);
-}
-
-// Rows o0 .. o0 + 127 of B, 8 values (chunk t % 8 + 8 j) of rows t / 8 + 32 i.
-struct BRegs {
-    uint4 v[2][4];
+struct ExpandShape {
+    uint32_t kbs, b_stages, slots, smem;
 };
-__device__ __forceinline__ void load_b(BRegs &r, const LoraParams &p, const uint16_t *b, uint32_t rank, uint32_t o0) {
-#pragma unroll
-    for (uint32_t j = 0; j < 2; ++j) {
-        const uint32_t c = threadIdx.x % 8 + 8 * j;
-#pragma unroll
-        for (uint32_t i = 0; i < 4; ++i) {
-            const uint32_t o = o0 + threadIdx.x / 8 + 32 * i;
-            r.v[j][i] = make_uint4(0, 0, 0, 0);
-            if (c * 8 < rank && o < p.out_dim) r.v[j][i] = __ldg(reinterpret_cast<const uint4 *>(b + (uint64_t)o * p.max_rank + c * 8));
-        }
-    }
-}
-template <int NW> __device__ __forceinline__ void store_b(uint8_t *tile, uint32_t step, const BRegs &r, uint32_t rank) {
-#pragma unroll
-    for (uint32_t j = 0; j < 2; ++j) {
-        const uint32_t c = threadIdx.x % 8 + 8 * j;
-        if (c * 8 >= round16(rank)) continue;
-#pragma unroll
-        for (uint32_t i = 0; i < 4; ++i) {
-            uint4 v = r.v[j][i];
-            if (rank < c * 8 + 8) v = first_values(v, (int)rank - (int)c * 8);
-            uint4 x[NW];
-            if constexpr (NW == 2) terms_f16<NW>(x, v);
-            else x[0] = v;
-#pragma unroll
-            for (int e = 0; e < NW; ++e)
-                *reinterpret_cast<uint4 *>(tile + e * step + j * PLANE + swizzled(threadIdx.x / 8 + 32 * i, c % 8)) = x[e];
-        }
-    }
+template <int NW> __host__ __device__ constexpr ExpandShape expand_shape(uint32_t max_rank) {
+    ExpandShape s{};
+    s.kbs = kblocks(max_rank);
+    s.b_stages = NW * s.kbs > 2 ? 1 : 2;
+    const uint32_t fixed = 1024 + s.kbs * PLANE * (3 + NW * s.b_stages), room = SMEM_MOST - fixed;
+    // a multiple of the groups: a slot stays with one group and one copying warp, so none runs a phase of it ahead
+    s.slots = room / SLOT < MAX_SLOTS ? room / SLOT & ~3u : MAX_SLOTS;
+    s.smem = fixed + s.slots * SLOT;
+    return s;
 }
 
-template <int NW> __global__ void __launch_bounds__(TT) k_lora_expand(const LoraParams p) {
+// A CTA's share of the line of (tile, 128 outputs), one after another.
+struct Units {
+    uint64_t at, end;
+    uint32_t n_chunks, tile, chunk;
+    int4 T;                               // {adapter, first of perm, tokens, rank}
+    bool new_tile;
+    __device__ __forceinline__ Units(const LoraParams &p) {
+        n_chunks = (p.out_dim + OM - 1) / OM;
+        const uint64_t line = (uint64_t)p.tiles[0].x * n_chunks;
+        at = line * blockIdx.x / gridDim.x;
+        end = line * (blockIdx.x + 1) / gridDim.x;
+        if (at < end) first(p);
+    }
+    __device__ __forceinline__ void first(const LoraParams &p) {
+        tile = (uint32_t)(at / n_chunks);
+        chunk = (uint32_t)(at % n_chunks);
+        T = p.tiles[1 + tile];
+        new_tile = true;
+    }
+    __device__ __forceinline__ bool live() const { return at < end; }
+    __device__ __forceinline__ void next(const LoraParams &p) {
+        new_tile = false;
+        if (++at >= end) return;
+        if (++chunk == n_chunks) {
+            chunk = 0;
+            T = p.tiles[1 + ++tile];
+            new_tile = true;
+        }
+    }
+};
+
+// WHOLE: rows of base start on 16-byte boundaries and have whole 16 bytes.
+template <int NW, bool WHOLE> __global__ void __launch_bounds__(ET, 1) k_lora_expand(const LoraParams p) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort_flag;
-    __shared__ uint64_t done[2];
-    __shared__ uint32_t toks[TM];
+    __shared__ uint64_t full[MAX_SLOTS], empty[MAX_SLOTS], b_full[2], b_empty[2], d_full[2], d_empty[2];
     uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     const uint32_t t = threadIdx.x, warp = t >> 5, lane = t & 31u;
-    const uint32_t cols_max = round16(p.max_rank), kbs = kblocks(p.max_rank), step = kbs * PLANE;
-    uint8_t *bs = smem + 3 * step;                           // two stages of NW terms
+    const ExpandShape sh = expand_shape<NW>(p.max_rank);
+    const uint32_t cols_max = round16(p.max_rank), step = sh.kbs * PLANE;
+    uint8_t *bs = smem + 3 * step, *ring = bs + sh.b_stages * NW * step;
     if (t == 0) {
-        mbar_init(&done[0], 1);
-        mbar_init(&done[1], 1);
+        for (uint32_t i = 0; i < MAX_SLOTS; ++i) {
+            mbar_init(&full[i], 32);
+            mbar_init(&empty[i], 4);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&b_full[i], B_THREADS);
+            mbar_init(&b_empty[i], 1);
+            mbar_init(&d_full[i], 1);
+            mbar_init(&d_empty[i], 4 * E_GROUPS);
+        }
         abort_flag = 0;
         fence_mbar_init();
     }
     grid_dep_wait();
-    if (warp == 0) tmem_alloc(&tmem_slot, 2 * TM);
+    if (warp == E_MMA) tmem_alloc(&tmem_slot, 2 * TM);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
-    const uint32_t n_chunks = (p.out_dim + OM - 1) / OM;
-    const uint64_t line = (uint64_t)p.tiles[0].x * n_chunks;
-    uint64_t at = line * blockIdx.x / gridDim.x;
-    const uint64_t end = line * (blockIdx.x + 1) / gridDim.x;
-    uint32_t u = 0;                                          // chunks so far
-    while (at < end) {
-        const int4 T = p.tiles[1 + at / n_chunks];
-        const uint32_t ch0 = (uint32_t)(at % n_chunks), ch1 = (uint32_t)min((uint64_t)n_chunks, ch0 + (end - at));
-        at += ch1 - ch0;
-        const uint32_t count = T.z, rank = T.w;
-        __syncthreads();                                     // the last tile's tokens and terms are no longer read
-        if (t < count) toks[t] = p.perm[T.y + t];
-        if (T.x == NO_ADAPTER) {
-            __syncthreads();
-            const uint32_t o0 = ch0 * OM, wide = min(p.out_dim, ch1 * OM) - o0;
-            for (uint32_t i = t; i < count * wide; i += 8 * TT) {
-                float v[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const uint32_t j = i + e * TT;
-                    v[e] = p.base && j < count * wide ? p.base[(uint64_t)toks[j / wide] * p.base_stride + o0 + j % wide] : 0.0f;
+    const auto wait = [&](uint64_t *bar, uint32_t parity) { return tile_wait(bar, parity, p.err, &abort_flag); };
+    if (warp < E_COPY0) {
+        const uint32_t group = warp >> 2, q = warp & 3, col = q * 32 + lane, out_step = (uint32_t)p.out_stride * 4;
+        uint32_t n = 0, u = 0;                               // slots and products so far
+        for (Units w(p); w.live(); w.next(p)) {
+            const uint32_t count = w.T.z, o = w.chunk * OM + col;
+            const bool product = w.T.x != NO_ADAPTER;
+            const bool all = w.chunk * OM + OM <= p.out_dim;
+            uint8_t *const to = reinterpret_cast<uint8_t *>(p.out + o);
+            bool ready = !product;
+            for (uint32_t s0 = 0; s0 < count; s0 += SLOT_TOK, ++n) {
+                if (n % E_GROUPS != group) continue;
+                const uint32_t slot = n % sh.slots, rows = min(SLOT_TOK, count - s0);
+                const float *f = reinterpret_cast<const float *>(ring + slot * SLOT) + col;
+                const uint32_t tok = lane < rows ? p.perm[w.T.y + s0 + lane] : 0;
+                if (!ready) {
+                    wait(&d_full[u & 1], (u / 2) & 1);
+                    tc_fence_after();
+                    ready = true;
                 }
+                wait(&full[slot], (n / sh.slots) & 1);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const uint32_t j = i + e * TT;
-                    if (j < count * wide) p.out[(uint64_t)toks[j / wide] * p.out_stride + o0 + j % wide] = v[e];
+                for (uint32_t h = 0; h < SLOT_TOK; h += 16) {
+                    uint32_t d[16];
+                    float y[16];
+                    if (product) tc_ld16(tmem + (u & 1) * TM + (q << 21) + s0 + h, d);
+#pragma unroll
+                    for (uint32_t e = 0; e < 16; ++e) y[e] = p.base ? f[(h + e) * OM] : 0.0f;
+                    if (product) {
+                        tc_wait_ld();
+                        tc_regs_ready(d);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) y[e] += __uint_as_float(d[e]);
+                    }
+                    if (h) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&empty[slot]);
+                    }
+                    if (all && rows == SLOT_TOK) {
+#pragma unroll
+                        for (uint32_t e = 0; e < 16; ++e)
+                            *reinterpret_cast<float *>(to + (uint64_t)__shfl_sync(0xffffffffu, tok, h + e) * out_step) = y[e];
+                    } else {
+#pragma unroll
+                        for (uint32_t e = 0; e < 16; ++e) {
+                            const uint32_t row = __shfl_sync(0xffffffffu, tok, h + e);
+                            if (h + e < rows && o < p.out_dim) *reinterpret_cast<float *>(to + (uint64_t)row * out_step) = y[e];
+                        }
+                    }
                 }
             }
-            continue;
-        }
-        const uint16_t *b = p.b + (uint64_t)T.x * p.b_stride;
-        const uint32_t kr = round16(rank), cols = round16(count);
-        const uint32_t idesc = tc_idesc(OM, cols, true);
-        BRegs br;
-        load_b(br, p, b, rank, ch0 * OM);
-        for (uint32_t i = t; i < count * 3 * (kr / 8); i += TT) {
-            const uint32_t c = i % (kr / 8), rj = i / (kr / 8), j = rj % 3, r = rj / 3;
-            *reinterpret_cast<uint4 *>(smem + j * step + c / 8 * PLANE + swizzled(r, c % 8)) =
-                *reinterpret_cast<const uint4 *>(p.low + ((uint64_t)(T.y + r) * 3 + j) * cols_max + c * 8);
-        }
-        // after a stage's stores: one accumulator, for a rank's few steps drop no more than roundings would
-        const auto issue = [&](uint32_t v) {
-            fence_async_smem();
-            tc_fence_before();
-            __syncthreads();
-            if (warp == 0 && elect_one()) {
-                tc_fence_after();
-                for (uint32_t kb = 0; kb * KB < kr; ++kb)
-                    issue_terms<3, NW, false>(tmem + (v & 1) * TM, 0, smem_addr(smem) + kb * PLANE, step,
-                                              smem_addr(bs) + (v & 1) * NW * step + kb * PLANE, step, (int)(min(KB, kr - kb * KB) / 16), idesc,
-                                              kb != 0, true);
-                tc_commit(&done[v & 1]);
+            if (product) {
+                if (!ready) wait(&d_full[u & 1], (u / 2) & 1);   // a tile of few slots is the other groups' alone
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&d_empty[u & 1]);
+                ++u;
             }
-        };
-        store_b<NW>(bs + (u & 1) * NW * step, step, br, rank);
-        issue(u);
-        if (ch0 + 1 < ch1) load_b(br, p, b, rank, (ch0 + 1) * OM);
-        for (uint32_t ch = ch0; ch < ch1; ++ch, ++u) {
-            const uint32_t o = ch * OM + (warp & 3) * 32 + lane;
-            const bool live = o < p.out_dim;
-            const uint32_t c0 = (warp >> 2) * 16;
-            float base[16];
-            const auto load_base = [&](uint32_t c) {
+        }
+    } else if (warp < E_COPY0 + E_COPIES) {
+        uint32_t n = 0;
+        for (Units w(p); w.live(); w.next(p)) {
+            const uint32_t count = w.T.z, o0 = w.chunk * OM, width = min(OM, p.out_dim - o0);
+            for (uint32_t s0 = 0; s0 < count; s0 += SLOT_TOK, ++n) {
+                if (n % E_COPIES != warp - E_COPY0) continue;
+                const uint32_t slot = n % sh.slots, rows = min(SLOT_TOK, count - s0), uses = n / sh.slots;
+                const uint32_t tok = p.base && lane < rows ? p.perm[w.T.y + s0 + lane] : 0;
+                if (uses) wait(&empty[slot], (uses - 1) & 1);
+                if (p.base) {
+                    const uint32_t dst = smem_addr(ring + slot * SLOT);
+                    const float *base = p.base + o0;
+                    const uint32_t base_step = (uint32_t)p.base_stride * 4;
+#pragma unroll 8
+                    for (uint32_t e = 0; e < rows; ++e) {
+                        const float *src = reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(base) +
+                                                                           (uint64_t)__shfl_sync(0xffffffffu, tok, e) * base_step);
+                        if constexpr (WHOLE) {
+                            if (lane * 4 < width) cp_async16_part(dst + e * OM * 4 + lane * 16, src + lane * 4, 16);
+                        } else {
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    base[e] = live && p.base && c + e < count ? p.base[(uint64_t)toks[c + e] * p.base_stride + o] : 0.0f;
-            };
-            if (c0 < cols) load_base(c0);
-            tile_wait(&done[u & 1], (u / 2) & 1, p.err, &abort_flag);
+                            for (uint32_t c = lane; c < OM; c += 32)
+                                if (c < width) cp_async4_part(dst + e * OM * 4 + c * 4, src + c, 4);
+                        }
+                    }
+                }
+                cp_async_arrive(&full[slot]);
+            }
+        }
+        cp_async_wait<0>();                                  // nothing lands after the CTA has gone
+    } else if (warp == E_MMA) {
+        uint32_t u = 0;
+        for (Units w(p); w.live(); w.next(p)) {
+            if (w.T.x == NO_ADAPTER) continue;
+            const uint32_t kr = round16(w.T.w), st = u % sh.b_stages;
+            const uint32_t idesc = tc_idesc(OM, round16(w.T.z), true);
+            wait(&b_full[st], (u / sh.b_stages) & 1);
+            if (u >= 2) wait(&d_empty[u & 1], (u / 2 - 1) & 1);
             tc_fence_after();
-            if (ch + 1 < ch1) {
-                store_b<NW>(bs + ((u + 1) & 1) * NW * step, step, br, rank);
-                issue(u + 1);
-                if (ch + 2 < ch1) load_b(br, p, b, rank, (ch + 2) * OM);
+            if (elect_one()) {
+                for (uint32_t kb = 0; kb * KB < kr; ++kb)
+                    issue_terms<3, NW, false>(tmem + (u & 1) * TM, 0, smem_addr(smem) + kb * PLANE, step, smem_addr(bs) + st * NW * step + kb * PLANE,
+                                              step, (int)(min(KB, kr - kb * KB) / 16), idesc, kb != 0, true);
+                tc_commit(&b_empty[st]);
+                tc_commit(&d_full[u & 1]);
             }
-            for (uint32_t c = c0; c < cols; c += 32) {
-                uint32_t d[16];
-                tc_ld16(tmem + (u & 1) * TM + ((warp & 3) << 21) + c, d);
-                tc_wait_ld();
-                tc_regs_ready(d);
-                float y[16];
+            __syncwarp();
+            ++u;
+        }
+    } else {
+        const uint32_t b = t - E_B0 * 32;
+        uint32_t u = 0;
+        for (Units w(p); w.live(); w.next(p)) {
+            if (w.T.x == NO_ADAPTER) continue;
+            const uint32_t rank = w.T.w, kr = round16(rank), st = u % sh.b_stages, o0 = w.chunk * OM;
+            const uint16_t *wb = p.b + (uint64_t)w.T.x * p.b_stride;
+            uint4 v[8];
+            const auto load = [&](uint32_t c) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) y[e] = base[e] + __uint_as_float(d[e]);
-                if (c + 32 < cols) load_base(c + 32);
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    if (live && c + e < count) p.out[(uint64_t)toks[c + e] * p.out_stride + o] = y[e];
+                for (uint32_t i = 0; i < 8; ++i) {
+                    const uint32_t o = o0 + b / 8 + 16 * i;
+                    v[i] = make_uint4(0, 0, 0, 0);
+                    if (c * 8 < rank && o < p.out_dim) v[i] = __ldg(reinterpret_cast<const uint4 *>(wb + (uint64_t)o * p.max_rank + c * 8));
+                }
+            };
+            load(b % 8);
+            if (u >= sh.b_stages) wait(&b_empty[st], (u / sh.b_stages - 1) & 1);
+            if (w.new_tile || u == 0) {
+                // the sums of the tile before are read until its last product is done
+                if (u) wait(&b_empty[(u - 1) % sh.b_stages], ((u - 1) / sh.b_stages) & 1);
+                const uint32_t row_chunks = kr / 8;
+#pragma unroll 4
+                for (uint32_t i = b; i < (uint32_t)w.T.z * 3 * row_chunks; i += B_THREADS) {
+                    const uint32_t c = i % row_chunks, rj = i / row_chunks, j = rj % 3, r = rj / 3;
+                    *reinterpret_cast<uint4 *>(smem + j * step + c / 8 * PLANE + swizzled(r, c % 8)) =
+                        __ldg(reinterpret_cast<const uint4 *>(p.low + ((uint64_t)(w.T.y + r) * 3 + j) * cols_max + c * 8));
+                }
             }
+            for (uint32_t c = b % 8;; c += 8) {
+                if (c * 8 < kr) {
+#pragma unroll
+                    for (uint32_t i = 0; i < 8; ++i) {
+                        uint4 x[NW], y = v[i];
+                        if (rank < c * 8 + 8) y = first_values(y, (int)rank - (int)c * 8);
+                        if constexpr (NW == 2) terms_f16<NW>(x, y);
+                        else x[0] = y;
+#pragma unroll
+                        for (int e = 0; e < NW; ++e)
+                            *reinterpret_cast<uint4 *>(bs + (st * NW + e) * step + c / 8 * PLANE + swizzled(b / 8 + 16 * i, c % 8)) = x[e];
+                    }
+                }
+                if ((c + 8) / 8 * KB >= kr) break;
+                load(c + 8);
+            }
+            fence_async_smem();
+            mbar_arrive(&b_full[st]);
+            ++u;
         }
     }
+    tc_fence_before();
     __syncthreads();
-    if (warp == 0) tmem_free(tmem, 2 * TM);
+    if (warp == E_MMA) tmem_free(tmem, 2 * TM);
 }
 
 // ---------------------------------------------------------------- launchers
-template <int XK, int NX, int NW> cudaError_t launch_shrink(const LoraParams &p, unsigned clusters, cudaStream_t st) {
+template <int XK, int NX, int NW> cudaError_t launch_shrink(LoraParams p, unsigned tiles, int num_sms, cudaStream_t st) {
     static SmemAllowed allowed;
-    const cudaError_t e = allow_smem(allowed, reinterpret_cast<const void *>(k_lora_shrink<XK, NX, NW>), shrink_smem<NX, NW>(LORA_MAX_RANK));
+    cudaError_t e = allow_smem(allowed, reinterpret_cast<const void *>(k_lora_shrink<XK, NX, NW>), SMEM_MOST);
     if (e != cudaSuccess) return e;
-    return launch_dependent(k_lora_shrink<XK, NX, NW>, p, dim3(clusters * SC), TT, shrink_smem<NX, NW>(p.max_rank), st);
+    // Clusters that fit at a time are fewer than SMs / CTAs (15 of 8, 36 of 4 on 152 SMs): more tiles than clusters of 8
+    // take clusters of 4.
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(ST);
+    cfg.dynamicSmemBytes = shrink_shape<XK, NX, NW>(p.max_rank).smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    int fit = 0;
+    for (p.shrink_cluster = SC_MOST;; p.shrink_cluster /= 2) {
+        cfg.gridDim = dim3((unsigned)num_sms / p.shrink_cluster * p.shrink_cluster);
+        attr[1].val.clusterDim.x = p.shrink_cluster;
+        if ((e = cudaOccupancyMaxActiveClusters(&fit, k_lora_shrink<XK, NX, NW>, &cfg)) != cudaSuccess) return e;
+        if (fit < 1) fit = 1;
+        if (tiles <= (unsigned)fit || p.shrink_cluster == 4) break;
+    }
+    cfg.gridDim = dim3((tiles < (unsigned)fit ? tiles : (unsigned)fit) * p.shrink_cluster);
+    e = cudaLaunchKernelEx(&cfg, k_lora_shrink<XK, NX, NW>, (const LoraParams)p);
+    return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
-template <int NW> cudaError_t launch_expand(const LoraParams &p, int num_sms, cudaStream_t st) {
+template <int NW, bool WHOLE> cudaError_t launch_expand_rows(const LoraParams &p, int num_sms, cudaStream_t st) {
     static SmemAllowed allowed;
-    const cudaError_t e = allow_smem(allowed, reinterpret_cast<const void *>(k_lora_expand<NW>), expand_smem<NW>(LORA_MAX_RANK));
+    const cudaError_t e = allow_smem(allowed, reinterpret_cast<const void *>(k_lora_expand<NW, WHOLE>), SMEM_MOST);
     if (e != cudaSuccess) return e;
-    const uint32_t smem = expand_smem<NW>(p.max_rank);
-    const unsigned ctas = (unsigned)num_sms * (smem <= 112 * 1024 ? 2 : 1);
-    return launch_dependent(k_lora_expand<NW>, p, dim3(ctas), TT, smem, st);
+    return launch_dependent(k_lora_expand<NW, WHOLE>, p, dim3((unsigned)num_sms), ET, expand_shape<NW>(p.max_rank).smem, st);
+}
+template <int NW> cudaError_t launch_expand(const LoraParams &p, int num_sms, cudaStream_t st) {
+    const bool whole = p.out_dim % 4 == 0 && p.base_stride % 4 == 0;
+    return whole ? launch_expand_rows<NW, true>(p, num_sms, st) : launch_expand_rows<NW, false>(p, num_sms, st);
 }
 
 // The most tiles that a call can have.
@@ -609,14 +813,14 @@ cudaError_t launch_lora_tc(const LoraParams &q, void *scratch, int num_sms, cuda
     cudaError_t e = allow_smem(allowed, reinterpret_cast<const void *>(k_lora_route), (LORA_MAX_ADAPTERS + 1) * sizeof(int));
     if (e != cudaSuccess) return e;
     if ((e = launch_dependent(k_lora_route, p, dim3(1), RT, (p.n_adapters + 1) * sizeof(int), st)) != cudaSuccess) return e;
-    const uint64_t most = most_tiles(p.n_tok, p.n_adapters), room = (uint64_t)num_sms * 2 / SC;
-    const unsigned clusters = (unsigned)(most < room ? most : room);
+    const uint64_t most = most_tiles(p.n_tok, p.n_adapters);
+    const unsigned tiles = (unsigned)(most < 65536 ? most : 65536);
     const bool bf = p.bf16;
     switch (p.x_type) {
-        case Q8_TYPE_F32: e = bf ? launch_shrink<X_F32, 3, 1>(p, clusters, st) : launch_shrink<X_F32, 3, 2>(p, clusters, st); break;
-        case Q8_TYPE_Q8_0: e = bf ? launch_shrink<X_Q8, 3, 1>(p, clusters, st) : launch_shrink<X_Q8, 3, 2>(p, clusters, st); break;
-        case Q8_TYPE_BF16: e = bf ? launch_shrink<X_RAW, 1, 1>(p, clusters, st) : launch_shrink<X_RAW, 1, 2>(p, clusters, st); break;
-        default: e = bf ? launch_shrink<X_F16, 2, 1>(p, clusters, st) : launch_shrink<X_RAW, 1, 1>(p, clusters, st);
+        case Q8_TYPE_F32: e = bf ? launch_shrink<X_F32, 3, 1>(p, tiles, num_sms, st) : launch_shrink<X_F32, 3, 2>(p, tiles, num_sms, st); break;
+        case Q8_TYPE_Q8_0: e = bf ? launch_shrink<X_Q8, 3, 1>(p, tiles, num_sms, st) : launch_shrink<X_Q8, 3, 2>(p, tiles, num_sms, st); break;
+        case Q8_TYPE_BF16: e = bf ? launch_shrink<X_RAW, 1, 1>(p, tiles, num_sms, st) : launch_shrink<X_RAW, 1, 2>(p, tiles, num_sms, st); break;
+        default: e = bf ? launch_shrink<X_F16, 2, 1>(p, tiles, num_sms, st) : launch_shrink<X_RAW, 1, 1>(p, tiles, num_sms, st);
     }
     if (e != cudaSuccess) return e;
     return bf ? launch_expand<1>(p, num_sms, st) : launch_expand<2>(p, num_sms, st);

@@ -72,7 +72,8 @@ SIZES = [
     # tokens, in, out, rank, adapters
     (1, 32, 1, 8, 1), (1, 4096, 4096, 16, 3), (2, 1024, 300, 8, 2), (5, 96, 7, 24, 4), (9, 2080, 1025, 64, 3),
     (16, 1024, 4100, 32, 40), (33, 512, 64, 128, 5), (64, 256, 2048, 16, 64), (100, 992, 515, 40, 7), (129, 512, 384, 16, 2),
-    (257, 1024, 130, 64, 3), (300, 96, 2050, 8, 300), (700, 2048, 257, 128, 9), (1025, 320, 640, 48, 1)]
+    (257, 1024, 130, 64, 3), (300, 96, 2050, 8, 300), (700, 2048, 257, 128, 9), (1025, 320, 640, 48, 1), (300, 512, 388, 128, 3),
+    (200, 4096, 1000, 72, 2), (450, 256, 4108, 16, 2), (513, 64, 20, 64, 1)]
 
 
 @pytest.mark.parametrize("size", SIZES, ids=lambda s: "x".join(map(str, s)))
