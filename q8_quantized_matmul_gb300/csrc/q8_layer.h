@@ -42,16 +42,20 @@ struct LoraParams {
     uint32_t n_tok;
     int *err;
     uint32_t splits;                      // clusters that share a group's outputs (set by the launcher)
-    // many tokens: [0].x tiles, then {adapter (-1: none), first of perm, tokens, rank}; tokens by adapter; their scaled
-    // rank-sized sums as three bf16 terms [n_tok][3][max_rank rounded up to 16]
-    int4 *tiles;
+    // many tokens: [0] = {tiles, groups}, then tiles {adapter (-1: none), first of perm, tokens, rank}; groups of up to
+    // LORA_GROUP tokens alike; tokens by adapter; the tiles' scaled rank-sized sums as three bf16 terms
+    // [n_tok][3][max_rank rounded up to 16]
+    int4 *tiles, *groups;
     uint32_t *perm;
     uint16_t *low;
     uint32_t shrink_cluster;              // CTAs that share a tile of tokens (set by the launcher)
 };
 constexpr uint32_t LORA_MAX_RANK = 128, LORA_MAX_ADAPTERS = 16384;
 constexpr uint32_t LORA_FEW = 64;         // up to so many tokens take launch_lora
+constexpr uint32_t LORA_GROUP = 4;        // tokens of one adapter that k_lora multiplies by its weights at a time
+constexpr uint32_t LORA_TILE_MIN = 16;    // of more tokens: an adapter with fewer has no tile but groups
 cudaError_t launch_lora(const LoraParams &p, int num_sms, cudaStream_t st);
+cudaError_t launch_lora_groups(const LoraParams &p, int num_sms, cudaStream_t st);
 size_t lora_tc_scratch(uint32_t n_tok, uint32_t n_adapters, uint32_t max_rank);
 cudaError_t launch_lora_tc(const LoraParams &p, void *scratch, int num_sms, cudaStream_t st);
 

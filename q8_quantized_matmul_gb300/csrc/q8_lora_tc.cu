@@ -1,7 +1,8 @@
 // q8_lora_tc.cu -- low-rank adapters of many tokens on the tensor cores: out[t] = base[t] + s_a B_a (A_a x[t]).
 //
-//   k_lora_route   one CTA orders the tokens by adapter and cuts them into tiles of up to 128 tokens of one adapter.  The
-//                  order inside an adapter is left to chance: a token's result does not depend on its place in a tile.
+//   k_lora_route   one CTA orders the tokens by adapter and cuts them into tiles of up to 128 tokens of one adapter; adapters
+//                  with fewer than 16 tokens go to k_lora_groups (q8_lora.cu) instead.  The order inside an adapter is left to
+//                  chance: a token's result does not depend on its place in a tile or group.
 //   k_lora_shrink  a cluster of 8 CTAs a tile, each an eighth of in_dim: low = A x with the tokens along the rows of the
 //                  product.  The eighths are added through distributed shared memory in a fixed order.
 //   k_lora_expand  tiles of 128 outputs (rows) by the tile's tokens (columns): a warp's lanes hold neighbouring outputs of one
@@ -28,83 +29,112 @@ constexpr int NO_ADAPTER = -1;
 // ---------------------------------------------------------------- route
 constexpr int RT = 1024;
 
-// Inclusive sums of two values over the CTA; totals on every thread.
-__device__ __forceinline__ void scan2(int &a, int &b, int &ta, int &tb, int2 *warps) {
+struct Sums {
+    int tokens, tiles, groups;
+    __device__ __forceinline__ Sums operator+(const Sums &o) const { return {tokens + o.tokens, tiles + o.tiles, groups + o.groups}; }
+};
+__device__ __forceinline__ Sums shfl_up(const Sums &s, int o) {
+    return {__shfl_up_sync(0xffffffffu, s.tokens, o), __shfl_up_sync(0xffffffffu, s.tiles, o), __shfl_up_sync(0xffffffffu, s.groups, o)};
+}
+// Exclusive sums over the CTA; totals on every thread.
+__device__ __forceinline__ Sums scan(const Sums &mine, Sums &total, Sums *warps) {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    Sums s = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, b, o);
-        if (lane >= o) a += x, b += y;
+        const Sums v = shfl_up(s, o);
+        if (lane >= o) s = s + v;
     }
-    if (lane == 31) warps[w] = make_int2(a, b);
+    if (lane == 31) warps[w] = s;
     __syncthreads();
     if (w == 0) {
-        int2 v = warps[lane];
+        Sums v = warps[lane];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, v.x, o), y = __shfl_up_sync(0xffffffffu, v.y, o);
-            if (lane >= o) v.x += x, v.y += y;
+            const Sums x = shfl_up(v, o);
+            if (lane >= o) v = v + x;
         }
         warps[lane] = v;
     }
     __syncthreads();
-    if (w) a += warps[w - 1].x, b += warps[w - 1].y;
-    ta = warps[31].x;
-    tb = warps[31].y;
+    total = warps[31];
+    if (w) s = s + warps[w - 1];
+    return {s.tokens - mine.tokens, s.tiles - mine.tiles, s.groups - mine.groups};
 }
 
-// Bucket of token i: its adapter, n_adapters for none (-1: nothing to do for it either, base is out).
-__device__ __forceinline__ int bucket_of(const LoraParams &p, uint32_t i, bool tell) {
-    const int32_t id = p.adapter_of[i];
-    if (id >= 0 && (uint32_t)id < p.n_adapters && rank_of(p, id, tell) > 0) return id;
-    if (tell && id >= 0 && (uint32_t)id >= p.n_adapters) raise_error(p.err, DEV_ERANGE);
-    return p.base == p.out ? -1 : (int)p.n_adapters;
-}
+constexpr int AT_ONCE = 4;                // tokens of a thread whose ids are loaded together
 
 __global__ void __launch_bounds__(RT) k_lora_route(const LoraParams p) {
-    extern __shared__ int counts[];       // [n_adapters + 1]: tokens, then the next free place
-    __shared__ int2 warps[32];
+    extern __shared__ int counts[];       // [n_adapters + 1]: tokens (the last: of none), then the next free place
+    __shared__ Sums warps[RT / 32];
     const int n = (int)p.n_adapters + 1, lane = threadIdx.x & 31;
     for (int i = threadIdx.x; i < n; i += RT) counts[i] = 0;
     grid_dep_wait();
     __syncthreads();
-    const uint32_t rounds = (p.n_tok + RT - 1) / RT;
+    const uint32_t rounds = (p.n_tok + AT_ONCE * RT - 1) / (AT_ONCE * RT);
+    const auto buckets = [&](uint32_t round, int (&b)[AT_ONCE], bool tell) {
+#pragma unroll
+        for (int q = 0; q < AT_ONCE; ++q) {
+            const uint32_t i = (round * AT_ONCE + q) * RT + threadIdx.x;
+            b[q] = i < p.n_tok ? p.adapter_of[i] : -2;
+        }
+#pragma unroll
+        for (int q = 0; q < AT_ONCE; ++q) {
+            if (b[q] == -2 && (round * AT_ONCE + q) * RT + threadIdx.x >= p.n_tok) {
+                b[q] = -1;
+            } else if (b[q] < 0 || b[q] >= n - 1) {
+                if (tell && b[q] >= 0) raise_error(p.err, DEV_ERANGE);
+                b[q] = n - 1;
+            }
+        }
+    };
+    int b[AT_ONCE];
     for (uint32_t r = 0; r < rounds; ++r) {
-        const uint32_t i = r * RT + threadIdx.x;
-        const int b = i < p.n_tok ? bucket_of(p, i, true) : -1;
-        const unsigned same = __match_any_sync(0xffffffffu, b);
-        if (b >= 0 && lane == __ffs(same) - 1) atomicAdd(&counts[b], __popc(same));
+        buckets(r, b, true);
+#pragma unroll
+        for (int q = 0; q < AT_ONCE; ++q) {
+            const unsigned same = __match_any_sync(0xffffffffu, b[q]);
+            if (b[q] >= 0 && lane == __ffs(same) - 1) atomicAdd(&counts[b[q]], __popc(same));
+        }
     }
     __syncthreads();
+    // what becomes of an adapter's tokens: tiles, groups, or (no adapter, or one of rank 0) tiles that copy base
     const int per = (n + RT - 1) / RT, b0 = min(n, (int)threadIdx.x * per), b1 = min(n, b0 + per);
-    int tokens = 0, tiles = 0, all, n_tiles;
-    for (int b = b0; b < b1; ++b) {
-        tokens += counts[b];
-        tiles += (counts[b] + (int)TM - 1) / (int)TM;
+    const auto kind = [&](int i, int c, int &rank) -> Sums {
+        rank = c && i < n - 1 ? (int)rank_of(p, i, false) : 0;
+        if (rank == 0) return {c, p.base == p.out ? 0 : (c + (int)TM - 1) / (int)TM, 0};
+        if (c < (int)LORA_TILE_MIN) return {c, 0, (c + (int)LORA_GROUP - 1) / (int)LORA_GROUP};
+        return {c, (c + (int)TM - 1) / (int)TM, 0};
+    };
+    Sums mine = {0, 0, 0}, total;
+    int rank;
+    for (int i = b0; i < b1; ++i) {
+        if (counts[i] && i < n - 1) rank_of(p, i, true);
+        mine = mine + kind(i, counts[i], rank);
     }
-    int t = tokens, k = tiles;
-    scan2(t, k, all, n_tiles, warps);
-    t -= tokens;
-    k -= tiles;
-    for (int b = b0; b < b1; ++b) {
-        const int c = counts[b];
-        counts[b] = t;
-        const bool bare = b == (int)p.n_adapters;
-        const int rank = bare || c == 0 ? 0 : (int)rank_of(p, b, false);
-        for (int at = 0; at < c; at += TM, ++k)
-            p.tiles[1 + k] = make_int4(bare ? NO_ADAPTER : b, t + at, min((int)TM, c - at), rank);
-        t += c;
+    Sums at = scan(mine, total, warps);
+    for (int i = b0; i < b1; ++i) {
+        const int c = counts[i];
+        const Sums k = kind(i, c, rank);
+        counts[i] = at.tokens;
+        for (int j = 0; j < k.tiles; ++j)
+            p.tiles[1 + at.tiles + j] = make_int4(rank ? i : NO_ADAPTER, at.tokens + j * (int)TM, min((int)TM, c - j * (int)TM), rank);
+        for (int j = 0; j < k.groups; ++j)
+            p.groups[at.groups + j] = make_int4(i, at.tokens + j * (int)LORA_GROUP, min((int)LORA_GROUP, c - j * (int)LORA_GROUP), rank);
+        at = at + k;
     }
-    if (threadIdx.x == 0) p.tiles[0] = make_int4(n_tiles, 0, 0, 0);
+    if (threadIdx.x == 0) p.tiles[0] = make_int4(total.tiles, total.groups, 0, 0);
     __syncthreads();
     for (uint32_t r = 0; r < rounds; ++r) {
-        const uint32_t i = r * RT + threadIdx.x;
-        const int b = i < p.n_tok ? bucket_of(p, i, false) : -1;
-        const unsigned same = __match_any_sync(0xffffffffu, b);
-        int at = 0;
-        if (b >= 0 && lane == __ffs(same) - 1) at = atomicAdd(&counts[b], __popc(same));
-        at = __shfl_sync(0xffffffffu, at, __ffs(same) - 1) + __popc(same & ((1u << lane) - 1u));
-        if (b >= 0) p.perm[at] = i;
+        if (rounds > 1) buckets(r, b, false);
+#pragma unroll
+        for (int q = 0; q < AT_ONCE; ++q) {
+            const unsigned same = __match_any_sync(0xffffffffu, b[q]);
+            int place = 0;
+            if (b[q] >= 0 && lane == __ffs(same) - 1) place = atomicAdd(&counts[b[q]], __popc(same));
+            place = __shfl_sync(0xffffffffu, place, __ffs(same) - 1) + __popc(same & ((1u << lane) - 1u));
+            if (b[q] >= 0) p.perm[place] = (r * AT_ONCE + q) * RT + threadIdx.x;
+        }
     }
 }
 
@@ -792,12 +822,17 @@ template <int NW> cudaError_t launch_expand(const LoraParams &p, int num_sms, cu
 uint64_t most_tiles(uint64_t n_tok, uint64_t n_adapters) {
     return n_tok / TM + (n_tok < n_adapters + 1 ? n_tok : n_adapters + 1);
 }
+uint64_t most_groups(uint64_t n_tok, uint64_t n_adapters) {
+    const uint64_t few = n_adapters * ((LORA_TILE_MIN + LORA_GROUP - 2) / LORA_GROUP);
+    return n_tok < few ? n_tok : few;
+}
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
+size_t list_bytes(const uint64_t n) { return up256(n * sizeof(int4)); }
 
 }  // namespace
 
 size_t lora_tc_scratch(uint32_t n_tok, uint32_t n_adapters, uint32_t max_rank) {
-    return up256((1 + most_tiles(n_tok, n_adapters)) * sizeof(int4)) + up256((size_t)n_tok * 4) +
+    return list_bytes(1 + most_tiles(n_tok, n_adapters)) + list_bytes(most_groups(n_tok, n_adapters)) + up256((size_t)n_tok * 4) +
            (size_t)n_tok * 3 * round16(max_rank) * 2;
 }
 
@@ -805,7 +840,9 @@ cudaError_t launch_lora_tc(const LoraParams &q, void *scratch, int num_sms, cuda
     LoraParams p = q;
     uint8_t *at = static_cast<uint8_t *>(scratch);
     p.tiles = reinterpret_cast<int4 *>(at);
-    at += up256((1 + most_tiles(p.n_tok, p.n_adapters)) * sizeof(int4));
+    at += list_bytes(1 + most_tiles(p.n_tok, p.n_adapters));
+    p.groups = reinterpret_cast<int4 *>(at);
+    at += list_bytes(most_groups(p.n_tok, p.n_adapters));
     p.perm = reinterpret_cast<uint32_t *>(at);
     at += up256((size_t)p.n_tok * 4);
     p.low = reinterpret_cast<uint16_t *>(at);
@@ -813,6 +850,7 @@ cudaError_t launch_lora_tc(const LoraParams &q, void *scratch, int num_sms, cuda
     cudaError_t e = allow_smem(allowed, reinterpret_cast<const void *>(k_lora_route), (LORA_MAX_ADAPTERS + 1) * sizeof(int));
     if (e != cudaSuccess) return e;
     if ((e = launch_dependent(k_lora_route, p, dim3(1), RT, (p.n_adapters + 1) * sizeof(int), st)) != cudaSuccess) return e;
+    if ((e = launch_lora_groups(p, num_sms, st)) != cudaSuccess) return e;
     const uint64_t most = most_tiles(p.n_tok, p.n_adapters);
     const unsigned tiles = (unsigned)(most < 65536 ? most : 65536);
     const bool bf = p.bf16;
