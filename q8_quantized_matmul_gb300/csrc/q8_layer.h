@@ -51,7 +51,11 @@ struct LoraParams {
     uint32_t shrink_cluster;              // CTAs that share a tile of tokens (set by the launcher)
 };
 constexpr uint32_t LORA_MAX_RANK = 128, LORA_MAX_ADAPTERS = 16384;
-constexpr uint32_t LORA_FEW = 64;         // up to so many tokens take launch_lora
+// Few tokens take launch_lora, which searches the tokens of an adapter anew in every CTA and reads the weights again for each
+// four of them, but is one launch.  launch_lora / launch_lora_tc, us, 4096 to 4096:
+//   rank 16   64 tokens: 64 adapters 6.9 / 18, one 8.2 / 25; 128: 14.6 / 29, 15.7 / 27; 192: 24 / 41, 24 / 28
+//   rank 64   64 tokens: 64 adapters 23 / 42, one 21 / 27;   96: 43 / 48, 33 / 29
+inline bool lora_few(uint64_t n_tok, uint32_t max_rank) { return n_tok <= 64 || (n_tok <= 128 && n_tok * max_rank <= 2048); }
 constexpr uint32_t LORA_GROUP = 4;        // tokens of one adapter that k_lora multiplies by its weights at a time
 constexpr uint32_t LORA_TILE_MIN = 16;    // of more tokens: an adapter with fewer has no tile but groups
 cudaError_t launch_lora(const LoraParams &p, int num_sms, cudaStream_t st);

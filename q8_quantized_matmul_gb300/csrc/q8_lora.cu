@@ -169,9 +169,18 @@ __device__ __forceinline__ void group_share(const LoraParams &p, Shared &sh, int
     cluster_wait();
 }
 
+// A lone token takes more rows and outputs at a time.
+template <int T>
+__device__ __forceinline__ void share_of(const LoraParams &p, Shared &sh, int32_t id, uint32_t rank, uint32_t n, const uint32_t (&mine)[T],
+                                         uint32_t share, uint32_t shares, uint32_t k) {
+    const uint32_t first[1] = {mine[0]};
+    if (T == 1) group_share<1, 4, 2>(p, sh, id, rank, 1, first, share, shares, k);
+    else if (n == 1) group_share<1, 4, 4>(p, sh, id, rank, 1, first, share, shares, k);
+    else group_share<T, 2, 2>(p, sh, id, rank, n, mine, share, shares, k);
+}
+
 // A cluster (p.splits of them) a token: those of a group's tokens share its outputs.
-template <int T, int RR, int U>
-__global__ void __cluster_dims__(LC, 1, 1) __launch_bounds__(LT, 3) k_lora(const LoraParams p) {
+template <int T> __global__ void __cluster_dims__(LC, 1, 1) __launch_bounds__(LT, 4) k_lora(const LoraParams p) {
     __shared__ __align__(16) Shared sh;
     const uint32_t t = threadIdx.x, lane = t & 31u, warp = t >> 5, k = cluster_rank();
     const uint32_t cluster = blockIdx.x / LC, j = cluster / p.splits, split = cluster - j * p.splits;
@@ -215,11 +224,11 @@ __global__ void __cluster_dims__(LC, 1, 1) __launch_bounds__(LT, 3) k_lora(const
 #pragma unroll
         for (int m = 0; m < T; ++m) mine[m] = m < n ? sh.tok[m] : 0;
     }
-    group_share<T, RR, U>(p, sh, id, rank, n, mine, split * n + pos, p.splits * n, k);
+    share_of<T>(p, sh, id, rank, n, mine, split * n + pos, p.splits * n, k);
 }
 
 // The groups of the list that k_lora_route made: adapters with too few tokens for a tile.
-__global__ void __cluster_dims__(LC, 1, 1) __launch_bounds__(LT, 3) k_lora_groups(const LoraParams p) {
+__global__ void __cluster_dims__(LC, 1, 1) __launch_bounds__(LT, 4) k_lora_groups(const LoraParams p) {
     __shared__ __align__(16) Shared sh;
     const uint32_t k = cluster_rank(), cluster = blockIdx.x / LC, clusters = gridDim.x / LC;
     grid_dep_wait();
@@ -232,7 +241,7 @@ __global__ void __cluster_dims__(LC, 1, 1) __launch_bounds__(LT, 3) k_lora_group
         uint32_t mine[LORA_GROUP];
 #pragma unroll
         for (int m = 0; m < (int)LORA_GROUP; ++m) mine[m] = m < g.z ? p.perm[g.y + m] : 0;
-        group_share<LORA_GROUP, 2, 2>(p, sh, g.x, (uint32_t)g.w, (uint32_t)g.z, mine, i % shares, shares, k);
+        share_of<LORA_GROUP>(p, sh, g.x, (uint32_t)g.w, (uint32_t)g.z, mine, i % shares, shares, k);
         __syncthreads();
     }
 }
@@ -241,16 +250,18 @@ __global__ void __cluster_dims__(LC, 1, 1) __launch_bounds__(LT, 3) k_lora_group
 
 cudaError_t launch_lora(const LoraParams &q, int num_sms, cudaStream_t st) {
     LoraParams p = q;
-    // as many clusters a group as fill the SMs with four CTAs each, of at least a thread an output
-    const uint32_t most = (p.out_dim + LT * LC - 1) / (LT * LC), want = (uint32_t)(4 * num_sms) / (p.n_tok * LC);
-    p.splits = want < 1 ? 1 : want > most ? most : want;
+    // As many clusters a token as give each SM two CTAs, of at least a thread an output.  Four fit on an SM; what does not
+    // fit at once costs a whole chain more (64 adapters of one token, 4096 to 4096, rank 16: 6.9 us, 10.5 with room for
+    // three), and more clusters repeat the product with A (8 tokens, 1024 to 32768: 5.0 us with two an SM, 5.9 with four).
+    const uint32_t most = (p.out_dim + LT * LC - 1) / (LT * LC), want = ((uint32_t)(2 * num_sms) + p.n_tok * LC - 1) / (p.n_tok * LC);
+    p.splits = want > most ? most : want;
     const dim3 grid((unsigned)((uint64_t)LC * p.splits * p.n_tok));
-    if (p.n_tok == 1) return launch_dependent(k_lora<1, 4, 4>, p, grid, LT, 0, st);
-    return launch_dependent(k_lora<LORA_GROUP, 2, 2>, p, grid, LT, 0, st);
+    if (p.n_tok == 1) return launch_dependent(k_lora<1>, p, grid, LT, 0, st);
+    return launch_dependent(k_lora<LORA_GROUP>, p, grid, LT, 0, st);
 }
 
 cudaError_t launch_lora_groups(const LoraParams &p, int num_sms, cudaStream_t st) {
-    const unsigned fit = (unsigned)num_sms * 3 / LC;
+    const unsigned fit = (unsigned)num_sms * 4 / LC;
     return launch_dependent(k_lora_groups, p, dim3(fit * LC), LT, 0, st);
 }
 
