@@ -120,100 +120,137 @@ __global__ void __launch_bounds__(APPEND_THREADS) k_kv_append(const KvAppendPara
 
 // ---------------------------------------------------------------- reading back
 constexpr int READ_THREADS = 256;
-constexpr int READ_ROWS = 32;             // rows of a CTA
-constexpr int READ_AHEAD = 4;
+constexpr int READ_ROWS = 64;             // most rows of a CTA
+constexpr int READ_STARTS = 1024;         // starts that a CTA keeps
+constexpr int READ_AHEAD = 4;             // loads in flight a thread
 
-// Eight cached values as they lie in a page (Q8_0: quants in x and y, and their scale), as fp32.
-__device__ __forceinline__ void cached8(float (&y)[8], const uint4 &v, uint16_t d, int type) {
+// 32 bytes at once where the rows start on such boundaries, else 16 at a time.
+__device__ __forceinline__ void store32(void *to, const uint32_t (&w)[8], bool whole) {
+    if (whole) {
+        asm volatile("st.global.v8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]),
+                     "r"(w[6]), "r"(w[7]), "l"(to)
+                     : "memory");
+    } else {
+        static_cast<uint4 *>(to)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        static_cast<uint4 *>(to)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
+// Values of a row, N of them (16 of Q8_0 with their scale, else 8), stored in out_type; i0: the place of the first.
+template <bool Q8> __device__ __forceinline__ void store_cached(void *out, int out_type, int type, uint64_t i0, const uint4 &v, uint16_t d, bool whole) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    if (type == Q8_TYPE_Q8_0) {
+    if constexpr (Q8) {
         const float s = half_bits_to_float(d);
+        float y[16];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < 4; ++h) {
             float q[4];
             quants4(q, w[h]);
 #pragma unroll
             for (int e = 0; e < 4; ++e) y[4 * h + e] = q[e] * s;
         }
-        return;
-    }
+        uint32_t o[8];
+        if (out_type == Q8_TYPE_F32) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        y[2 * e] = type == Q8_TYPE_BF16 ? __uint_as_float(w[e] << 16) : half_bits_to_float((uint16_t)w[e]);
-        y[2 * e + 1] = type == Q8_TYPE_BF16 ? __uint_as_float(w[e] & 0xffff0000u) : half_bits_to_float((uint16_t)(w[e] >> 16));
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(y[8 * h + e]);
+                store32(static_cast<float *>(out) + i0 + 8 * h, o, whole);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = out_type == Q8_TYPE_BF16 ? pack16<true>(y[2 * e], y[2 * e + 1]) : pack16<false>(y[2 * e], y[2 * e + 1]);
+            store32(static_cast<uint16_t *>(out) + i0, o, whole);
+        }
+    } else if (type == out_type) {
+        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + i0) = v;
+    } else {
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            y[2 * e] = type == Q8_TYPE_BF16 ? __uint_as_float(w[e] << 16) : half_bits_to_float((uint16_t)w[e]);
+            y[2 * e + 1] = type == Q8_TYPE_BF16 ? __uint_as_float(w[e] & 0xffff0000u) : half_bits_to_float((uint16_t)(w[e] >> 16));
+        }
+        store_out8(out, out_type, i0, y, true);
     }
 }
 
-// Rows [32 blockIdx.x, ...) of K (blockIdx.y 0) or V: where each lies is looked up once, then one thread per 8 values.
-__global__ void __launch_bounds__(READ_THREADS) k_kv_read(const KvReadParams p) {
-    __shared__ int2 at[READ_ROWS];        // page (-1: none, the row is zeros; -2: no row), row in the page
+// Rows [rows_cta blockIdx.x, ...) of K (blockIdx.y 0) or V: where each lies is looked up once, then a thread takes 16 bytes of a
+// page at a time.
+template <bool Q8> __global__ void __launch_bounds__(READ_THREADS) k_kv_read(const KvReadParams p) {
+    __shared__ int64_t at[READ_ROWS];     // the row's first byte in head 0's tile from the pool's start (-1: none, zeros; -2: no row)
+    __shared__ int row_of[READ_ROWS];     // its row in the page
+    __shared__ int32_t starts[READ_STARTS];
     grid_dep_wait();
-    const bool v = blockIdx.y == (p.k_out ? 1u : 0u);
+    const bool v = blockIdx.y == (p.k_out ? 1u : 0u), kept = p.n_seq < READ_STARTS;
+    if (kept)
+        for (uint32_t s = threadIdx.x; s <= p.n_seq; s += READ_THREADS) starts[s] = p.k_start[s];
+    __syncthreads();
+    const int32_t *start = kept ? starts : p.k_start;
     if (blockIdx.x == 0 && blockIdx.y == 0) {
         bool bad = false;
         for (uint32_t s = threadIdx.x; s <= p.n_seq; s += READ_THREADS) {
-            const int32_t k = p.k_start[s];
-            bad |= k < 0 || (uint32_t)k > p.n_k || (s && k < p.k_start[s - 1]) || (!s && k);
+            const int32_t k = start[s];
+            bad |= k < 0 || (uint32_t)k > p.n_k || (s && k < start[s - 1]) || (!s && k);
         }
         if (bad) raise_error(p.err, DEV_ERANGE);
     }
-    const uint32_t row0 = blockIdx.x * READ_ROWS, rows = min((uint32_t)READ_ROWS, p.n_k - row0);
+    const uint32_t row0 = blockIdx.x * p.rows_cta, rows = min(p.rows_cta, p.n_k - row0);
     if (threadIdx.x < rows) {
         const int32_t row = (int32_t)(row0 + threadIdx.x);
         // the last sequence that starts at or before the row
         uint32_t lo = 0, hi = p.n_seq + 1;
         while (lo < hi) {
             const uint32_t mid = (lo + hi) / 2;
-            if (p.k_start[mid] <= row) lo = mid + 1;
+            if (start[mid] <= row) lo = mid + 1;
             else hi = mid;
         }
-        int2 a = make_int2(-2, 0);
+        int64_t a = -2;
+        int in_page = 0;
         if (lo > 0 && lo <= p.n_seq) {
             const uint32_t s = lo - 1;
             const int32_t r = p.seqs ? p.seqs[s] : (int32_t)s;
-            const int64_t pos = (int64_t)(p.first ? p.first[s] : 0) + row - p.k_start[s];
+            const int64_t pos = (int64_t)(p.first ? p.first[s] : 0) + row - start[s];
             const int64_t slot = pos >> p.c.page_shift;
-            a.x = -1;
+            a = -1;
             if (r >= 0 && (uint32_t)r < p.n_rows && pos >= 0 && slot < p.max_pages) {
                 const int32_t page = p.table[(uint64_t)r * p.table_stride + slot];
-                if (page >= 0 && (uint32_t)page < p.c.n_pages) a = make_int2(page, (int)(pos & ((1 << p.c.page_shift) - 1)));
+                if (page >= 0 && (uint32_t)page < p.c.n_pages) {
+                    in_page = (int)(pos & ((1 << p.c.page_shift) - 1));
+                    a = (int64_t)((uint64_t)page * p.c.page_stride + (uint64_t)in_page * p.c.dim * (Q8 ? 1 : 2));
+                }
             }
-            if (a.x < 0) raise_error(p.err, DEV_ERANGE);
+            if (a < 0) raise_error(p.err, DEV_ERANGE);
         }
         at[threadIdx.x] = a;
+        row_of[threadIdx.x] = in_page;
     }
     __syncthreads();
-    const uint32_t shift = 28 - __clz(p.c.dim), per_row = p.c.n_kv << shift, items = rows * per_row;
+    constexpr uint32_t N = Q8 ? 16 : 8;   // values of an item
+    const uint32_t shift = (Q8 ? 27 : 28) - __clz(p.c.dim), per_row = p.c.n_kv << shift, items = rows * per_row, mask = (1u << shift) - 1u;
     const uint8_t *pool = v ? p.c.v : p.c.k;
     void *out = v ? p.v_out : p.k_out;
     const uint64_t stride = v ? p.v_stride : p.k_stride;
-    const uint32_t dr = READ_THREADS / per_row, dc = READ_THREADS % per_row;
+    const uint32_t dr = READ_THREADS / per_row, dc = READ_THREADS % per_row, scales = p.c.dim << p.c.page_shift;
     uint32_t r = threadIdx.x / per_row, c = threadIdx.x % per_row;
-    // READ_AHEAD loads in flight a thread
     for (uint32_t i0 = threadIdx.x; i0 < items; i0 += READ_AHEAD * READ_THREADS) {
         uint4 w[READ_AHEAD];
         uint16_t d[READ_AHEAD];
-        uint32_t rs[READ_AHEAD], cs[READ_AHEAD];
+        int64_t to[READ_AHEAD];
 #pragma unroll
         for (int j = 0; j < READ_AHEAD; ++j) {
-            rs[j] = r;
-            cs[j] = c;
+            to[j] = -1;
             w[j] = make_uint4(0, 0, 0, 0);
             d[j] = 0;
             if (i0 + j * READ_THREADS < items) {
-                const int2 a = at[r];
-                if (a.x >= 0) {
-                    const uint32_t h = c >> shift, d0 = (c & ((1u << shift) - 1u)) * 8;
-                    const uint8_t *tile = pool + (uint64_t)a.x * p.c.page_stride + (uint64_t)h * p.c.tile_bytes;
-                    if (p.c.type == Q8_TYPE_Q8_0) {
-                        const uint2 q = __ldcs(reinterpret_cast<const uint2 *>(tile + (uint64_t)a.y * p.c.dim + d0));
-                        w[j].x = q.x;
-                        w[j].y = q.y;
-                        d[j] = __ldg(reinterpret_cast<const uint16_t *>(tile + ((uint64_t)p.c.dim << p.c.page_shift) +
-                                                                        ((uint64_t)a.y * (p.c.dim / QK) + d0 / QK) * 2));
-                    } else {
-                        w[j] = __ldcs(reinterpret_cast<const uint4 *>(tile + ((uint64_t)a.y * p.c.dim + d0) * 2));
-                    }
+                const int64_t a = at[r];
+                if (a != -2) to[j] = (int64_t)((row0 + r) * stride) + c * N;
+                if (a >= 0) {
+                    const uint8_t *tile = pool + (uint64_t)(c >> shift) * p.c.tile_bytes, *src = tile + a;
+                    w[j] = __ldcs(reinterpret_cast<const uint4 *>(src + (c & mask) * 16));
+                    // a page's first byte, its scales, this row's of them
+                    if (Q8)
+                        d[j] = __ldg(reinterpret_cast<const uint16_t *>(src - row_of[r] * (int)p.c.dim + scales) + row_of[r] * (p.c.dim / QK) + (c & mask) / 2);
                 }
             }
             r += dr;
@@ -224,17 +261,8 @@ __global__ void __launch_bounds__(READ_THREADS) k_kv_read(const KvReadParams p) 
             }
         }
 #pragma unroll
-        for (int j = 0; j < READ_AHEAD; ++j) {
-            if (i0 + j * READ_THREADS >= items || at[rs[j]].x == -2) continue;
-            const uint64_t to = (row0 + rs[j]) * stride + cs[j] * 8;
-            if (p.c.type == p.out_type) {
-                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + to) = w[j];
-                continue;
-            }
-            float y[8];
-            cached8(y, w[j], d[j], p.c.type);
-            store_out8(out, p.out_type, to, y, true);
-        }
+        for (int j = 0; j < READ_AHEAD; ++j)
+            if (to[j] >= 0) store_cached<Q8>(out, p.out_type, p.c.type, (uint64_t)to[j], w[j], d[j], p.whole);
     }
 }
 
@@ -583,9 +611,20 @@ cudaError_t launch_kv_append(KvAppendParams p, int num_sms, cudaStream_t st) {
     return launch_dependent(k_kv_append, p, dim3((unsigned)ctas, (unsigned)parts), APPEND_THREADS, 0, st);
 }
 
-cudaError_t launch_kv_read(const KvReadParams &p, int, cudaStream_t st) {
-    const unsigned ctas = (p.n_k + READ_ROWS - 1) / READ_ROWS;
-    return launch_dependent(k_kv_read, p, dim3(ctas, (p.k_out ? 1u : 0u) + (p.v_out ? 1u : 0u)), READ_THREADS, 0, st);
+cudaError_t launch_kv_read(const KvReadParams &q, int num_sms, cudaStream_t st) {
+    KvReadParams p = q;
+    // enough CTAs for every SM, then as many rows as spread the look-ups
+    const unsigned both = (p.k_out ? 1u : 0u) + (p.v_out ? 1u : 0u);
+    p.rows_cta = READ_ROWS;
+    while (p.rows_cta > 4 && (uint64_t)(p.n_k + p.rows_cta - 1) / p.rows_cta * both < 2 * (uint64_t)num_sms) p.rows_cta /= 2;
+    uint64_t bits = (uint64_t)(uintptr_t)p.k_out | (uint64_t)(uintptr_t)p.v_out;
+    const uint32_t size = p.out_type == Q8_TYPE_F32 ? 4 : 2;
+    if (p.k_out) bits |= p.k_stride * size;
+    if (p.v_out) bits |= p.v_stride * size;
+    p.whole = (bits & 31u) == 0;
+    const dim3 grid((p.n_k + p.rows_cta - 1) / p.rows_cta, both);
+    if (p.c.type == Q8_TYPE_Q8_0) return launch_dependent(k_kv_read<true>, p, grid, READ_THREADS, 0, st);
+    return launch_dependent(k_kv_read<false>, p, grid, READ_THREADS, 0, st);
 }
 
 size_t kv_pages_scratch(uint32_t n, uint32_t n_pages) {

@@ -44,6 +44,8 @@ struct KvReadParams {
     const int32_t *table, *seqs, *first, *k_start;
     uint64_t table_stride;
     uint32_t max_pages, n_rows, n_seq, n_k;
+    uint32_t rows_cta;                    // set by the launcher, as
+    bool whole;                           // rows that start on 32-byte boundaries
     int *err;
 };
 cudaError_t launch_kv_read(const KvReadParams &p, int num_sms, cudaStream_t st);

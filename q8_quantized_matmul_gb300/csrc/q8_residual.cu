@@ -36,16 +36,8 @@ __device__ __forceinline__ Sum2 add(Sum2 s, Sum2 t) {
     return {hi, __fadd_rn(__fadd_rn(s.lo, t.lo), e)};
 }
 
-// The products of two pairs, each on its own: a packed product whose only use is a packed sum is made one fused
-// operation with it, whatever the rounding that both ask for.
-__device__ __forceinline__ uint64_t mul2_alone(uint64_t a, uint64_t b) {
-    float a0, a1, b0, b1;
-    split2(a0, a1, a);
-    split2(b0, b1, b);
-    return pair2(__fmul_rn(a0, b0), __fmul_rn(a1, b1));
-}
-
-// The sums of the even and of the odd values' squares: twelve instructions for two values.
+// The sums of the even and of the odd values' squares: twelve instructions for two values.  The products are taken one by
+// one: a packed product that a packed sum uses is made one fused operation with it, whatever the rounding both ask for.
 struct Squares {
     uint64_t hi = 0, lo = 0;
     __device__ __forceinline__ void operator+=(uint64_t x) {
@@ -65,26 +57,48 @@ struct Squares {
     }
 };
 
-// The whole CTA's sum, rounded to fp32, on every thread.  part: 32 words that no other call of the row uses.
-__device__ __forceinline__ float cta_sum(const Squares &q, Sum2 *part) {
-    Sum2 s = q.both();
-#pragma unroll
-    for (int o = 16; o; o >>= 1)
-        s = add(s, {__shfl_xor_sync(0xffffffffu, s.hi, o), __shfl_xor_sync(0xffffffffu, s.lo, o)});
-    const int lane = threadIdx.x & 31, warps = (int)(blockDim.x >> 5);
-    if (lane == 0) part[threadIdx.x >> 5] = s;
-    __syncthreads();
-    s = lane < warps ? part[lane] : Sum2{0.0f, 0.0f};
-#pragma unroll
-    for (int o = 16; o; o >>= 1)
-        if (o < warps) s = add(s, {__shfl_xor_sync(0xffffffffu, s.hi, o), __shfl_xor_sync(0xffffffffu, s.lo, o)});
-    s.hi = __shfl_sync(0xffffffffu, s.hi, 0);
-    s.lo = __shfl_sync(0xffffffffu, s.lo, 0);
-    return isinf(s.hi) ? s.hi : __fadd_rn(s.hi, s.lo);
-}
-
 __device__ __forceinline__ float inverse_rms(float total, float dim, float eps) {
     return __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(total, dim), eps)));
+}
+
+__device__ __forceinline__ Sum2 lane_sum(Sum2 s, int from) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        if (o <= from) s = add(s, {__shfl_xor_sync(0xffffffffu, s.hi, o), __shfl_xor_sync(0xffffffffu, s.lo, o)});
+    return s;
+}
+
+// r of the whole CTA's values on every thread.  part: words that no other call of the row uses.  ONE_WARP: one warp joins every
+// thread's sums and takes the root (a longer chain, but 100 instructions less in every other warp); else each warp joins its
+// own, and then all of them for itself.
+template <int MAXT, bool ONE_WARP> struct Part {
+    Sum2 sums[ONE_WARP ? MAXT : 32];
+    float r;
+};
+template <int MAXT, bool ONE_WARP>
+__device__ __forceinline__ float cta_inverse_rms(const Squares &q, Part<MAXT, ONE_WARP> &part, float dim, float eps) {
+    Sum2 s = q.both();
+    const int lane = threadIdx.x & 31, warps = (int)(blockDim.x >> 5);
+    if constexpr (ONE_WARP) {
+        part.sums[threadIdx.x] = s;
+        __syncthreads();
+        if (threadIdx.x < 32) {
+            for (int w = 1; w < warps; ++w) s = add(s, part.sums[w * 32 + lane]);
+            s = lane_sum(s, 16);
+            if (lane == 0) part.r = inverse_rms(isinf(s.hi) ? s.hi : __fadd_rn(s.hi, s.lo), dim, eps);
+        }
+        __syncthreads();
+        return part.r;
+    } else {
+        s = lane_sum(s, 16);
+        if (lane == 0) part.sums[threadIdx.x >> 5] = s;
+        __syncthreads();
+        s = lane < warps ? part.sums[lane] : Sum2{0.0f, 0.0f};
+        s = lane_sum(s, warps > 16 ? 16 : warps > 8 ? 8 : warps > 4 ? 4 : warps > 2 ? 2 : warps > 1 ? 1 : 0);
+        s.hi = __shfl_sync(0xffffffffu, s.hi, 0);
+        s.lo = __shfl_sync(0xffffffffu, s.lo, 0);
+        return inverse_rms(isinf(s.hi) ? s.hi : __fadd_rn(s.hi, s.lo), dim, eps);
+    }
 }
 
 // 32 bytes of a row at once where it starts on such a boundary, else 16 at a time.
@@ -147,14 +161,86 @@ __device__ __forceinline__ void store8(void *out, int type, uint64_t i0, const f
     store_out8(out, type, i0, y, active);
 }
 
-// One CTA a row at a time; a thread has chunks of 8 values t, t + T, ..., NS of them.  AHEAD: the next row is loaded while
-// this one is worked on.
-template <int NS, int MAXT, int MINB, bool AHEAD, bool HWIDE, bool YWIDE>
+__device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either is
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
+// The quantiser (see quantize8: the same bytes) of eight values a lane, four lanes a block, in packed pairs: k, the whole number
+// next to x (1 / d) with an approximate 1 / d, is roundf(x / d) where the two differ by less than 0.4999 (their errors reach
+// 3 2^-23 128 < 5e-5); a lane with one that does not (or with a d of no reciprocal: the difference is then no number) divides.
+__device__ __forceinline__ void quantize8_pairs(const uint64_t (&x)[4], uint32_t &lo, uint32_t &hi, uint16_t &dh) {
+    float v[8];
+    unpack(v, x);
+    float amax = fmaxf(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))),
+                       fmaxf(fmaxf(fabsf(v[4]), fabsf(v[5])), fmaxf(fabsf(v[6]), fabsf(v[7]))));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    const float d = __fdiv_rn(amax, 127.0f);
+    float rd;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rd) : "f"(d));
+    const uint64_t rd2 = pair2(rd, rd), magic = pair2(ROUND_MAGIC, ROUND_MAGIC);
+    uint32_t t[8];
+    float off = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const uint64_t sm = fma2(x[e], rd2, magic), r = fma2(x[e], rd2, sub2(magic, sm));
+        float a, b, ra, rb;
+        split2(a, b, sm);
+        split2(ra, rb, r);
+        t[2 * e] = __float_as_uint(a);
+        t[2 * e + 1] = __float_as_uint(b);
+        off = max_nan(off, max_nan(fabsf(ra), fabsf(rb)));
+    }
+    lo = __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410);
+    hi = __byte_perm(__byte_perm(t[4], t[5], 0x0040), __byte_perm(t[6], t[7], 0x0040), 0x5410);
+    dh = __half_as_ushort(__float2half_rn(d));
+    if (!(off < 0.4999f)) {
+        lo = hi = 0;
+        if (d != 0.0f) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                lo |= (uint32_t)(uint8_t)(int8_t)(int)roundf(__fdiv_rn(v[e], d)) << (8 * e);
+                hi |= (uint32_t)(uint8_t)(int8_t)(int)roundf(__fdiv_rn(v[4 + e], d)) << (8 * e);
+            }
+        }
+    }
+}
+
+// A warp's 32 chunks of a row as Q8_0 (272 bytes; less at the row's end), through shared memory: written by its lanes, 34 bytes apart
+// and two at a time, a row took four times the sectors.
+__device__ __forceinline__ void store_q8_warp(uint8_t *dst, uint8_t *stage, const uint64_t (&n)[4], uint32_t live_chunks) {
+    const uint32_t lane = threadIdx.x & 31u;
+    uint32_t lo, hi;
+    uint16_t dh;
+    quantize8_pairs(n, lo, hi, dh);
+    uint16_t *at = reinterpret_cast<uint16_t *>(stage + lane / 4 * QB + 2 + lane % 4 * 8);
+    at[0] = (uint16_t)lo;
+    at[1] = (uint16_t)(lo >> 16);
+    at[2] = (uint16_t)hi;
+    at[3] = (uint16_t)(hi >> 16);
+    if (lane % 4 == 0) at[-1] = dh;
+    __syncwarp();
+    const uint32_t bytes = live_chunks / 4 * QB;
+    if (bytes == 272 && (reinterpret_cast<uintptr_t>(dst) & 15u) == 0) {
+        if (lane < 17) reinterpret_cast<uint4 *>(dst)[lane] = reinterpret_cast<const uint4 *>(stage)[lane];
+    } else {
+        for (uint32_t i = lane; i < bytes / 2; i += 32) reinterpret_cast<uint16_t *>(dst)[i] = reinterpret_cast<const uint16_t *>(stage)[i];
+    }
+    __syncwarp();
+}
+
+// One CTA a row at a time; a thread has chunks of 8 values t, t + T, ..., NS of them.  MANY: for many rows a CTA: the next row is
+// loaded while this one is worked on, one warp takes the roots.
+template <int NS, int MAXT, int MINB, bool MANY, bool HWIDE, bool YWIDE>
 __global__ void __launch_bounds__(MAXT, MINB) k_residual_norm(const ResidualNormParams p, int h_type, int y_type) {
-    __shared__ Sum2 part[2][32];
+    __shared__ __align__(16) uint8_t stages[MAXT / 32][272];
+    __shared__ Part<MAXT, MANY> part[2];
     const uint32_t chunks = p.dim / 8, t = threadIdx.x, T = blockDim.x;
     const float dim = (float)p.dim;
     const bool hbf = h_type == Q8_TYPE_BF16, ybf = y_type == Q8_TYPE_BF16, whole = p.whole;
+    const uint32_t row_bytes = p.dim / QK * QB;
     const uint64_t scale2 = pair2(p.residual_scale, p.residual_scale);
     Raw8<YWIDE> yraw[NS];
     Raw8<HWIDE> hraw[NS];
@@ -171,10 +257,10 @@ __global__ void __launch_bounds__(MAXT, MINB) k_residual_norm(const ResidualNorm
         }
     };
     grid_dep_wait();
-    if (AHEAD) load_row(blockIdx.x);
+    if (MANY) load_row(blockIdx.x);
     for (uint64_t row = blockIdx.x; row < p.n_tok; row += gridDim.x) {
         const float *gate = p.gate ? p.gate + row * p.gate_stride : nullptr;
-        if (!AHEAD) load_row(row);
+        if (!MANY) load_row(row);
         float ry = 1.0f;
         if (p.post) {
             Squares acc;
@@ -186,7 +272,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_residual_norm(const ResidualNorm
 #pragma unroll
                     for (int e = 0; e < 4; ++e) acc += v[e];
                 }
-            ry = inverse_rms(cta_sum(acc, part[0]), dim, p.eps);
+            ry = cta_inverse_rms(acc, part[0], dim, p.eps);
         }
         const uint64_t ry2 = pair2(ry, ry);
         uint64_t hv[NS][4];
@@ -200,22 +286,27 @@ __global__ void __launch_bounds__(MAXT, MINB) k_residual_norm(const ResidualNorm
             values<HWIDE>(hv[s], hraw[s], hbf);
             if (p.post) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) u[e] = mul2_alone(u[e], ry2);
+                for (int e = 0; e < 4; ++e) u[e] = mul2(u[e], ry2);
                 if (p.gamma_post) {
                     load_pairs(g, p.gamma_post + c * 8, whole);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) u[e] = mul2_alone(u[e], g[e]);
+                    for (int e = 0; e < 4; ++e) u[e] = mul2(u[e], g[e]);
                 }
             }
             if (gate) {
                 load_pairs(g, gate + c * 8, whole);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) u[e] = mul2_alone(g[e], u[e]);
+                for (int e = 0; e < 4; ++e) u[e] = mul2(g[e], u[e]);
             }
+            float h[8], v[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) hv[s][e] = add2(mul2_alone(scale2, hv[s][e]), u[e]);
-            float h[8];
+            for (int e = 0; e < 4; ++e) hv[s][e] = mul2(scale2, hv[s][e]);
             unpack(h, hv[s]);
+            unpack(v, u);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) h[e] = __fadd_rn(h[e], v[e]);   // one by one: see Squares
+#pragma unroll
+            for (int e = 0; e < 4; ++e) hv[s][e] = pair2(h[2 * e], h[2 * e + 1]);
             if constexpr (!HWIDE) {   // the next norm is of the stored value
                 Raw8<false> r;
 #pragma unroll
@@ -229,19 +320,18 @@ __global__ void __launch_bounds__(MAXT, MINB) k_residual_norm(const ResidualNorm
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc += hv[s][e];
         }
-        if (AHEAD && row + gridDim.x < p.n_tok) load_row(row + gridDim.x);
+        if (MANY && row + gridDim.x < p.n_tok) load_row(row + gridDim.x);
         if (!p.n_out) {
             if (p.post) __syncthreads();   // part[0] of the next row
             continue;
         }
-        const float rh = inverse_rms(cta_sum(acc, part[1]), dim, p.eps);
+        const float rh = cta_inverse_rms(acc, part[1], dim, p.eps);
         const uint64_t rh2 = pair2(rh, rh);
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
             const uint32_t c = t + s * T;
             if ((c & ~31u) >= chunks) continue;      // whole warps: the quantiser shuffles
             uint64_t g[4];
-            float n[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
             if (c < chunks) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) hv[s][e] = mul2(hv[s][e], rh2);
@@ -250,46 +340,67 @@ __global__ void __launch_bounds__(MAXT, MINB) k_residual_norm(const ResidualNorm
 #pragma unroll
                     for (int e = 0; e < 4; ++e) hv[s][e] = mul2(hv[s][e], g[e]);
                 }
-                unpack(n, hv[s]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) hv[s][e] = 0;
             }
-            store8(p.n_out, p.n_type, row * p.dim + (uint64_t)c * 8, n, c < chunks, whole);
+            if (p.n_type == Q8_TYPE_Q8_0) {
+                const uint32_t c0 = c & ~31u;
+                store_q8_warp(static_cast<uint8_t *>(p.n_out) + row * row_bytes + (uint64_t)c0 / 4 * QB, stages[t / 32], hv[s], min(32u, chunks - c0));
+            } else {
+                float n[8];
+                unpack(n, hv[s]);
+                store8(p.n_out, p.n_type, row * p.dim + (uint64_t)c * 8, n, c < chunks, whole);
+            }
         }
-        // part[0] is written again after part[1]'s barrier, part[1] after part[0]'s (none without the first norm)
+        // part[0] is written again after part[1]'s barriers, part[1] after part[0]'s (none without the first norm)
         if (!p.post) __syncthreads();
     }
 }
 
-template <class K>
-cudaError_t launch_rows(K kernel, const ResidualNormParams &p, int h_type, int y_type, int threads, int ctas, cudaStream_t st) {
+template <int NS, int MAXT, int MINB, bool MANY, bool HWIDE, bool YWIDE>
+cudaError_t launch_rows(const ResidualNormParams &p, int h_type, int y_type, int num_sms, cudaStream_t st) {
+    const auto kernel = k_residual_norm<NS, MAXT, MINB, MANY, HWIDE, YWIDE>;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(p.n_tok < (uint64_t)ctas ? p.n_tok : (uint64_t)ctas));
-    cfg.blockDim = dim3((unsigned)threads);
+    const unsigned threads = (p.dim / 8 + NS - 1) / NS + 31 & ~31u;
+    cfg.blockDim = dim3(threads);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p, h_type, y_type);
+    int fit = 0;
+    cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, (int)threads, 0);
+    if (e != cudaSuccess) return e;
+    if (fit < 1) fit = 1;
+    const uint64_t ctas = (uint64_t)num_sms * fit;
+    cfg.gridDim = dim3((unsigned)(p.n_tok < ctas ? p.n_tok : ctas));
+    e = cudaLaunchKernelEx(&cfg, kernel, p, h_type, y_type);
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
+#ifndef VAR
+#define VAR 0
+#endif
 template <bool HWIDE, bool YWIDE>
 cudaError_t launch_typed(const ResidualNormParams &p, int h_type, int y_type, int num_sms, cudaStream_t st) {
     const uint32_t chunks = p.dim / 8;
-    const auto threads = [&](int ns) { return (int)((chunks + ns - 1) / ns + 31) & ~31; };
-    // CTAs that fill the SMs: 65536 registers, 32 CTAs
-    const auto ctas = [&](int ns, int regs) {
-        const int per = 65536 / (regs * threads(ns));
-        return num_sms * (per > 32 ? 32 : per < 1 ? 1 : per);
-    };
-    if (chunks <= 512)
-        return launch_rows(k_residual_norm<1, 512, 2, true, HWIDE, YWIDE>, p, h_type, y_type, threads(1), ctas(1, 64), st);
-    if (chunks <= 1024)
-        return launch_rows(k_residual_norm<2, 512, 1, true, HWIDE, YWIDE>, p, h_type, y_type, threads(2), ctas(2, 128), st);
-    if (chunks <= 2048)
-        return launch_rows(k_residual_norm<4, 512, 1, false, HWIDE, YWIDE>, p, h_type, y_type, threads(4), ctas(4, 128), st);
-    return launch_rows(k_residual_norm<4, 1024, 1, false, HWIDE, YWIDE>, p, h_type, y_type, threads(4), ctas(4, 64), st);
+    // Few rows: as many threads a row as it has chunks, the shortest chain.  Many: more values a thread, for the joining of
+    // the two-word sums costs every warp alike.
+    if (chunks <= 512 && p.n_tok <= (uint64_t)(2 * num_sms)) return launch_rows<1, 512, 2, false, HWIDE, YWIDE>(p, h_type, y_type, num_sms, st);
+#if VAR == 0
+    if (chunks <= 512) return launch_rows<2, 256, 3, true, HWIDE, YWIDE>(p, h_type, y_type, num_sms, st);
+#elif VAR == 1
+    if (chunks <= 512) return launch_rows<1, 512, 2, true, HWIDE, YWIDE>(p, h_type, y_type, num_sms, st);
+#elif VAR == 2
+    if (chunks <= 512) return launch_rows<2, 256, 4, true, HWIDE, YWIDE>(p, h_type, y_type, num_sms, st);
+#else
+    if (chunks <= 512) return launch_rows<4, 128, 4, true, HWIDE, YWIDE>(p, h_type, y_type, num_sms, st);
+#endif
+    if (chunks <= 1024) return launch_rows<4, 256, 2, true, HWIDE, YWIDE>(p, h_type, y_type, num_sms, st);
+    if (chunks <= 2048) return launch_rows<4, 512, 1, true, HWIDE, YWIDE>(p, h_type, y_type, num_sms, st);
+    return launch_rows<4, 1024, 1, false, HWIDE, YWIDE>(p, h_type, y_type, num_sms, st);
 }
 
 }  // namespace
