@@ -120,9 +120,8 @@ __global__ void __launch_bounds__(APPEND_THREADS) k_kv_append(const KvAppendPara
 
 // ---------------------------------------------------------------- reading back
 constexpr int READ_THREADS = 256;
-constexpr int READ_ROWS = 64;             // most rows of a CTA
+constexpr int READ_ROWS = 16;             // most rows of a CTA
 constexpr int READ_STARTS = 1024;         // starts that a CTA keeps
-constexpr int READ_AHEAD = 4;             // loads in flight a thread
 
 // 32 bytes at once where the rows start on such boundaries, else 16 at a time.
 __device__ __forceinline__ void store32(void *to, const uint32_t (&w)[8], bool whole) {
@@ -178,6 +177,7 @@ template <bool Q8> __device__ __forceinline__ void store_cached(void *out, int o
 // Rows [rows_cta blockIdx.x, ...) of K (blockIdx.y 0) or V: where each lies is looked up once, then a thread takes 16 bytes of a
 // page at a time.
 template <bool Q8> __global__ void __launch_bounds__(READ_THREADS) k_kv_read(const KvReadParams p) {
+    constexpr int READ_AHEAD = Q8 ? 2 : 4;   // loads in flight a thread (Q8_0 needs more registers: with four 38.9 us instead of 32.9)
     __shared__ int64_t at[READ_ROWS];     // the row's first byte in head 0's tile from the pool's start (-1: none, zeros; -2: no row)
     __shared__ int row_of[READ_ROWS];     // its row in the page
     __shared__ int32_t starts[READ_STARTS];

@@ -30,7 +30,7 @@ constexpr int NO_ADAPTER = -1;
 constexpr int RT = 1024;
 
 struct Sums {
-    int tokens, tiles, groups;
+    int tokens, tiles, groups;            // (first scan: adapters with enough tokens, tiles were all to have them, -)
     __device__ __forceinline__ Sums operator+(const Sums &o) const { return {tokens + o.tokens, tiles + o.tiles, groups + o.groups}; }
 };
 __device__ __forceinline__ Sums shfl_up(const Sums &s, int o) {
@@ -100,13 +100,21 @@ __global__ void __launch_bounds__(RT) k_lora_route(const LoraParams p) {
     __syncthreads();
     // what becomes of an adapter's tokens: tiles, groups, or (no adapter, or one of rank 0) tiles that copy base
     const int per = (n + RT - 1) / RT, b0 = min(n, (int)threadIdx.x * per), b1 = min(n, b0 + per);
+    Sums mine = {0, 0, 0}, total;
+    for (int i = b0; i < b1; ++i)
+        if (i < n - 1 && counts[i]) mine = mine + Sums{counts[i] >= (int)LORA_TILE_MIN, (counts[i] + (int)TM - 1) / (int)TM, 0};
+    scan(mine, total, warps);
+    __syncthreads();
+    // Groups spare a tile's work for few tokens, but are a kernel of their own: only where there are no tiles otherwise, or so
+    // many that they would wait for each other (333 tokens of 12 adapters: 33 us with both, see q8_layer.h)
+    const bool groups = total.tokens == 0 || total.tiles > (int)LORA_TILES_AT_ONCE;
     const auto kind = [&](int i, int c, int &rank) -> Sums {
         rank = c && i < n - 1 ? (int)rank_of(p, i, false) : 0;
         if (rank == 0) return {c, p.base == p.out ? 0 : (c + (int)TM - 1) / (int)TM, 0};
-        if (c < (int)LORA_TILE_MIN) return {c, 0, (c + (int)LORA_GROUP - 1) / (int)LORA_GROUP};
+        if (groups && c < (int)LORA_TILE_MIN) return {c, 0, (c + (int)LORA_GROUP - 1) / (int)LORA_GROUP};
         return {c, (c + (int)TM - 1) / (int)TM, 0};
     };
-    Sums mine = {0, 0, 0}, total;
+    mine = {0, 0, 0};
     int rank;
     for (int i = b0; i < b1; ++i) {
         if (counts[i] && i < n - 1) rank_of(p, i, true);
@@ -166,23 +174,20 @@ template <int N> __device__ __forceinline__ void terms_f16(uint4 (&out)[N], cons
 // Byte offset of 16-byte chunk c of row r in a tile of 128-byte rows, swizzled as the matrix descriptors say.
 __device__ __forceinline__ uint32_t swizzled(uint32_t r, uint32_t c) { return r * 128 + ((c ^ (r & 7u)) << 4); }
 
-// The products of one K step: x terms times weight terms, those that reach 2^-24.  x, w: the terms' tiles, x_step and w_step
-// bytes apart.  Term (0, 0) goes to d; the others to d + rest, or with rest 0 to d as well.  acc, acc_rest: whether the
-// accumulators hold sums already.
-template <int NX, int NW, bool X_IS_A>
-__device__ __forceinline__ void issue_terms(uint32_t d, uint32_t rest, uint32_t x, uint32_t x_step, uint32_t w, uint32_t w_step,
-                                            int ksteps, uint32_t idesc, bool acc, bool acc_rest) {
+// The products of one K step of 16 * ksteps values: weight terms (rows of the product) times low's three terms, those that reach
+// 2^-24, into one accumulator.  acc: whether it holds sums already.
+template <int NW>
+__device__ __forceinline__ void issue_terms(uint32_t d, uint32_t low, uint32_t low_step, uint32_t w, uint32_t w_step, int ksteps, uint32_t idesc,
+                                            bool acc) {
 #pragma unroll
-    for (int i = 0; i < NX; ++i)
+    for (int i = 0; i < 3; ++i)
 #pragma unroll
         for (int j = 0; j < NW; ++j) {
             if (i + j > 2) continue;
-            const uint64_t xd = sw128_desc(x + i * x_step), wd = sw128_desc(w + j * w_step);
-            const bool apart = i + j && rest;
+            const uint64_t ld = sw128_desc(low + i * low_step), wd = sw128_desc(w + j * w_step);
             for (int k = 0; k < ksteps; ++k) {
-                tc_mma_f16(apart ? d + rest : d, (X_IS_A ? xd : wd) + 2 * k, (X_IS_A ? wd : xd) + 2 * k, idesc, apart ? acc_rest : acc);
-                if (apart) acc_rest = true;
-                else acc = true;
+                tc_mma_f16(d, wd + 2 * k, ld + 2 * k, idesc, acc);
+                acc = true;
             }
         }
 }
@@ -198,34 +203,36 @@ __device__ __forceinline__ void tmem_free(uint32_t tmem, uint32_t cols) {
 // ---------------------------------------------------------------- shrink
 enum XKind { X_F32, X_Q8, X_RAW, X_F16 };   // RAW: 16-bit values as they are; F16: split into two bf16 terms
 
-// Warps 0-15 turn raw rows into terms, two groups of eight a K step in turn, and finish the tile; warps 16-19 copy raw rows into a ring, warp 20 issues the products.
+// Warps 0-15 turn raw rows into terms (x's in TMEM, the weights' in shared memory), two groups of eight a K step in turn, and
+// finish the tile; warps 16-19 copy raw rows into a ring, warp 20 issues the products.
 // The warps that fence their shared-memory writes for the tensor cores load nothing from global memory themselves: the fence
 // waits for a warp's outstanding loads (with the loads in registers, two steps ahead, a step took 2.4 us).
 constexpr int CONVERT = 512, GROUP = 256, COPY = 128, ST = CONVERT + COPY + 32;
-constexpr uint32_t MAX_RAW = 4;
+constexpr uint32_t MAX_RAW = 6;
 
 __host__ __device__ constexpr uint32_t round16(uint32_t r) { return (r + 15u) & ~15u; }
 
 template <int XK> constexpr uint32_t RAW_PITCH = XK == X_F32 ? 256 : XK == X_Q8 ? 80 : 128;   // bytes of a raw row of x
 struct ShrinkShape {
-    uint32_t stage, stages, raw, raws, body, smem;           // as many converting groups as stages
+    uint32_t stage, raw, raws, body, smem;
 };
-template <int XK, int NX, int NW> __host__ __device__ constexpr ShrinkShape shrink_shape(uint32_t max_rank) {
+template <int XK, int NW> __host__ __device__ constexpr ShrinkShape shrink_shape(uint32_t max_rank) {
     ShrinkShape s{};
     const uint32_t cols = round16(max_rank), room = SMEM_MOST - 1024;
-    s.stage = NX * PLANE + NW * cols * 128;
+    s.stage = NW * cols * 128;                               // the weights' terms of a K step
     s.raw = TM * RAW_PITCH<XK> + cols * 128;
-    s.stages = 2 * s.stage + 2 * s.raw <= room ? 2 : 1;
-    s.body = s.stages * s.stage;
+    s.body = 2 * s.stage;
     const uint32_t part = TM * (cols + 4) * 4;               // the CTA's sums take the stages' place
     if (s.body < part) s.body = part;
     s.body = (s.body + 1023) & ~1023u;
     s.raws = (room - s.body) / s.raw;
     if (s.raws > MAX_RAW) s.raws = MAX_RAW;
-    if (s.stages == 2) s.raws &= ~1u;                        // a raw slot stays with one group, so none runs a phase of it ahead
+    s.raws &= ~1u;                                           // a raw slot stays with one group, so none runs a phase of it ahead
     s.smem = 1024 + s.body + s.raws * s.raw;
     return s;
 }
+// TMEM columns: sums of the first terms' products at 0, of the others at REST, two stages of x terms (32 columns a term).
+constexpr uint32_t REST = 128, X_COLS = 256, X_STAGE = 96;
 
 // `bytes` of 16 or 4 global -> shared, the rest zeros.
 __device__ __forceinline__ void cp_async16_part(uint32_t dst, const void *src, uint32_t bytes) {
@@ -285,7 +292,7 @@ __device__ __forceinline__ void copy_raw(const LoraParams &p, uint8_t *raw, cons
         const uint8_t *x = static_cast<const uint8_t *>(p.x) + ((uint64_t)k0 * SIZE + (in ? c * 16 : 0));
 #pragma unroll 8
         for (uint32_t row = b / LANES; row < count; row += COPY / LANES)
-            cp_async16_part(x_dst + row * RAW_PITCH<XK> + c * 16, x + (uint64_t)toks[row] * p.x_stride * SIZE, in ? 16 : 0);
+            cp_async16_part(x_dst + row * RAW_PITCH<XK> + ((c ^ (row & 7u)) << 4), x + (uint64_t)toks[row] * p.x_stride * SIZE, in ? 16 : 0);
     }
     const uint32_t c = b % 8;
     const bool in = c * 8 < left;
@@ -294,69 +301,84 @@ __device__ __forceinline__ void copy_raw(const LoraParams &p, uint8_t *raw, cons
         cp_async16_part(w_dst + row * 128 + c * 16, a + (uint64_t)row * p.in_dim + k0 + (in ? c * 8 : 0), in ? 16 : 0);
 }
 
-// A raw step as terms in a stage (thread t of a group's 256).
+// A raw step as terms (thread t of a group's 256): a thread has 32 of a row's 64 values, the row its lane of TMEM.
 template <int XK, int NX, int NW>
-__device__ __forceinline__ void convert(const LoraParams &p, uint8_t *stage, const uint8_t *raw, const uint32_t *toks, uint32_t k0, uint32_t cols,
-                                        uint32_t w_step, uint64_t *raw_empty, uint32_t t) {
-    constexpr uint32_t LANES = XK == X_F32 || XK == X_Q8 ? 16 : 8, ROWS = TM * LANES / GROUP, WROWS = LORA_MAX_RANK * 8 / GROUP;
-    const uint32_t c = t % LANES;
-    uint4 x[ROWS], w[WROWS];
+__device__ __forceinline__ void convert(const LoraParams &p, uint32_t x_tmem, uint8_t *w_stage, const uint8_t *raw, const uint32_t *toks, uint32_t k0,
+                                        uint32_t cols, uint32_t w_step, uint64_t *raw_empty, uint32_t t) {
+    constexpr uint32_t WROWS = LORA_MAX_RANK * 8 / GROUP;
+    const uint32_t row = t % 128, half = t / 128;
+    uint4 x[8], w[WROWS];
+    uint16_t d = 0;
+    if constexpr (XK == X_Q8) {
+        // the row's copy starts on a word; its first block 0 or 2 bytes behind that
+        const uint32_t odd = ((uint32_t)(p.in_dim / QK) & toks[row] & 1u) * 2;
+        const uint16_t *blk = reinterpret_cast<const uint16_t *>(raw + row * RAW_PITCH<XK> + odd + half * QB);
+        const bool in = k0 + half * 32 < p.in_dim;
+        d = in ? blk[0] : (uint16_t)0;
 #pragma unroll
-    for (uint32_t i = 0; i < ROWS; ++i) {
-        const uint32_t row = t / LANES + i * (GROUP / LANES);
-        if constexpr (XK == X_Q8) {
-            // the row's copy starts on a word; its first block 0 or 2 bytes behind that
-            const uint32_t odd = ((uint32_t)(p.in_dim / QK) & toks[row] & 1u) * 2;
-            const uint16_t *blk = reinterpret_cast<const uint16_t *>(raw + row * RAW_PITCH<XK> + odd + (c >= 8 ? QB : 0));
-            const bool in = k0 + c * 4 < p.in_dim;
-            x[i].x = in ? blk[1 + c % 8 * 2] | (uint32_t)blk[2 + c % 8 * 2] << 16 : 0u;
-            x[i].y = in ? blk[0] : 0u;
-        } else {
-            x[i] = *reinterpret_cast<const uint4 *>(raw + row * RAW_PITCH<XK> + c * 16);
+        for (int i = 0; i < 2; ++i) {
+            uint32_t *q = reinterpret_cast<uint32_t *>(&x[i]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) q[e] = in ? blk[1 + 8 * i + 2 * e] | (uint32_t)blk[2 + 8 * i + 2 * e] << 16 : 0u;
         }
+    } else {
+        constexpr uint32_t N = XK == X_F32 ? 8 : 4;          // 16-byte pieces of 32 values
+#pragma unroll
+        for (uint32_t i = 0; i < N; ++i) x[i] = *reinterpret_cast<const uint4 *>(raw + row * RAW_PITCH<XK> + (((half * N + i) ^ (row & 7u)) << 4));
     }
 #pragma unroll
     for (uint32_t i = 0; i < WROWS; ++i) {
-        const uint32_t row = t / 8 + i * (GROUP / 8);
-        if (row < cols) w[i] = *reinterpret_cast<const uint4 *>(raw + TM * RAW_PITCH<XK> + row * 128 + t % 8 * 16);
+        const uint32_t r = t / 8 + i * (GROUP / 8);
+        if (r < cols) w[i] = *reinterpret_cast<const uint4 *>(raw + TM * RAW_PITCH<XK> + r * 128 + t % 8 * 16);
     }
     __syncwarp();
     if (t % 32 == 0) mbar_arrive(raw_empty);
+    uint32_t terms[NX][16];                                  // pairs of values
 #pragma unroll
-    for (uint32_t i = 0; i < ROWS; ++i) {
-        const uint32_t row = t / LANES + i * (GROUP / LANES);
-        if constexpr (LANES == 16) {
-            const uint32_t at = swizzled(row, c / 2) + c % 2 * 8;
+    for (int i = 0; i < 8; ++i) {
+        if constexpr (XK == X_F32 || XK == X_Q8) {
             float v[4] = {__uint_as_float(x[i].x), __uint_as_float(x[i].y), __uint_as_float(x[i].z), __uint_as_float(x[i].w)};
             if constexpr (XK == X_Q8) {
-                quants4(v, x[i].x);
-                const float d = half_bits_to_float((uint16_t)x[i].y);
+                quants4(v, reinterpret_cast<const uint32_t *>(x)[i]);
+                const float s = half_bits_to_float(d);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] *= d;
+                for (int e = 0; e < 4; ++e) v[e] *= s;
             }
             uint32_t lo[NX], hi[NX];
             terms2<NX>(lo, v[0], v[1]);
             terms2<NX>(hi, v[2], v[3]);
 #pragma unroll
-            for (int j = 0; j < NX; ++j) *reinterpret_cast<uint2 *>(stage + j * PLANE + at) = make_uint2(lo[j], hi[j]);
-        } else {
+            for (int j = 0; j < NX; ++j) {
+                terms[j][2 * i] = lo[j];
+                terms[j][2 * i + 1] = hi[j];
+            }
+        } else if (i < 4) {
             uint4 y[NX];
             if constexpr (XK == X_F16) terms_f16<NX>(y, x[i]);
             else y[0] = x[i];
 #pragma unroll
-            for (int j = 0; j < NX; ++j) *reinterpret_cast<uint4 *>(stage + j * PLANE + swizzled(row, c)) = y[j];
+            for (int j = 0; j < NX; ++j) {
+                terms[j][4 * i] = y[j].x;
+                terms[j][4 * i + 1] = y[j].y;
+                terms[j][4 * i + 2] = y[j].z;
+                terms[j][4 * i + 3] = y[j].w;
+            }
         }
     }
 #pragma unroll
+    for (int j = 0; j < NX; ++j) tc_st16(x_tmem + (row / 32 << 21) + j * 32 + half * 16, terms[j]);
+#pragma unroll
     for (uint32_t i = 0; i < WROWS; ++i) {
-        const uint32_t row = t / 8 + i * (GROUP / 8);
-        if (row >= cols) continue;
+        const uint32_t r = t / 8 + i * (GROUP / 8);
+        if (r >= cols) continue;
         uint4 y[NW];
         if constexpr (NW == 2) terms_f16<NW>(y, w[i]);
         else y[0] = w[i];
 #pragma unroll
-        for (int j = 0; j < NW; ++j) *reinterpret_cast<uint4 *>(stage + NX * PLANE + j * w_step + swizzled(row, t % 8)) = y[j];
+        for (int j = 0; j < NW; ++j) *reinterpret_cast<uint4 *>(w_stage + j * w_step + swizzled(r, t % 8)) = y[j];
     }
+    tc_wait_st();
+    tc_fence_before();
 }
 
 template <int XK, int NX, int NW>
@@ -368,11 +390,10 @@ __global__ void __launch_bounds__(ST, 1) k_lora_shrink(const LoraParams p) {
     __shared__ uint64_t raw_full[MAX_RAW], raw_empty[MAX_RAW], st_full[2], st_empty[2], tok_full[2], tok_empty[2], d_full, parts_ready,
         parts_read;
     uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-    const ShrinkShape sh = shrink_shape<XK, NX, NW>(p.max_rank);
+    const ShrinkShape sh = shrink_shape<XK, NW>(p.max_rank);
     uint8_t *ring = smem + sh.body;
     const uint32_t t = threadIdx.x, warp = t >> 5, lane = t & 31u, k = cluster_rank(), SC = p.shrink_cluster;
     const uint32_t cols_max = round16(p.max_rank), w_step = cols_max * 128;
-    const uint32_t tmem_cols = cols_max <= 16 ? 32 : cols_max <= 32 ? 64 : cols_max <= 64 ? 128 : 256, rest = tmem_cols / 2;
     if (t == 0) {
         for (uint32_t i = 0; i < MAX_RAW; ++i) {
             mbar_init(&raw_full[i], COPY);
@@ -393,7 +414,7 @@ __global__ void __launch_bounds__(ST, 1) k_lora_shrink(const LoraParams p) {
     cluster_arrive();   // every CTA's barriers are there
     cluster_wait();
     grid_dep_wait();
-    if (warp == ST / 32 - 1) tmem_alloc(&tmem_slot, tmem_cols);
+    if (warp == ST / 32 - 1) tmem_alloc(&tmem_slot, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -426,12 +447,23 @@ __global__ void __launch_bounds__(ST, 1) k_lora_shrink(const LoraParams p) {
             // ------------------------------------------------ products
             const uint32_t idesc = tc_idesc(TM, cols, !(XK == X_RAW && !p.bf16 && NW == 1));
             for (uint32_t kb = kb0; kb < kb1; ++kb, ++n) {
-                const uint32_t s = n % sh.stages;
-                wait(&st_full[s], (n / sh.stages) & 1);
+                const uint32_t s = n & 1;
+                wait(&st_full[s], (n / 2) & 1);
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint32_t at = smem_addr(smem + s * sh.stage);
-                    issue_terms<NX, NW, true>(tmem, rest, at, PLANE, at + NX * PLANE, w_step, KB / 16, idesc, kb != kb0, kb != kb0);
+                    const uint32_t x = tmem + X_COLS + s * X_STAGE, w = smem_addr(smem + s * sh.stage);
+#pragma unroll
+                    for (int i = 0; i < NX; ++i)
+#pragma unroll
+                        for (int j = 0; j < NW; ++j) {
+                            if (i + j > 2) continue;
+                            // the first product of an accumulator starts it
+                            const bool starts = kb == kb0 && (i + j == 0 || (i == 0 && j == 1) || (NW == 1 && i == 1));
+                            const uint64_t wd = sw128_desc(w + j * w_step);
+#pragma unroll
+                            for (int k = 0; k < (int)KB / 16; ++k)
+                                tc_mma_f16_ta(i + j ? tmem + REST : tmem, x + i * 32 + k * 8, wd + 2 * k, idesc, !(starts && k == 0));
+                        }
                     tc_commit(&st_empty[s]);
                     if (kb + 1 == kb1) tc_commit(&d_full);
                 }
@@ -441,11 +473,13 @@ __global__ void __launch_bounds__(ST, 1) k_lora_shrink(const LoraParams p) {
             // ------------------------------------------------ terms
             wait(&tok_full[tiles & 1], (tiles / 2) & 1);
             for (uint32_t kb = kb0; kb < kb1; ++kb, ++n) {
-                if (n % sh.stages != t / GROUP) continue;
-                const uint32_t r = n % sh.raws, s = n % sh.stages, use = n / sh.stages;
+                if (n % 2 != t / GROUP) continue;
+                const uint32_t r = n % sh.raws, s = n & 1, use = n / 2;
                 wait(&raw_full[r], (n / sh.raws) & 1);
                 if (use) wait(&st_empty[s], (use - 1) & 1);
-                convert<XK, NX, NW>(p, smem + s * sh.stage, ring + r * sh.raw, tok, kb * KB, cols, w_step, &raw_empty[r], t % GROUP);
+                tc_fence_after();
+                convert<XK, NX, NW>(p, tmem + X_COLS + s * X_STAGE, smem + s * sh.stage, ring + r * sh.raw, tok, kb * KB, cols, w_step, &raw_empty[r],
+                                    t % GROUP);
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&st_full[s]);
@@ -464,7 +498,7 @@ __global__ void __launch_bounds__(ST, 1) k_lora_shrink(const LoraParams p) {
                 if (kb0 < kb1) {
                     const uint32_t at = tmem + ((warp & 3) << 21) + c;
                     tc_ld16(at, d0);
-                    if constexpr (NX + NW > 2) tc_ld16(at + rest, d1);
+                    if constexpr (NX + NW > 2) tc_ld16(at + REST, d1);
                     tc_wait_ld();
                     tc_regs_ready(d0);
                     tc_regs_ready(d1);
@@ -520,7 +554,7 @@ __global__ void __launch_bounds__(ST, 1) k_lora_shrink(const LoraParams p) {
     if (warp >= CONVERT / 32 && warp < (CONVERT + COPY) / 32) cp_async_wait<0>();   // nothing lands after the CTA has gone
     tc_fence_before();
     __syncthreads();
-    if (warp == ST / 32 - 1) tmem_free(tmem, tmem_cols);
+    if (warp == ST / 32 - 1) tmem_free(tmem, 512);
     cluster_arrive();   // no CTA leaves while another may still read its sums, expired waits included
     cluster_wait();
 }
@@ -713,8 +747,8 @@ template <int NW, bool WHOLE> __global__ void __launch_bounds__(ET, 1) k_lora_ex
             tc_fence_after();
             if (elect_one()) {
                 for (uint32_t kb = 0; kb * KB < kr; ++kb)
-                    issue_terms<3, NW, false>(tmem + (u & 1) * TM, 0, smem_addr(smem) + kb * PLANE, step, smem_addr(bs) + st * NW * step + kb * PLANE,
-                                              step, (int)(min(KB, kr - kb * KB) / 16), idesc, kb != 0, true);
+                    issue_terms<NW>(tmem + (u & 1) * TM, smem_addr(smem) + kb * PLANE, step, smem_addr(bs) + st * NW * step + kb * PLANE, step,
+                                    (int)(min(KB, kr - kb * KB) / 16), idesc, kb != 0);
                 tc_commit(&b_empty[st]);
                 tc_commit(&d_full[u & 1]);
             }
@@ -790,7 +824,7 @@ template <int XK, int NX, int NW> cudaError_t launch_shrink(LoraParams p, unsign
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(ST);
-    cfg.dynamicSmemBytes = shrink_shape<XK, NX, NW>(p.max_rank).smem;
+    cfg.dynamicSmemBytes = shrink_shape<XK, NW>(p.max_rank).smem;
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
