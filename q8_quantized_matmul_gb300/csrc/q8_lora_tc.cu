@@ -12,11 +12,16 @@
 // weight of two, and a product of two bf16 is exact in the fp32 accumulators.  Terms below 2^-24 of the
 // product are left out.  The first terms' products and the rest are summed apart, for the tensor cores drop what is shifted
 // out of a sum.  bf16 x takes one term, fp16 x two (one and kind f16 with fp16 adapters).
+#include <cstring>
+
 #include "q8_launch.h"
 #include "q8_lora.cuh"
 #include "q8_tcgen05.cuh"
 
 namespace q8 {
+
+bool encode_rows32_tmap(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, uint64_t row_stride);
+
 namespace {
 
 constexpr uint32_t TM = 128;              // tokens of a tile
@@ -560,8 +565,10 @@ __global__ void __launch_bounds__(ST, 1) k_lora_shrink(const LoraParams p) {
 }
 
 // ---------------------------------------------------------------- expand
-// base comes into a ring of slots of 32 tokens by 128 outputs (512-byte pieces of rows, asynchronous copies), the products are
-// added on the way out.  What is in flight does not depend on the registers of the warps that add.
+// base comes into a ring of slots of 32 tokens by 128 outputs (512-byte pieces of rows), the products are added in the slot or on
+// the way out.  What is in flight does not depend on the registers of the warps that add.  With TMA (rows that start on 16-byte
+// boundaries) the copy engine gathers and scatters the rows four at a time: through the load-store unit a slot's 16-byte copies
+// and 4-byte stores took about as long as its bytes take from memory (4096 x 4096 outputs: 36 us).
 //   warps 0-15   four groups of four, slots in turn: slot + product -> out
 //   warps 16-17  base -> slots, in turn
 //   warp 18      products
@@ -584,6 +591,9 @@ template <int NW> __host__ __device__ constexpr ExpandShape expand_shape(uint32_
     s.smem = fixed + s.slots * SLOT;
     return s;
 }
+
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
 
 // A CTA's share of the line of (tile, 128 outputs), one after another.
 struct Units {
@@ -616,8 +626,31 @@ struct Units {
     }
 };
 
-// WHOLE: rows of base start on 16-byte boundaries and have whole 16 bytes.
-template <int NW, bool WHOLE> __global__ void __launch_bounds__(ET, 1) k_lora_expand(const LoraParams p) {
+// Four rows' pieces of 128 values, from column x on, global -> shared (2 KB, counted on bar) and back.
+__device__ __forceinline__ void gather4(void *dst, const CUtensorMap *map, int x, const int (&r)[4], uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(
+            smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(smem_addr(bar))
+        : "memory");
+}
+__device__ __forceinline__ void scatter4(const CUtensorMap *map, int x, const int (&r)[4], const void *src) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile::scatter4.bulk_group [%0, {%1, %2, %3, %4, %5}], [%6];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(smem_addr(src))
+                 : "memory");
+}
+// Rows 4 lane .. 4 lane + 3 of a slot's tokens (lane l holds token l).
+__device__ __forceinline__ void four_rows(int (&r)[4], uint32_t tok) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r[j] = (int)__shfl_sync(0xffffffffu, tok, (4 * lane + j) & 31);
+}
+
+// TMA: rows of base and out start on 16-byte boundaries and have whole 16 bytes; tm_base, tm_out: their maps.
+template <int NW, bool TMA>
+__global__ void __launch_bounds__(ET, 1) k_lora_expand(const LoraParams p, const __grid_constant__ CUtensorMap tm_base,
+                                                       const __grid_constant__ CUtensorMap tm_out) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort_flag;
@@ -628,6 +661,10 @@ template <int NW, bool WHOLE> __global__ void __launch_bounds__(ET, 1) k_lora_ex
     const uint32_t cols_max = round16(p.max_rank), step = sh.kbs * PLANE;
     uint8_t *bs = smem + 3 * step, *ring = bs + sh.b_stages * NW * step;
     if (t == 0) {
+        if (TMA) {
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_base)) : "memory");
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_out)) : "memory");
+        }
         for (uint32_t i = 0; i < MAX_SLOTS; ++i) {
             mbar_init(&full[i], 32);
             mbar_init(&empty[i], 4);
@@ -651,6 +688,14 @@ template <int NW, bool WHOLE> __global__ void __launch_bounds__(ET, 1) k_lora_ex
     if (warp < E_COPY0) {
         const uint32_t group = warp >> 2, q = warp & 3, col = q * 32 + lane, out_step = (uint32_t)p.out_stride * 4;
         uint32_t n = 0, u = 0;                               // slots and products so far
+        int sent = -1;                                       // the slot that the copy engine may still read (warp q = 0)
+        const auto release_sent = [&] {
+            if (sent < 0) return;
+            bulk_wait_read<0>();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[sent]);
+            sent = -1;
+        };
         for (Units w(p); w.live(); w.next(p)) {
             const uint32_t count = w.T.z, o = w.chunk * OM + col;
             const bool product = w.T.x != NO_ADAPTER;
@@ -659,8 +704,10 @@ template <int NW, bool WHOLE> __global__ void __launch_bounds__(ET, 1) k_lora_ex
             bool ready = !product;
             for (uint32_t s0 = 0; s0 < count; s0 += SLOT_TOK, ++n) {
                 if (n % E_GROUPS != group) continue;
+                if (TMA) release_sent();
                 const uint32_t slot = n % sh.slots, rows = min(SLOT_TOK, count - s0);
-                const float *f = reinterpret_cast<const float *>(ring + slot * SLOT) + col;
+                const uint32_t sent_rows = TMA && all ? rows & ~3u : 0;   // rows that leave from the slot; the others from here
+                float *f = reinterpret_cast<float *>(ring + slot * SLOT) + col;
                 const uint32_t tok = lane < rows ? p.perm[w.T.y + s0 + lane] : 0;
                 if (!ready) {
                     wait(&d_full[u & 1], (u / 2) & 1);
@@ -668,34 +715,54 @@ template <int NW, bool WHOLE> __global__ void __launch_bounds__(ET, 1) k_lora_ex
                     ready = true;
                 }
                 wait(&full[slot], (n / sh.slots) & 1);
+                if (product || !p.base || sent_rows < rows) {   // else the slot leaves as it came
 #pragma unroll
-                for (uint32_t h = 0; h < SLOT_TOK; h += 16) {
-                    uint32_t d[16];
-                    float y[16];
-                    if (product) tc_ld16(tmem + (u & 1) * TM + (q << 21) + s0 + h, d);
+                    for (uint32_t h = 0; h < SLOT_TOK; h += 16) {
+                        if (h >= rows) break;
+                        uint32_t d[16];
+                        float y[16];
+                        if (product) tc_ld16(tmem + (u & 1) * TM + (q << 21) + s0 + h, d);
 #pragma unroll
-                    for (uint32_t e = 0; e < 16; ++e) y[e] = p.base ? f[(h + e) * OM] : 0.0f;
-                    if (product) {
-                        tc_wait_ld();
-                        tc_regs_ready(d);
+                        for (uint32_t e = 0; e < 16; ++e) y[e] = p.base ? f[(h + e) * OM] : 0.0f;
+                        if (product) {
+                            tc_wait_ld();
+                            tc_regs_ready(d);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) y[e] += __uint_as_float(d[e]);
-                    }
-                    if (h) {
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&empty[slot]);
-                    }
-                    if (all && rows == SLOT_TOK) {
+                            for (int e = 0; e < 16; ++e) y[e] += __uint_as_float(d[e]);
+                        }
+                        if (sent_rows >= h + 16) {
 #pragma unroll
-                        for (uint32_t e = 0; e < 16; ++e)
-                            *reinterpret_cast<float *>(to + (uint64_t)__shfl_sync(0xffffffffu, tok, h + e) * out_step) = y[e];
-                    } else {
+                            for (uint32_t e = 0; e < 16; ++e) f[(h + e) * OM] = y[e];
+                        } else if (all && rows == SLOT_TOK) {
 #pragma unroll
-                        for (uint32_t e = 0; e < 16; ++e) {
-                            const uint32_t row = __shfl_sync(0xffffffffu, tok, h + e);
-                            if (h + e < rows && o < p.out_dim) *reinterpret_cast<float *>(to + (uint64_t)row * out_step) = y[e];
+                            for (uint32_t e = 0; e < 16; ++e)
+                                *reinterpret_cast<float *>(to + (uint64_t)__shfl_sync(0xffffffffu, tok, h + e) * out_step) = y[e];
+                        } else {
+#pragma unroll
+                            for (uint32_t e = 0; e < 16; ++e) {
+                                const uint32_t row = __shfl_sync(0xffffffffu, tok, h + e);
+                                if (h + e < sent_rows) f[(h + e) * OM] = y[e];
+                                else if (h + e < rows && o < p.out_dim) *reinterpret_cast<float *>(to + (uint64_t)row * out_step) = y[e];
+                            }
                         }
                     }
+                }
+                if (sent_rows) {
+                    fence_async_smem();
+                    named_bar_sync(1 + (int)group, 128);
+                    if (q == 0) {
+                        int r[4];
+                        four_rows(r, tok);
+                        if (lane < sent_rows / 4) scatter4(&tm_out, (int)(w.chunk * OM), r, ring + slot * SLOT + lane * 4 * OM * 4);
+                        bulk_commit();
+                        sent = (int)slot;
+                        // with one slot a group its next one waits for this
+                        if (sh.slots < 2 * E_GROUPS) release_sent();
+                    }
+                }
+                if (!sent_rows || q != 0) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&empty[slot]);
                 }
             }
             if (product) {
@@ -706,8 +773,9 @@ template <int NW, bool WHOLE> __global__ void __launch_bounds__(ET, 1) k_lora_ex
                 ++u;
             }
         }
+        if (TMA) release_sent();
     } else if (warp < E_COPY0 + E_COPIES) {
-        uint32_t n = 0;
+        uint32_t n = 0, filled = 0;                          // slots so far; those that the copy engine has written
         for (Units w(p); w.live(); w.next(p)) {
             const uint32_t count = w.T.z, o0 = w.chunk * OM, width = min(OM, p.out_dim - o0);
             for (uint32_t s0 = 0; s0 < count; s0 += SLOT_TOK, ++n) {
@@ -715,6 +783,19 @@ template <int NW, bool WHOLE> __global__ void __launch_bounds__(ET, 1) k_lora_ex
                 const uint32_t slot = n % sh.slots, rows = min(SLOT_TOK, count - s0), uses = n / sh.slots;
                 const uint32_t tok = p.base && lane < rows ? p.perm[w.T.y + s0 + lane] : 0;
                 if (uses) wait(&empty[slot], (uses - 1) & 1);
+                if (TMA && p.base && width == OM) {
+                    // whole groups of four rows; a last group reads some row again
+                    const uint32_t first = __shfl_sync(0xffffffffu, tok, 0);
+                    int r[4];
+                    four_rows(r, lane < rows ? tok : first);
+                    const uint32_t groups = (rows + 3) / 4;
+                    if (lane == 0) mbar_arrive_expect_tx(&full[slot], groups * 4 * OM * 4);
+                    else mbar_arrive(&full[slot]);
+                    __syncwarp();
+                    if (lane < groups && !abort_flag) gather4(ring + slot * SLOT + lane * 4 * OM * 4, &tm_base, (int)o0, r, &full[slot]);
+                    filled |= 1u << slot;
+                    continue;
+                }
                 if (p.base) {
                     const uint32_t dst = smem_addr(ring + slot * SLOT);
                     const float *base = p.base + o0;
@@ -723,7 +804,7 @@ template <int NW, bool WHOLE> __global__ void __launch_bounds__(ET, 1) k_lora_ex
                     for (uint32_t e = 0; e < rows; ++e) {
                         const float *src = reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(base) +
                                                                            (uint64_t)__shfl_sync(0xffffffffu, tok, e) * base_step);
-                        if constexpr (WHOLE) {
+                        if constexpr (TMA) {
                             if (lane * 4 < width) cp_async16_part(dst + e * OM * 4 + lane * 16, src + lane * 4, 16);
                         } else {
 #pragma unroll
@@ -736,6 +817,11 @@ template <int NW, bool WHOLE> __global__ void __launch_bounds__(ET, 1) k_lora_ex
             }
         }
         cp_async_wait<0>();                                  // nothing lands after the CTA has gone
+        if (TMA && abort_flag && filled) {                   // only an expired wait leaves gathered slots unread
+            const uint64_t t_end = global_timer_ns() + WAIT_LIMIT_NS;
+            for (uint32_t i = 0; i < sh.slots; ++i)
+                if (filled >> i & 1u) mbar_drain(&full[i], ((n - 1 - i) / sh.slots) & 1, t_end);
+        }
     } else if (warp == E_MMA) {
         uint32_t u = 0;
         for (Units w(p); w.live(); w.next(p)) {
@@ -841,15 +927,31 @@ template <int XK, int NX, int NW> cudaError_t launch_shrink(LoraParams p, unsign
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
-template <int NW, bool WHOLE> cudaError_t launch_expand_rows(const LoraParams &p, int num_sms, cudaStream_t st) {
+template <int NW, bool TMA>
+cudaError_t launch_expand_rows(const LoraParams &p, const CUtensorMap &tm_base, const CUtensorMap &tm_out, int num_sms, cudaStream_t st) {
     static SmemAllowed allowed;
-    const cudaError_t e = allow_smem(allowed, reinterpret_cast<const void *>(k_lora_expand<NW, WHOLE>), SMEM_MOST);
+    cudaError_t e = allow_smem(allowed, reinterpret_cast<const void *>(k_lora_expand<NW, TMA>), SMEM_MOST);
     if (e != cudaSuccess) return e;
-    return launch_dependent(k_lora_expand<NW, WHOLE>, p, dim3((unsigned)num_sms), ET, expand_shape<NW>(p.max_rank).smem, st);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)num_sms);
+    cfg.blockDim = dim3(ET);
+    cfg.dynamicSmemBytes = expand_shape<NW>(p.max_rank).smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, k_lora_expand<NW, TMA>, p, tm_base, tm_out);
+    return e == cudaSuccess ? cudaGetLastError() : e;
 }
 template <int NW> cudaError_t launch_expand(const LoraParams &p, int num_sms, cudaStream_t st) {
-    const bool whole = p.out_dim % 4 == 0 && p.base_stride % 4 == 0;
-    return whole ? launch_expand_rows<NW, true>(p, num_sms, st) : launch_expand_rows<NW, false>(p, num_sms, st);
+    CUtensorMap base, out;
+    if (p.out_dim % 4 == 0 && encode_rows32_tmap(&out, p.out, p.out_dim, p.n_tok, p.out_stride) &&
+        encode_rows32_tmap(&base, p.base ? p.base : p.out, p.out_dim, p.n_tok, p.base ? p.base_stride : p.out_stride))
+        return launch_expand_rows<NW, true>(p, base, out, num_sms, st);
+    memset(&base, 0, sizeof base);
+    return launch_expand_rows<NW, false>(p, base, base, num_sms, st);
 }
 
 // The most tiles that a call can have.
