@@ -866,9 +866,11 @@ __global__ void __launch_bounds__(ET, 1) k_lora_expand(const LoraParams p, const
 #pragma unroll 4
                 for (uint32_t i = b; i < (uint32_t)w.T.z * 3 * row_chunks; i += B_THREADS) {
                     const uint32_t c = i % row_chunks, rj = i / row_chunks, j = rj % 3, r = rj / 3;
-                    *reinterpret_cast<uint4 *>(smem + j * step + c / 8 * PLANE + swizzled(r, c % 8)) =
-                        __ldg(reinterpret_cast<const uint4 *>(p.low + ((uint64_t)(w.T.y + r) * 3 + j) * cols_max + c * 8));
+                    cp_async16(smem_addr(smem + j * step + c / 8 * PLANE + swizzled(r, c % 8)),
+                               p.low + ((uint64_t)(w.T.y + r) * 3 + j) * cols_max + c * 8, true);
                 }
+                cp_async_commit();
+                cp_async_wait<0>();
             }
             for (uint32_t c = b % 8;; c += 8) {
                 if (c * 8 < kr) {
