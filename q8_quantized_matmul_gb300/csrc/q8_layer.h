@@ -48,7 +48,8 @@ struct LoraParams {
     int4 *tiles, *groups;
     uint32_t *perm;
     uint16_t *low;
-    uint32_t shrink_cluster;              // CTAs that share a tile of tokens (set by the launcher)
+    uint32_t shrink_cluster;              // CTAs that share a tile of tokens (set by the launcher), and
+    bool x_tma;                           // whether x's rows come through the copy engine
 };
 constexpr uint32_t LORA_MAX_RANK = 128, LORA_MAX_ADAPTERS = 16384;
 // Few tokens take launch_lora, which searches the tokens of an adapter anew in every CTA and reads the weights again for each

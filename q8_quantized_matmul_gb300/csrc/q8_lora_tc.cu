@@ -20,6 +20,7 @@
 
 namespace q8 {
 
+bool encode_gather_tmap(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, uint64_t row_stride, uint32_t size);
 bool encode_rows32_tmap(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, uint64_t row_stride);
 
 namespace {
@@ -275,10 +276,20 @@ __device__ __forceinline__ bool cluster_bar_wait(uint64_t *bar, uint32_t parity,
     }
 }
 
-// One K step of x and of the weights, as they lie in memory, by the copying warps (thread b of 128).
+// Four rows' boxes, from column x on, global -> shared (counted on bar).
+__device__ __forceinline__ void gather4(void *dst, const CUtensorMap *map, int x, const int (&r)[4], uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(
+            smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(smem_addr(bar))
+        : "memory");
+}
+// One K step of x and of the weights, as they lie in memory, by the copying warps (thread b of 128).  fp32 rows lie in two tiles of
+// 32 values, 16-bit ones in one of 64: 128 bytes a row, 16-byte chunks swizzled by row.  With x_tma four rows a time come through
+// the copy engine (`full` counts them).
 template <int XK>
-__device__ __forceinline__ void copy_raw(const LoraParams &p, uint8_t *raw, const uint16_t *a, uint32_t rank, const uint32_t *toks, uint32_t count,
-                                         uint32_t k0, uint32_t b) {
+__device__ __forceinline__ void copy_raw(const LoraParams &p, const CUtensorMap *tm_x, uint8_t *raw, const uint16_t *a, uint32_t rank,
+                                         const uint32_t *toks, uint32_t count, uint32_t k0, uint32_t b, uint64_t *full) {
     const uint32_t x_dst = smem_addr(raw), w_dst = x_dst + TM * RAW_PITCH<XK>;
     const uint32_t left = min(KB, p.in_dim - k0);            // 32 or 64 values
     if constexpr (XK == X_Q8) {
@@ -290,14 +301,28 @@ __device__ __forceinline__ void copy_raw(const LoraParams &p, uint8_t *raw, cons
             const uint64_t s = ((uint64_t)toks[row] * (p.in_dim / QK) + k0 / QK) * QB, at = (s & ~(uint64_t)3) + 4 * w, end = s + left / QK * QB;
             cp_async4_part(x_dst + row * RAW_PITCH<XK> + 4 * w, x + (at < end ? at : 0), at < end ? (uint32_t)min((uint64_t)4, end - at) : 0u);
         }
+        if (b == 0) mbar_arrive(full);
+    } else if (p.x_tma) {
+        constexpr uint32_t HALVES = XK == X_F32 ? 2 : 1;
+        const uint32_t groups = (count + 3) / 4, halves = XK == X_F32 ? left / 32 : 1;
+        if (b == 0) mbar_arrive_expect_tx(full, groups * halves * 512);
+        const uint32_t g = b / 32 * 8 + b % 8, h = b % 32 / 8;
+        if (h < HALVES && h < halves && g < groups) {
+            int r[4];
+#pragma unroll
+            for (uint32_t j = 0; j < 4; ++j) r[j] = (int)toks[4 * g + j < count ? 4 * g + j : 0];
+            gather4(raw + h * PLANE + g * 512, tm_x, (int)(k0 + 32 * h), r, full);
+        }
+        __syncwarp();
     } else {
+        if (b == 0) mbar_arrive(full);
         constexpr uint32_t SIZE = XK == X_F32 ? 4 : 2, LANES = KB * SIZE / 16;   // threads of a row
         const uint32_t c = b % LANES;
         const bool in = c * 16 < left * SIZE;
         const uint8_t *x = static_cast<const uint8_t *>(p.x) + ((uint64_t)k0 * SIZE + (in ? c * 16 : 0));
 #pragma unroll 8
         for (uint32_t row = b / LANES; row < count; row += COPY / LANES)
-            cp_async16_part(x_dst + row * RAW_PITCH<XK> + ((c ^ (row & 7u)) << 4), x + (uint64_t)toks[row] * p.x_stride * SIZE, in ? 16 : 0);
+            cp_async16_part(x_dst + c / 8 * PLANE + swizzled(row, c % 8), x + (uint64_t)toks[row] * p.x_stride * SIZE, in ? 16 : 0);
     }
     const uint32_t c = b % 8;
     const bool in = c * 8 < left;
@@ -327,9 +352,12 @@ __device__ __forceinline__ void convert(const LoraParams &p, uint32_t x_tmem, ui
             for (int e = 0; e < 4; ++e) q[e] = in ? blk[1 + 8 * i + 2 * e] | (uint32_t)blk[2 + 8 * i + 2 * e] << 16 : 0u;
         }
     } else {
-        constexpr uint32_t N = XK == X_F32 ? 8 : 4;          // 16-byte pieces of 32 values
+        const bool in = k0 + half * 32 < p.in_dim;
 #pragma unroll
-        for (uint32_t i = 0; i < N; ++i) x[i] = *reinterpret_cast<const uint4 *>(raw + row * RAW_PITCH<XK> + (((half * N + i) ^ (row & 7u)) << 4));
+        for (uint32_t i = 0; i < (XK == X_F32 ? 8u : 4u); ++i) {   // 16-byte pieces of 32 values
+            x[i] = *reinterpret_cast<const uint4 *>(raw + (XK == X_F32 ? half * PLANE + swizzled(row, i) : swizzled(row, half * 4 + i)));
+            if (!in) x[i] = make_uint4(0, 0, 0, 0);
+        }
     }
 #pragma unroll
     for (uint32_t i = 0; i < WROWS; ++i) {
@@ -387,7 +415,7 @@ __device__ __forceinline__ void convert(const LoraParams &p, uint32_t x_tmem, ui
 }
 
 template <int XK, int NX, int NW>
-__global__ void __launch_bounds__(ST, 1) k_lora_shrink(const LoraParams p) {
+__global__ void __launch_bounds__(ST, 1) k_lora_shrink(const LoraParams p, const __grid_constant__ CUtensorMap tm_x) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort_flag;
@@ -401,7 +429,7 @@ __global__ void __launch_bounds__(ST, 1) k_lora_shrink(const LoraParams p) {
     const uint32_t cols_max = round16(p.max_rank), w_step = cols_max * 128;
     if (t == 0) {
         for (uint32_t i = 0; i < MAX_RAW; ++i) {
-            mbar_init(&raw_full[i], COPY);
+            mbar_init(&raw_full[i], COPY + 1);
             mbar_init(&raw_empty[i], GROUP / 32);
         }
         for (int i = 0; i < 2; ++i) {
@@ -445,7 +473,7 @@ __global__ void __launch_bounds__(ST, 1) k_lora_shrink(const LoraParams p) {
             for (uint32_t kb = kb0; kb < kb1; ++kb, ++n) {
                 const uint32_t r = n % sh.raws, use = n / sh.raws;
                 if (use) wait(&raw_empty[r], (use - 1) & 1);
-                copy_raw<XK>(p, ring + r * sh.raw, a, rank, tok, count, kb * KB, b);
+                copy_raw<XK>(p, &tm_x, ring + r * sh.raw, a, rank, tok, count, kb * KB, b, &raw_full[r]);
                 cp_async_arrive(&raw_full[r]);
             }
         } else if (warp == ST / 32 - 1) {
@@ -556,7 +584,13 @@ __global__ void __launch_bounds__(ST, 1) k_lora_shrink(const LoraParams p) {
         }
         ++tiles;
     }
-    if (warp >= CONVERT / 32 && warp < (CONVERT + COPY) / 32) cp_async_wait<0>();   // nothing lands after the CTA has gone
+    if (warp >= CONVERT / 32 && warp < (CONVERT + COPY) / 32) {
+        cp_async_wait<0>();                                  // nothing lands after the CTA has gone
+        if (p.x_tma && abort_flag) {                         // only an expired wait leaves raw slots unread
+            const uint64_t t_end = global_timer_ns() + WAIT_LIMIT_NS;
+            for (uint32_t i = 0; i < min(n, sh.raws); ++i) mbar_drain(&raw_full[i], ((n - 1 - i) / sh.raws) & 1, t_end);
+        }
+    }
     tc_fence_before();
     __syncthreads();
     if (warp == ST / 32 - 1) tmem_free(tmem, 512);
@@ -626,14 +660,6 @@ struct Units {
     }
 };
 
-// Four rows' pieces of 128 values, from column x on, global -> shared (2 KB, counted on bar) and back.
-__device__ __forceinline__ void gather4(void *dst, const CUtensorMap *map, int x, const int (&r)[4], uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(
-            smem_addr(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(smem_addr(bar))
-        : "memory");
-}
 __device__ __forceinline__ void scatter4(const CUtensorMap *map, int x, const int (&r)[4], const void *src) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile::scatter4.bulk_group [%0, {%1, %2, %3, %4, %5}], [%6];" ::"l"(
                      reinterpret_cast<uint64_t>(map)),
@@ -925,7 +951,10 @@ template <int XK, int NX, int NW> cudaError_t launch_shrink(LoraParams p, unsign
         if (tiles <= (unsigned)fit || p.shrink_cluster == 4) break;
     }
     cfg.gridDim = dim3((tiles < (unsigned)fit ? tiles : (unsigned)fit) * p.shrink_cluster);
-    e = cudaLaunchKernelEx(&cfg, k_lora_shrink<XK, NX, NW>, (const LoraParams)p);
+    CUtensorMap x;
+    memset(&x, 0, sizeof x);
+    p.x_tma = XK != X_Q8 && encode_gather_tmap(&x, p.x, p.in_dim, p.n_tok, p.x_stride, XK == X_F32 ? 4 : 2);
+    e = cudaLaunchKernelEx(&cfg, k_lora_shrink<XK, NX, NW>, (const LoraParams)p, (const CUtensorMap)x);
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 

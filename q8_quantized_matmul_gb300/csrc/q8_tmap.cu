@@ -111,6 +111,21 @@ bool encode_rows32_tmap(CUtensorMap *map, const void *base, uint64_t cols, uint6
     return r == CUDA_SUCCESS;
 }
 
+// Strided rows of fp32, fp16 or bf16 (size 4 or 2 bytes; only copied), a box of 128 bytes of one row with the 128-byte swizzle: the
+// gather of four rows at a time puts 16-byte chunk j of row r of its tile at chunk j ^ (r & 7).
+bool encode_gather_tmap(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, uint64_t row_stride, uint32_t size) {
+    if (!load_encoder()) return false;
+    if (rows == 0 || cols * size < 128 || (row_stride * size) % 16 || (reinterpret_cast<uintptr_t>(base) & 15u)) return false;
+    cuuint64_t dims[2] = {cols, rows};
+    cuuint64_t strides[1] = {row_stride * size};
+    cuuint32_t box[2] = {128 / size, 1};
+    cuuint32_t estr[2] = {1, 1};
+    const CUresult r = g_encode(map, size == 4 ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void *>(base), dims,
+                                strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 // fp32 rows cut into Q8_0 blocks: a [n_blocks][32] view of x (one 128-byte row
 // per block) with a box of box_blocks blocks and the 128-byte swizzle, so that in
 // shared memory the 16-byte chunk j of block b lies at chunk j ^ (b & 7) of the
