@@ -144,7 +144,7 @@ int q8_rmsnorm_quantize(void *xq, float *y, const float *x, const float *gamma, 
  *   residual_scale  finite;  eps > 0 and finite.
  * dim % 32 == 0, at most 32768.  Strides are elements, multiples of 8, at least dim (gate:
  * a multiple of 4, or 0); pointers 16-byte aligned.  h_out and n_out must not overlap y,
- * gate or the gammas, nor each other.  NaN and infinities stay in their row.
+ * gate, the gammas or each other, n_out not h.  NaN and infinities stay in their row.
  */
 int q8_residual_norm(void *n_out, int n_type, void *h_out, uint64_t h_out_stride, const void *h, int h_type,
                      uint64_t h_stride, const void *y, int y_type, uint64_t y_stride, int post, const float *gamma_post,
@@ -496,10 +496,13 @@ int q8_kv_read(void *k_out, uint64_t k_stride, void *v_out, uint64_t v_stride, i
  *              during the call.
  *   adapter_of in: int32 [n_tok], in any order (tokens of one adapter need not be neighbours).
  * x, the rank-sized sums and all other sums keep fp32 accuracy (24 bits of every x and of every
- * rank-sized sum take part in the products, which are exact, sums in fp32); a value beyond 2^127
- * or not finite makes its token's row not finite.  An id of n_adapters or beyond counts as negative, a
- * rank outside its range is cut to it; both raise Q8_ERANGE.  Pointers are 16-byte aligned (the id, rank
- * and scale arrays 4-byte).
+ * rank-sized sum take part in the products, which are exact; sums in fp32, in an order that goes by
+ * the number of tokens and the adapters' shares of them, not by the tokens' order).  A value of x or
+ * of an adapter that is not finite spoils the tokens that it belongs to, no others.  An id of
+ * n_adapters or beyond counts as negative, a rank outside its range is cut to it (of an adapter that
+ * a token has); both raise Q8_ERANGE.  Pointers are 16-byte aligned (the id, rank and scale arrays
+ * 4-byte), strides of out and base below 2^30.  out must not overlap x or the adapters.  A few tokens
+ * are one launch without scratch; many (more than 64, or 128 of small ranks) use the library's scratch.
  */
 typedef struct q8_adapters {
     const void *a, *b;       /* device */
@@ -671,7 +674,8 @@ void q8_debug_fail_next_alloc(int count);
  * q8_rmsnorm_quantize runs for rows of at most 4096 values and at least 12
  * rows per SM, and the tcgen05 kernels of q8_attn_prompt and, for 16-bit
  * caches with more than 16 query heads of 256 or 512 values on a key-value
- * head and room for more than 256 positions, of q8_attn_decode) run with every wait limited to
+ * head and room for more than 256 positions, of q8_attn_decode, and the first tcgen05 kernel of
+ * q8_lora) run with every wait limited to
  * limit_ns nanoseconds (0: the normal 2 s) and with their producer issuing no
  * copy at all, so the consumers wait on buffers that never fill.  Each such
  * kernel then raises Q8_ETIMEOUT for q8_last_error(), stops waiting, lets any

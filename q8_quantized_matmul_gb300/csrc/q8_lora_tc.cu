@@ -12,6 +12,7 @@
 // weight of two, and a product of two bf16 is exact in the fp32 accumulators.  Terms below 2^-24 of the
 // product are left out.  The first terms' products and the rest are summed apart, for the tensor cores drop what is shifted
 // out of a sum.  bf16 x takes one term, fp16 x two (one and kind f16 with fp16 adapters).
+#include <atomic>
 #include <cstring>
 
 #include "q8_launch.h"
@@ -235,6 +236,9 @@ template <int XK, int NW> __host__ __device__ constexpr ShrinkShape shrink_shape
     if (s.raws > MAX_RAW) s.raws = MAX_RAW;
     s.raws &= ~1u;                                           // a raw slot stays with one group, so none runs a phase of it ahead
     s.smem = 1024 + s.body + s.raws * s.raw;
+    // Never two CTAs on an SM: each takes all of TMEM, and one that waits for it while its cluster waits for it could hold up a
+    // cluster that the other CTA's cluster waits for.
+    if (s.smem < 116 * 1024) s.smem = 116 * 1024;
     return s;
 }
 // TMEM columns: sums of the first terms' products at 0, of the others at REST, two stages of x terms (32 columns a term).
@@ -454,7 +458,8 @@ __global__ void __launch_bounds__(ST, 1) k_lora_shrink(const LoraParams p, const
     const uint32_t tmem = tmem_slot;
     const int n_tiles = p.tiles[0].x, clusters = (int)(gridDim.x / SC);
     const uint32_t nb = (p.in_dim + KB - 1) / KB, kb0 = nb * k / SC, kb1 = nb * (k + 1) / SC;
-    const auto wait = [&](uint64_t *bar, uint32_t parity) { return tile_wait(bar, parity, p.err, &abort_flag); };
+    const uint64_t lim = wait_limit(p.wait_ns);
+    const auto wait = [&](uint64_t *bar, uint32_t parity) { return tile_wait(bar, parity, p.err, &abort_flag, lim); };
     uint32_t n = 0;                                          // K steps so far
     int tiles = 0;                                           // tiles so far
     for (int tile = (int)(blockIdx.x / SC); tile < n_tiles; tile += clusters) {
@@ -473,6 +478,7 @@ __global__ void __launch_bounds__(ST, 1) k_lora_shrink(const LoraParams p, const
             for (uint32_t kb = kb0; kb < kb1; ++kb, ++n) {
                 const uint32_t r = n % sh.raws, use = n / sh.raws;
                 if (use) wait(&raw_empty[r], (use - 1) & 1);
+                if (p.withhold) continue;                    // the failure-detection test hook
                 copy_raw<XK>(p, &tm_x, ring + r * sh.raw, a, rank, tok, count, kb * KB, b, &raw_full[r]);
                 cp_async_arrive(&raw_full[r]);
             }
@@ -586,7 +592,7 @@ __global__ void __launch_bounds__(ST, 1) k_lora_shrink(const LoraParams p, const
     }
     if (warp >= CONVERT / 32 && warp < (CONVERT + COPY) / 32) {
         cp_async_wait<0>();                                  // nothing lands after the CTA has gone
-        if (p.x_tma && abort_flag) {                         // only an expired wait leaves raw slots unread
+        if (p.x_tma && abort_flag && !p.withhold) {          // only an expired wait leaves raw slots unread
             const uint64_t t_end = global_timer_ns() + WAIT_LIMIT_NS;
             for (uint32_t i = 0; i < min(n, sh.raws); ++i) mbar_drain(&raw_full[i], ((n - 1 - i) / sh.raws) & 1, t_end);
         }
@@ -942,12 +948,19 @@ template <int XK, int NX, int NW> cudaError_t launch_shrink(LoraParams p, unsign
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    int fit = 0;
+    int dev = -1, fit = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    static std::atomic<int> fits[2][64];                     // clusters of 8 and of 4 that fit on a device, asked for once
     for (p.shrink_cluster = SC_MOST;; p.shrink_cluster /= 2) {
-        cfg.gridDim = dim3((unsigned)num_sms / p.shrink_cluster * p.shrink_cluster);
+        std::atomic<int> *known = dev >= 0 && dev < 64 ? &fits[p.shrink_cluster == 4][dev] : nullptr;
         attr[1].val.clusterDim.x = p.shrink_cluster;
-        if ((e = cudaOccupancyMaxActiveClusters(&fit, k_lora_shrink<XK, NX, NW>, &cfg)) != cudaSuccess) return e;
-        if (fit < 1) fit = 1;
+        fit = known ? known->load(std::memory_order_relaxed) : 0;
+        if (fit < 1) {
+            cfg.gridDim = dim3((unsigned)num_sms / p.shrink_cluster * p.shrink_cluster);
+            if ((e = cudaOccupancyMaxActiveClusters(&fit, k_lora_shrink<XK, NX, NW>, &cfg)) != cudaSuccess) return e;
+            if (fit < 1) fit = 1;
+            if (known) known->store(fit, std::memory_order_relaxed);
+        }
         if (tiles <= (unsigned)fit || p.shrink_cluster == 4) break;
     }
     cfg.gridDim = dim3((tiles < (unsigned)fit ? tiles : (unsigned)fit) * p.shrink_cluster);

@@ -370,10 +370,12 @@ cudaError_t launch_rows(const ResidualNormParams &p, int h_type, int y_type, int
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    int fit = 0;
-    cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, (int)threads, 0);
-    if (e != cudaSuccess) return e;
-    if (fit < 1) fit = 1;
+    cudaError_t e = cudaSuccess;
+    int fit = 1;
+    if (p.n_tok > (uint64_t)num_sms) {
+        if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, (int)threads, 0)) != cudaSuccess) return e;
+        if (fit < 1) fit = 1;
+    }
     const uint64_t ctas = (uint64_t)num_sms * fit;
     cfg.gridDim = dim3((unsigned)(p.n_tok < ctas ? p.n_tok : ctas));
     e = cudaLaunchKernelEx(&cfg, kernel, p, h_type, y_type);

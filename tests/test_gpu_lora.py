@@ -1,4 +1,6 @@
 """GPU tests of q8_lora against its definition in 64 bits."""
+import time
+
 import numpy as np
 import pytest
 
@@ -204,3 +206,23 @@ def test_helper_refusals(q8):
         with pytest.raises((TypeError, ValueError, q8.Q8Error)):
             bad()
     assert q8.lora(x[:0], a, b, ids[:0]).shape == (0, 40)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_adapters_expired_wait_and_recovery(q8, dtype):
+    """The first tcgen05 kernel of q8_lora with its copies withheld: its clusters end with an error, and the next call is right."""
+    x = torch.randn(700, 1024, device=DEV).to(dtype)
+    a, b = (torch.randn(2, 16, 1024, device=DEV) / 32).bfloat16(), torch.randn(2, 256, 16, device=DEV).bfloat16()
+    ids = (torch.arange(700, device=DEV) % 2).int()
+    want = q8.lora(x, a, b, ids)
+    assert q8.q8_last_error() == 0
+    q8.q8_debug_expire_waits(1, 200_000)   # 0.2 ms instead of the normal 2 s
+    try:
+        t0 = time.perf_counter()
+        q8.lora(x, a, b, ids)
+        assert q8.q8_last_error() == q8.Q8_ETIMEOUT
+        assert time.perf_counter() - t0 < 1.5, "an expired wait did not end its kernel promptly"
+    finally:
+        q8.q8_debug_expire_waits(0, 0)
+    assert torch.equal(q8.lora(x, a, b, ids), want)
+    assert q8.q8_last_error() == 0
