@@ -1,17 +1,20 @@
 // q8_lora_tc.cu -- low-rank adapters of many tokens on the tensor cores: out[t] = base[t] + s_a B_a (A_a x[t]).
 //
-//   k_lora_route   one CTA orders the tokens by adapter and cuts them into tiles of up to 128 tokens of one adapter; adapters
-//                  with fewer than 16 tokens go to k_lora_groups (q8_lora.cu) instead.  The order inside an adapter is left to
+//   k_lora_route   one CTA orders the tokens by adapter and cuts them into tiles of up to 128 tokens of one adapter (or, where that
+//                  spares something, groups of 4 for k_lora_groups in q8_lora.cu).  The order inside an adapter is left to
 //                  chance: a token's result does not depend on its place in a tile or group.
-//   k_lora_shrink  a cluster of 8 CTAs a tile, each an eighth of in_dim: low = A x with the tokens along the rows of the
-//                  product.  The eighths are added through distributed shared memory in a fixed order.
+//   k_lora_shrink  a cluster of 8 or 4 CTAs a tile, each a part of in_dim: low = A x with the tokens along the rows of the
+//                  product.  The parts are added through distributed shared memory in a fixed order.
 //   k_lora_expand  tiles of 128 outputs (rows) by the tile's tokens (columns): a warp's lanes hold neighbouring outputs of one
 //                  token, so base and out are read and written in whole lines.
+// 4096 tokens of 4 adapters, 4096 to 4096, rank 64, fp32 x: route 6 us, groups 3 (nothing to do), shrink 29 (67 MB of x: 1.3 us a
+// K step of 32 KB on 128 SMs; with the terms, the products and the fence taken out 0.9, so the copies, the terms and their
+// stores each take part), expand 26 (134 MB: 5.2 TB/s).  2048 tokens, 1024 to 32768, rank 16: expand 90 (537 MB, 6.0 TB/s).
 //
 // fp32 accuracy from 16-bit products: an fp32 value is the exact sum of three bf16 terms (8 of its 24 bits each), an fp16
 // weight of two, and a product of two bf16 is exact in the fp32 accumulators.  Terms below 2^-24 of the
-// product are left out.  The first terms' products and the rest are summed apart, for the tensor cores drop what is shifted
-// out of a sum.  bf16 x takes one term, fp16 x two (one and kind f16 with fp16 adapters).
+// product are left out.  The first terms' products and the rest are summed apart, or the rest first, for the tensor cores drop what
+// is shifted out of a sum.  bf16 x takes one term, fp16 x two (one and kind f16 with fp16 adapters).
 #include <atomic>
 #include <cstring>
 
@@ -181,19 +184,21 @@ template <int N> __device__ __forceinline__ void terms_f16(uint4 (&out)[N], cons
 // Byte offset of 16-byte chunk c of row r in a tile of 128-byte rows, swizzled as the matrix descriptors say.
 __device__ __forceinline__ uint32_t swizzled(uint32_t r, uint32_t c) { return r * 128 + ((c ^ (r & 7u)) << 4); }
 
-// The products of one K step of 16 * ksteps values: weight terms (rows of the product) times low's three terms, those that reach
-// 2^-24, into one accumulator.  acc: whether it holds sums already.
+// A tile's products over kr values (rows: the weights', columns: low's three terms), those that reach 2^-24, into one accumulator.
+// The small ones come first: the tensor cores drop what is shifted out of a sum, so that only the steps of the first terms'
+// products, one for 16 values, cost bits of the result.
 template <int NW>
-__device__ __forceinline__ void issue_terms(uint32_t d, uint32_t low, uint32_t low_step, uint32_t w, uint32_t w_step, int ksteps, uint32_t idesc,
-                                            bool acc) {
+__device__ __forceinline__ void issue_terms(uint32_t d, uint32_t low, uint32_t w, uint32_t step, uint32_t kr, uint32_t idesc) {
+    bool acc = false;
 #pragma unroll
-    for (int i = 0; i < 3; ++i)
+    for (int small = 2; small >= 0; --small)
 #pragma unroll
         for (int j = 0; j < NW; ++j) {
-            if (i + j > 2) continue;
-            const uint64_t ld = sw128_desc(low + i * low_step), wd = sw128_desc(w + j * w_step);
-            for (int k = 0; k < ksteps; ++k) {
-                tc_mma_f16(d, wd + 2 * k, ld + 2 * k, idesc, acc);
+            const int i = small - j;
+            if (i < 0) continue;
+            for (uint32_t k = 0; k < kr; k += 16) {
+                const uint32_t at = k / KB * PLANE;
+                tc_mma_f16(d, sw128_desc(w + j * step + at) + k % KB / 8, sw128_desc(low + i * step + at) + k % KB / 8, idesc, acc);
                 acc = true;
             }
         }
@@ -241,8 +246,11 @@ template <int XK, int NW> __host__ __device__ constexpr ShrinkShape shrink_shape
     if (s.smem < 116 * 1024) s.smem = 116 * 1024;
     return s;
 }
-// TMEM columns: sums of the first terms' products at 0, of the others at REST, two stages of x terms (32 columns a term).
-constexpr uint32_t REST = 128, X_COLS = 256, X_STAGE = 96;
+// TMEM columns: the sums of the small terms' products, then up to four of the first terms' (the 16-value steps of a K step in turn:
+// the tensor cores drop what is shifted out of a sum, 4096 values in one accumulator cost 5e-7 of it), from X_COLS on two stages of x
+// terms (32 columns a term).
+constexpr uint32_t X_COLS = 320, X_STAGE = 96;
+__host__ __device__ constexpr uint32_t accumulators(uint32_t cols) { return cols <= 64 ? 4 : cols <= 96 ? 2 : 1; }
 
 // `bytes` of 16 or 4 global -> shared, the rest zeros.
 __device__ __forceinline__ void cp_async16_part(uint32_t dst, const void *src, uint32_t bytes) {
@@ -430,7 +438,7 @@ __global__ void __launch_bounds__(ST, 1) k_lora_shrink(const LoraParams p, const
     const ShrinkShape sh = shrink_shape<XK, NW>(p.max_rank);
     uint8_t *ring = smem + sh.body;
     const uint32_t t = threadIdx.x, warp = t >> 5, lane = t & 31u, k = cluster_rank(), SC = p.shrink_cluster;
-    const uint32_t cols_max = round16(p.max_rank), w_step = cols_max * 128;
+    const uint32_t cols_max = round16(p.max_rank), w_step = cols_max * 128, turn = accumulators(cols_max) - 1;
     if (t == 0) {
         for (uint32_t i = 0; i < MAX_RAW; ++i) {
             mbar_init(&raw_full[i], COPY + 1);
@@ -496,12 +504,14 @@ __global__ void __launch_bounds__(ST, 1) k_lora_shrink(const LoraParams p, const
 #pragma unroll
                         for (int j = 0; j < NW; ++j) {
                             if (i + j > 2) continue;
-                            // the first product of an accumulator starts it
-                            const bool starts = kb == kb0 && (i + j == 0 || (i == 0 && j == 1) || (NW == 1 && i == 1));
+                            const bool small = i + j > 0, first_small = (i == 0 && j == 1) || (NW == 1 && i == 1);
                             const uint64_t wd = sw128_desc(w + j * w_step);
 #pragma unroll
-                            for (int k = 0; k < (int)KB / 16; ++k)
-                                tc_mma_f16_ta(i + j ? tmem + REST : tmem, x + i * 32 + k * 8, wd + 2 * k, idesc, !(starts && k == 0));
+                            for (uint32_t k = 0; k < KB / 16; ++k) {
+                                // the first product of an accumulator starts it
+                                const bool starts = kb == kb0 && (small ? first_small && k == 0 : k <= turn);
+                                tc_mma_f16_ta(small ? tmem : tmem + (1 + (k & turn)) * cols_max, x + i * 32 + k * 8, wd + 2 * k, idesc, !starts);
+                            }
                         }
                     tc_commit(&st_empty[s]);
                     if (kb + 1 == kb1) tc_commit(&d_full);
@@ -531,26 +541,21 @@ __global__ void __launch_bounds__(ST, 1) k_lora_shrink(const LoraParams p, const
             named_bar_sync(2, CONVERT);
             const uint32_t row = (warp & 3) * 32 + lane;
             for (uint32_t c = (warp >> 2) * 16; c < cols; c += 16 * (CONVERT / 128)) {
-                uint32_t d0[16], d1[16];
+                float sum[16];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) d0[e] = d1[e] = 0;
-                if (kb0 < kb1) {
-                    const uint32_t at = tmem + ((warp & 3) << 21) + c;
-                    tc_ld16(at, d0);
-                    if constexpr (NX + NW > 2) tc_ld16(at + REST, d1);
-                    tc_wait_ld();
-                    tc_regs_ready(d0);
-                    tc_regs_ready(d1);
-                }
+                for (int e = 0; e < 16; ++e) sum[e] = 0.0f;
+                if (kb0 < kb1)
+                    for (uint32_t i = NX + NW > 2 ? 0 : 1; i <= 1 + turn; ++i) {   // the small ones first
+                        uint32_t d[16];
+                        tc_ld16(tmem + ((warp & 3) << 21) + i * cols_max + c, d);
+                        tc_wait_ld();
+                        tc_regs_ready(d);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) sum[e] += __uint_as_float(d[e]);
+                    }
 #pragma unroll
                 for (int e = 0; e < 16; e += 4) {
-                    float4 v = make_float4(__uint_as_float(d0[e]), __uint_as_float(d0[e + 1]), __uint_as_float(d0[e + 2]), __uint_as_float(d0[e + 3]));
-                    if constexpr (NX + NW > 2) {
-                        v.x += __uint_as_float(d1[e]);
-                        v.y += __uint_as_float(d1[e + 1]);
-                        v.z += __uint_as_float(d1[e + 2]);
-                        v.w += __uint_as_float(d1[e + 3]);
-                    }
+                    const float4 v = make_float4(sum[e], sum[e + 1], sum[e + 2], sum[e + 3]);
                     *reinterpret_cast<float4 *>(part + row * pitch + c + e) = v;
                 }
             }
@@ -785,7 +790,7 @@ __global__ void __launch_bounds__(ET, 1) k_lora_expand(const LoraParams p, const
                     if (q == 0) {
                         int r[4];
                         four_rows(r, tok);
-                        if (lane < sent_rows / 4) scatter4(&tm_out, (int)(w.chunk * OM), r, ring + slot * SLOT + lane * 4 * OM * 4);
+                        if (lane * 4 < sent_rows) scatter4(&tm_out, (int)(w.chunk * OM), r, ring + slot * SLOT + lane * 4 * OM * 4);
                         bulk_commit();
                         sent = (int)slot;
                         // with one slot a group its next one waits for this
@@ -864,9 +869,7 @@ __global__ void __launch_bounds__(ET, 1) k_lora_expand(const LoraParams p, const
             if (u >= 2) wait(&d_empty[u & 1], (u / 2 - 1) & 1);
             tc_fence_after();
             if (elect_one()) {
-                for (uint32_t kb = 0; kb * KB < kr; ++kb)
-                    issue_terms<NW>(tmem + (u & 1) * TM, smem_addr(smem) + kb * PLANE, step, smem_addr(bs) + st * NW * step + kb * PLANE, step,
-                                    (int)(min(KB, kr - kb * KB) / 16), idesc, kb != 0);
+                issue_terms<NW>(tmem + (u & 1) * TM, smem_addr(smem), smem_addr(bs) + st * NW * step, step, kr, idesc);
                 tc_commit(&b_empty[st]);
                 tc_commit(&d_full[u & 1]);
             }
@@ -936,7 +939,9 @@ template <int XK, int NX, int NW> cudaError_t launch_shrink(LoraParams p, unsign
     cudaError_t e = allow_smem(allowed, reinterpret_cast<const void *>(k_lora_shrink<XK, NX, NW>), SMEM_MOST);
     if (e != cudaSuccess) return e;
     // Clusters that fit at a time are fewer than SMs / CTAs (15 of 8, 36 of 4 on 152 SMs): more tiles than clusters of 8
-    // take clusters of 4.
+    // take clusters of 4 (4096 tokens with clusters of 8: three rounds, 52 us; of 4: one, 31).  Sums of over 96 columns have one
+    // accumulator, and stay with the shorter sums of clusters of 8.
+    const uint32_t least = accumulators(round16(p.max_rank)) > 1 ? 4 : 8;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -961,7 +966,7 @@ template <int XK, int NX, int NW> cudaError_t launch_shrink(LoraParams p, unsign
             if (fit < 1) fit = 1;
             if (known) known->store(fit, std::memory_order_relaxed);
         }
-        if (tiles <= (unsigned)fit || p.shrink_cluster == 4) break;
+        if (tiles <= (unsigned)fit || p.shrink_cluster == least) break;
     }
     cfg.gridDim = dim3((tiles < (unsigned)fit ? tiles : (unsigned)fit) * p.shrink_cluster);
     CUtensorMap x;
