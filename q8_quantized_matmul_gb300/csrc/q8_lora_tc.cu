@@ -7,7 +7,7 @@
 //                  product.  The parts are added through distributed shared memory in a fixed order.
 //   k_lora_expand  tiles of 128 outputs (rows) by the tile's tokens (columns): a warp's lanes hold neighbouring outputs of one
 //                  token, so base and out are read and written in whole lines.
-// 4096 tokens of 4 adapters, 4096 to 4096, rank 64, fp32 x: route 6 us, groups 3 (nothing to do), shrink 29 (67 MB of x: 1.3 us a
+// 4096 tokens of 4 adapters, 4096 to 4096, rank 64, fp32 x: route 6 us, shrink 29 (67 MB of x: 1.3 us a
 // K step of 32 KB on 128 SMs; with the terms, the products and the fence taken out 0.9, so the copies, the terms and their
 // stores each take part), expand 26 (134 MB: 5.2 TB/s).  2048 tokens, 1024 to 32768, rank 16: expand 90 (537 MB, 6.0 TB/s).
 //
@@ -40,7 +40,7 @@ constexpr int NO_ADAPTER = -1;
 constexpr int RT = 1024;
 
 struct Sums {
-    int tokens, tiles, groups;            // (first scan: adapters with enough tokens, tiles were all to have them, -)
+    int tokens, tiles, groups;            // (where groups are weighed: adapters with enough tokens, tiles were all to have them, -)
     __device__ __forceinline__ Sums operator+(const Sums &o) const { return {tokens + o.tokens, tiles + o.tiles, groups + o.groups}; }
 };
 __device__ __forceinline__ Sums shfl_up(const Sums &s, int o) {
@@ -111,13 +111,16 @@ __global__ void __launch_bounds__(RT) k_lora_route(const LoraParams p) {
     // what becomes of an adapter's tokens: tiles, groups, or (no adapter, or one of rank 0) tiles that copy base
     const int per = (n + RT - 1) / RT, b0 = min(n, (int)threadIdx.x * per), b1 = min(n, b0 + per);
     Sums mine = {0, 0, 0}, total;
-    for (int i = b0; i < b1; ++i)
-        if (i < n - 1 && counts[i]) mine = mine + Sums{counts[i] >= (int)LORA_TILE_MIN, (counts[i] + (int)TM - 1) / (int)TM, 0};
-    scan(mine, total, warps);
-    __syncthreads();
     // Groups spare a tile's work for few tokens, but are a kernel of their own: only where there are no tiles otherwise, or so
-    // many that they would wait for each other (333 tokens of 12 adapters: 33 us with both, see q8_layer.h)
-    const bool groups = total.tokens == 0 || total.tiles > (int)LORA_TILES_AT_ONCE;
+    // many that they would wait for each other
+    bool groups = false;
+    if (p.groups) {
+        for (int i = b0; i < b1; ++i)
+            if (i < n - 1 && counts[i]) mine = mine + Sums{counts[i] >= (int)LORA_TILE_MIN, (counts[i] + (int)TM - 1) / (int)TM, 0};
+        scan(mine, total, warps);
+        __syncthreads();
+        groups = total.tokens == 0 || total.tiles > (int)LORA_TILES_AT_ONCE;
+    }
     const auto kind = [&](int i, int c, int &rank) -> Sums {
         rank = c && i < n - 1 ? (int)rank_of(p, i, false) : 0;
         if (rank == 0) return {c, p.base == p.out ? 0 : (c + (int)TM - 1) / (int)TM, 0};
@@ -1026,7 +1029,10 @@ cudaError_t launch_lora_tc(const LoraParams &q, void *scratch, int num_sms, cuda
     uint8_t *at = static_cast<uint8_t *>(scratch);
     p.tiles = reinterpret_cast<int4 *>(at);
     at += list_bytes(1 + most_tiles(p.n_tok, p.n_adapters));
-    p.groups = reinterpret_cast<int4 *>(at);
+    // Where all tiles run at once in any case there are no groups, and no kernel for them (333 tokens of 12 adapters: 24.0 us, 26.3
+    // with it).
+    const bool groups = most_tiles(p.n_tok, p.n_adapters) > LORA_TILES_AT_ONCE;
+    p.groups = groups ? reinterpret_cast<int4 *>(at) : nullptr;
     at += list_bytes(most_groups(p.n_tok, p.n_adapters));
     p.perm = reinterpret_cast<uint32_t *>(at);
     at += up256((size_t)p.n_tok * 4);
@@ -1035,7 +1041,7 @@ cudaError_t launch_lora_tc(const LoraParams &q, void *scratch, int num_sms, cuda
     cudaError_t e = allow_smem(allowed, reinterpret_cast<const void *>(k_lora_route), (LORA_MAX_ADAPTERS + 1) * sizeof(int));
     if (e != cudaSuccess) return e;
     if ((e = launch_dependent(k_lora_route, p, dim3(1), RT, (p.n_adapters + 1) * sizeof(int), st)) != cudaSuccess) return e;
-    if ((e = launch_lora_groups(p, num_sms, st)) != cudaSuccess) return e;
+    if (groups && (e = launch_lora_groups(p, num_sms, st)) != cudaSuccess) return e;
     const uint64_t most = most_tiles(p.n_tok, p.n_adapters);
     const unsigned tiles = (unsigned)(most < 65536 ? most : 65536);
     const bool bf = p.bf16;
