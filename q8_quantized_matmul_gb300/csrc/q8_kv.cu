@@ -210,7 +210,7 @@ template <bool Q8> __global__ void __launch_bounds__(READ_THREADS) k_kv_read(con
         if (lo > 0 && lo <= p.n_seq) {
             const uint32_t s = lo - 1;
             const int32_t r = p.seqs ? p.seqs[s] : (int32_t)s;
-            const int64_t pos = (int64_t)(p.first ? p.first[s] : 0) + row - start[s];
+            const int64_t pos = (int64_t)(p.first ? p.first[s] : 0) + row - max(start[s], 0);
             const int64_t slot = pos >> p.c.page_shift;
             a = -1;
             if (r >= 0 && (uint32_t)r < p.n_rows && pos >= 0 && slot < p.max_pages) {

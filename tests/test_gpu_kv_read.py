@@ -111,6 +111,8 @@ def test_bad_pages_rows_and_starts(q8):
     assert rc == q8.Q8_ERANGE
     got, rc = call([[2, 3]], [2, 5], 5)                               # does not start at 0
     assert rc == q8.Q8_ERANGE and (got[:2] == 7).all() and torch.equal(got[2:].float(), torch.from_numpy(k[0, 2, 0, :3]))
+    got, rc = call([[2, 3]], [-4, 5], 5)                              # below 0: cut
+    assert rc == q8.Q8_ERANGE and torch.equal(got.float(), torch.from_numpy(k[0, 2, 0, :5]))
     assert call([[2, 3]], [0, 5], 5)[1] == 0
 
 
@@ -126,6 +128,20 @@ def test_far_positions_and_many_sequences(q8):
     for g, x in zip(got, (k, v)):
         assert np.array_equal(g.float().cpu().numpy()[:, 0], x[0, at, 0, first % 16])
     assert q8.q8_last_error() == 0
+
+
+def test_pools_and_rows_beyond_32_bits(q8):
+    page, kv, dim, pages = 256, 1, 256, 40000                         # 5.2 GB a pool
+    cache = q8.KVCache.empty(q8.Q8_TYPE_BF16, 1, pages, page, kv, dim)
+    table = [[39999, 0, 35000]]
+    want = torch.randn(3 * page, kv, dim, device=DEV).bfloat16()
+    for i, p in enumerate(table[0]):
+        cache.k[0, p].copy_(want[i * page:(i + 1) * page].view(-1).view(torch.uint8))
+    n, stride = 3 * page - 100, 1 << 22
+    rows = torch.empty(n * stride, dtype=torch.bfloat16, device=DEV).view(n, stride)[:, :dim].unsqueeze(1)
+    v = torch.empty(n, kv, dim, dtype=torch.bfloat16, device=DEV)
+    q8.kv_read(cache, 0, i32(table), i32([0, n]), n, first=i32([100]), out=(rows, v))
+    assert torch.equal(rows, want[100:]) and not v.any() and q8.q8_last_error() == 0
 
 
 @pytest.mark.parametrize("kind", ["bf16", "q8"])
