@@ -133,8 +133,8 @@ int q8_rmsnorm_quantize(void *xq, float *y, const float *x, const float *gamma, 
  * norm before the next block is that of the stored h'.
  *   n_out      out: [n_tok][dim] of n_type: Q8_TYPE_Q8_0 (blocks for q8_matmul_q, exactly
  *              the q8_quantize_act bytes of n), F32, F16 or BF16; NULL: only h'.
- *   h_out      out: rows h_out_stride apart, of h_type; may be h (with h's stride); NULL:
- *              h' is not stored (then n_out must be given).
+ *   h_out      out: rows h_out_stride apart, of h_type; may be h (with h's stride), else must
+ *              not overlap it; NULL: h' is not stored (then n_out must be given).
  *   h          in: the residual stream, F32, F16 or BF16, rows h_stride apart.
  *   y          in: the block's result, F32, F16 or BF16, rows y_stride apart.
  *   gamma_post, gamma_next  in: fp32 [dim], or NULL for all ones (gamma_post is used with
@@ -461,7 +461,8 @@ int q8_attn_prompt(void *out, int out_type, float *lse, const void *q, const voi
  * the values that the cache holds (Q8_0: d * q), rounded to out_type (to nearest even; cached
  * values of out_type are copied).
  *   k_out, v_out  out: F32, F16 or BF16 (out_type), rows of n_kv_heads heads, k_stride and
- *              v_stride elements apart (multiples of 8); either may be NULL.
+ *              v_stride elements apart (multiples of 8); either may be NULL.  They must not
+ *              overlap each other or the pools.
  *   seqs       in: int32 [n_seq], rows of `table` (n_rows of them), or NULL: row s.
  *   first      in: int32 [n_seq], or NULL: zeros.
  *   k_start    in: int32 [n_seq + 1], rising, from 0 to at most n_k; as in q8_attn_prompt, values
@@ -481,7 +482,8 @@ int q8_kv_read(void *k_out, uint64_t k_stride, void *v_out, uint64_t v_stride, i
  * adapter_of[t]:
  *   out[t][o] = base[t][o] + scales[a] * sum_{i < ranks[a]} B_a[o][i] * (sum_j A_a[i][j] x[t][j])
  * and out[t] = base[t] (zeros without a base) for a negative a.
- *   out        out: fp32, rows out_stride apart; may be base (with base's stride).
+ *   out        out: fp32, rows out_stride apart; may be base (with base's stride), else must not
+ *              overlap it.
  *   base       in: fp32, rows base_stride apart, or NULL: zeros.
  *   x          in: the projection's input, x_type F32, F16, BF16 (rows x_stride apart, in
  *              elements, a multiple of 8) or Q8_0 (the blocks that q8_matmul_q takes, rows

@@ -99,6 +99,51 @@ def test_who_has_which_adapter(q8, n, ids):
         assert not c.call(q8, base=None).any()
 
 
+def test_tiles_and_groups_of_many_tokens(q8):
+    """More tokens than one round of the ordering, adapters with many, few and single tokens: so many tiles that small shares go
+    in groups; and a full list of adapters."""
+    rng = np.random.default_rng(7)
+    n = 5300
+    ids = np.concatenate([rng.integers(0, 3, 4000), 3 + np.arange(600) // 15, 43 + np.arange(300) // 20, 58 + np.arange(200), np.full(200, -1)])
+    c = Case(7, n, 64, 136, 16, 258, "bf16", ids=rng.permutation(ids))
+    c.check(c.call(q8))
+    c = Case(8, 400, 32, 12, 8, 16384, "f16", "bf16")
+    c.check(c.call(q8))
+    assert q8.q8_last_error() == 0
+
+
+@pytest.mark.parametrize("n", [50, 130])
+def test_rows_far_apart(q8, n):
+    """Rows whose offsets pass 32 bits."""
+    stride = 1 << (25 if n < 100 else 24)
+    c = Case(n, n, 128, 256, 40, 3, "bf16")
+    x = torch.empty(n * stride, device=DEV).view(n, stride)[:, :128]
+    out = torch.empty(n * stride, device=DEV).view(n, stride)[:, 64:320]
+    x.copy_(c.x), out.copy_(torch.from_numpy(c.base))
+    c.check(c.call(q8, base=out, out=out) if n < 100 else
+            q8.lora(x, c.a.to(DEV), c.b.to(DEV), i32(c.ids), i32(c.ranks), torch.from_numpy(c.scales).to(DEV), out, out))
+
+
+def test_graphs_outlive_a_larger_call(q8):
+    """Two captured calls and a later one that needs more scratch: the replays still give their results."""
+    graphs = []
+    for n in (200, 333):
+        c = Case(n, n, 256, 200, 16, 3, "bf16")
+        x, a, b, ids, ranks = c.x.to(DEV), c.a.to(DEV), c.b.to(DEV), i32(c.ids), i32(c.ranks)
+        scales, base = torch.from_numpy(c.scales).to(DEV), torch.from_numpy(c.base).to(DEV)
+        q8.lora(x, a, b, ids, ranks, scales, base)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = q8.lora(x, a, b, ids, ranks, scales, base)
+        graphs.append((c, graph, out, (x, a, b, ids, ranks, scales, base)))
+    big = Case(1, 6000, 32, 64, 128, 2, "f16")
+    big.check(big.call(q8))
+    for c, graph, out, _ in graphs + graphs[::-1]:
+        out.zero_()
+        graph.replay()
+        c.check(out)
+
+
 @pytest.mark.parametrize("n", [2, 150])
 def test_without_base_scales_ranks(q8, n):
     c = Case(n, n, 512, 260, 16, 3, "f16", ragged=False, base=False)

@@ -79,6 +79,40 @@ def test_many_rows_and_no_gammas(q8, tokens):
     check(q8, n, "q8", want_n)
 
 
+@pytest.mark.parametrize("dim", [1024, 4128, 8192, 11232])
+@pytest.mark.parametrize("h,y,out", [("f32", "f32", "q8"), ("bf16", "f16", "bf16")])
+@pytest.mark.parametrize("shift", [0, 4])
+def test_more_rows_than_two_an_sm(q8, dim, h, y, out, shift):
+    """Every form for many rows; shift: rows that start between 32-byte boundaries (fp32)."""
+    rng = np.random.default_rng(dim)
+    n = 420
+    hv, yv = typed(rng, (n, dim), h, 3.0), typed(rng, (n, dim), y)
+    gp, gn = typed(rng, (dim,), "f32"), typed(rng, (dim + 4,), "f32")
+    store = lambda v: torch.from_numpy(v).to(DT[h]).float().numpy()
+    want_n, want_h = layer_plain.residual_norm(hv, yv, gn[shift:shift + dim], EPS, gp, True, store=store)
+    wide = torch.zeros(n, dim + 8, device=DEV, dtype=DT[h])
+    at = shift if h == "f32" else 2 * shift
+    wide[:, at:at + dim] = up(hv, h)
+    got_n, got_h = q8.residual_norm(wide[:, at:at + dim], up(yv, y), up(gn)[shift:shift + dim], EPS, gamma_post=up(gp), post=True,
+                                    out_type=code(q8, out))
+    assert np.array_equal(got_h.float().cpu().numpy(), want_h)
+    check(q8, got_n, out, want_n)
+
+
+def test_rows_far_apart(q8):
+    """Rows whose offsets pass 32 bits."""
+    rng = np.random.default_rng(2)
+    n, dim, stride = 80, 256, 1 << 24
+    hv, yv = typed(rng, (n, dim), "f32"), typed(rng, (n, dim), "bf16")
+    want_n, want_h = layer_plain.residual_norm(hv, yv, None, EPS)
+    h = torch.empty(n * stride, device=DEV).view(n, stride)[:, 8:8 + dim]
+    y = torch.empty(n * stride, device=DEV, dtype=torch.bfloat16).view(n, stride)[:, :dim]
+    h.copy_(up(hv)), y.copy_(up(yv, "bf16"))
+    got, _ = q8.residual_norm(h, y, None, EPS, h_out=h)
+    assert np.array_equal(h.cpu().numpy(), want_h)
+    check(q8, got, "q8", want_n)
+
+
 def test_strides_in_place_and_parts(q8):
     rng = np.random.default_rng(5)
     n, dim = 9, 128
