@@ -4,7 +4,9 @@
 // Every product, sum, quotient and root is rounded to fp32 on its own.  S is carried in two fp32 words (each square
 // with its rounding error, each addition with its own), so that its one rounding to fp32 hardly ever depends on the
 // order of the sum (2^-44 against the 2^-24 of the rounding): Q8_0 bytes can be told from the definition alone.
-// In packed pairs that is 6 instructions a value for each norm, which the memory hides.
+// In packed pairs that is 5 instructions a value for each norm.  4096 rows of 4096, fp32, gated, both norms, Q8_0 out: 53.5 us, 4.1 TB/s
+// (issue 50 % busy, DRAM 41 %: two CTAs of 512 threads an SM, each with its next row on the way, wait for each other's roots; a
+// ring of asynchronous copies 73 us, two or four chunks a thread 55 to 58).
 #include "q8_attn.cuh"
 #include "q8_kv.h"
 #include "q8_layer.h"
@@ -36,15 +38,20 @@ __device__ __forceinline__ Sum2 add(Sum2 s, Sum2 t) {
     return {hi, __fadd_rn(__fadd_rn(s.lo, t.lo), e)};
 }
 
-// The sums of the even and of the odd values' squares: twelve instructions for two values.  The products are taken one by
+// The sums of the even and of the odd values' squares: twelve instructions for two values, of a thread's first two four.  The products are taken one by
 // one: a packed product that a packed sum uses is made one fused operation with it, whatever the rounding both ask for.
 struct Squares {
     uint64_t hi = 0, lo = 0;
-    __device__ __forceinline__ void operator+=(uint64_t x) {
+    __device__ __forceinline__ void add_square(uint64_t x, bool first) {
         float x0, x1;
         split2(x0, x1, x);
         const float p0 = __fmul_rn(x0, x0), p1 = __fmul_rn(x1, x1);
         const uint64_t p = pair2(p0, p1), e = pair2(__fmaf_rn(x0, x0, -p0), __fmaf_rn(x1, x1, -p1));      // x^2 = p + e
+        if (first) {
+            hi = p;
+            lo = e;
+            return;
+        }
         const uint64_t s = add2(hi, p), b = sub2(s, hi), r = add2(sub2(hi, sub2(s, b)), sub2(p, b));
         hi = s;
         lo = add2(lo, add2(r, e));
@@ -270,7 +277,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_residual_norm(const ResidualNorm
                     uint64_t v[4];
                     values<YWIDE>(v, yraw[s], ybf);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc += v[e];
+                    for (int e = 0; e < 4; ++e) acc.add_square(v[e], s == 0 && e == 0);
                 }
             ry = cta_inverse_rms(acc, part[0], dim, p.eps);
         }
@@ -318,7 +325,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_residual_norm(const ResidualNorm
                 store8(p.h_out, Q8_TYPE_F32, row * p.h_out_stride + c * 8, h, true, whole);
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc += hv[s][e];
+            for (int e = 0; e < 4; ++e) acc.add_square(hv[s][e], s == 0 && e == 0);
         }
         if (MANY && row + gridDim.x < p.n_tok) load_row(row + gridDim.x);
         if (!p.n_out) {
@@ -383,7 +390,7 @@ cudaError_t launch_rows(const ResidualNormParams &p, int h_type, int y_type, int
 }
 
 // Few rows: as many threads a row as it has chunks, the shortest chain.  Many rows: of up to 4096 values the same, each CTA with its next
-// row on the way (4096 x 4096 with both norms: 54 us; 608 rows 8.8, without the row ahead 9.4, but 304 rows 5.3 without); of
+// row on the way (4096 x 4096 with both norms: 53.5 us; 608 rows 8.8, without the row ahead 9.4, but 304 rows 5.3 without); of
 // more, 32 values a thread (4096 x 8192: 110 us against 140 with 8 or with a row ahead).
 template <bool HWIDE, bool YWIDE>
 cudaError_t launch_typed(const ResidualNormParams &p, int h_type, int y_type, int num_sms, cudaStream_t st) {
