@@ -1006,9 +1006,10 @@ template <int NW> cudaError_t launch_expand(const LoraParams &p, int num_sms, cu
     return launch_expand_rows<NW, false>(p, base, base, num_sms, st);
 }
 
-// The most tiles that a call can have.
+// The most tiles that a call can have: c tokens take (c - 1) / TM + 1, of as many adapters (or none) as there may be.
 uint64_t most_tiles(uint64_t n_tok, uint64_t n_adapters) {
-    return n_tok / TM + (n_tok < n_adapters + 1 ? n_tok : n_adapters + 1);
+    const uint64_t shares = n_tok < n_adapters + 1 ? n_tok : n_adapters + 1;
+    return (n_tok - shares) / TM + shares;
 }
 uint64_t most_groups(uint64_t n_tok, uint64_t n_adapters) {
     const uint64_t few = n_adapters * ((LORA_TILE_MIN + LORA_GROUP - 2) / LORA_GROUP);
