@@ -199,7 +199,7 @@ template <int T> __global__ void __cluster_dims__(LC, 1, 1) __launch_bounds__(LT
         }
         return;
     }
-    const uint32_t rank = rank_of(p, id, t == 0);
+    const uint32_t rank = cut_rank(p, given_rank(p, id), t == 0);
     uint32_t n = 1, pos = 0, mine[T] = {j};
     if (T > 1) {
         // groups are T tokens of the adapter in their order: j's place in its group, and the others

@@ -42,9 +42,9 @@ __device__ __forceinline__ void values16(float (&v)[8], const uint4 &r, bool bf1
     }
 }
 
-// An adapter's rank; one outside [0, max_rank] is cut and raises Q8_ERANGE (by the thread that says so).
-__device__ __forceinline__ uint32_t rank_of(const LoraParams &p, int32_t id, bool tell) {
-    const int32_t r = p.ranks ? p.ranks[id] : (int32_t)p.max_rank;
+// A rank as given; one outside [0, max_rank] is cut and raises Q8_ERANGE (by the thread that says so).
+__device__ __forceinline__ int32_t given_rank(const LoraParams &p, int32_t id) { return p.ranks ? p.ranks[id] : (int32_t)p.max_rank; }
+__device__ __forceinline__ uint32_t cut_rank(const LoraParams &p, int32_t r, bool tell) {
     if (r >= 0 && r <= (int32_t)p.max_rank) return (uint32_t)r;
     if (tell) raise_error(p.err, DEV_ERANGE);
     return r < 0 ? 0u : p.max_rank;

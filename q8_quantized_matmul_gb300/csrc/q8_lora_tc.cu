@@ -82,6 +82,8 @@ __global__ void __launch_bounds__(RT) k_lora_route(const LoraParams p) {
     grid_dep_wait();
     __syncthreads();
     const uint32_t rounds = (p.n_tok + AT_ONCE * RT - 1) / (AT_ONCE * RT);
+    const int per = (n + RT - 1) / RT, b0 = min(n, (int)threadIdx.x * per), b1 = min(n, b0 + per);   // this thread's adapters
+    const int32_t first_rank = b0 < n - 1 ? given_rank(p, b0) : 0;   // asked for with the ids
     const auto buckets = [&](uint32_t round, int (&b)[AT_ONCE], bool tell) {
 #pragma unroll
         for (int q = 0; q < AT_ONCE; ++q) {
@@ -109,7 +111,6 @@ __global__ void __launch_bounds__(RT) k_lora_route(const LoraParams p) {
     }
     __syncthreads();
     // what becomes of an adapter's tokens: tiles, groups, or (no adapter, or one of rank 0) tiles that copy base
-    const int per = (n + RT - 1) / RT, b0 = min(n, (int)threadIdx.x * per), b1 = min(n, b0 + per);
     Sums mine = {0, 0, 0}, total;
     // Groups spare a tile's work for few tokens, but are a kernel of their own: only where there are no tiles otherwise, or so
     // many that they would wait for each other
@@ -121,22 +122,19 @@ __global__ void __launch_bounds__(RT) k_lora_route(const LoraParams p) {
         __syncthreads();
         groups = total.tokens == 0 || total.tiles > (int)LORA_TILES_AT_ONCE;
     }
-    const auto kind = [&](int i, int c, int &rank) -> Sums {
-        rank = c && i < n - 1 ? (int)rank_of(p, i, false) : 0;
+    const auto kind = [&](int i, int c, int &rank, bool tell) -> Sums {
+        rank = c && i < n - 1 ? (int)cut_rank(p, i == b0 ? first_rank : given_rank(p, i), tell) : 0;
         if (rank == 0) return {c, p.base == p.out ? 0 : (c + (int)TM - 1) / (int)TM, 0};
         if (groups && c < (int)LORA_TILE_MIN) return {c, 0, (c + (int)LORA_GROUP - 1) / (int)LORA_GROUP};
         return {c, (c + (int)TM - 1) / (int)TM, 0};
     };
     mine = {0, 0, 0};
     int rank;
-    for (int i = b0; i < b1; ++i) {
-        if (counts[i] && i < n - 1) rank_of(p, i, true);
-        mine = mine + kind(i, counts[i], rank);
-    }
+    for (int i = b0; i < b1; ++i) mine = mine + kind(i, counts[i], rank, true);
     Sums at = scan(mine, total, warps);
     for (int i = b0; i < b1; ++i) {
         const int c = counts[i];
-        const Sums k = kind(i, c, rank);
+        const Sums k = kind(i, c, rank, false);
         counts[i] = at.tokens;
         for (int j = 0; j < k.tiles; ++j)
             p.tiles[1 + at.tiles + j] = make_int4(rank ? i : NO_ADAPTER, at.tokens + j * (int)TM, min((int)TM, c - j * (int)TM), rank);
