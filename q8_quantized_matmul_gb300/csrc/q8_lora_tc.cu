@@ -7,7 +7,7 @@
 //                  product.  The parts are added through distributed shared memory in a fixed order.
 //   k_lora_expand  tiles of 128 outputs (rows) by the tile's tokens (columns): a warp's lanes hold neighbouring outputs of one
 //                  token, so base and out are read and written in whole lines.
-// 4096 tokens of 4 adapters, 4096 to 4096, rank 64, fp32 x: route 6 us, shrink 29 (67 MB of x: 1.3 us a
+// 4096 tokens of 4 adapters, 4096 to 4096, rank 64, fp32 x: route 5 us, shrink 28 (67 MB of x: 1.3 us a
 // K step of 32 KB on 128 SMs; with the terms, the products and the fence taken out 0.9, so the copies, the terms and their
 // stores each take part), expand 26 (134 MB: 5.2 TB/s).  2048 tokens, 1024 to 32768, rank 16: expand 90 (537 MB, 6.0 TB/s).
 //
@@ -35,6 +35,11 @@ constexpr uint32_t PLANE = TM * 128;      // bytes of one term's 128 x 64 tile
 constexpr uint32_t SC_MOST = 8;           // CTAs of a cluster of k_lora_shrink
 constexpr uint32_t SMEM_MOST = 225 * 1024;   // dynamic shared memory; the barriers and token lists come on top
 constexpr int NO_ADAPTER = -1;
+
+// The next kernel's CTAs may come to free SMs and set themselves up (they wait for the end of this kernel before they read): 1.1 us
+// a call in the two places.  They take TMEM only behind that wait: one that came early could take it from a kernel that this chain
+// waits for.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // ---------------------------------------------------------------- route
 constexpr int RT = 1024;
@@ -78,6 +83,7 @@ __global__ void __launch_bounds__(RT) k_lora_route(const LoraParams p) {
     extern __shared__ int counts[];       // [n_adapters + 1]: tokens (the last: of none), then the next free place
     __shared__ Sums warps[RT / 32];
     const int n = (int)p.n_adapters + 1, lane = threadIdx.x & 31;
+    let_next_start();
     for (int i = threadIdx.x; i < n; i += RT) counts[i] = 0;
     grid_dep_wait();
     __syncthreads();
@@ -440,6 +446,7 @@ __global__ void __launch_bounds__(ST, 1) k_lora_shrink(const LoraParams p, const
     uint8_t *ring = smem + sh.body;
     const uint32_t t = threadIdx.x, warp = t >> 5, lane = t & 31u, k = cluster_rank(), SC = p.shrink_cluster;
     const uint32_t cols_max = round16(p.max_rank), w_step = cols_max * 128, turn = accumulators(cols_max) - 1;
+    let_next_start();
     if (t == 0) {
         for (uint32_t i = 0; i < MAX_RAW; ++i) {
             mbar_init(&raw_full[i], COPY + 1);
