@@ -73,7 +73,7 @@ class Case:
 SIZES = [
     # tokens, in, out, rank, adapters
     (1, 32, 1, 8, 1), (1, 4096, 4096, 16, 3), (2, 1024, 300, 8, 2), (5, 96, 7, 24, 4), (9, 2080, 1025, 64, 3),
-    (16, 1024, 4100, 32, 40), (33, 512, 64, 128, 5), (64, 256, 2048, 16, 64), (100, 992, 515, 40, 7), (129, 512, 384, 16, 2),
+    (16, 1024, 4100, 32, 40), (33, 512, 64, 128, 5), (64, 256, 2048, 16, 64), (100, 992, 515, 40, 7), (129, 512, 384, 16, 2), (193, 512, 384, 16, 2),
     (257, 1024, 130, 64, 3), (300, 96, 2050, 8, 300), (700, 2048, 257, 128, 9), (1025, 320, 640, 48, 1), (300, 512, 388, 128, 3),
     (200, 4096, 1000, 72, 2), (450, 256, 4108, 16, 2), (513, 64, 20, 64, 1)]
 
@@ -144,7 +144,7 @@ def test_graphs_outlive_a_larger_call(q8):
         c.check(out)
 
 
-@pytest.mark.parametrize("n", [2, 150])
+@pytest.mark.parametrize("n", [2, 250])
 def test_without_base_scales_ranks(q8, n):
     c = Case(n, n, 512, 260, 16, 3, "f16", ragged=False, base=False)
     c.check(c.call(q8))
@@ -153,7 +153,7 @@ def test_without_base_scales_ranks(q8, n):
     c.check(c.call(q8, scales=None, ranks=None))
 
 
-@pytest.mark.parametrize("n", [3, 140])
+@pytest.mark.parametrize("n", [3, 140, 240])
 def test_strides_and_in_place(q8, n):
     """Adapters of two projections in one pool each, x and out slices of wider tensors, out on base."""
     c = Case(n, n, 256, 192, 16, 3, "bf16")
@@ -174,7 +174,7 @@ def test_strides_and_in_place(q8, n):
     assert (wide[:, 192:] == 7).all()
 
 
-@pytest.mark.parametrize("n", [6, 150])
+@pytest.mark.parametrize("n", [6, 250])
 def test_bad_ids_and_ranks(q8, n):
     c = Case(n, n, 128, 96, 16, 4, "bf16", ragged=False)
     c.ids[1], c.ids[n - 2] = 4, 2 ** 31 - 1
@@ -188,7 +188,7 @@ def test_bad_ids_and_ranks(q8, n):
     assert q8.q8_last_error() == q8.Q8_ERANGE and q8.q8_last_error() == 0
 
 
-@pytest.mark.parametrize("n", [8, 160])
+@pytest.mark.parametrize("n", [8, 160, 260])
 def test_values_that_are_not_finite_stay_in_their_row(q8, n):
     c = Case(n, n, 256, 130, 16, 2, "f16", ids=np.arange(n) % 3 - 1)
     clean = c.call(q8)
