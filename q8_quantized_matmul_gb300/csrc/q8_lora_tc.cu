@@ -235,14 +235,15 @@ template <int XK> constexpr uint32_t RAW_PITCH = XK == X_F32 ? 256 : XK == X_Q8 
 struct ShrinkShape {
     uint32_t stage, raw, raws, body, smem;
 };
-template <int XK, int NW> __host__ __device__ constexpr ShrinkShape shrink_shape(uint32_t max_rank) {
+template <int XK, int NW, bool RUNS> __host__ __device__ constexpr ShrinkShape shrink_shape(uint32_t max_rank) {
     ShrinkShape s{};
     const uint32_t cols = round16(max_rank), room = SMEM_MOST - 1024;
     s.stage = NW * cols * 128;                               // the weights' terms of a K step
     s.raw = TM * RAW_PITCH<XK> + cols * 128;
     s.body = 2 * s.stage;
-    const uint32_t part = TM * (cols + 4) * 4;               // the CTA's sums take the stages' place
-    if (s.body < part) s.body = part;
+    const uint32_t part = TM * (cols + (RUNS ? 0 : 4)) * 4;  // the CTA's sums take the stages' place, or (RUNS) lie behind them
+    if (RUNS) s.body += part;
+    else if (s.body < part) s.body = part;
     s.body = (s.body + 1023) & ~1023u;
     s.raws = (room - s.body) / s.raw;
     if (s.raws > MAX_RAW) s.raws = MAX_RAW;
@@ -253,11 +254,23 @@ template <int XK, int NW> __host__ __device__ constexpr ShrinkShape shrink_shape
     if (s.smem < 116 * 1024) s.smem = 116 * 1024;
     return s;
 }
+static_assert(shrink_shape<X_F32, 2, true>(LORA_MAX_RANK).raws == 2, "the largest: a slot of raw rows for each group");
 // TMEM columns: the sums of the small terms' products, then up to four of the first terms' (the 16-value steps of a K step in turn:
-// the tensor cores drop what is shifted out of a sum, 4096 values in one accumulator cost 5e-7 of it), from X_COLS on two stages of x
+// the tensor cores drop what is shifted out of a sum), from X_COLS on two stages of x
 // terms (32 columns a term).
 constexpr uint32_t X_COLS = 320, X_STAGE = 96;
 __host__ __device__ constexpr uint32_t accumulators(uint32_t cols) { return cols <= 64 ? 4 : cols <= 96 ? 2 : 1; }
+// What is dropped grows with a sum's length, by 2^-26 of the sum for every 16 values and always towards zero.  So long sums are taken in
+// runs of 16 products an accumulator, and the runs added up in shared memory: 3e-7 whatever in_dim is, where 4096 values in one
+// accumulator cost 4e-6 (and a plain fp32 product of 4096 to 32768 values 4 to 8e-7).  A run's end costs about 0.8 us.
+constexpr uint32_t RUN = 16;
+__host__ __device__ constexpr uint32_t run_steps(uint32_t cols) { return RUN * accumulators(cols) / (KB / 16); }
+
+// Place of 16-byte chunk c of row r in the CTA's sums: neighbouring rows' chunks lie in different banks.
+template <bool RUNS> __device__ __forceinline__ uint32_t part_at(uint32_t r, uint32_t c, uint32_t cols) {
+    if constexpr (RUNS) return r * cols + ((c ^ (cols & 16 ? r >> 1 & 3 : r & 7)) << 2);
+    return r * (cols + 4) + c * 4;
+}
 
 // `bytes` of 16 or 4 global -> shared, the rest zeros.
 __device__ __forceinline__ void cp_async16_part(uint32_t dst, const void *src, uint32_t bytes) {
@@ -433,7 +446,8 @@ __device__ __forceinline__ void convert(const LoraParams &p, uint32_t x_tmem, ui
     tc_fence_before();
 }
 
-template <int XK, int NX, int NW>
+// RUNS: sums of more than RUN products an accumulator are taken in runs.
+template <int XK, int NX, int NW, bool RUNS>
 __global__ void __launch_bounds__(ST, 1) k_lora_shrink(const LoraParams p, const __grid_constant__ CUtensorMap tm_x) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint32_t tmem_slot;
@@ -442,7 +456,7 @@ __global__ void __launch_bounds__(ST, 1) k_lora_shrink(const LoraParams p, const
     __shared__ uint64_t raw_full[MAX_RAW], raw_empty[MAX_RAW], st_full[2], st_empty[2], tok_full[2], tok_empty[2], d_full, parts_ready,
         parts_read;
     uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-    const ShrinkShape sh = shrink_shape<XK, NW>(p.max_rank);
+    const ShrinkShape sh = shrink_shape<XK, NW, RUNS>(p.max_rank);
     uint8_t *ring = smem + sh.body;
     const uint32_t t = threadIdx.x, warp = t >> 5, lane = t & 31u, k = cluster_rank(), SC = p.shrink_cluster;
     const uint32_t cols_max = round16(p.max_rank), w_step = cols_max * 128, turn = accumulators(cols_max) - 1;
@@ -474,14 +488,16 @@ __global__ void __launch_bounds__(ST, 1) k_lora_shrink(const LoraParams p, const
     const uint32_t tmem = tmem_slot;
     const int n_tiles = p.tiles[0].x, clusters = (int)(gridDim.x / SC);
     const uint32_t nb = (p.in_dim + KB - 1) / KB, kb0 = nb * k / SC, kb1 = nb * (k + 1) / SC;
+    const uint32_t run = RUNS ? run_steps(cols_max) : 0xffffffffu;
     const uint64_t lim = wait_limit(p.wait_ns);
     const auto wait = [&](uint64_t *bar, uint32_t parity) { return tile_wait(bar, parity, p.err, &abort_flag, lim); };
-    uint32_t n = 0;                                          // K steps so far
+    float *part = reinterpret_cast<float *>(smem + (RUNS ? 2 * sh.stage : 0));
+    uint32_t n = 0, runs = 0;                                // K steps and (RUNS) runs so far
     int tiles = 0;                                           // tiles so far
     for (int tile = (int)(blockIdx.x / SC); tile < n_tiles; tile += clusters) {
         const int4 T = p.tiles[1 + tile];
         if (T.x == NO_ADAPTER) continue;
-        const uint32_t count = T.z, rank = T.w, cols = round16(rank), pitch = cols + 4;
+        const uint32_t count = T.z, rank = T.w, cols = round16(rank);
         uint32_t *tok = toks[tiles & 1];
         if (warp >= CONVERT / 32 && warp < (CONVERT + COPY) / 32) {
             // ------------------------------------------------ raw rows -> ring
@@ -501,6 +517,7 @@ __global__ void __launch_bounds__(ST, 1) k_lora_shrink(const LoraParams p, const
         } else if (warp == ST / 32 - 1) {
             // ------------------------------------------------ products
             const uint32_t idesc = tc_idesc(TM, cols, !(XK == X_RAW && !p.bf16 && NW == 1));
+            uint32_t of_run = 0;
             for (uint32_t kb = kb0; kb < kb1; ++kb, ++n) {
                 const uint32_t s = n & 1;
                 wait(&st_full[s], (n / 2) & 1);
@@ -517,57 +534,80 @@ __global__ void __launch_bounds__(ST, 1) k_lora_shrink(const LoraParams p, const
 #pragma unroll
                             for (uint32_t k = 0; k < KB / 16; ++k) {
                                 // the first product of an accumulator starts it
-                                const bool starts = kb == kb0 && (small ? first_small && k == 0 : k <= turn);
+                                const bool starts = (!RUNS || small ? kb == kb0 : of_run == 0) && (small ? first_small && k == 0 : k <= turn);
                                 tc_mma_f16_ta(small ? tmem : tmem + (1 + (k & turn)) * cols_max, x + i * 32 + k * 8, wd + 2 * k, idesc, !starts);
                             }
                         }
                     tc_commit(&st_empty[s]);
-                    if (kb + 1 == kb1) tc_commit(&d_full);
+                    if (kb + 1 == kb1 || (RUNS && of_run + 1 == run)) tc_commit(&d_full);
                 }
                 __syncwarp();
+                if (RUNS && ++of_run == run) of_run = 0;
             }
         } else {
             // ------------------------------------------------ terms
             wait(&tok_full[tiles & 1], (tiles / 2) & 1);
+            const uint32_t row = (warp & 3) * 32 + lane;
+            // this CTA's sums, one row a thread, from accumulator `first` on: stored, or (more) added to those of the runs before
+            const auto take_sums = [&](uint32_t first, bool more) {
+                for (uint32_t c = (warp >> 2) * 16; c < cols; c += 16 * (CONVERT / 128)) {
+                    float sum[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) sum[e] = 0.0f;
+                    if (kb0 < kb1)
+                        for (uint32_t i = first; i <= 1 + turn; ++i) {
+                            uint32_t d[16];
+                            tc_ld16(tmem + ((warp & 3) << 21) + i * cols_max + c, d);
+                            tc_wait_ld();
+                            tc_regs_ready(d);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) sum[e] += __uint_as_float(d[e]);
+                        }
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4) {
+                        float4 *at = reinterpret_cast<float4 *>(part + part_at<RUNS>(row, (c + e) / 4, cols));
+                        float4 v = make_float4(sum[e], sum[e + 1], sum[e + 2], sum[e + 3]);
+                        if (RUNS && more) {
+                            const float4 before = *at;
+                            v = make_float4(before.x + v.x, before.y + v.y, before.z + v.z, before.w + v.w);
+                        }
+                        *at = v;
+                    }
+                }
+                tc_fence_before();
+            };
+            uint32_t left = run;
             for (uint32_t kb = kb0; kb < kb1; ++kb, ++n) {
-                if (n % 2 != t / GROUP) continue;
-                const uint32_t r = n % sh.raws, s = n & 1, use = n / 2;
-                wait(&raw_full[r], (n / sh.raws) & 1);
-                if (use) wait(&st_empty[s], (use - 1) & 1);
-                tc_fence_after();
-                convert<XK, NX, NW>(p, tmem + X_COLS + s * X_STAGE, smem + s * sh.stage, ring + r * sh.raw, tok, kb * KB, cols, w_step, &raw_empty[r],
-                                    t % GROUP);
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&st_full[s]);
+                const bool mine = n % 2 == t / GROUP;
+                const uint32_t s = n & 1;
+                if (mine) {
+                    const uint32_t r = n % sh.raws, use = n / 2;
+                    wait(&raw_full[r], (n / sh.raws) & 1);
+                    if (use) wait(&st_empty[s], (use - 1) & 1);
+                    tc_fence_after();
+                    convert<XK, NX, NW>(p, tmem + X_COLS + s * X_STAGE, smem + s * sh.stage, ring + r * sh.raw, tok, kb * KB, cols, w_step,
+                                        &raw_empty[r], t % GROUP);
+                    fence_async_smem();
+                    __syncwarp();
+                }
+                if constexpr (RUNS) {
+                    // (the small terms' sums go on to the end: what they lose is small as well.)  The next run's first step is
+                    // there, but released only once all have read
+                    if (left-- == 0) {
+                        wait(&d_full, runs++ & 1);
+                        tc_fence_after();
+                        take_sums(1, kb - kb0 > run);
+                        named_bar_sync(2, CONVERT);
+                        left = run - 1;
+                    }
+                }
+                if (mine && lane == 0) mbar_arrive(&st_full[s]);
             }
             if (lane == 0) mbar_arrive(&tok_empty[tiles & 1]);
-            // this CTA's sums, one row a thread
-            float *part = reinterpret_cast<float *>(smem);
-            if (kb0 < kb1) wait(&d_full, tiles & 1);
+            if (kb0 < kb1) wait(&d_full, (RUNS ? runs++ : (uint32_t)tiles) & 1);
             tc_fence_after();
             named_bar_sync(2, CONVERT);
-            const uint32_t row = (warp & 3) * 32 + lane;
-            for (uint32_t c = (warp >> 2) * 16; c < cols; c += 16 * (CONVERT / 128)) {
-                float sum[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) sum[e] = 0.0f;
-                if (kb0 < kb1)
-                    for (uint32_t i = NX + NW > 2 ? 0 : 1; i <= 1 + turn; ++i) {   // the small ones first
-                        uint32_t d[16];
-                        tc_ld16(tmem + ((warp & 3) << 21) + i * cols_max + c, d);
-                        tc_wait_ld();
-                        tc_regs_ready(d);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) sum[e] += __uint_as_float(d[e]);
-                    }
-#pragma unroll
-                for (int e = 0; e < 16; e += 4) {
-                    const float4 v = make_float4(sum[e], sum[e + 1], sum[e + 2], sum[e + 3]);
-                    *reinterpret_cast<float4 *>(part + row * pitch + c + e) = v;
-                }
-            }
-            tc_fence_before();
+            take_sums(NX + NW > 2 ? 0 : 1, kb1 - kb0 > run);   // the small ones first
             named_bar_sync(2, CONVERT);
             if (t < SC) arrive_at(&parts_ready, t);
             cluster_bar_wait(&parts_ready, tiles & 1, p.err, &abort_flag);
@@ -580,7 +620,7 @@ __global__ void __launch_bounds__(ST, 1) k_lora_shrink(const LoraParams p, const
 #pragma unroll
                 for (uint32_t q = 0; q < SC_MOST; ++q) {
                     if (q >= SC) break;
-                    const float4 f = ld_cluster4(cluster_addr(part + r * pitch + c, q));
+                    const float4 f = ld_cluster4(cluster_addr(part + part_at<RUNS>(r, c / 4, cols), q));
                     v[0] += f.x;
                     v[1] += f.y;
                     v[2] += f.z;
@@ -942,14 +982,11 @@ __global__ void __launch_bounds__(ET, 1) k_lora_expand(const LoraParams p, const
 }
 
 // ---------------------------------------------------------------- launchers
-template <int XK, int NX, int NW> cudaError_t launch_shrink(LoraParams p, unsigned tiles, int num_sms, cudaStream_t st) {
+template <int XK, int NX, int NW, bool RUNS> cudaError_t launch_shrink_of(LoraParams p, unsigned tiles, int num_sms, cudaStream_t st) {
     static SmemAllowed allowed;
-    cudaError_t e = allow_smem(allowed, reinterpret_cast<const void *>(k_lora_shrink<XK, NX, NW>), SMEM_MOST);
+    const auto kernel = k_lora_shrink<XK, NX, NW, RUNS>;
+    cudaError_t e = allow_smem(allowed, reinterpret_cast<const void *>(kernel), SMEM_MOST);
     if (e != cudaSuccess) return e;
-    // Clusters that fit at a time are fewer than SMs / CTAs (15 of 8, 36 of 4 on 152 SMs): more tiles than clusters of 8
-    // take clusters of 4 (4096 tokens with clusters of 8: three rounds, 52 us; of 4: one, 31).  Sums of over 96 columns have one
-    // accumulator, and stay with the shorter sums of clusters of 8.
-    const uint32_t least = accumulators(round16(p.max_rank)) > 1 ? 4 : 8;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -957,10 +994,15 @@ template <int XK, int NX, int NW> cudaError_t launch_shrink(LoraParams p, unsign
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(ST);
-    cfg.dynamicSmemBytes = shrink_shape<XK, NW>(p.max_rank).smem;
+    cfg.dynamicSmemBytes = shrink_shape<XK, NW, RUNS>(p.max_rank).smem;
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
+    // Clusters that fit at a time are fewer than SMs / CTAs (15 of 8, 36 of 4 on 152 SMs): more tiles than clusters of 8
+    // take clusters of 4 (4096 tokens with clusters of 8: three rounds, 52 us; of 4: one, 31).  Ranks above 96, whose runs are a quarter
+    // as long, do so from two rounds on (4096 to 4096, rank 128, whole calls: 36 tiles 92 and 67 us; 8192 inputs, 12 tiles of at most 16:
+    // 49 and 69).
+    const unsigned most_rounds = accumulators(round16(p.max_rank)) > 1 ? 1 : 2;
     int dev = -1, fit = 0;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
     static std::atomic<int> fits[2][64];                     // clusters of 8 and of 4 that fit on a device, asked for once
@@ -970,18 +1012,25 @@ template <int XK, int NX, int NW> cudaError_t launch_shrink(LoraParams p, unsign
         fit = known ? known->load(std::memory_order_relaxed) : 0;
         if (fit < 1) {
             cfg.gridDim = dim3((unsigned)num_sms / p.shrink_cluster * p.shrink_cluster);
-            if ((e = cudaOccupancyMaxActiveClusters(&fit, k_lora_shrink<XK, NX, NW>, &cfg)) != cudaSuccess) return e;
+            if ((e = cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg)) != cudaSuccess) return e;
             if (fit < 1) fit = 1;
             if (known) known->store(fit, std::memory_order_relaxed);
         }
-        if (tiles <= (unsigned)fit || p.shrink_cluster == least) break;
+        if (tiles <= most_rounds * (unsigned)fit || p.shrink_cluster == 4) break;
     }
+    // the kernel of whole sums takes no more K steps a CTA than one run has
+    const uint32_t steps = ((p.in_dim + KB - 1) / KB + p.shrink_cluster - 1) / p.shrink_cluster;
+    if constexpr (!RUNS)
+        if (steps > run_steps(round16(p.max_rank))) return launch_shrink_of<XK, NX, NW, true>(p, tiles, num_sms, st);
     cfg.gridDim = dim3((tiles < (unsigned)fit ? tiles : (unsigned)fit) * p.shrink_cluster);
     CUtensorMap x;
     memset(&x, 0, sizeof x);
     p.x_tma = XK != X_Q8 && encode_gather_tmap(&x, p.x, p.in_dim, p.n_tok, p.x_stride, XK == X_F32 ? 4 : 2);
-    e = cudaLaunchKernelEx(&cfg, k_lora_shrink<XK, NX, NW>, (const LoraParams)p, (const CUtensorMap)x);
+    e = cudaLaunchKernelEx(&cfg, kernel, (const LoraParams)p, (const CUtensorMap)x);
     return e == cudaSuccess ? cudaGetLastError() : e;
+}
+template <int XK, int NX, int NW> cudaError_t launch_shrink(const LoraParams &p, unsigned tiles, int num_sms, cudaStream_t st) {
+    return launch_shrink_of<XK, NX, NW, false>(p, tiles, num_sms, st);
 }
 
 template <int NW, bool TMA>
