@@ -50,7 +50,7 @@ struct LoraParams {
     uint16_t *low;
     uint32_t shrink_cluster;              // CTAs that share a tile of tokens (set by the launcher), and
     bool x_tma;                           // whether x's rows come through the copy engine
-    uint64_t wait_ns;                     // failure-detection test hook (k_lora_shrink), see GemvParams
+    uint64_t wait_ns;                     // failure-detection test hook (k_lora_shrink, k_lora_expand), see GemvParams
     int withhold;
 };
 constexpr uint32_t LORA_MAX_RANK = 128, LORA_MAX_ADAPTERS = 16384;

@@ -36,6 +36,19 @@ constexpr uint32_t SC_MOST = 8;           // CTAs of a cluster of k_lora_shrink
 constexpr uint32_t SMEM_MOST = 225 * 1024;   // dynamic shared memory; the barriers and token lists come on top
 constexpr int NO_ADAPTER = -1;
 
+// After an expired wait the warps go on (in bounds, on whatever the buffers hold) and may release a buffer whose copy has not landed.
+// The flag is set before any such release, so a warp that reads it behind its own wait issues no copy then, and no barrier of a copy in
+// flight is armed again.
+__device__ __forceinline__ bool aborted(const volatile int *flag) { return __any_sync(0xffffffffu, *flag != 0); }
+// Nothing lands after a CTA has gone, and no product is in flight when TMEM goes: a pause, by one warp that the others' end waits for.
+// (Waits for the very copies and products, which have to be kept count of, took 0.5 us from every call; these take microseconds.)
+__device__ __forceinline__ void linger(const volatile int *flag) {
+    if (*flag == 0) return;
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 1000000) {}
+    __syncwarp();
+}
+
 // The next kernel's CTAs may come to free SMs and set themselves up (they wait for the end of this kernel before they read): 1.1 us
 // a call in the two places.  They take TMEM only behind that wait: one that came early could take it from a kernel that this chain
 // waits for.
@@ -288,7 +301,7 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
 __device__ __forceinline__ void arrive_at(uint64_t *bar, uint32_t cta) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr(bar, cta)) : "memory");
 }
-__device__ __forceinline__ bool cluster_bar_wait(uint64_t *bar, uint32_t parity, int *err, volatile int *abort) {
+__device__ __forceinline__ bool cluster_bar_wait(uint64_t *bar, uint32_t parity, int *err, volatile int *abort, uint64_t limit_ns) {
     const uint64_t t0 = global_timer_ns();
     for (uint32_t it = 0;; ++it) {
         uint32_t ok;
@@ -299,7 +312,7 @@ __device__ __forceinline__ bool cluster_bar_wait(uint64_t *bar, uint32_t parity,
         if (ok) return true;
         if ((it & 255u) == 255u) {
             if (*abort) return false;
-            if (global_timer_ns() - t0 > WAIT_LIMIT_NS) {
+            if (global_timer_ns() - t0 > limit_ns) {
                 raise_error(err, DEV_ETIMEOUT);
                 *abort = 1;
                 return false;
@@ -510,7 +523,7 @@ __global__ void __launch_bounds__(ST, 1) k_lora_shrink(const LoraParams p, const
             for (uint32_t kb = kb0; kb < kb1; ++kb, ++n) {
                 const uint32_t r = n % sh.raws, use = n / sh.raws;
                 if (use) wait(&raw_empty[r], (use - 1) & 1);
-                if (p.withhold) continue;                    // the failure-detection test hook
+                if (p.withhold || aborted(&abort_flag)) continue;   // (withhold: the failure-detection test hook)
                 copy_raw<XK>(p, &tm_x, ring + r * sh.raw, a, rank, tok, count, kb * KB, b, &raw_full[r]);
                 cp_async_arrive(&raw_full[r]);
             }
@@ -610,7 +623,7 @@ __global__ void __launch_bounds__(ST, 1) k_lora_shrink(const LoraParams p, const
             take_sums(NX + NW > 2 ? 0 : 1, kb1 - kb0 > run);   // the small ones first
             named_bar_sync(2, CONVERT);
             if (t < SC) arrive_at(&parts_ready, t);
-            cluster_bar_wait(&parts_ready, tiles & 1, p.err, &abort_flag);
+            cluster_bar_wait(&parts_ready, tiles & 1, p.err, &abort_flag, lim);
             // an eighth of the rows: the parts in order, the scale, three terms
             const float scale = p.scales ? p.scales[T.x] : 1.0f;
             const uint32_t r0 = count * k / SC, r1 = count * (k + 1) / SC, quads = cols / 4;
@@ -638,21 +651,18 @@ __global__ void __launch_bounds__(ST, 1) k_lora_shrink(const LoraParams p, const
             // the stages may be written over once every CTA has read
             named_bar_sync(2, CONVERT);
             if (t < SC) arrive_at(&parts_read, t);
-            cluster_bar_wait(&parts_read, tiles & 1, p.err, &abort_flag);
+            cluster_bar_wait(&parts_read, tiles & 1, p.err, &abort_flag, lim);
             tc_fence_after();
         }
         ++tiles;
     }
-    if (warp >= CONVERT / 32 && warp < (CONVERT + COPY) / 32) {
-        cp_async_wait<0>();                                  // nothing lands after the CTA has gone
-        if (p.x_tma && abort_flag && !p.withhold) {          // only an expired wait leaves raw slots unread
-            const uint64_t t_end = global_timer_ns() + WAIT_LIMIT_NS;
-            for (uint32_t i = 0; i < min(n, sh.raws); ++i) mbar_drain(&raw_full[i], ((n - 1 - i) / sh.raws) & 1, t_end);
-        }
-    }
+    if (warp >= CONVERT / 32 && warp < (CONVERT + COPY) / 32) cp_async_wait<0>();   // nothing lands after the CTA has gone
     tc_fence_before();
     __syncthreads();
-    if (warp == ST / 32 - 1) tmem_free(tmem, 512);
+    if (warp == ST / 32 - 1) {
+        linger(&abort_flag);
+        tmem_free(tmem, 512);
+    }
     cluster_arrive();   // no CTA leaves while another may still read its sums, expired waits included
     cluster_wait();
 }
@@ -769,7 +779,8 @@ __global__ void __launch_bounds__(ET, 1) k_lora_expand(const LoraParams p, const
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
-    const auto wait = [&](uint64_t *bar, uint32_t parity) { return tile_wait(bar, parity, p.err, &abort_flag); };
+    const uint64_t lim = wait_limit(p.wait_ns);
+    const auto wait = [&](uint64_t *bar, uint32_t parity) { return tile_wait(bar, parity, p.err, &abort_flag, lim); };
     if (warp < E_COPY0) {
         const uint32_t group = warp >> 2, q = warp & 3, col = q * 32 + lane, out_step = (uint32_t)p.out_stride * 4;
         uint32_t n = 0, u = 0;                               // slots and products so far
@@ -860,7 +871,7 @@ __global__ void __launch_bounds__(ET, 1) k_lora_expand(const LoraParams p, const
         }
         if (TMA) release_sent();
     } else if (warp < E_COPY0 + E_COPIES) {
-        uint32_t n = 0, filled = 0;                          // slots so far; those that the copy engine has written
+        uint32_t n = 0;                                      // slots so far
         for (Units w(p); w.live(); w.next(p)) {
             const uint32_t count = w.T.z, o0 = w.chunk * OM, width = min(OM, p.out_dim - o0);
             for (uint32_t s0 = 0; s0 < count; s0 += SLOT_TOK, ++n) {
@@ -868,6 +879,7 @@ __global__ void __launch_bounds__(ET, 1) k_lora_expand(const LoraParams p, const
                 const uint32_t slot = n % sh.slots, rows = min(SLOT_TOK, count - s0), uses = n / sh.slots;
                 const uint32_t tok = p.base && lane < rows ? p.perm[w.T.y + s0 + lane] : 0;
                 if (uses) wait(&empty[slot], (uses - 1) & 1);
+                if (aborted(&abort_flag) || (p.withhold && warp > E_COPY0)) continue;   // (withhold: the failure-detection test hook)
                 if (TMA && p.base && width == OM) {
                     // whole groups of four rows; a last group reads some row again
                     const uint32_t first = __shfl_sync(0xffffffffu, tok, 0);
@@ -877,8 +889,7 @@ __global__ void __launch_bounds__(ET, 1) k_lora_expand(const LoraParams p, const
                     if (lane == 0) mbar_arrive_expect_tx(&full[slot], groups * 4 * OM * 4);
                     else mbar_arrive(&full[slot]);
                     __syncwarp();
-                    if (lane < groups && !abort_flag) gather4(ring + slot * SLOT + lane * 4 * OM * 4, &tm_base, (int)o0, r, &full[slot]);
-                    filled |= 1u << slot;
+                    if (lane < groups) gather4(ring + slot * SLOT + lane * 4 * OM * 4, &tm_base, (int)o0, r, &full[slot]);
                     continue;
                 }
                 if (p.base) {
@@ -902,11 +913,6 @@ __global__ void __launch_bounds__(ET, 1) k_lora_expand(const LoraParams p, const
             }
         }
         cp_async_wait<0>();                                  // nothing lands after the CTA has gone
-        if (TMA && abort_flag && filled) {                   // only an expired wait leaves gathered slots unread
-            const uint64_t t_end = global_timer_ns() + WAIT_LIMIT_NS;
-            for (uint32_t i = 0; i < sh.slots; ++i)
-                if (filled >> i & 1u) mbar_drain(&full[i], ((n - 1 - i) / sh.slots) & 1, t_end);
-        }
     } else if (warp == E_MMA) {
         uint32_t u = 0;
         for (Units w(p); w.live(); w.next(p)) {
@@ -978,7 +984,10 @@ __global__ void __launch_bounds__(ET, 1) k_lora_expand(const LoraParams p, const
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == E_MMA) tmem_free(tmem, 2 * TM);
+    if (warp == E_MMA) {
+        linger(&abort_flag);
+        tmem_free(tmem, 2 * TM);
+    }
 }
 
 // ---------------------------------------------------------------- launchers
