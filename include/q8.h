@@ -506,8 +506,8 @@ int q8_kv_read(void *k_out, uint64_t k_stride, void *v_out, uint64_t v_stride, i
  * n_adapters or beyond counts as negative, a rank outside its range is cut to it (of an adapter that
  * a token has); both raise Q8_ERANGE.  Pointers are 16-byte aligned (the id, rank and scale arrays
  * 4-byte), strides of out and base below 2^30.  out must not overlap x or the adapters.  A few tokens
- * are one launch without scratch; many (more than 192, or tokens times max_rank
- * above 4096) use the library's scratch.
+ * are one launch without scratch; many (more than 192, or fewer where few adapters of high rank or
+ * many outputs are shared) use the library's scratch.
  */
 typedef struct q8_adapters {
     const void *a, *b;       /* device */

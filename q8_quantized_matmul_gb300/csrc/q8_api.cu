@@ -1637,7 +1637,7 @@ int q8_lora(float *out, uint64_t out_stride, const float *base, uint64_t base_st
     p.n_tok = (uint32_t)n_tok;
     p.err = s->err;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (q8::lora_few(p.n_tok, p.max_rank)) return status_of(q8::launch_lora(p, s->num_sms, st));
+    if (q8::lora_few(p.n_tok, p.max_rank, p.in_dim, p.out_dim, p.n_adapters, s->num_sms)) return status_of(q8::launch_lora(p, s->num_sms, st));
     if ((rc = reserve_scratch(s, q8::lora_tc_scratch(p.n_tok, p.n_adapters, p.max_rank), st))) return rc;
     take_expiry(p.wait_ns, p.withhold);
     return status_of(q8::launch_lora_tc(p, s->scratch.p, s->num_sms, st));

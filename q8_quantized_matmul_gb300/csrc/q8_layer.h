@@ -5,6 +5,8 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "q8_lora_plan.h"
+
 namespace q8 {
 
 struct ResidualNormParams {
@@ -54,14 +56,6 @@ struct LoraParams {
     int withhold;
 };
 constexpr uint32_t LORA_MAX_RANK = 128, LORA_MAX_ADAPTERS = 16384;
-// Few tokens take launch_lora, which searches the tokens of an adapter anew in every CTA and reads the weights again for each
-// four of them, but is one launch.  launch_lora / launch_lora_tc, us, 4096 to 4096, an adapter each | one for all:
-//   rank 16   64 tokens 6.9 / 15.6 | 8.2 / 24;   192 24 / 33 | 24 / 26;   256 34 / 45 | 33 / 26
-//   rank 32  128 tokens 23 / 30 | 24 / 26
-//   rank 64   64 tokens 23 / 32 | 21 / 26;       96 40 / 46 | 33 / 27
-//   rank 128  32 tokens 27 / 63 | 36 / 27;       64 41 / 50 | 38 / 28
-// (2048 to 1000 alike; 1024 to 32768 with one adapter for all it is later: 64 tokens of rank 64 33 / 20, an adapter each 88 / 97).
-inline bool lora_few(uint64_t n_tok, uint32_t max_rank) { return n_tok <= 192 && n_tok * max_rank <= 4096; }
 constexpr uint32_t LORA_GROUP = 4;        // tokens of one adapter that k_lora multiplies by its weights at a time
 constexpr uint32_t LORA_TILE_MIN = 16;    // of more tokens: an adapter with fewer may have groups in place of a tile
 constexpr uint32_t LORA_TILES_AT_ONCE = 36;   // clusters of k_lora_shrink that fit at a time

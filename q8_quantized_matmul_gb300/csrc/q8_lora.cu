@@ -12,8 +12,8 @@
 namespace q8 {
 namespace {
 
-constexpr int LC = 8;            // CTAs of a cluster
-constexpr int LT = 256;          // threads of a CTA
+constexpr int LC = LORA_CLUSTER; // CTAs of a cluster
+constexpr int LT = LORA_THREADS; // threads of a CTA
 
 // Values i .. i + 7 (i a multiple of 8) of a token's x.
 __device__ __forceinline__ void x8(float (&v)[8], const LoraParams &p, uint64_t tok, uint32_t i) {
@@ -252,11 +252,7 @@ __global__ void __cluster_dims__(LC, 1, 1) __launch_bounds__(LT, 4) k_lora_group
 
 cudaError_t launch_lora(const LoraParams &q, int num_sms, cudaStream_t st) {
     LoraParams p = q;
-    // As many clusters a token as give each SM two CTAs, of at least a thread an output.  Four fit on an SM; what does not
-    // fit at once costs a whole chain more (64 adapters of one token, 4096 to 4096, rank 16: 6.9 us, 10.5 with room for
-    // three), and more clusters repeat the product with A (8 tokens, 1024 to 32768: 5.0 us with two an SM, 5.9 with four).
-    const uint32_t most = (p.out_dim + LT * LC - 1) / (LT * LC), want = ((uint32_t)(2 * num_sms) + p.n_tok * LC - 1) / (p.n_tok * LC);
-    p.splits = want > most ? most : want;
+    p.splits = lora_splits(p.n_tok, p.out_dim, num_sms);
     const dim3 grid((unsigned)((uint64_t)LC * p.splits * p.n_tok));
     if (p.n_tok == 1) return launch_dependent(k_lora<1>, p, grid, LT, 0, st);
     return launch_dependent(k_lora<LORA_GROUP>, p, grid, LT, 0, st);
