@@ -495,7 +495,9 @@ def kq_moe_matmul(W_experts, fmt: int, n_expert: int, expert_stride: int, ids, x
 
 
 # ------------------------------------------------------------------ paged key-value cache, attention, a layer's paths
-# These calls take microseconds on the GPU, so their marshalling is compiled: csrc/q8_torch.cpp.
+# These calls take microseconds on the GPU, so their marshalling is compiled: csrc/q8_torch.cpp.  They are for inference: results carry
+# no gradients, whatever their inputs require.  kv_read, residual_norm and lora mark what they write in place (out, h_out) as changed, so
+# that autograd refuses a backward pass which needs the old values.
 EXT_PATH = os.path.join(_PKG, "_q8torch.so")
 _ext_mod = None
 
@@ -635,5 +637,5 @@ def lora(x, a, b, adapter_of, ranks=None, scales=None, base=None, out=None):
     """base + scales[i] b[i] (a[i] x[t]) with i = adapter_of[t] (int32 [n_tok]; negative: base alone).  x [n_tok, in_dim]
     float32, 16 bit or Q8_0 blocks (uint8 [n_tok, in_dim/32*34]); a [n, rank, in_dim] and b [n, out_dim, rank] 16 bit;
     ranks int32 [n] (None: all of them), scales float32 [n] (None: 1); base and out float32 [n_tok, out_dim] (rows
-    strided), out may be base.  -> out."""
+    strided), out may be base.  -> out, without gradients (adapters are served here, not trained)."""
     return (_ext_mod or _load_ext()).lora(x, a, b, adapter_of, ranks, scales, base, out)

@@ -160,6 +160,12 @@ void *stream_for(const q8_kv_cache *c, PyObject *const *a, std::initializer_list
 
 PyObject *wrap(const at::Tensor &t) { return THPVariable_Wrap(t); }
 
+// A tensor of the caller's that a call wrote: autograd has to see that it changed, or a gradient that needs its old values
+// would be computed from the new ones.
+void written(const at::Tensor &t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 PyObject *none_or(const at::Tensor &t) {
     if (t.defined()) return wrap(t);
     Py_RETURN_NONE;
@@ -460,6 +466,10 @@ PyObject *kv_read(PyObject *const *a, Py_ssize_t n) {
         return f_read(kp, ks, vp, vs, out_type, c, layer, t.p, t.stride, (uint32_t)t.width, (uint32_t)t.rows, seqs, first, start,
                       (uint32_t)(n_start - 1), rows, st);
     });
+    if (a[8] != Py_None) {
+        written(k);
+        written(v);
+    }
     return Py_BuildValue("(NN)", wrap(k), wrap(v));
 }
 
@@ -537,6 +547,7 @@ PyObject *residual_norm(PyObject *const *a, Py_ssize_t n) {
     call("q8_residual_norm", [&] {
         return f_residual(op, out_type, hop, hos, hp, ht, hs, yp, yt, ys, post, before, gate, gs, scale, next, eps, dim, tok, st);
     });
+    if (a[9] != Py_None && a[9] != Py_False) written(ho);
     return Py_BuildValue("(NN)", none_or(out), none_or(ho));
 }
 
@@ -597,6 +608,7 @@ PyObject *lora(PyObject *const *a, Py_ssize_t n) {
     const void *xp = x.data_ptr();
     void *st = stream_for(nullptr, a, {0, 1, 2, 3, 4, 5, 6, 7});
     call("q8_lora", [&] { return f_lora(op, os, base, bs, xp, xt, xs, &ad, ids, tok, st); });
+    if (a[7] != Py_None) written(out);
     return wrap(out);
 }
 
