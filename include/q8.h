@@ -128,8 +128,12 @@ int q8_rmsnorm_quantize(void *xq, float *y, const float *x, const float *gamma, 
  *   n  = (h' * r(h')) * gamma_next              stored in n_out[t]
  *   r(x) = 1 / sqrt(S / dim + eps),  S = sum_i x_i^2
  * fp32 arithmetic, every product, sum, quotient and root rounded to nearest on its own, in
- * the order written; S is the sum rounded to fp32 once (it is carried in two fp32 words,
- * relative error below 2^-44), so results do not depend on an order of summation.  The
+ * the order written; S is the sum rounded to fp32 once.  It is carried in two fp32 words
+ * (relative error below 2^-37, 2^-46 as a rule), so S is the definition's but in rows whose
+ * exact sum lies that near to halfway between two fp32 numbers: one in some 2^20, whose
+ * result may also differ between calls of other numbers of tokens (never between repeated
+ * calls).  Values below 2^-51 are outside that bound (their squares' rounding errors are
+ * too small for fp32): they can matter only with an eps below 1e-25.  The
  * norm before the next block is that of the stored h'.
  *   n_out      out: [n_tok][dim] of n_type: Q8_TYPE_Q8_0 (blocks for q8_matmul_q, exactly
  *              the q8_quantize_act bytes of n), F32, F16 or BF16; NULL: only h'.
