@@ -8,7 +8,8 @@
 //                 on 8: 11.3 us, 4.2 TB/s; 32 tokens into Q8_0 pages: 2.7 us.
 //   k_kv_read     the cached values back as rows: a stream (2 or 34/32 bytes a value in, 2 or 4 out); one thread per 16 bytes of
 //                 a page.  3 documents up to 60 003, 4 heads of 256, fp16: 185 us, 6.7 TB/s; 12 prompts up to 8192, 8 heads
-//                 of 128, Q8_0 to bf16: 32 us, 5.0 TB/s (issue 54 % busy with the conversions); 300 rows: 2.5 us.
+//                 of 128, Q8_0 to bf16: 32 us, 5.0 TB/s (loads and the look-ups before them: long scoreboard 8.7, barrier 3.0 cycles an
+//                 issue, issue 54 % busy); 300 rows: 2.5 us.
 //   k_kv_*_plan   one CTA: prefix sums over the requests and over the reference counts.
 //   k_kv_*_apply  table rows, counts and page data of the planned moves, over the whole GPU: 16-byte copies, four
 //                 in flight a thread (32 forks of 3, 16 layers: 18 us with the plan, 5.4 TB/s).

@@ -58,7 +58,7 @@ struct LoraParams {
 constexpr uint32_t LORA_MAX_RANK = 128, LORA_MAX_ADAPTERS = 16384;
 constexpr uint32_t LORA_GROUP = 4;        // tokens of one adapter that k_lora multiplies by its weights at a time
 constexpr uint32_t LORA_TILE_MIN = 16;    // of more tokens: an adapter with fewer may have groups in place of a tile
-constexpr uint32_t LORA_TILES_AT_ONCE = 36;   // clusters of k_lora_shrink that fit at a time
+constexpr uint32_t LORA_TILES_AT_ONCE = 36;   // clusters of k_lora_shrink that fit at a time on 152 SMs (on fewer, groups would only be weighed later)
 cudaError_t launch_lora(const LoraParams &p, int num_sms, cudaStream_t st);
 cudaError_t launch_lora_groups(const LoraParams &p, int num_sms, cudaStream_t st);
 size_t lora_tc_scratch(uint32_t n_tok, uint32_t n_adapters, uint32_t max_rank);

@@ -6,7 +6,7 @@
 // order of the sum (error below 2^-37, 2^-46 as a rule, against the 2^-24 of the rounding; |x| >= 2^-51): Q8_0 bytes can be
 // told from the definition alone but in one row of some 2^20.
 // In packed pairs that is 5 instructions a value for each norm.  4096 rows of 4096, fp32, gated, both norms, Q8_0 out: 53.5 us, 4.1 TB/s
-// (issue 50 % busy, DRAM 41 %: two CTAs of 512 threads an SM, each with its next row on the way, wait for each other's roots; a
+// (bound by the joins, two a row with two barriers each: barrier 7.2 cycles an issue, issue 50 % busy, DRAM 41 %; a
 // ring of asynchronous copies 73 us, two or four chunks a thread 55 to 58).
 #include "q8_attn.cuh"
 #include "q8_kv.h"
@@ -392,7 +392,8 @@ cudaError_t launch_rows(const ResidualNormParams &p, int h_type, int y_type, int
 
 // Few rows: as many threads a row as it has chunks, the shortest chain.  Many rows: of up to 4096 values the same, each CTA with its next
 // row on the way (4096 x 4096 with both norms: 53.5 us; 608 rows 8.8, without the row ahead 9.4, but 304 rows 5.3 without); of
-// more, 32 values a thread (4096 x 8192: 110 us against 140 with 8 or with a row ahead).
+// more, 32 values a thread (4096 x 8192: 110 us against 140 with 8 or with a row ahead).  Above 16384 values 64 registers a thread do not
+// hold them, and 232 to 744 bytes a thread are spilled (2048 rows of 16384: 139 us, of 16416: 228, of 32768: 375).
 template <bool HWIDE, bool YWIDE>
 cudaError_t launch_typed(const ResidualNormParams &p, int h_type, int y_type, int num_sms, cudaStream_t st) {
     const uint32_t chunks = p.dim / 8;
