@@ -503,15 +503,16 @@ int q8_kv_read(void *k_out, uint64_t k_stride, void *v_out, uint64_t v_stride, i
  *   adapter_of in: int32 [n_tok], in any order (tokens of one adapter need not be neighbours).
  * x, the rank-sized sums and all other sums keep fp32 accuracy (24 bits of every x and of every
  * rank-sized sum take part in the products, which are exact; sums in fp32, in an order that goes by
- * the number of tokens and the adapters' shares of them, not by the tokens' order).  The root mean square
+ * the sizes, the numbers of tokens and adapters and the adapters' shares of the tokens, not by the
+ * tokens' order).  The root mean square
  * of the errors is 1 to 5e-7 of the adapters' part, whatever in_dim is: of many tokens the tensor cores add
  * up to 16 products at a time, of 16 values each, where they drop what fp32 would round.  A value of x or
  * of an adapter that is not finite spoils the tokens that it belongs to, no others.  An id of
  * n_adapters or beyond counts as negative, a rank outside its range is cut to it (of an adapter that
  * a token has); both raise Q8_ERANGE.  Pointers are 16-byte aligned (the id, rank and scale arrays
- * 4-byte), strides of out and base below 2^30.  out must not overlap x or the adapters.  A few tokens
- * are one launch without scratch; many (more than 192, or fewer where few adapters of high rank or
- * many outputs are shared) use the library's scratch.
+ * 4-byte), strides of out and base below 2^30.  out must not overlap x or the adapters.  Calls of at
+ * most 192 tokens, with tokens times max_rank at most 4096 and at least a quarter as many adapters
+ * (n_adapters) as tokens, are one launch without scratch; others may use the library's scratch.
  */
 typedef struct q8_adapters {
     const void *a, *b;       /* device */

@@ -275,7 +275,7 @@ constexpr uint32_t X_COLS = 320, X_STAGE = 96;
 __host__ __device__ constexpr uint32_t accumulators(uint32_t cols) { return cols <= 64 ? 4 : cols <= 96 ? 2 : 1; }
 // What is dropped grows with a sum's length, by 2^-26 of the sum for every 16 values and always towards zero.  So long sums are taken in
 // runs of 16 products an accumulator, and the runs added up in shared memory: 3e-7 whatever in_dim is, where 4096 values in one
-// accumulator cost 4e-6 (and a plain fp32 product of 4096 to 32768 values 4 to 8e-7).  A run's end costs about 0.8 us.
+// accumulator cost 4e-6 (and a plain fp32 product of 4096 to 32768 values 4 to 8e-7).  A run's end costs 0.5 to 0.8 us.
 constexpr uint32_t RUN = 16;
 __host__ __device__ constexpr uint32_t run_steps(uint32_t cols) { return RUN * accumulators(cols) / (KB / 16); }
 

@@ -43,6 +43,14 @@ def test_the_path_taken_is_the_quicker_one(plan, n_in, n_out, rank, n, adapters,
     assert (few if plan.few(n, rank, n_in, n_out, adapters) else many) <= 1.1 * min(few, many)
 
 
+@pytest.mark.parametrize("n_in,n_out", [(32, 1), (1024, 32768), (1 << 31, 1), (32, (1 << 30) - 1), (65536, 65536)])
+def test_calls_that_are_promised_no_scratch(plan, n_in, n_out):
+    """At most 192 tokens, tokens times rank at most 4096, a quarter as many adapters as tokens: whatever the sizes."""
+    for rank in range(8, 129, 8):
+        for n in range(1, min(192, 4096 // rank) + 1):
+            assert plan.few(n, rank, n_in, n_out, -(-n // 4)) and plan.few(n, rank, n_in, n_out, 16384)
+
+
 def test_the_ends_of_the_range(plan):
     for n_in, n_out in ((32, 1), (1 << 31, 1), (32, (1 << 30) - 1), (4096, 4096)):
         assert not plan.few(193, 8, n_in, n_out, 16384) and not plan.few((1 << 31) - 1, 128, n_in, n_out, 1)
